@@ -70,7 +70,8 @@ enum {
   ATTN_ERR_MISALIGNED = 3,    /* a BSHD base address not 16-byte aligned */
   ATTN_ERR_CUDA = 4,          /* a CUDA runtime / driver call failed */
   ATTN_ERR_DEVICE_TIMEOUT = 5, /* reported by attn_last_device_error() */
-  ATTN_ERR_WORKSPACE = 6      /* workspace missing, too small or misaligned */
+  ATTN_ERR_WORKSPACE = 6,     /* workspace missing, too small or misaligned */
+  ATTN_ERR_BAD_PAGE = 7       /* reported by attn_last_device_error(): a page table entry was not a page */
 };
 
 /*
@@ -144,8 +145,9 @@ const char* attn_last_error_message(void);
 /*
  * Synchronises `stream`, then returns and clears the current device's error word:
  * 0 when no kernel reported a failure, ATTN_ERR_DEVICE_TIMEOUT when a pipeline
- * wait timed out (the site is written to *site if site != NULL), ATTN_ERR_CUDA if
- * the synchronisation itself failed.
+ * wait timed out (the site is written to *site if site != NULL), ATTN_ERR_BAD_PAGE
+ * when a paged-cache call met a page outside its table or pool (site: an
+ * ATTN_KV4_SITE_* value), ATTN_ERR_CUDA if the synchronisation itself failed.
  */
 int attn_last_device_error(void* stream, int* site);
 
@@ -371,6 +373,73 @@ int attn_bwd_fp8(const void* q8, const void* k8, const void* v8, const void* do8
                  size_t workspace_bytes, void* stream);
 
 /*
+ * A 4-bit paged key/value cache, for serving: tokens are quantised into pages
+ * (attn_kv4_append), the newest tokens of every sequence attend over them
+ * (attn_kv4_decode), and pages are copied when a sequence forks or a pool is compacted
+ * (attn_kv4_copy_pages).  attn_kv4_gather reads tokens back as bf16, for example to
+ * prefill a continuation over a cached prefix.
+ *
+ * Pool.  uint8 [n_pages, H_kv, attn_kv4_block_bytes(page_size, d)], 16-byte aligned,
+ *   allocated by the caller; page_size in {16, 32, 64, 128} tokens, d = d_qk = d_v in
+ *   {64, 128}.  Pages need no initialisation: no token that was not written is read as
+ *   one.  page_table: device int32 [B, max_pages]; tokens page_size * i .. of sequence b
+ *   live in page page_table[b][i].  Which page is free or shared is the caller's
+ *   business; a call writes a page only for tokens that it appends or pages it copies to.
+ * Format.  Every 16 consecutive dims of a token and head share a scale s, an unsigned
+ *   8-bit float (bits 14..7 of a half-precision number: 5 exponent and 3 mantissa bits);
+ *   a value is held as (c - 8) s with a code c in 0..15.  s = max|x| / 7 rounded to
+ *   nearest (ties to even, at most 61440), c = 8 + clamp(round(x / s), -8, 7).  So a value
+ *   is off by at most s / 2, and at most max|x| / 13, while max|x| / 7 is between 2^-14 and
+ *   61440.  Sixteen values with an infinity or NaN among them are held as NaN.  Held
+ *   values are bf16 numbers exactly.
+ *
+ * attn_kv4_append: k, v bf16 packed rows [T][H_kv, d] (row t at k + t * k_row_stride
+ *   elements, so that slices of a fused projection need no copy; strides are multiples of
+ *   8 elements and at least H_kv * d).  Rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device
+ *   int32 [B + 1], ascending from 0) become tokens seq_lens[b], seq_lens[b] + 1, ... of
+ *   sequence b (device int32 [B]: its length before the call).  Rows past cu_seqlens[B]
+ *   are skipped.  Two rows must not name the same token of the same page.
+ * attn_kv4_gather: the reverse, into k, v bf16 [T, H_kv, d]: row cu_seqlens[b] + i is token
+ *   seq_lens[b] + i of sequence b as it is held.  Rows past cu_seqlens[B] are left alone
+ *   (zero_rest = 0) or zeroed.
+ * attn_kv4_decode: q bf16 [B, S_q, H_q, d]: the S_q newest tokens of every sequence, whose
+ *   seq_lens[b] tokens (these included; device int32 [B], clamped to [0, max_pages *
+ *   page_size]) are in the cache.  Query s sits at pos = seq_lens[b] - S_q + s and sees the
+ *   keys j <= pos, and j >= pos - window when window >= 0.  o bf16 [B, S_q, H_q, d]; lse
+ *   fp32 [B, H_q, S_q] (may be NULL).  A query that sees no key gets o = 0 and lse = the
+ *   sink logit.  scale, window, softmax_type and softmax_offset as for attn_fwd.
+ *   workspace: device scratch of attn_kv4_decode_workspace_size() bytes, 256-byte aligned,
+ *   not shared with a call that may run at the same time.  Bitwise reproducible.
+ * attn_kv4_copy_pages: page dst[i] = page src[i] for i < n, in each of n_layers pools that
+ *   follow one another ([n_layers, n_pages, page_bytes], page_bytes a multiple of 16).
+ *   src and dst are HOST arrays: they are checked and read before the call returns and
+ *   become part of the launch (a captured graph keeps them).  A page may be the source
+ *   of several copies.  ATTN_ERR_INVALID_ARG for a page outside [0, n_pages), a
+ *   destination named twice, or a page that is both source and destination.
+ *
+ * Errors as attn_fwd (H_q % H_kv != 0 and null pointers: ATTN_ERR_INVALID_ARG; other page
+ * sizes and head dims: ATTN_ERR_UNSUPPORTED).  A token whose page is not in the table
+ * or the pool is not written, reads as zeros, and makes attn_last_device_error() return
+ * ATTN_ERR_BAD_PAGE.
+ */
+enum { ATTN_KV4_SITE_APPEND = 1, ATTN_KV4_SITE_GATHER = 2, ATTN_KV4_SITE_DECODE = 3 };
+/* Bytes of one page and kv head; 0 for an unsupported page size or head dim. */
+int attn_kv4_block_bytes(int page_size, int d);
+int attn_kv4_append(const void* k, const void* v, const int* cu_seqlens, void* pool, const int* page_table,
+                    const int* seq_lens, int B, int T, int H_kv, int d, int n_pages, int page_size, int max_pages,
+                    long long k_row_stride, long long v_row_stride, void* stream);
+int attn_kv4_gather(const void* pool, const int* page_table, const int* cu_seqlens, const int* seq_lens, void* k,
+                    void* v, int B, int T, int H_kv, int d, int n_pages, int page_size, int max_pages, int zero_rest,
+                    void* stream);
+size_t attn_kv4_decode_workspace_size(int B, int S_q, int H_q, int H_kv, int d);
+int attn_kv4_decode(const void* q, const void* pool, const int* page_table, const int* seq_lens, void* o, float* lse,
+                    int B, int S_q, int H_q, int H_kv, int d, int n_pages, int page_size, int max_pages, float scale,
+                    int window, int softmax_type, const float* softmax_offset, void* workspace,
+                    size_t workspace_bytes, void* stream);
+int attn_kv4_copy_pages(void* pool, int n_layers, int n_pages, size_t page_bytes, const int* src, const int* dst,
+                        int n, void* stream);
+
+/*
  * Failure-path self-test.  Every pipeline wait in the kernels is bounded (about one
  * second); on expiry the kernel stores 0x100 + a site code in a per-GPU device error
  * word, every other wait gives up at once, in-flight copies and MMAs are drained with
@@ -399,7 +468,8 @@ enum {
   ATTN_KERNEL_BWD_Q = 3,           /* query-stationary deterministic dQ kernel */
   ATTN_KERNEL_BWD_DQ_CONVERT = 4,  /* fp32 dQ accumulator -> bf16; split dK/dV combine */
   ATTN_KERNEL_FP8_QUANT = 5,       /* E4M3 amax and quantisation */
-  ATTN_KERNEL_CLASSES = 6
+  ATTN_KERNEL_KV4 = 6,             /* 4-bit cache: append, gather, copy, decode */
+  ATTN_KERNEL_CLASSES = 7
 };
 int attn_timing_enable(int on);
 int attn_timing_read(double* ms, int* launches, int n);

@@ -16,6 +16,7 @@ v [B,S_kv,H_kv,d_v]; lse fp32 [B,H_q,S_q]; softmax_offset fp32 [H_q].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -110,6 +111,19 @@ def _load():
     lib.attn_bwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i,
                                  i, i, i, f, i, i, i, vp, vp, sz, vp]
     lib.attn_bwd_fp8.restype = i
+    ll = ctypes.c_longlong
+    lib.attn_kv4_block_bytes.argtypes = [i, i]
+    lib.attn_kv4_block_bytes.restype = i
+    lib.attn_kv4_append.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, ll, ll, vp]
+    lib.attn_kv4_append.restype = i
+    lib.attn_kv4_gather.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp]
+    lib.attn_kv4_gather.restype = i
+    lib.attn_kv4_decode_workspace_size.argtypes = [i, i, i, i, i]
+    lib.attn_kv4_decode_workspace_size.restype = sz
+    lib.attn_kv4_decode.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, i, vp, vp, sz, vp]
+    lib.attn_kv4_decode.restype = i
+    lib.attn_kv4_copy_pages.argtypes = [vp, i, i, sz, vp, vp, i, vp]
+    lib.attn_kv4_copy_pages.restype = i
     _lib = lib
     return lib
 
@@ -156,7 +170,7 @@ def attn_last_error_message() -> str:
 
 
 def attn_last_device_error(stream=None):
-    """Synchronise the stream; return (status, site) of the device error word and clear it."""
+    """Synchronise the stream; return (status, site) of the device error words and clear them."""
     site = ctypes.c_int(0)
     st = _load().attn_last_device_error(_stream(stream), ctypes.byref(site))
     return st, site.value
@@ -363,7 +377,7 @@ def attn_bwd_bias(q, k, v, o, dout, lse, dq, dk, dv, d_offset, bias, dbias, **kw
     attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, d_offset, bias=bias, dbias=dbias, **kw)
 
 
-KERNEL_CLASSES = ("fwd", "bwd_preprocess", "bwd_kv", "bwd_q", "bwd_dq_convert", "fp8_quantize")
+KERNEL_CLASSES = ("fwd", "bwd_preprocess", "bwd_kv", "bwd_q", "bwd_dq_convert", "fp8_quantize", "kv4")
 
 
 def attn_timing_enable(on: bool = True) -> None:
@@ -604,6 +618,232 @@ def sdpa_backward_fp8(q, k, v, o, dout, lse, *, ds_amax=None, ds_amax_out=None, 
     attn_bwd_fp8(q8, k8, v8, do8, qt8, kt8, dot8, sq, sk, sv, sdo, o, lse, ds_amax, dq, dk, dv, d_offset,
                  ds_amax_out=ds_amax_out, **kw)
     return dq, dk, dv, d_offset
+
+
+# ----------------------------------------------------------------------------- 4-bit paged cache
+
+
+def _one_device(*tensors):
+    """A context with the device of the tensors (None skipped) as the current one; they share it."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return torch.cuda.device(dev)
+
+
+def _allocating(stream):
+    """A context in which new tensors belong to the stream that the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def kv4_pool(n_pages, H_kv, d, page_size, *, n_layers=None, device="cuda"):
+    """A pool of pages of the 4-bit cache: uint8 [n_pages, H_kv, block] (with n_layers, one such
+    pool per layer: [n_layers, n_pages, H_kv, block]).  Its contents need no initialisation."""
+    block = kv4_block_bytes(page_size, d)
+    shape = (n_pages, H_kv, block) if n_layers is None else (n_layers, n_pages, H_kv, block)
+    return torch.empty(shape, dtype=torch.uint8, device=device)
+
+
+def attn_kv4_block_bytes(page_size, d) -> int:
+    return int(_load().attn_kv4_block_bytes(int(page_size), int(d)))
+
+
+def kv4_block_bytes(page_size, d) -> int:
+    """Bytes of one page and kv head: page_size tokens of K and V at 4.5 bits a value."""
+    n = attn_kv4_block_bytes(page_size, d)
+    if n == 0:
+        raise ValueError(f"page_size must be 16, 32, 64 or 128 and d 64 or 128, got {page_size} and {d}")
+    return n
+
+
+def _check_paged(pool, page_table, seq_lens, d):
+    """Checks of a pool [n_pages, H_kv, block] with its page table and lengths; returns the
+    sizes (B, n_pages, H_kv, page_size, max_pages)."""
+    _check(pool, "pool", torch.uint8, 3)
+    _check(page_table, "page_table", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    n_pages, H_kv, block = pool.shape
+    page_size = block * 8 // (9 * d) if d else 0
+    if kv4_block_bytes(page_size, d) != block:
+        raise ValueError(f"pool must be [n_pages, H_kv, kv4_block_bytes(page_size, {d})], got {tuple(pool.shape)}")
+    B, max_pages = page_table.shape
+    if seq_lens.shape[0] != B:
+        raise ValueError(f"seq_lens: one length per row of page_table ({B}), got {seq_lens.shape[0]}")
+    return B, n_pages, H_kv, page_size, max_pages
+
+
+def _check_cu(cu, name, B=None):
+    _check(cu, name, torch.int32, 1)
+    if cu.shape[0] < 1 or (B is not None and cu.shape[0] != B + 1):
+        raise ValueError(f"{name} must hold one offset per sequence and the end"
+                         + (f" ({B + 1} values)" if B is not None else "") + f", got {cu.shape[0]}")
+
+
+def _check_rows(t, name, H, d):
+    """A packed bf16 tensor [T, H, d] whose rows may be apart (a slice of a fused projection)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
+        raise ValueError(f"{name} must be [T, {H}, {d}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape[0] == 0:
+        return H * d
+    if (t.stride(2) != 1 and d > 1) or (t.stride(1) != d and H > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    stride = t.stride(0) if t.shape[0] > 1 else H * d
+    if stride < H * d or stride % 8:
+        raise ValueError(f"{name}: rows must not overlap and must be a multiple of 8 elements apart, got {stride}")
+    return stride
+
+
+def attn_kv4_append(k, v, cu_seqlens, pool, page_table, seq_lens, *, stream=None):
+    """Quantise packed keys and values (bf16 [T, H_kv, d]) into the pages of a 4-bit cache.
+
+    Rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32 [B+1] on the device) become tokens
+    seq_lens[b], seq_lens[b] + 1, ... of sequence b (int32 [B]: its length before the call).
+    pool: uint8 [n_pages, H_kv, block] (kv4_pool); page_table: int32 [B, max_pages].  The rows
+    of k and v may be apart, as in a slice of a fused projection."""
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, H_kv, d], got shape {tuple(k.shape)}")
+    T, _, d = k.shape
+    B, n_pages, H_kv, page_size, max_pages = _check_paged(pool, page_table, seq_lens, d)
+    ks, vs = _check_rows(k, "k", H_kv, d), _check_rows(v, "v", H_kv, d)
+    if v.shape[0] != T:
+        raise ValueError(f"k and v must have the same rows, got {T} and {v.shape[0]}")
+    _check_cu(cu_seqlens, "cu_seqlens", B)
+    with _one_device(k, v, cu_seqlens, pool, page_table, seq_lens):
+        st = _load().attn_kv4_append(_ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(pool), _ptr(page_table), _ptr(seq_lens),
+                                     B, T, H_kv, d, n_pages, page_size, max_pages, ks, vs, _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_append")
+
+
+def attn_kv4_gather(pool, page_table, cu_seqlens, seq_lens, k, v, *, zero_rest=False, stream=None):
+    """Read tokens of a 4-bit cache back into preallocated packed k, v (bf16 [T, H_kv, d]): row
+    cu_seqlens[b] + i is token seq_lens[b] + i of sequence b.  Rows past cu_seqlens[B] are left
+    alone, or zeroed with zero_rest."""
+    _check(k, "k", torch.bfloat16, 3)
+    _check(v, "v", torch.bfloat16, 3)
+    T, _, d = k.shape
+    B, n_pages, H_kv, page_size, max_pages = _check_paged(pool, page_table, seq_lens, d)
+    for t, n in ((k, "k"), (v, "v")):
+        if tuple(t.shape) != (T, H_kv, d):
+            raise ValueError(f"{n} must be {(T, H_kv, d)}, got {tuple(t.shape)}")
+    _check_cu(cu_seqlens, "cu_seqlens", B)
+    with _one_device(k, v, cu_seqlens, pool, page_table, seq_lens):
+        st = _load().attn_kv4_gather(_ptr(pool), _ptr(page_table), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(k), _ptr(v),
+                                     B, T, H_kv, d, n_pages, page_size, max_pages, int(bool(zero_rest)),
+                                     _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_gather")
+
+
+def kv4_gather(pool, page_table, cu_seqlens, seq_lens, total, d, *, stream=None):
+    """attn_kv4_gather into new tensors of `total` rows: returns (k, v), zeros in the rows of no
+    sequence."""
+    with _one_device(pool), _allocating(stream):
+        k = torch.empty((int(total), pool.shape[-2], int(d)), dtype=torch.bfloat16, device=pool.device)
+        v = torch.empty_like(k)
+        attn_kv4_gather(pool, page_table, cu_seqlens, seq_lens, k, v, zero_rest=True, stream=stream)
+    return k, v
+
+
+def attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d) -> int:
+    return int(_load().attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d))
+
+
+def attn_kv4_decode(q, pool, page_table, seq_lens, o, lse=None, *, window=-1, softmax_type=VANILLA,
+                    softmax_offset=None, scale=0.0, workspace=None, stream=None):
+    """Attention of the S_q newest tokens of every sequence over its 4-bit cache, into
+    preallocated o (bf16, q's shape [B, S_q, H_q, d]) and, if given, lse (fp32 [B, H_q, S_q]).
+
+    seq_lens: int32 [B] on the device, tokens in the cache (the S_q newest among them); query
+    s sits at seq_lens[b] - S_q + s and sees the keys up to its own place, with window >= 0
+    the last window + 1 of them.  workspace: uint8 of attn_kv4_decode_workspace_size() bytes
+    or more, not shared with a call that may run at the same time (None: a new one)."""
+    _check(q, "q", torch.bfloat16, 4)
+    _check(o, "o", torch.bfloat16, 4)
+    B, S_q, H_q, d = q.shape
+    Bt, n_pages, H_kv, page_size, max_pages = _check_paged(pool, page_table, seq_lens, d)
+    if Bt != B:
+        raise ValueError(f"page_table must have one row per batch entry ({B}), got {Bt}")
+    if o.shape != q.shape:
+        raise ValueError(f"o must have q's shape {tuple(q.shape)}, got {tuple(o.shape)}")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, 3)
+        if tuple(lse.shape) != (B, H_q, S_q):
+            raise ValueError(f"lse must be {(B, H_q, S_q)}, got {tuple(lse.shape)}")
+    if softmax_offset is not None:
+        _check(softmax_offset, "softmax_offset", torch.float32, 1)
+        if softmax_offset.shape[0] != H_q:
+            raise ValueError(f"softmax_offset must have one value per query head ({H_q})")
+    with _one_device(q, pool, page_table, seq_lens, o, lse, softmax_offset, workspace), _allocating(stream):
+        if workspace is None:
+            workspace = torch.empty(max(attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d), 256), dtype=torch.uint8,
+                                    device=q.device)
+        else:
+            _check(workspace, "workspace", torch.uint8, 1)
+        st = _load().attn_kv4_decode(_ptr(q), _ptr(pool), _ptr(page_table), _ptr(seq_lens), _ptr(o), _ptr(lse), B, S_q,
+                                     H_q, H_kv, d, n_pages, page_size, max_pages, float(scale or 0.0), int(window),
+                                     _stype(softmax_type), _ptr(softmax_offset), _ptr(workspace), workspace.numel(),
+                                     _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_decode")
+
+
+def sdpa_decode_kv4(q, pool, page_table, seq_lens, *, window=-1, softmax_type=VANILLA, softmax_offset=None, scale=0.0,
+                    workspace=None, stream=None):
+    """Allocate O and LSE, run attn_kv4_decode, return (o, lse)."""
+    B, S_q, H_q, _ = q.shape
+    with _one_device(q), _allocating(stream):
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((B, H_q, S_q), dtype=torch.float32, device=q.device)
+        attn_kv4_decode(q, pool, page_table, seq_lens, o, lse, window=window, softmax_type=softmax_type,
+                        softmax_offset=softmax_offset, scale=scale, workspace=workspace, stream=stream)
+    return o, lse
+
+
+def _host_pages(pages, name):
+    t = pages if isinstance(pages, torch.Tensor) else torch.tensor(pages)
+    if t.dim() == 1 and t.numel() == 0:
+        t = t.to(torch.int32)
+    if t.is_cuda:
+        raise ValueError(f"{name}: page numbers are read on the host; pass a list or a CPU tensor")
+    if t.dtype not in (torch.int32, torch.int64) or t.dim() != 1:
+        raise ValueError(f"{name} must be a one-dimensional list of whole numbers")
+    if t.dtype == torch.int64:  # a number past 32 bits must not wrap into a page
+        if t.numel() and (int(t.max()) > 0x7fffffff or int(t.min()) < -0x80000000):
+            raise ValueError(f"{name}: page number out of range")
+        t = t.to(torch.int32)
+    return t.contiguous()
+
+
+def attn_kv4_copy_pages(pool, src, dst, *, stream=None):
+    """Copy page src[i] to page dst[i] for every i, in the pool [n_pages, H_kv, block] or in
+    each layer of [n_layers, n_pages, H_kv, block]: a fork's partly filled last page, or the
+    moves of a compaction.  src, dst: lists or CPU tensors, checked before anything is
+    launched: a destination named twice, a page that is both source and destination, or a page
+    outside the pool is refused."""
+    if pool.dim() not in (3, 4):
+        raise ValueError(f"pool must be [n_pages, H_kv, block] or [n_layers, n_pages, H_kv, block], got "
+                         f"{tuple(pool.shape)}")
+    _check(pool, "pool", torch.uint8, pool.dim())
+    src, dst = _host_pages(src, "src"), _host_pages(dst, "dst")
+    if src.shape != dst.shape:
+        raise ValueError(f"src and dst must have the same length, got {src.shape[0]} and {dst.shape[0]}")
+    n_layers = pool.shape[0] if pool.dim() == 4 else 1
+    n_pages, H_kv, block = pool.shape[-3:]
+    with _one_device(pool):
+        st = _load().attn_kv4_copy_pages(_ptr(pool), n_layers, n_pages, H_kv * block, _ptr(src), _ptr(dst),
+                                         src.shape[0], _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_copy_pages")
 
 
 # ----------------------------------------------------------------------------- conveniences

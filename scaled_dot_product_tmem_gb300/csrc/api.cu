@@ -24,7 +24,9 @@ void set_error(const char* what, cudaError_t e) {
 }
 void set_error(const char* what) { snprintf(g_last_error, sizeof(g_last_error), "%s", what); }
 
-__device__ int g_device_error;  // one word per GPU: 0 or kErrTimeoutBase + site
+// two words per GPU: 0 or kErrTimeoutBase + site of a wait that ran out; 0 or the site of a
+// page outside its table or pool (its own word: the first one makes running waits give up)
+__device__ int g_device_error[2];
 
 constexpr int kMaxDevices = 64;
 
@@ -136,8 +138,16 @@ int timed(int kind, int nlaunch, cudaStream_t s, F&& launch) {
 }  // namespace
 
 namespace sdpa {
-// The device error word of the current device, for the other host files of the library.
+// The device error words of the current device, for the other host files of the library.
 int* device_error_word() { return device_error_ptr(); }
+int* device_page_error_word() {
+  int* p = device_error_ptr();
+  return p ? p + 1 : nullptr;
+}
+void set_last_error(const char* what, cudaError_t e) { set_error(what, e); }
+int timed_launch(int kind, int nlaunch, cudaStream_t s, int (*launch)(void*), void* ctx) {
+  return timed(kind, nlaunch, s, [&] { return launch(ctx); });
+}
 
 bool dims_supported(int d_qk, int d_v) {
   return (d_qk == 64 || d_qk == 128 || d_qk == 192) && (d_v == 64 || d_v == 128);
@@ -200,6 +210,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_DEVICE_TIMEOUT: return "device pipeline wait timed out";
     case ATTN_ERR_WORKSPACE: return "workspace missing, too small or misaligned";
+    case ATTN_ERR_BAD_PAGE: return "page outside the page table or the pool";
     default: return "unknown status";
   }
 }
@@ -208,13 +219,13 @@ int attn_last_device_error(void* stream, int* site) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
   int* p = device_error_ptr();
   if (!p) return ATTN_ERR_CUDA;
-  int v = 0;
-  if (cudaMemcpy(&v, p, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (site) *site = v;
-  if (v == 0) return ATTN_OK;
-  const int zero = 0;
-  if (cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
-  return ATTN_ERR_DEVICE_TIMEOUT;
+  int v[2] = {0, 0};
+  if (cudaMemcpy(v, p, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (site) *site = v[0] ? v[0] : v[1];
+  if (v[0] == 0 && v[1] == 0) return ATTN_OK;
+  const int zero[2] = {0, 0};
+  if (cudaMemcpy(p, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
+  return v[0] ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_ERR_BAD_PAGE;
 }
 
 // Checks of an additive bias [bias_B, bias_H, S_q, S_kv] (bf16, 16-byte aligned) and

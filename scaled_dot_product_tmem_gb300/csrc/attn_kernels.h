@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "kv4.cuh"
+
 namespace sdpa {
 
 struct FwdParams {
@@ -159,12 +161,67 @@ int launch_bwd_kv_fp8(int d, const CUtensorMap& tq8, const CUtensorMap& tk8, con
 int launch_bwd_q_fp8(int d, const CUtensorMap& tq8_128, const CUtensorMap& tk8, const CUtensorMap& tv8,
                      const CUtensorMap& tdo8_128, const CUtensorMap& tkt8, const BwdParams& p, cudaStream_t stream);
 
+// ----------------------------------------------------------------- 4-bit paged cache (kv4.cuh)
+// Filling (append) and reading back (gather): rows t of packed [T, H_kv, d] tensors; sequence
+// b's rows are cu[b] .. cu[b + 1] - 1 and become its tokens start[b], start[b] + 1, ...
+struct Kv4StoreParams {
+  Kv4Pool c;
+  int B, T;
+  const int* cu;     // [B + 1]
+  const int* start;  // [B]
+  const __nv_bfloat16* k = nullptr;  // append: row t at k + t * k_stride, [H_kv, d] contiguous
+  const __nv_bfloat16* v = nullptr;
+  long long k_stride = 0, v_stride = 0;
+  __nv_bfloat16* k_out = nullptr;  // gather: [T, H_kv, d]
+  __nv_bfloat16* v_out = nullptr;
+  int zero_rest = 0;  // gather: zero the rows of no sequence
+  uint8_t* pool;
+  int* page_err;  // device word: set to `site` when a token's page is not in the table or the pool
+  int site;
+};
+int launch_kv4_append(const Kv4StoreParams& p, cudaStream_t stream);
+int launch_kv4_gather(const Kv4StoreParams& p, cudaStream_t stream);
+
+// Page pairs of one copy launch, passed as kernel arguments.
+constexpr int kKv4PairsMax = 480;
+struct Kv4Pairs {
+  int2 at[kKv4PairsMax];  // source page, destination page
+};
+int launch_kv4_copy(uint8_t* pool, int n_layers, long long layer_bytes, long long page_bytes, const int* src,
+                    const int* dst, int n, cudaStream_t stream);
+
+// Attention of the S_q newest tokens of every sequence over the cache.
+struct Kv4DecodeParams {
+  Kv4Pool c;
+  int B, S_q, H_q;
+  float scale_log2;
+  int window, softmax_type;
+  const float* offset;
+  const int* seq_lens;      // [B]
+  const __nv_bfloat16* q;   // [B, S_q, H_q, d]
+  const uint8_t* pool;
+  __nv_bfloat16* o;         // [B, S_q, H_q, d]
+  float* lse;               // [B, H_q, S_q] or null
+  int* page_err;
+  int site;
+  int* err;
+};
+size_t kv4_decode_workspace(int B, int S_q, int H_q, int H_kv, int d);
+int launch_kv4_decode(const Kv4DecodeParams& p, void* workspace, cudaStream_t stream);
+
 // One warp waits on an mbarrier nobody arrives at: after the wait limit it records
 // kErrTimeoutBase + site in *err and returns (the failure path, without a fault).
 int launch_selftest_wait(int* err, int site, cudaStream_t stream);
 
 // Device error word of the current device (null if CUDA cannot report it).
 int* device_error_word();
+// The word after it: set when a kernel met a page outside its table or pool.
+int* device_page_error_word();
+// The calling thread's last error text (what failed, CUDA's message).
+void set_last_error(const char* what, cudaError_t e);
+// Runs launch(ctx), which enqueues `nlaunch` kernels of class `kind` on stream s, inside the
+// measurement aid's event pair when that is on.
+int timed_launch(int kind, int nlaunch, cudaStream_t s, int (*launch)(void*), void* ctx);
 
 // Argument rules shared by every entry point (sizes, flags, head dims): ATTN_OK or an
 // error status of the public header.
