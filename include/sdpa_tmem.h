@@ -6,7 +6,9 @@
  *
  * with grouped-query heads, a causal mask with an optional left sliding window,
  * distinct Q/K and V head dims, and three sink softmax types; plus padded batches
- * with per-entry lengths (attn_fwd_varlen / attn_bwd_varlen), an additive bias with
+ * with per-entry lengths (attn_fwd_varlen / attn_bwd_varlen), packed sequences
+ * (attn_fwd_packed / attn_bwd_packed), a 4-bit paged key/value cache with the attention
+ * that reads it (attn_kv4_*), an additive bias with
  * its gradient (attn_fwd_bias / attn_bwd_bias), attention dropout (attn_fwd_dropout /
  * attn_bwd_dropout), an E4M3 forward with per-tensor scaling (attn_fp8_amax,
  * attn_fp8_quantize, attn_fwd_fp8) and its FP8 backward (attn_fp8_quantize_e5m2,
@@ -134,6 +136,37 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
                     int d_qk, int d_v, float scale, int causal, int window, int softmax_type,
                     const float* softmax_offset, const int* seq_lens_q, const int* seq_lens_kv, int deterministic,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Packed sequences: sequences of different lengths one after another in q, o, dout, dq
+ * [T_q, H_q, d] and k, v, dk, dv [T_kv, H_kv, d], with no padding rows.  cu_seqlens_q and
+ * cu_seqlens_kv: device int32 [B + 1], ascending (4-byte aligned, read by the kernels);
+ * sequence b holds query rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 and key rows
+ * likewise, and computes as a batch entry of its own: attn_fwd / attn_bwd with B = 1 on
+ * its rows (masks count positions from the sequence's first row).  cu_seqlens_kv NULL:
+ * the same as cu_seqlens_q.  A sequence may have no queries, no keys or neither; a row
+ * that sees no key gets o = 0 and lse = the sink logit.  lse: fp32 [H_q, T_q].  Values of
+ * one sequence, infinities and NaN included, never reach another sequence's results.
+ * Offsets are clamped to [0, T] and to their running maximum.  Rows that belong to no
+ * sequence (past the last one, or before cu_seqlens[0]) are left alone; zero_rest != 0
+ * writes the ones past the last sequence: o, dq, dk, dv = 0, lse = -inf.
+ * attn_bwd_packed is bitwise reproducible.  For LEARNABLE sinks its d_offset carries fp32
+ * rounding only, not that of the stored bf16 o.
+ * workspace: device scratch of attn_packed_workspace_size() bytes (backward 0 or 1),
+ * 256-byte aligned, not shared with a call that may run at the same time.
+ * Supported head dims: (d_qk, d_v) in {(64, 64), (128, 128), (192, 128)}.  Errors as
+ * attn_fwd and attn_bwd.
+ */
+size_t attn_packed_workspace_size(int B, int T_q, int T_kv, int H_q, int H_kv, int d_qk, int d_v, int backward);
+int attn_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_seqlens_q,
+                    const int* cu_seqlens_kv, int B, int T_q, int T_kv, int H_q, int H_kv, int d_qk, int d_v,
+                    float scale, int causal, int window, int softmax_type, const float* softmax_offset, int zero_rest,
+                    void* workspace, size_t workspace_bytes, void* stream);
+int attn_bwd_packed(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                    void* dq, void* dk, void* dv, float* d_offset, const int* cu_seqlens_q, const int* cu_seqlens_kv,
+                    int B, int T_q, int T_kv, int H_q, int H_kv, int d_qk, int d_v, float scale, int causal,
+                    int window, int softmax_type, const float* softmax_offset, int zero_rest, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* attn_status_string(int status);

@@ -111,6 +111,13 @@ def _load():
     lib.attn_bwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i,
                                  i, i, i, f, i, i, i, vp, vp, sz, vp]
     lib.attn_bwd_fp8.restype = i
+    lib.attn_packed_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+    lib.attn_packed_workspace_size.restype = sz
+    lib.attn_fwd_packed.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, i, i, vp, i, vp, sz, vp]
+    lib.attn_fwd_packed.restype = i
+    lib.attn_bwd_packed.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, i, i,
+                                    vp, i, vp, sz, vp]
+    lib.attn_bwd_packed.restype = i
     ll = ctypes.c_longlong
     lib.attn_kv4_block_bytes.argtypes = [i, i]
     lib.attn_kv4_block_bytes.restype = i
@@ -620,7 +627,7 @@ def sdpa_backward_fp8(q, k, v, o, dout, lse, *, ds_amax=None, ds_amax_out=None, 
     return dq, dk, dv, d_offset
 
 
-# ----------------------------------------------------------------------------- 4-bit paged cache
+# ----------------------------------------------------------------------------- packed sequences
 
 
 def _one_device(*tensors):
@@ -639,6 +646,160 @@ def _one_device(*tensors):
 def _allocating(stream):
     """A context in which new tensors belong to the stream that the call runs on."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _check_cu(cu, name, B=None):
+    _check(cu, name, torch.int32, 1)
+    if cu.shape[0] < 1 or (B is not None and cu.shape[0] != B + 1):
+        raise ValueError(f"{name} must hold one offset per sequence and the end"
+                         + (f" ({B + 1} values)" if B is not None else "") + f", got {cu.shape[0]}")
+
+
+def attn_packed_workspace_size(B, T_q, T_kv, H_q, H_kv, d_qk, d_v, backward=False) -> int:
+    return int(_load().attn_packed_workspace_size(B, T_q, T_kv, H_q, H_kv, d_qk, d_v, int(bool(backward))))
+
+
+def _check_packed(q, k, v, cu_q, cu_kv, softmax_offset):
+    """Checks shared by the packed calls; returns (B, T_q, T_kv, H_q, H_kv, d_qk, d_v)."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _check(t, n, torch.bfloat16, 3)
+    T_q, H_q, d_qk = q.shape
+    T_kv, H_kv, d_v = v.shape
+    if tuple(k.shape) != (T_kv, H_kv, d_qk):
+        raise ValueError(f"k must be {(T_kv, H_kv, d_qk)} (v's rows and heads, q's head dim), got {tuple(k.shape)}")
+    _check_cu(cu_q, "cu_seqlens_q")
+    B = cu_q.shape[0] - 1
+    if cu_kv is not None:
+        _check_cu(cu_kv, "cu_seqlens_kv", B)
+    elif T_q != T_kv:
+        raise ValueError(f"without cu_seqlens_kv the keys share the queries' offsets: {T_q} and {T_kv} rows")
+    if softmax_offset is not None:
+        _check(softmax_offset, "softmax_offset", torch.float32, 1)
+        if softmax_offset.shape[0] != H_q:
+            raise ValueError(f"softmax_offset must have one value per query head ({H_q})")
+    return B, T_q, T_kv, H_q, H_kv, d_qk, d_v
+
+
+def _packed_workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    _check(workspace, "workspace", torch.uint8, 1)
+    return workspace
+
+
+def attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv=None, *, causal=True, window=-1,
+                    softmax_type=VANILLA, softmax_offset=None, scale=0.0, zero_rest=False, workspace=None,
+                    stream=None):
+    """Forward over packed sequences into preallocated o [T_q, H_q, d_v] bf16 and lse [H_q, T_q]
+    fp32: q [T_q, H_q, d_qk], k [T_kv, H_kv, d_qk], v [T_kv, H_kv, d_v].
+
+    cu_seqlens_q / cu_seqlens_kv: int32 [B+1] on the device, sequence b's rows are
+    cu_seqlens[b] .. cu_seqlens[b+1] - 1 (cu_seqlens_kv None: the queries' offsets).  Rows past
+    the last sequence are left alone, or zeroed with zero_rest (lse -inf).  workspace: uint8 of
+    attn_packed_workspace_size() bytes or more, not shared with a call that may run at the
+    same time (None: a new one)."""
+    sizes = _check_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
+    _, T_q, _, H_q, _, _, d_v = sizes
+    _check(o, "o", torch.bfloat16, 3)
+    _check(lse, "lse", torch.float32, 2)
+    if tuple(o.shape) != (T_q, H_q, d_v) or tuple(lse.shape) != (H_q, T_q):
+        raise ValueError(f"o must be {(T_q, H_q, d_v)} and lse {(H_q, T_q)}, got {tuple(o.shape)}, {tuple(lse.shape)}")
+    with _one_device(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, softmax_offset, workspace), _allocating(stream):
+        ws = _packed_workspace(workspace, attn_packed_workspace_size(*sizes) if workspace is None else 0, q.device)
+        st = _load().attn_fwd_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens_q),
+                                     _ptr(cu_seqlens_kv), *sizes, float(scale or 0.0), int(bool(causal)), int(window),
+                                     _stype(softmax_type), _ptr(softmax_offset), int(bool(zero_rest)), _ptr(ws),
+                                     ws.numel(), _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_fwd_packed")
+
+
+def attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv=None, *, causal=True,
+                    window=-1, softmax_type=VANILLA, softmax_offset=None, scale=0.0, zero_rest=False, workspace=None,
+                    stream=None):
+    """Backward of attn_fwd_packed into preallocated dq, dk, dv (bf16, shapes of q, k, v) and
+    d_offset (fp32 [H_q]; learnable sinks, else None).  Bitwise reproducible."""
+    sizes = _check_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
+    _, T_q, _, H_q, _, _, d_v = sizes
+    _check(lse, "lse", torch.float32, 2)
+    if tuple(lse.shape) != (H_q, T_q):
+        raise ValueError(f"lse must be {(H_q, T_q)}, got {tuple(lse.shape)}")
+    for t, n, shape in ((o, "o", (T_q, H_q, d_v)), (dout, "dout", (T_q, H_q, d_v)), (dq, "dq", tuple(q.shape)),
+                        (dk, "dk", tuple(k.shape)), (dv, "dv", tuple(v.shape))):
+        _check(t, n, torch.bfloat16, 3)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
+    if d_offset is not None:
+        _check(d_offset, "d_offset", torch.float32, 1)
+        if d_offset.shape[0] != H_q:
+            raise ValueError(f"d_offset must have one value per query head ({H_q})")
+    with _one_device(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv, softmax_offset,
+                     workspace), _allocating(stream):
+        ws = _packed_workspace(workspace, attn_packed_workspace_size(*sizes, True) if workspace is None else 0,
+                               q.device)
+        st = _load().attn_bwd_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
+                                     _ptr(dv), _ptr(d_offset), _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv), *sizes,
+                                     float(scale or 0.0), int(bool(causal)), int(window), _stype(softmax_type),
+                                     _ptr(softmax_offset), int(bool(zero_rest)), _ptr(ws), ws.numel(),
+                                     _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_bwd_packed")
+
+
+def sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv=None, *, causal=True, window=-1, softmax_type=VANILLA,
+                        softmax_offset=None, scale=0.0, workspace=None, stream=None):
+    """Allocate O and LSE, run attn_fwd_packed, return (o, lse); rows past the last sequence are
+    zero (lse -inf)."""
+    with _one_device(q), _allocating(stream):
+        o = torch.empty((q.shape[0], q.shape[1], v.shape[2]), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, causal=causal, window=window,
+                        softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale, zero_rest=True,
+                        workspace=workspace, stream=stream)
+    return o, lse
+
+
+def sdpa_backward_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv=None, *, causal=True, window=-1,
+                         softmax_type=VANILLA, softmax_offset=None, scale=0.0, workspace=None, stream=None):
+    """Allocate dQ, dK, dV (and d_offset for the learnable sink), run attn_bwd_packed, return
+    them; gradients of rows past the last sequence are zero."""
+    with _one_device(q), _allocating(stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        d_off = (torch.empty((q.shape[1],), dtype=torch.float32, device=q.device)
+                 if _stype(softmax_type) == LEARNABLE else None)
+        attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_off, cu_seqlens_q, cu_seqlens_kv, causal=causal,
+                        window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
+                        zero_rest=True, workspace=workspace, stream=stream)
+    return dq, dk, dv, d_off
+
+
+class SDPAPackedFunction(torch.autograd.Function):
+    """autograd wrapper of the packed entry points."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset, causal, window, softmax_type, scale):
+        ctx.kw = dict(causal=causal, window=window, softmax_type=softmax_type, scale=scale)
+        o, lse = sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset=softmax_offset, **ctx.kw)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
+        return o
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, o, lse, cu_q, cu_kv, off = ctx.saved_tensors
+        dq, dk, dv, d_off = sdpa_backward_packed(q, k, v, o, dout.contiguous(), lse, cu_q, cu_kv, softmax_offset=off,
+                                                 **ctx.kw)
+        return dq, dk, dv, None, None, d_off, None, None, None, None
+
+
+def attention_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv=None, softmax_offset=None, *, causal=True, window=-1,
+                     softmax_type=VANILLA, scale=0.0):
+    """Differentiable attention over packed sequences: q [T_q, H_q, d_qk], k [T_kv, H_kv, d_qk],
+    v [T_kv, H_kv, d_v]; q, k, v and the learnable offset receive gradients."""
+    return SDPAPackedFunction.apply(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset, causal, window,
+                                    softmax_type, scale)
+
+
+# ----------------------------------------------------------------------------- 4-bit paged cache
 
 
 def kv4_pool(n_pages, H_kv, d, page_size, *, n_layers=None, device="cuda"):
@@ -675,13 +836,6 @@ def _check_paged(pool, page_table, seq_lens, d):
     if seq_lens.shape[0] != B:
         raise ValueError(f"seq_lens: one length per row of page_table ({B}), got {seq_lens.shape[0]}")
     return B, n_pages, H_kv, page_size, max_pages
-
-
-def _check_cu(cu, name, B=None):
-    _check(cu, name, torch.int32, 1)
-    if cu.shape[0] < 1 or (B is not None and cu.shape[0] != B + 1):
-        raise ValueError(f"{name} must hold one offset per sequence and the end"
-                         + (f" ({B + 1} values)" if B is not None else "") + f", got {cu.shape[0]}")
 
 
 def _check_rows(t, name, H, d):

@@ -95,7 +95,8 @@ enum KvSite { kKvFull = 0x20, kKvQFull, kKvQEmpty, kKvS, kKvDP, kKvP, kKvDS, kKv
 // PERSIST: the CTAs take tiles from a counter in global memory until it runs out; otherwise
 // the grid has one CTA per tile and the tile loops below run once (the cross-tile barriers
 // compile away).
-template <int D_QK, int D_V, bool FUSE_DQ, bool VL, bool BIAS = false, bool DROP = false, bool PERSIST = false>
+template <int D_QK, int D_V, bool FUSE_DQ, bool VL, bool BIAS = false, bool DROP = false, bool PERSIST = false,
+          bool PK = false>
 __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
     attn_bwd_kv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
                        const BwdParams p) {
   using C = KvCfg<D_QK, D_V, FUSE_DQ, BIAS>;
   static_assert(!DROP || (!BIAS && !VL), "dropout: full-length batches without a bias");
+  static_assert(!PK || (VL && !BIAS && !DROP && !FUSE_DQ && !PERSIST), "packed: the deterministic form");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -140,15 +142,38 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
   // slots and barrier phases.
   const int n_kv = (p.S_kv + C::BN - 1) / C::BN;
   const int n_gr = p.H_kv * p.B * p.ns;  // group = (b, kv head, head split)
-  const int n_tiles = n_kv * n_gr;
+  const int n_tiles = PK ? p.counts->kv_tiles * p.H_kv * p.ns : n_kv * n_gr;
+  if (PK && (int)blockIdx.x >= n_tiles) return;  // the grid is the host's bound on the tiles
+  // packed: a tile that ends past its sequence lands on this barrier first (the ring's place)
+  [[maybe_unused]] uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_TMEM_SLOT + 8);
   const int per_chunk = kKvChunk * n_kv;
   const int Gs = p.G / p.ns;  // query heads a tile walks
   struct Tile {
     int b, hk, split, h0, n0, ilo, nq, nsteps;
+    int qr, kr, wr;  // packed: the sequence's first row in q, in k and v, and in the workspace (else 0)
     MaskSpec mask;
   };
   auto tile_of = [&](int ti) {
     Tile t;
+    if constexpr (PK) {  // the plan lists the kv tiles; (kv head, head split) innermost
+      const int nh = p.H_kv * p.ns;
+      const PackedTile e = load_packed_tile(p.tiles_kv, ti / nh);
+      t.b = 0;
+      t.split = ti % nh % p.ns;
+      t.hk = ti % nh / p.ns;
+      t.h0 = t.hk * p.G + t.split * Gs;
+      t.n0 = e.m0;
+      t.qr = e.q0;
+      t.kr = e.k0;
+      t.wr = e.ws0;
+      t.mask = MaskSpec{e.Lq, e.Lk, p.causal, p.window};
+      int hi = -1;
+      t.ilo = 0;
+      t.nq = q_tile_range(t.mask, t.n0, t.n0 + C::BN - 1, C::BQ, &t.ilo, &hi) ? hi - t.ilo + 1 : 0;
+      t.nsteps = t.nq * Gs;
+      return t;
+    }
+    t.qr = t.kr = t.wr = 0;
     const int chunk = ti / per_chunk, within = ti % per_chunk;
     const int csize = min(kKvChunk, n_gr - chunk * kKvChunk);
     const int g = chunk * kKvChunk + within % csize;
@@ -193,6 +218,7 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
   };
 
   if (threadIdx.x == 0) {
+    if constexpr (PK) mbar_init(raw_full, 1);
     mbar_init(kv_full, 1);
     for (int s = 0; s < C::NQ; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
     mbar_init(&s_ready[0], 1);
@@ -228,7 +254,15 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
 
   if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    // Packed: the whole warp walks the steps, its first lane issues.  Rows past a sequence's end
+    // belong to the next one: their P and dS are 0, but 0 times an infinity or NaN is NaN, so
+    // the rows of K, V, Q and dO past the end are zeroed once their tile has landed.
+    if (PK || lane == 0) {
+      const bool lead = !PK || lane == 0;
+      [[maybe_unused]] int n_raw = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+        return PK ? mbar_wait_warp(bar, parity, err, site) : mbar_wait(bar, parity, err, site);
+      };
       const bool btma = BIAS && p.bias_tma;  // each stage also brings the step's bias tile
       bool ok = true, first = true;
       int g0 = 0, ne = 0;  // steps and non-empty tiles so far
@@ -250,7 +284,7 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
           if constexpr (PERSIST) ti_next = atomicAdd(p.tile_counter, 1);
           continue;
         }
-        if (first) {
+        if (first && lead) {
           tma_prefetch_desc(&tmQ);
           tma_prefetch_desc(&tmK);
           tma_prefetch_desc(&tmV);
@@ -260,31 +294,55 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
         }
         // K/V of this tile replace the previous tile's once its S, dP (and dQ^T) products are done
         if (PERSIST && ne > 0 && !mbar_wait(kv_empty, (ne - 1) & 1, err, kKvEmpty)) break;
-        mbar_arrive_expect_tx(kv_full, (C::QCH + C::VCH) * C::KCHUNK);
-        for (int c = 0; c < C::QCH; ++c)
-          tma_load_4d(smem + C::OFF_K + c * C::KCHUNK, &tmK, kv_full, c * 64, t.hk, t.n0, t.b);
-        for (int c = 0; c < C::VCH; ++c)
-          tma_load_4d(smem + C::OFF_V + c * C::KCHUNK, &tmV, kv_full, c * 64, t.hk, t.n0, t.b);
+        const int k_real = PK ? t.mask.S_kv - t.n0 : C::BN;  // keys of this tile that are the sequence's
+        uint64_t* kv_bar = k_real < C::BN ? raw_full : kv_full;
+        if (lead) {
+          mbar_arrive_expect_tx(kv_bar, (C::QCH + C::VCH) * C::KCHUNK);
+          for (int c = 0; c < C::QCH; ++c)
+            tma_load_4d(smem + C::OFF_K + c * C::KCHUNK, &tmK, kv_bar, c * 64, t.hk, t.kr + t.n0, t.b);
+          for (int c = 0; c < C::VCH; ++c)
+            tma_load_4d(smem + C::OFF_V + c * C::KCHUNK, &tmV, kv_bar, c * 64, t.hk, t.kr + t.n0, t.b);
+        }
+        if (PK && k_real < C::BN) {
+          if (!wait(raw_full, n_raw++ & 1, kKvFull)) break;
+          zero_tile_rows(smem + C::OFF_K, C::QCH + C::VCH, C::KCHUNK, C::BN, k_real, lane);  // V follows K
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lead) mbar_arrive(kv_full);
+        }
         for (int s = 0; s < t.nsteps; ++s) {
           const int g = g0 + s, st = g % C::NQ;
-          if (!mbar_wait(&q_empty[st], ((g / C::NQ) & 1) ^ 1, err, kKvQEmpty)) {
+          if (!wait(&q_empty[st], ((g / C::NQ) & 1) ^ 1, kKvQEmpty)) {
             ok = false;
             break;
           }
           const int h = t.h0 + s / t.nq;
           const int q0 = (t.ilo + s % t.nq) * C::BQ;
-          mbar_arrive_expect_tx(&q_full[st], C::Q_STAGE + C::DO_STAGE + C::L_STAGE + (btma ? C::B_STAGE : 0));
-          if (btma)  // rows past S_q and keys past S_kv come in as zeros
-            tma_load_4d(smem + C::OFF_B + st * C::B_STAGE, &tmB, &q_full[st], t.n0, q0, p.bias_sh ? h : 0,
-                        p.bias_sb ? t.b : 0);
-          for (int c = 0; c < C::QCH; ++c)
-            tma_load_4d(smem + C::OFF_Q + st * C::Q_STAGE + c * C::QCHUNK, &tmQ, &q_full[st], c * 64, h, q0, t.b);
-          for (int c = 0; c < C::VCH; ++c)
-            tma_load_4d(smem + C::OFF_DO + st * C::DO_STAGE + c * C::QCHUNK, &tmDO, &q_full[st], c * 64, h, q0,
-                        t.b);
-          const size_t row = ((size_t)t.b * p.H_q + h) * p.S_pad + q0;
-          bulk_load(smem + C::OFF_L + st * C::L_STAGE, p.nlse2 + row, C::BQ * 4, &q_full[st]);
-          bulk_load(smem + C::OFF_L + st * C::L_STAGE + C::BQ * 4, p.Dsum + row, C::BQ * 4, &q_full[st]);
+          const int q_real = PK ? t.mask.S_q - q0 : C::BQ;  // rows of this step that are the sequence's
+          uint64_t* q_bar = q_real < C::BQ ? raw_full : &q_full[st];
+          if (lead) {
+            mbar_arrive_expect_tx(q_bar, C::Q_STAGE + C::DO_STAGE + C::L_STAGE + (btma ? C::B_STAGE : 0));
+            if (btma)  // rows past S_q and keys past S_kv come in as zeros
+              tma_load_4d(smem + C::OFF_B + st * C::B_STAGE, &tmB, &q_full[st], t.n0, q0, p.bias_sh ? h : 0,
+                          p.bias_sb ? t.b : 0);
+            for (int c = 0; c < C::QCH; ++c)
+              tma_load_4d(smem + C::OFF_Q + st * C::Q_STAGE + c * C::QCHUNK, &tmQ, q_bar, c * 64, h, t.qr + q0, t.b);
+            for (int c = 0; c < C::VCH; ++c)
+              tma_load_4d(smem + C::OFF_DO + st * C::DO_STAGE + c * C::QCHUNK, &tmDO, q_bar, c * 64, h, t.qr + q0,
+                          t.b);
+            const size_t row = ((size_t)t.b * p.H_q + h) * p.S_pad + t.wr + q0;
+            bulk_load(smem + C::OFF_L + st * C::L_STAGE, p.nlse2 + row, C::BQ * 4, q_bar);
+            bulk_load(smem + C::OFF_L + st * C::L_STAGE + C::BQ * 4, p.Dsum + row, C::BQ * 4, q_bar);
+          }
+          if (PK && q_real < C::BQ) {
+            ok = wait(raw_full, n_raw++ & 1, kKvQFull);
+            if (!ok) break;
+            zero_tile_rows(smem + C::OFF_Q + st * C::Q_STAGE, C::QCH, C::QCHUNK, C::BQ, q_real, lane);
+            zero_tile_rows(smem + C::OFF_DO + st * C::DO_STAGE, C::VCH, C::QCHUNK, C::BQ, q_real, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lead) mbar_arrive(&q_full[st]);
+          }
         }
         // the next tile is taken once this one's loads are issued: late enough that the
         // counter still balances the last tiles, early enough to hide the atomic
@@ -567,8 +625,8 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
         tc_fence_after();
       }
       {
-        const bool row_ok = key < p.S_kv;  // all lanes load TMEM; only real keys store
-        const int krow = row_ok ? key : 0;
+        const bool row_ok = key < (PK ? t.mask.S_kv : p.S_kv);  // all lanes load TMEM; only real keys store
+        const int krow = t.kr + (row_ok ? key : 0);
         const int ncols = w == 0 ? D_V : D_QK;
         const int col0 = w == 0 ? C::COL_DV : C::COL_DK;
         const float mul = w == 0 ? (DROP ? p.drop_scale : 1.f) : p.scale;
@@ -769,13 +827,16 @@ enum QSite { kQQ = 0x40, kQKFull, kQKEmpty, kQVFull, kQVEmpty, kQS, kQDP, kQDS, 
 // PERSIST: the CTAs (one per SM) take tiles from a counter in global memory, as the
 // persistent kv kernels do; otherwise the grid has one CTA per tile and the tile loops
 // run once (the cross-tile barriers compile away).
-template <int D_QK, int D_V, bool VL, bool BIAS = false, bool DROP = false, bool PERSIST = false>
+template <int D_QK, int D_V, bool VL, bool BIAS = false, bool DROP = false, bool PERSIST = false, bool PK = false,
+          bool ROWSUM = false>
 __global__ void __launch_bounds__(352, 1)
     attn_bwd_q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                       const BwdParams p) {
   using C = QCfg<D_QK, D_V>;
   static_assert(!DROP || (!BIAS && !VL), "dropout: full-length batches without a bias");
+  static_assert(!PK || (VL && !BIAS && !DROP && !PERSIST), "packed: one CTA per tile");
+  static_assert(!ROWSUM || PK, "row sums of dS: packed batches with a learnable sink");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -805,14 +866,34 @@ __global__ void __launch_bounds__(352, 1)
   // and numbers the kv tiles of all of them in one sequence n (stages, barrier phases).
   const int n_qt = (p.S_q + C::BM - 1) / C::BM;
   const int n_gr = p.H_q * p.B;
-  const int n_tiles = n_qt * n_gr;
+  const int n_tiles = PK ? p.counts->q_tiles * p.H_q : n_qt * n_gr;
+  if (PK && (int)blockIdx.x >= n_tiles) return;  // the grid is the host's bound on the tiles
+  // packed: a kv tile that ends past its sequence lands on this barrier first (the ring's place)
+  [[maybe_unused]] uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_TMEM_SLOT + 8);
   const int per_chunk = kKvChunk * n_qt;
   struct Tile {
     int b, h, hk, m0, jlo, nj;
+    int qr, kr, wr;  // packed: the sequence's first row in q, in k and v, and in the workspace (else 0)
     MaskSpec mask;
   };
   auto tile_of = [&](int ti) {
     Tile t;
+    if constexpr (PK) {  // the plan lists the query tiles; heads innermost
+      const PackedTile e = load_packed_tile(p.tiles_q, ti / p.H_q);
+      t.b = 0;
+      t.h = ti % p.H_q;
+      t.hk = t.h / p.G;
+      t.m0 = e.m0;
+      t.qr = e.q0;
+      t.kr = e.k0;
+      t.wr = e.ws0;
+      t.mask = MaskSpec{e.Lq, e.Lk, p.causal, p.window};
+      int hi = 0;
+      t.jlo = 1;
+      t.nj = kv_tile_range(t.mask, t.m0, t.m0 + C::BM - 1, C::BN, &t.jlo, &hi) ? hi - t.jlo + 1 : 0;
+      return t;
+    }
+    t.qr = t.kr = t.wr = 0;
     const int chunk = ti / per_chunk, within = ti % per_chunk;
     const int csize = min(kKvChunk, n_gr - chunk * kKvChunk);
     const int g = chunk * kKvChunk + within % csize;
@@ -848,6 +929,7 @@ __global__ void __launch_bounds__(352, 1)
   };
 
   if (threadIdx.x == 0) {
+    if constexpr (PK) mbar_init(raw_full, 1);
     mbar_init(q_full, 1);
     for (int s = 0; s < C::NK; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
     for (int s = 0; s < C::NV; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1); }
@@ -879,7 +961,23 @@ __global__ void __launch_bounds__(352, 1)
   int* err = p.err;
 
   if (warp == 9) {
-    if (lane == 0) {
+    // Packed: as in the kv kernel; here only K and V rows past the sequence's end can reach
+    // another row (Q and dO rows past it stay in their own).
+    if (PK || lane == 0) {
+      const bool lead = !PK || lane == 0;
+      [[maybe_unused]] int n_raw = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+        return PK ? mbar_wait_warp(bar, parity, err, site) : mbar_wait(bar, parity, err, site);
+      };
+      // rows from `real` on of a landed tile: zeroed, then the tile counts as full
+      [[maybe_unused]] auto clear_rest = [&](uint8_t* base, int chunks, int real, uint64_t* full, int site) {
+        if (!wait(raw_full, n_raw++ & 1, site)) return false;
+        zero_tile_rows(base, chunks, C::CHUNK, C::BN, real, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lead) mbar_arrive(full);
+        return true;
+      };
       bool ok = true, first = true;
       int n0 = 0, ne = 0, ti_next = 0;  // kv tiles and non-empty tiles so far
       for (int k = 0;; ++k) {
@@ -899,7 +997,7 @@ __global__ void __launch_bounds__(352, 1)
           if constexpr (PERSIST) ti_next = atomicAdd(p.tile_counter_q, 1);
           continue;
         }
-        if (first) {
+        if (first && lead) {
           tma_prefetch_desc(&tmQ);
           tma_prefetch_desc(&tmK);
           tma_prefetch_desc(&tmV);
@@ -908,30 +1006,48 @@ __global__ void __launch_bounds__(352, 1)
         }
         // Q/dO of this tile replace the previous tile's once its S and dP products are done
         if (PERSIST && ne > 0 && !mbar_wait(qo_empty, (ne - 1) & 1, err, kQQEmpty)) break;
-        mbar_arrive_expect_tx(q_full, (C::QCH + C::VCH) * C::CHUNK);
-        for (int c = 0; c < C::QCH; ++c)
-          tma_load_4d(smem + C::OFF_Q + c * C::CHUNK, &tmQ, q_full, c * 64, t.h, t.m0, t.b);
-        for (int c = 0; c < C::VCH; ++c)
-          tma_load_4d(smem + C::OFF_DO + c * C::CHUNK, &tmDO, q_full, c * 64, t.h, t.m0, t.b);
+        if (lead) {
+          mbar_arrive_expect_tx(q_full, (C::QCH + C::VCH) * C::CHUNK);
+          for (int c = 0; c < C::QCH; ++c)
+            tma_load_4d(smem + C::OFF_Q + c * C::CHUNK, &tmQ, q_full, c * 64, t.h, t.qr + t.m0, t.b);
+          for (int c = 0; c < C::VCH; ++c)
+            tma_load_4d(smem + C::OFF_DO + c * C::CHUNK, &tmDO, q_full, c * 64, t.h, t.qr + t.m0, t.b);
+        }
         for (int j0 = 0; j0 < t.nj; ++j0) {
           const int n = n0 + j0, j = t.jlo + j0;
           const int sk = n % C::NK, sv = n % C::NV;
-          if (!mbar_wait(&k_empty[sk], ((n / C::NK) & 1) ^ 1, err, kQKEmpty)) {
+          const int real = PK ? t.mask.S_kv - j * C::BN : C::BN;  // keys of this tile that are the sequence's
+          const bool part = PK && real < C::BN;
+          if (!wait(&k_empty[sk], ((n / C::NK) & 1) ^ 1, kQKEmpty)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&k_full[sk], C::QCH * C::CHUNK);
-          for (int c = 0; c < C::QCH; ++c)
-            tma_load_4d(smem + C::OFF_K + (sk * C::QCH + c) * C::CHUNK, &tmK, &k_full[sk], c * 64, t.hk, j * C::BN,
-                        t.b);
-          if (!mbar_wait(&v_empty[sv], ((n / C::NV) & 1) ^ 1, err, kQVEmpty)) {
+          if (lead) {
+            uint64_t* bar = part ? raw_full : &k_full[sk];
+            mbar_arrive_expect_tx(bar, C::QCH * C::CHUNK);
+            for (int c = 0; c < C::QCH; ++c)
+              tma_load_4d(smem + C::OFF_K + (sk * C::QCH + c) * C::CHUNK, &tmK, bar, c * 64, t.hk, t.kr + j * C::BN,
+                          t.b);
+          }
+          if (part && !clear_rest(smem + C::OFF_K + sk * C::QCH * C::CHUNK, C::QCH, real, &k_full[sk], kQKFull)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&v_full[sv], C::VCH * C::CHUNK);
-          for (int c = 0; c < C::VCH; ++c)
-            tma_load_4d(smem + C::OFF_V + (sv * C::VCH + c) * C::CHUNK, &tmV, &v_full[sv], c * 64, t.hk, j * C::BN,
-                        t.b);
+          if (!wait(&v_empty[sv], ((n / C::NV) & 1) ^ 1, kQVEmpty)) {
+            ok = false;
+            break;
+          }
+          if (lead) {
+            uint64_t* bar = part ? raw_full : &v_full[sv];
+            mbar_arrive_expect_tx(bar, C::VCH * C::CHUNK);
+            for (int c = 0; c < C::VCH; ++c)
+              tma_load_4d(smem + C::OFF_V + (sv * C::VCH + c) * C::CHUNK, &tmV, bar, c * 64, t.hk, t.kr + j * C::BN,
+                          t.b);
+          }
+          if (part && !clear_rest(smem + C::OFF_V + sv * C::VCH * C::CHUNK, C::VCH, real, &v_full[sv], kQVFull)) {
+            ok = false;
+            break;
+          }
         }
         if constexpr (PERSIST) ti_next = atomicAdd(p.tile_counter_q, 1);
         n0 += t.nj;
@@ -1054,8 +1170,9 @@ __global__ void __launch_bounds__(352, 1)
     const int b = t.b, h = t.h;
     const int i = t.m0 + r;
     float nl2row = -INFINITY, drow = 0.f;
-    if (i < p.S_q && t.nj > 0) {
-      const size_t ri = ((size_t)b * p.H_q + h) * p.S_pad + i;
+    [[maybe_unused]] uint64_t rs2 = 0ull;  // ROWSUM: this row's sum of dS over its 64-key halves, paired
+    if (i < (PK ? t.mask.S_q : p.S_q) && t.nj > 0) {
+      const size_t ri = ((size_t)b * p.H_q + h) * p.S_pad + t.wr + i;
       nl2row = p.nlse2[ri];
       drow = p.Dsum[ri];
     }
@@ -1152,6 +1269,7 @@ __global__ void __launch_bounds__(352, 1)
                              f2_sub(f2_pack(__uint_as_float(rr[2 * c]), __uint_as_float(rr[2 * c + 1])), drow2)),
                       a, bq);
           }
+          if constexpr (ROWSUM) rs2 = f2_add(rs2, f2_pack(a, bq));
           pk[c] = pack_bf16x2(a, bq);
         }
         tmem_st16(lane_addr + colP + 64 * w + c0 / 2, pk);
@@ -1168,8 +1286,13 @@ __global__ void __launch_bounds__(352, 1)
       tc_fence_after();
     }
     {
-      const bool row_ok = i < p.S_q;  // all lanes load TMEM; only real rows store
-      __nv_bfloat16* dst = p.dq + (((size_t)b * p.S_q + (row_ok ? i : 0)) * p.H_q + h) * D_QK;
+      const bool row_ok = i < (PK ? t.mask.S_q : p.S_q);  // all lanes load TMEM; only real rows store
+      if constexpr (ROWSUM) {
+        float sa, sb;
+        f2_unpack(rs2, sa, sb);
+        if (row_ok) p.ds_rowsum[((size_t)w * p.H_q + h) * p.S_pad + t.wr + i] = sa + sb;
+      }
+      __nv_bfloat16* dst = p.dq + (((size_t)b * p.S_q + t.qr + (row_ok ? i : 0)) * p.H_q + h) * D_QK;
       constexpr int HALF = D_QK / 2;
 #pragma unroll 1
       for (int c0 = w * HALF; c0 < (w + 1) * HALF; c0 += 32) {

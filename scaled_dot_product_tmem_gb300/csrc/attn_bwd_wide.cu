@@ -67,12 +67,13 @@ enum KvWSite { kWFull = 0x80, kWQFull, kWQEmpty, kWS, kWDP, kWP, kWDS, kWDvDone,
 // PERSIST: the CTAs (one per SM) take tiles from a counter in global memory, as the
 // persistent fused-dQ kernel does; otherwise the grid has one CTA per tile and the tile
 // loops run once (the cross-tile barriers compile away).
-template <int D_QK, int D_V, bool VL, bool PERSIST = false>
+template <int D_QK, int D_V, bool VL, bool PERSIST = false, bool PK = false>
 __global__ void __launch_bounds__(352, 1)
     attn_bwd_kvw_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                         const BwdParams p) {
   using C = KvWCfg<D_QK, D_V>;
+  static_assert(!PK || (VL && !PERSIST), "packed: one CTA per tile");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -100,15 +101,38 @@ __global__ void __launch_bounds__(352, 1)
   // numbers the steps of all of them in one sequence g (stages, barrier phases).
   const int n_kv = (p.S_kv + C::BN - 1) / C::BN;
   const int n_gr = p.H_kv * p.B * p.ns;
-  const int n_tiles = n_kv * n_gr;
+  const int n_tiles = PK ? p.counts->kv_tiles * p.H_kv * p.ns : n_kv * n_gr;
+  if (PK && (int)blockIdx.x >= n_tiles) return;  // the grid is the host's bound on the tiles
+  // packed: a tile that ends past its sequence lands on this barrier first (the ring's place)
+  [[maybe_unused]] uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_TMEM_SLOT + 8);
   const int per_chunk = kKvChunk * n_kv;
   const int Gs = p.G / p.ns;
   struct Tile {
     int b, hk, split, h0, n0, ilo, nq, nsteps;
+    int qr, kr, wr;  // packed: the sequence's first row in q, in k and v, and in the workspace (else 0)
     MaskSpec mask;
   };
   auto tile_of = [&](int ti) {
     Tile t;
+    if constexpr (PK) {  // the plan lists the kv tiles; (kv head, head split) innermost
+      const int nh = p.H_kv * p.ns;
+      const PackedTile e = load_packed_tile(p.tiles_kv, ti / nh);
+      t.b = 0;
+      t.split = ti % nh % p.ns;
+      t.hk = ti % nh / p.ns;
+      t.h0 = t.hk * p.G + t.split * Gs;
+      t.n0 = e.m0;
+      t.qr = e.q0;
+      t.kr = e.k0;
+      t.wr = e.ws0;
+      t.mask = MaskSpec{e.Lq, e.Lk, p.causal, p.window};
+      int hi = -1;
+      t.ilo = 0;
+      t.nq = q_tile_range(t.mask, t.n0, t.n0 + C::BN - 1, C::BQ, &t.ilo, &hi) ? hi - t.ilo + 1 : 0;
+      t.nsteps = t.nq * Gs;
+      return t;
+    }
+    t.qr = t.kr = t.wr = 0;
     const int chunk = ti / per_chunk, within = ti % per_chunk;
     const int csize = min(kKvChunk, n_gr - chunk * kKvChunk);
     const int g = chunk * kKvChunk + within % csize;
@@ -145,6 +169,7 @@ __global__ void __launch_bounds__(352, 1)
   };
 
   if (threadIdx.x == 0) {
+    if constexpr (PK) mbar_init(raw_full, 1);
     mbar_init(kv_full, 1);
     for (int s = 0; s < C::NQ; ++s) {
       mbar_init(&q_full[s], 1);
@@ -178,7 +203,14 @@ __global__ void __launch_bounds__(352, 1)
 
   if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    // Packed: as in the 64-row kernel, the whole warp walks the steps, and rows of K, V, Q and
+    // dO past the sequence's end are zeroed once their tile has landed.
+    if (PK || lane == 0) {
+      const bool lead = !PK || lane == 0;
+      [[maybe_unused]] int n_raw = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+        return PK ? mbar_wait_warp(bar, parity, err, site) : mbar_wait(bar, parity, err, site);
+      };
       bool ok = true, first = true;
       int g0 = 0, ne = 0, ti_next = 0;
       for (int k = 0;; ++k) {
@@ -198,7 +230,7 @@ __global__ void __launch_bounds__(352, 1)
           if constexpr (PERSIST) ti_next = atomicAdd(p.tile_counter, 1);
           continue;
         }
-        if (first) {
+        if (first && lead) {
           tma_prefetch_desc(&tmQ);
           tma_prefetch_desc(&tmK);
           tma_prefetch_desc(&tmV);
@@ -206,29 +238,53 @@ __global__ void __launch_bounds__(352, 1)
           first = false;
         }
         if (PERSIST && ne > 0 && !mbar_wait(kv_empty, (ne - 1) & 1, err, kWEmpty)) break;
-        mbar_arrive_expect_tx(kv_full, (C::QCH + C::VCH) * C::KCHUNK);
-        for (int c = 0; c < C::QCH; ++c)
-          tma_load_4d(smem + C::OFF_K + c * C::KCHUNK, &tmK, kv_full, c * 64, t.hk, t.n0, t.b);
-        for (int c = 0; c < C::VCH; ++c)
-          tma_load_4d(smem + C::OFF_V + c * C::KCHUNK, &tmV, kv_full, c * 64, t.hk, t.n0, t.b);
+        const int k_real = PK ? t.mask.S_kv - t.n0 : C::BN;  // keys of this tile that are the sequence's
+        if (lead) {
+          uint64_t* bar = k_real < C::BN ? raw_full : kv_full;
+          mbar_arrive_expect_tx(bar, (C::QCH + C::VCH) * C::KCHUNK);
+          for (int c = 0; c < C::QCH; ++c)
+            tma_load_4d(smem + C::OFF_K + c * C::KCHUNK, &tmK, bar, c * 64, t.hk, t.kr + t.n0, t.b);
+          for (int c = 0; c < C::VCH; ++c)
+            tma_load_4d(smem + C::OFF_V + c * C::KCHUNK, &tmV, bar, c * 64, t.hk, t.kr + t.n0, t.b);
+        }
+        if (PK && k_real < C::BN) {
+          if (!wait(raw_full, n_raw++ & 1, kWFull)) break;
+          zero_tile_rows(smem + C::OFF_K, C::QCH + C::VCH, C::KCHUNK, C::BN, k_real, lane);  // V follows K
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lead) mbar_arrive(kv_full);
+        }
         for (int s = 0; s < t.nsteps; ++s) {
           const int g = g0 + s, st = g % C::NQ;
-          if (!mbar_wait(&q_empty[st], ((g / C::NQ) & 1) ^ 1, err, kWQEmpty)) {
+          if (!wait(&q_empty[st], ((g / C::NQ) & 1) ^ 1, kWQEmpty)) {
             ok = false;
             break;
           }
           const int h = t.h0 + s / t.nq;
           const int q0 = (t.ilo + s % t.nq) * C::BQ;
-          mbar_arrive_expect_tx(&q_full[st], C::Q_STAGE + C::DO_STAGE + C::L_STAGE);
-          for (int c = 0; c < C::QCH; ++c)
-            tma_load_4d(smem + C::OFF_Q + st * C::Q_STAGE + c * C::QCHUNK, &tmQ, &q_full[st], c * 64, h, q0, t.b);
-          for (int c = 0; c < C::VCH; ++c)
-            tma_load_4d(smem + C::OFF_DO + st * C::DO_STAGE + c * C::QCHUNK, &tmDO, &q_full[st], c * 64, h, q0,
-                        t.b);
-          // q0 + 128 <= S_pad: the rows are padded to a multiple of 128
-          const size_t row = ((size_t)t.b * p.H_q + h) * p.S_pad + q0;
-          bulk_load(smem + C::OFF_L + st * C::L_STAGE, p.nlse2 + row, C::BQ * 4, &q_full[st]);
-          bulk_load(smem + C::OFF_L + st * C::L_STAGE + C::BQ * 4, p.Dsum + row, C::BQ * 4, &q_full[st]);
+          const int q_real = PK ? t.mask.S_q - q0 : C::BQ;  // rows of this step that are the sequence's
+          if (lead) {
+            uint64_t* bar = q_real < C::BQ ? raw_full : &q_full[st];
+            mbar_arrive_expect_tx(bar, C::Q_STAGE + C::DO_STAGE + C::L_STAGE);
+            for (int c = 0; c < C::QCH; ++c)
+              tma_load_4d(smem + C::OFF_Q + st * C::Q_STAGE + c * C::QCHUNK, &tmQ, bar, c * 64, h, t.qr + q0, t.b);
+            for (int c = 0; c < C::VCH; ++c)
+              tma_load_4d(smem + C::OFF_DO + st * C::DO_STAGE + c * C::QCHUNK, &tmDO, bar, c * 64, h, t.qr + q0,
+                          t.b);
+            // q0 + 128 <= the sequence's padded rows: they are a multiple of 128
+            const size_t row = ((size_t)t.b * p.H_q + h) * p.S_pad + t.wr + q0;
+            bulk_load(smem + C::OFF_L + st * C::L_STAGE, p.nlse2 + row, C::BQ * 4, bar);
+            bulk_load(smem + C::OFF_L + st * C::L_STAGE + C::BQ * 4, p.Dsum + row, C::BQ * 4, bar);
+          }
+          if (PK && q_real < C::BQ) {
+            ok = wait(raw_full, n_raw++ & 1, kWQFull);
+            if (!ok) break;
+            zero_tile_rows(smem + C::OFF_Q + st * C::Q_STAGE, C::QCH, C::QCHUNK, C::BQ, q_real, lane);
+            zero_tile_rows(smem + C::OFF_DO + st * C::DO_STAGE, C::VCH, C::QCHUNK, C::BQ, q_real, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lead) mbar_arrive(&q_full[st]);
+          }
         }
         if constexpr (PERSIST) ti_next = atomicAdd(p.tile_counter, 1);
         g0 += t.nsteps;
@@ -447,8 +503,8 @@ __global__ void __launch_bounds__(352, 1)
         tc_fence_after();
       }
       {
-        const bool row_ok = key < p.S_kv;  // all lanes load TMEM; only real keys store
-        const int krow = row_ok ? key : 0;
+        const bool row_ok = key < (PK ? t.mask.S_kv : p.S_kv);  // all lanes load TMEM; only real keys store
+        const int krow = t.kr + (row_ok ? key : 0);
         const int ncols = w == 0 ? D_V : D_QK;
         const int col0 = w == 0 ? C::COL_DV : C::COL_DK;
         const float mul = w == 0 ? 1.f : p.scale;
@@ -542,6 +598,26 @@ int launch_bwd_kv_wide(int d_qk, int d_v, const CUtensorMap& tq128, const CUtens
   if (p.bias || p.drop_t) return -2;
   if (d_qk == 128 && d_v == 128) return launch_kvw_t<128, 128>(tq128, tk, tv, tdo128, p, stream);
   if (d_qk == 64 && d_v == 64) return launch_kvw_t<64, 64>(tq128, tk, tv, tdo128, p, stream);
+  return -2;
+}
+
+// The packed form: one CTA per listed tile (those of the bound past the list end at once).
+template <int D_QK, int D_V>
+static int launch_kvw_packed_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& tdo, const BwdParams& p, cudaStream_t stream) {
+  using C = KvWCfg<D_QK, D_V>;
+  const long long grid = p.tile_bound_kv * p.H_kv * p.ns;
+  if (grid <= 0 || grid > 0x7fffffffLL) return -2;
+  auto kern = attn_bwd_kvw_kernel<D_QK, D_V, true, false, true>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
+  kern<<<(unsigned)grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tdo, p);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_bwd_kv_wide_packed(int d, const CUtensorMap& tq128, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo128, const BwdParams& p, cudaStream_t stream) {
+  if (d == 128) return launch_kvw_packed_t<128, 128>(tq128, tk, tv, tdo128, p, stream);
+  if (d == 64) return launch_kvw_packed_t<64, 64>(tq128, tk, tv, tdo128, p, stream);
   return -2;
 }
 

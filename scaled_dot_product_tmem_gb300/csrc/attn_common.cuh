@@ -12,6 +12,7 @@
 // TransformerEngine", step 7: query i sees keys j <= i.)
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 #include <cstdint>
 
@@ -95,6 +96,37 @@ __host__ __device__ __forceinline__ bool tile_fully_visible(const MaskSpec& m, i
   if (m.causal && k1 > r0) return false;
   if (m.window >= 0 && k0 < r1 - m.window) return false;
   return true;
+}
+
+// A packed batch (sequences one after another in [T, H, d] tensors): one work tile of a
+// kernel, as the plan kernel lists it.  q0 / k0: the sequence's first query / key row in the
+// packed tensors; Lq / Lk its lengths; m0 the tile's first row within the sequence; ws0 the
+// sequence's first row in workspace rows padded to multiples of 128.
+struct PackedTile {
+  int q0, Lq, k0, Lk, b, m0, ws0, unused;
+};
+static_assert(sizeof(PackedTile) == 32, "read as two 16-byte words");
+
+__device__ __forceinline__ PackedTile load_packed_tile(const PackedTile* t, int i) {
+  const int4* w = reinterpret_cast<const int4*>(t + i);
+  const int4 a = __ldg(w), b = __ldg(w + 1);
+  return PackedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+// What the plan of a packed batch counts.
+struct PackedCounts {
+  int fwd_tiles, kv_tiles, q_tiles;  // entries of the tile lists
+  int q_end, kv_end;                 // rows of the last sequence end here: rows past them are no sequence's
+  int unused[3];
+};
+
+// Zero rows [from, rows) of `chunks` shared-memory chunks of rows x 128 bytes (a warp).  Whole
+// 128-byte rows: the swizzle permutes bytes inside a row only.
+__device__ __forceinline__ void zero_tile_rows(uint8_t* base, int chunks, int chunk_bytes, int rows, int from,
+                                               int lane) {
+  for (int c = 0; c < chunks; ++c)
+    for (int o = from * 128 + lane * 16; o < rows * 128; o += 32 * 16)
+      *reinterpret_cast<uint4*>(base + c * chunk_bytes + o) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {

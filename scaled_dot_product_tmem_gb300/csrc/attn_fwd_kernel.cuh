@@ -91,27 +91,41 @@ struct FwdCfg {
 // [J0, J1] is the union.  Causal work is ordered heaviest query block first.
 struct FwdTile {
   int h, b, hk, m0, J0, J1;
+  int q0, k0;  // packed batch: the sequence's first row in q / in k and v (else 0)
   int jlo[2], jhi[2];
   bool exists[2], active[2], any;
   MaskSpec mask;  // with the entry's own lengths
 };
 
-template <int BM, int BN, bool VL>
+template <int BM, int BN, bool VL, bool PK = false>
 __device__ __forceinline__ FwdTile fwd_tile(const FwdParams& p, int nqb, int wi) {
   FwdTile T;
-  const int hb = wi % (p.H_q * p.B);
-  const int q = wi / (p.H_q * p.B);
-  const int qb = p.causal ? nqb - 1 - q : q;
-  T.h = hb % p.H_q;
-  T.b = hb / p.H_q;
-  T.hk = T.h / p.G;
-  T.m0 = qb * 2 * BM;
-  T.mask = VL ? MaskSpec{entry_len(p.seq_q, T.b, p.S_q), entry_len(p.seq_kv, T.b, p.S_kv), p.causal, p.window}
-              : MaskSpec{p.S_q, p.S_kv, p.causal, p.window};
+  if constexpr (PK) {  // the plan lists the tiles, most work first; every head takes each
+    const PackedTile e = load_packed_tile(p.tiles, wi / p.H_q);
+    T.h = wi % p.H_q;
+    T.b = 0;
+    T.m0 = e.m0;
+    T.q0 = e.q0;
+    T.k0 = e.k0;
+    T.mask = MaskSpec{e.Lq, e.Lk, p.causal, p.window};
+    T.hk = T.h / p.G;
+  } else {
+    const int hb = wi % (p.H_q * p.B);
+    const int q = wi / (p.H_q * p.B);
+    const int qb = p.causal ? nqb - 1 - q : q;
+    T.h = hb % p.H_q;
+    T.b = hb / p.H_q;
+    T.hk = T.h / p.G;
+    T.m0 = qb * 2 * BM;
+    T.q0 = T.k0 = 0;
+    T.mask = VL ? MaskSpec{entry_len(p.seq_q, T.b, p.S_q), entry_len(p.seq_kv, T.b, p.S_kv), p.causal, p.window}
+                : MaskSpec{p.S_q, p.S_kv, p.causal, p.window};
+  }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int r0 = T.m0 + t * BM;
-    T.exists[t] = r0 < p.S_q;  // rows of the padded tensor: they get an output either way
+    // rows of the padded tensor: they get an output either way
+    T.exists[t] = r0 < (PK ? T.mask.S_q : p.S_q);
     T.active[t] = T.exists[t] && kv_tile_range(T.mask, r0, r0 + BM - 1, BN, &T.jlo[t], &T.jhi[t]);
     if (!T.active[t]) { T.jlo[t] = 1; T.jhi[t] = 0; }
   }
@@ -128,7 +142,8 @@ enum FwdSite { kSiteQ = 1, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSi
 template <int D_QK, bool BIAS>
 constexpr bool fwd_bias_staged() { return BIAS && D_QK <= 128; }
 
-template <int D_QK, int D_V, int NK, int NV, bool VL, bool F8 = false, bool BIAS = false, bool DROP = false>
+template <int D_QK, int D_V, int NK, int NV, bool VL, bool F8 = false, bool BIAS = false, bool DROP = false,
+          bool PK = false>
 __global__ void __launch_bounds__(320, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmB,
@@ -136,6 +151,7 @@ __global__ void __launch_bounds__(320, 1)
   constexpr bool BT = fwd_bias_staged<D_QK, BIAS>();
   using C = FwdCfg<D_QK, D_V, NK, NV, F8, BT>;
   static_assert(!DROP || (!F8 && !BIAS && !VL), "dropout: full-length bf16 batches without a bias");
+  static_assert(!PK || (VL && !F8 && !BIAS && !DROP), "packed: the bf16 form with per-sequence lengths");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -157,9 +173,12 @@ __global__ void __launch_bounds__(320, 1)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int nqb = (p.S_q + 2 * C::BM - 1) / (2 * C::BM);
-  const int n_work = nqb * p.H_q * p.B;
+  const int n_work = PK ? p.counts->fwd_tiles * p.H_q : nqb * p.H_q * p.B;
+  // packed: a V tile that ends past its sequence lands on this barrier first (beside the TMEM address)
+  [[maybe_unused]] uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_TMEM_SLOT + 8);
 
   if (threadIdx.x == 0) {
+    if constexpr (PK) mbar_init(raw_full, 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < NK; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
@@ -192,36 +211,50 @@ __global__ void __launch_bounds__(320, 1)
   // ...; every role walks the same sequence and counts barrier phases across tiles.
   if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
+    // Packed: the whole warp walks the tiles, its first lane issues.  The rows of a sequence's
+    // last kv tile past its end belong to the next sequence (or to none): P is 0 there, but 0
+    // times an infinity or NaN is NaN, so those V rows are zeroed once the tile has landed.
+    if (PK || lane == 0) {
+      const bool lead = !PK || lane == 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+        return PK ? mbar_wait_warp(bar, parity, err, site) : mbar_wait(bar, parity, err, site);
+      };
+      [[maybe_unused]] int n_raw = 0;
+      if (lead) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
       if (b_tma) tma_prefetch_desc(&tmB);
       int n = 0, nw = 0;  // kv stages loaded, Q tiles loaded
       [[maybe_unused]] int nb[2] = {0, 0};  // bias tiles loaded per query tile
       bool ok = true;
       for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-        const FwdTile T = fwd_tile<C::BM, C::BN, VL>(p, nqb, wi);
+        const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi);
         if (!T.any) continue;
         // Q of the previous tile must have been read by that tile's last S MMAs
-        if (nw > 0) ok = mbar_wait(q_empty, (nw - 1) & 1, err, kSiteQ);
+        if (nw > 0) ok = wait(q_empty, (nw - 1) & 1, kSiteQ);
         if (!ok) break;
         const uint32_t qbytes = (T.active[0] ? C::Q_TILE : 0) + (T.active[1] ? C::Q_TILE : 0);
-        mbar_arrive_expect_tx(q_full, qbytes);
-        for (int t = 0; t < 2; ++t)
-          if (T.active[t])
-            for (int c = 0; c < C::QCH; ++c)
-              tma_load_4d(smem + C::OFF_Q + t * C::Q_TILE + c * C::CHUNK, &tmQ, q_full, c * 64, T.h,
-                          T.m0 + t * C::BM, T.b);
+        if (lead) {
+          mbar_arrive_expect_tx(q_full, qbytes);
+          for (int t = 0; t < 2; ++t)
+            if (T.active[t])
+              for (int c = 0; c < C::QCH; ++c)
+                tma_load_4d(smem + C::OFF_Q + t * C::Q_TILE + c * C::CHUNK, &tmQ, q_full, c * 64, T.h,
+                            T.q0 + T.m0 + t * C::BM, T.b);
+        }
         ++nw;
         for (int j = T.J0; j <= T.J1 && ok; ++j, ++n) {
           const int sk = n % NK, sv = n % NV;
-          ok = mbar_wait(&k_empty[sk], ((n / NK) & 1) ^ 1, err, kSiteKEmpty);
+          ok = wait(&k_empty[sk], ((n / NK) & 1) ^ 1, kSiteKEmpty);
           if (!ok) break;
-          mbar_arrive_expect_tx(&k_full[sk], C::K_STAGE);
-          for (int c = 0; c < C::QCH; ++c)
-            tma_load_4d(smem + C::OFF_K + sk * C::K_STAGE + c * C::CHUNK, &tmK, &k_full[sk], c * 64, T.hk,
-                        j * C::BN, T.b);
+          if (lead) {
+            mbar_arrive_expect_tx(&k_full[sk], C::K_STAGE);
+            for (int c = 0; c < C::QCH; ++c)
+              tma_load_4d(smem + C::OFF_K + sk * C::K_STAGE + c * C::CHUNK, &tmK, &k_full[sk], c * 64, T.hk,
+                          T.k0 + j * C::BN, T.b);
+          }
           if constexpr (BT) {
             // each query tile's bias tile for kv tile j, once its softmax has read the last one
             // (ahead of V(j), which is only needed after that softmax); the next one is
@@ -243,8 +276,27 @@ __global__ void __launch_bounds__(320, 1)
             }
           }
           if (!ok) break;
-          ok = mbar_wait(&v_empty[sv], ((n / NV) & 1) ^ 1, err, kSiteVEmpty);
+          ok = wait(&v_empty[sv], ((n / NV) & 1) ^ 1, kSiteVEmpty);
           if (!ok) break;
+          if constexpr (PK) {
+            const int real = T.mask.S_kv - j * C::BN;  // rows of this tile that are the sequence's
+            uint64_t* bar = real < C::BN ? raw_full : &v_full[sv];
+            if (lead) {
+              mbar_arrive_expect_tx(bar, C::V_STAGE);
+              for (int c = 0; c < C::VCH; ++c)
+                tma_load_4d(smem + C::OFF_V + sv * C::V_STAGE + c * C::CHUNK, &tmV, bar, c * 64, T.hk,
+                            T.k0 + j * C::BN, T.b);
+            }
+            if (real < C::BN) {
+              ok = wait(raw_full, n_raw++ & 1, kSiteVFull);
+              if (!ok) break;
+              zero_tile_rows(smem + C::OFF_V + sv * C::V_STAGE, C::VCH, C::CHUNK, C::BN, real, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lead) mbar_arrive(&v_full[sv]);
+            }
+            continue;
+          }
           mbar_arrive_expect_tx(&v_full[sv], C::V_STAGE);
           if constexpr (F8) {  // V^T: keys innermost
             tma_load_4d(smem + C::OFF_V + sv * C::V_STAGE, &tmV, &v_full[sv], j * C::BN, 0, T.hk, T.b);
@@ -321,7 +373,7 @@ __global__ void __launch_bounds__(320, 1)
     int pc[2] = {0, 0};     // p_ready phases consumed per query tile
     bool ok = true, issued = false;
     for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-      const FwdTile T = fwd_tile<C::BM, C::BN, VL>(p, nqb, wi);
+      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi);
       if (!T.any) continue;
       issued = true;
       ok = mbar_wait_warp(q_full, nw & 1, err, kSiteQ);
@@ -391,7 +443,7 @@ __global__ void __launch_bounds__(320, 1)
     [[maybe_unused]] const uint8_t* btile = smem + C::OFF_B + t * C::B_TILE + r * 128;  // this row, first box
     bool ok = true;
     for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-      const FwdTile T = fwd_tile<C::BM, C::BN, VL>(p, nqb, wi);
+      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi);
       // this warpgroup's query tile, selected without a run-time index into T (which
       // would move T to local memory)
       const bool my_exists = t ? T.exists[1] : T.exists[0];
@@ -582,9 +634,9 @@ __global__ void __launch_bounds__(320, 1)
         ++od;
         tc_fence_after();
       }
-      const bool row_ok = i < p.S_q;
+      const bool row_ok = i < (PK ? T.mask.S_q : p.S_q);
       const float inv = l > 0.f ? o_mul / l : 0.f;
-      __nv_bfloat16* orow = p.o + (((size_t)b * p.S_q + (row_ok ? i : 0)) * p.H_q + h) * D_V;
+      __nv_bfloat16* orow = p.o + (((size_t)b * p.S_q + T.q0 + (row_ok ? i : 0)) * p.H_q + h) * D_V;
 #pragma unroll 1
       for (int c0 = 0; c0 < D_V; c0 += 32) {
         uint32_t rr[32];
@@ -607,7 +659,17 @@ __global__ void __launch_bounds__(320, 1)
       }
       if (row_ok) {
         const float m_sub = (m_run == -INFINITY) ? 0.f : m_run;
-        p.lse[((size_t)b * p.H_q + h) * p.S_q + i] = l > 0.f ? (m_sub + lg2(l)) * kLn2 : -INFINITY;
+        p.lse[((size_t)b * p.H_q + h) * p.S_q + T.q0 + i] = l > 0.f ? (m_sub + lg2(l)) * kLn2 : -INFINITY;
+      }
+    }
+    if constexpr (PK) {
+      if (p.zero_rest) {  // rows of no sequence: o = 0, lse = -inf
+        const int end = p.counts->q_end, rest = p.S_q - end;
+        const size_t n16 = (size_t)rest * p.H_q * (D_V / 8), at = blockIdx.x * 256 + threadIdx.x;
+        uint4* o16 = reinterpret_cast<uint4*>(p.o + (size_t)end * p.H_q * D_V);
+        for (size_t e = at; e < n16; e += (size_t)gridDim.x * 256) o16[e] = make_uint4(0u, 0u, 0u, 0u);
+        for (size_t e = at; e < (size_t)rest * p.H_q; e += (size_t)gridDim.x * 256)
+          p.lse[(e / rest) * p.S_q + end + e % rest] = -INFINITY;
       }
     }
   }
@@ -621,11 +683,12 @@ __global__ void __launch_bounds__(320, 1)
   }
 }
 
-template <int D_QK, int D_V, int NK, int NV, bool VL, bool F8 = false, bool BIAS = false, bool DROP = false>
+template <int D_QK, int D_V, int NK, int NV, bool VL, bool F8 = false, bool BIAS = false, bool DROP = false,
+          bool PK = false>
 inline int launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams& p,
                         cudaStream_t stream, const CUtensorMap* tb = nullptr) {
   using C = FwdCfg<D_QK, D_V, NK, NV, F8, fwd_bias_staged<D_QK, BIAS>()>;
-  auto kern = attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP>;
+  auto kern = attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP, PK>;
   static bool attr_set = false;
   if (!attr_set) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
@@ -639,7 +702,9 @@ inline int launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
         cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n_sm <= 0)
       return -1;
   }
-  const long long n_work = (long long)((p.S_q + 2 * C::BM - 1) / (2 * C::BM)) * p.H_q * p.B;
+  // (packed: at most one tile more for every sequence; tile_bound carries their number)
+  const long long n_work =
+      PK ? p.tile_bound * p.H_q : (long long)((p.S_q + 2 * C::BM - 1) / (2 * C::BM)) * p.H_q * p.B;
   const unsigned grid = (unsigned)(n_work < n_sm ? n_work : n_sm);
   kern<<<grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tb ? *tb : tq, p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;

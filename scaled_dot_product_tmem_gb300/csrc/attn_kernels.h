@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "attn_common.cuh"
 #include "kv4.cuh"
 
 namespace sdpa {
@@ -33,6 +34,12 @@ struct FwdParams {
   const unsigned long long* rng = nullptr;
   unsigned drop_t = 0;
   float drop_scale = 1.f;
+  // packed batch (B = 1, S_q / S_kv the rows of the packed tensors): the plan's tile list, and
+  // whether the rows of no sequence are zeroed
+  const PackedTile* tiles = nullptr;
+  const PackedCounts* counts = nullptr;
+  long long tile_bound = 0;  // the list has at most this many tiles (the host's bound)
+  int zero_rest = 0;
 };
 
 // Returns 0 on a successful launch, -2 for an unsupported (d_qk, d_v), -1 on a
@@ -102,6 +109,15 @@ struct BwdParams {
   const float* descale_do = nullptr;
   const float* ds_amax = nullptr;
   float* ds_amax_out = nullptr;
+  // packed batch (B = 1, S_q / S_kv the rows of the packed tensors, S_pad the padded workspace
+  // rows of one head): the plan's tile lists; with a learnable sink, the dQ kernel's two
+  // fp32 row sums of dS, [2][H_q][S_pad]
+  const PackedTile* tiles_kv = nullptr;
+  const PackedTile* tiles_q = nullptr;
+  const PackedCounts* counts = nullptr;
+  float* ds_rowsum = nullptr;
+  long long tile_bound_kv = 0, tile_bound_q = 0;  // the lists have at most this many tiles
+  int zero_rest = 0;
 };
 
 int launch_bwd_preprocess(int d_v, const BwdParams& p, cudaStream_t stream);
