@@ -5,8 +5,28 @@
 //   the sequence (the S_q queries are its last S_q tokens); softmax with an optional sink
 //   logit; o = P V; lse = log of the denominator.
 //
-// One warp takes one (sequence, query, head): lane l holds d/32 dims, a score is a
-// warp-wide sum, and the running maximum and denominator are kept in fp32.
+// Bound by reading the cache (9d/8 bytes for each token and kv head), so each byte is read
+// once for all query rows that share a kv head (rows = G S_q, in blocks of 8 NT <= 32), and
+// the arithmetic must keep up with the memory: 23 bytes a cycle and SM are 41 values to
+// decode, for which the CUDA cores have 3 instructions each and no time left for products.
+//   - Products run on the tensor core as mma.sync m16n8k16 with tokens (scores) or head dims
+//     (outputs) as the 16 rows and the query rows as the 8 columns, so that a group of 4 to 8
+//     query heads wastes little of it, and a decoded operand serves every column block.
+//     (A tcgen05 product wants 128 rows of decoded operand in shared memory or TMEM: writing
+//     them back costs more than the whole decode.)
+//   - A code pair is decoded by a mask (128 + c as bf16 bits) and one paired fma with the
+//     scale, (128 + c) s - 136 s = (c - 8) s: exact, since every intermediate has at most 8
+//     significant bits.  Which pairs of dims or tokens share a register is free as long as
+//     both operands of a product agree, so a lane's 16-byte load feeds its own fragments.
+//   - The probabilities are rounded to bf16 (2^-8 relative) for P V; their sum is fp32.
+//   - Work is cut evenly over the CTAs of a persistent grid (units of 32 tokens of one
+//     sequence and kv head, in order), whatever the lengths; a (sequence, head) that spans
+//     several CTAs leaves fp32 partial sums in the workspace, which a second kernel joins in
+//     CTA order: bitwise reproducible.
+//   - Each warp streams its own units through a ring of bulk copies, four copies a page: no
+//     barrier between warps inside a segment.
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "attn_kernels.h"
 #include "kv4.cuh"
@@ -14,71 +34,719 @@
 
 namespace sdpa {
 
-template <int D>
-__global__ void __launch_bounds__(128) kv4_decode_kernel(const Kv4DecodeParams p) {
-  constexpr int E = D / 32;  // dims of a lane
-  const int lane = threadIdx.x % 32;
-  const long long row = (long long)blockIdx.x * 4 + threadIdx.x / 32;
-  if (row >= (long long)p.B * p.S_q * p.H_q) return;
-  const int h = (int)(row % p.H_q), s = (int)(row / p.H_q % p.S_q), b = (int)(row / p.H_q / p.S_q);
-  const int hk = h / (p.H_q / p.c.H_kv), P = p.c.page_size, x0 = lane * E;
-  const int len = entry_len(p.seq_lens, b, p.c.max_pages * P);
-  const int pos = len - p.S_q + s;
-  const int lo = p.window >= 0 && pos > p.window ? pos - p.window : 0;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[(size_t)row * D + x0 + e]) * p.scale_log2;
-    o[e] = 0.f;
-  }
-  if (p.softmax_type == 1) { m = 0.f; l = 1.f; }
-  if (p.softmax_type == 2) { m = p.offset[h] * kLog2e; l = 1.f; }
-  for (int j = lo; j <= pos; ++j) {
-    const int pg = kv4_page(p.c, b, j), w = j % P;
-    float k[E], v[E];
-    if (pg < 0 && lane == 0) atomicCAS(p.page_err, 0, p.site);
-    const uint8_t* base = p.pool + ((size_t)max(pg, 0) * p.c.H_kv + hk) * kv4_block_bytes(P, D);
-    const float sk = pg < 0 ? 0.f : kv4_scale_value(base[kv4_off_sk(P, D) + w * (D / 16) + x0 / 16]);
-    const float sv =
-        pg < 0 ? 0.f : kv4_scale_value(base[kv4_off_sv(P, D) + (w >> 1) * (D / 8) + (x0 / 16) * 2 + (w & 1)]);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int x = x0 + e;
-      const int ck = pg < 0 ? 8 : (base[w * (D / 2) + x / 2] >> (4 * (x & 1))) & 15;
-      const int cv = pg < 0 ? 8
-                            : (base[kv4_off_v(P, D) + kv4_v_at(w, x / (D / 8), D) + (x % (D / 8)) / 2] >>
-                               (4 * (x & 1))) & 15;
-      k[e] = (float)(ck - 8) * sk;
-      v[e] = (float)(cv - 8) * sv;
-    }
-    float t = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) t = fmaf(q[e], k[e], t);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    const float mn = fmaxf(m, t);
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    const float a = ex2(m - ms), pr = ex2(t - ms);
-    l = l * a + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + pr * v[e];
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) p.o[(size_t)row * D + x0 + e] = __float2bfloat16(o[e] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[((size_t)b * p.H_q + h) * p.S_q + s] = l > 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l)) * kLn2 : -INFINITY;
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kUnit = 32;         // tokens of one unit (one ring stage of a warp)
+constexpr int kStages = 3;
+constexpr int kMaxCtas = 152 * 4;  // partial-sum slots in the workspace
+constexpr int kMinUnits = kWarps;  // units of a CTA before another one is put to work
+
+enum Kv4Site { kKv4Full = 0xA0 };
+
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// d (16 x 8 fp32) += a (16 x 16 bf16, rows) b (16 x 8 bf16, columns)
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8 x 8 matrix of 16-bit values spread over a warp
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-size_t kv4_decode_workspace(int B, int S_q, int H_q, int H_kv, int d) { return 256; }
+// Codes c in bits 0-3 and 16-19 of w as the bf16 pair (c - 8) s, with s and -136 s paired.
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t s, uint32_t m136s) {
+  return bf2_fma((w & 0x000F000Fu) | 0x43004300u, s, m136s);
+}
+// Two scale bytes (low, next) as a bf16 pair.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t two) {
+  const float lo = __half2float(__ushort_as_half((unsigned short)((two & 0xFFu) << 7)));
+  const float hi = __half2float(__ushort_as_half((unsigned short)((two >> 8) << 7)));
+  return pack_bf16x2(lo, hi);
+}
+constexpr uint32_t kM136 = 0xC308C308u;  // -136 as a bf16 pair
+
+// A row's end: sums relative to maximum m (log2 units), the sink joins the denominator.
+struct Kv4Sums {
+  float mul, lse;  // what the sums are multiplied by; log of the denominator
+};
+__device__ __forceinline__ Kv4Sums kv4_finish(const Kv4DecodeParams& p, int h, float m, float l) {
+  const float sink = p.softmax_type == 0 ? -INFINITY : p.softmax_type == 1 ? 0.f : p.offset[h] * kLog2e;
+  const float mm = fmaxf(m, sink);
+  if (mm == -INFINITY) return l == l ? Kv4Sums{0.f, -INFINITY} : Kv4Sums{l, l};  // no key (l is 0) or a NaN
+  const float f = m == -INFINITY ? 0.f : ex2(m - mm);
+  const float den = l * f + (sink == -INFINITY ? 0.f : ex2(sink - mm));
+  return Kv4Sums{f / den, (mm + lg2(den)) * kLn2};
+}
+
+// The keys of one unit row and the sizes of one sequence.
+struct Seq {
+  int len;    // tokens in the cache
+  int first;  // first unit any query sees
+  int n;      // units
+};
+__device__ __forceinline__ Seq seq_of(const Kv4DecodeParams& p, int b) {
+  Seq s;
+  s.len = entry_len(p.seq_lens, b, p.c.max_pages * p.c.page_size);
+  const int lo = p.window >= 0 && s.len - p.S_q > p.window ? s.len - p.S_q - p.window : 0;  // the first query's
+  s.first = lo / kUnit;
+  s.n = s.len > 0 ? (s.len - 1) / kUnit - s.first + 1 : 0;
+  return s;
+}
+
+// Block-wide: the units of all sequences before b0 and of all (each sequence counts H_eff
+// times its units), and, for a unit u, the sequence that holds it with the units before it.
+template <int THREADS>
+struct UnitScan {
+  long long total;
+  __device__ void run(const Kv4DecodeParams& p, int H_eff, long long* part) {
+    long long t = 0;
+    for (int b = threadIdx.x; b < p.B; b += THREADS) t += seq_of(p, b).n;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = t;
+    __syncthreads();
+    t = 0;
+    for (int w = 0; w < THREADS / 32; ++w) t += part[w];
+    total = t * H_eff;
+    __syncthreads();
+  }
+  // The units (times H_eff) of sequences 0 .. b_end - 1; with find >= 0 instead stops at the
+  // sequence that holds unit `find`: returns the units before it and sets *b.
+  __device__ long long before(const Kv4DecodeParams& p, int H_eff, int b_end, long long find, int* b,
+                              long long* part) {
+    long long carry = 0;
+    for (int base = 0; base < b_end; base += THREADS) {
+      const int i = base + threadIdx.x;
+      const long long n = i < b_end ? (long long)seq_of(p, i).n * H_eff : 0;
+      long long s = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, s, off);
+        if (threadIdx.x % 32 >= off) s += o;
+      }
+      if (threadIdx.x % 32 == 31) part[threadIdx.x / 32] = s;
+      __syncthreads();
+      long long sum = carry;
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < (int)threadIdx.x / 32) s += part[w];
+        sum += part[w];
+      }
+      __syncthreads();
+      if (find >= 0 && find < sum) {  // uniform: the unit is in this chunk
+        const long long lo = carry + s - n;
+        if (n > 0 && find >= lo && find < lo + n) {
+          part[0] = lo;
+          part[1] = i;
+        }
+        __syncthreads();
+        const long long r = part[0];
+        *b = (int)part[1];
+        __syncthreads();
+        return r;
+      }
+      carry = sum;
+    }
+    return carry;
+  }
+};
+
+// CTA c of n takes units [cta_first(c), cta_first(c + 1)).
+__device__ __forceinline__ long long cta_first(long long total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int cta_of(long long total, int n, long long u) {
+  int c = (int)(((u + 1) * n - 1) / total);  // the last c with cta_first(c) <= u
+  while (c > 0 && cta_first(total, n, c) > u) --c;
+  while (c + 1 < n && cta_first(total, n, c + 1) <= u) ++c;
+  return c;
+}
+__device__ __forceinline__ int ctas_used(long long total, int grid) {
+  const long long want = (total + kMinUnits - 1) / kMinUnits;
+  return want < grid ? (int)(want > 0 ? want : 1) : grid;
+}
+
+template <int D, int NT>
+struct DecCfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int STAGE = kUnit * D * 9 / 8;
+  static constexpr int S_V = kUnit * D / 2, S_SK = kUnit * D, S_SV = kUnit * D + kUnit * D / 16;
+  static constexpr int OFF_Q = kWarps * kStages * STAGE;  // query fragments where they do not stay in registers
+  static constexpr bool Q_SMEM = NT > 2;
+  static constexpr int Q_BYTES = Q_SMEM ? (D / 16) * NT * 32 * 8 : 0;
+  static constexpr int XS = D + 4;  // row stride of the exchange (bank spread)
+  static constexpr int OFF_X = OFF_Q + Q_BYTES;
+  static constexpr int OFF_ML = OFF_X + ROWS * XS * 4;           // [kWarps][ROWS] maxima, then sums
+  static constexpr int OFF_SCAN = OFF_ML + 2 * kWarps * ROWS * 4;
+  static constexpr int OFF_BAR = OFF_SCAN + 64;
+  static constexpr int SMEM = OFF_BAR + kWarps * kStages * 8;
+  static constexpr int SLOT = ROWS * (D + 2);  // floats of one partial: rows of sums, maxima, denominators
+};
+
+}  // namespace
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4DecodeParams p, int row_blocks,
+                                                                 float* partial) {
+  using C = DecCfg<D, NT>;
+  constexpr int MT = D / 16;  // 16-row tiles of the head dim = k steps of a score
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  uint8_t* ring = smem + warp * kStages * C::STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * kStages;
+  float* xch = reinterpret_cast<float*>(smem + C::OFF_X);
+  float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* xl = xm + kWarps * C::ROWS;
+  long long* part = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
+  const int G = p.H_q / p.c.H_kv, R = G * p.S_q, H_eff = p.c.H_kv * row_blocks;
+  const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
+
+  if (lane == 0)
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
+  fence_barrier_init();
+  UnitScan<32 * kWarps> scan;
+  scan.run(p, H_eff, part);  // (its barriers also order the mbarrier set-up)
+  if (scan.total == 0) return;
+  const int n_cta = ctas_used(scan.total, gridDim.x);
+  if ((int)blockIdx.x >= n_cta) return;
+  const long long u_begin = cta_first(scan.total, n_cta, blockIdx.x);
+  const long long u_end = cta_first(scan.total, n_cta, blockIdx.x + 1);
+  int b = 0;
+  long long seq_u0 = scan.before(p, H_eff, p.B, u_begin, &b, part);  // first unit of sequence b
+
+  // ---- producer state of this warp: its next unit to load
+  struct Cursor {
+    int b, vh, unit;    // sequence, (kv head, row block), unit within the sequence's
+    long long u;        // running number
+    Seq s;
+  };
+  auto locate = [&](long long u, int b0, long long u0) {
+    Cursor c;
+    c.u = u;
+    c.b = b0;
+    c.s = seq_of(p, b0);
+    const long long r = u - u0;
+    c.vh = (int)(r / c.s.n);
+    c.unit = (int)(r % c.s.n);
+    return c;
+  };
+  auto advance = [&](Cursor& c, int by) {  // by < 32; may cross sequences
+    c.u += by;
+    c.unit += by;
+    if (c.u >= u_end) return;
+    while (c.unit >= c.s.n) {
+      c.unit -= c.s.n;
+      if (++c.vh == H_eff) {
+        c.vh = 0;
+        do {
+          ++c.b;
+          c.s = seq_of(p, c.b);
+        } while (c.s.n == 0);
+      }
+    }
+  };
+  // Copies of a unit: lane i < 8 moves part i % 4 (K codes, V codes, K scales, V scales) of the
+  // unit's page i / 4 (two pages when page_size is 16, else one).
+  const int sub_pages = P < kUnit ? kUnit / P : 1, sub_tok = P < kUnit ? P : kUnit;
+  auto page_for = [&](const Cursor& c) {  // this lane's page (a load to be used one step later)
+    const int tok = (c.s.first + c.unit) * kUnit + (lane / 4) * sub_tok;
+    return lane < 4 * sub_pages && c.u < u_end && tok < c.s.len ? kv4_page(p.c, c.b, tok) : -2;
+  };
+  auto issue = [&](const Cursor& c, int stage, int page) {
+    const int tok = (c.s.first + c.unit) * kUnit + (lane / 4) * sub_tok;
+    uint8_t* st = ring + stage * C::STAGE;
+    // whole 16-token groups up to the sequence's end
+    const int n = page == -2 ? 0 : min(sub_tok, (c.s.len - tok + 15) / 16 * 16);
+    const int part_ = lane % 4, t0 = (lane / 4) * sub_tok;
+    const int per = part_ < 2 ? D / 2 : D / 16;  // bytes of a token in this part
+    const int dst = (part_ == 0 ? 0 : part_ == 1 ? C::S_V : part_ == 2 ? C::S_SK : C::S_SV) + t0 * per;
+    const bool bad = page == -1;
+    const uint32_t bytes = page >= 0 ? n * per : 0;
+    if (__any_sync(0xffffffffu, bad)) {  // not a page: its tokens read as zeros (scale 0)
+      if (bad) {
+        if (part_ >= 2)
+          for (int o = 0; o < n * per; o += 4) *reinterpret_cast<uint32_t*>(st + dst + o) = 0u;
+        atomicCAS(p.page_err, 0, p.site);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+    }
+    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(&bars[stage], all);
+    __syncwarp();
+    if (bytes) {
+      const int off = part_ == 0 ? 0 : part_ == 1 ? kv4_off_v(P, D) : part_ == 2 ? kv4_off_sk(P, D) : kv4_off_sv(P, D);
+      const uint8_t* src =
+          p.pool + ((size_t)page * p.c.H_kv + c.vh / row_blocks) * blk + off + (size_t)(tok % P) * per;
+      bulk_load(st + dst, src, bytes, &bars[stage]);
+    }
+  };
+
+  Cursor load = locate(u_begin, b, seq_u0);
+  advance(load, warp);
+  int page = page_for(load), n_issued = 0;
+  auto issue_next = [&]() {
+    if (load.u >= u_end) return;
+    issue(load, n_issued % kStages, page);
+    ++n_issued;
+    advance(load, kWarps);
+    page = load.u < u_end ? page_for(load) : -2;
+  };
+  for (int s = 0; s < kStages; ++s) issue_next();
+
+  // ---- segments: the CTA's units of one (sequence, kv head, row block) after another
+  int used = 0;
+  bool ok = true;
+  Cursor seg = locate(u_begin, b, seq_u0);
+  while (seg.u < u_end) {
+    const int seg_n = (int)min((long long)(seg.s.n - seg.unit), u_end - seg.u);
+    const bool whole = seg.unit == 0 && seg_n == seg.s.n;
+    const int hk = seg.vh / row_blocks, r0 = (seg.vh % row_blocks) * C::ROWS;
+    const int len = seg.s.len, first_tok = (seg.s.first + seg.unit) * kUnit;
+    // query fragments: lane (g, t) holds row r0 + 8 nt + g; dims [t D/4, (t + 1) D/4), in pairs
+    // (x, x + 4) of each 8, the pairing of a code word's nibbles
+    uint32_t qf[C::Q_SMEM ? 1 : MT][NT][2];
+    uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
+    if (!C::Q_SMEM || warp == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + 8 * nt + g;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (((size_t)seg.b * p.S_q + r / G) * p.H_q + hk * G + r % G) * D + t * (D / 4));
+#pragma unroll
+        for (int j = 0; j < MT / 2; ++j) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (r < R) w = __ldg(src + j);
+          const uint32_t p0 = __byte_perm(w.x, w.z, 0x5410), p1 = __byte_perm(w.x, w.z, 0x7632);
+          const uint32_t p2 = __byte_perm(w.y, w.w, 0x5410), p3 = __byte_perm(w.y, w.w, 0x7632);
+          if constexpr (C::Q_SMEM) {
+            qs[((2 * j) * NT + nt) * 32 + lane] = make_uint2(p0, p1);
+            qs[((2 * j + 1) * NT + nt) * 32 + lane] = make_uint2(p2, p3);
+          } else {
+            qf[2 * j][nt][0] = p0;
+            qf[2 * j][nt][1] = p1;
+            qf[2 * j + 1][nt][0] = p2;
+            qf[2 * j + 1][nt][1] = p3;
+          }
+        }
+      }
+    }
+    if constexpr (C::Q_SMEM) __syncthreads();
+    // this lane's score columns: rows r0 + 8 nt + 2 t and + 1
+    int row_hi[NT][2], row_lo[NT][2];
+    int hi_min = len - 1, lo_max = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + 8 * nt + 2 * t + e, pos = len - p.S_q + min(r, R - 1) / G;
+        row_hi[nt][e] = pos;
+        row_lo[nt][e] = p.window >= 0 ? pos - p.window : 0;
+      }
+    hi_min = len - p.S_q + r0 / G;
+    lo_max = p.window >= 0 ? len - 1 - p.window : 0;
+    const int lo_min = p.window >= 0 ? len - p.S_q - p.window : 0;
+    float acc[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    // units of this segment that are this warp's: running numbers congruent to u_begin + warp
+    const int skip = (int)((warp - (seg.u - u_begin) % kWarps + kWarps) % kWarps);
+    for (int k = skip; k < seg_n; k += kWarps) {
+      const int stage = used % kStages;
+      ok = ok && mbar_wait_warp(&bars[stage], (used / kStages) & 1, p.err, kKv4Full);
+      ++used;
+      if (ok) {
+        const uint8_t* st = ring + stage * C::STAGE;
+        const int k0 = first_tok + k * kUnit;
+        const bool edge = k0 + kUnit - 1 > hi_min || k0 < lo_max;  // some key is hidden from some row
+        float s[2][NT][4];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[sub][nt][e] = 0.f;
+        // ---- scores of 2 x 16 tokens: lane (g, t) decodes tokens g, g + 8, its quarter of the dims
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          const int ta = 16 * sub + g, tb = ta + 8;
+          uint32_t wa[MT / 2], wb[MT / 2], sa, sb;
+          if constexpr (D == 128) {
+            *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(st + ta * (D / 2) + t * 16);
+            *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(st + tb * (D / 2) + t * 16);
+            sa = scale_pair(*reinterpret_cast<const unsigned short*>(st + C::S_SK + ta * (D / 16) + 2 * t));
+            sb = scale_pair(*reinterpret_cast<const unsigned short*>(st + C::S_SK + tb * (D / 16) + 2 * t));
+          } else {
+            *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(st + ta * (D / 2) + t * 8);
+            *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(st + tb * (D / 2) + t * 8);
+            sa = scale_pair(st[C::S_SK + ta * (D / 16) + t]);
+            sb = scale_pair(st[C::S_SK + tb * (D / 16) + t]);
+          }
+#pragma unroll
+          for (int j = 0; j < MT / 2; ++j) {  // a word: 8 dims, two k steps; 16 dims share a scale
+            const uint32_t s2a = j < 2 ? __byte_perm(sa, sa, 0x1010) : __byte_perm(sa, sa, 0x3232);
+            const uint32_t s2b = j < 2 ? __byte_perm(sb, sb, 0x1010) : __byte_perm(sb, sb, 0x3232);
+            const uint32_t ca = bf2_mul(s2a, kM136), cb = bf2_mul(s2b, kM136);
+            uint32_t a[4], c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[e] = decode_pair(wa[j] >> (4 * e), s2a, ca);
+              c[e] = decode_pair(wb[j] >> (4 * e), s2b, cb);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (C::Q_SMEM) {
+                const uint2 q0 = qs[((2 * j) * NT + nt) * 32 + lane], q1 = qs[((2 * j + 1) * NT + nt) * 32 + lane];
+                mma_16816(s[sub][nt], a[0], c[0], a[1], c[1], q0.x, q0.y);
+                mma_16816(s[sub][nt], a[2], c[2], a[3], c[3], q1.x, q1.y);
+              } else {
+                mma_16816(s[sub][nt], a[0], c[0], a[1], c[1], qf[2 * j][nt][0], qf[2 * j][nt][1]);
+                mma_16816(s[sub][nt], a[2], c[2], a[3], c[3], qf[2 * j + 1][nt][0], qf[2 * j + 1][nt][1]);
+              }
+            }
+          }
+        }
+        // ---- softmax: s[sub][nt][e + 2 f] is token 16 sub + g + 8 f, row 2 t + e.  The running
+        // maximum moves only when some score passes it by 2^8 (the sums stay exact: they are
+        // relative to the maximum that was used)
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                float& x = s[sub][nt][e + 2 * f];
+                x *= p.scale_log2;
+                if (edge) {
+                  const int j = k0 + 16 * sub + g + 8 * f;
+                  if (j > row_hi[nt][e] || j < row_lo[nt][e]) x = -INFINITY;
+                }
+                mx = fmaxf(mx, x);
+              }
+            grow |= mx > m[nt][e] + 8.f;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+              const float mn = fmaxf(m[nt][e], mx);
+              const float alpha = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
+              m[nt][e] = mn;
+              l[nt][e] *= alpha;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                acc[mt][nt][e] *= alpha;
+                acc[mt][nt][e + 2] *= alpha;
+              }
+            }
+        }
+        uint32_t pb[2][NT][2];  // P as the column operand: rows of the product = tokens
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const float x0 = ex2(s[sub][nt][2 * f] - m0), x1 = ex2(s[sub][nt][2 * f + 1] - m1);
+              l[nt][0] += x0;
+              l[nt][1] += x1;
+              pb[sub][nt][f] = transpose_8x8(pack_bf16x2(x0, x1));
+            }
+        }
+        // ---- outputs: lane (g, t) decodes eighth g of the head dim of token pairs t and t + 4
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          uint32_t lo[2][MT / 4], hi[2][MT / 4], sv[2], cv[2];  // [pair][word]: both tokens' nibbles
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int u = 8 * sub + t + 4 * f;
+            const uint8_t* at = st + C::S_V + u * D + (g ^ kv4_slot_xor(u, D)) * (D / 8);
+            uint32_t two;
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(at);  // token 2u: x, y; token 2u + 1: z, w
+              lo[f][0] = __byte_perm(w.x, w.z, 0x5410);
+              hi[f][0] = __byte_perm(w.x, w.z, 0x7632);
+              lo[f][1] = __byte_perm(w.y, w.w, 0x5410);
+              hi[f][1] = __byte_perm(w.y, w.w, 0x7632);
+              two = *reinterpret_cast<const unsigned short*>(st + C::S_SV + u * (D / 8) + 2 * g);
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(at);
+              lo[f][0] = __byte_perm(w.x, w.y, 0x5410);
+              hi[f][0] = __byte_perm(w.x, w.y, 0x7632);
+              two = *reinterpret_cast<const unsigned short*>(st + C::S_SV + u * (D / 8) + 2 * (g / 2));
+            }
+            if (edge) {  // tokens that no row sees: whatever their bytes are, they add nothing
+              const int j = k0 + 2 * u;
+              if (j > len - 1 || j < lo_min) two &= 0xFF00u;
+              if (j + 1 > len - 1 || j + 1 < lo_min) two &= 0x00FFu;
+            }
+            sv[f] = scale_pair(two);
+            cv[f] = bf2_mul(sv[f], kM136);
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            // rows g and g + 8 of the tile: dims x and x + D/16 of the eighth
+            uint32_t a[4];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              if constexpr (D == 128) {
+                a[2 * f] = decode_pair((mt < 4 ? lo[f][0] : hi[f][0]) >> (4 * (mt % 4)), sv[f], cv[f]);
+                a[2 * f + 1] = decode_pair((mt < 4 ? lo[f][1] : hi[f][1]) >> (4 * (mt % 4)), sv[f], cv[f]);
+              } else {
+                a[2 * f] = decode_pair(lo[f][0] >> (4 * mt), sv[f], cv[f]);
+                a[2 * f + 1] = decode_pair(hi[f][0] >> (4 * mt), sv[f], cv[f]);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(acc[mt][nt], a[0], a[1], a[2], a[3], pb[sub][nt][0], pb[sub][nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage: it may be filled again
+      issue_next();
+    }
+
+    // ---- the warps' sums become one: maxima and denominators, then the rows, warp by warp
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
+        if (g == 0) {
+          xm[warp * C::ROWS + 8 * nt + 2 * t + e] = m[nt][e];
+          xl[warp * C::ROWS + 8 * nt + 2 * t + e] = l[nt][e];
+        }
+      }
+    __syncthreads();
+    float f[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nt + 2 * t + e;
+        float mm = xm[r];
+        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, xm[w * C::ROWS + r]);
+        f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mm);
+      }
+    for (int w = 0; w < kWarps; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int q = 0; q < MT / 2; ++q) {
+              // D/8 consecutive dims of row 2 t + e: tiles 0.. give the first half, their + 8 rows the second
+              constexpr int QH = MT / 4;
+              float4* at = reinterpret_cast<float4*>(xch + (8 * nt + 2 * t + e) * C::XS + g * (D / 8) + 4 * q);
+              const int mt = 4 * (q % QH), hf = q / QH;
+              float4 v = make_float4(acc[mt][nt][e + 2 * hf] * f[nt][e], acc[mt + 1][nt][e + 2 * hf] * f[nt][e],
+                                     acc[mt + 2][nt][e + 2 * hf] * f[nt][e], acc[mt + 3][nt][e + 2 * hf] * f[nt][e]);
+              if (w > 0) {
+                const float4 o = *at;
+                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+              }
+              *at = v;
+            }
+      }
+      __syncthreads();
+    }
+    // ---- the whole of a (sequence, head): outputs; a piece of it: partial sums
+    const bool at_begin = seg.u == u_begin;
+    float* slot = partial + ((size_t)2 * blockIdx.x + (at_begin ? 0 : 1)) * C::SLOT;
+    for (int r = warp; r < C::ROWS && r0 + r < R; r += kWarps) {
+      float mm = xm[r], ll = 0.f;
+      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, xm[w * C::ROWS + r]);
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = xm[w * C::ROWS + r], lw = xl[w * C::ROWS + r];
+        ll += mw == -INFINITY ? lw : lw * ex2(mw - mm);  // (no key: lw is 0, or a NaN that has to stay)
+      }
+      if (whole) {
+        const int qs_ = (r0 + r) / G, h = hk * G + (r0 + r) % G;
+        const Kv4Sums z = kv4_finish(p, h, mm, ll);
+        __nv_bfloat16* o = p.o + (((size_t)seg.b * p.S_q + qs_) * p.H_q + h) * D;
+        for (int x = 2 * lane; x < D; x += 64)
+          *reinterpret_cast<uint32_t*>(o + x) = pack_bf16x2(xch[r * C::XS + x] * z.mul, xch[r * C::XS + x + 1] * z.mul);
+        if (lane == 0 && p.lse) p.lse[((size_t)seg.b * p.H_q + h) * p.S_q + qs_] = z.lse;
+      } else {
+        for (int x = lane; x < D; x += 32) slot[r * D + x] = xch[r * C::XS + x];
+        if (lane == 0) {
+          slot[C::ROWS * D + r] = mm;
+          slot[C::ROWS * D + C::ROWS + r] = ll;
+        }
+      }
+    }
+    __syncthreads();  // the exchange is free for the next segment
+    seg.u += seg_n;
+    seg.unit += seg_n;
+    if (seg.u < u_end && seg.unit >= seg.s.n) {
+      seg.unit = 0;
+      if (++seg.vh == H_eff) {
+        seg.vh = 0;
+        do {
+          ++seg.b;
+          seg.s = seq_of(p, seg.b);
+        } while (seg.s.n == 0);
+      }
+    }
+  }
+}
+
+// Joins the pieces of every (sequence, head) that spans several CTAs, in CTA order, and writes
+// the rows of sequences without a token.  One block per (sequence, kv head, row block, row).
+template <int D>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeParams p, int row_blocks, int rows, int grid,
+                                                       const float* partial) {
+  __shared__ long long part[8];
+  __shared__ float wgt[kMaxCtas], red[8], sums[8][D];
+  const int G = p.H_q / p.c.H_kv, R = G * p.S_q, H_eff = p.c.H_kv * row_blocks;
+  const int b = blockIdx.x / H_eff, vh = blockIdx.x % H_eff, r = blockIdx.y;
+  const int hk = vh / row_blocks, row = (vh % row_blocks) * rows + r;
+  if (row >= R) return;
+  const Seq s = seq_of(p, b);
+  const int qs = row / G, h = hk * G + row % G;
+  __nv_bfloat16* o = p.o + (((size_t)b * p.S_q + qs) * p.H_q + h) * D;
+  float* lse = p.lse ? p.lse + ((size_t)b * p.H_q + h) * p.S_q + qs : nullptr;
+  if (s.n == 0) {
+    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(o)[threadIdx.x] = 0u;
+    if (threadIdx.x == 0 && lse) *lse = kv4_finish(p, h, -INFINITY, 0.f).lse;
+    return;
+  }
+  UnitScan<256> scan;
+  scan.run(p, H_eff, part);
+  int unused;
+  const long long u0 = scan.before(p, H_eff, b, -1, &unused, part) + (long long)vh * s.n;
+  const int n_cta = ctas_used(scan.total, grid);
+  const int c0 = cta_of(scan.total, n_cta, u0), c1 = cta_of(scan.total, n_cta, u0 + s.n - 1);
+  if (c0 == c1) return;  // one CTA had all of it
+  const int slot_floats = rows * (D + 2), n = c1 - c0 + 1;
+  auto slot_of = [&](int c) {  // the piece is the CTA's first where the CTA starts inside it
+    return partial + ((size_t)2 * c + (cta_first(scan.total, n_cta, c) >= u0 ? 0 : 1)) * slot_floats;
+  };
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto block_max = [&](float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[0];
+    for (int w = 1; w < 8; ++w) v = fmaxf(v, red[w]);
+    __syncthreads();
+    return v;
+  };
+  float mx = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += 256) mx = fmaxf(mx, slot_of(c0 + i)[rows * D + r]);
+  mx = block_max(mx);
+  float ll = 0.f;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const float* sl = slot_of(c0 + i);
+    const float mi = sl[rows * D + r], w = mi == -INFINITY ? 0.f : ex2(mi - mx);
+    wgt[i] = w;
+    const float li = sl[rows * D + rows + r];
+    ll += mi == -INFINITY ? li : w * li;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
+  if (lane == 0) red[warp] = ll;
+  __syncthreads();
+  ll = 0.f;
+  for (int w = 0; w < 8; ++w) ll += red[w];
+  constexpr int E = D / 32;
+  float a[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) a[e] = 0.f;
+  for (int i = warp; i < n; i += 8) {
+    const float w = wgt[i];
+    const float* sl = slot_of(c0 + i) + r * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (w != 0.f) a[e] = fmaf(w, sl[e], a[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = a[e];
+  __syncthreads();
+  const Kv4Sums z = kv4_finish(p, h, mx, ll);
+  if (threadIdx.x < D) {
+    float v = 0.f;
+    for (int w = 0; w < 8; ++w) v += sums[w][threadIdx.x];
+    o[threadIdx.x] = __float2bfloat16(v * z.mul);
+  }
+  if (threadIdx.x == 0 && lse) *lse = z.lse;
+}
+
+namespace {
+
+int n_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+template <int D, int NT>
+int launch_t(const Kv4DecodeParams& p, float* partial, cudaStream_t stream) {
+  using C = DecCfg<D, NT>;
+  auto kern = kv4_decode_kernel<D, NT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
+  int per_sm = 0, sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * kWarps, C::SMEM) != cudaSuccess)
+    return -1;
+  const int grid = std::max(1, std::min(kMaxCtas, per_sm * sms));
+  const int rows = p.H_q / p.c.H_kv * p.S_q, blocks = (rows + C::ROWS - 1) / C::ROWS;
+  const long long join = (long long)p.B * p.c.H_kv * blocks;
+  if (join > 0x7fffffffLL) return -2;
+  kern<<<grid, 32 * kWarps, C::SMEM, stream>>>(p, blocks, partial);
+  kv4_join_kernel<D><<<dim3((unsigned)join, std::min(rows, C::ROWS)), 256, 0, stream>>>(p, blocks, C::ROWS, grid,
+                                                                                        partial);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+size_t kv4_decode_workspace(int B, int S_q, int H_q, int H_kv, int d) {
+  const long long rows = (long long)(H_q / H_kv) * S_q;
+  const int nt = rows > 16 ? 4 : n_tiles((int)rows);
+  return (size_t)kMaxCtas * 2 * 8 * nt * (d + 2) * sizeof(float);
+}
 
 int launch_kv4_decode(const Kv4DecodeParams& p, void* workspace, cudaStream_t stream) {
-  const long long rows = (long long)p.B * p.S_q * p.H_q;
-  const unsigned blocks = (unsigned)((rows + 3) / 4);
-  if (p.c.d == 128) kv4_decode_kernel<128><<<blocks, 128, 0, stream>>>(p);
-  else kv4_decode_kernel<64><<<blocks, 128, 0, stream>>>(p);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  float* partial = static_cast<float*>(workspace);
+  const int nt = n_tiles(p.H_q / p.c.H_kv * p.S_q);
+  if (p.c.d == 128)
+    return nt == 1   ? launch_t<128, 1>(p, partial, stream)
+           : nt == 2 ? launch_t<128, 2>(p, partial, stream)
+                     : launch_t<128, 4>(p, partial, stream);
+  return nt == 1   ? launch_t<64, 1>(p, partial, stream)
+         : nt == 2 ? launch_t<64, 2>(p, partial, stream)
+                   : launch_t<64, 4>(p, partial, stream);
 }
 
 }  // namespace sdpa
