@@ -19,12 +19,12 @@
 //     significant bits.  Which pairs of dims or tokens share a register is free as long as
 //     both operands of a product agree, so a lane's 16-byte load feeds its own fragments.
 //   - The probabilities are rounded to bf16 (2^-8 relative) for P V; their sum is fp32.
-//   - Work is cut evenly over the CTAs of a persistent grid (units of 32 tokens of one
+//   - Work is cut evenly over the CTAs of a persistent grid (units of 128 tokens of one
 //     sequence and kv head, in order), whatever the lengths; a (sequence, head) that spans
 //     several CTAs leaves fp32 partial sums in the workspace, which a second kernel joins in
 //     CTA order: bitwise reproducible.
-//   - Each warp streams its own units through a ring of bulk copies, four copies a page: no
-//     barrier between warps inside a segment.
+//   - A fifth warp walks the page table and streams units into a ring by bulk copies, four a
+//     page; each of the other four takes 32 tokens of every unit.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -36,13 +36,14 @@ namespace sdpa {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kUnit = 32;         // tokens of one unit (one ring stage of a warp)
+constexpr int kWarps = 4;                  // computing warps
+constexpr int kSub = 32;                   // tokens of a unit that one warp takes
+constexpr int kUnit = kWarps * kSub;       // tokens of one unit (one ring stage)
 constexpr int kStages = 3;
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxCtas = 152 * 4;  // partial-sum slots in the workspace
-constexpr int kMinUnits = kWarps;  // units of a CTA before another one is put to work
 
-enum Kv4Site { kKv4Full = 0xA0 };
+enum Kv4Site { kKv4Full = 0xA0, kKv4Empty };
 
 __device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -175,8 +176,7 @@ __device__ __forceinline__ int cta_of(long long total, int n, long long u) {
   return c;
 }
 __device__ __forceinline__ int ctas_used(long long total, int grid) {
-  const long long want = (total + kMinUnits - 1) / kMinUnits;
-  return want < grid ? (int)(want > 0 ? want : 1) : grid;
+  return total < grid ? (int)total : grid;
 }
 
 template <int D, int NT>
@@ -184,148 +184,146 @@ struct DecCfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int STAGE = kUnit * D * 9 / 8;
   static constexpr int S_V = kUnit * D / 2, S_SK = kUnit * D, S_SV = kUnit * D + kUnit * D / 16;
-  static constexpr int OFF_Q = kWarps * kStages * STAGE;  // query fragments where they do not stay in registers
+  static constexpr int OFF_Q = kStages * STAGE;  // query fragments where they do not stay in registers
   static constexpr bool Q_SMEM = NT > 2;
   static constexpr int Q_BYTES = Q_SMEM ? (D / 16) * NT * 32 * 8 : 0;
   static constexpr int XS = D + 4;  // row stride of the exchange (bank spread)
   static constexpr int OFF_X = OFF_Q + Q_BYTES;
   static constexpr int OFF_ML = OFF_X + ROWS * XS * 4;           // [kWarps][ROWS] maxima, then sums
   static constexpr int OFF_SCAN = OFF_ML + 2 * kWarps * ROWS * 4;
-  static constexpr int OFF_BAR = OFF_SCAN + 64;
-  static constexpr int SMEM = OFF_BAR + kWarps * kStages * 8;
+  static constexpr int OFF_BAR = OFF_SCAN + 64;  // full[kStages], empty[kStages]
+  static constexpr int SMEM = OFF_BAR + 2 * kStages * 8;
   static constexpr int SLOT = ROWS * (D + 2);  // floats of one partial: rows of sums, maxima, denominators
 };
 
 }  // namespace
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4DecodeParams p, int row_blocks,
-                                                                 float* partial) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
+    kv4_decode_kernel(const Kv4DecodeParams p, int row_blocks, float* partial) {
   using C = DecCfg<D, NT>;
   constexpr int MT = D / 16;  // 16-row tiles of the head dim = k steps of a score
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  uint8_t* ring = smem + warp * kStages * C::STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * kStages;
-  float* xch = reinterpret_cast<float*>(smem + C::OFF_X);
-  float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);
-  float* xl = xm + kWarps * C::ROWS;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + kStages;
   long long* part = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
   const int G = p.H_q / p.c.H_kv, R = G * p.S_q, H_eff = p.c.H_kv * row_blocks;
-  const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
 
-  if (lane == 0)
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
-  fence_barrier_init();
-  UnitScan<32 * kWarps> scan;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    fence_barrier_init();
+  }
+  UnitScan<kThreads> scan;
   scan.run(p, H_eff, part);  // (its barriers also order the mbarrier set-up)
   if (scan.total == 0) return;
   const int n_cta = ctas_used(scan.total, gridDim.x);
   if ((int)blockIdx.x >= n_cta) return;
   const long long u_begin = cta_first(scan.total, n_cta, blockIdx.x);
   const long long u_end = cta_first(scan.total, n_cta, blockIdx.x + 1);
-  int b = 0;
-  long long seq_u0 = scan.before(p, H_eff, p.B, u_begin, &b, part);  // first unit of sequence b
-
-  // ---- producer state of this warp: its next unit to load
+  // The CTA's units are a run of segments: units of one (sequence, kv head, row block) in order.
   struct Cursor {
-    int b, vh, unit;    // sequence, (kv head, row block), unit within the sequence's
-    long long u;        // running number
+    int b, vh, unit;  // sequence, kv head and row block, unit within the sequence's
     Seq s;
+  } at;
+  {
+    const long long r = u_begin - scan.before(p, H_eff, p.B, u_begin, &at.b, part);
+    at.s = seq_of(p, at.b);
+    at.vh = (int)(r / at.s.n);
+    at.unit = (int)(r % at.s.n);
+  }
+  auto next_segment = [&](Cursor& c) {
+    c.unit = 0;
+    if (++c.vh < H_eff) return;
+    c.vh = 0;
+    do {
+      ++c.b;
+      c.s = seq_of(p, c.b);
+    } while (c.s.n == 0);
   };
-  auto locate = [&](long long u, int b0, long long u0) {
-    Cursor c;
-    c.u = u;
-    c.b = b0;
-    c.s = seq_of(p, b0);
-    const long long r = u - u0;
-    c.vh = (int)(r / c.s.n);
-    c.unit = (int)(r % c.s.n);
-    return c;
-  };
-  auto advance = [&](Cursor& c, int by) {  // by < 32; may cross sequences
-    c.u += by;
-    c.unit += by;
-    if (c.u >= u_end) return;
-    while (c.unit >= c.s.n) {
-      c.unit -= c.s.n;
-      if (++c.vh == H_eff) {
-        c.vh = 0;
-        do {
-          ++c.b;
-          c.s = seq_of(p, c.b);
-        } while (c.s.n == 0);
-      }
-    }
-  };
-  // Copies of a unit: lane i < 8 moves part i % 4 (K codes, V codes, K scales, V scales) of the
-  // unit's page i / 4 (two pages when page_size is 16, else one).
-  const int sub_pages = P < kUnit ? kUnit / P : 1, sub_tok = P < kUnit ? P : kUnit;
-  auto page_for = [&](const Cursor& c) {  // this lane's page (a load to be used one step later)
-    const int tok = (c.s.first + c.unit) * kUnit + (lane / 4) * sub_tok;
-    return lane < 4 * sub_pages && c.u < u_end && tok < c.s.len ? kv4_page(p.c, c.b, tok) : -2;
-  };
-  auto issue = [&](const Cursor& c, int stage, int page) {
-    const int tok = (c.s.first + c.unit) * kUnit + (lane / 4) * sub_tok;
-    uint8_t* st = ring + stage * C::STAGE;
-    // whole 16-token groups up to the sequence's end
-    const int n = page == -2 ? 0 : min(sub_tok, (c.s.len - tok + 15) / 16 * 16);
-    const int part_ = lane % 4, t0 = (lane / 4) * sub_tok;
+  int left = (int)(u_end - u_begin);
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer
+    // Lane i copies part i % 4 (K codes, V codes, K scales, V scales) of piece i / 4 of a unit; a
+    // piece is a page, or the unit's part of one.  Its page is looked up one unit ahead.
+    const int P = p.c.page_size, piece = min(P, kUnit), pieces = kUnit / piece;
+    const int part_ = lane % 4, t0 = lane / 4 * piece;
     const int per = part_ < 2 ? D / 2 : D / 16;  // bytes of a token in this part
-    const int dst = (part_ == 0 ? 0 : part_ == 1 ? C::S_V : part_ == 2 ? C::S_SK : C::S_SV) + t0 * per;
-    const bool bad = page == -1;
-    const uint32_t bytes = page >= 0 ? n * per : 0;
-    if (__any_sync(0xffffffffu, bad)) {  // not a page: its tokens read as zeros (scale 0)
-      if (bad) {
-        if (part_ >= 2)
-          for (int o = 0; o < n * per; o += 4) *reinterpret_cast<uint32_t*>(st + dst + o) = 0u;
-        atomicCAS(p.page_err, 0, p.site);
-        fence_proxy_async_smem();
+    const int src_off = part_ == 0 ? 0 : part_ == 1 ? kv4_off_v(P, D) : part_ == 2 ? kv4_off_sk(P, D) : kv4_off_sv(P, D);
+    const int dst_off = (part_ == 0 ? 0 : part_ == 1 ? C::S_V : part_ == 2 ? C::S_SK : C::S_SV) + t0 * per;
+    const size_t block = kv4_block_bytes(P, D), page_bytes = block * p.c.H_kv;
+    auto page_of = [&]() {
+      const int tok = (at.s.first + at.unit) * kUnit + t0;
+      return lane < 4 * pieces && tok < at.s.len ? kv4_page(p.c, at.b, tok) : -2;
+    };
+    int page = page_of();
+    for (int i = 0; i < left; ++i) {
+      const int stage = i % kStages;
+      uint8_t* st = smem + stage * C::STAGE;
+      const int tok = (at.s.first + at.unit) * kUnit + t0;
+      // whole 16-token groups up to the sequence's end
+      const int bytes = page == -2 ? 0 : min(piece, (at.s.len - tok + 15) / 16 * 16) * per;
+      const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (at.vh / row_blocks) * block + src_off +
+                           (size_t)(tok % P) * per;
+      const int have = page;
+      if (i + 1 < left) {
+        if (++at.unit == at.s.n) next_segment(at);
+        page = page_of();
       }
+      if (i >= kStages && !mbar_wait_warp(&empty[stage], (i / kStages - 1) & 1, p.err, kKv4Empty)) break;
+      if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
+        if (have == -1) {
+          if (part_ >= 2)
+            for (int o = 0; o < bytes; o += 4) *reinterpret_cast<uint32_t*>(st + dst_off + o) = 0u;
+          atomicCAS(p.page_err, 0, p.site);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+      }
+      const uint32_t all = __reduce_add_sync(0xffffffffu, have >= 0 ? bytes : 0);
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], all);
       __syncwarp();
+      if (have >= 0) bulk_load(st + dst_off, src, bytes, &full[stage]);
     }
-    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
-    if (lane == 0) mbar_arrive_expect_tx(&bars[stage], all);
-    __syncwarp();
-    if (bytes) {
-      const int off = part_ == 0 ? 0 : part_ == 1 ? kv4_off_v(P, D) : part_ == 2 ? kv4_off_sk(P, D) : kv4_off_sv(P, D);
-      const uint8_t* src =
-          p.pool + ((size_t)page * p.c.H_kv + c.vh / row_blocks) * blk + off + (size_t)(tok % P) * per;
-      bulk_load(st + dst, src, bytes, &bars[stage]);
+    // every copy this warp started must land before the CTA may exit: wait for the last ones
+    for (int s = 0; s < kStages && s < left; ++s) {
+      const int last = s + (left - 1 - s) / kStages * kStages;
+      mbar_wait_warp(&full[s], (last / kStages) & 1, p.err, kKv4Full);
     }
-  };
+    return;
+  }
 
-  Cursor load = locate(u_begin, b, seq_u0);
-  advance(load, warp);
-  int page = page_for(load), n_issued = 0;
-  auto issue_next = [&]() {
-    if (load.u >= u_end) return;
-    issue(load, n_issued % kStages, page);
-    ++n_issued;
-    advance(load, kWarps);
-    page = load.u < u_end ? page_for(load) : -2;
-  };
-  for (int s = 0; s < kStages; ++s) issue_next();
-
-  // ---- segments: the CTA's units of one (sequence, kv head, row block) after another
-  int used = 0;
+  // ------------------------------------------------------------------ computing warps
+  float* xch = reinterpret_cast<float*>(smem + C::OFF_X);
+  float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* xl = xm + kWarps * C::ROWS;
+  const int g = lane / 4, t = lane % 4;
+  const int off_k = (warp * kSub + g) * (D / 2) + t * (D / 8);
+  const int off_sk = C::S_SK + (warp * kSub + g) * (D / 16) + t * (D / 64);
+  // token pairs u = 4 n + t of this warp's tokens: the slot permutation depends on t alone
+  const int off_v = C::S_V + (warp * (kSub / 2) + t) * D + (g ^ kv4_slot_xor(t, D)) * (D / 8);
+  const int off_sv = C::S_SV + (warp * (kSub / 2) + t) * (D / 8) + 2 * (D == 128 ? g : g / 2);
+  int i = 0;  // units consumed
   bool ok = true;
-  Cursor seg = locate(u_begin, b, seq_u0);
-  while (seg.u < u_end) {
-    const int seg_n = (int)min((long long)(seg.s.n - seg.unit), u_end - seg.u);
-    const bool whole = seg.unit == 0 && seg_n == seg.s.n;
-    const int hk = seg.vh / row_blocks, r0 = (seg.vh % row_blocks) * C::ROWS;
-    const int len = seg.s.len, first_tok = (seg.s.first + seg.unit) * kUnit;
+  while (left > 0) {
+    const int seg_n = min(at.s.n - at.unit, left);
+    const bool whole = at.unit == 0 && seg_n == at.s.n, at_begin = i == 0;
+    const int hk = at.vh / row_blocks, r0 = (at.vh % row_blocks) * C::ROWS;
+    const int len = at.s.len;
     // query fragments: lane (g, t) holds row r0 + 8 nt + g; dims [t D/4, (t + 1) D/4), in pairs
     // (x, x + 4) of each 8, the pairing of a code word's nibbles
     uint32_t qf[C::Q_SMEM ? 1 : MT][NT][2];
-    uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
+    [[maybe_unused]] uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
     if (!C::Q_SMEM || warp == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = r0 + 8 * nt + g;
         const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (((size_t)seg.b * p.S_q + r / G) * p.H_q + hk * G + r % G) * D + t * (D / 4));
+            p.q + (((size_t)at.b * p.S_q + r / G) * p.H_q + hk * G + r % G) * D + t * (D / 4));
 #pragma unroll
         for (int j = 0; j < MT / 2; ++j) {
           uint4 w = make_uint4(0u, 0u, 0u, 0u);
@@ -344,20 +342,10 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
         }
       }
     }
-    if constexpr (C::Q_SMEM) __syncthreads();
-    // this lane's score columns: rows r0 + 8 nt + 2 t and + 1
-    int row_hi[NT][2], row_lo[NT][2];
-    int hi_min = len - 1, lo_max = 0;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = r0 + 8 * nt + 2 * t + e, pos = len - p.S_q + min(r, R - 1) / G;
-        row_hi[nt][e] = pos;
-        row_lo[nt][e] = p.window >= 0 ? pos - p.window : 0;
-      }
-    hi_min = len - p.S_q + r0 / G;
-    lo_max = p.window >= 0 ? len - 1 - p.window : 0;
+    if constexpr (C::Q_SMEM) named_bar_sync(1, 32 * kWarps);
+    // keys that every row sees: [lo_max, hi_min]; that some row sees: [lo_min, len - 1]
+    const int hi_min = len - p.S_q + r0 / G;
+    const int lo_max = p.window >= 0 ? len - 1 - p.window : 0;
     const int lo_min = p.window >= 0 ? len - p.S_q - p.window : 0;
     float acc[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -370,16 +358,13 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // units of this segment that are this warp's: running numbers congruent to u_begin + warp
-    const int skip = (int)((warp - (seg.u - u_begin) % kWarps + kWarps) % kWarps);
-    for (int k = skip; k < seg_n; k += kWarps) {
-      const int stage = used % kStages;
-      ok = ok && mbar_wait_warp(&bars[stage], (used / kStages) & 1, p.err, kKv4Full);
-      ++used;
-      if (ok) {
-        const uint8_t* st = ring + stage * C::STAGE;
-        const int k0 = first_tok + k * kUnit;
-        const bool edge = k0 + kUnit - 1 > hi_min || k0 < lo_max;  // some key is hidden from some row
+    int k0 = (at.s.first + at.unit) * kUnit + warp * kSub;  // this warp's first token of the unit
+    for (int k = 0; k < seg_n; ++k, ++i, k0 += kUnit) {
+      const int stage = i % kStages;
+      ok = ok && mbar_wait_warp(&full[stage], (i / kStages) & 1, p.err, kKv4Full);
+      if (ok && k0 < len && k0 + kSub > lo_min) {
+        const uint8_t* st = smem + stage * C::STAGE;
+        const bool edge = k0 + kSub - 1 > hi_min || k0 < lo_max;  // some key is hidden from some row
         float s[2][NT][4];
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
@@ -390,18 +375,19 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
         // ---- scores of 2 x 16 tokens: lane (g, t) decodes tokens g, g + 8, its quarter of the dims
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-          const int ta = 16 * sub + g, tb = ta + 8;
           uint32_t wa[MT / 2], wb[MT / 2], sa, sb;
+          const uint8_t* ka = st + off_k + sub * 16 * (D / 2);
+          const uint8_t* ks = st + off_sk + sub * 16 * (D / 16);
           if constexpr (D == 128) {
-            *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(st + ta * (D / 2) + t * 16);
-            *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(st + tb * (D / 2) + t * 16);
-            sa = scale_pair(*reinterpret_cast<const unsigned short*>(st + C::S_SK + ta * (D / 16) + 2 * t));
-            sb = scale_pair(*reinterpret_cast<const unsigned short*>(st + C::S_SK + tb * (D / 16) + 2 * t));
+            *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(ka);
+            *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(ka + 8 * (D / 2));
+            sa = scale_pair(*reinterpret_cast<const unsigned short*>(ks));
+            sb = scale_pair(*reinterpret_cast<const unsigned short*>(ks + 8 * (D / 16)));
           } else {
-            *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(st + ta * (D / 2) + t * 8);
-            *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(st + tb * (D / 2) + t * 8);
-            sa = scale_pair(st[C::S_SK + ta * (D / 16) + t]);
-            sb = scale_pair(st[C::S_SK + tb * (D / 16) + t]);
+            *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(ka);
+            *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(ka + 8 * (D / 2));
+            sa = scale_pair(ks[0]);
+            sb = scale_pair(ks[8 * (D / 16)]);
           }
 #pragma unroll
           for (int j = 0; j < MT / 2; ++j) {  // a word: 8 dims, two k steps; 16 dims share a scale
@@ -427,38 +413,43 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
             }
           }
         }
-        // ---- softmax: s[sub][nt][e + 2 f] is token 16 sub + g + 8 f, row 2 t + e.  The running
-        // maximum moves only when some score passes it by 2^8 (the sums stay exact: they are
-        // relative to the maximum that was used)
+        // ---- softmax: s[sub][nt][e + 2 f] is token 16 sub + g + 8 f, row r0 + 8 nt + 2 t + e.  The
+        // running maximum (in log2 units) moves only when some score passes it by 2^8 (the sums
+        // stay exact: they are relative to the maximum that was used)
+        if (edge) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int pos = len - p.S_q + min(r0 + 8 * nt + 2 * t + e, R - 1) / G;
+              const int lo = p.window >= 0 ? pos - p.window : 0;
+#pragma unroll
+              for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                  const int j = k0 + 16 * sub + g + 8 * f;
+                  if (j > pos || j < lo) s[sub][nt][e + 2 * f] = -INFINITY;
+                }
+            }
+        }
+        float mx[NT][2];
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-              for (int f = 0; f < 2; ++f) {
-                float& x = s[sub][nt][e + 2 * f];
-                x *= p.scale_log2;
-                if (edge) {
-                  const int j = k0 + 16 * sub + g + 8 * f;
-                  if (j > row_hi[nt][e] || j < row_lo[nt][e]) x = -INFINITY;
-                }
-                mx = fmaxf(mx, x);
-              }
-            grow |= mx > m[nt][e] + 8.f;
+            mx[nt][e] = p.scale_log2 * fmaxf(fmax3(s[0][nt][e], s[0][nt][e + 2], s[1][nt][e]), s[1][nt][e + 2]);
+            grow |= mx[nt][e] > m[nt][e] + 8.f;
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
 #pragma unroll
-              for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-              const float mn = fmaxf(m[nt][e], mx);
+              for (int off = 4; off < 32; off <<= 1)
+                mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
+              const float mn = fmaxf(m[nt][e], mx[nt][e]);
               const float alpha = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
               m[nt][e] = mn;
               l[nt][e] *= alpha;
@@ -472,12 +463,13 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
         uint32_t pb[2][NT][2];  // P as the column operand: rows of the product = tokens
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-              const float x0 = ex2(s[sub][nt][2 * f] - m0), x1 = ex2(s[sub][nt][2 * f + 1] - m1);
+              const float x0 = ex2(fmaf(s[sub][nt][2 * f], p.scale_log2, m0));
+              const float x1 = ex2(fmaf(s[sub][nt][2 * f + 1], p.scale_log2, m1));
               l[nt][0] += x0;
               l[nt][1] += x1;
               pb[sub][nt][f] = transpose_8x8(pack_bf16x2(x0, x1));
@@ -489,24 +481,22 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
           uint32_t lo[2][MT / 4], hi[2][MT / 4], sv[2], cv[2];  // [pair][word]: both tokens' nibbles
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const int u = 8 * sub + t + 4 * f;
-            const uint8_t* at = st + C::S_V + u * D + (g ^ kv4_slot_xor(u, D)) * (D / 8);
-            uint32_t two;
+            const int u = 8 * sub + 4 * f;  // (+ t)
+            const uint8_t* va = st + off_v + u * D;
+            uint32_t two = *reinterpret_cast<const unsigned short*>(st + off_sv + u * (D / 8));
             if constexpr (D == 128) {
-              const uint4 w = *reinterpret_cast<const uint4*>(at);  // token 2u: x, y; token 2u + 1: z, w
+              const uint4 w = *reinterpret_cast<const uint4*>(va);  // token 2u: x, y; token 2u + 1: z, w
               lo[f][0] = __byte_perm(w.x, w.z, 0x5410);
               hi[f][0] = __byte_perm(w.x, w.z, 0x7632);
               lo[f][1] = __byte_perm(w.y, w.w, 0x5410);
               hi[f][1] = __byte_perm(w.y, w.w, 0x7632);
-              two = *reinterpret_cast<const unsigned short*>(st + C::S_SV + u * (D / 8) + 2 * g);
             } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(at);
+              const uint2 w = *reinterpret_cast<const uint2*>(va);
               lo[f][0] = __byte_perm(w.x, w.y, 0x5410);
               hi[f][0] = __byte_perm(w.x, w.y, 0x7632);
-              two = *reinterpret_cast<const unsigned short*>(st + C::S_SV + u * (D / 8) + 2 * (g / 2));
             }
             if (edge) {  // tokens that no row sees: whatever their bytes are, they add nothing
-              const int j = k0 + 2 * u;
+              const int j = k0 + 2 * (u + t);
               if (j > len - 1 || j < lo_min) two &= 0xFF00u;
               if (j + 1 > len - 1 || j + 1 < lo_min) two &= 0x00FFu;
             }
@@ -533,7 +523,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
         }
       }
       __syncwarp();  // every lane has read the stage: it may be filled again
-      issue_next();
+      if (lane == 0) mbar_arrive(&empty[stage]);
     }
 
     // ---- the warps' sums become one: maxima and denominators, then the rows, warp by warp
@@ -548,7 +538,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
           xl[warp * C::ROWS + 8 * nt + 2 * t + e] = l[nt][e];
         }
       }
-    __syncthreads();
+    named_bar_sync(1, 32 * kWarps);
     float f[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -569,21 +559,20 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
             for (int q = 0; q < MT / 2; ++q) {
               // D/8 consecutive dims of row 2 t + e: tiles 0.. give the first half, their + 8 rows the second
               constexpr int QH = MT / 4;
-              float4* at = reinterpret_cast<float4*>(xch + (8 * nt + 2 * t + e) * C::XS + g * (D / 8) + 4 * q);
+              float4* x = reinterpret_cast<float4*>(xch + (8 * nt + 2 * t + e) * C::XS + g * (D / 8) + 4 * q);
               const int mt = 4 * (q % QH), hf = q / QH;
               float4 v = make_float4(acc[mt][nt][e + 2 * hf] * f[nt][e], acc[mt + 1][nt][e + 2 * hf] * f[nt][e],
                                      acc[mt + 2][nt][e + 2 * hf] * f[nt][e], acc[mt + 3][nt][e + 2 * hf] * f[nt][e]);
               if (w > 0) {
-                const float4 o = *at;
+                const float4 o = *x;
                 v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
               }
-              *at = v;
+              *x = v;
             }
       }
-      __syncthreads();
+      named_bar_sync(1, 32 * kWarps);
     }
     // ---- the whole of a (sequence, head): outputs; a piece of it: partial sums
-    const bool at_begin = seg.u == u_begin;
     float* slot = partial + ((size_t)2 * blockIdx.x + (at_begin ? 0 : 1)) * C::SLOT;
     for (int r = warp; r < C::ROWS && r0 + r < R; r += kWarps) {
       float mm = xm[r], ll = 0.f;
@@ -595,10 +584,10 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
       if (whole) {
         const int qs_ = (r0 + r) / G, h = hk * G + (r0 + r) % G;
         const Kv4Sums z = kv4_finish(p, h, mm, ll);
-        __nv_bfloat16* o = p.o + (((size_t)seg.b * p.S_q + qs_) * p.H_q + h) * D;
+        __nv_bfloat16* o = p.o + (((size_t)at.b * p.S_q + qs_) * p.H_q + h) * D;
         for (int x = 2 * lane; x < D; x += 64)
           *reinterpret_cast<uint32_t*>(o + x) = pack_bf16x2(xch[r * C::XS + x] * z.mul, xch[r * C::XS + x + 1] * z.mul);
-        if (lane == 0 && p.lse) p.lse[((size_t)seg.b * p.H_q + h) * p.S_q + qs_] = z.lse;
+        if (lane == 0 && p.lse) p.lse[((size_t)at.b * p.H_q + h) * p.S_q + qs_] = z.lse;
       } else {
         for (int x = lane; x < D; x += 32) slot[r * D + x] = xch[r * C::XS + x];
         if (lane == 0) {
@@ -607,19 +596,9 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_decode_kernel(const Kv4Decode
         }
       }
     }
-    __syncthreads();  // the exchange is free for the next segment
-    seg.u += seg_n;
-    seg.unit += seg_n;
-    if (seg.u < u_end && seg.unit >= seg.s.n) {
-      seg.unit = 0;
-      if (++seg.vh == H_eff) {
-        seg.vh = 0;
-        do {
-          ++seg.b;
-          seg.s = seq_of(p, seg.b);
-        } while (seg.s.n == 0);
-      }
-    }
+    named_bar_sync(1, 32 * kWarps);  // the exchange is free for the next segment
+    left -= seg_n;
+    if (left > 0) next_segment(at);
   }
 }
 
@@ -717,13 +696,13 @@ int launch_t(const Kv4DecodeParams& p, float* partial, cudaStream_t stream) {
   int per_sm = 0, sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * kWarps, C::SMEM) != cudaSuccess)
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, C::SMEM) != cudaSuccess)
     return -1;
   const int grid = std::max(1, std::min(kMaxCtas, per_sm * sms));
   const int rows = p.H_q / p.c.H_kv * p.S_q, blocks = (rows + C::ROWS - 1) / C::ROWS;
   const long long join = (long long)p.B * p.c.H_kv * blocks;
   if (join > 0x7fffffffLL) return -2;
-  kern<<<grid, 32 * kWarps, C::SMEM, stream>>>(p, blocks, partial);
+  kern<<<grid, kThreads, C::SMEM, stream>>>(p, blocks, partial);
   kv4_join_kernel<D><<<dim3((unsigned)join, std::min(rows, C::ROWS)), 256, 0, stream>>>(p, blocks, C::ROWS, grid,
                                                                                         partial);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
