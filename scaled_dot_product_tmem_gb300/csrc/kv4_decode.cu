@@ -71,14 +71,17 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 }
 
 // Codes c in bits 0-3 and 16-19 of w as the bf16 pair (c - 8) s, with s and -136 s paired.
+// The mask and the exponent bits are one three-input operation, (w & mask) | bits.
 __device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t s, uint32_t m136s) {
-  return bf2_fma((w & 0x000F000Fu) | 0x43004300u, s, m136s);
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(0x000F000Fu), "r"(0x43004300u));
+  return bf2_fma(x, s, m136s);
 }
-// Two scale bytes (low, next) as a bf16 pair.
+// Two scale bytes (low, next) as a bf16 pair: bits 14..7 of two half-precision numbers.
 __device__ __forceinline__ uint32_t scale_pair(uint32_t two) {
-  const float lo = __half2float(__ushort_as_half((unsigned short)((two & 0xFFu) << 7)));
-  const float hi = __half2float(__ushort_as_half((unsigned short)((two >> 8) << 7)));
-  return pack_bf16x2(lo, hi);
+  const uint32_t h = __byte_perm(two, 0u, 0x4140) << 7;
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16x2(f.x, f.y);
 }
 constexpr uint32_t kM136 = 0xC308C308u;  // -136 as a bf16 pair
 
