@@ -16,6 +16,12 @@ bool supported(int page_size, int d) {
   return (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128) && (d == 64 || d == 128);
 }
 
+int log2_of(int page_size) {
+  int n = 0;
+  while ((1 << n) < page_size) ++n;
+  return n;
+}
+
 // Sizes shared by the calls that walk a page table.
 int check_sizes(int B, int H_kv, int d, int n_pages, int page_size, int max_pages) {
   if (B < 0 || H_kv <= 0 || n_pages < 0 || max_pages < 0) return ATTN_ERR_INVALID_ARG;
@@ -53,7 +59,7 @@ int attn_kv4_append(const void* k, const void* v, const int* cu_seqlens, void* p
       !aligned(cu_seqlens, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4))
     return ATTN_ERR_MISALIGNED;
   sdpa::Kv4StoreParams p;
-  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d};
+  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d, log2_of(page_size)};
   p.B = B;
   p.T = T;
   p.cu = cu_seqlens;
@@ -82,7 +88,7 @@ int attn_kv4_gather(const void* pool, const int* page_table, const int* cu_seqle
       !aligned(page_table, 4) || !aligned(seq_lens, 4))
     return ATTN_ERR_MISALIGNED;
   sdpa::Kv4StoreParams p;
-  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d};
+  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d, log2_of(page_size)};
   p.B = B;
   p.T = T;
   p.cu = cu_seqlens;
@@ -122,7 +128,7 @@ int attn_kv4_decode(const void* q, const void* pool, const int* page_table, cons
       workspace_bytes < sdpa::kv4_decode_workspace(B, S_q, H_q, H_kv, d))
     return ATTN_ERR_WORKSPACE;
   sdpa::Kv4DecodeParams p;
-  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d};
+  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d, log2_of(page_size)};
   p.B = B;
   p.S_q = S_q;
   p.H_q = H_q;

@@ -30,6 +30,7 @@ struct Kv4Pool {
   const int* page_table;  // [B, max_pages]
   int n_pages, page_size, max_pages;
   int H_kv, d;
+  int page_shift;  // log2(page_size)
 };
 
 // Byte offsets of the four parts inside a block.
@@ -66,9 +67,9 @@ __device__ __forceinline__ float kv4_scale_value(int byte) {
 constexpr int kKv4BadScale = 0xFF;  // 16 values with an infinity or NaN among them: a NaN scale
 
 // The page that holds token `pos` of sequence b, or -1 (outside the table or the pool).
-__device__ __forceinline__ int kv4_page(const Kv4Pool& c, int b, long long pos) {
-  if (pos < 0 || pos >= (long long)c.max_pages * c.page_size) return -1;
-  const int pg = __ldg(c.page_table + (size_t)b * c.max_pages + (int)(pos / c.page_size));
+__device__ __forceinline__ int kv4_page(const Kv4Pool& c, int b, int pos) {
+  if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) return -1;
+  const int pg = __ldg(c.page_table + (size_t)b * c.max_pages + (pos >> c.page_shift));
   return (pg < 0 || pg >= c.n_pages) ? -1 : pg;
 }
 

@@ -58,15 +58,22 @@ __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
 // d (16 x 8 fp32) += a (16 x 16 bf16, rows) b (16 x 8 bf16, columns)
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = a b
+__device__ __forceinline__ void mma_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // transpose of an 8 x 8 matrix of 16-bit values spread over a warp
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
       // whole 16-token groups up to the sequence's end
       const int bytes = page == -2 ? 0 : min(piece, (at.s.len - tok + 15) / 16 * 16) * per;
       const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (at.vh / row_blocks) * block + src_off +
-                           (size_t)(tok % P) * per;
+                           (size_t)(tok & (P - 1)) * per;
       const int have = page;
       if (i + 1 < left) {
         if (++at.unit == at.s.n) next_segment(at);
@@ -369,53 +376,48 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
         const uint8_t* st = smem + stage * C::STAGE;
         const bool edge = k0 + kSub - 1 > hi_min || k0 < lo_max;  // some key is hidden from some row
         float s[2][NT][4];
+        // ---- scores of 2 x 16 tokens: lane (g, t) decodes tokens g, g + 8, its quarter of the dims
+        uint32_t wk[2][2][MT / 2], sk[2][2];  // [half of 16][token g or g + 8]
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[sub][nt][e] = 0.f;
-        // ---- scores of 2 x 16 tokens: lane (g, t) decodes tokens g, g + 8, its quarter of the dims
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          uint32_t wa[MT / 2], wb[MT / 2], sa, sb;
-          const uint8_t* ka = st + off_k + sub * 16 * (D / 2);
-          const uint8_t* ks = st + off_sk + sub * 16 * (D / 16);
-          if constexpr (D == 128) {
-            *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(ka);
-            *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(ka + 8 * (D / 2));
-            sa = scale_pair(*reinterpret_cast<const unsigned short*>(ks));
-            sb = scale_pair(*reinterpret_cast<const unsigned short*>(ks + 8 * (D / 16)));
-          } else {
-            *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(ka);
-            *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(ka + 8 * (D / 2));
-            sa = scale_pair(ks[0]);
-            sb = scale_pair(ks[8 * (D / 16)]);
+          for (int f = 0; f < 2; ++f) {
+            const uint8_t* kc = st + off_k + (16 * sub + 8 * f) * (D / 2);
+            const uint8_t* ks = st + off_sk + (16 * sub + 8 * f) * (D / 16);
+            if constexpr (D == 128) {
+              *reinterpret_cast<uint4*>(wk[sub][f]) = *reinterpret_cast<const uint4*>(kc);
+              sk[sub][f] = scale_pair(*reinterpret_cast<const unsigned short*>(ks));
+            } else {
+              *reinterpret_cast<uint2*>(wk[sub][f]) = *reinterpret_cast<const uint2*>(kc);
+              sk[sub][f] = scale_pair(ks[0]);
+            }
           }
 #pragma unroll
-          for (int j = 0; j < MT / 2; ++j) {  // a word: 8 dims, two k steps; 16 dims share a scale
-            const uint32_t s2a = j < 2 ? __byte_perm(sa, sa, 0x1010) : __byte_perm(sa, sa, 0x3232);
-            const uint32_t s2b = j < 2 ? __byte_perm(sb, sb, 0x1010) : __byte_perm(sb, sb, 0x3232);
-            const uint32_t ca = bf2_mul(s2a, kM136), cb = bf2_mul(s2b, kM136);
-            uint32_t a[4], c[4];
+        for (int j = 0; j < MT / 2; ++j)  // a word: 8 dims, two k steps; 16 dims share a scale
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              a[e] = decode_pair(wa[j] >> (4 * e), s2a, ca);
-              c[e] = decode_pair(wb[j] >> (4 * e), s2b, cb);
+          for (int sub = 0; sub < 2; ++sub) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const uint32_t s2 = __byte_perm(sk[sub][f], 0u, j < 2 ? 0x1010 : 0x3232), c2 = bf2_mul(s2, kM136);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[f][e] = decode_pair(wk[sub][f][j] >> (4 * e), s2, c2);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              uint2 q0, q1;
               if constexpr (C::Q_SMEM) {
-                const uint2 q0 = qs[((2 * j) * NT + nt) * 32 + lane], q1 = qs[((2 * j + 1) * NT + nt) * 32 + lane];
-                mma_16816(s[sub][nt], a[0], c[0], a[1], c[1], q0.x, q0.y);
-                mma_16816(s[sub][nt], a[2], c[2], a[3], c[3], q1.x, q1.y);
+                q0 = qs[((2 * j) * NT + nt) * 32 + lane];
+                q1 = qs[((2 * j + 1) * NT + nt) * 32 + lane];
               } else {
-                mma_16816(s[sub][nt], a[0], c[0], a[1], c[1], qf[2 * j][nt][0], qf[2 * j][nt][1]);
-                mma_16816(s[sub][nt], a[2], c[2], a[3], c[3], qf[2 * j + 1][nt][0], qf[2 * j + 1][nt][1]);
+                q0 = make_uint2(qf[2 * j][nt][0], qf[2 * j][nt][1]);
+                q1 = make_uint2(qf[2 * j + 1][nt][0], qf[2 * j + 1][nt][1]);
               }
+              if (j == 0) mma_16816_zero(s[sub][nt], a[0][0], a[1][0], a[0][1], a[1][1], q0.x, q0.y);
+              else mma_16816(s[sub][nt], a[0][0], a[1][0], a[0][1], a[1][1], q0.x, q0.y);
+              mma_16816(s[sub][nt], a[0][2], a[1][2], a[0][3], a[1][3], q1.x, q1.y);
             }
           }
-        }
         // ---- softmax: s[sub][nt][e + 2 f] is token 16 sub + g + 8 f, row r0 + 8 nt + 2 t + e.  The
         // running maximum (in log2 units) moves only when some score passes it by 2^8 (the sums
         // stay exact: they are relative to the maximum that was used)

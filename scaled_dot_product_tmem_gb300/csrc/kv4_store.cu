@@ -25,11 +25,11 @@ __device__ __forceinline__ void find_tokens(const Kv4StoreParams& p, int t0, Tok
       const int b = packed_row_entry(p.cu, p.B, t);
       if (b >= 0) {
         const long long pos = (long long)__ldg(p.start + b) + (t - __ldg(p.cu + b));
-        const int pg = kv4_page(p.c, b, pos);
+        const int pg = pos > 0x7fffffffLL ? -1 : kv4_page(p.c, b, (int)pos);  // (pos may be negative)
         a.block = -1;
         if (pg >= 0) {
           a.block = (long long)pg * p.c.H_kv * kv4_block_bytes(p.c.page_size, p.c.d);
-          a.w = (int)(pos % p.c.page_size);
+          a.w = (int)pos & (p.c.page_size - 1);
         } else {
           atomicCAS(p.page_err, 0, p.site);
         }
