@@ -120,67 +120,54 @@ __device__ __forceinline__ Seq seq_of(const Kv4DecodeParams& p, int b) {
   return s;
 }
 
-// Block-wide: the units of all sequences before b0 and of all (each sequence counts H_eff
-// times its units), and, for a unit u, the sequence that holds it with the units before it.
-template <int THREADS>
+// How the units of a call are numbered: sequence by sequence, each sequence's H_eff heads (kv
+// head and row block) one after another.  Every warp works this out for itself: a few loads
+// and shuffles, and no barrier.
 struct UnitScan {
-  long long total;
-  __device__ void run(const Kv4DecodeParams& p, int H_eff, long long* part) {
+  long long total;  // units of all sequences and heads
+  __device__ void run(const Kv4DecodeParams& p, int H_eff) {
     long long t = 0;
-    for (int b = threadIdx.x; b < p.B; b += THREADS) t += seq_of(p, b).n;
+    for (int b = threadIdx.x % 32; b < p.B; b += 32) t += seq_of(p, b).n;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = t;
-    __syncthreads();
-    t = 0;
-    for (int w = 0; w < THREADS / 32; ++w) t += part[w];
     total = t * H_eff;
-    __syncthreads();
   }
-  // The units (times H_eff) of sequences 0 .. b_end - 1; with find >= 0 instead stops at the
-  // sequence that holds unit `find`: returns the units before it and sets *b.
-  __device__ long long before(const Kv4DecodeParams& p, int H_eff, int b_end, long long find, int* b,
-                              long long* part) {
+  // The units of sequences 0 .. b_end - 1; with find >= 0 stops at the sequence that holds unit
+  // `find`: returns the units before it and sets *b.
+  __device__ long long before(const Kv4DecodeParams& p, int H_eff, int b_end, long long find, int* b) {
+    const int lane = threadIdx.x % 32;
     long long carry = 0;
-    for (int base = 0; base < b_end; base += THREADS) {
-      const int i = base + threadIdx.x;
+    for (int base = 0; base < b_end; base += 32) {
+      const int i = base + lane;
       const long long n = i < b_end ? (long long)seq_of(p, i).n * H_eff : 0;
       long long s = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, s, off);
-        if (threadIdx.x % 32 >= off) s += o;
+        if (lane >= off) s += o;
       }
-      if (threadIdx.x % 32 == 31) part[threadIdx.x / 32] = s;
-      __syncthreads();
-      long long sum = carry;
-      for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < (int)threadIdx.x / 32) s += part[w];
-        sum += part[w];
+      s += carry;  // units up to and with sequence i
+      const unsigned holds = __ballot_sync(0xffffffffu, find >= 0 && find < s);
+      if (holds) {
+        const int w = __ffs(holds) - 1;
+        *b = base + w;
+        return __shfl_sync(0xffffffffu, s - n, w);
       }
-      __syncthreads();
-      if (find >= 0 && find < sum) {  // uniform: the unit is in this chunk
-        const long long lo = carry + s - n;
-        if (n > 0 && find >= lo && find < lo + n) {
-          part[0] = lo;
-          part[1] = i;
-        }
-        __syncthreads();
-        const long long r = part[0];
-        *b = (int)part[1];
-        __syncthreads();
-        return r;
-      }
-      carry = sum;
+      carry = __shfl_sync(0xffffffffu, s, 31);
     }
     return carry;
   }
 };
 
 // CTA c of n takes units [cta_first(c), cta_first(c + 1)).
-__device__ __forceinline__ long long cta_first(long long total, int n, int c) { return total * c / n; }
+// (32-bit division where the product fits, as it nearly always does)
+__device__ __forceinline__ long long muldiv(long long a, int b, long long d) {
+  return a < (1 << 22) && d < (1LL << 32) ? (long long)((unsigned)a * (unsigned)b / (unsigned)d) : a * b / d;
+}
+static_assert(((1LL << 22) - 1) * kMaxCtas < (1LL << 32), "the 32-bit product");
+__device__ __forceinline__ long long cta_first(long long total, int n, int c) { return muldiv(total, c, n); }
 __device__ __forceinline__ int cta_of(long long total, int n, long long u) {
-  int c = (int)(((u + 1) * n - 1) / total);  // the last c with cta_first(c) <= u
+  int c = (int)muldiv(u, n, total);  // near the last c with cta_first(c) <= u
   while (c > 0 && cta_first(total, n, c) > u) --c;
   while (c + 1 < n && cta_first(total, n, c + 1) <= u) ++c;
   return c;
@@ -200,8 +187,7 @@ struct DecCfg {
   static constexpr int XS = D + 4;  // row stride of the exchange (bank spread)
   static constexpr int OFF_X = OFF_Q + Q_BYTES;
   static constexpr int OFF_ML = OFF_X + ROWS * XS * 4;           // [kWarps][ROWS] maxima, then sums
-  static constexpr int OFF_SCAN = OFF_ML + 2 * kWarps * ROWS * 4;
-  static constexpr int OFF_BAR = OFF_SCAN + 64;  // full[kStages], empty[kStages]
+  static constexpr int OFF_BAR = OFF_ML + 2 * kWarps * ROWS * 4;  // full[kStages], empty[kStages]
   static constexpr int SMEM = OFF_BAR + 2 * kStages * 8;
   static constexpr int SLOT = ROWS * (D + 2);  // floats of one partial: rows of sums, maxima, denominators
 };
@@ -217,7 +203,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + kStages;
-  long long* part = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
   const int G = p.H_q / p.c.H_kv, R = G * p.S_q, H_eff = p.c.H_kv * row_blocks;
 
   if (threadIdx.x == 0) {
@@ -227,8 +212,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     }
     fence_barrier_init();
   }
-  UnitScan<kThreads> scan;
-  scan.run(p, H_eff, part);  // (its barriers also order the mbarrier set-up)
+  grid_launch_dependents();  // the join may be set up meanwhile
+  UnitScan scan;
+  scan.run(p, H_eff);
+  __syncthreads();  // the barriers are set up
   if (scan.total == 0) return;
   const int n_cta = ctas_used(scan.total, gridDim.x);
   if ((int)blockIdx.x >= n_cta) return;
@@ -240,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     Seq s;
   } at;
   {
-    const long long r = u_begin - scan.before(p, H_eff, p.B, u_begin, &at.b, part);
+    const long long r = u_begin - scan.before(p, H_eff, p.B, u_begin, &at.b);  // < 2^31: one sequence's
     at.s = seq_of(p, at.b);
     at.vh = (int)(r / at.s.n);
     at.unit = (int)(r % at.s.n);
@@ -607,83 +594,85 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
   }
 }
 
-// Joins the pieces of every (sequence, head) that spans several CTAs, in CTA order, and writes
-// the rows of sequences without a token.  One block per (sequence, kv head, row block, row).
+// Joins the pieces of every (sequence, head) that spans several CTAs, and writes the rows of
+// sequences without a token.  One block per (sequence, kv head, row block, row): warp w takes
+// pieces w, w + 8, ... in order, then the eight are added in order.  Launched while the
+// decode kernel runs: it waits for that kernel's end before it reads a piece.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeParams p, int row_blocks, int rows, int grid,
                                                        const float* partial) {
-  __shared__ long long part[8];
-  __shared__ float wgt[kMaxCtas], red[8], sums[8][D];
+  __shared__ float red[2][8], sums[8][D];
   const int G = p.H_q / p.c.H_kv, R = G * p.S_q, H_eff = p.c.H_kv * row_blocks;
   const int b = blockIdx.x / H_eff, vh = blockIdx.x % H_eff, r = blockIdx.y;
   const int hk = vh / row_blocks, row = (vh % row_blocks) * rows + r;
-  if (row >= R) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // every block waits, also one with nothing to do: this grid must not end before the decode
+  // kernel, or what follows on the stream could start beside it
   const Seq s = seq_of(p, b);
+  if (row >= R) {
+    grid_wait();
+    return;
+  }
   const int qs = row / G, h = hk * G + row % G;
   __nv_bfloat16* o = p.o + (((size_t)b * p.S_q + qs) * p.H_q + h) * D;
   float* lse = p.lse ? p.lse + ((size_t)b * p.H_q + h) * p.S_q + qs : nullptr;
   if (s.n == 0) {
+    grid_wait();
     if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(o)[threadIdx.x] = 0u;
     if (threadIdx.x == 0 && lse) *lse = kv4_finish(p, h, -INFINITY, 0.f).lse;
     return;
   }
-  UnitScan<256> scan;
-  scan.run(p, H_eff, part);
+  UnitScan scan;
+  scan.run(p, H_eff);
   int unused;
-  const long long u0 = scan.before(p, H_eff, b, -1, &unused, part) + (long long)vh * s.n;
+  const long long u0 = scan.before(p, H_eff, b, -1, &unused) + (long long)vh * s.n;
   const int n_cta = ctas_used(scan.total, grid);
   const int c0 = cta_of(scan.total, n_cta, u0), c1 = cta_of(scan.total, n_cta, u0 + s.n - 1);
-  if (c0 == c1) return;  // one CTA had all of it
-  const int slot_floats = rows * (D + 2), n = c1 - c0 + 1;
-  auto slot_of = [&](int c) {  // the piece is the CTA's first where the CTA starts inside it
-    return partial + ((size_t)2 * c + (cta_first(scan.total, n_cta, c) >= u0 ? 0 : 1)) * slot_floats;
-  };
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  auto block_max = [&](float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    v = red[0];
-    for (int w = 1; w < 8; ++w) v = fmaxf(v, red[w]);
-    __syncthreads();
-    return v;
-  };
-  float mx = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += 256) mx = fmaxf(mx, slot_of(c0 + i)[rows * D + r]);
-  mx = block_max(mx);
-  float ll = 0.f;
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const float* sl = slot_of(c0 + i);
-    const float mi = sl[rows * D + r], w = mi == -INFINITY ? 0.f : ex2(mi - mx);
-    wgt[i] = w;
-    const float li = sl[rows * D + rows + r];
-    ll += mi == -INFINITY ? li : w * li;
+  if (c0 == c1) {  // one CTA had all of it
+    grid_wait();
+    return;
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
-  if (lane == 0) red[warp] = ll;
-  __syncthreads();
-  ll = 0.f;
-  for (int w = 0; w < 8; ++w) ll += red[w];
+  const int slot_floats = rows * (D + 2);
   constexpr int E = D / 32;
-  float a[E];
+  float a[E], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) a[e] = 0.f;
-  for (int i = warp; i < n; i += 8) {
-    const float w = wgt[i];
-    const float* sl = slot_of(c0 + i) + r * D + lane * E;
+  grid_wait();
+#pragma unroll 2
+  for (int c = c0 + warp; c <= c1; c += 8) {
+    // the piece is the CTA's first where the CTA starts inside it
+    const float* sl = partial + ((size_t)2 * c + (cta_first(scan.total, n_cta, c) >= u0 ? 0 : 1)) * slot_floats;
+    const float mi = sl[rows * D + r], li = sl[rows * D + rows + r];
+    float v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (w != 0.f) a[e] = fmaf(w, sl[e], a[e]);
+    for (int e = 0; e < E; ++e) v[e] = sl[r * D + lane * E + e];
+    const float mn = fmaxf(m, mi);
+    const float f = m == -INFINITY ? 0.f : ex2(m - mn), w = mi == -INFINITY ? 0.f : ex2(mi - mn);
+    l = (m == -INFINITY ? l : l * f) + (mi == -INFINITY ? li : li * w);  // (no key: 0, or a NaN that has to stay)
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = a[e] * f + (w == 0.f ? 0.f : v[e] * w);
+    m = mn;
+  }
+  if (lane == 0) {
+    red[0][warp] = m;
+    red[1][warp] = l;
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = a[e];
   __syncthreads();
+  float mx = red[0][0], ll = 0.f;
+  for (int w = 1; w < 8; ++w) mx = fmaxf(mx, red[0][w]);
+  float f[8];
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    f[w] = red[0][w] == -INFINITY ? 0.f : ex2(red[0][w] - mx);
+    ll += red[0][w] == -INFINITY ? red[1][w] : red[1][w] * f[w];
+  }
   const Kv4Sums z = kv4_finish(p, h, mx, ll);
   if (threadIdx.x < D) {
     float v = 0.f;
-    for (int w = 0; w < 8; ++w) v += sums[w][threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v = fmaf(sums[w][threadIdx.x], f[w], v);
     o[threadIdx.x] = __float2bfloat16(v * z.mul);
   }
   if (threadIdx.x == 0 && lse) *lse = z.lse;
@@ -708,8 +697,17 @@ int launch_t(const Kv4DecodeParams& p, float* partial, cudaStream_t stream) {
   const long long join = (long long)p.B * p.c.H_kv * blocks;
   if (join > 0x7fffffffLL) return -2;
   kern<<<grid, kThreads, C::SMEM, stream>>>(p, blocks, partial);
-  kv4_join_kernel<D><<<dim3((unsigned)join, std::min(rows, C::ROWS)), 256, 0, stream>>>(p, blocks, C::ROWS, grid,
-                                                                                        partial);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)join, std::min(rows, C::ROWS));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv4_join_kernel<D>, p, blocks, (int)C::ROWS, grid, (const float*)partial) != cudaSuccess)
+    return -1;
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
