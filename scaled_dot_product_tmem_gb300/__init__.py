@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -630,22 +631,41 @@ def sdpa_backward_fp8(q, k, v, o, dout, lse, *, ds_amax=None, ds_amax_out=None, 
 # ----------------------------------------------------------------------------- packed sequences
 
 
-def _one_device(*tensors):
-    """A context with the device of the tensors (None skipped) as the current one; they share it."""
-    dev = None
+def _p(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _device_of(*tensors):
+    """The one CUDA device of the tensors (None skipped), as its number."""
+    dev = -1
     for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    return torch.cuda.device(dev)
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if dev >= 0 or i < 0:
+                    raise ValueError(f"tensors on different devices, or not on a CUDA device: {t.device} and others")
+                dev = i
+    return dev
 
 
-def _allocating(stream):
-    """A context in which new tensors belong to the stream that the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+@contextlib.contextmanager
+def _on(dev, stream):
+    """Device `dev` current, and new tensors belonging to the stream that the call runs on."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _elsewhere(dev, stream):
+    """Whether a call has to leave the current device or stream to allocate its tensors."""
+    return stream is not None or dev != torch.cuda.current_device()
+
+
+def _raw_stream(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _check_cu(cu, name, B=None):
@@ -655,6 +675,7 @@ def _check_cu(cu, name, B=None):
                          + (f" ({B + 1} values)" if B is not None else "") + f", got {cu.shape[0]}")
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_packed_workspace_size(B, T_q, T_kv, H_q, H_kv, d_qk, d_v, backward=False) -> int:
     return int(_load().attn_packed_workspace_size(B, T_q, T_kv, H_q, H_kv, d_qk, d_v, int(bool(backward))))
 
@@ -680,7 +701,7 @@ def _check_packed(q, k, v, cu_q, cu_kv, softmax_offset):
     return B, T_q, T_kv, H_q, H_kv, d_qk, d_v
 
 
-def _packed_workspace(workspace, need, device):
+def _workspace(workspace, need, device):
     if workspace is None:
         return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
     _check(workspace, "workspace", torch.uint8, 1)
@@ -704,12 +725,17 @@ def attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv=None, *, causal
     _check(lse, "lse", torch.float32, 2)
     if tuple(o.shape) != (T_q, H_q, d_v) or tuple(lse.shape) != (H_q, T_q):
         raise ValueError(f"o must be {(T_q, H_q, d_v)} and lse {(H_q, T_q)}, got {tuple(o.shape)}, {tuple(lse.shape)}")
-    with _one_device(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, softmax_offset, workspace), _allocating(stream):
-        ws = _packed_workspace(workspace, attn_packed_workspace_size(*sizes) if workspace is None else 0, q.device)
-        st = _load().attn_fwd_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens_q),
-                                     _ptr(cu_seqlens_kv), *sizes, float(scale or 0.0), int(bool(causal)), int(window),
-                                     _stype(softmax_type), _ptr(softmax_offset), int(bool(zero_rest)), _ptr(ws),
-                                     ws.numel(), _stream(stream))
+    dev = _device_of(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, softmax_offset, workspace)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, causal=causal, window=window,
+                                   softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
+                                   zero_rest=zero_rest, workspace=workspace)
+    ws = _workspace(workspace, attn_packed_workspace_size(*sizes) if workspace is None else 0, q.device)
+    st = _load().attn_fwd_packed(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(cu_seqlens_q), _p(cu_seqlens_kv), *sizes,
+                                 float(scale or 0.0), int(bool(causal)), int(window), _stype(softmax_type),
+                                 _p(softmax_offset), int(bool(zero_rest)), _p(ws), ws.numel(),
+                                 _raw_stream(dev, stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_packed")
 
@@ -733,15 +759,19 @@ def attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, c
         _check(d_offset, "d_offset", torch.float32, 1)
         if d_offset.shape[0] != H_q:
             raise ValueError(f"d_offset must have one value per query head ({H_q})")
-    with _one_device(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv, softmax_offset,
-                     workspace), _allocating(stream):
-        ws = _packed_workspace(workspace, attn_packed_workspace_size(*sizes, True) if workspace is None else 0,
-                               q.device)
-        st = _load().attn_bwd_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
-                                     _ptr(dv), _ptr(d_offset), _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv), *sizes,
-                                     float(scale or 0.0), int(bool(causal)), int(window), _stype(softmax_type),
-                                     _ptr(softmax_offset), int(bool(zero_rest)), _ptr(ws), ws.numel(),
-                                     _stream(stream))
+    dev = _device_of(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv, softmax_offset,
+                     workspace)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv,
+                                   causal=causal, window=window, softmax_type=softmax_type,
+                                   softmax_offset=softmax_offset, scale=scale, zero_rest=zero_rest,
+                                   workspace=workspace)
+    ws = _workspace(workspace, attn_packed_workspace_size(*sizes, True) if workspace is None else 0, q.device)
+    st = _load().attn_bwd_packed(_p(q), _p(k), _p(v), _p(o), _p(dout), _p(lse), _p(dq), _p(dk), _p(dv), _p(d_offset),
+                                 _p(cu_seqlens_q), _p(cu_seqlens_kv), *sizes, float(scale or 0.0), int(bool(causal)),
+                                 int(window), _stype(softmax_type), _p(softmax_offset), int(bool(zero_rest)), _p(ws),
+                                 ws.numel(), _raw_stream(dev, stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_bwd_packed")
 
@@ -750,12 +780,16 @@ def sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv=None, *, causal=Tru
                         softmax_offset=None, scale=0.0, workspace=None, stream=None):
     """Allocate O and LSE, run attn_fwd_packed, return (o, lse); rows past the last sequence are
     zero (lse -inf)."""
-    with _one_device(q), _allocating(stream):
-        o = torch.empty((q.shape[0], q.shape[1], v.shape[2]), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-        attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, causal=causal, window=window,
-                        softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale, zero_rest=True,
-                        workspace=workspace, stream=stream)
+    kw = dict(causal=causal, window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
+              workspace=workspace)
+    dev = _device_of(q)
+    if dev >= 0 and _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, **kw)
+    T_q, H_q, _ = q.shape
+    o = torch.empty((T_q, H_q, v.shape[2]), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((H_q, T_q), dtype=torch.float32, device=q.device)
+    attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, zero_rest=True, **kw)
     return o, lse
 
 
@@ -763,13 +797,16 @@ def sdpa_backward_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv=None
                          softmax_type=VANILLA, softmax_offset=None, scale=0.0, workspace=None, stream=None):
     """Allocate dQ, dK, dV (and d_offset for the learnable sink), run attn_bwd_packed, return
     them; gradients of rows past the last sequence are zero."""
-    with _one_device(q), _allocating(stream):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        d_off = (torch.empty((q.shape[1],), dtype=torch.float32, device=q.device)
-                 if _stype(softmax_type) == LEARNABLE else None)
-        attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_off, cu_seqlens_q, cu_seqlens_kv, causal=causal,
-                        window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
-                        zero_rest=True, workspace=workspace, stream=stream)
+    kw = dict(causal=causal, window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
+              workspace=workspace)
+    dev = _device_of(q)
+    if dev >= 0 and _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return sdpa_backward_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv, **kw)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    d_off = (torch.empty((q.shape[1],), dtype=torch.float32, device=q.device)
+             if _stype(softmax_type) == LEARNABLE else None)
+    attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_off, cu_seqlens_q, cu_seqlens_kv, zero_rest=True, **kw)
     return dq, dk, dv, d_off
 
 
@@ -810,6 +847,7 @@ def kv4_pool(n_pages, H_kv, d, page_size, *, n_layers=None, device="cuda"):
     return torch.empty(shape, dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=64)
 def attn_kv4_block_bytes(page_size, d) -> int:
     return int(_load().attn_kv4_block_bytes(int(page_size), int(d)))
 
@@ -871,9 +909,12 @@ def attn_kv4_append(k, v, cu_seqlens, pool, page_table, seq_lens, *, stream=None
     if v.shape[0] != T:
         raise ValueError(f"k and v must have the same rows, got {T} and {v.shape[0]}")
     _check_cu(cu_seqlens, "cu_seqlens", B)
-    with _one_device(k, v, cu_seqlens, pool, page_table, seq_lens):
-        st = _load().attn_kv4_append(_ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(pool), _ptr(page_table), _ptr(seq_lens),
-                                     B, T, H_kv, d, n_pages, page_size, max_pages, ks, vs, _stream(stream))
+    dev = _device_of(k, v, cu_seqlens, pool, page_table, seq_lens)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_append(k, v, cu_seqlens, pool, page_table, seq_lens)
+    st = _load().attn_kv4_append(_p(k), _p(v), _p(cu_seqlens), _p(pool), _p(page_table), _p(seq_lens), B, T, H_kv, d,
+                                 n_pages, page_size, max_pages, ks, vs, _raw_stream(dev, stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_kv4_append")
 
@@ -890,10 +931,12 @@ def attn_kv4_gather(pool, page_table, cu_seqlens, seq_lens, k, v, *, zero_rest=F
         if tuple(t.shape) != (T, H_kv, d):
             raise ValueError(f"{n} must be {(T, H_kv, d)}, got {tuple(t.shape)}")
     _check_cu(cu_seqlens, "cu_seqlens", B)
-    with _one_device(k, v, cu_seqlens, pool, page_table, seq_lens):
-        st = _load().attn_kv4_gather(_ptr(pool), _ptr(page_table), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(k), _ptr(v),
-                                     B, T, H_kv, d, n_pages, page_size, max_pages, int(bool(zero_rest)),
-                                     _stream(stream))
+    dev = _device_of(k, v, cu_seqlens, pool, page_table, seq_lens)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_gather(pool, page_table, cu_seqlens, seq_lens, k, v, zero_rest=zero_rest)
+    st = _load().attn_kv4_gather(_p(pool), _p(page_table), _p(cu_seqlens), _p(seq_lens), _p(k), _p(v), B, T, H_kv, d,
+                                 n_pages, page_size, max_pages, int(bool(zero_rest)), _raw_stream(dev, stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_kv4_gather")
 
@@ -901,13 +944,17 @@ def attn_kv4_gather(pool, page_table, cu_seqlens, seq_lens, k, v, *, zero_rest=F
 def kv4_gather(pool, page_table, cu_seqlens, seq_lens, total, d, *, stream=None):
     """attn_kv4_gather into new tensors of `total` rows: returns (k, v), zeros in the rows of no
     sequence."""
-    with _one_device(pool), _allocating(stream):
-        k = torch.empty((int(total), pool.shape[-2], int(d)), dtype=torch.bfloat16, device=pool.device)
-        v = torch.empty_like(k)
-        attn_kv4_gather(pool, page_table, cu_seqlens, seq_lens, k, v, zero_rest=True, stream=stream)
+    dev = _device_of(pool)
+    if dev >= 0 and _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv4_gather(pool, page_table, cu_seqlens, seq_lens, total, d)
+    k = torch.empty((int(total), pool.shape[-2], int(d)), dtype=torch.bfloat16, device=pool.device)
+    v = torch.empty_like(k)
+    attn_kv4_gather(pool, page_table, cu_seqlens, seq_lens, k, v, zero_rest=True)
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d) -> int:
     return int(_load().attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d))
 
@@ -937,16 +984,17 @@ def attn_kv4_decode(q, pool, page_table, seq_lens, o, lse=None, *, window=-1, so
         _check(softmax_offset, "softmax_offset", torch.float32, 1)
         if softmax_offset.shape[0] != H_q:
             raise ValueError(f"softmax_offset must have one value per query head ({H_q})")
-    with _one_device(q, pool, page_table, seq_lens, o, lse, softmax_offset, workspace), _allocating(stream):
-        if workspace is None:
-            workspace = torch.empty(max(attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d), 256), dtype=torch.uint8,
-                                    device=q.device)
-        else:
-            _check(workspace, "workspace", torch.uint8, 1)
-        st = _load().attn_kv4_decode(_ptr(q), _ptr(pool), _ptr(page_table), _ptr(seq_lens), _ptr(o), _ptr(lse), B, S_q,
-                                     H_q, H_kv, d, n_pages, page_size, max_pages, float(scale or 0.0), int(window),
-                                     _stype(softmax_type), _ptr(softmax_offset), _ptr(workspace), workspace.numel(),
-                                     _stream(stream))
+    dev = _device_of(q, pool, page_table, seq_lens, o, lse, softmax_offset, workspace)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_decode(q, pool, page_table, seq_lens, o, lse, window=window, softmax_type=softmax_type,
+                                   softmax_offset=softmax_offset, scale=scale, workspace=workspace)
+    ws = _workspace(workspace, attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d) if workspace is None else 0,
+                    q.device)
+    st = _load().attn_kv4_decode(_p(q), _p(pool), _p(page_table), _p(seq_lens), _p(o), _p(lse), B, S_q, H_q, H_kv, d,
+                                 n_pages, page_size, max_pages, float(scale or 0.0), int(window),
+                                 _stype(softmax_type), _p(softmax_offset), _p(ws), ws.numel(),
+                                 _raw_stream(dev, stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_kv4_decode")
 
@@ -954,12 +1002,16 @@ def attn_kv4_decode(q, pool, page_table, seq_lens, o, lse=None, *, window=-1, so
 def sdpa_decode_kv4(q, pool, page_table, seq_lens, *, window=-1, softmax_type=VANILLA, softmax_offset=None, scale=0.0,
                     workspace=None, stream=None):
     """Allocate O and LSE, run attn_kv4_decode, return (o, lse)."""
+    dev = _device_of(q)
+    if dev >= 0 and _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return sdpa_decode_kv4(q, pool, page_table, seq_lens, window=window, softmax_type=softmax_type,
+                                   softmax_offset=softmax_offset, scale=scale, workspace=workspace)
     B, S_q, H_q, _ = q.shape
-    with _one_device(q), _allocating(stream):
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
-        lse = torch.empty((B, H_q, S_q), dtype=torch.float32, device=q.device)
-        attn_kv4_decode(q, pool, page_table, seq_lens, o, lse, window=window, softmax_type=softmax_type,
-                        softmax_offset=softmax_offset, scale=scale, workspace=workspace, stream=stream)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H_q, S_q), dtype=torch.float32, device=q.device)
+    attn_kv4_decode(q, pool, page_table, seq_lens, o, lse, window=window, softmax_type=softmax_type,
+                    softmax_offset=softmax_offset, scale=scale, workspace=workspace)
     return o, lse
 
 
@@ -993,9 +1045,12 @@ def attn_kv4_copy_pages(pool, src, dst, *, stream=None):
         raise ValueError(f"src and dst must have the same length, got {src.shape[0]} and {dst.shape[0]}")
     n_layers = pool.shape[0] if pool.dim() == 4 else 1
     n_pages, H_kv, block = pool.shape[-3:]
-    with _one_device(pool):
-        st = _load().attn_kv4_copy_pages(_ptr(pool), n_layers, n_pages, H_kv * block, _ptr(src), _ptr(dst),
-                                         src.shape[0], _stream(stream))
+    dev = _device_of(pool)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_copy_pages(pool, src, dst)
+    st = _load().attn_kv4_copy_pages(_p(pool), n_layers, n_pages, H_kv * block, _p(src), _p(dst), src.shape[0],
+                                     _raw_stream(dev, stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_kv4_copy_pages")
 

@@ -26,6 +26,7 @@
 //   - A fifth warp walks the page table and streams units into a ring by bulk copies, four a
 //     page; each of the other four takes 32 tokens of every unit.
 #include <algorithm>
+#include <atomic>
 
 #include "attn_common.cuh"
 #include "attn_kernels.h"
@@ -686,13 +687,20 @@ template <int D, int NT>
 int launch_t(const Kv4DecodeParams& p, float* partial, cudaStream_t stream) {
   using C = DecCfg<D, NT>;
   auto kern = kv4_decode_kernel<D, NT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
-  int per_sm = 0, sms = 0, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, C::SMEM) != cudaSuccess)
-    return -1;
-  const int grid = std::max(1, std::min(kMaxCtas, per_sm * sms));
+  // the grid that fills the device, found (and the kernel's shared memory allowed) once a device
+  static std::atomic<int> grids[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  int grid = grids[dev].load(std::memory_order_acquire);
+  if (grid == 0) {
+    int per_sm = 0, sms = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, C::SMEM) != cudaSuccess)
+      return -1;
+    grid = std::max(1, std::min(kMaxCtas, per_sm * sms));
+    grids[dev].store(grid, std::memory_order_release);
+  }
   const int rows = p.H_q / p.c.H_kv * p.S_q, blocks = (rows + C::ROWS - 1) / C::ROWS;
   const long long join = (long long)p.B * p.c.H_kv * blocks;
   if (join > 0x7fffffffLL) return -2;
