@@ -142,6 +142,10 @@ __global__ void __launch_bounds__(FUSE_DQ ? 480 : 352, 1)
   // slots and barrier phases.
   const int n_kv = (p.S_kv + C::BN - 1) / C::BN;
   const int n_gr = p.H_kv * p.B * p.ns;  // group = (b, kv head, head split)
+  if constexpr (PK) {
+    grid_wait();  // the plan and the preprocess
+    grid_launch_dependents();  // (only now: the dQ kernel relies on the preprocess without waiting for it)
+  }
   const int n_tiles = PK ? p.counts->kv_tiles * p.H_kv * p.ns : n_kv * n_gr;
   if (PK && (int)blockIdx.x >= n_tiles) return;  // the grid is the host's bound on the tiles
   // packed: a tile that ends past its sequence lands on this barrier first (the ring's place)
@@ -867,7 +871,13 @@ __global__ void __launch_bounds__(352, 1)
   const int n_qt = (p.S_q + C::BM - 1) / C::BM;
   const int n_gr = p.H_q * p.B;
   const int n_tiles = PK ? p.counts->q_tiles * p.H_q : n_qt * n_gr;
-  if (PK && (int)blockIdx.x >= n_tiles) return;  // the grid is the host's bound on the tiles
+  // Packed: this kernel is launched behind the kv kernel and may start in its tail; all it needs was
+  // there before that one's blocks let it start.  Every block waits for the kv kernel at its end,
+  // so that what follows on the stream finds both done.
+  if (PK && (int)blockIdx.x >= n_tiles) {  // the grid is the host's bound on the tiles
+    grid_wait();
+    return;
+  }
   // packed: a kv tile that ends past its sequence lands on this barrier first (the ring's place)
   [[maybe_unused]] uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_TMEM_SLOT + 8);
   const int per_chunk = kKvChunk * n_qt;
@@ -1333,6 +1343,7 @@ __global__ void __launch_bounds__(352, 1)
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
+  if constexpr (PK) grid_wait();
 }
 
 template <int D_QK, int D_V, KernVariant KV = KernVariant::kPlain>

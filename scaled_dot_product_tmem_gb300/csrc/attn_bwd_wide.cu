@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_bwd_kernels.cuh"
+#include "launch.h"
 
 namespace sdpa {
 
@@ -101,6 +102,10 @@ __global__ void __launch_bounds__(352, 1)
   // numbers the steps of all of them in one sequence g (stages, barrier phases).
   const int n_kv = (p.S_kv + C::BN - 1) / C::BN;
   const int n_gr = p.H_kv * p.B * p.ns;
+  if constexpr (PK) {
+    grid_wait();  // the plan and the preprocess
+    grid_launch_dependents();  // (only now: the dQ kernel relies on the preprocess without waiting for it)
+  }
   const int n_tiles = PK ? p.counts->kv_tiles * p.H_kv * p.ns : n_kv * n_gr;
   if (PK && (int)blockIdx.x >= n_tiles) return;  // the grid is the host's bound on the tiles
   // packed: a tile that ends past its sequence lands on this barrier first (the ring's place)
@@ -610,8 +615,7 @@ static int launch_kvw_packed_t(const CUtensorMap& tq, const CUtensorMap& tk, con
   if (grid <= 0 || grid > 0x7fffffffLL) return -2;
   auto kern = attn_bwd_kvw_kernel<D_QK, D_V, true, false, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
-  kern<<<(unsigned)grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tdo, p);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(kern, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, true, tq, tk, tv, tdo, p);
 }
 
 int launch_bwd_kv_wide_packed(int d, const CUtensorMap& tq128, const CUtensorMap& tk, const CUtensorMap& tv,

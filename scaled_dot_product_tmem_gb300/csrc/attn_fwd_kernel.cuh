@@ -50,6 +50,7 @@
 #include "attn_common.cuh"
 #include "attn_kernels.h"
 #include "dropout.cuh"
+#include "launch.h"
 #include "ptx.cuh"
 
 namespace sdpa {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(320, 1)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int nqb = (p.S_q + 2 * C::BM - 1) / (2 * C::BM);
-  const int n_work = PK ? p.counts->fwd_tiles * p.H_q : nqb * p.H_q * p.B;
+  [[maybe_unused]] int n_work = nqb * p.H_q * p.B;
   // packed: a V tile that ends past its sequence lands on this barrier first (beside the TMEM address)
   [[maybe_unused]] uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_TMEM_SLOT + 8);
 
@@ -206,6 +207,10 @@ __global__ void __launch_bounds__(320, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int* err = p.err;
+  if constexpr (PK) {  // set up while the plan was made
+    grid_wait();
+    n_work = p.counts->fwd_tiles * p.H_q;
+  }
 
   // The CTA is persistent: it takes work tiles wi = blockIdx.x, blockIdx.x + gridDim.x,
   // ...; every role walks the same sequence and counts barrier phases across tiles.
@@ -706,6 +711,7 @@ inline int launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   const long long n_work =
       PK ? p.tile_bound * p.H_q : (long long)((p.S_q + 2 * C::BM - 1) / (2 * C::BM)) * p.H_q * p.B;
   const unsigned grid = (unsigned)(n_work < n_sm ? n_work : n_sm);
+  if constexpr (PK) return launch_kernel(kern, dim3(grid), C::THREADS, C::SMEM, stream, true, tq, tk, tv, tq, p);
   kern<<<grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tb ? *tb : tq, p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

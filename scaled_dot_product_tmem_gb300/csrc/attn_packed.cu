@@ -12,6 +12,7 @@
 #include "attn_bwd_kernels.cuh"
 #include "attn_fwd_kernel.cuh"
 #include "attn_packed.h"
+#include "launch.h"
 
 namespace sdpa {
 
@@ -148,6 +149,7 @@ __device__ int list_tiles(const PackedPlanParams& p, const int* cq, const int* c
 
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlanParams p) {
   __shared__ int hist[kPlanThreads], part[32];
+  grid_launch_dependents();
   clean_offsets(p.cu_q, p.B, p.T_q, p.clean_q, part);
   const int* ck = p.clean_q;
   if (p.cu_kv != p.cu_q || p.T_kv != p.T_q) {
@@ -196,6 +198,8 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
   constexpr int TPR = D_V / 8, RPP = 256 / TPR, TILE = 64, NR = TILE / RPP;
   __shared__ float dsum[TILE];
   const int h = blockIdx.y;
+  grid_launch_dependents();
+  grid_wait();  // the plan
   if ((int)(blockIdx.x / 2) < p.counts->q_tiles) {
     const PackedTile e = load_packed_tile(p.tiles_q, blockIdx.x / 2);
     const int i0 = e.m0 + (blockIdx.x % 2) * TILE, sub = threadIdx.x % TPR;
@@ -253,10 +257,9 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
 int launch_packed_preprocess(int d_qk, int d_v, const BwdParams& p, cudaStream_t stream) {
   if (2 * p.tile_bound_q > 0x7fffffffLL) return -2;
   const dim3 grid((unsigned)(2 * p.tile_bound_q), p.H_q);
-  if (d_v == 64) packed_preprocess_kernel<64><<<grid, 256, 0, stream>>>(p, d_qk);
-  else if (d_v == 128) packed_preprocess_kernel<128><<<grid, 256, 0, stream>>>(p, d_qk);
-  else return -2;
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  if (d_v == 64) return launch_kernel(packed_preprocess_kernel<64>, grid, 256, 0, stream, true, p, d_qk);
+  if (d_v == 128) return launch_kernel(packed_preprocess_kernel<128>, grid, 256, 0, stream, true, p, d_qk);
+  return -2;
 }
 
 // d offset_h = -sum_i ps_i D*_i with ps_i = exp(offset_h - LSE_i) and D*_i = dO_i . O_i of the
@@ -339,28 +342,27 @@ int launch_bwd_kv_packed_mla(const CUtensorMap& tq64, const CUtensorMap& tk, con
   if (grid <= 0 || grid > 0x7fffffffLL) return -2;
   auto kern = attn_bwd_kv_kernel<192, 128, false, true, false, false, false, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
-  kern<<<(unsigned)grid, C::THREADS, C::SMEM, stream>>>(tq64, tk, tv, tdo64, tq64, tq64, p);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(kern, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, true, tq64, tk, tv, tdo64, tq64, tq64, p);
 }
 
 template <int D_QK, int D_V>
 static int launch_q_packed_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const CUtensorMap& tdo, const BwdParams& p, cudaStream_t stream) {
+                             const CUtensorMap& tdo, const BwdParams& p, bool early, cudaStream_t stream) {
   using C = QCfg<D_QK, D_V>;
   const long long grid = p.tile_bound_q * p.H_q;
   if (grid <= 0 || grid > 0x7fffffffLL) return -2;
   auto kern = p.ds_rowsum ? attn_bwd_q_kernel<D_QK, D_V, true, false, false, false, true, true>
                           : attn_bwd_q_kernel<D_QK, D_V, true, false, false, false, true, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
-  kern<<<(unsigned)grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tdo, p);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(kern, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, early, tq, tk, tv, tdo, p);
 }
 
+// early: right behind the kv kernel on the stream, whose tail it may overlap (it needs nothing of it).
 int launch_bwd_q_packed(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                        const CUtensorMap& tdo, const BwdParams& p, cudaStream_t stream) {
-  if (d_qk == 128 && d_v == 128) return launch_q_packed_t<128, 128>(tq, tk, tv, tdo, p, stream);
-  if (d_qk == 64 && d_v == 64) return launch_q_packed_t<64, 64>(tq, tk, tv, tdo, p, stream);
-  if (d_qk == 192 && d_v == 128) return launch_q_packed_t<192, 128>(tq, tk, tv, tdo, p, stream);
+                        const CUtensorMap& tdo, const BwdParams& p, bool early, cudaStream_t stream) {
+  if (d_qk == 128 && d_v == 128) return launch_q_packed_t<128, 128>(tq, tk, tv, tdo, p, early, stream);
+  if (d_qk == 64 && d_v == 64) return launch_q_packed_t<64, 64>(tq, tk, tv, tdo, p, early, stream);
+  if (d_qk == 192 && d_v == 128) return launch_q_packed_t<192, 128>(tq, tk, tv, tdo, p, early, stream);
   return -2;
 }
 

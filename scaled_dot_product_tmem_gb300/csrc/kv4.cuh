@@ -24,6 +24,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace sdpa {
 
 struct Kv4Pool {
@@ -64,6 +66,32 @@ __device__ __forceinline__ float kv4_scale_value(int byte) {
   return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
 
+// Paired bf16 arithmetic.
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Codes c in bits 0-3 and 16-19 of w as the bf16 pair (c - 8) s, with s and -136 s paired.
+// The mask and the exponent bits are one three-input operation, (w & mask) | bits.
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t s, uint32_t m136s) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(0x000F000Fu), "r"(0x43004300u));
+  return bf2_fma(x, s, m136s);
+}
+// Two scale bytes (low, next) as a bf16 pair: bits 14..7 of two half-precision numbers.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t two) {
+  const uint32_t h = __byte_perm(two, 0u, 0x4140) << 7;
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16x2(f.x, f.y);
+}
+constexpr uint32_t kM136 = 0xC308C308u;  // -136 as a bf16 pair
+
 constexpr int kKv4BadScale = 0xFF;  // 16 values with an infinity or NaN among them: a NaN scale
 
 // The page that holds token `pos` of sequence b, or -1 (outside the table or the pool).
@@ -71,20 +99,6 @@ __device__ __forceinline__ int kv4_page(const Kv4Pool& c, int b, int pos) {
   if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) return -1;
   const int pg = __ldg(c.page_table + (size_t)b * c.max_pages + (pos >> c.page_shift));
   return (pg < 0 || pg >= c.n_pages) ? -1 : pg;
-}
-
-// Which sequence holds row t of a packed tensor: the last b with cu[b] <= t, checked
-// against its end; -1 when no sequence does.  Offsets that are not ascending may give any
-// sequence, never a row outside the one returned.
-__device__ __forceinline__ int packed_row_entry(const int* cu, int B, int t) {
-  int lo = 0, hi = B;  // cu[lo] <= t is looked for in [0, B)
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid + 1;
-    else hi = mid;
-  }
-  const int b = lo - 1;
-  return (b >= 0 && __ldg(cu + b) <= t && t < __ldg(cu + b + 1)) ? b : -1;
 }
 
 }  // namespace sdpa

@@ -31,6 +31,7 @@
 #include "attn_common.cuh"
 #include "attn_kernels.h"
 #include "kv4.cuh"
+#include "launch.h"
 #include "ptx.cuh"
 
 namespace sdpa {
@@ -46,16 +47,6 @@ constexpr int kMaxCtas = 152 * 4;  // partial-sum slots in the workspace
 
 enum Kv4Site { kKv4Full = 0xA0, kKv4Empty };
 
-__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 // d (16 x 8 fp32) += a (16 x 16 bf16, rows) b (16 x 8 bf16, columns)
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -77,21 +68,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-
-// Codes c in bits 0-3 and 16-19 of w as the bf16 pair (c - 8) s, with s and -136 s paired.
-// The mask and the exponent bits are one three-input operation, (w & mask) | bits.
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t s, uint32_t m136s) {
-  uint32_t x;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(0x000F000Fu), "r"(0x43004300u));
-  return bf2_fma(x, s, m136s);
-}
-// Two scale bytes (low, next) as a bf16 pair: bits 14..7 of two half-precision numbers.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t two) {
-  const uint32_t h = __byte_perm(two, 0u, 0x4140) << 7;
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_bf16x2(f.x, f.y);
-}
-constexpr uint32_t kM136 = 0xC308C308u;  // -136 as a bf16 pair
 
 // A row's end: sums relative to maximum m (log2 units), the sink joins the denominator.
 struct Kv4Sums {
@@ -705,18 +681,8 @@ int launch_t(const Kv4DecodeParams& p, float* partial, cudaStream_t stream) {
   const long long join = (long long)p.B * p.c.H_kv * blocks;
   if (join > 0x7fffffffLL) return -2;
   kern<<<grid, kThreads, C::SMEM, stream>>>(p, blocks, partial);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)join, std::min(rows, C::ROWS));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv4_join_kernel<D>, p, blocks, (int)C::ROWS, grid, (const float*)partial) != cudaSuccess)
-    return -1;
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(kv4_join_kernel<D>, dim3((unsigned)join, std::min(rows, C::ROWS)), 256, 0, stream, true, p, blocks,
+                       (int)C::ROWS, grid, (const float*)partial);
 }
 
 }  // namespace

@@ -9,22 +9,40 @@ namespace sdpa {
 
 namespace {
 
-constexpr int kTok = 16;  // tokens of one block of threads
+constexpr int kTok = 16;  // tokens of one block of 256 threads: 16 threads look each one up
 
 struct TokenAt {
   long long block;  // byte offset of the token's page in the pool (head 0), -1: nowhere, -2: no sequence
   int w;            // the token's place in its page
 };
 
-// Where rows t0 .. t0 + kTok - 1 of the packed tensors live in the pool.
+// Where rows t0 .. t0 + kTok - 1 of the packed tensors live in the pool.  A row's sequence is the
+// last b with cu[b] <= t (checked against its end): 16 lanes search the offsets 16 ways at a
+// time, so that a few dependent loads find it.  Offsets that are not ascending may give any
+// sequence, never a row outside the one returned.
 __device__ __forceinline__ void find_tokens(const Kv4StoreParams& p, int t0, TokenAt* at) {
-  if (threadIdx.x < kTok) {
-    const int t = t0 + threadIdx.x;
+  const int lane16 = threadIdx.x % 16, half = threadIdx.x & 16, i = threadIdx.x / 16;
+  const int t = t0 + i;
+  int lo = 0, n = p.B;  // the count of cu[0 .. B) that are <= t lies in [lo, lo + n]
+  while (__any_sync(0xffffffffu, n > 0)) {
+    const int step = (n + 15) / 16, at_ = lo + lane16 * step;
+    const bool le = lane16 * step < n && __ldg(p.cu + at_) <= t;
+    const int c = __popc((__ballot_sync(0xffffffffu, le) >> half) & 0xFFFFu);
+    if (c == 0) {
+      n = 0;
+    } else {
+      const int rest = n - ((c - 1) * step + 1);
+      lo += (c - 1) * step + 1;
+      n = min(step - 1, rest);
+    }
+  }
+  if (lane16 == 0) {
     TokenAt a{-2, 0};
-    if (t < p.T) {
-      const int b = packed_row_entry(p.cu, p.B, t);
-      if (b >= 0) {
-        const long long pos = (long long)__ldg(p.start + b) + (t - __ldg(p.cu + b));
+    const int b = lo - 1;
+    if (t < p.T && b >= 0) {
+      const int first = __ldg(p.cu + b), end = __ldg(p.cu + b + 1), start = __ldg(p.start + b);
+      if (first <= t && t < end) {
+        const long long pos = (long long)start + (t - first);
         const int pg = pos > 0x7fffffffLL ? -1 : kv4_page(p.c, b, (int)pos);  // (pos may be negative)
         a.block = -1;
         if (pg >= 0) {
@@ -35,130 +53,169 @@ __device__ __forceinline__ void find_tokens(const Kv4StoreParams& p, int t0, Tok
         }
       }
     }
-    at[threadIdx.x] = a;
+    at[i] = a;
   }
   __syncthreads();
 }
 
+// 16 values to codes and a scale byte.  c = round(x / s) without a division: y = x (1/s) is off
+// by 2^-22 or so, ties x / s = k + 1/2 are exact numbers, and any other x / s is at least 2^-9
+// away from a tie (x has 8 significant bits, s has 4), so y rounded to multiples of 2^-12
+// falls on the same side as x / s, and ties on themselves; the second rounding is then the
+// definition's.
+__device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint32_t (&c)[2]) {
+  const uint32_t ws[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  uint32_t mx = 0u;  // largest magnitudes of both halves: bf16 bits order as the numbers do
+#pragma unroll
+  for (int q = 0; q < 8; ++q) mx = __vmaxu2(mx, ws[q] & 0x7FFF7FFFu);
+  const uint32_t top = max(mx >> 16, mx & 0xFFFFu);
+  c[0] = c[1] = 0x88888888u;  // zeros
+  if (top >= 0x7F80u) return kKv4BadScale;
+  const int sb = kv4_scale_byte(__uint_as_float(top << 16));
+  if (sb == 0) return 0;
+  const float inv = __frcp_rn(kv4_scale_value(sb));
+  const uint64_t inv2 = f2_pack(inv, inv);
+  constexpr float kGrid = 1.5f * 2048.f, kInt = 1.5f * 8388608.f;  // adding it rounds to 2^-12, to whole numbers
+  const uint64_t up = f2_pack(kGrid, kGrid), down = f2_pack(-kGrid, -kGrid), whole = f2_pack(kInt, kInt);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint64_t y = f2_mul(f2_pack(__uint_as_float(ws[q] << 16), __uint_as_float(ws[q] & 0xFFFF0000u)), inv2);
+    y = f2_add(f2_add(y, up), down);
+    float a, b;
+    f2_unpack(y, a, b);
+    a = fminf(fmaxf(a, -8.f), 7.f);
+    b = fminf(fmaxf(b, -8.f), 7.f);
+    f2_unpack(f2_add(f2_pack(a, b), whole), a, b);  // the low bits are the whole number
+    const uint32_t two = (__float_as_uint(a) & 15u) | ((__float_as_uint(b) & 15u) << 4);
+    if (q % 4 == 0) c[q / 4] = two;
+    else c[q / 4] |= two << (8 * (q % 4));
+  }
+  c[0] ^= 0x88888888u;  // c = 8 + whole number
+  c[1] ^= 0x88888888u;
+  return sb;
+}
+
 }  // namespace
 
-// One thread quantises 16 values.  Consecutive threads take the groups of one token and
-// head, then the block's tokens, then heads: a warp reads whole rows of K or V and writes
-// one contiguous run of codes (K) or whole token pairs (V).
+// One thread quantises 16 dims of a token's K and of its V for one head after another.
+// Consecutive threads take the groups of one token and head, then the block's tokens, then
+// heads: a warp reads whole rows of K or V and writes one contiguous run of codes (K) or
+// whole token pairs (V).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4StoreParams p) {
-  constexpr int NG = D / 16;
+  constexpr int NG = D / 16, HS = 256 / (NG * kTok);  // heads a block takes at a time
   __shared__ TokenAt at[kTok];
   const int t0 = blockIdx.x * kTok;
   find_tokens(p, t0, at);
   const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
-  const int n = kTok * NG * p.c.H_kv;
-  for (int it = threadIdx.x; it < 2 * n; it += 256) {
-    const int is_v = it >= n;
-    const int e = is_v ? it - n : it;
-    const int g = e % NG, tk = (e / NG) % kTok, h = e / (NG * kTok);
-    const TokenAt a = at[tk];
-    if (a.block < 0) continue;
-    const __nv_bfloat16* src =
-        (is_v ? p.v + (t0 + tk) * p.v_stride : p.k + (t0 + tk) * p.k_stride) + (size_t)h * D + g * 16;
-    const uint4 x0 = __ldg(reinterpret_cast<const uint4*>(src)), x1 = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    const uint32_t ws[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-    float f[16], amax = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      f[2 * q] = __uint_as_float(ws[q] << 16);
-      f[2 * q + 1] = __uint_as_float(ws[q] & 0xFFFF0000u);
-    }
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      bad |= !(fabsf(f[q]) <= 3.4028234e38f);
-      amax = fmaxf(amax, fabsf(f[q]));
-    }
-    const int sb = bad ? kKv4BadScale : kv4_scale_byte(amax);
-    const float s = kv4_scale_value(sb);
-    uint32_t c[2] = {0x88888888u, 0x88888888u};  // all zeros
-    if (!bad && sb > 0) {
-      c[0] = c[1] = 0u;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int v = max(-8, min(7, __float2int_rn(__fdiv_rn(f[q], s)))) + 8;
-        c[q / 8] |= (uint32_t)v << (4 * (q % 8));
-      }
-    }
-    uint8_t* base = p.pool + a.block + (size_t)h * blk;
-    if (!is_v) {
-      *reinterpret_cast<uint2*>(base + a.w * (D / 2) + g * 8) = make_uint2(c[0], c[1]);
-      base[kv4_off_sk(P, D) + a.w * NG + g] = (uint8_t)sb;
+  const int g = threadIdx.x % NG, tk = threadIdx.x / NG % kTok;
+  const TokenAt a = at[tk];
+  if (a.block < 0) return;
+  const __nv_bfloat16* kr = p.k + (size_t)(t0 + tk) * p.k_stride + g * 16;
+  const __nv_bfloat16* vr = p.v + (size_t)(t0 + tk) * p.v_stride + g * 16;
+  uint8_t* page = p.pool + a.block;
+  const int at_k = a.w * (D / 2) + g * 8, at_sk = kv4_off_sk(P, D) + a.w * NG + g;
+  const int at_sv = kv4_off_sv(P, D) + (a.w >> 1) * 2 * NG + 2 * g + (a.w & 1);
+  const int at_v0 = kv4_off_v(P, D) + kv4_v_at(a.w, D == 128 ? g : 2 * g, D);
+  const int at_v1 = kv4_off_v(P, D) + kv4_v_at(a.w, 2 * g + 1, D);  // D = 64: 16 dims are two eighths
+#pragma unroll 2
+  for (int h = threadIdx.x / (NG * kTok) + HS * blockIdx.y; h < p.c.H_kv; h += HS * gridDim.y) {
+    const uint4* ks = reinterpret_cast<const uint4*>(kr + (size_t)h * D);
+    const uint4* vs = reinterpret_cast<const uint4*>(vr + (size_t)h * D);
+    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+    uint8_t* base = page + (size_t)h * blk;
+    uint32_t c[2];
+    int sb = quantise16(k0, k1, c);
+    *reinterpret_cast<uint2*>(base + at_k) = make_uint2(c[0], c[1]);
+    base[at_sk] = (uint8_t)sb;
+    sb = quantise16(v0, v1, c);
+    if constexpr (D == 128) {
+      *reinterpret_cast<uint2*>(base + at_v0) = make_uint2(c[0], c[1]);
     } else {
-      uint8_t* vb = base + kv4_off_v(P, D);
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint2*>(vb + kv4_v_at(a.w, g, D)) = make_uint2(c[0], c[1]);
-      } else {  // 16 values are two eighths of the head dim
-        *reinterpret_cast<uint32_t*>(vb + kv4_v_at(a.w, 2 * g, D)) = c[0];
-        *reinterpret_cast<uint32_t*>(vb + kv4_v_at(a.w, 2 * g + 1, D)) = c[1];
-      }
-      base[kv4_off_sv(P, D) + (a.w >> 1) * 2 * NG + 2 * g + (a.w & 1)] = (uint8_t)sb;
+      *reinterpret_cast<uint32_t*>(base + at_v0) = c[0];
+      *reinterpret_cast<uint32_t*>(base + at_v1) = c[1];
     }
+    base[at_sv] = (uint8_t)sb;
   }
 }
 
-// The reverse: one thread turns 16 codes into 16 bf16 values (exact).  Tokens whose page is
-// not in the pool read as zeros; rows of no sequence are left alone, or zeroed on request.
+// 16 codes as 16 bf16 values (exact).
+__device__ __forceinline__ void held16(uint2 c, int sb, uint4 (&o)[2]) {
+  const uint32_t s = scale_pair((uint32_t)sb * 0x0101u), m = bf2_mul(s, kM136);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t w = q ? c.y : c.x;
+    // pairs (0, 4), (1, 5), (2, 6), (3, 7), then neighbours
+    const uint32_t a = decode_pair(w, s, m), b = decode_pair(w >> 4, s, m), d = decode_pair(w >> 8, s, m),
+                   e = decode_pair(w >> 12, s, m);
+    o[q] = make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(d, e, 0x5410), __byte_perm(a, b, 0x7632),
+                      __byte_perm(d, e, 0x7632));
+  }
+}
+
+// The reverse.  Tokens whose page is not in the pool read as zeros; rows of no sequence are left
+// alone, or zeroed on request.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4StoreParams p) {
-  constexpr int NG = D / 16;
+  constexpr int NG = D / 16, HS = 256 / (NG * kTok);
   __shared__ TokenAt at[kTok];
   const int t0 = blockIdx.x * kTok;
   find_tokens(p, t0, at);
   const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
-  const int n = kTok * NG * p.c.H_kv;
-  for (int it = threadIdx.x; it < 2 * n; it += 256) {
-    const int is_v = it >= n;
-    const int e = is_v ? it - n : it;
-    const int g = e % NG, tk = (e / NG) % kTok, h = e / (NG * kTok);
-    const TokenAt a = at[tk];
-    if (t0 + tk >= p.T || (a.block == -2 && !p.zero_rest)) continue;
-    uint2 c = make_uint2(0u, 0u);
-    float s = 0.f;
-    if (a.block >= 0) {
-      const uint8_t* base = p.pool + a.block + (size_t)h * blk;
-      if (!is_v) {
-        c = __ldg(reinterpret_cast<const uint2*>(base + a.w * (D / 2) + g * 8));
-        s = kv4_scale_value(__ldg(base + kv4_off_sk(P, D) + a.w * NG + g));
+  const int g = threadIdx.x % NG, tk = threadIdx.x / NG % kTok;
+  const TokenAt a = at[tk];
+  if (t0 + tk >= p.T || (a.block == -2 && !p.zero_rest)) return;
+  const bool have = a.block >= 0;
+  const uint8_t* page = p.pool + (have ? a.block : 0);
+  const int at_k = a.w * (D / 2) + g * 8, at_sk = kv4_off_sk(P, D) + a.w * NG + g;
+  const int at_sv = kv4_off_sv(P, D) + (a.w >> 1) * 2 * NG + 2 * g + (a.w & 1);
+  const int at_v0 = kv4_off_v(P, D) + kv4_v_at(a.w, D == 128 ? g : 2 * g, D);
+  const int at_v1 = kv4_off_v(P, D) + kv4_v_at(a.w, 2 * g + 1, D);
+  const size_t row = (size_t)(t0 + tk) * p.c.H_kv;
+#pragma unroll 4
+  for (int h = threadIdx.x / (NG * kTok) + HS * blockIdx.y; h < p.c.H_kv; h += HS * gridDim.y) {
+    const uint8_t* base = page + (size_t)h * blk;
+    uint2 ck = make_uint2(0u, 0u), cv = ck;
+    int sk = 0, sv = 0;
+    if (have) {
+      ck = __ldg(reinterpret_cast<const uint2*>(base + at_k));
+      sk = __ldg(base + at_sk);
+      if constexpr (D == 128) {
+        cv = __ldg(reinterpret_cast<const uint2*>(base + at_v0));
       } else {
-        const uint8_t* vb = base + kv4_off_v(P, D);
-        if constexpr (D == 128) {
-          c = __ldg(reinterpret_cast<const uint2*>(vb + kv4_v_at(a.w, g, D)));
-        } else {
-          c.x = __ldg(reinterpret_cast<const uint32_t*>(vb + kv4_v_at(a.w, 2 * g, D)));
-          c.y = __ldg(reinterpret_cast<const uint32_t*>(vb + kv4_v_at(a.w, 2 * g + 1, D)));
-        }
-        s = kv4_scale_value(__ldg(base + kv4_off_sv(P, D) + (a.w >> 1) * 2 * NG + 2 * g + (a.w & 1)));
+        cv.x = __ldg(reinterpret_cast<const uint32_t*>(base + at_v0));
+        cv.y = __ldg(reinterpret_cast<const uint32_t*>(base + at_v1));
       }
+      sv = __ldg(base + at_sv);
     }
-    uint32_t o[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t w = q < 4 ? c.x : c.y;
-      const int lo = (int)((w >> (8 * (q % 4))) & 15u) - 8, hi = (int)((w >> (8 * (q % 4) + 4)) & 15u) - 8;
-      o[q] = pack_bf16x2((float)lo * s, (float)hi * s);
-    }
-    __nv_bfloat16* dst = (is_v ? p.v_out : p.k_out) + ((size_t)(t0 + tk) * p.c.H_kv + h) * D + g * 16;
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    uint4 o[2];
+    held16(ck, sk, o);
+    uint4* kd = reinterpret_cast<uint4*>(p.k_out + (row + h) * D + g * 16);
+    kd[0] = o[0];
+    kd[1] = o[1];
+    held16(cv, sv, o);
+    uint4* vd = reinterpret_cast<uint4*>(p.v_out + (row + h) * D + g * 16);
+    vd[0] = o[0];
+    vd[1] = o[1];
   }
+}
+
+// Blocks: kTok tokens each; with few tokens the heads are spread over more of them.
+static dim3 store_grid(const Kv4StoreParams& p) {
+  const int x = (p.T + kTok - 1) / kTok, hs = 256 / (p.c.d / 16 * kTok), y_max = (p.c.H_kv + hs - 1) / hs;
+  const int y = x >= 152 * 4 ? 1 : (152 * 4 + x - 1) / x;
+  return dim3((unsigned)x, (unsigned)(y < y_max ? y : y_max));
 }
 
 int launch_kv4_append(const Kv4StoreParams& p, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)((p.T + kTok - 1) / kTok);
+  const dim3 blocks = store_grid(p);
   if (p.c.d == 128) kv4_append_kernel<128><<<blocks, 256, 0, stream>>>(p);
   else kv4_append_kernel<64><<<blocks, 256, 0, stream>>>(p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_kv4_gather(const Kv4StoreParams& p, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)((p.T + kTok - 1) / kTok);
+  const dim3 blocks = store_grid(p);
   if (p.c.d == 128) kv4_gather_kernel<128><<<blocks, 256, 0, stream>>>(p);
   else kv4_gather_kernel<64><<<blocks, 256, 0, stream>>>(p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
