@@ -20,9 +20,10 @@
 //     both operands of a product agree, so a lane's 16-byte load feeds its own fragments.
 //   - The probabilities are rounded to bf16 (2^-8 relative) for P V; their sum is fp32.
 //   - Work is cut evenly over the CTAs of a persistent grid (units of 128 tokens of one
-//     sequence and kv head, in order), whatever the lengths; a (sequence, head) that spans
-//     several CTAs leaves fp32 partial sums in the workspace, which a second kernel joins in
-//     CTA order: bitwise reproducible.
+//     sequence and kv head, in order, and one unit more for each such segment: its queries,
+//     the sum over its warps and its output cost about as much), whatever the lengths; a
+//     (sequence, head) that spans several CTAs leaves fp32 partial sums in the workspace, which a
+//     second kernel joins in CTA order: bitwise reproducible.
 //   - A fifth warp walks the page table and streams units into a ring by bulk copies, four a
 //     page; each of the other four takes 32 tokens of every unit.
 #include <algorithm>
@@ -44,6 +45,7 @@ constexpr int kUnit = kWarps * kSub;       // tokens of one unit (one ring stage
 constexpr int kStages = 3;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxCtas = 152 * 4;  // partial-sum slots in the workspace
+constexpr int kSegCost = 1;        // a segment's fixed costs, in units
 
 enum Kv4Site { kKv4Full = 0xA0, kKv4Empty };
 
@@ -87,6 +89,7 @@ struct Seq {
   int len;    // tokens in the cache
   int first;  // first unit any query sees
   int n;      // units
+  __device__ __forceinline__ int numbers() const { return n > 0 ? n + kSegCost : 0; }
 };
 __device__ __forceinline__ Seq seq_of(const Kv4DecodeParams& p, int b) {
   Seq s;
@@ -98,13 +101,14 @@ __device__ __forceinline__ Seq seq_of(const Kv4DecodeParams& p, int b) {
 }
 
 // How the units of a call are numbered: sequence by sequence, each sequence's H_eff heads (kv
-// head and row block) one after another.  Every warp works this out for itself: a few loads
+// head and row block) one after another; a segment (sequence, head) of n units has n + kSegCost
+// numbers, the first of them for its fixed costs.  Every warp works this out for itself: a few loads
 // and shuffles, and no barrier.
 struct UnitScan {
-  long long total;  // units of all sequences and heads
+  long long total;  // numbers of all sequences and heads
   __device__ void run(const Kv4DecodeParams& p, int H_eff) {
     long long t = 0;
-    for (int b = threadIdx.x % 32; b < p.B; b += 32) t += seq_of(p, b).n;
+    for (int b = threadIdx.x % 32; b < p.B; b += 32) t += seq_of(p, b).numbers();
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
     total = t * H_eff;
@@ -116,7 +120,7 @@ struct UnitScan {
     long long carry = 0;
     for (int base = 0; base < b_end; base += 32) {
       const int i = base + lane;
-      const long long n = i < b_end ? (long long)seq_of(p, i).n * H_eff : 0;
+      const long long n = i < b_end ? (long long)seq_of(p, i).numbers() * H_eff : 0;
       long long s = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -150,7 +154,8 @@ __device__ __forceinline__ int cta_of(long long total, int n, long long u) {
   return c;
 }
 __device__ __forceinline__ int ctas_used(long long total, int grid) {
-  return total < grid ? (int)total : grid;
+  const long long want = (total + kSegCost) / (kSegCost + 1);
+  return want < grid ? (int)want : grid;
 }
 
 template <int D, int NT>
@@ -162,8 +167,8 @@ struct DecCfg {
   static constexpr bool Q_SMEM = NT > 2;
   static constexpr int Q_BYTES = Q_SMEM ? (D / 16) * NT * 32 * 8 : 0;
   static constexpr int XS = D + 4;  // row stride of the exchange (bank spread)
-  static constexpr int OFF_X = OFF_Q + Q_BYTES;
-  static constexpr int OFF_ML = OFF_X + ROWS * XS * 4;           // [kWarps][ROWS] maxima, then sums
+  static constexpr int OFF_X = OFF_Q + Q_BYTES;                  // [kWarps][ROWS][XS] sums of the four warps
+  static constexpr int OFF_ML = OFF_X + kWarps * ROWS * XS * 4;  // [kWarps][ROWS] maxima, then denominators
   static constexpr int OFF_BAR = OFF_ML + 2 * kWarps * ROWS * 4;  // full[kStages], empty[kStages]
   static constexpr int SMEM = OFF_BAR + 2 * kStages * 8;
   static constexpr int SLOT = ROWS * (D + 2);  // floats of one partial: rows of sums, maxima, denominators
@@ -200,25 +205,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
   const long long u_end = cta_first(scan.total, n_cta, blockIdx.x + 1);
   // The CTA's units are a run of segments: units of one (sequence, kv head, row block) in order.
   struct Cursor {
-    int b, vh, unit;  // sequence, kv head and row block, unit within the sequence's
+    int b, vh;      // sequence, kv head and row block
+    int from, to;   // this CTA's units of it (from == to: only its fixed costs)
+    int left;       // numbers of this CTA after this segment
     Seq s;
   } at;
-  {
-    const long long r = u_begin - scan.before(p, H_eff, p.B, u_begin, &at.b);  // < 2^31: one sequence's
-    at.s = seq_of(p, at.b);
-    at.vh = (int)(r / at.s.n);
-    at.unit = (int)(r % at.s.n);
-  }
-  auto next_segment = [&](Cursor& c) {
-    c.unit = 0;
-    if (++c.vh < H_eff) return;
-    c.vh = 0;
-    do {
-      ++c.b;
-      c.s = seq_of(p, c.b);
-    } while (c.s.n == 0);
+  auto enter = [&](Cursor& c, int number) {  // the segment from its `number` on
+    const int take = min(c.s.numbers() - number, c.left);
+    c.from = max(number - kSegCost, 0);
+    c.to = max(number + take - kSegCost, 0);
+    c.left -= take;
   };
-  int left = (int)(u_end - u_begin);
+  auto next_segment = [&](Cursor& c) {
+    if (++c.vh == H_eff) {
+      c.vh = 0;
+      do {
+        ++c.b;
+        c.s = seq_of(p, c.b);
+      } while (c.s.n == 0);
+    }
+    enter(c, 0);
+  };
+  {
+    const long long r = u_begin - scan.before(p, H_eff, p.B, u_begin, &at.b);
+    at.s = seq_of(p, at.b);
+    at.vh = (int)(r / at.s.numbers());
+    at.left = (int)(u_end - u_begin);
+    enter(at, (int)(r % at.s.numbers()));
+  }
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
@@ -230,25 +244,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     const int src_off = part_ == 0 ? 0 : part_ == 1 ? kv4_off_v(P, D) : part_ == 2 ? kv4_off_sk(P, D) : kv4_off_sv(P, D);
     const int dst_off = (part_ == 0 ? 0 : part_ == 1 ? C::S_V : part_ == 2 ? C::S_SK : C::S_SV) + t0 * per;
     const size_t block = kv4_block_bytes(P, D), page_bytes = block * p.c.H_kv;
+    int unit = at.from;
+    auto settle = [&]() {  // to the next unit there is; false: none
+      while (unit >= at.to) {
+        if (at.left == 0) return false;
+        next_segment(at);
+        unit = at.from;
+      }
+      return true;
+    };
     auto page_of = [&]() {
-      const int tok = (at.s.first + at.unit) * kUnit + t0;
+      const int tok = (at.s.first + unit) * kUnit + t0;
       return lane < 4 * pieces && tok < at.s.len ? kv4_page(p.c, at.b, tok) : -2;
     };
-    int page = page_of();
-    for (int i = 0; i < left; ++i) {
-      const int stage = i % kStages;
+    bool more = settle();
+    int page = more ? page_of() : -2, n = 0;
+    bool ok = true;
+    for (; more && ok; ++n) {
+      const int stage = n % kStages;
       uint8_t* st = smem + stage * C::STAGE;
-      const int tok = (at.s.first + at.unit) * kUnit + t0;
+      const int tok = (at.s.first + unit) * kUnit + t0;
       // whole 16-token groups up to the sequence's end
       const int bytes = page == -2 ? 0 : min(piece, (at.s.len - tok + 15) / 16 * 16) * per;
       const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (at.vh / row_blocks) * block + src_off +
                            (size_t)(tok & (P - 1)) * per;
       const int have = page;
-      if (i + 1 < left) {
-        if (++at.unit == at.s.n) next_segment(at);
-        page = page_of();
-      }
-      if (i >= kStages && !mbar_wait_warp(&empty[stage], (i / kStages - 1) & 1, p.err, kKv4Empty)) break;
+      ++unit;
+      more = settle();
+      if (more) page = page_of();
+      if (n >= kStages) ok = mbar_wait_warp(&empty[stage], (n / kStages - 1) & 1, p.err, kKv4Empty);
+      if (!ok) break;
       if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
         if (have == -1) {
           if (part_ >= 2)
@@ -264,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
       if (have >= 0) bulk_load(st + dst_off, src, bytes, &full[stage]);
     }
     // every copy this warp started must land before the CTA may exit: wait for the last ones
-    for (int s = 0; s < kStages && s < left; ++s) {
-      const int last = s + (left - 1 - s) / kStages * kStages;
+    for (int s = 0; s < kStages && s < n; ++s) {
+      const int last = s + (n - 1 - s) / kStages * kStages;
       mbar_wait_warp(&full[s], (last / kStages) & 1, p.err, kKv4Full);
     }
     return;
@@ -283,9 +308,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
   const int off_sv = C::S_SV + (warp * (kSub / 2) + t) * (D / 8) + 2 * (D == 128 ? g : g / 2);
   int i = 0;  // units consumed
   bool ok = true;
-  while (left > 0) {
-    const int seg_n = min(at.s.n - at.unit, left);
-    const bool whole = at.unit == 0 && seg_n == at.s.n, at_begin = i == 0;
+  for (bool at_begin = true;; at_begin = false) {
+    if (at.from == at.to) {
+      if (at.left == 0) break;
+      next_segment(at);
+      continue;
+    }
+    const int seg_n = at.to - at.from;
+    const bool whole = seg_n == at.s.n;
     const int hk = at.vh / row_blocks, r0 = (at.vh % row_blocks) * C::ROWS;
     const int len = at.s.len;
     // query fragments: lane (g, t) holds row r0 + 8 nt + g; dims [t D/4, (t + 1) D/4), in pairs
@@ -332,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    int k0 = (at.s.first + at.unit) * kUnit + warp * kSub;  // this warp's first token of the unit
+    int k0 = (at.s.first + at.from) * kUnit + warp * kSub;  // this warp's first token of the unit
     for (int k = 0; k < seg_n; ++k, ++i, k0 += kUnit) {
       const int stage = i % kStages;
       ok = ok && mbar_wait_warp(&full[stage], (i / kStages) & 1, p.err, kKv4Full);
@@ -495,79 +525,77 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
 
-    // ---- the warps' sums become one: maxima and denominators, then the rows, warp by warp
+    // ---- the warps' sums become one: each leaves its own, with its maxima and denominators
+    {
+      float* mine = xch + warp * C::ROWS * C::XS;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * nt + 2 * t + e;
+          float ll = l[nt][e];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
-        if (g == 0) {
-          xm[warp * C::ROWS + 8 * nt + 2 * t + e] = m[nt][e];
-          xl[warp * C::ROWS + 8 * nt + 2 * t + e] = l[nt][e];
+          for (int off = 4; off < 32; off <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
+          if (g == 0) {
+            xm[warp * C::ROWS + r] = m[nt][e];
+            xl[warp * C::ROWS + r] = ll;
+          }
+#pragma unroll
+          for (int q = 0; q < MT / 2; ++q) {
+            // D/8 consecutive dims of row r: tiles 0.. give the first half, their + 8 rows the second
+            constexpr int QH = MT / 4;
+            const int mt = 4 * (q % QH), hf = q / QH;
+            *reinterpret_cast<float4*>(mine + r * C::XS + g * (D / 8) + 4 * q) =
+                make_float4(acc[mt][nt][e + 2 * hf], acc[mt + 1][nt][e + 2 * hf], acc[mt + 2][nt][e + 2 * hf],
+                            acc[mt + 3][nt][e + 2 * hf]);
+          }
         }
-      }
-    named_bar_sync(1, 32 * kWarps);
-    float f[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * nt + 2 * t + e;
-        float mm = xm[r];
-        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, xm[w * C::ROWS + r]);
-        f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mm);
-      }
-    for (int w = 0; w < kWarps; ++w) {
-      if (warp == w) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int q = 0; q < MT / 2; ++q) {
-              // D/8 consecutive dims of row 2 t + e: tiles 0.. give the first half, their + 8 rows the second
-              constexpr int QH = MT / 4;
-              float4* x = reinterpret_cast<float4*>(xch + (8 * nt + 2 * t + e) * C::XS + g * (D / 8) + 4 * q);
-              const int mt = 4 * (q % QH), hf = q / QH;
-              float4 v = make_float4(acc[mt][nt][e + 2 * hf] * f[nt][e], acc[mt + 1][nt][e + 2 * hf] * f[nt][e],
-                                     acc[mt + 2][nt][e + 2 * hf] * f[nt][e], acc[mt + 3][nt][e + 2 * hf] * f[nt][e]);
-              if (w > 0) {
-                const float4 o = *x;
-                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-              }
-              *x = v;
-            }
-      }
-      named_bar_sync(1, 32 * kWarps);
     }
+    named_bar_sync(1, 32 * kWarps);
     // ---- the whole of a (sequence, head): outputs; a piece of it: partial sums
     float* slot = partial + ((size_t)2 * blockIdx.x + (at_begin ? 0 : 1)) * C::SLOT;
     for (int r = warp; r < C::ROWS && r0 + r < R; r += kWarps) {
-      float mm = xm[r], ll = 0.f;
+      float mm = xm[r], ll = 0.f, f[kWarps];
+#pragma unroll
       for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, xm[w * C::ROWS + r]);
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = xm[w * C::ROWS + r], lw = xl[w * C::ROWS + r];
-        ll += mw == -INFINITY ? lw : lw * ex2(mw - mm);  // (no key: lw is 0, or a NaN that has to stay)
+        f[w] = mw == -INFINITY ? 0.f : ex2(mw - mm);
+        ll += mw == -INFINITY ? lw : lw * f[w];  // (no key: lw is 0, or a NaN that has to stay)
       }
+      auto sum2 = [&](int x) {  // dims x, x + 1
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 o = *reinterpret_cast<const float2*>(xch + (w * C::ROWS + r) * C::XS + x);
+          v.x = fmaf(o.x, f[w], v.x);
+          v.y = fmaf(o.y, f[w], v.y);
+        }
+        return v;
+      };
       if (whole) {
         const int qs_ = (r0 + r) / G, h = hk * G + (r0 + r) % G;
         const Kv4Sums z = kv4_finish(p, h, mm, ll);
         __nv_bfloat16* o = p.o + (((size_t)at.b * p.S_q + qs_) * p.H_q + h) * D;
-        for (int x = 2 * lane; x < D; x += 64)
-          *reinterpret_cast<uint32_t*>(o + x) = pack_bf16x2(xch[r * C::XS + x] * z.mul, xch[r * C::XS + x + 1] * z.mul);
+#pragma unroll
+        for (int x = 2 * lane; x < D; x += 64) {
+          const float2 v = sum2(x);
+          *reinterpret_cast<uint32_t*>(o + x) = pack_bf16x2(v.x * z.mul, v.y * z.mul);
+        }
         if (lane == 0 && p.lse) p.lse[((size_t)at.b * p.H_q + h) * p.S_q + qs_] = z.lse;
       } else {
-        for (int x = lane; x < D; x += 32) slot[r * D + x] = xch[r * C::XS + x];
+#pragma unroll
+        for (int x = 2 * lane; x < D; x += 64) *reinterpret_cast<float2*>(slot + r * D + x) = sum2(x);
         if (lane == 0) {
           slot[C::ROWS * D + r] = mm;
           slot[C::ROWS * D + C::ROWS + r] = ll;
         }
       }
     }
+    if (at.left == 0) break;
     named_bar_sync(1, 32 * kWarps);  // the exchange is free for the next segment
-    left -= seg_n;
-    if (left > 0) next_segment(at);
+    next_segment(at);
   }
 }
 
@@ -602,9 +630,9 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeParams p, 
   UnitScan scan;
   scan.run(p, H_eff);
   int unused;
-  const long long u0 = scan.before(p, H_eff, b, -1, &unused) + (long long)vh * s.n;
+  const long long u0 = scan.before(p, H_eff, b, -1, &unused) + (long long)vh * s.numbers();
   const int n_cta = ctas_used(scan.total, grid);
-  const int c0 = cta_of(scan.total, n_cta, u0), c1 = cta_of(scan.total, n_cta, u0 + s.n - 1);
+  const int c0 = cta_of(scan.total, n_cta, u0 + kSegCost), c1 = cta_of(scan.total, n_cta, u0 + kSegCost + s.n - 1);
   if (c0 == c1) {  // one CTA had all of it
     grid_wait();
     return;
