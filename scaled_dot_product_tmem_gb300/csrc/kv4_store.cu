@@ -73,22 +73,34 @@ __device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint
   if (top >= 0x7F80u) return kKv4BadScale;
   const int sb = kv4_scale_byte(__uint_as_float(top << 16));
   if (sb == 0) return 0;
+  // s is within 2^-4 of max|x| / 7, so |x / s| < 7.5 and needs no clamping, unless s is below 2^-14
+  // (fewer bits) or the largest scale
+  const bool far = sb < 8 || sb == 0xF7;
   const float inv = __frcp_rn(kv4_scale_value(sb));
   const uint64_t inv2 = f2_pack(inv, inv);
   constexpr float kGrid = 1.5f * 2048.f, kInt = 1.5f * 8388608.f;  // adding it rounds to 2^-12, to whole numbers
   const uint64_t up = f2_pack(kGrid, kGrid), down = f2_pack(-kGrid, -kGrid), whole = f2_pack(kInt, kInt);
+  uint64_t y[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    uint64_t y = f2_mul(f2_pack(__uint_as_float(ws[q] << 16), __uint_as_float(ws[q] & 0xFFFF0000u)), inv2);
-    y = f2_add(f2_add(y, up), down);
+    y[q] = f2_mul(f2_pack(__uint_as_float(ws[q] << 16), __uint_as_float(ws[q] & 0xFFFF0000u)), inv2);
+    y[q] = f2_add(f2_add(y[q], up), down);
+  }
+  if (far) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float a, b;
+      f2_unpack(y[q], a, b);
+      y[q] = f2_pack(fminf(fmaxf(a, -8.f), 7.f), fminf(fmaxf(b, -8.f), 7.f));
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
     float a, b;
-    f2_unpack(y, a, b);
-    a = fminf(fmaxf(a, -8.f), 7.f);
-    b = fminf(fmaxf(b, -8.f), 7.f);
-    f2_unpack(f2_add(f2_pack(a, b), whole), a, b);  // the low bits are the whole number
-    const uint32_t two = (__float_as_uint(a) & 15u) | ((__float_as_uint(b) & 15u) << 4);
-    if (q % 4 == 0) c[q / 4] = two;
-    else c[q / 4] |= two << (8 * (q % 4));
+    f2_unpack(f2_add(y[q], whole), a, b);  // the low bits are the whole number
+    // the low nibbles side by side: bits above them fall to the mask or to the next shift
+    const uint32_t two = (__float_as_uint(a) & 15u) + (__float_as_uint(b) & 15u) * 16u;
+    c[q / 4] = q % 4 == 0 ? two : c[q / 4] + (two << (8 * (q % 4)));
   }
   c[0] ^= 0x88888888u;  // c = 8 + whole number
   c[1] ^= 0x88888888u;
@@ -139,83 +151,71 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4StoreParams p)
   }
 }
 
-// 16 codes as 16 bf16 values (exact).
-__device__ __forceinline__ void held16(uint2 c, int sb, uint4 (&o)[2]) {
+// 8 codes as 8 bf16 values (exact).
+__device__ __forceinline__ uint4 held8(uint32_t w, int sb) {
   const uint32_t s = scale_pair((uint32_t)sb * 0x0101u), m = bf2_mul(s, kM136);
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint32_t w = q ? c.y : c.x;
-    // pairs (0, 4), (1, 5), (2, 6), (3, 7), then neighbours
-    const uint32_t a = decode_pair(w, s, m), b = decode_pair(w >> 4, s, m), d = decode_pair(w >> 8, s, m),
-                   e = decode_pair(w >> 12, s, m);
-    o[q] = make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(d, e, 0x5410), __byte_perm(a, b, 0x7632),
-                      __byte_perm(d, e, 0x7632));
-  }
+  // pairs (0, 4), (1, 5), (2, 6), (3, 7), then neighbours
+  const uint32_t a = decode_pair(w, s, m), b = decode_pair(w >> 4, s, m), d = decode_pair(w >> 8, s, m),
+                 e = decode_pair(w >> 12, s, m);
+  return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(d, e, 0x5410), __byte_perm(a, b, 0x7632),
+                    __byte_perm(d, e, 0x7632));
 }
 
-// The reverse.  Tokens whose page is not in the pool read as zeros; rows of no sequence are left
-// alone, or zeroed on request.
+// The reverse: one thread turns a word of 8 codes into 16 bytes, so that a warp writes whole rows.
+// Tokens whose page is not in the pool read as zeros; rows of no sequence are left alone, or
+// zeroed on request.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4StoreParams p) {
-  constexpr int NG = D / 16, HS = 256 / (NG * kTok);
+  constexpr int NW = D / 8, TS = 256 / NW;  // words of a row; tokens a block takes at a time
   __shared__ TokenAt at[kTok];
   const int t0 = blockIdx.x * kTok;
   find_tokens(p, t0, at);
   const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
-  const int g = threadIdx.x % NG, tk = threadIdx.x / NG % kTok;
-  const TokenAt a = at[tk];
-  if (t0 + tk >= p.T || (a.block == -2 && !p.zero_rest)) return;
-  const bool have = a.block >= 0;
-  const uint8_t* page = p.pool + (have ? a.block : 0);
-  const int at_k = a.w * (D / 2) + g * 8, at_sk = kv4_off_sk(P, D) + a.w * NG + g;
-  const int at_sv = kv4_off_sv(P, D) + (a.w >> 1) * 2 * NG + 2 * g + (a.w & 1);
-  const int at_v0 = kv4_off_v(P, D) + kv4_v_at(a.w, D == 128 ? g : 2 * g, D);
-  const int at_v1 = kv4_off_v(P, D) + kv4_v_at(a.w, 2 * g + 1, D);
-  const size_t row = (size_t)(t0 + tk) * p.c.H_kv;
+  const int x = threadIdx.x % NW, g = x / 2;
+#pragma unroll
+  for (int tk = threadIdx.x / NW; tk < kTok; tk += TS) {
+    const TokenAt a = at[tk];
+    if (t0 + tk >= p.T || (a.block == -2 && !p.zero_rest)) continue;
+    const bool have = a.block >= 0;
+    const uint8_t* page = p.pool + (have ? a.block : 0);
+    const int at_k = a.w * (D / 2) + x * 4, at_sk = kv4_off_sk(P, D) + a.w * (D / 16) + g;
+    const int at_v = kv4_off_v(P, D) + (D == 128 ? kv4_v_at(a.w, g, D) + (x % 2) * 4 : kv4_v_at(a.w, x, D));
+    const int at_sv = kv4_off_sv(P, D) + (a.w >> 1) * (D / 8) + 2 * g + (a.w & 1);
+    const size_t row = (size_t)(t0 + tk) * p.c.H_kv;
 #pragma unroll 4
-  for (int h = threadIdx.x / (NG * kTok) + HS * blockIdx.y; h < p.c.H_kv; h += HS * gridDim.y) {
-    const uint8_t* base = page + (size_t)h * blk;
-    uint2 ck = make_uint2(0u, 0u), cv = ck;
-    int sk = 0, sv = 0;
-    if (have) {
-      ck = __ldg(reinterpret_cast<const uint2*>(base + at_k));
-      sk = __ldg(base + at_sk);
-      if constexpr (D == 128) {
-        cv = __ldg(reinterpret_cast<const uint2*>(base + at_v0));
-      } else {
-        cv.x = __ldg(reinterpret_cast<const uint32_t*>(base + at_v0));
-        cv.y = __ldg(reinterpret_cast<const uint32_t*>(base + at_v1));
+    for (int h = blockIdx.y; h < p.c.H_kv; h += gridDim.y) {
+      const uint8_t* base = page + (size_t)h * blk;
+      uint32_t ck = 0u, cv = 0u;
+      int sk = 0, sv = 0;
+      if (have) {
+        ck = __ldg(reinterpret_cast<const uint32_t*>(base + at_k));
+        cv = __ldg(reinterpret_cast<const uint32_t*>(base + at_v));
+        sk = __ldg(base + at_sk);
+        sv = __ldg(base + at_sv);
       }
-      sv = __ldg(base + at_sv);
+      *reinterpret_cast<uint4*>(p.k_out + (row + h) * D + x * 8) = held8(ck, sk);
+      *reinterpret_cast<uint4*>(p.v_out + (row + h) * D + x * 8) = held8(cv, sv);
     }
-    uint4 o[2];
-    held16(ck, sk, o);
-    uint4* kd = reinterpret_cast<uint4*>(p.k_out + (row + h) * D + g * 16);
-    kd[0] = o[0];
-    kd[1] = o[1];
-    held16(cv, sv, o);
-    uint4* vd = reinterpret_cast<uint4*>(p.v_out + (row + h) * D + g * 16);
-    vd[0] = o[0];
-    vd[1] = o[1];
   }
 }
 
-// Blocks: kTok tokens each; with few tokens the heads are spread over more of them.
-static dim3 store_grid(const Kv4StoreParams& p) {
-  const int x = (p.T + kTok - 1) / kTok, hs = 256 / (p.c.d / 16 * kTok), y_max = (p.c.H_kv + hs - 1) / hs;
+// Blocks: kTok tokens each, `heads` of them at a time; with few tokens the heads are spread over
+// more blocks.
+static dim3 store_grid(const Kv4StoreParams& p, int heads) {
+  const int x = (p.T + kTok - 1) / kTok, y_max = (p.c.H_kv + heads - 1) / heads;
   const int y = x >= 152 * 4 ? 1 : (152 * 4 + x - 1) / x;
   return dim3((unsigned)x, (unsigned)(y < y_max ? y : y_max));
 }
 
 int launch_kv4_append(const Kv4StoreParams& p, cudaStream_t stream) {
-  const dim3 blocks = store_grid(p);
+  const dim3 blocks = store_grid(p, 256 / (p.c.d / 16 * kTok));
   if (p.c.d == 128) kv4_append_kernel<128><<<blocks, 256, 0, stream>>>(p);
   else kv4_append_kernel<64><<<blocks, 256, 0, stream>>>(p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_kv4_gather(const Kv4StoreParams& p, cudaStream_t stream) {
-  const dim3 blocks = store_grid(p);
+  const dim3 blocks = store_grid(p, 1);
   if (p.c.d == 128) kv4_gather_kernel<128><<<blocks, 256, 0, stream>>>(p);
   else kv4_gather_kernel<64><<<blocks, 256, 0, stream>>>(p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
