@@ -28,141 +28,171 @@ namespace sdpa {
 //             flight belong to few sequences, whose other operand they share in L2.
 // The order inside a bucket varies from run to run; no result depends on it.
 // =============================================================================
-constexpr int kPlanThreads = 1024;
+// Latency is all that counts here (a few thousand numbers), so the block has 256 threads where
+// the sequences allow it (cheaper barriers), the offsets stay in shared memory, and the two lists
+// of a backward share their barriers.
+constexpr int kPlanSeqs = 1024;  // sequences whose offsets fit in shared memory
 
 namespace {
-
-// The running maximum of clamped offsets, by the whole block.
-__device__ void clean_offsets(const int* cu, int B, int T, int* out, int* part) {
-  int carry = 0;
-  for (int base = 0; base <= B; base += kPlanThreads) {
-    const int i = base + threadIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int v = i <= B ? min(max(__ldg(cu + i), 0), T) : 0;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) v = max(v, __shfl_up_sync(0xffffffffu, v, off));  // (own value below `off`)
-    if (lane == 31) part[warp] = v;
-    __syncthreads();
-    int before = carry;
-    for (int w = 0; w < warp; ++w) before = max(before, part[w]);
-    v = max(v, before);
-    if (i <= B) out[i] = v;
-    __syncthreads();
-    if (threadIdx.x == kPlanThreads - 1) part[0] = v;
-    __syncthreads();
-    carry = part[0];
-    __syncthreads();
-  }
-}
 
 enum PlanKind { kPlanFwd, kPlanKv, kPlanQ };
 
 template <int KIND>
-struct PlanRows {
-  static constexpr int value = KIND == kPlanFwd ? 256 : 128;
-};
+constexpr int plan_rows() { return KIND == kPlanFwd ? 256 : 128; }
 
-// Lists one kernel's tiles; returns their number.
-template <int KIND>
-__device__ int list_tiles(const PackedPlanParams& p, const int* cq, const int* ck, PackedTile* out, int* hist,
-                          int* part) {
-  constexpr int ROWS = PlanRows<KIND>::value;
+// f(sequence b, its four numbers, its tiles n, first tile, step between tiles) for every sequence
+// with tiles: those of up to 8 tiles by one thread each, longer ones by the warp.
+template <int KIND, int NT, class F>
+__device__ __forceinline__ void plan_walk(int B, const int* cq, const int* ck, F f) {
+  constexpr int ROWS = plan_rows<KIND>();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  auto bucket = [&](int Lq, int Lk, int n, int j) {
-    int w = n;
-    if constexpr (KIND == kPlanFwd) {
-      int lo = 1, hi = 0;
-      w = kv_tile_range(MaskSpec{Lq, Lk, p.causal, p.window}, j * ROWS, j * ROWS + ROWS - 1, 128, &lo, &hi)
-              ? hi - lo + 1 : 0;
+  for (int b0 = warp * 32; b0 < B; b0 += NT) {
+    const int b = b0 + lane;
+    int q0 = 0, Lq = 0, k0 = 0, Lk = 0;
+    if (b < B) {
+      q0 = cq[b];
+      Lq = cq[b + 1] - q0;
+      k0 = ck[b];
+      Lk = ck[b + 1] - k0;
     }
-    return min(w, kPlanThreads - 1);
-  };
-  // f(sequence b, its four numbers, its tiles n, first tile, step between tiles): sequences of up
-  // to 8 tiles by one thread each, longer ones by the warp
-  auto walk = [&](auto f) {
-    for (int b0 = warp * 32; b0 < p.B; b0 += kPlanThreads) {
-      const int b = b0 + lane;
-      int q0 = 0, Lq = 0, k0 = 0, Lk = 0;
-      if (b < p.B) {
-        q0 = cq[b];
-        Lq = cq[b + 1] - q0;
-        k0 = ck[b];
-        Lk = ck[b + 1] - k0;
-      }
-      const int n = ((KIND == kPlanKv ? Lk : Lq) + ROWS - 1) / ROWS;
-      if (n > 0 && n <= 8) f(b, q0, Lq, k0, Lk, n, 0, 1);
-      for (unsigned m = __ballot_sync(0xffffffffu, n > 8); m; m &= m - 1) {
-        const int s = __ffs(m) - 1;
-        f(b0 + s, __shfl_sync(0xffffffffu, q0, s), __shfl_sync(0xffffffffu, Lq, s), __shfl_sync(0xffffffffu, k0, s),
-          __shfl_sync(0xffffffffu, Lk, s), __shfl_sync(0xffffffffu, n, s), lane, 32);
-      }
+    const int n = ((KIND == kPlanKv ? Lk : Lq) + ROWS - 1) / ROWS;
+    if (n > 0 && n <= 8) f(b, q0, Lq, k0, Lk, n, 0, 1);
+    for (unsigned m = __ballot_sync(0xffffffffu, n > 8); m; m &= m - 1) {
+      const int s = __ffs(m) - 1;
+      f(b0 + s, __shfl_sync(0xffffffffu, q0, s), __shfl_sync(0xffffffffu, Lq, s), __shfl_sync(0xffffffffu, k0, s),
+        __shfl_sync(0xffffffffu, Lk, s), __shfl_sync(0xffffffffu, n, s), lane, 32);
     }
-  };
-  hist[threadIdx.x] = 0;
-  __syncthreads();
-  walk([&](int, int, int Lq, int, int Lk, int n, int j0, int step) {
+  }
+}
+
+// The bucket of tile j of a sequence of n tiles: the kv tiles it sees (forward), or n.
+template <int KIND, int NT>
+__device__ __forceinline__ int plan_bucket(const PackedPlanParams& p, int Lq, int Lk, int n, int j) {
+  int w = n;
+  if constexpr (KIND == kPlanFwd) {
+    int lo = 1, hi = 0;
+    w = kv_tile_range(MaskSpec{Lq, Lk, p.causal, p.window}, j * 256, j * 256 + 255, 128, &lo, &hi) ? hi - lo + 1 : 0;
+  }
+  return min(w, NT - 1);
+}
+
+template <int KIND, int NT>
+__device__ __forceinline__ void plan_count(const PackedPlanParams& p, const int* cq, const int* ck, int* hist) {
+  plan_walk<KIND, NT>(p.B, cq, ck, [&](int, int, int Lq, int, int Lk, int n, int j0, int step) {
     if constexpr (KIND == kPlanFwd) {
-      for (int j = j0; j < n; j += step) atomicAdd(&hist[bucket(Lq, Lk, n, j)], 1);
+      for (int j = j0; j < n; j += step) atomicAdd(&hist[plan_bucket<KIND, NT>(p, Lq, Lk, n, j)], 1);
     } else if (j0 == 0) {
-      atomicAdd(&hist[bucket(Lq, Lk, n, 0)], n);
+      atomicAdd(&hist[plan_bucket<KIND, NT>(p, Lq, Lk, n, 0)], n);
     }
   });
-  __syncthreads();
-  // first entry of each bucket, the highest bucket first
-  const int mine = hist[kPlanThreads - 1 - threadIdx.x];
-  int sum = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, sum, off);
-    if (lane >= off) sum += o;
-  }
-  if (lane == 31) part[warp] = sum;
-  __syncthreads();
-  int total = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) sum += part[w];
-    total += part[w];
-  }
-  hist[kPlanThreads - 1 - threadIdx.x] = sum - mine;
-  __syncthreads();
-  walk([&](int b, int q0, int Lq, int k0, int Lk, int n, int j0, int step) {
+}
+
+template <int KIND, int NT>
+__device__ __forceinline__ void plan_place(const PackedPlanParams& p, const int* cq, const int* ck, int* next,
+                                           PackedTile* out) {
+  plan_walk<KIND, NT>(p.B, cq, ck, [&](int b, int q0, int Lq, int k0, int Lk, int n, int j0, int step) {
     int base = 0;
     if constexpr (KIND != kPlanFwd) {
-      if (j0 == 0) base = atomicAdd(&hist[bucket(Lq, Lk, n, 0)], n);
+      if (j0 == 0) base = atomicAdd(&next[plan_bucket<KIND, NT>(p, Lq, Lk, n, 0)], n);
       if (step == 32) base = __shfl_sync(0xffffffffu, base, 0);
     }
     for (int j = j0; j < n; j += step) {
       int at, tile = j;
       if constexpr (KIND == kPlanFwd) {
-        at = atomicAdd(&hist[bucket(Lq, Lk, n, j)], 1);
+        at = atomicAdd(&next[plan_bucket<KIND, NT>(p, Lq, Lk, n, j)], 1);
       } else {
         at = base + j;
         if (KIND == kPlanQ && p.causal) tile = n - 1 - j;  // under a causal mask the last query tile sees most
       }
       int4* e = reinterpret_cast<int4*>(out + at);
       e[0] = make_int4(q0, Lq, k0, Lk);
-      e[1] = make_int4(b, tile * ROWS, (int)(((long long)q0 + 128LL * b) / 128 * 128), 0);
+      e[1] = make_int4(b, tile * plan_rows<KIND>(), (int)(((long long)q0 + 128LL * b) / 128 * 128), 0);
     }
   });
-  __syncthreads();
-  return total;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlanParams p) {
-  __shared__ int hist[kPlanThreads], part[32];
+template <int NT, bool BWD>
+__global__ void __launch_bounds__(NT) packed_plan_kernel(const PackedPlanParams p) {
+  __shared__ int hist[2][NT], part[2][NT / 32], sq[kPlanSeqs + 1], sk[kPlanSeqs + 1];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   grid_launch_dependents();
-  clean_offsets(p.cu_q, p.B, p.T_q, p.clean_q, part);
-  const int* ck = p.clean_q;
-  if (p.cu_kv != p.cu_q || p.T_kv != p.T_q) {
-    clean_offsets(p.cu_kv, p.B, p.T_kv, p.clean_kv, part);
-    ck = p.clean_kv;
+  const bool same = p.cu_kv == p.cu_q && p.T_kv == p.T_q, small = p.B <= kPlanSeqs;
+  int* cq = small ? sq : p.clean_q;
+  int* ck = same ? cq : (small ? sk : p.clean_kv);
+  hist[0][threadIdx.x] = hist[1][threadIdx.x] = 0;
+  // the running maxima of the clamped offsets
+  int carry_q = 0, carry_k = 0;
+  for (int base = 0; base <= p.B; base += NT) {
+    const int i = base + threadIdx.x;
+    int q = i <= p.B ? min(max(__ldg(p.cu_q + i), 0), p.T_q) : 0;
+    int k = i <= p.B && !same ? min(max(__ldg(p.cu_kv + i), 0), p.T_kv) : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {  // (below `off` a lane gets its own value)
+      q = max(q, __shfl_up_sync(0xffffffffu, q, off));
+      k = max(k, __shfl_up_sync(0xffffffffu, k, off));
+    }
+    if (lane == 31) {
+      part[0][warp] = q;
+      part[1][warp] = k;
+    }
+    __syncthreads();
+    int top_q = carry_q, top_k = carry_k;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w == warp) {
+        q = max(q, top_q);
+        k = max(k, top_k);
+      }
+      top_q = max(top_q, part[0][w]);
+      top_k = max(top_k, part[1][w]);
+    }
+    carry_q = top_q;
+    carry_k = top_k;
+    if (i <= p.B) {
+      cq[i] = q;
+      if (!same) ck[i] = k;
+    }
+    __syncthreads();
+  }
+  constexpr int A = BWD ? kPlanKv : kPlanFwd;
+  PackedTile* list_a = BWD ? p.tiles_kv : p.tiles_fwd;
+  plan_count<A, NT>(p, cq, ck, hist[0]);
+  if constexpr (BWD) plan_count<kPlanQ, NT>(p, cq, ck, hist[1]);
+  __syncthreads();
+  // first entry of each bucket, the highest bucket first
+  int sum[2], mine[2], total[2] = {0, 0};
+#pragma unroll
+  for (int l = 0; l < 2; ++l) {
+    mine[l] = sum[l] = hist[l][NT - 1 - threadIdx.x];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum[l], off);
+      if (lane >= off) sum[l] += o;
+    }
+    if (lane == 31) part[l][warp] = sum[l];
   }
   __syncthreads();
-  PackedCounts c{};
-  if (p.tiles_fwd) c.fwd_tiles = list_tiles<kPlanFwd>(p, p.clean_q, ck, p.tiles_fwd, hist, part);
-  if (p.tiles_kv) c.kv_tiles = list_tiles<kPlanKv>(p, p.clean_q, ck, p.tiles_kv, hist, part);
-  if (p.tiles_q) c.q_tiles = list_tiles<kPlanQ>(p, p.clean_q, ck, p.tiles_q, hist, part);
+#pragma unroll
+  for (int l = 0; l < 2; ++l) {
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) sum[l] += part[l][w];
+      total[l] += part[l][w];
+    }
+    hist[l][NT - 1 - threadIdx.x] = sum[l] - mine[l];
+  }
+  __syncthreads();
+  plan_place<A, NT>(p, cq, ck, hist[0], list_a);
+  if constexpr (BWD) plan_place<kPlanQ, NT>(p, cq, ck, hist[1], p.tiles_q);
   if (threadIdx.x == 0) {
-    c.q_end = p.clean_q[p.B];
+    PackedCounts c{};
+    if (BWD) {
+      c.kv_tiles = total[0];
+      c.q_tiles = total[1];
+    } else {
+      c.fwd_tiles = total[0];
+    }
+    c.q_end = cq[p.B];
     c.kv_end = ck[p.B];
     *p.counts = c;
   }
@@ -171,7 +201,14 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 }  // namespace
 
 int launch_packed_plan(const PackedPlanParams& p, cudaStream_t stream) {
-  packed_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  const bool bwd = p.tiles_fwd == nullptr;
+  if (p.B < 256) {
+    if (bwd) packed_plan_kernel<256, true><<<1, 256, 0, stream>>>(p);
+    else packed_plan_kernel<256, false><<<1, 256, 0, stream>>>(p);
+  } else {
+    if (bwd) packed_plan_kernel<1024, true><<<1, 1024, 0, stream>>>(p);
+    else packed_plan_kernel<1024, false><<<1, 1024, 0, stream>>>(p);
+  }
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
