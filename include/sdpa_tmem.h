@@ -148,8 +148,8 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
  * that sees no key gets o = 0 and lse = the sink logit.  lse: fp32 [H_q, T_q].  Values of
  * one sequence, infinities and NaN included, never reach another sequence's results.
  * Offsets are clamped to [0, T] and to their running maximum.  Rows that belong to no
- * sequence (past the last one, or before cu_seqlens[0]) are left alone; zero_rest != 0
- * writes the ones past the last sequence: o, dq, dk, dv = 0, lse = -inf.
+ * sequence (past the last one, or before cu_seqlens[0]) are left alone; with zero_rest != 0
+ * they get o, dq, dk, dv = 0 and lse = -inf.
  * attn_bwd_packed is bitwise reproducible.  For LEARNABLE sinks its d_offset carries fp32
  * rounding only, not that of the stored bf16 o.
  * workspace: device scratch of attn_packed_workspace_size() bytes (backward 0 or 1),

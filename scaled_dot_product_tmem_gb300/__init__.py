@@ -664,6 +664,11 @@ def _elsewhere(dev, stream):
     return stream is not None or dev != torch.cuda.current_device()
 
 
+def _window(window):
+    """The window as a C int: one past 32 bits must not wrap into a small one."""
+    return max(-1, min(int(window), 0x7fffffff))
+
+
 def _raw_stream(dev, stream):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -715,8 +720,8 @@ def attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv=None, *, causal
     fp32: q [T_q, H_q, d_qk], k [T_kv, H_kv, d_qk], v [T_kv, H_kv, d_v].
 
     cu_seqlens_q / cu_seqlens_kv: int32 [B+1] on the device, sequence b's rows are
-    cu_seqlens[b] .. cu_seqlens[b+1] - 1 (cu_seqlens_kv None: the queries' offsets).  Rows past
-    the last sequence are left alone, or zeroed with zero_rest (lse -inf).  workspace: uint8 of
+    cu_seqlens[b] .. cu_seqlens[b+1] - 1 (cu_seqlens_kv None: the queries' offsets).  Rows of no
+    sequence are left alone, or zeroed with zero_rest (lse -inf).  workspace: uint8 of
     attn_packed_workspace_size() bytes or more, not shared with a call that may run at the
     same time (None: a new one)."""
     sizes = _check_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
@@ -733,7 +738,7 @@ def attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv=None, *, causal
                                    zero_rest=zero_rest, workspace=workspace)
     ws = _workspace(workspace, attn_packed_workspace_size(*sizes) if workspace is None else 0, q.device)
     st = _load().attn_fwd_packed(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(cu_seqlens_q), _p(cu_seqlens_kv), *sizes,
-                                 float(scale or 0.0), int(bool(causal)), int(window), _stype(softmax_type),
+                                 float(scale or 0.0), int(bool(causal)), _window(window), _stype(softmax_type),
                                  _p(softmax_offset), int(bool(zero_rest)), _p(ws), ws.numel(),
                                  _raw_stream(dev, stream))
     if st != ATTN_OK:
@@ -770,7 +775,7 @@ def attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, c
     ws = _workspace(workspace, attn_packed_workspace_size(*sizes, True) if workspace is None else 0, q.device)
     st = _load().attn_bwd_packed(_p(q), _p(k), _p(v), _p(o), _p(dout), _p(lse), _p(dq), _p(dk), _p(dv), _p(d_offset),
                                  _p(cu_seqlens_q), _p(cu_seqlens_kv), *sizes, float(scale or 0.0), int(bool(causal)),
-                                 int(window), _stype(softmax_type), _p(softmax_offset), int(bool(zero_rest)), _p(ws),
+                                 _window(window), _stype(softmax_type), _p(softmax_offset), int(bool(zero_rest)), _p(ws),
                                  ws.numel(), _raw_stream(dev, stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_bwd_packed")
@@ -778,8 +783,8 @@ def attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, c
 
 def sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv=None, *, causal=True, window=-1, softmax_type=VANILLA,
                         softmax_offset=None, scale=0.0, workspace=None, stream=None):
-    """Allocate O and LSE, run attn_fwd_packed, return (o, lse); rows past the last sequence are
-    zero (lse -inf)."""
+    """Allocate O and LSE, run attn_fwd_packed, return (o, lse); rows of no sequence are zero (lse
+    -inf)."""
     kw = dict(causal=causal, window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
               workspace=workspace)
     dev = _device_of(q)
@@ -796,7 +801,7 @@ def sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv=None, *, causal=Tru
 def sdpa_backward_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv=None, *, causal=True, window=-1,
                          softmax_type=VANILLA, softmax_offset=None, scale=0.0, workspace=None, stream=None):
     """Allocate dQ, dK, dV (and d_offset for the learnable sink), run attn_bwd_packed, return
-    them; gradients of rows past the last sequence are zero."""
+    them; gradients of rows of no sequence are zero."""
     kw = dict(causal=causal, window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
               workspace=workspace)
     dev = _device_of(q)
@@ -992,7 +997,7 @@ def attn_kv4_decode(q, pool, page_table, seq_lens, o, lse=None, *, window=-1, so
     ws = _workspace(workspace, attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d) if workspace is None else 0,
                     q.device)
     st = _load().attn_kv4_decode(_p(q), _p(pool), _p(page_table), _p(seq_lens), _p(o), _p(lse), B, S_q, H_q, H_kv, d,
-                                 n_pages, page_size, max_pages, float(scale or 0.0), int(window),
+                                 n_pages, page_size, max_pages, float(scale or 0.0), _window(window),
                                  _stype(softmax_type), _p(softmax_offset), _p(ws), ws.numel(),
                                  _raw_stream(dev, stream))
     if st != ATTN_OK:

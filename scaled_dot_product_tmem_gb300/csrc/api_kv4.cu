@@ -1,6 +1,7 @@
 // api_kv4.cu -- the C ABI of the 4-bit paged key/value cache: argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <new>
 #include <vector>
@@ -31,10 +32,11 @@ int check_sizes(int B, int H_kv, int d, int n_pages, int page_size, int max_page
 }
 
 template <class F>
-int launch(const char* what, cudaStream_t s, F f) {
+int launch(const char* what, int n, cudaStream_t s, F f) {
   const int rc = sdpa::timed_launch(
-      ATTN_KERNEL_KV4, 1, s, [](void* ctx) { return (*static_cast<F*>(ctx))(); }, &f);
+      ATTN_KERNEL_KV4, n, s, [](void* ctx) { return (*static_cast<F*>(ctx))(); }, &f);
   if (rc == 0) return ATTN_OK;
+  if (rc == -2) return ATTN_ERR_UNSUPPORTED;
   sdpa::set_last_error(what, cudaGetLastError());
   return ATTN_ERR_CUDA;
 }
@@ -73,7 +75,7 @@ int attn_kv4_append(const void* k, const void* v, const int* cu_seqlens, void* p
   p.site = ATTN_KV4_SITE_APPEND;
   if (!p.page_err) return ATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch("kv4 append launch", s, [&] { return sdpa::launch_kv4_append(p, s); });
+  return launch("kv4 append launch", 1, s, [&] { return sdpa::launch_kv4_append(p, s); });
 }
 
 int attn_kv4_gather(const void* pool, const int* page_table, const int* cu_seqlens, const int* seq_lens, void* k,
@@ -101,7 +103,7 @@ int attn_kv4_gather(const void* pool, const int* page_table, const int* cu_seqle
   p.site = ATTN_KV4_SITE_GATHER;
   if (!p.page_err) return ATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch("kv4 gather launch", s, [&] { return sdpa::launch_kv4_gather(p, s); });
+  return launch("kv4 gather launch", 1, s, [&] { return sdpa::launch_kv4_gather(p, s); });
 }
 
 size_t attn_kv4_decode_workspace_size(int B, int S_q, int H_q, int H_kv, int d) {
@@ -133,7 +135,8 @@ int attn_kv4_decode(const void* q, const void* pool, const int* page_table, cons
   p.S_q = S_q;
   p.H_q = H_q;
   p.scale_log2 = sdpa::resolve_scale(scale, d) * 1.4426950408889634f;
-  p.window = window < 0 ? -1 : window;
+  // a window of the whole table and more is none (and its arithmetic could pass 32 bits)
+  p.window = window < 0 || window >= (long long)max_pages * page_size ? -1 : window;
   p.softmax_type = softmax_type;
   p.offset = softmax_offset;
   p.seq_lens = seq_lens;
@@ -146,7 +149,7 @@ int attn_kv4_decode(const void* q, const void* pool, const int* page_table, cons
   p.site = ATTN_KV4_SITE_DECODE;
   if (!p.err || !p.page_err) return ATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch("kv4 decode launch", s, [&] { return sdpa::launch_kv4_decode(p, workspace, s); });
+  return launch("kv4 decode launch", 2, s, [&] { return sdpa::launch_kv4_decode(p, workspace, s); });
 }
 
 int attn_kv4_copy_pages(void* pool, int n_layers, int n_pages, size_t page_bytes, const int* src, const int* dst,
@@ -156,19 +159,30 @@ int attn_kv4_copy_pages(void* pool, int n_layers, int n_pages, size_t page_bytes
   if (!pool || !src || !dst) return ATTN_ERR_INVALID_ARG;
   if (!aligned(pool, 16)) return ATTN_ERR_MISALIGNED;
   if (n_layers > 65535) return ATTN_ERR_UNSUPPORTED;
+  for (int i = 0; i < n; ++i)
+    if (src[i] < 0 || src[i] >= n_pages || dst[i] < 0 || dst[i] >= n_pages) return ATTN_ERR_INVALID_ARG;
   try {
-    std::vector<unsigned char> use(n_pages, 0);  // 1: a source, 2: a destination
-    for (int i = 0; i < n; ++i) {
-      if (src[i] < 0 || src[i] >= n_pages || dst[i] < 0 || dst[i] >= n_pages) return ATTN_ERR_INVALID_ARG;
-      if ((use[src[i]] & 2) || use[dst[i]] || src[i] == dst[i]) return ATTN_ERR_INVALID_ARG;
-      use[src[i]] = 1;
-      use[dst[i]] = 2;
+    if (n_pages <= (1 << 20)) {  // what every page is used as
+      std::vector<unsigned char> use(n_pages, 0);
+      for (int i = 0; i < n; ++i) use[src[i]] = 1;
+      for (int i = 0; i < n; ++i) {
+        if (use[dst[i]]) return ATTN_ERR_INVALID_ARG;  // a source, or a destination already
+        use[dst[i]] = 1;
+      }
+    } else {
+      std::vector<int> from(src, src + n), to(dst, dst + n);
+      std::sort(from.begin(), from.end());
+      std::sort(to.begin(), to.end());
+      if (std::adjacent_find(to.begin(), to.end()) != to.end()) return ATTN_ERR_INVALID_ARG;
+      for (int page : to)
+        if (std::binary_search(from.begin(), from.end(), page)) return ATTN_ERR_INVALID_ARG;
     }
   } catch (const std::bad_alloc&) {
-    return ATTN_ERR_INVALID_ARG;
+    sdpa::set_last_error("kv4 page copy: host memory for the check", cudaErrorMemoryAllocation);
+    return ATTN_ERR_CUDA;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch("kv4 page copy launch", s, [&] {
+  return launch("kv4 page copy launch", (n + sdpa::kKv4PairsMax - 1) / sdpa::kKv4PairsMax, s, [&] {
     return sdpa::launch_kv4_copy(static_cast<uint8_t*>(pool), n_layers, (long long)n_pages * (long long)page_bytes,
                                  (long long)page_bytes, src, dst, n, s);
   });

@@ -124,7 +124,7 @@ int attn_fwd_packed(const void* q, const void* k, const void* v, void* o, float*
   plan.cu_kv = cu_seqlens_kv;
   plan.B = B; plan.T_q = T_q; plan.T_kv = T_kv;
   plan.causal = causal ? 1 : 0;
-  plan.window = window < 0 ? -1 : window;
+  plan.window = window < 0 || window >= T_q ? -1 : window;  // (no row looks further back than T_q - 1)
   plan.clean_q = reinterpret_cast<int*>(ws + w.clean_q);
   plan.clean_kv = reinterpret_cast<int*>(ws + w.clean_kv);
   plan.counts = reinterpret_cast<sdpa::PackedCounts*>(ws + w.counts);
@@ -192,7 +192,7 @@ int attn_bwd_packed(const void* q, const void* k, const void* v, const void* o, 
   plan.cu_kv = cu_seqlens_kv;
   plan.B = B; plan.T_q = T_q; plan.T_kv = T_kv;
   plan.causal = causal ? 1 : 0;
-  plan.window = window < 0 ? -1 : window;
+  plan.window = window < 0 || window >= T_q ? -1 : window;  // (no row looks further back than T_q - 1)
   plan.clean_q = reinterpret_cast<int*>(ws + w.clean_q);
   plan.clean_kv = reinterpret_cast<int*>(ws + w.clean_kv);
   plan.counts = reinterpret_cast<sdpa::PackedCounts*>(ws + w.counts);

@@ -116,8 +116,10 @@ __device__ __forceinline__ PackedTile load_packed_tile(const PackedTile* t, int 
 // What the plan of a packed batch counts.
 struct PackedCounts {
   int fwd_tiles, kv_tiles, q_tiles;  // entries of the tile lists
-  int q_end, kv_end;                 // rows of the last sequence end here: rows past them are no sequence's
-  int unused[3];
+  // the sequences' rows: [q_begin, q_end) and [kv_begin, kv_end) (they follow one another, so the
+  // rows before and behind these belong to no sequence)
+  int q_begin, q_end, kv_begin, kv_end;
+  int unused;
 };
 
 // Zero rows [from, rows) of `chunks` shared-memory chunks of rows x 128 bytes (a warp).  Whole

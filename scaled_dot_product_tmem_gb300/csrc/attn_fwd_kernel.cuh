@@ -669,12 +669,16 @@ __global__ void __launch_bounds__(320, 1)
     }
     if constexpr (PK) {
       if (p.zero_rest) {  // rows of no sequence: o = 0, lse = -inf
-        const int end = p.counts->q_end, rest = p.S_q - end;
-        const size_t n16 = (size_t)rest * p.H_q * (D_V / 8), at = blockIdx.x * 256 + threadIdx.x;
-        uint4* o16 = reinterpret_cast<uint4*>(p.o + (size_t)end * p.H_q * D_V);
-        for (size_t e = at; e < n16; e += (size_t)gridDim.x * 256) o16[e] = make_uint4(0u, 0u, 0u, 0u);
-        for (size_t e = at; e < (size_t)rest * p.H_q; e += (size_t)gridDim.x * 256)
-          p.lse[(e / rest) * p.S_q + end + e % rest] = -INFINITY;
+        const PackedCounts c = *p.counts;
+        const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x, step = (size_t)gridDim.x * 256;
+        auto clear = [&](int from, int to) {
+          uint4* o16 = reinterpret_cast<uint4*>(p.o + (size_t)from * p.H_q * D_V);
+          const size_t n16 = (size_t)(to - from) * p.H_q * (D_V / 8), rows = to - from;
+          for (size_t e = at; e < n16; e += step) o16[e] = make_uint4(0u, 0u, 0u, 0u);
+          for (size_t e = at; e < rows * p.H_q; e += step) p.lse[(e / rows) * p.S_q + from + e % rows] = -INFINITY;
+        };
+        clear(0, c.q_begin);
+        clear(c.q_end, p.S_q);
       }
     }
   }

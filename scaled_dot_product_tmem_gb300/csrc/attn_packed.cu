@@ -192,7 +192,9 @@ __global__ void __launch_bounds__(NT) packed_plan_kernel(const PackedPlanParams 
     } else {
       c.fwd_tiles = total[0];
     }
+    c.q_begin = cq[0];
     c.q_end = cq[p.B];
+    c.kv_begin = ck[0];
     c.kv_end = ck[p.B];
     *p.counts = c;
   }
@@ -280,14 +282,18 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
     const size_t at = ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
     const size_t step = (size_t)gridDim.x * gridDim.y * 256;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    auto clear = [&](__nv_bfloat16* x, int from, int rows, int H, int d) {
+    auto clear = [&](__nv_bfloat16* x, int from, int to, int H, int d) {
       uint4* x16 = reinterpret_cast<uint4*>(x + (size_t)from * H * d);
-      const size_t n = (size_t)(rows - from) * H * (d / 8);
+      const size_t n = (size_t)(to - from) * H * (d / 8);
       for (size_t i = at; i < n; i += step) x16[i] = z;
     };
-    clear(p.dq, p.counts->q_end, p.S_q, p.H_q, d_qk);
-    clear(p.dk, p.counts->kv_end, p.S_kv, p.H_kv, d_qk);
-    clear(p.dv, p.counts->kv_end, p.S_kv, p.H_kv, D_V);
+    const PackedCounts c = *p.counts;
+    clear(p.dq, 0, c.q_begin, p.H_q, d_qk);
+    clear(p.dq, c.q_end, p.S_q, p.H_q, d_qk);
+    clear(p.dk, 0, c.kv_begin, p.H_kv, d_qk);
+    clear(p.dk, c.kv_end, p.S_kv, p.H_kv, d_qk);
+    clear(p.dv, 0, c.kv_begin, p.H_kv, D_V);
+    clear(p.dv, c.kv_end, p.S_kv, p.H_kv, D_V);
   }
 }
 
@@ -346,8 +352,8 @@ int launch_packed_doffset(const BwdParams& p, cudaStream_t stream) {
 __global__ void __launch_bounds__(256) packed_kv_combine_kernel(const float4* __restrict__ part,
                                                                 uint2* __restrict__ out, size_t slice4,
                                                                 const PackedCounts* counts, int row4, int ns) {
-  const size_t n4 = (size_t)counts->kv_end * row4;
-  for (size_t t = (size_t)blockIdx.x * 256 + threadIdx.x; t < n4; t += (size_t)gridDim.x * 256) {
+  const size_t n4 = (size_t)counts->kv_end * row4, t0 = (size_t)counts->kv_begin * row4;
+  for (size_t t = t0 + (size_t)blockIdx.x * 256 + threadIdx.x; t < n4; t += (size_t)gridDim.x * 256) {
     float4 a = part[t];
     for (int s = 1; s < ns; ++s) {
       const float4 b = part[(size_t)s * slice4 + t];

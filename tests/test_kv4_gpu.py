@@ -186,6 +186,8 @@ DECODE = [
     ("window", [500, 20, 130, 1], 1, 8, 2, 128, 64, 100, "vanilla"),
     ("window0_only_itself", [40, 1], 2, 4, 2, 64, 16, 0, "vanilla"),
     ("window_multi_token_sink", [300, 65], 5, 4, 2, 64, 128, 33, "learnable"),
+    ("huge_window_short_entries", [2, 40, 0], 4, 4, 2, 64, 16, 2 ** 31 - 1, "vanilla"),
+    ("window_past_32_bits", [200], 1, 4, 2, 64, 16, 2 ** 40, "vanilla"),
     ("long_context", [5000, 1, 2600], 1, 8, 2, 128, 64, -1, "vanilla"),
     ("long_prompt_of_queries", [150], 100, 4, 2, 64, 32, -1, "vanilla"),
 ]

@@ -141,6 +141,9 @@ def test_copy_pages_validation(lib):
     assert cp([3], [3]) == INVALID
     assert cp([0], [8]) == INVALID and cp([-1], [2]) == INVALID and cp([9], [2]) == INVALID
     assert cp([0], [1], byts=60) == INVALID
+    big = 1 << 22                              # pools past a million pages are checked by sorting
+    assert cp([5, 7], [9, 9], n_pages=big) == INVALID and cp([5, 9], [9, 1], n_pages=big) == INVALID
+    assert cp([5], [5], n_pages=big) == INVALID and cp([5], [big], n_pages=big) == INVALID
     assert cp([0], [1], pool=None) == INVALID and cp([0], [1], pool=MIS) == MISALIGNED
     assert cp([0], [1], n_pages=-1) == INVALID and cp([0], [1], layers=-1) == INVALID
     assert cp([0], [1], layers=70000) == UNSUPPORTED

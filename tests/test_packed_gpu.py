@@ -206,6 +206,25 @@ def test_rows_of_no_sequence_are_left_alone():
     assert a.shape[0] == 0 and g2[1].shape[0] == 0
 
 
+def test_rows_before_the_first_sequence_and_huge_windows():
+    sdpa = _sdpa()
+    x = _inputs([100], [100], 4, 2, 128, 128, 12, extra=20)
+    q, k, v, do = (x[n].cuda() for n in ("q", "k", "v", "dout"))
+    cu = _i32([30, 30, 100])
+    o, lse = sdpa.sdpa_forward_packed(q, k, v, cu, window=2 ** 40)
+    g = sdpa.sdpa_backward_packed(q, k, v, o, do, lse, cu, window=2 ** 31 - 1)
+    part = [t[30:100].contiguous() for t in (q, k, v)]
+    o1, lse1 = sdpa.sdpa_forward_packed(*part, _i32([0, 70]))
+    g1 = sdpa.sdpa_backward_packed(*part, o1, do[30:100].contiguous(), lse1, _i32([0, 70]))
+    _clean()
+    assert torch.equal(o[30:100], o1) and torch.equal(lse[:, 30:100], lse1)
+    for a, b in zip(g[:3], g1[:3]):
+        assert torch.equal(a[30:100], b)
+    for t in (o, *g[:3]):
+        assert torch.all(t[:30] == 0) and torch.all(t[100:] == 0)
+    assert torch.all(lse[:, :30] == -float("inf")) and torch.all(lse[:, 100:] == -float("inf"))
+
+
 def test_offsets_that_are_not_offsets_are_clamped():
     """Not ascending, negative, past the end: each is clamped to [0, T] and to the running
     maximum, and nothing outside the tensors is touched."""
