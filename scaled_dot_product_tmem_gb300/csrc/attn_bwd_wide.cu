@@ -613,8 +613,8 @@ static int launch_kvw_packed_t(const CUtensorMap& tq, const CUtensorMap& tk, con
   using C = KvWCfg<D_QK, D_V>;
   const long long grid = p.tile_bound_kv * p.H_kv * p.ns;
   if (grid <= 0 || grid > 0x7fffffffLL) return -2;
-  auto kern = attn_bwd_kvw_kernel<D_QK, D_V, true, false, true>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
+  constexpr auto kern = attn_bwd_kvw_kernel<D_QK, D_V, true, false, true>;
+  if (!allow_smem<kern>(C::SMEM)) return -1;
   return launch_kernel(kern, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, true, tq, tk, tv, tdo, p);
 }
 

@@ -699,7 +699,9 @@ inline int launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   using C = FwdCfg<D_QK, D_V, NK, NV, F8, fwd_bias_staged<D_QK, BIAS>()>;
   auto kern = attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP, PK>;
   static bool attr_set = false;
-  if (!attr_set) {
+  if constexpr (PK) {
+    if (!allow_smem<attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP, PK>>(C::SMEM)) return -1;
+  } else if (!attr_set) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
     attr_set = true;
   }

@@ -383,8 +383,8 @@ int launch_bwd_kv_packed_mla(const CUtensorMap& tq64, const CUtensorMap& tk, con
   using C = KvCfg<192, 128, false>;
   const long long grid = p.tile_bound_kv * p.H_kv * p.ns;
   if (grid <= 0 || grid > 0x7fffffffLL) return -2;
-  auto kern = attn_bwd_kv_kernel<192, 128, false, true, false, false, false, true>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
+  constexpr auto kern = attn_bwd_kv_kernel<192, 128, false, true, false, false, false, true>;
+  if (!allow_smem<kern>(C::SMEM)) return -1;
   return launch_kernel(kern, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, true, tq64, tk, tv, tdo64, tq64, tq64, p);
 }
 
@@ -394,9 +394,10 @@ static int launch_q_packed_t(const CUtensorMap& tq, const CUtensorMap& tk, const
   using C = QCfg<D_QK, D_V>;
   const long long grid = p.tile_bound_q * p.H_q;
   if (grid <= 0 || grid > 0x7fffffffLL) return -2;
-  auto kern = p.ds_rowsum ? attn_bwd_q_kernel<D_QK, D_V, true, false, false, false, true, true>
-                          : attn_bwd_q_kernel<D_QK, D_V, true, false, false, false, true, false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
+  constexpr auto plain = attn_bwd_q_kernel<D_QK, D_V, true, false, false, false, true, false>;
+  constexpr auto sums = attn_bwd_q_kernel<D_QK, D_V, true, false, false, false, true, true>;
+  const auto kern = p.ds_rowsum ? sums : plain;
+  if (!(p.ds_rowsum ? allow_smem<sums>(C::SMEM) : allow_smem<plain>(C::SMEM))) return -1;
   return launch_kernel(kern, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, early, tq, tk, tv, tdo, p);
 }
 

@@ -2,6 +2,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace sdpa {
 
 // Launches kern(args...).  early: with programmatic stream serialization, so the grid may be set up
@@ -21,6 +23,18 @@ inline int launch_kernel(void (*kern)(P...), dim3 grid, unsigned threads, size_t
   cfg.attrs = &attr;
   cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess ? 0 : -1;
+}
+
+// Allows a kernel its dynamic shared memory, once a device (a bit for each in the kernel's own word).
+template <auto KERN>
+inline bool allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (done.load(std::memory_order_acquire) >> dev & 1ull) return true;
+  if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(1ull << dev, std::memory_order_acq_rel);
+  return true;
 }
 
 }  // namespace sdpa
