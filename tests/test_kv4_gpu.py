@@ -306,6 +306,31 @@ def test_copy_pages():
     sdpa.attn_kv4_copy_pages(got, [], [])
 
 
+def test_pages_past_4_gb():
+    """Pages whose bytes lie past 2^32: append, gather, decode and copy address them."""
+    sdpa = _sdpa()
+    H, d, page, n_pages = 8, 128, 64, 62000  # 73,728 bytes a page: 4.57 GB
+    pool = sdpa.kv4_pool(n_pages, H, d, page)
+    lens = [130, 70]
+    gen = torch.Generator().manual_seed(15)
+    k, v = (torch.randn((200, H, d), generator=gen).to(torch.bfloat16) for _ in range(2))
+    table = _i32([[61999, 3, 60000], [59999, 61000, -1]])
+    sdpa.attn_kv4_append(k.cuda(), v.cuda(), _cu(lens), pool, table, _i32([0, 0]))
+    kk, vv = sdpa.kv4_gather(pool, table, _cu(lens), _i32([0, 0]), 200, d)
+    q = torch.randn((2, 1, 16, d), generator=gen).to(torch.bfloat16)
+    o, lse = sdpa.sdpa_decode_kv4(q.cuda(), pool, table, _i32(lens))
+    sdpa.attn_kv4_copy_pages(pool, [61999, 60000, 59999], [5, 61500, 61998])
+    moved = _i32([[5, 3, 61500], [61998, 61000, -1]])
+    o2, lse2 = sdpa.sdpa_decode_kv4(q.cuda(), pool, moved, _i32(lens))
+    _clean()
+    c = Cache.__new__(Cache)
+    c.lens, c.at = lens, np.array([0, 130, 200])
+    c.k, c.v = kv4.held(k.double().numpy()), kv4.held(v.double().numpy())
+    assert np.array_equal(kk.double().cpu().numpy(), c.k) and np.array_equal(vv.double().cpu().numpy(), c.v)
+    _check_decode(c, q, o, lse)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_refusals():
     sdpa = _sdpa()
     c = Cache([20], 2, 64, 16)
