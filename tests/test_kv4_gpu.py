@@ -353,6 +353,39 @@ def test_refusals():
                              softmax_offset=torch.zeros(3, device="cuda"))
 
 
+def test_calls_on_two_streams_at_once():
+    """Decodes and appends of two caches, many times over on two streams without waiting for each
+    other, give the bits of the same calls one at a time."""
+    sdpa = _sdpa()
+    caches = [Cache([900, 33, 2000], 2, 128, 64, seed=30), Cache([70, 1500, 5, 641], 2, 64, 16, seed=31)]
+    gen = torch.Generator().manual_seed(32)
+    qs = [torch.randn((len(c.lens), 1, 8, c.d), generator=gen).to(torch.bfloat16).cuda() for c in caches]
+    alone = [sdpa.sdpa_decode_kv4(q, c.pool, c.table, c.seq_lens) for q, c in zip(qs, caches)]
+    news = [(c.kt[:len(c.lens)].cuda(), c.vt[:len(c.lens)].cuda(), _cu([1] * len(c.lens)), c.seq_lens - 1) for c in caches]
+    _clean()
+    streams = [torch.cuda.Stream() for _ in caches]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    out = [[], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(caches, streams)):
+            with torch.cuda.stream(s):
+                out[i].append(sdpa.sdpa_decode_kv4(qs[i], c.pool, c.table, c.seq_lens))
+    for i, (c, s) in enumerate(zip(caches, streams)):  # and with new last tokens
+        k, v, cu, start = news[i]
+        sdpa.attn_kv4_append(k, v, cu, c.pool, c.table, start, stream=s)
+        out[i].append(sdpa.sdpa_decode_kv4(qs[i], c.pool, c.table, c.seq_lens, stream=s))
+    for s in streams:
+        s.synchronize()
+    _clean()
+    for i, c in enumerate(caches):
+        for o, lse in out[i][:-1]:
+            assert torch.equal(o, alone[i][0]) and torch.equal(lse, alone[i][1])
+        for b, end in enumerate(c.at[1:]):
+            c.k[end - 1], c.v[end - 1] = (kv4.held(t[b].double().cpu().numpy()) for t in news[i][:2])
+        _check_decode(c, qs[i], *out[i][-1])
+
+
 def test_serving_loop_captured_and_on_another_stream():
     """Prompts enter the cache, a request forks, and each step appends one token and attends: the
     steps run eagerly on a side stream and again as a captured graph, with the same bits."""

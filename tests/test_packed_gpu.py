@@ -331,6 +331,39 @@ def test_autograd_and_cross_offsets():
         assert torch.equal(leaf[n].grad, got[g]), n
 
 
+def test_calls_on_two_streams_at_once():
+    """Forward and backward of two packed batches, many times over on two streams without waiting
+    for each other, give the bits of the same calls one at a time."""
+    sdpa = _sdpa()
+    jobs = []
+    for lens, dims, seed in (([300, 41, 700], (128, 128), 41), ([64, 512, 1, 130], (64, 64), 42)):
+        x = _inputs(lens, lens, 4, 2, *dims, seed)
+        jobs.append(([x[n].cuda() for n in ("q", "k", "v", "dout")], x["off"].cuda(), _cu(lens)))
+
+    def step(job, stream=None):
+        (q, k, v, do), off, cu = job
+        kw = dict(softmax_type=LEARNABLE, softmax_offset=off, stream=stream)
+        o, lse = sdpa.sdpa_forward_packed(q, k, v, cu, **kw)
+        return (o, lse) + sdpa.sdpa_backward_packed(q, k, v, o, do, lse, cu, **kw)
+
+    alone = [step(j) for j in jobs]
+    _clean()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i].append(step(jobs[i], s))
+    for s in streams:
+        s.synchronize()
+    _clean()
+    for i in range(2):
+        for res in got[i]:
+            for a, b in zip(res, alone[i]):
+                assert torch.equal(a, b)
+
+
 def test_captured_graphs_and_another_stream():
     """Forward and backward captured twice, with workspaces of their own, replay on new offsets
     with the eager run's bits; and the eager run on a side stream has them too."""
