@@ -198,10 +198,11 @@ struct Kv4StoreParams {
 int launch_kv4_append(const Kv4StoreParams& p, cudaStream_t stream);
 int launch_kv4_gather(const Kv4StoreParams& p, cudaStream_t stream);
 
-// Page pairs of one copy launch, passed as kernel arguments.
-constexpr int kKv4PairsMax = 480;
+// Page pairs of one copy launch, passed as kernel arguments: few, or as many as fit (30 KB).
+constexpr int kKv4PairsFew = 60, kKv4PairsMax = 3840;
+template <int N>
 struct Kv4Pairs {
-  int2 at[kKv4PairsMax];  // source page, destination page
+  int2 at[N];  // source page, destination page
 };
 int launch_kv4_copy(uint8_t* pool, int n_layers, long long layer_bytes, long long page_bytes, const int* src,
                     const int* dst, int n, cudaStream_t stream);

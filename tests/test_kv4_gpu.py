@@ -287,7 +287,8 @@ def test_lengths_past_the_table_are_clamped():
 def test_copy_pages():
     sdpa = _sdpa()
     gen = torch.Generator().manual_seed(14)
-    for shape in ((40, 3, sdpa.kv4_block_bytes(16, 64)), (2, 1200, 1, sdpa.kv4_block_bytes(32, 128))):
+    for shape in ((40, 3, sdpa.kv4_block_bytes(16, 64)), (2, 1200, 1, sdpa.kv4_block_bytes(32, 128)),
+                  (9500, 1, sdpa.kv4_block_bytes(16, 64))):  # more pairs than one launch takes
         pool = torch.randint(0, 256, shape, generator=gen, dtype=torch.uint8)
         n_pages = shape[-3]
         perm = torch.randperm(n_pages, generator=gen)
