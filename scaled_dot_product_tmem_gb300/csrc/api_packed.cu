@@ -209,6 +209,9 @@ int attn_bwd_packed(const void* q, const void* k, const void* v, const void* o, 
   p.offset = softmax_offset;
   p.seq_q = nullptr;
   p.seq_kv = nullptr;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
   p.o = static_cast<const __nv_bfloat16*>(o);
   p.dout = static_cast<const __nv_bfloat16*>(dout);
   p.lse = lse;

@@ -112,6 +112,9 @@ struct BwdParams {
   // packed batch (B = 1, S_q / S_kv the rows of the packed tensors, S_pad the padded workspace
   // rows of one head): the plan's tile lists; with a learnable sink, the dQ kernel's two
   // fp32 row sums of dS, [2][H_q][S_pad]
+  const __nv_bfloat16* q = nullptr;  // [S_q, H_q, d_qk], for the preprocess
+  const __nv_bfloat16* k = nullptr;  // [S_kv, H_kv, d_qk]
+  const __nv_bfloat16* v = nullptr;  // [S_kv, H_kv, d_v]
   const PackedTile* tiles_kv = nullptr;
   const PackedTile* tiles_q = nullptr;
   const PackedCounts* counts = nullptr;

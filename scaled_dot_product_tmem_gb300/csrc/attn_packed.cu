@@ -231,9 +231,90 @@ int launch_attn_fwd_packed(int d_qk, int d_v, const CUtensorMap& tq, const CUten
 // Backward preprocess: D = rowsum(dO * O) and -LSE log2(e) in the workspace's padded rows (the
 // padding: D = 0, -inf), one block per 64 rows of a query tile and head; on request also
 // zeros in the gradient rows of no sequence.
+//
+// D enters dS = P (dP - D) with the rounding of the stored bf16 O, 2^-8 |O|.  Against |dP| that
+// falls with the number n of keys a row sees (O is a mean of n values), while the row's dS
+// (P is about 1 / n) grows: a sequence's first rows carry most of the error, and they are many
+// in a batch of short sequences.  The first kExactRows rows that see at most kExactRows keys
+// therefore get D from O summed anew in fp32.  (Eight sequences of 1 to 512 rows: dQ and dK off
+// by 0.0026 of their norm from the stored O; the two roundings that stay, of dS and of the
+// result, are 0.0024.)
 // =============================================================================
-template <int D_V>
-__global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams p, int d_qk) {
+constexpr int kExactRows = 16;
+
+// D of row i of the sequence from P and V in fp32, by TPR lanes (rows of one warp may see different
+// numbers n of keys, from key lo on).  do8: this lane's 8 dims of dO.
+template <int D_QK, int D_V>
+__device__ __forceinline__ float exact_d(const BwdParams& p, const PackedTile& e, int h, int i, int lo, int n,
+                                         const uint4& do8) {
+  constexpr int TPR = D_V / 8, NQ = D_QK / (4 * TPR);  // words of 4 dims a lane has of q and k
+  const int sub = threadIdx.x % TPR, hk = h / p.G;
+  const bool some = n > 0;
+  const size_t qrow = ((size_t)(e.q0 + (some ? i : 0)) * p.H_q + h) * D_QK;
+  float q[4 * NQ], o[8], nl = 0.f;
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    const uint2 w = some ? *reinterpret_cast<const uint2*>(p.q + qrow + (u * TPR + sub) * 4) : make_uint2(0u, 0u);
+    q[4 * u] = __uint_as_float(w.x << 16);
+    q[4 * u + 1] = __uint_as_float(w.x & 0xFFFF0000u);
+    q[4 * u + 2] = __uint_as_float(w.y << 16);
+    q[4 * u + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+  }
+  if (some) nl = -p.lse[(size_t)h * p.S_q + e.q0 + i] * kLog2e;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) o[x] = 0.f;
+  if (!__any_sync(0xffffffffu, some)) return 0.f;
+  // Keys past the row's last are loaded as its last and weigh nothing: no branch parts the loads.
+  // Four keys at a time: scores, their sums over the lanes, values.
+  const int most = __reduce_max_sync(0xffffffffu, n);
+#pragma unroll 1
+  for (int t0 = 0; t0 < most; t0 += 4) {
+    float s[4];
+    uint4 v8[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const size_t row = (size_t)(e.k0 + (some ? lo + min(t0 + t, n - 1) : 0)) * p.H_kv + hk;
+      v8[t] = __ldg(reinterpret_cast<const uint4*>(p.v + row * D_V + sub * 8));
+      s[t] = 0.f;
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.k + row * D_QK + (u * TPR + sub) * 4));
+        s[t] = fmaf(q[4 * u], __uint_as_float(w.x << 16), s[t]);
+        s[t] = fmaf(q[4 * u + 1], __uint_as_float(w.x & 0xFFFF0000u), s[t]);
+        s[t] = fmaf(q[4 * u + 2], __uint_as_float(w.y << 16), s[t]);
+        s[t] = fmaf(q[4 * u + 3], __uint_as_float(w.y & 0xFFFF0000u), s[t]);
+      }
+    }
+#pragma unroll
+    for (int off = TPR / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], off);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const bool see = t0 + t < n;
+      const float w = see ? ex2(fmaf(s[t], p.scale_log2, nl)) : 0.f;
+      const uint32_t ws[4] = {v8[t].x, v8[t].y, v8[t].z, v8[t].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        o[2 * x] = see ? fmaf(w, __uint_as_float(ws[x] << 16), o[2 * x]) : o[2 * x];
+        o[2 * x + 1] = see ? fmaf(w, __uint_as_float(ws[x] & 0xFFFF0000u), o[2 * x + 1]) : o[2 * x + 1];
+      }
+    }
+  }
+  const uint32_t gs[4] = {do8.x, do8.y, do8.z, do8.w};
+  float acc = 0.f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    acc = fmaf(o[2 * x], __uint_as_float(gs[x] << 16), acc);
+    acc = fmaf(o[2 * x + 1], __uint_as_float(gs[x] & 0xFFFF0000u), acc);
+  }
+#pragma unroll
+  for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  return acc;
+}
+
+template <int D_QK, int D_V>
+__global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams p) {
   constexpr int TPR = D_V / 8, RPP = 256 / TPR, TILE = 64, NR = TILE / RPP;
   __shared__ float dsum[TILE];
   const int h = blockIdx.y;
@@ -268,6 +349,17 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
       for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
       if (sub == 0) dsum[threadIdx.x / TPR + k * RPP] = acc;
     }
+    // the sequence's first rows: all in the first pass, RPP >= kExactRows rows of whole warps
+    static_assert(RPP >= kExactRows && kExactRows % (32 / TPR) == 0, "the exact rows are whole warps of one pass");
+    const int i = i0 + threadIdx.x / TPR;
+    if (i0 == 0 && i < kExactRows) {
+      int lo = 0, hi = -1;
+      visible_keys<true>(MaskSpec{e.Lq, e.Lk, p.causal, p.window}, i, &lo, &hi);
+      const int n = hi - lo + 1;
+      const bool few = n > 0 && n <= kExactRows;
+      const float d = exact_d<D_QK, D_V>(p, e, h, i, lo, few ? n : 0, g[0]);
+      if (few && sub == 0) dsum[i] = d;
+    }
     __syncthreads();
     if (threadIdx.x < TILE) {
       const int i = i0 + threadIdx.x;
@@ -288,10 +380,10 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
       for (size_t i = at; i < n; i += step) x16[i] = z;
     };
     const PackedCounts c = *p.counts;
-    clear(p.dq, 0, c.q_begin, p.H_q, d_qk);
-    clear(p.dq, c.q_end, p.S_q, p.H_q, d_qk);
-    clear(p.dk, 0, c.kv_begin, p.H_kv, d_qk);
-    clear(p.dk, c.kv_end, p.S_kv, p.H_kv, d_qk);
+    clear(p.dq, 0, c.q_begin, p.H_q, D_QK);
+    clear(p.dq, c.q_end, p.S_q, p.H_q, D_QK);
+    clear(p.dk, 0, c.kv_begin, p.H_kv, D_QK);
+    clear(p.dk, c.kv_end, p.S_kv, p.H_kv, D_QK);
     clear(p.dv, 0, c.kv_begin, p.H_kv, D_V);
     clear(p.dv, c.kv_end, p.S_kv, p.H_kv, D_V);
   }
@@ -300,8 +392,9 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
 int launch_packed_preprocess(int d_qk, int d_v, const BwdParams& p, cudaStream_t stream) {
   if (2 * p.tile_bound_q > 0x7fffffffLL) return -2;
   const dim3 grid((unsigned)(2 * p.tile_bound_q), p.H_q);
-  if (d_v == 64) return launch_kernel(packed_preprocess_kernel<64>, grid, 256, 0, stream, true, p, d_qk);
-  if (d_v == 128) return launch_kernel(packed_preprocess_kernel<128>, grid, 256, 0, stream, true, p, d_qk);
+  if (d_qk == 64 && d_v == 64) return launch_kernel(packed_preprocess_kernel<64, 64>, grid, 256, 0, stream, true, p);
+  if (d_qk == 128 && d_v == 128) return launch_kernel(packed_preprocess_kernel<128, 128>, grid, 256, 0, stream, true, p);
+  if (d_qk == 192 && d_v == 128) return launch_kernel(packed_preprocess_kernel<192, 128>, grid, 256, 0, stream, true, p);
   return -2;
 }
 
