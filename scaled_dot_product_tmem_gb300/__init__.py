@@ -13,6 +13,17 @@ and it raises if the library has not been built.
 
 Tensors are BSHD bf16 on the GPU: q [B,S_q,H_q,d_qk], k [B,S_kv,H_kv,d_qk],
 v [B,S_kv,H_kv,d_v]; lse fp32 [B,H_q,S_q]; softmax_offset fp32 [H_q].
+
+Sequences of different lengths without padding rows, [T,H,d] with int32 offsets:
+
+    o = attention_packed(q, k, v, cu_seqlens)
+
+Serving over a 4-bit paged cache: attn_kv4_append fills it, sdpa_decode_kv4 attends over it,
+attn_kv4_copy_pages forks and compacts it, kv4_gather reads it back:
+
+    pool = kv4_pool(n_pages, H_kv, d, page_size)
+    attn_kv4_append(k, v, cu_seqlens, pool, page_table, seq_lens)
+    o, lse = sdpa_decode_kv4(q, pool, page_table, seq_lens + 1)
 """
 from __future__ import annotations
 

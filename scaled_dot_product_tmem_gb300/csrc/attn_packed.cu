@@ -27,6 +27,8 @@ namespace sdpa {
 //   kv and q  whole sequences by length, a sequence's heaviest tiles first: the tiles in
 //             flight belong to few sequences, whose other operand they share in L2.
 // The order inside a bucket varies from run to run; no result depends on it.
+// Measured: about 4 us for 4 to 16 sequences (6.5 with 1024 threads and offsets in global memory),
+// most of it hidden behind the set-up of the kernel that follows.
 // =============================================================================
 // Latency is all that counts here (a few thousand numbers), so the block has 256 threads where
 // the sequences allow it (cheaper barriers), the offsets stay in shared memory, and the two lists

@@ -26,6 +26,11 @@
 //     second kernel joins in CTA order: bitwise reproducible.
 //   - A fifth warp walks the page table and streams units into a ring by bulk copies, four a
 //     page; each of the other four takes 32 tokens of every unit.
+//
+// Measured (d = 128, 8 kv heads): 329,377 tokens of 4 sequences with 8 query rows a kv head, 380 MB
+// of cache, 88 us (4.3 TB/s; the copies alone take 70, the arithmetic alone 84: the masks and
+// shifts of the decode keep the half-rate ALU pipe at 59 %); 42,031 tokens of 16 sequences,
+// 48 MB, 22 us, of which about 10 are the chain lengths - page - copy - products - join.
 #include <algorithm>
 #include <atomic>
 
