@@ -14,10 +14,11 @@
 //     query heads wastes little of it, and a decoded operand serves every column block.
 //     (A tcgen05 product wants 128 rows of decoded operand in shared memory or TMEM: writing
 //     them back costs more than the whole decode.)
-//   - A code pair is decoded by a mask (128 + c as bf16 bits) and one paired fma with the
-//     scale, (128 + c) s - 136 s = (c - 8) s: exact, since every intermediate has at most 8
-//     significant bits.  Which pairs of dims or tokens share a register is free as long as
-//     both operands of a product agree, so a lane's 16-byte load feeds its own fragments.
+//   - A code pair is decoded by a mask and one paired fma with the scale, as (c - 8) s 2^-23
+//     (kv4.cuh; the power of two is undone in the scores' scale and in the outputs): exact, and
+//     half of the codes need no shift.  Which pairs of dims or tokens share a register is free
+//     as long as both operands of a product agree, so a lane's 16-byte load feeds its own
+//     fragments.
 //   - The probabilities are rounded to bf16 (2^-8 relative) for P V; their sum is fp32.
 //   - Work is cut evenly over the CTAs of a persistent grid (units of 128 tokens of one
 //     sequence and kv head, in order, and one unit more for each such segment: its queries,
@@ -28,9 +29,9 @@
 //     page; each of the other four takes 32 tokens of every unit.
 //
 // Measured (d = 128, 8 kv heads): 329,377 tokens of 4 sequences with 8 query rows a kv head, 380 MB
-// of cache, 88 us (4.3 TB/s; the copies alone take 70, the arithmetic alone 84: the masks and
-// shifts of the decode keep the half-rate ALU pipe at 59 %); 42,031 tokens of 16 sequences,
-// 48 MB, 22 us, of which about 10 are the chain lengths - page - copy - products - join.
+// of cache, 80 us (4.7 TB/s; the copies alone take 70; 88 with an exponent set in every code and
+// a shift for three of four); 42,031 tokens of 16 sequences, 48 MB, 21 us, of which about 10 are
+// the chain lengths - page - copy - products - join.
 #include <algorithm>
 #include <atomic>
 
@@ -86,7 +87,7 @@ __device__ __forceinline__ Kv4Sums kv4_finish(const Kv4DecodeParams& p, int h, f
   if (mm == -INFINITY) return l == l ? Kv4Sums{0.f, -INFINITY} : Kv4Sums{l, l};  // no key (l is 0) or a NaN
   const float f = m == -INFINITY ? 0.f : ex2(m - mm);
   const float den = l * f + (sink == -INFINITY ? 0.f : ex2(sink - mm));
-  return Kv4Sums{f / den, (mm + lg2(den)) * kLn2};
+  return Kv4Sums{f / den * kKv4SmallUndo, (mm + lg2(den)) * kLn2};
 }
 
 // The keys of one unit row and the sizes of one sequence.
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
   // token pairs u = 4 n + t of this warp's tokens: the slot permutation depends on t alone
   const int off_v = C::S_V + (warp * (kSub / 2) + t) * D + (g ^ kv4_slot_xor(t, D)) * (D / 8);
   const int off_sv = C::S_SV + (warp * (kSub / 2) + t) * (D / 8) + 2 * (D == 128 ? g : g / 2);
+  const float sl2 = p.scale_log2 * kKv4SmallUndo;
   int i = 0;  // units consumed
   bool ok = true;
   for (bool at_begin = true;; at_begin = false) {
@@ -424,9 +426,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
             uint32_t a[2][4];
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-              const uint32_t s2 = __byte_perm(sk[sub][f], 0u, j < 2 ? 0x1010 : 0x3232), c2 = bf2_mul(s2, kM136);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) a[f][e] = decode_pair(wk[sub][f][j] >> (4 * e), s2, c2);
+              const Kv4Small k2 = small_scales(__byte_perm(sk[sub][f], 0u, j < 2 ? 0x1010 : 0x3232));
+              const uint32_t w = wk[sub][f][j], w8 = w >> 8;
+              a[f][0] = decode_small_lo(w, k2);
+              a[f][1] = decode_small_hi(w, k2);
+              a[f][2] = decode_small_lo(w8, k2);
+              a[f][3] = decode_small_hi(w8, k2);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mx[nt][e] = p.scale_log2 * fmaxf(fmax3(s[0][nt][e], s[0][nt][e + 2], s[1][nt][e]), s[1][nt][e + 2]);
+            mx[nt][e] = sl2 * fmaxf(fmax3(s[0][nt][e], s[0][nt][e + 2], s[1][nt][e]), s[1][nt][e + 2]);
             grow |= mx[nt][e] > m[nt][e] + 8.f;
           }
         if (__any_sync(0xffffffffu, grow)) {
@@ -498,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
           for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-              const float x0 = ex2(fmaf(s[sub][nt][2 * f], p.scale_log2, m0));
-              const float x1 = ex2(fmaf(s[sub][nt][2 * f + 1], p.scale_log2, m1));
+              const float x0 = ex2(fmaf(s[sub][nt][2 * f], sl2, m0));
+              const float x1 = ex2(fmaf(s[sub][nt][2 * f + 1], sl2, m1));
               l[nt][0] += x0;
               l[nt][1] += x1;
               pb[sub][nt][f] = transpose_8x8(pack_bf16x2(x0, x1));
@@ -508,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
         // ---- outputs: lane (g, t) decodes eighth g of the head dim of token pairs t and t + 4
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-          uint32_t lo[2][MT / 4], hi[2][MT / 4], sv[2], cv[2];  // [pair][word]: both tokens' nibbles
+          uint32_t lo[2][MT / 4], hi[2][MT / 4];  // [pair][word]: both tokens' nibbles 0-3, 4-7
+          Kv4Small kv[2];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int u = 8 * sub + 4 * f;  // (+ t)
@@ -530,8 +536,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
               if (j > len - 1 || j < lo_min) two &= 0xFF00u;
               if (j + 1 > len - 1 || j + 1 < lo_min) two &= 0x00FFu;
             }
-            sv[f] = scale_pair(two);
-            cv[f] = bf2_mul(sv[f], kM136);
+            kv[f] = small_scales(scale_pair(two));
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -539,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
             uint32_t a[4];
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-              if constexpr (D == 128) {
-                a[2 * f] = decode_pair((mt < 4 ? lo[f][0] : hi[f][0]) >> (4 * (mt % 4)), sv[f], cv[f]);
-                a[2 * f + 1] = decode_pair((mt < 4 ? lo[f][1] : hi[f][1]) >> (4 * (mt % 4)), sv[f], cv[f]);
-              } else {
-                a[2 * f] = decode_pair(lo[f][0] >> (4 * mt), sv[f], cv[f]);
-                a[2 * f + 1] = decode_pair(hi[f][0] >> (4 * mt), sv[f], cv[f]);
+              const int e = mt % 4;  // nibble of the half
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t* half = D == 128 ? (mt < 4 ? lo[f] : hi[f]) + (r * MT / 8) : r == 0 ? lo[f] : hi[f];
+                const uint32_t w = *half >> (e < 2 ? 0 : 8);
+                a[2 * f + r] = e % 2 == 0 ? decode_small_lo(w, kv[f]) : decode_small_hi(w, kv[f]);
               }
             }
 #pragma unroll
