@@ -870,10 +870,10 @@ __global__ void __launch_bounds__(352, 1)
   // and numbers the kv tiles of all of them in one sequence n (stages, barrier phases).
   const int n_qt = (p.S_q + C::BM - 1) / C::BM;
   const int n_gr = p.H_q * p.B;
-  const int n_tiles = PK ? p.counts->q_tiles * p.H_q : n_qt * n_gr;
+  const int n_tiles = PK ? __ldcg(&p.counts->q_tiles) * p.H_q : n_qt * n_gr;
   // Packed: this kernel is launched behind the kv kernel and may start in its tail; all it needs was
-  // there before that one's blocks let it start.  Every block waits for the kv kernel at its end,
-  // so that what follows on the stream finds both done.
+  // there before that one's blocks let it start, and it reads that from L2.  Every block waits for
+  // the kv kernel at its end, so that what follows on the stream finds both done.
   if (PK && (int)blockIdx.x >= n_tiles) {  // the grid is the host's bound on the tiles
     grid_wait();
     return;
@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(352, 1)
   auto tile_of = [&](int ti) {
     Tile t;
     if constexpr (PK) {  // the plan lists the query tiles; heads innermost
-      const PackedTile e = load_packed_tile(p.tiles_q, ti / p.H_q);
+      const PackedTile e = load_packed_tile<true>(p.tiles_q, ti / p.H_q);
       t.b = 0;
       t.h = ti % p.H_q;
       t.hk = t.h / p.G;
@@ -1183,8 +1183,8 @@ __global__ void __launch_bounds__(352, 1)
     [[maybe_unused]] uint64_t rs2 = 0ull;  // ROWSUM: this row's sum of dS over its 64-key halves, paired
     if (i < (PK ? t.mask.S_q : p.S_q) && t.nj > 0) {
       const size_t ri = ((size_t)b * p.H_q + h) * p.S_pad + t.wr + i;
-      nl2row = p.nlse2[ri];
-      drow = p.Dsum[ri];
+      nl2row = PK ? __ldcg(p.nlse2 + ri) : p.nlse2[ri];
+      drow = PK ? __ldcg(p.Dsum + ri) : p.Dsum[ri];
     }
     // bias: this row of the bias plane (rows past S_q read row S_q - 1; their P is 0)
     [[maybe_unused]] const __nv_bfloat16* brow =

@@ -107,9 +107,11 @@ struct PackedTile {
 };
 static_assert(sizeof(PackedTile) == 32, "read as two 16-byte words");
 
+// L2: past the SM's own cache, for a kernel that relies on an earlier one without waiting for it.
+template <bool L2 = false>
 __device__ __forceinline__ PackedTile load_packed_tile(const PackedTile* t, int i) {
   const int4* w = reinterpret_cast<const int4*>(t + i);
-  const int4 a = __ldg(w), b = __ldg(w + 1);
+  const int4 a = L2 ? __ldcg(w) : __ldg(w), b = L2 ? __ldcg(w + 1) : __ldg(w + 1);
   return PackedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
