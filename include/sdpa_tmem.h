@@ -440,7 +440,8 @@ int attn_bwd_fp8(const void* q8, const void* k8, const void* v8, const void* do8
  *   page_size]) are in the cache.  Query s sits at pos = seq_lens[b] - S_q + s and sees the
  *   keys j <= pos, and j >= pos - window when window >= 0.  o bf16 [B, S_q, H_q, d]; lse
  *   fp32 [B, H_q, S_q] (may be NULL).  A query that sees no key gets o = 0 and lse = the
- *   sink logit.  scale, window, softmax_type and softmax_offset as for attn_fwd.
+ *   sink logit.  scale, window, softmax_type and softmax_offset as for attn_fwd
+ *   (ATTN_ERR_UNSUPPORTED for a finite scale above 1e30).
  *   workspace: device scratch of attn_kv4_decode_workspace_size() bytes, 256-byte aligned,
  *   not shared with a call that may run at the same time.  Bitwise reproducible.
  * attn_kv4_copy_pages: page dst[i] = page src[i] for i < n, in each of n_layers pools that

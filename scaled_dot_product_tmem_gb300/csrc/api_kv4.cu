@@ -121,6 +121,8 @@ int attn_kv4_decode(const void* q, const void* pool, const int* page_table, cons
   st = sdpa::check_common(B, S_q, 0, H_q, H_kv, d, d, 1, window, softmax_type, softmax_offset);
   if (st != ATTN_OK) return st;
   if ((long long)B * S_q * H_q > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  // (the kernel multiplies scores held as 2^-23 of their value by scale 2^23 log2(e))
+  if (sdpa::resolve_scale(scale, d) > 1e30f) return ATTN_ERR_UNSUPPORTED;
   if (B == 0 || S_q == 0) return ATTN_OK;
   if (!q || !o || !seq_lens || (max_pages > 0 && (!pool || !page_table))) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(pool, 16) || !aligned(lse, 4) || !aligned(page_table, 4) ||

@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     // keys that every row sees: [lo_max, hi_min]; that some row sees: [lo_min, len - 1]
     const int hi_min = len - p.S_q + r0 / G;
     const int lo_max = p.window >= 0 ? len - 1 - p.window : 0;
-    const int lo_min = p.window >= 0 ? len - p.S_q - p.window : 0;
+    const int lo_min = p.window >= 0 && len - p.S_q > p.window ? len - p.S_q - p.window : 0;
     float acc[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int pos = len - p.S_q + min(r0 + 8 * nt + 2 * t + e, R - 1) / G;
-              const int lo = p.window >= 0 ? pos - p.window : 0;
+              const int lo = p.window >= 0 && pos > p.window ? pos - p.window : 0;
 #pragma unroll
               for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
@@ -751,7 +751,7 @@ int launch_t(const Kv4DecodeParams& p, float* partial, cudaStream_t stream) {
   const int rows = p.H_q / p.c.H_kv * p.S_q, blocks = (rows + C::ROWS - 1) / C::ROWS;
   const long long join = (long long)p.B * p.c.H_kv * blocks;
   if (join > 0x7fffffffLL) return -2;
-  kern<<<grid, kThreads, C::SMEM, stream>>>(p, blocks, partial);
+  if (launch_kernel(kern, dim3((unsigned)grid), kThreads, C::SMEM, stream, false, p, blocks, partial) != 0) return -1;
   return launch_kernel(kv4_join_kernel<D>, dim3((unsigned)join, std::min(rows, C::ROWS)), 256, 0, stream, true, p, blocks,
                        (int)C::ROWS, grid, (const float*)partial);
 }

@@ -232,6 +232,40 @@ def test_decode_scale_large_scores_and_no_lse():
         assert np.all(np.abs(lse[b].double().cpu().numpy() - rl) <= 2.0 ** -17 * mag + 2.0 ** -18 * (1 + np.abs(rl)))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_over_the_whole_range_of_scales(d):
+    """Groups of 16 dims with scales from a few 2^-17 to tens of thousands side by side."""
+    sdpa = _sdpa()
+    gen, L, page = torch.Generator().manual_seed(8), 150, 32
+    k = torch.randn((L, 1, d), generator=gen)
+    k[..., :32] *= 2.0 ** -14
+    v = torch.randn((L, 1, d), generator=gen) * torch.logspace(-14, 16, d // 16, base=2.0).repeat_interleave(16)
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    c = Cache([L], 1, d, page)
+    sdpa.attn_kv4_append(k.cuda(), v.cuda(), _cu([L]), c.pool, c.table, _i32([0]))
+    c.k, c.v = kv4.held(k.double().numpy()), kv4.held(v.double().numpy())
+    assert 0 < np.abs(c.v[..., :16]).max() < 2.0 ** -11 and np.abs(c.v[..., -16:]).max() >= 2.0 ** 17
+    assert np.abs(c.k[..., :32]).max() > 0
+    q = torch.randn((1, 1, 4, d), generator=gen).to(torch.bfloat16)
+    q[..., :32] *= 2.0 ** 14
+    o, lse = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, c.table, c.seq_lens)
+    _clean()
+    _check_decode(c, q, o, lse)
+
+
+def test_decode_window_and_queries_past_32_bits_together():
+    """A table of 2^31 - 128 tokens, a window of nearly all of them and more queries than tokens:
+    the window's first key lies below -2^31."""
+    sdpa = _sdpa()
+    c = Cache([1, 130], 1, 64, 128)
+    table = torch.full((2, 2 ** 24 - 1), -1, dtype=torch.int32, device="cuda")
+    table[:, :2] = c.table
+    q = torch.randn((2, 200, 4, 64), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    o, lse = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, table, c.seq_lens, window=2 ** 31 - 130)
+    _clean()
+    _check_decode(c, q, o, lse)
+
+
 def test_decode_nan_reaches_its_own_head_and_entry_only():
     sdpa = _sdpa()
     c = Cache([40, 40], 2, 64, 16, seed=8)

@@ -129,6 +129,16 @@ def test_decode_validation(lib):
     assert dec(B=0) == OK and dec(S=0) == OK
 
 
+def test_decode_refuses_scales_past_1e30(lib):
+    def dec(scale, B):
+        return lib.attn_kv4_decode(P, P, P, P, P, None, B, 1, 8, 2, 128, 4, 16, 3, ctypes.c_float(scale), -1, 0, None,
+                                   None, ctypes.c_size_t(0), None)
+
+    assert dec(1.5e30, 2) == UNSUPPORTED and dec(3e38, 0) == UNSUPPORTED
+    assert dec(1e30, 0) == OK and dec(float("inf"), 0) == OK and dec(-1.0, 0) == OK  # (not positive and finite: 1/sqrt(d))
+    assert dec(1e30, 2) == WORKSPACE
+
+
 def test_copy_pages_validation(lib):
     def cp(src, dst, n_pages=8, layers=1, byts=64, pool=P):
         a = (ctypes.c_int * max(len(src), 1))(*src)
