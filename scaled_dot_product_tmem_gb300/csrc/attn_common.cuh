@@ -124,6 +124,45 @@ struct PackedCounts {
   int unused;
 };
 
+// A small packed batch needs no plan kernel: every CTA finds its one tile itself.
+constexpr int kOwnSeqs = 31;  // one lane an offset
+struct PackedOffsets {
+  const int* cu_q = nullptr;
+  const int* cu_kv = nullptr;
+  int B = 0, T_q = 0, T_kv = 0;
+};
+struct OwnTile {
+  PackedTile e;
+  int n, q_begin, q_end, unused;  // tiles of the batch; the sequences' rows
+};
+// Tile i of ROWS query rows, in the order of the sequences (a warp).
+template <int ROWS>
+__device__ __forceinline__ void find_own_tile(const PackedOffsets& c, int i, OwnTile* out) {
+  const int lane = threadIdx.x % 32;
+  const bool same = c.cu_kv == c.cu_q && c.T_kv == c.T_q;
+  int q = lane <= c.B ? min(max(__ldg(c.cu_q + lane), 0), c.T_q) : 0;
+  int k = lane <= c.B && !same ? min(max(__ldg(c.cu_kv + lane), 0), c.T_kv) : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {  // running maxima (below `off` a lane gets its own value)
+    q = max(q, __shfl_up_sync(0xffffffffu, q, off));
+    k = max(k, __shfl_up_sync(0xffffffffu, k, off));
+  }
+  if (same) k = q;
+  const int Lq = __shfl_down_sync(0xffffffffu, q, 1) - q, Lk = __shfl_down_sync(0xffffffffu, k, 1) - k;
+  const int n = lane < c.B ? (Lq + ROWS - 1) / ROWS : 0;
+  int upto = n;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += o;
+  }
+  const int j = i - (upto - n);
+  if (j >= 0 && j < n) out->e = PackedTile{q, Lq, k, Lk, lane, j * ROWS, 0, 0};
+  if (lane == 31) out->n = upto;
+  if (lane == 0) out->q_begin = q;
+  if (lane == c.B) out->q_end = q;
+}
+
 // Zero rows [from, rows) of `chunks` shared-memory chunks of rows x 128 bytes (a warp).  Whole
 // 128-byte rows: the swizzle permutes bytes inside a row only.
 __device__ __forceinline__ void zero_tile_rows(uint8_t* base, int chunks, int chunk_bytes, int rows, int from,

@@ -58,7 +58,7 @@ namespace sdpa {
 // BT: the bias tiles of the two query tiles are staged in shared memory by TMA.
 // OS: the output leaves through shared memory (4 KB a softmax warp), so that a warp stores whole
 // 128-byte lines.
-template <int D_QK, int D_V, int NK, int NV, bool F8 = false, bool BT = false, bool OS = false>
+template <int D_QK, int D_V, int NK, int NV, bool F8 = false, bool BT = false, bool OS = false, bool PK = false>
 struct FwdCfg {
   static constexpr int BM = 128, BN = 128;
   // bf16: boxes of 64 head dims (one 128-byte swizzle row each); E4M3: one box of
@@ -82,7 +82,8 @@ struct FwdCfg {
   // q_empty, then (BT) b_full[2], b_empty[2]
   static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + (BT ? 4 : 0);
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM_USED = OFF_TMEM_SLOT + 16 + 1024;
+  static constexpr int OFF_OWN = OFF_TMEM_SLOT + 16;  // packed: the tile a CTA found itself
+  static constexpr int SMEM_USED = OFF_OWN + (PK ? (int)sizeof(OwnTile) : 0) + 1024;
   // at least 117 KB so that one CTA per SM holds the 512 TMEM columns
   static constexpr int SMEM = SMEM_USED > 117 * 1024 ? SMEM_USED : 117 * 1024;
   static constexpr int THREADS = 320;
@@ -101,11 +102,13 @@ struct FwdTile {
   MaskSpec mask;  // with the entry's own lengths
 };
 
-template <int BM, int BN, bool VL, bool PK = false>
-__device__ __forceinline__ FwdTile fwd_tile(const FwdParams& p, int nqb, int wi) {
+template <int BM, int BN, bool VL, bool PK = false, bool OWN = false>
+__device__ __forceinline__ FwdTile fwd_tile(const FwdParams& p, int nqb, int wi, const OwnTile* own) {
   FwdTile T;
   if constexpr (PK) {  // the plan lists the tiles, most work first; every head takes each
-    const PackedTile e = load_packed_tile(p.tiles, wi / p.H_q);
+    PackedTile e;
+    if constexpr (OWN) e = own->e;
+    else e = load_packed_tile(p.tiles, wi / p.H_q);
     T.h = wi % p.H_q;
     T.b = 0;
     T.m0 = e.m0;
@@ -151,16 +154,17 @@ template <int D_QK, bool PK>
 constexpr bool fwd_out_staged() { return PK && D_QK <= 128; }
 
 template <int D_QK, int D_V, int NK, int NV, bool VL, bool F8 = false, bool BIAS = false, bool DROP = false,
-          bool PK = false>
+          bool PK = false, bool OWN = false>
 __global__ void __launch_bounds__(320, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmB,
                     const FwdParams p) {
   constexpr bool BT = fwd_bias_staged<D_QK, BIAS>();
   constexpr bool OS = fwd_out_staged<D_QK, PK>();
-  using C = FwdCfg<D_QK, D_V, NK, NV, F8, BT, OS>;
+  using C = FwdCfg<D_QK, D_V, NK, NV, F8, BT, OS, PK>;
   static_assert(!DROP || (!F8 && !BIAS && !VL), "dropout: full-length bf16 batches without a bias");
   static_assert(!PK || (VL && !F8 && !BIAS && !DROP), "packed: the bf16 form with per-sequence lengths");
+  static_assert(PK || !OWN, "OWN: a packed batch of at most one tile a CTA");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -210,12 +214,17 @@ __global__ void __launch_bounds__(320, 1)
     tmem_alloc<512>(tmem_slot);
     tmem_relinquish();
   }
+  [[maybe_unused]] OwnTile* own = reinterpret_cast<OwnTile*>(smem + C::OFF_OWN);
+  if constexpr (OWN)
+    if (warp == 9) find_own_tile<2 * C::BM>(p.own, blockIdx.x / p.H_q, own);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int* err = p.err;
-  if constexpr (PK) {  // set up while the plan was made
+  if constexpr (OWN) {
+    n_work = own->n * p.H_q;
+  } else if constexpr (PK) {  // set up while the plan was made
     grid_wait();
     n_work = p.counts->fwd_tiles * p.H_q;
   }
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(320, 1)
       [[maybe_unused]] int nb[2] = {0, 0};  // bias tiles loaded per query tile
       bool ok = true;
       for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-        const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi);
+        const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK, OWN>(p, nqb, wi, own);
         if (!T.any) continue;
         // Q of the previous tile must have been read by that tile's last S MMAs
         if (nw > 0) ok = wait(q_empty, (nw - 1) & 1, kSiteQ);
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(320, 1)
     int pc[2] = {0, 0};     // p_ready phases consumed per query tile
     bool ok = true, issued = false;
     for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi);
+      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK, OWN>(p, nqb, wi, own);
       if (!T.any) continue;
       issued = true;
       ok = mbar_wait_warp(q_full, nw & 1, err, kSiteQ);
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(320, 1)
     [[maybe_unused]] const uint8_t* btile = smem + C::OFF_B + t * C::B_TILE + r * 128;  // this row, first box
     bool ok = true;
     for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi);
+      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK, OWN>(p, nqb, wi, own);
       // this warpgroup's query tile, selected without a run-time index into T (which
       // would move T to local memory)
       const bool my_exists = t ? T.exists[1] : T.exists[0];
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(320, 1)
     }
     if constexpr (PK) {
       if (p.zero_rest) {  // rows of no sequence: o = 0, lse = -inf
-        const PackedCounts c = *p.counts;
+        const int q_begin = OWN ? own->q_begin : p.counts->q_begin, q_end = OWN ? own->q_end : p.counts->q_end;
         const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x, step = (size_t)gridDim.x * 256;
         auto clear = [&](int from, int to) {
           uint4* o16 = reinterpret_cast<uint4*>(p.o + (size_t)from * p.H_q * D_V);
@@ -708,8 +717,8 @@ __global__ void __launch_bounds__(320, 1)
           for (size_t e = at; e < n16; e += step) o16[e] = make_uint4(0u, 0u, 0u, 0u);
           for (size_t e = at; e < rows * p.H_q; e += step) p.lse[(e / rows) * p.S_q + from + e % rows] = -INFINITY;
         };
-        clear(0, c.q_begin);
-        clear(c.q_end, p.S_q);
+        clear(0, q_begin);
+        clear(q_end, p.S_q);
       }
     }
   }
@@ -724,14 +733,14 @@ __global__ void __launch_bounds__(320, 1)
 }
 
 template <int D_QK, int D_V, int NK, int NV, bool VL, bool F8 = false, bool BIAS = false, bool DROP = false,
-          bool PK = false>
+          bool PK = false, bool OWN = false>
 inline int launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams& p,
                         cudaStream_t stream, const CUtensorMap* tb = nullptr) {
-  using C = FwdCfg<D_QK, D_V, NK, NV, F8, fwd_bias_staged<D_QK, BIAS>(), fwd_out_staged<D_QK, PK>()>;
-  auto kern = attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP, PK>;
+  using C = FwdCfg<D_QK, D_V, NK, NV, F8, fwd_bias_staged<D_QK, BIAS>(), fwd_out_staged<D_QK, PK>(), PK>;
+  auto kern = attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP, PK, OWN>;
   static bool attr_set = false;
   if constexpr (PK) {
-    if (!allow_smem<attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP, PK>>(C::SMEM)) return -1;
+    if (!allow_smem<attn_fwd_kernel<D_QK, D_V, NK, NV, VL, F8, BIAS, DROP, PK, OWN>>(C::SMEM)) return -1;
   } else if (!attr_set) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
     attr_set = true;
@@ -748,6 +757,7 @@ inline int launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   const long long n_work =
       PK ? p.tile_bound * p.H_q : (long long)((p.S_q + 2 * C::BM - 1) / (2 * C::BM)) * p.H_q * p.B;
   const unsigned grid = (unsigned)(n_work < n_sm ? n_work : n_sm);
+  if constexpr (OWN) return launch_kernel(kern, dim3((unsigned)n_work), C::THREADS, C::SMEM, stream, false, tq, tk, tv, tq, p);
   if constexpr (PK) return launch_kernel(kern, dim3(grid), C::THREADS, C::SMEM, stream, true, tq, tk, tv, tq, p);
   kern<<<grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tb ? *tb : tq, p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;

@@ -40,6 +40,7 @@ struct FwdParams {
   const PackedCounts* counts = nullptr;
   long long tile_bound = 0;  // the list has at most this many tiles (the host's bound)
   int zero_rest = 0;
+  PackedOffsets own;  // tiles null: a small batch, whose CTAs find their tiles themselves
 };
 
 // Returns 0 on a successful launch, -2 for an unsupported (d_qk, d_v), -1 on a

@@ -1,4 +1,5 @@
-// attn_packed.cu -- attention over packed sequences: the plan kernel that lists the work tiles,
+// attn_packed.cu -- attention over packed sequences: the plan kernel that lists the work tiles
+// (a small forward does without: find_own_tile in attn_common.cuh),
 // the packed instantiations of the forward and of the deterministic backward kernels, and
 // the backward's small kernels in their packed form.
 //
@@ -219,14 +220,22 @@ int launch_packed_plan(const PackedPlanParams& p, cudaStream_t stream) {
 // =============================================================================
 // Forward
 // =============================================================================
+template <bool OWN>
+static int launch_fwd_packed_t(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const FwdParams& p, cudaStream_t stream) {
+  if (d_qk == 128 && d_v == 128)
+    return launch_fwd_t<128, 128, 2, 2, true, false, false, false, true, OWN>(tq, tk, tv, p, stream);
+  if (d_qk == 64 && d_v == 64)
+    return launch_fwd_t<64, 64, 4, 4, true, false, false, false, true, OWN>(tq, tk, tv, p, stream);
+  if (d_qk == 192 && d_v == 128)
+    return launch_fwd_t<192, 128, 2, 1, true, false, false, false, true, OWN>(tq, tk, tv, p, stream);
+  return -2;
+}
+
 int launch_attn_fwd_packed(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const FwdParams& p, cudaStream_t stream) {
-  if (d_qk == 128 && d_v == 128)
-    return launch_fwd_t<128, 128, 2, 2, true, false, false, false, true>(tq, tk, tv, p, stream);
-  if (d_qk == 64 && d_v == 64) return launch_fwd_t<64, 64, 4, 4, true, false, false, false, true>(tq, tk, tv, p, stream);
-  if (d_qk == 192 && d_v == 128)
-    return launch_fwd_t<192, 128, 2, 1, true, false, false, false, true>(tq, tk, tv, p, stream);
-  return -2;
+  return p.tiles ? launch_fwd_packed_t<false>(d_qk, d_v, tq, tk, tv, p, stream)
+                 : launch_fwd_packed_t<true>(d_qk, d_v, tq, tk, tv, p, stream);
 }
 
 // =============================================================================

@@ -238,6 +238,31 @@ def test_offsets_that_are_not_offsets_are_clamped():
         assert torch.equal(a[n], b[n]), n
 
 
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("raw", [[0, 300, 300, 557, 558], [7, 100, 40, 612, 9999, 3], [-5, 0, 0, 640]])
+def test_forward_with_and_without_a_plan_kernel(dims, raw):
+    """A batch small enough for its blocks to find their tiles themselves, and the same one with
+    empty sequences behind it until a plan kernel has to list them: every bit the same, rows of
+    no sequence included; so with offsets of the keys' own."""
+    sdpa = _sdpa()
+    T, H, H_kv = 640, 4, 2
+    x = _inputs([T], [T], H, H_kv, *dims, 5)
+    q, k, v = (x[n].cuda() for n in "qkv")
+    kv = [0] + [(3 * c) // 4 for c in raw[1:]]
+    for cu_kv in (None, kv):
+        for kw in (dict(window=70), dict(causal=False, softmax_type=OFF_BY_ONE)):
+            many = lambda c: None if c is None else _i32(c + [c[-1]] * 40)
+            few = lambda c: None if c is None else _i32(c)
+            a = sdpa.sdpa_forward_packed(q, k, v, few(raw), few(cu_kv), **kw)
+            b = sdpa.sdpa_forward_packed(q, k, v, many(raw), many(cu_kv), **kw)
+            _clean()
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), (cu_kv, kw)
+    lens = [0] * 30 + [T]  # the most sequences that need no plan kernel, and one more
+    a, b = (sdpa.sdpa_forward_packed(q, k, v, _cu(n)) for n in (lens, [0] + lens))
+    _clean()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_more_sequences_than_plan_threads_and_a_long_one():
     """3,000 short sequences around one of 5,000 rows; a sample of them against the oracle."""
     g = np.random.default_rng(1)
