@@ -1,6 +1,6 @@
 // kv4_store.cu -- filling, reading and copying the 4-bit paged key/value cache (layout and
 // number format in kv4.cuh).  Each kernel moves each byte once.  Measured with 8 heads of 128:
-// 15,677 tokens appended in 18 us (83 MB; 60 % of the issue slots, the rounding of 32 M values) and
+// 15,677 tokens appended in 16 us (83 MB; 18 us without the loads ahead of the lookup) and
 // read back in 14 us; 1500 pages of 64 tokens copied in 4 layers in 134 us (885 MB moved,
 // 6.6 TB/s); one token of each of 64 sequences appended or read back in about 3 us (lookups).
 #include "attn_kernels.h"
@@ -60,11 +60,13 @@ __device__ __forceinline__ void find_tokens(const Kv4StoreParams& p, int t0, Tok
   __syncthreads();
 }
 
-// 16 values to codes and a scale byte.  c = round(x / s) without a division: y = x (1/s) is off
-// by 2^-22 or so, ties x / s = k + 1/2 are exact numbers, and any other x / s is at least 2^-9
-// away from a tie (x has 8 significant bits, s has 4), so y rounded to multiples of 2^-12
-// falls on the same side as x / s, and ties on themselves; the second rounding is then the
-// definition's.
+// 16 values to codes and a scale byte.  c = round(x / s) without a division: x (1/s) is off by
+// 2^-22 or so, ties x / s = k + 1/2 are exact numbers, and any other x / s is at least 2^-9
+// away from a tie (x has 8 significant bits, s has 4), so one fma that rounds x (1/s) to multiples
+// of 2^-12 (by adding 3 * 2^10) falls on the same side as x / s, and ties on themselves; the
+// second rounding, to whole numbers (by going on to 3 * 2^22), is then the definition's.  The
+// bits of those sums are whole numbers with an offset, so a word of 8 codes is their sum with
+// weights 16^i and one constant for all offsets.
 __device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint32_t (&c)[2]) {
   const uint32_t ws[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
   uint32_t mx = 0u;  // largest magnitudes of both halves: bf16 bits order as the numbers do
@@ -80,32 +82,32 @@ __device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint
   const bool far = sb < 8 || sb == 0xF7;
   const float inv = __frcp_rn(kv4_scale_value(sb));
   const uint64_t inv2 = f2_pack(inv, inv);
-  constexpr float kGrid = 1.5f * 2048.f, kInt = 1.5f * 8388608.f;  // adding it rounds to 2^-12, to whole numbers
-  const uint64_t up = f2_pack(kGrid, kGrid), down = f2_pack(-kGrid, -kGrid), whole = f2_pack(kInt, kInt);
+  constexpr float kGrid = 1.5f * 2048.f, kInt = 1.5f * 8388608.f;
+  const uint64_t grid = f2_pack(kGrid, kGrid), whole = f2_pack(kInt - kGrid, kInt - kGrid);
   uint64_t y[8];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    y[q] = f2_mul(f2_pack(__uint_as_float(ws[q] << 16), __uint_as_float(ws[q] & 0xFFFF0000u)), inv2);
-    y[q] = f2_add(f2_add(y[q], up), down);
-  }
+  for (int q = 0; q < 8; ++q)
+    y[q] = f2_fma(f2_pack(__uint_as_float(ws[q] << 16), __uint_as_float(ws[q] & 0xFFFF0000u)), inv2, grid);
   if (far) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       float a, b;
       f2_unpack(y[q], a, b);
-      y[q] = f2_pack(fminf(fmaxf(a, -8.f), 7.f), fminf(fmaxf(b, -8.f), 7.f));
+      y[q] = f2_pack(fminf(fmaxf(a, kGrid - 8.f), kGrid + 7.f), fminf(fmaxf(b, kGrid - 8.f), kGrid + 7.f));
     }
   }
+  constexpr uint32_t kOffset = 0x4B400000u - 8u;  // bits of kInt, and code 8 for 0
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float a, b;
-    f2_unpack(f2_add(y[q], whole), a, b);  // the low bits are the whole number
-    // the low nibbles side by side: bits above them fall to the mask or to the next shift
-    const uint32_t two = (__float_as_uint(a) & 15u) + (__float_as_uint(b) & 15u) * 16u;
-    c[q / 4] = q % 4 == 0 ? two : c[q / 4] + (two << (8 * (q % 4)));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w = 0u;
+#pragma unroll
+    for (int q = 3; q >= 0; --q) {
+      float a, b;
+      f2_unpack(f2_add(y[4 * h + q], whole), a, b);
+      w = (w * 16u + __float_as_uint(b)) * 16u + __float_as_uint(a);
+    }
+    c[h] = w - kOffset * 0x11111111u;
   }
-  c[0] ^= 0x88888888u;  // c = 8 + whole number
-  c[1] ^= 0x88888888u;
   return sb;
 }
 
@@ -120,29 +122,41 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4StoreParams p)
   constexpr int NG = D / 16, HS = 256 / (NG * kTok);  // heads a block takes at a time
   __shared__ TokenAt at[kTok];
   const int t0 = blockIdx.x * kTok;
-  find_tokens(p, t0, at);
   const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
   const int g = threadIdx.x % NG, tk = threadIdx.x / NG % kTok;
-  const TokenAt a = at[tk];
-  if (a.block < 0) return;
   const __nv_bfloat16* kr = p.k + (size_t)(t0 + tk) * p.k_stride + g * 16;
   const __nv_bfloat16* vr = p.v + (size_t)(t0 + tk) * p.v_stride + g * 16;
+  // a head's values are loaded ahead: the first while the tokens are looked up, then each while
+  // the one before it is rounded
+  uint4 k0, k1, v0, v1;
+  auto load = [&](int h) {
+    const uint4* ks = reinterpret_cast<const uint4*>(kr + (size_t)h * D);
+    const uint4* vs = reinterpret_cast<const uint4*>(vr + (size_t)h * D);
+    k0 = __ldg(ks);
+    k1 = __ldg(ks + 1);
+    v0 = __ldg(vs);
+    v1 = __ldg(vs + 1);
+  };
+  int h = threadIdx.x / (NG * kTok) + HS * blockIdx.y;
+  if (t0 + tk < p.T && h < p.c.H_kv) load(h);
+  find_tokens(p, t0, at);
+  const TokenAt a = at[tk];
+  if (a.block < 0) return;
   uint8_t* page = p.pool + a.block;
   const int at_k = a.w * (D / 2) + g * 8, at_sk = kv4_off_sk(P, D) + a.w * NG + g;
   const int at_sv = kv4_off_sv(P, D) + (a.w >> 1) * 2 * NG + 2 * g + (a.w & 1);
   const int at_v0 = kv4_off_v(P, D) + kv4_v_at(a.w, D == 128 ? g : 2 * g, D);
   const int at_v1 = kv4_off_v(P, D) + kv4_v_at(a.w, 2 * g + 1, D);  // D = 64: 16 dims are two eighths
 #pragma unroll 2
-  for (int h = threadIdx.x / (NG * kTok) + HS * blockIdx.y; h < p.c.H_kv; h += HS * gridDim.y) {
-    const uint4* ks = reinterpret_cast<const uint4*>(kr + (size_t)h * D);
-    const uint4* vs = reinterpret_cast<const uint4*>(vr + (size_t)h * D);
-    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+  for (; h < p.c.H_kv; h += HS * gridDim.y) {
+    const uint4 ka = k0, kb = k1, va = v0, vb = v1;
+    if (h + HS * gridDim.y < p.c.H_kv) load(h + HS * gridDim.y);
     uint8_t* base = page + (size_t)h * blk;
     uint32_t c[2];
-    int sb = quantise16(k0, k1, c);
+    int sb = quantise16(ka, kb, c);
     *reinterpret_cast<uint2*>(base + at_k) = make_uint2(c[0], c[1]);
     base[at_sk] = (uint8_t)sb;
-    sb = quantise16(v0, v1, c);
+    sb = quantise16(va, vb, c);
     if constexpr (D == 128) {
       *reinterpret_cast<uint2*>(base + at_v0) = make_uint2(c[0], c[1]);
     } else {
