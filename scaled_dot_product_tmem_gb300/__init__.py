@@ -677,7 +677,8 @@ def _elsewhere(dev, stream):
 
 def _window(window):
     """The window as a C int: one past 32 bits must not wrap into a small one."""
-    return max(-1, min(int(window), 0x7fffffff))
+    w = int(window)
+    return w if -1 <= w <= 0x7fffffff else -1 if w < 0 else 0x7fffffff
 
 
 def _raw_stream(dev, stream):
@@ -702,7 +703,7 @@ def _check_packed(q, k, v, cu_q, cu_kv, softmax_offset):
         _check(t, n, torch.bfloat16, 3)
     T_q, H_q, d_qk = q.shape
     T_kv, H_kv, d_v = v.shape
-    if tuple(k.shape) != (T_kv, H_kv, d_qk):
+    if k.shape != (T_kv, H_kv, d_qk):
         raise ValueError(f"k must be {(T_kv, H_kv, d_qk)} (v's rows and heads, q's head dim), got {tuple(k.shape)}")
     _check_cu(cu_q, "cu_seqlens_q")
     B = cu_q.shape[0] - 1
@@ -747,13 +748,34 @@ def attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv=None, *, causal
             return attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, causal=causal, window=window,
                                    softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
                                    zero_rest=zero_rest, workspace=workspace)
+    _run_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, sizes, dev, causal, window, softmax_type,
+                    softmax_offset, scale, zero_rest, workspace)
+
+
+# The _run_* functions: the call itself, on the current stream of the current device `dev`, of checked
+# arguments.  The calls that allocate their results come here too, past checks of tensors they made.
+def _run_fwd_packed(q, k, v, o, lse, cu_q, cu_kv, sizes, dev, causal, window, softmax_type, softmax_offset, scale,
+                    zero_rest, workspace):
     ws = _workspace(workspace, attn_packed_workspace_size(*sizes) if workspace is None else 0, q.device)
-    st = _load().attn_fwd_packed(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(cu_seqlens_q), _p(cu_seqlens_kv), *sizes,
+    st = _load().attn_fwd_packed(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(cu_q), _p(cu_kv), *sizes,
                                  float(scale or 0.0), int(bool(causal)), _window(window), _stype(softmax_type),
                                  _p(softmax_offset), int(bool(zero_rest)), _p(ws), ws.numel(),
-                                 _raw_stream(dev, stream))
+                                 _raw_stream(dev, None))
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_packed")
+
+
+def _check_bwd_packed(q, k, v, o, dout, lse, cu_q, cu_kv, softmax_offset):
+    sizes = _check_packed(q, k, v, cu_q, cu_kv, softmax_offset)
+    _, T_q, _, H_q, _, _, d_v = sizes
+    _check(lse, "lse", torch.float32, 2)
+    if lse.shape != (H_q, T_q):
+        raise ValueError(f"lse must be {(H_q, T_q)}, got {tuple(lse.shape)}")
+    for t, n in ((o, "o"), (dout, "dout")):
+        _check(t, n, torch.bfloat16, 3)
+        if t.shape != (T_q, H_q, d_v):
+            raise ValueError(f"{n} must be {(T_q, H_q, d_v)}, got {tuple(t.shape)}")
+    return sizes
 
 
 def attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv=None, *, causal=True,
@@ -761,20 +783,15 @@ def attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, c
                     stream=None):
     """Backward of attn_fwd_packed into preallocated dq, dk, dv (bf16, shapes of q, k, v) and
     d_offset (fp32 [H_q]; learnable sinks, else None).  Bitwise reproducible."""
-    sizes = _check_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
-    _, T_q, _, H_q, _, _, d_v = sizes
-    _check(lse, "lse", torch.float32, 2)
-    if tuple(lse.shape) != (H_q, T_q):
-        raise ValueError(f"lse must be {(H_q, T_q)}, got {tuple(lse.shape)}")
-    for t, n, shape in ((o, "o", (T_q, H_q, d_v)), (dout, "dout", (T_q, H_q, d_v)), (dq, "dq", tuple(q.shape)),
-                        (dk, "dk", tuple(k.shape)), (dv, "dv", tuple(v.shape))):
+    sizes = _check_bwd_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
+    for t, n, of in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
         _check(t, n, torch.bfloat16, 3)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
+        if t.shape != of.shape:
+            raise ValueError(f"{n} must be {tuple(of.shape)}, got {tuple(t.shape)}")
     if d_offset is not None:
         _check(d_offset, "d_offset", torch.float32, 1)
-        if d_offset.shape[0] != H_q:
-            raise ValueError(f"d_offset must have one value per query head ({H_q})")
+        if d_offset.shape[0] != q.shape[1]:
+            raise ValueError(f"d_offset must have one value per query head ({q.shape[1]})")
     dev = _device_of(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv, softmax_offset,
                      workspace)
     if _elsewhere(dev, stream):
@@ -783,11 +800,17 @@ def attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, c
                                    causal=causal, window=window, softmax_type=softmax_type,
                                    softmax_offset=softmax_offset, scale=scale, zero_rest=zero_rest,
                                    workspace=workspace)
+    _run_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_seqlens_q, cu_seqlens_kv, sizes, dev, causal,
+                    window, softmax_type, softmax_offset, scale, zero_rest, workspace)
+
+
+def _run_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_offset, cu_q, cu_kv, sizes, dev, causal, window, softmax_type,
+                    softmax_offset, scale, zero_rest, workspace):
     ws = _workspace(workspace, attn_packed_workspace_size(*sizes, True) if workspace is None else 0, q.device)
     st = _load().attn_bwd_packed(_p(q), _p(k), _p(v), _p(o), _p(dout), _p(lse), _p(dq), _p(dk), _p(dv), _p(d_offset),
-                                 _p(cu_seqlens_q), _p(cu_seqlens_kv), *sizes, float(scale or 0.0), int(bool(causal)),
+                                 _p(cu_q), _p(cu_kv), *sizes, float(scale or 0.0), int(bool(causal)),
                                  _window(window), _stype(softmax_type), _p(softmax_offset), int(bool(zero_rest)), _p(ws),
-                                 ws.numel(), _raw_stream(dev, stream))
+                                 ws.numel(), _raw_stream(dev, None))
     if st != ATTN_OK:
         raise AttnError(st, "attn_bwd_packed")
 
@@ -796,16 +819,18 @@ def sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv=None, *, causal=Tru
                         softmax_offset=None, scale=0.0, workspace=None, stream=None):
     """Allocate O and LSE, run attn_fwd_packed, return (o, lse); rows of no sequence are zero (lse
     -inf)."""
-    kw = dict(causal=causal, window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
-              workspace=workspace)
-    dev = _device_of(q)
-    if dev >= 0 and _elsewhere(dev, stream):
+    sizes = _check_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
+    dev = _device_of(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset, workspace)
+    if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, **kw)
-    T_q, H_q, _ = q.shape
-    o = torch.empty((T_q, H_q, v.shape[2]), dtype=torch.bfloat16, device=q.device)
+            return sdpa_forward_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv, causal=causal, window=window,
+                                       softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
+                                       workspace=workspace)
+    _, T_q, _, H_q, _, _, d_v = sizes
+    o = torch.empty((T_q, H_q, d_v), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((H_q, T_q), dtype=torch.float32, device=q.device)
-    attn_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, zero_rest=True, **kw)
+    _run_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, sizes, dev, causal, window, softmax_type,
+                    softmax_offset, scale, True, workspace)
     return o, lse
 
 
@@ -813,16 +838,18 @@ def sdpa_backward_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv=None
                          softmax_type=VANILLA, softmax_offset=None, scale=0.0, workspace=None, stream=None):
     """Allocate dQ, dK, dV (and d_offset for the learnable sink), run attn_bwd_packed, return
     them; gradients of rows of no sequence are zero."""
-    kw = dict(causal=causal, window=window, softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
-              workspace=workspace)
-    dev = _device_of(q)
-    if dev >= 0 and _elsewhere(dev, stream):
+    sizes = _check_bwd_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv, softmax_offset)
+    dev = _device_of(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv, softmax_offset, workspace)
+    if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return sdpa_backward_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv, **kw)
+            return sdpa_backward_packed(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_kv, causal=causal,
+                                        window=window, softmax_type=softmax_type, softmax_offset=softmax_offset,
+                                        scale=scale, workspace=workspace)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     d_off = (torch.empty((q.shape[1],), dtype=torch.float32, device=q.device)
              if _stype(softmax_type) == LEARNABLE else None)
-    attn_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_off, cu_seqlens_q, cu_seqlens_kv, zero_rest=True, **kw)
+    _run_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, d_off, cu_seqlens_q, cu_seqlens_kv, sizes, dev, causal, window,
+                    softmax_type, softmax_offset, scale, True, workspace)
     return dq, dk, dv, d_off
 
 
@@ -975,6 +1002,20 @@ def attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d) -> int:
     return int(_load().attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d))
 
 
+def _check_decode(q, pool, page_table, seq_lens, softmax_offset):
+    """Checks of a decode's inputs; returns (B, S_q, H_q, H_kv, d, n_pages, page_size, max_pages)."""
+    _check(q, "q", torch.bfloat16, 4)
+    B, S_q, H_q, d = q.shape
+    Bt, n_pages, H_kv, page_size, max_pages = _check_paged(pool, page_table, seq_lens, d)
+    if Bt != B:
+        raise ValueError(f"page_table must have one row per batch entry ({B}), got {Bt}")
+    if softmax_offset is not None:
+        _check(softmax_offset, "softmax_offset", torch.float32, 1)
+        if softmax_offset.shape[0] != H_q:
+            raise ValueError(f"softmax_offset must have one value per query head ({H_q})")
+    return B, S_q, H_q, H_kv, d, n_pages, page_size, max_pages
+
+
 def attn_kv4_decode(q, pool, page_table, seq_lens, o, lse=None, *, window=-1, softmax_type=VANILLA,
                     softmax_offset=None, scale=0.0, workspace=None, stream=None):
     """Attention of the S_q newest tokens of every sequence over its 4-bit cache, into
@@ -984,33 +1025,30 @@ def attn_kv4_decode(q, pool, page_table, seq_lens, o, lse=None, *, window=-1, so
     s sits at seq_lens[b] - S_q + s and sees the keys up to its own place, with window >= 0
     the last window + 1 of them.  workspace: uint8 of attn_kv4_decode_workspace_size() bytes
     or more, not shared with a call that may run at the same time (None: a new one)."""
-    _check(q, "q", torch.bfloat16, 4)
+    sizes = _check_decode(q, pool, page_table, seq_lens, softmax_offset)
+    B, S_q, H_q = sizes[:3]
     _check(o, "o", torch.bfloat16, 4)
-    B, S_q, H_q, d = q.shape
-    Bt, n_pages, H_kv, page_size, max_pages = _check_paged(pool, page_table, seq_lens, d)
-    if Bt != B:
-        raise ValueError(f"page_table must have one row per batch entry ({B}), got {Bt}")
     if o.shape != q.shape:
         raise ValueError(f"o must have q's shape {tuple(q.shape)}, got {tuple(o.shape)}")
     if lse is not None:
         _check(lse, "lse", torch.float32, 3)
-        if tuple(lse.shape) != (B, H_q, S_q):
+        if lse.shape != (B, H_q, S_q):
             raise ValueError(f"lse must be {(B, H_q, S_q)}, got {tuple(lse.shape)}")
-    if softmax_offset is not None:
-        _check(softmax_offset, "softmax_offset", torch.float32, 1)
-        if softmax_offset.shape[0] != H_q:
-            raise ValueError(f"softmax_offset must have one value per query head ({H_q})")
     dev = _device_of(q, pool, page_table, seq_lens, o, lse, softmax_offset, workspace)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attn_kv4_decode(q, pool, page_table, seq_lens, o, lse, window=window, softmax_type=softmax_type,
                                    softmax_offset=softmax_offset, scale=scale, workspace=workspace)
-    ws = _workspace(workspace, attn_kv4_decode_workspace_size(B, S_q, H_q, H_kv, d) if workspace is None else 0,
-                    q.device)
-    st = _load().attn_kv4_decode(_p(q), _p(pool), _p(page_table), _p(seq_lens), _p(o), _p(lse), B, S_q, H_q, H_kv, d,
-                                 n_pages, page_size, max_pages, float(scale or 0.0), _window(window),
-                                 _stype(softmax_type), _p(softmax_offset), _p(ws), ws.numel(),
-                                 _raw_stream(dev, stream))
+    _run_kv4_decode(q, pool, page_table, seq_lens, o, lse, sizes, dev, window, softmax_type, softmax_offset, scale,
+                    workspace)
+
+
+def _run_kv4_decode(q, pool, page_table, seq_lens, o, lse, sizes, dev, window, softmax_type, softmax_offset, scale,
+                    workspace):
+    ws = _workspace(workspace, attn_kv4_decode_workspace_size(*sizes[:5]) if workspace is None else 0, q.device)
+    st = _load().attn_kv4_decode(_p(q), _p(pool), _p(page_table), _p(seq_lens), _p(o), _p(lse), *sizes,
+                                 float(scale or 0.0), _window(window), _stype(softmax_type), _p(softmax_offset),
+                                 _p(ws), ws.numel(), _raw_stream(dev, None))
     if st != ATTN_OK:
         raise AttnError(st, "attn_kv4_decode")
 
@@ -1018,16 +1056,16 @@ def attn_kv4_decode(q, pool, page_table, seq_lens, o, lse=None, *, window=-1, so
 def sdpa_decode_kv4(q, pool, page_table, seq_lens, *, window=-1, softmax_type=VANILLA, softmax_offset=None, scale=0.0,
                     workspace=None, stream=None):
     """Allocate O and LSE, run attn_kv4_decode, return (o, lse)."""
-    dev = _device_of(q)
-    if dev >= 0 and _elsewhere(dev, stream):
+    sizes = _check_decode(q, pool, page_table, seq_lens, softmax_offset)
+    dev = _device_of(q, pool, page_table, seq_lens, softmax_offset, workspace)
+    if _elsewhere(dev, stream):
         with _on(dev, stream):
             return sdpa_decode_kv4(q, pool, page_table, seq_lens, window=window, softmax_type=softmax_type,
                                    softmax_offset=softmax_offset, scale=scale, workspace=workspace)
-    B, S_q, H_q, _ = q.shape
     o = torch.empty_like(q)
-    lse = torch.empty((B, H_q, S_q), dtype=torch.float32, device=q.device)
-    attn_kv4_decode(q, pool, page_table, seq_lens, o, lse, window=window, softmax_type=softmax_type,
-                    softmax_offset=softmax_offset, scale=scale, workspace=workspace)
+    lse = torch.empty((sizes[0], sizes[2], sizes[1]), dtype=torch.float32, device=q.device)
+    _run_kv4_decode(q, pool, page_table, seq_lens, o, lse, sizes, dev, window, softmax_type, softmax_offset, scale,
+                    workspace)
     return o, lse
 
 
