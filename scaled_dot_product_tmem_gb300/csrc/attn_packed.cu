@@ -253,81 +253,94 @@ int launch_attn_fwd_packed(int d_qk, int d_v, const CUtensorMap& tq, const CUten
 // =============================================================================
 constexpr int kExactRows = 16;
 
-// D of row i of the sequence from P and V in fp32, by TPR lanes (rows of one warp may see different
-// numbers n of keys, from key lo on).  do8: this lane's 8 dims of dO.
+// Those rows see some of the sequence's first kExactRows keys only, so a block has the 16 rows of
+// Q and dO and the 16 of K and V in shared memory, and thread (i, j) forms P_ij (dO_i . v_j):
+// D_i is their sum over 16 lanes.  (The loads are on their way together with those of O.)
 template <int D_QK, int D_V>
-__device__ __forceinline__ float exact_d(const BwdParams& p, const PackedTile& e, int h, int i, int lo, int n,
-                                         const uint4& do8) {
-  constexpr int TPR = D_V / 8, NQ = D_QK / (4 * TPR);  // words of 4 dims a lane has of q and k
-  const int sub = threadIdx.x % TPR, hk = h / p.G;
-  const bool some = n > 0;
-  const size_t qrow = ((size_t)(e.q0 + (some ? i : 0)) * p.H_q + h) * D_QK;
-  float q[4 * NQ], o[8], nl = 0.f;
+struct ExactRows {
+  static constexpr int CQ = D_QK / 8, CV = D_V / 8;  // 16-byte pieces of a row
+  static constexpr int NQ = (kExactRows * CQ + 255) / 256, NV = (kExactRows * CV + 255) / 256;
+  static constexpr int SQ = CQ + 1, SV = CV + 1;  // row strides in pieces: 8 rows fall on different banks
+  struct Smem {
+    uint4 q[kExactRows * SQ], k[kExactRows * SQ], v[kExactRows * SV], g[kExactRows * SV];
+  };
+  uint4 q[NQ], k[NQ], v[NV];
+  float nl;
+
+  __device__ __forceinline__ void load(const BwdParams& p, const PackedTile& e, int h) {
+    const int hk = h / p.G;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int u = 0; u < NQ; ++u) {
-    const uint2 w = some ? *reinterpret_cast<const uint2*>(p.q + qrow + (u * TPR + sub) * 4) : make_uint2(0u, 0u);
-    q[4 * u] = __uint_as_float(w.x << 16);
-    q[4 * u + 1] = __uint_as_float(w.x & 0xFFFF0000u);
-    q[4 * u + 2] = __uint_as_float(w.y << 16);
-    q[4 * u + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+    for (int u = 0; u < NQ; ++u) {
+      const int x = threadIdx.x + u * 256, r = x / CQ, c = x % CQ;
+      q[u] = r < kExactRows && r < e.Lq
+                 ? __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)(e.q0 + r) * p.H_q + h) * D_QK) + c) : zero;
+      k[u] = r < kExactRows && r < e.Lk
+                 ? __ldg(reinterpret_cast<const uint4*>(p.k + ((size_t)(e.k0 + r) * p.H_kv + hk) * D_QK) + c) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int x = threadIdx.x + u * 256, r = x / CV, c = x % CV;
+      v[u] = r < kExactRows && r < e.Lk
+                 ? __ldg(reinterpret_cast<const uint4*>(p.v + ((size_t)(e.k0 + r) * p.H_kv + hk) * D_V) + c) : zero;
+    }
+    const int i = threadIdx.x / 16;
+    nl = i < e.Lq ? -p.lse[(size_t)h * p.S_q + e.q0 + i] * kLog2e : 0.f;
   }
-  if (some) nl = -p.lse[(size_t)h * p.S_q + e.q0 + i] * kLog2e;
+  __device__ __forceinline__ void store(Smem& m) const {
 #pragma unroll
-  for (int x = 0; x < 8; ++x) o[x] = 0.f;
-  if (!__any_sync(0xffffffffu, some)) return 0.f;
-  // Keys past the row's last are loaded as its last and weigh nothing: no branch parts the loads.
-  // Four keys at a time: scores, their sums over the lanes, values.
-  const int most = __reduce_max_sync(0xffffffffu, n);
-#pragma unroll 1
-  for (int t0 = 0; t0 < most; t0 += 4) {
-    float s[4];
-    uint4 v8[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const size_t row = (size_t)(e.k0 + (some ? lo + min(t0 + t, n - 1) : 0)) * p.H_kv + hk;
-      v8[t] = __ldg(reinterpret_cast<const uint4*>(p.v + row * D_V + sub * 8));
-      s[t] = 0.f;
-#pragma unroll
-      for (int u = 0; u < NQ; ++u) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.k + row * D_QK + (u * TPR + sub) * 4));
-        s[t] = fmaf(q[4 * u], __uint_as_float(w.x << 16), s[t]);
-        s[t] = fmaf(q[4 * u + 1], __uint_as_float(w.x & 0xFFFF0000u), s[t]);
-        s[t] = fmaf(q[4 * u + 2], __uint_as_float(w.y << 16), s[t]);
-        s[t] = fmaf(q[4 * u + 3], __uint_as_float(w.y & 0xFFFF0000u), s[t]);
+    for (int u = 0; u < NQ; ++u) {
+      const int x = threadIdx.x + u * 256, r = x / CQ, c = x % CQ;
+      if (r < kExactRows) {
+        m.q[r * SQ + c] = q[u];
+        m.k[r * SQ + c] = k[u];
       }
     }
 #pragma unroll
-    for (int off = TPR / 2; off > 0; off >>= 1)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], off);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const bool see = t0 + t < n;
-      const float w = see ? ex2(fmaf(s[t], p.scale_log2, nl)) : 0.f;
-      const uint32_t ws[4] = {v8[t].x, v8[t].y, v8[t].z, v8[t].w};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        o[2 * x] = see ? fmaf(w, __uint_as_float(ws[x] << 16), o[2 * x]) : o[2 * x];
-        o[2 * x + 1] = see ? fmaf(w, __uint_as_float(ws[x] & 0xFFFF0000u), o[2 * x + 1]) : o[2 * x + 1];
-      }
+    for (int u = 0; u < NV; ++u) {
+      const int x = threadIdx.x + u * 256, r = x / CV, c = x % CV;
+      if (r < kExactRows) m.v[r * SV + c] = v[u];
     }
   }
-  const uint32_t gs[4] = {do8.x, do8.y, do8.z, do8.w};
-  float acc = 0.f;
+  template <int N>
+  __device__ __forceinline__ static float dot(const uint4* a, const uint4* b) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll 4
+    for (int c = 0; c < N; ++c) {
+      const uint4 x = a[c], y = b[c];
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    acc = fmaf(o[2 * x], __uint_as_float(gs[x] << 16), acc);
-    acc = fmaf(o[2 * x + 1], __uint_as_float(gs[x] & 0xFFFF0000u), acc);
+      for (int w = 0; w < 4; ++w) {
+        s[0] = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), s[0]);
+        s[1] = fmaf(__uint_as_float(xs[w] & 0xFFFF0000u), __uint_as_float(ys[w] & 0xFFFF0000u), s[1]);
+      }
+    }
+    return s[0] + s[1];
   }
+  // (every thread of the block, after store() and a barrier)
+  __device__ __forceinline__ void sums(const BwdParams& p, const PackedTile& e, const Smem& m, float* dsum) const {
+    const int i = threadIdx.x / 16, j = threadIdx.x % 16;
+    int lo = 0, hi = -1;
+    visible_keys<true>(MaskSpec{e.Lq, e.Lk, p.causal, p.window}, i, &lo, &hi);
+    const int n = hi - lo + 1;
+    const bool few = n > 0 && n <= kExactRows, see = few && j >= lo && j <= hi;
+    float t = 0.f;
+    if (__any_sync(0xffffffffu, see)) {
+      const float s = dot<CQ>(m.q + i * SQ, m.k + j * SQ), dp = dot<CV>(m.g + i * SV, m.v + j * SV);
+      t = see ? ex2(fmaf(s, p.scale_log2, nl)) * dp : 0.f;
 #pragma unroll
-  for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-  return acc;
-}
+      for (int off = 8; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    }
+    if (few && j == 0) dsum[i] = t;
+  }
+};
 
 template <int D_QK, int D_V>
 __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams p) {
   constexpr int TPR = D_V / 8, RPP = 256 / TPR, TILE = 64, NR = TILE / RPP;
+  using X = ExactRows<D_QK, D_V>;
   __shared__ float dsum[TILE];
+  __shared__ typename X::Smem xs;
   const int h = blockIdx.y;
   grid_launch_dependents();
   grid_wait();  // the plan
@@ -335,6 +348,8 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
     const PackedTile e = load_packed_tile(p.tiles_q, blockIdx.x / 2);
     const int i0 = e.m0 + (blockIdx.x % 2) * TILE, sub = threadIdx.x % TPR;
     uint4 a[NR], g[NR];
+    X exact;
+    if (i0 == 0) exact.load(p, e, h);
 #pragma unroll
     for (int k = 0; k < NR; ++k) {
       const int i = i0 + threadIdx.x / TPR + k * RPP;
@@ -360,16 +375,13 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
       for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
       if (sub == 0) dsum[threadIdx.x / TPR + k * RPP] = acc;
     }
-    // the sequence's first rows: all in the first pass, RPP >= kExactRows rows of whole warps
-    static_assert(RPP >= kExactRows && kExactRows % (32 / TPR) == 0, "the exact rows are whole warps of one pass");
-    const int i = i0 + threadIdx.x / TPR;
-    if (i0 == 0 && i < kExactRows) {
-      int lo = 0, hi = -1;
-      visible_keys<true>(MaskSpec{e.Lq, e.Lk, p.causal, p.window}, i, &lo, &hi);
-      const int n = hi - lo + 1;
-      const bool few = n > 0 && n <= kExactRows;
-      const float d = exact_d<D_QK, D_V>(p, e, h, i, lo, few ? n : 0, g[0]);
-      if (few && sub == 0) dsum[i] = d;
+    if (i0 == 0) {
+      static_assert(RPP >= kExactRows, "the exact rows are rows of the first pass");
+      const int r = threadIdx.x / TPR;
+      if (r < kExactRows) xs.g[r * X::SV + sub] = g[0];
+      exact.store(xs);
+      __syncthreads();
+      exact.sums(p, e, xs, dsum);
     }
     __syncthreads();
     if (threadIdx.x < TILE) {
