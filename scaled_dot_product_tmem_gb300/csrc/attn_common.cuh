@@ -121,7 +121,7 @@ struct PackedCounts {
   // the sequences' rows: [q_begin, q_end) and [kv_begin, kv_end) (they follow one another, so the
   // rows before and behind these belong to no sequence)
   int q_begin, q_end, kv_begin, kv_end;
-  int unused;
+  int next;  // forward: work tiles taken beyond each CTA's first
 };
 
 // A small packed batch needs no plan kernel: every CTA finds its one tile itself.

@@ -47,6 +47,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "attn_kernels.h"
 #include "dropout.cuh"
@@ -54,6 +56,12 @@
 #include "ptx.cuh"
 
 namespace sdpa {
+
+// A work tile of a packed batch as its CTA's producer passes it on.
+struct TakenTile {
+  PackedTile e;
+  int wi, unused;
+};
 
 // BT: the bias tiles of the two query tiles are staged in shared memory by TMA.
 // OS: the output leaves through shared memory (4 KB a softmax warp), so that a warp stores whole
@@ -79,11 +87,13 @@ struct FwdCfg {
   static constexpr int OFF_O = OFF_B + (BT ? 2 * B_TILE : 0);
   static constexpr int OFF_BAR = OFF_O + (OS ? 8 * 32 * 128 : 0);
   // q_full, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_ready[2], p_ready[2], o_done[2], mma_done,
-  // q_empty, then (BT) b_full[2], b_empty[2]
-  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + (BT ? 4 : 0);
+  // q_empty, then (BT) b_full[2], b_empty[2] or (PK) tile_full[2], tile_empty[2]
+  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + (BT || PK ? 4 : 0);
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_OWN = OFF_TMEM_SLOT + 16;  // packed: the tile a CTA found itself
-  static constexpr int SMEM_USED = OFF_OWN + (PK ? (int)sizeof(OwnTile) : 0) + 1024;
+  // packed: the tile a CTA found itself, or the two it took last
+  static constexpr int OFF_OWN = OFF_TMEM_SLOT + 16;
+  static constexpr int SMEM_USED =
+      OFF_OWN + (PK ? (int)std::max(sizeof(OwnTile), 2 * sizeof(TakenTile)) : 0) + 1024;
   // at least 117 KB so that one CTA per SM holds the 512 TMEM columns
   static constexpr int SMEM = SMEM_USED > 117 * 1024 ? SMEM_USED : 117 * 1024;
   static constexpr int THREADS = 320;
@@ -102,13 +112,10 @@ struct FwdTile {
   MaskSpec mask;  // with the entry's own lengths
 };
 
-template <int BM, int BN, bool VL, bool PK = false, bool OWN = false>
-__device__ __forceinline__ FwdTile fwd_tile(const FwdParams& p, int nqb, int wi, const OwnTile* own) {
+template <int BM, int BN, bool VL, bool PK = false>
+__device__ __forceinline__ FwdTile fwd_tile(const FwdParams& p, int nqb, int wi, const PackedTile& e) {
   FwdTile T;
-  if constexpr (PK) {  // the plan lists the tiles, most work first; every head takes each
-    PackedTile e;
-    if constexpr (OWN) e = own->e;
-    else e = load_packed_tile(p.tiles, wi / p.H_q);
+  if constexpr (PK) {  // tile wi / H_q of the batch, which every head takes
     T.h = wi % p.H_q;
     T.b = 0;
     T.m0 = e.m0;
@@ -143,7 +150,7 @@ __device__ __forceinline__ FwdTile fwd_tile(const FwdParams& p, int nqb, int wi,
 }
 
 enum FwdSite { kSiteQ = 1, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteS, kSiteP, kSiteO, kSiteDrain,
-               kSiteBFull, kSiteBEmpty };
+               kSiteBFull, kSiteBEmpty, kSiteTile };
 
 // Bias tiles staged by TMA for head dims up to 128 (the MLA dims keep the per-row loads).
 template <int D_QK, bool BIAS>
@@ -180,6 +187,10 @@ __global__ void __launch_bounds__(320, 1)
   uint64_t* q_empty = mma_done + 1;
   [[maybe_unused]] uint64_t* b_full = q_empty + 1;  // [2] (BT)
   [[maybe_unused]] uint64_t* b_empty = b_full + 2;  // [2]
+  // DYN: the tiles beyond a CTA's first come from a counter, through a ring of two
+  constexpr bool DYN = PK && !OWN;
+  [[maybe_unused]] uint64_t* tile_full = q_empty + 1;     // [2] the producer has passed a tile on
+  [[maybe_unused]] uint64_t* tile_empty = tile_full + 2;  // [2] every other warp has read it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM_SLOT);
   // the bias tiles are staged only when the rows are whole 16-byte units (S_kv % 8 == 0)
   [[maybe_unused]] const bool b_tma = BT && p.bias_tma;
@@ -192,6 +203,12 @@ __global__ void __launch_bounds__(320, 1)
 
   if (threadIdx.x == 0) {
     if constexpr (PK) mbar_init(raw_full, 1);
+    if constexpr (DYN) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&tile_full[s], 1);
+        mbar_init(&tile_empty[s], 9);  // the issuing warp and the softmax warps
+      }
+    }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < NK; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
@@ -231,6 +248,26 @@ __global__ void __launch_bounds__(320, 1)
 
   // The CTA is persistent: it takes work tiles wi = blockIdx.x, blockIdx.x + gridDim.x,
   // ...; every role walks the same sequence and counts barrier phases across tiles.
+  // Packed: the list falls in cost, by whole sequences' worth, and in turn the first CTA would get
+  // the dearest tile of every round (the last CTA was done at 91 to 113 us for 8 sequences of 64 to
+  // 2048 rows under a window of 1024, the mean at 100).  So a CTA takes its next tile from a
+  // counter when the loads of one are issued: 118 -> 113 us there, 540 -> 514 for 7 sequences of 93
+  // to 8192 rows (32 heads, 8 kv heads, d = 128).  The ring also spares the other warps the list.
+  [[maybe_unused]] TakenTile* ring = reinterpret_cast<TakenTile*>(smem + C::OFF_OWN);
+  [[maybe_unused]] PackedTile e;
+  // the tile after wi, a warp's k-th, in the warps other than the producer
+  auto take = [&](int wi, [[maybe_unused]] int k) -> int {
+    if constexpr (DYN) {
+      const int slot = k & 1;
+      if (!mbar_wait_warp(&tile_full[slot], (k >> 1) & 1, err, kSiteTile)) return n_work;
+      e = ring[slot].e;
+      wi = ring[slot].wi;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tile_empty[slot]);
+      return wi;
+    }
+    return wi + (int)gridDim.x;
+  };
   if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
     // Packed: the whole warp walks the tiles, its first lane issues.  The rows of a sequence's
@@ -251,8 +288,31 @@ __global__ void __launch_bounds__(320, 1)
       int n = 0, nw = 0;  // kv stages loaded, Q tiles loaded
       [[maybe_unused]] int nb[2] = {0, 0};  // bias tiles loaded per query tile
       bool ok = true;
-      for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-        const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK, OWN>(p, nqb, wi, own);
+      [[maybe_unused]] auto pass_on = [&](int wi, int k) {
+        const int slot = k & 1;
+        if (k >= 2 && !wait(&tile_empty[slot], ((k >> 1) - 1) & 1, kSiteTile)) return false;
+        if (wi < n_work) e = load_packed_tile(p.tiles, wi / p.H_q);
+        if (lead) {
+          ring[slot].e = e;
+          ring[slot].wi = wi;
+          mbar_arrive(&tile_full[slot]);
+        }
+        return true;
+      };
+      auto next = [&](int wi, [[maybe_unused]] int k) -> int {
+        if constexpr (DYN) {
+          if (!ok) return n_work;
+          int t = 0;
+          if (lead) t = gridDim.x + atomicAdd(&p.counts->next, 1);
+          t = __shfl_sync(0xffffffffu, t, 0);
+          ok = pass_on(t, k);
+          return t;
+        }
+        return wi + (int)gridDim.x;
+      };
+      if constexpr (DYN) ok = pass_on(blockIdx.x, 0);
+      for (int wi = blockIdx.x, k = 0; wi < n_work && ok; wi = next(wi, ++k)) {
+        const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi, OWN ? own->e : e);
         if (!T.any) continue;
         // Q of the previous tile must have been read by that tile's last S MMAs
         if (nw > 0) ok = wait(q_empty, (nw - 1) & 1, kSiteQ);
@@ -394,8 +454,8 @@ __global__ void __launch_bounds__(320, 1)
     int n = 0, nw = 0;      // kv stages consumed, Q tiles consumed
     int pc[2] = {0, 0};     // p_ready phases consumed per query tile
     bool ok = true, issued = false;
-    for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK, OWN>(p, nqb, wi, own);
+    for (int wi = DYN ? take(0, 0) : (int)blockIdx.x, k = 0; wi < n_work && ok; wi = take(wi, ++k)) {
+      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi, OWN ? own->e : e);
       if (!T.any) continue;
       issued = true;
       ok = mbar_wait_warp(q_full, nw & 1, err, kSiteQ);
@@ -464,8 +524,8 @@ __global__ void __launch_bounds__(320, 1)
     [[maybe_unused]] int nbc = 0;  // bias tiles consumed (BT)
     [[maybe_unused]] const uint8_t* btile = smem + C::OFF_B + t * C::B_TILE + r * 128;  // this row, first box
     bool ok = true;
-    for (int wi = blockIdx.x; wi < n_work && ok; wi += gridDim.x) {
-      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK, OWN>(p, nqb, wi, own);
+    for (int wi = DYN ? take(0, 0) : (int)blockIdx.x, k = 0; wi < n_work && ok; wi = take(wi, ++k)) {
+      const FwdTile T = fwd_tile<C::BM, C::BN, VL, PK>(p, nqb, wi, OWN ? own->e : e);
       // this warpgroup's query tile, selected without a run-time index into T (which
       // would move T to local memory)
       const bool my_exists = t ? T.exists[1] : T.exists[0];

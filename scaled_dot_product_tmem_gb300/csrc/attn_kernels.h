@@ -37,7 +37,7 @@ struct FwdParams {
   // packed batch (B = 1, S_q / S_kv the rows of the packed tensors): the plan's tile list, and
   // whether the rows of no sequence are zeroed
   const PackedTile* tiles = nullptr;
-  const PackedCounts* counts = nullptr;
+  PackedCounts* counts = nullptr;
   long long tile_bound = 0;  // the list has at most this many tiles (the host's bound)
   int zero_rest = 0;
   PackedOffsets own;  // tiles null: a small batch, whose CTAs find their tiles themselves

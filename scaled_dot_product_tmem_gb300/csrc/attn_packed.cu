@@ -24,7 +24,7 @@ namespace sdpa {
 // replaced by their running maximum, so sequences never overlap and the lists never pass the
 // host's bounds (T / rows + B entries).  A counting sort by bucket puts the most work first:
 //   forward   each 256-row query tile by the kv tiles it sees: the persistent CTAs take
-//             tiles in turn, and with falling costs no CTA ends up more than one tile behind;
+//             tiles from a counter, and with falling costs they end together;
 //   kv and q  whole sequences by length, a sequence's heaviest tiles first: the tiles in
 //             flight belong to few sequences, whose other operand they share in L2.
 // The order inside a bucket varies from run to run; no result depends on it.
