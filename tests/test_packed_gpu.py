@@ -263,6 +263,24 @@ def test_forward_with_and_without_a_plan_kernel(dims, raw):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("dims", [(64, 64), (192, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_sequences_with_and_without_keys(dims, causal):
+    """More work tiles than blocks, of any cost: some sequences have no keys, some no queries, and
+    a tile without keys follows one with keys in the same block."""
+    g = np.random.default_rng(int(causal))
+    lq = g.integers(0, 300, 90)
+    lk = np.where(g.random(90) < 0.4, 0, g.integers(1, 400, 90))
+    lq, lk = lq.tolist(), lk.tolist()
+    x = _inputs(lq, lk, 4, 2, *dims, seed=23)
+    kw = dict(causal=causal, window=-1, softmax_type=LEARNABLE)
+    got, ref = _run(x, _cu(lq), _cu(lk), **kw), _reference(x, lq, lk, **kw)
+    _compare(got, ref, f"{dims} causal={causal}")
+    again = _run(x, _cu(lq), _cu(lk), **kw)
+    for n, t in got.items():
+        assert torch.equal(t, again[n]), n
+
+
 def test_more_sequences_than_plan_threads_and_a_long_one():
     """3,000 short sequences around one of 5,000 rows; a sample of them against the oracle."""
     g = np.random.default_rng(1)
