@@ -25,12 +25,12 @@
 //     the sum over its warps and its output cost about as much), whatever the lengths; a
 //     (sequence, head) that spans several CTAs leaves fp32 partial sums in the workspace, which a
 //     second kernel joins in CTA order: bitwise reproducible.
-//   - A fifth warp walks the page table and streams units into a ring by bulk copies, four a
-//     page; each of the other four takes 32 tokens of every unit.
+//   - A fifth warp walks the page table and streams units into a ring, a page and head in one
+//     bulk copy; each of the other four takes 32 tokens of every unit.
 //
 // Measured (d = 128, 8 kv heads): 329,377 tokens of 4 sequences with 8 query rows a kv head, 380 MB
-// of cache, 80 us (4.7 TB/s; the copies alone take 70; 88 with an exponent set in every code and
-// a shift for three of four); 42,031 tokens of 16 sequences, 48 MB, 21 us, of which about 10 are
+// of cache, 78 us (4.9 TB/s; 80 with four copies a page, 88 with an exponent set in every code
+// and a shift for three of four as well); 42,031 tokens of 16 sequences, 48 MB, 21 us, of which about 10 are
 // the chain lengths - page - copy - products - join.
 #include <algorithm>
 #include <atomic>
@@ -194,7 +194,6 @@ template <int D, int NT>
 struct DecCfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int STAGE = kUnit * D * 9 / 8;
-  static constexpr int S_V = kUnit * D / 2, S_SK = kUnit * D, S_SV = kUnit * D + kUnit * D / 16;
   static constexpr int OFF_Q = kStages * STAGE;  // query fragments where they do not stay in registers
   static constexpr bool Q_SMEM = NT > 2;
   static constexpr int Q_BYTES = Q_SMEM ? (D / 16) * NT * 32 * 8 : 0;
@@ -268,14 +267,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
-    // Lane i copies part i % 4 (K codes, V codes, K scales, V scales) of piece i / 4 of a unit; a
-    // piece is a page, or the unit's part of one.  Its page is looked up one unit ahead.
-    const int P = p.c.page_size, piece = min(P, kUnit), pieces = kUnit / piece;
-    const int part_ = lane % 4, t0 = lane / 4 * piece;
-    const int per = part_ < 2 ? D / 2 : D / 16;  // bytes of a token in this part
-    const int src_off = part_ == 0 ? 0 : part_ == 1 ? kv4_off_v(P, D) : part_ == 2 ? kv4_off_sk(P, D) : kv4_off_sv(P, D);
-    const int dst_off = (part_ == 0 ? 0 : part_ == 1 ? C::S_V : part_ == 2 ? C::S_SK : C::S_SV) + t0 * per;
-    const size_t block = kv4_block_bytes(P, D), page_bytes = block * p.c.H_kv;
+    // Lane i copies the block of page i of a unit (whole, also past the sequence's end).  Its page is
+    // looked up one unit ahead.
+    const int P = p.c.page_size, pieces = kUnit / P, t0 = lane * P;
+    const int block = kv4_block_bytes(P, D);
+    const size_t page_bytes = (size_t)block * p.c.H_kv;
     int unit = at.from;
     auto settle = [&]() {  // to the next unit there is; false: none
       while (unit >= at.to) {
@@ -287,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     };
     auto page_of = [&]() {
       const int tok = (at.s.first + unit) * kUnit + t0;
-      return lane < 4 * pieces && tok < at.s.len ? kv4_page(p.c, at.b, tok) : -2;
+      return lane < pieces && tok < at.s.len ? kv4_page(p.c, at.b, tok) : -2;
     };
     bool more = settle();
     int page = more ? page_of() : -2, n = 0;
@@ -295,11 +291,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     for (; more && ok; ++n) {
       const int stage = n % kStages;
       uint8_t* st = smem + stage * C::STAGE;
-      const int tok = (at.s.first + unit) * kUnit + t0;
-      // whole 16-token groups up to the sequence's end
-      const int bytes = page == -2 ? 0 : min(piece, (at.s.len - tok + 15) / 16 * 16) * per;
-      const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (at.vh / row_blocks) * block + src_off +
-                           (size_t)(tok & (P - 1)) * per;
+      const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (size_t)(at.vh / row_blocks) * block;
       const int have = page;
       ++unit;
       more = settle();
@@ -308,17 +300,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
       if (!ok) break;
       if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
         if (have == -1) {
-          if (part_ >= 2)
-            for (int o = 0; o < bytes; o += 4) *reinterpret_cast<uint32_t*>(st + dst_off + o) = 0u;
+          for (int o = kv4_off_sk(P, D); o < block; o += 16)
+            *reinterpret_cast<uint4*>(st + lane * block + o) = make_uint4(0u, 0u, 0u, 0u);
           atomicCAS(p.page_err, 0, p.site);
           fence_proxy_async_smem();
         }
         __syncwarp();
       }
-      const uint32_t all = __reduce_add_sync(0xffffffffu, have >= 0 ? bytes : 0);
+      const uint32_t all = __popc(__ballot_sync(0xffffffffu, have >= 0)) * block;
       if (lane == 0) mbar_arrive_expect_tx(&full[stage], all);
       __syncwarp();
-      if (have >= 0) bulk_load(st + dst_off, src, bytes, &full[stage]);
+      if (have >= 0) bulk_load(st + lane * block, src, block, &full[stage]);
     }
     // every copy this warp started must land before the CTA may exit: wait for the last ones
     for (int s = 0; s < kStages && s < n; ++s) {
@@ -333,11 +325,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
   float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* xl = xm + kWarps * C::ROWS;
   const int g = lane / 4, t = lane % 4;
-  const int off_k = (warp * kSub + g) * (D / 2) + t * (D / 8);
-  const int off_sk = C::S_SK + (warp * kSub + g) * (D / 16) + t * (D / 64);
+  // where this warp's tokens lie in a stage: tokens warp * 32 + 16 sub on start at token `in` of a
+  // page, and sub 1 follows in the same page or is the next one
+  const int P = p.c.page_size, in = warp * kSub & (P - 1);
+  const int at_page = warp * kSub / P * kv4_block_bytes(P, D);
+  const bool next_page = P == 16;
+  const int d_k = next_page ? kv4_block_bytes(16, D) : 16 * (D / 2), d_sk = next_page ? d_k : 16 * (D / 16);
+  const int off_k = at_page + (in + g) * (D / 2) + t * (D / 8);
+  const int off_sk = at_page + kv4_off_sk(P, D) + (in + g) * (D / 16) + t * (D / 64);
   // token pairs u = 4 n + t of this warp's tokens: the slot permutation depends on t alone
-  const int off_v = C::S_V + (warp * (kSub / 2) + t) * D + (g ^ kv4_slot_xor(t, D)) * (D / 8);
-  const int off_sv = C::S_SV + (warp * (kSub / 2) + t) * (D / 8) + 2 * (D == 128 ? g : g / 2);
+  const int off_v = at_page + kv4_off_v(P, D) + (in / 2 + t) * D + (g ^ kv4_slot_xor(t, D)) * (D / 8);
+  const int off_sv = at_page + kv4_off_sv(P, D) + (in / 2 + t) * (D / 8) + 2 * (D == 128 ? g : g / 2);
   const float sl2 = p.scale_log2 * kKv4SmallUndo;
   int i = 0;  // units consumed
   bool ok = true;
@@ -409,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const uint8_t* kc = st + off_k + (16 * sub + 8 * f) * (D / 2);
-            const uint8_t* ks = st + off_sk + (16 * sub + 8 * f) * (D / 16);
+            const uint8_t* kc = st + off_k + sub * d_k + 8 * f * (D / 2);
+            const uint8_t* ks = st + off_sk + sub * d_sk + 8 * f * (D / 16);
             if constexpr (D == 128) {
               *reinterpret_cast<uint4*>(wk[sub][f]) = *reinterpret_cast<const uint4*>(kc);
               sk[sub][f] = scale_pair(*reinterpret_cast<const unsigned short*>(ks));
@@ -518,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int u = 8 * sub + 4 * f;  // (+ t)
-            const uint8_t* va = st + off_v + u * D;
-            uint32_t two = *reinterpret_cast<const unsigned short*>(st + off_sv + u * (D / 8));
+            const uint8_t* va = st + off_v + sub * d_k + 4 * f * D;
+            uint32_t two = *reinterpret_cast<const unsigned short*>(st + off_sv + sub * d_sk + 4 * f * (D / 8));
             if constexpr (D == 128) {
               const uint4 w = *reinterpret_cast<const uint4*>(va);  // token 2u: x, y; token 2u + 1: z, w
               lo[f][0] = __byte_perm(w.x, w.z, 0x5410);
