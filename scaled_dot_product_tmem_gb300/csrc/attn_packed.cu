@@ -245,102 +245,109 @@ int launch_attn_fwd_packed(int d_qk, int d_v, const CUtensorMap& tq, const CUten
 //
 // D enters dS = P (dP - D) with the rounding of the stored bf16 O, 2^-8 |O|.  Against |dP| that
 // falls with the number n of keys a row sees (O is a mean of n values), while the row's dS
-// (P is about 1 / n) grows: a sequence's first rows carry most of the error, and they are many
-// in a batch of short sequences.  The first kExactRows rows that see at most kExactRows keys
-// therefore get D from O summed anew in fp32.  (Eight sequences of 1 to 512 rows: dQ and dK off
-// by 0.0026 of their norm from the stored O; the two roundings that stay, of dS and of the
-// result, are 0.0024.)
+// (P is about 1 / n) grows: rows that see few keys carry most of the error, and they are many in a
+// batch of short sequences and all there are under a short window.  Rows that see at most
+// kFewKeys keys therefore get D = sum_j P_ij (dO_i . v_j) from fp32 scores.  (Eight sequences of 1
+// to 512 rows: dQ and dK off by 0.0026 of their norm from the stored O; the two roundings that
+// stay, of dS and of the result, are 0.0024.)
 // =============================================================================
-constexpr int kExactRows = 16;
+constexpr int kFewKeys = 32;
 
-// Those rows see some of the sequence's first kExactRows keys only, so a block has the 16 rows of
-// Q and dO and the 16 of K and V in shared memory, and thread (i, j) forms P_ij (dO_i . v_j):
-// D_i is their sum over 16 lanes.  (The loads are on their way together with those of O.)
+// d (16 x 8 fp32) += a (16 x 16 bf16, rows) b (16 x 8 bf16, columns)
+__device__ __forceinline__ void mma_16816_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Products of 16 rows of a (lane / 4 and lane / 4 + 8, null: zeros) with 16 rows of b: out[c][e + 2 f] is row
+// lane / 4 + 8 f of a times row 8 c + 2 (lane % 4) + e of b.  Each lane has a quarter of the dims of
+// its rows; which dims share a step is free as long as both operands agree.
+template <int N>
+__device__ __forceinline__ void rows_product(const uint4* a0, const uint4* a1, const uint4* b0, const uint4* b1,
+                                             float (&out)[2][4]) {
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[c][e] = 0.f;
+#pragma unroll 1
+  for (int x = 0; x < N / 32; ++x) {
+    const uint4 p = a0 ? __ldg(a0 + x) : zero, q = a1 ? __ldg(a1 + x) : zero;
+    const uint4 r[2] = {b0 ? __ldg(b0 + x) : zero, b1 ? __ldg(b1 + x) : zero};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      mma_16816_acc(out[c], p.x, q.x, p.y, q.y, r[c].x, r[c].y);
+      mma_16816_acc(out[c], p.z, q.z, p.w, q.w, r[c].z, r[c].w);
+    }
+  }
+}
+
+// The part of D that every second 16 keys from 16 `part` on give the 16 rows from r0 on, counted from the
+// first key that one of them with few keys sees (they see keys among the 47 from there on, since
+// first keys rise by at most one a row).  A warp; rows with more keys get nothing that is used.
 template <int D_QK, int D_V>
-struct ExactRows {
-  static constexpr int CQ = D_QK / 8, CV = D_V / 8;  // 16-byte pieces of a row
-  static constexpr int NQ = (kExactRows * CQ + 255) / 256, NV = (kExactRows * CV + 255) / 256;
-  static constexpr int SQ = CQ + 1, SV = CV + 1;  // row strides in pieces: 8 rows fall on different banks
-  struct Smem {
-    uint4 q[kExactRows * SQ], k[kExactRows * SQ], v[kExactRows * SV], g[kExactRows * SV];
-  };
-  uint4 q[NQ], k[NQ], v[NV];
-  float nl;
-
-  __device__ __forceinline__ void load(const BwdParams& p, const PackedTile& e, int h) {
-    const int hk = h / p.G;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void few_keys_part(const BwdParams& p, const PackedTile& e, int h, int r0, int part,
+                                              float* out) {
+  const int lane = threadIdx.x % 32, t = lane % 4, hk = h / p.G;
+  const MaskSpec m{e.Lq, e.Lk, p.causal, p.window};
+  int lo[2], hi[2], first = 0x7fffff00, last = -1;
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-      const int x = threadIdx.x + u * 256, r = x / CQ, c = x % CQ;
-      q[u] = r < kExactRows && r < e.Lq
-                 ? __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)(e.q0 + r) * p.H_q + h) * D_QK) + c) : zero;
-      k[u] = r < kExactRows && r < e.Lk
-                 ? __ldg(reinterpret_cast<const uint4*>(p.k + ((size_t)(e.k0 + r) * p.H_kv + hk) * D_QK) + c) : zero;
+  for (int f = 0; f < 2; ++f) {
+    visible_keys<true>(m, r0 + lane / 4 + 8 * f, &lo[f], &hi[f]);
+    if (hi[f] - lo[f] >= kFewKeys) hi[f] = lo[f] - 1;  // not a row of few keys
+    if (hi[f] >= lo[f]) {
+      first = min(first, lo[f]);
+      last = max(last, hi[f]);
     }
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int x = threadIdx.x + u * 256, r = x / CV, c = x % CV;
-      v[u] = r < kExactRows && r < e.Lk
-                 ? __ldg(reinterpret_cast<const uint4*>(p.v + ((size_t)(e.k0 + r) * p.H_kv + hk) * D_V) + c) : zero;
-    }
-    const int i = threadIdx.x / 16;
-    nl = i < e.Lq ? -p.lse[(size_t)h * p.S_q + e.q0 + i] * kLog2e : 0.f;
   }
-  __device__ __forceinline__ void store(Smem& m) const {
+  first = __reduce_min_sync(0xffffffffu, first);
+  last = __reduce_max_sync(0xffffffffu, last);
+  float d[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int k0 = first + 16 * part; k0 <= last; k0 += 32) {  // (no such row: first is past last)
+    const int key = k0 + lane / 4;
+    const uint4 *q[2], *g[2], *k[2], *v[2];
+    float nl[2];
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-      const int x = threadIdx.x + u * 256, r = x / CQ, c = x % CQ;
-      if (r < kExactRows) {
-        m.q[r * SQ + c] = q[u];
-        m.k[r * SQ + c] = k[u];
+    for (int f = 0; f < 2; ++f) {
+      const int i = r0 + lane / 4 + 8 * f;
+      const bool row = i < e.Lq, has = key + 8 * f < e.Lk;
+      const size_t qr = (size_t)(e.q0 + (row ? i : 0)) * p.H_q + h;
+      const size_t kr = (size_t)(e.k0 + (has ? key + 8 * f : 0)) * p.H_kv + hk;
+      q[f] = row ? reinterpret_cast<const uint4*>(p.q + qr * D_QK + t * (D_QK / 4)) : nullptr;
+      g[f] = row ? reinterpret_cast<const uint4*>(p.dout + qr * D_V + t * (D_V / 4)) : nullptr;
+      k[f] = has ? reinterpret_cast<const uint4*>(p.k + kr * D_QK + t * (D_QK / 4)) : nullptr;
+      v[f] = has ? reinterpret_cast<const uint4*>(p.v + kr * D_V + t * (D_V / 4)) : nullptr;
+      const float l = row ? p.lse[(size_t)h * p.S_q + e.q0 + i] : 0.f;
+      nl[f] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+    }
+    float s[2][4], dp[2][4];
+    rows_product<D_QK>(q[0], q[1], k[0], k[1], s);
+    rows_product<D_V>(g[0], g[1], v[0], v[1], dp);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int f = x / 2, j = k0 + 8 * c + 2 * t + x % 2;
+        if (j >= lo[f] && j <= hi[f]) d[f] = fmaf(ex2(fmaf(s[c][x], p.scale_log2, nl[f])), dp[c][x], d[f]);
       }
-    }
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int x = threadIdx.x + u * 256, r = x / CV, c = x % CV;
-      if (r < kExactRows) m.v[r * SV + c] = v[u];
-    }
   }
-  template <int N>
-  __device__ __forceinline__ static float dot(const uint4* a, const uint4* b) {
-    float s[2] = {0.f, 0.f};
-#pragma unroll 4
-    for (int c = 0; c < N; ++c) {
-      const uint4 x = a[c], y = b[c];
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        s[0] = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), s[0]);
-        s[1] = fmaf(__uint_as_float(xs[w] & 0xFFFF0000u), __uint_as_float(ys[w] & 0xFFFF0000u), s[1]);
-      }
-    }
-    return s[0] + s[1];
-  }
-  // (every thread of the block, after store() and a barrier)
-  __device__ __forceinline__ void sums(const BwdParams& p, const PackedTile& e, const Smem& m, float* dsum) const {
-    const int i = threadIdx.x / 16, j = threadIdx.x % 16;
-    int lo = 0, hi = -1;
-    visible_keys<true>(MaskSpec{e.Lq, e.Lk, p.causal, p.window}, i, &lo, &hi);
-    const int n = hi - lo + 1;
-    const bool few = n > 0 && n <= kExactRows, see = few && j >= lo && j <= hi;
-    float t = 0.f;
-    if (__any_sync(0xffffffffu, see)) {
-      const float s = dot<CQ>(m.q + i * SQ, m.k + j * SQ), dp = dot<CV>(m.g + i * SV, m.v + j * SV);
-      t = see ? ex2(fmaf(s, p.scale_log2, nl)) * dp : 0.f;
+  for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int off = 8; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    }
-    if (few && j == 0) dsum[i] = t;
+    for (int off = 1; off < 4; off <<= 1) d[f] += __shfl_xor_sync(0xffffffffu, d[f], off);
+  if (t == 0) {
+    out[lane / 4] = d[0];
+    out[lane / 4 + 8] = d[1];
   }
-};
+}
 
 template <int D_QK, int D_V>
-__global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(256, 5) packed_preprocess_kernel(const BwdParams p) {
   constexpr int TPR = D_V / 8, RPP = 256 / TPR, TILE = 64, NR = TILE / RPP;
-  using X = ExactRows<D_QK, D_V>;
-  __shared__ float dsum[TILE];
-  __shared__ typename X::Smem xs;
+  __shared__ float dsum[TILE], few_sum[2][TILE];
   const int h = blockIdx.y;
   grid_launch_dependents();
   grid_wait();  // the plan
@@ -348,8 +355,6 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
     const PackedTile e = load_packed_tile(p.tiles_q, blockIdx.x / 2);
     const int i0 = e.m0 + (blockIdx.x % 2) * TILE, sub = threadIdx.x % TPR;
     uint4 a[NR], g[NR];
-    X exact;
-    if (i0 == 0) exact.load(p, e, h);
 #pragma unroll
     for (int k = 0; k < NR; ++k) {
       const int i = i0 + threadIdx.x / TPR + k * RPP;
@@ -375,20 +380,23 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(const BwdParams 
       for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
       if (sub == 0) dsum[threadIdx.x / TPR + k * RPP] = acc;
     }
-    if (i0 == 0) {
-      static_assert(RPP >= kExactRows, "the exact rows are rows of the first pass");
-      const int r = threadIdx.x / TPR;
-      if (r < kExactRows) xs.g[r * X::SV + sub] = g[0];
-      exact.store(xs);
-      __syncthreads();
-      exact.sums(p, e, xs, dsum);
+    // rows of few keys: the first of a sequence, all under a short window, and where keys are few or
+    // end early
+    const bool few = i0 < kFewKeys || (p.window >= 0 && (p.window < kFewKeys || i0 + TILE > e.Lk)) || e.Lk <= kFewKeys;
+    if (few) {
+      const int warp = threadIdx.x / 32;
+      few_keys_part<D_QK, D_V>(p, e, h, i0 + warp / 2 * 16, warp % 2, &few_sum[warp % 2][warp / 2 * 16]);
     }
     __syncthreads();
     if (threadIdx.x < TILE) {
       const int i = i0 + threadIdx.x;
       const bool real = i < e.Lq;
       const size_t w = (size_t)h * p.S_pad + e.ws0 + i;
-      p.Dsum[w] = real ? dsum[threadIdx.x] : 0.f;
+      int lo = 0, hi = -1;
+      visible_keys<true>(MaskSpec{e.Lq, e.Lk, p.causal, p.window}, i, &lo, &hi);
+      const bool exact = few && hi >= lo && hi - lo < kFewKeys;
+      const float d = exact ? few_sum[0][threadIdx.x] + few_sum[1][threadIdx.x] : dsum[threadIdx.x];
+      p.Dsum[w] = real ? d : 0.f;
       const float l = real ? p.lse[(size_t)h * p.S_q + e.q0 + i] : -INFINITY;
       p.nlse2[w] = l == -INFINITY ? -INFINITY : -l * kLog2e;
     }

@@ -281,6 +281,25 @@ def test_many_sequences_with_and_without_keys(dims, causal):
         assert torch.equal(t, again[n]), n
 
 
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("window,lens_kv", [(0, None), (1, None), (5, None), (15, None), (16, None), (31, None),
+                                            (-1, [3, 1, 9, 2]), (-1, [32, 17, 16, 31]), (40, [90, 60, 130, 20])])
+def test_gradients_of_rows_that_see_few_keys(dims, window, lens_kv):
+    """dS and the results are rounded to bf16.  A rounding is off by at most 2^-8 of a value, evenly
+    over that step: 2^-8 / sqrt(3) for a mantissa of 1, with mantissas spread over [1, 2) 0.72 of
+    it, 0.00163 relative L2; two of them 0.0023, and with a tenth more for samples of 10^4 values
+    and the fp32 arithmetic 0.0026.  D from the stored bf16 O adds a third error of that size
+    where rows see few keys, so they get it from fp32 scores."""
+    lens = [150, 70, 201, 64]
+    x = _inputs(lens, lens_kv or lens, 4, 2, *dims, seed=31)
+    kw = dict(causal=True, window=window, softmax_type=OFF_BY_ONE)
+    got = _run(x, _cu(lens), _cu(lens_kv) if lens_kv else None, **kw)
+    ref = _reference(x, lens, lens_kv or lens, **kw)
+    for n in ("dq", "dk"):
+        e = rel_l2(got[n].double().cpu().numpy(), ref[n])
+        assert e <= 0.0026, f"{n}: {e}"
+
+
 def test_more_sequences_than_plan_threads_and_a_long_one():
     """3,000 short sequences around one of 5,000 rows; a sample of them against the oracle."""
     g = np.random.default_rng(1)
