@@ -524,3 +524,34 @@ def test_prefill_of_a_continuation_over_a_cached_prefix():
     bound = 2.0 ** -7 * (o2.float().abs() + vc.float().abs().max())
     assert torch.all((o[:, 0].float() - o2.float()).abs() <= bound)
     assert (lse[:, :, 0].t() - lse2).abs().max() <= TOL_LSE
+
+
+def test_one_workspace_for_batches_after_another():
+    """Work lists are written while the kernels that read them are already set up: forward and backward of
+    batches with other offsets, one after another in the same workspaces, never see an earlier list."""
+    sdpa = _sdpa()
+    T, H, H_kv, d = 5000, 8, 2, 64
+    x = _inputs([T], [T], H, H_kv, d, d, 47)
+    q, k, v, do = (x[n].cuda() for n in ("q", "k", "v", "dout"))
+    off = x["off"].cuda()
+    kw = dict(window=300, softmax_type=LEARNABLE, softmax_offset=off)
+    rng = np.random.default_rng(3)
+    batches = []
+    for _ in range(6):
+        cut = np.sort(rng.integers(0, T + 1, 39))
+        batches.append(_i32([0] + cut.tolist() + [T]))
+    alone = []
+    for cu in batches:
+        o, lse = sdpa.sdpa_forward_packed(q, k, v, cu, **kw)
+        alone.append((o, lse) + sdpa.sdpa_backward_packed(q, k, v, o, do, lse, cu, **kw))
+    ws = [torch.empty(sdpa.attn_packed_workspace_size(40, T, T, H, H_kv, d, d, b), dtype=torch.uint8, device="cuda")
+          for b in (False, True)]
+    got = []
+    for i in range(30):
+        cu = batches[i % 6]
+        o, lse = sdpa.sdpa_forward_packed(q, k, v, cu, workspace=ws[0], **kw)
+        got.append((o, lse) + sdpa.sdpa_backward_packed(q, k, v, o, do, lse, cu, workspace=ws[1], **kw))
+    _clean()
+    for i, res in enumerate(got):
+        for a, b in zip(res, alone[i % 6]):
+            assert torch.equal(a, b), i
