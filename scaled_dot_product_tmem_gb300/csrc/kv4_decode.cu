@@ -34,6 +34,7 @@
 // the chain lengths - page - copy - products - join.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "attn_common.cuh"
 #include "attn_kernels.h"
@@ -509,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
             }
         }
         // ---- outputs: lane (g, t) decodes eighth g of the head dim of token pairs t and t + 4
+        uint32_t nans = 0u;  // on an edge: its tokens with a NaN scale (a bit for each of the warp's 32)
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
           uint32_t lo[2][MT / 4], hi[2][MT / 4];  // [pair][word]: both tokens' nibbles 0-3, 4-7
@@ -533,6 +535,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
               const int j = k0 + 2 * (u + t);
               if (j > len - 1 || j < lo_min) two &= 0xFF00u;
               if (j + 1 > len - 1 || j + 1 < lo_min) two &= 0x00FFu;
+              // a row that does not see a token has P = 0, but 0 times NaN is NaN: such a token adds
+              // nothing here, and the rows that see it get their NaN below
+              if ((two & 0x00F8u) == 0x00F8u) {
+                nans |= 1u << (2 * (u + t));
+                two &= 0xFF00u;
+              }
+              if ((two & 0xF800u) == 0xF800u) {
+                nans |= 2u << (2 * (u + t));
+                two &= 0x00FFu;
+              }
             }
             kv[f] = small_scales(scale_pair(two));
           }
@@ -553,6 +565,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_16816(acc[mt][nt], a[0], a[1], a[2], a[3], pb[sub][nt][0], pb[sub][nt][1]);
           }
+        }
+        if (edge && __any_sync(0xffffffffu, nans != 0u)) {  // (rare)
+          nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
+          nans |= __shfl_xor_sync(0xffffffffu, nans, 2);  // all 32 tokens, eighth g
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int pos = len - p.S_q + min(r0 + 8 * nt + 2 * t + e, R - 1) / G;
+              const int lo = p.window >= 0 && pos > p.window ? pos - p.window : 0;
+              if (pos < k0 || lo - k0 > 31) continue;  // the row sees none of the 32
+              const int from = max(lo - k0, 0), to = min(pos - k0, 31);
+              if (nans & (0xffffffffu << from) & (0xffffffffu >> (31 - to))) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[mt][nt][e] = acc[mt][nt][e + 2] = NAN;
+              }
+            }
         }
       }
       __syncwarp();  // every lane has read the stage: it may be filled again

@@ -479,3 +479,70 @@ def test_serving_loop_captured_and_on_another_stream():
     k, v = (np.concatenate([torch.cat([toks[w][b], new[w][:, b]]).double().numpy() for b in range(3)]) for w in (0, 1))
     c.k, c.v, c.at = kv4.held(k), kv4.held(v), np.cumsum([0] + c.lens)
     _check_decode(c, qs[-1], eager[-1][0], eager[-1][1])
+
+
+def _spoil(c, places):
+    """The value of token `pos` of entry b, head h, gets a NaN in dim x: for (b, pos, h, x) in places."""
+    sdpa = _sdpa()
+    for b, pos, h, x in places:
+        at = int(c.at[b]) + pos
+        c.vt[at, h, x] = float("nan")
+        one = [int(i == b) for i in range(len(c.lens))]
+        start = [pos if i == b else 0 for i in range(len(c.lens))]
+        sdpa.attn_kv4_append(c.kt[at:at + 1].cuda(), c.vt[at:at + 1].cuda(), _cu(one), c.pool, c.table, _i32(start))
+        c.v[at] = kv4.held(c.vt[at].double().numpy())
+
+
+def _check_decode_with_nans(c, q, o, lse, **kw):
+    """o is NaN where the oracle's is, and there only; the rest within the bounds of _check_decode."""
+    q, o, lse = q.double().cpu().numpy(), o.double().cpu().numpy(), lse.double().cpu().numpy()
+    count = 0
+    for b, L in enumerate(c.lens):
+        sl = slice(int(c.at[b]), int(c.at[b + 1]))
+        ro, rl, a, mag = kv4.decode(q[b], c.k[sl], c.v[sl], L, **kw)
+        nan = np.isnan(ro)
+        count += nan.sum()
+        assert np.array_equal(np.isnan(o[b]), nan), f"entry {b} (len {L}): NaN in other places"
+        bound = np.where(nan, 0, 2.0 ** -8 * (a + np.abs(ro)) + 2.0 ** -14 * a)
+        assert np.all(np.where(nan, 0, np.abs(o[b] - ro)) <= bound), f"entry {b} (len {L})"
+        fin = np.isfinite(rl)
+        assert np.array_equal(lse[b][~fin], rl[~fin])
+        tol = 2.0 ** -17 * mag + 2.0 ** -18 * (1 + np.abs(np.where(fin, rl, 0)))
+        assert np.all(np.abs(np.where(fin, lse[b], 0) - np.where(fin, rl, 0)) <= tol)
+    return count
+
+
+# name, lens, S_q, H_q, H_kv, d, page, window, tokens from the end that hold a NaN
+NAN_HIDDEN = [
+    ("newest_of_two", [40, 33, 128, 129], 2, 4, 2, 64, 16, -1, [1]),
+    ("newest_of_two_d128", [40, 33, 128, 129], 2, 8, 2, 128, 64, -1, [1]),
+    ("middle_of_four", [70, 4, 257], 4, 4, 2, 128, 32, -1, [2]),
+    ("window_leaves_it", [200, 61, 300], 3, 4, 2, 128, 64, 20, [23, 21]),
+    ("window_leaves_it_d64", [200, 61, 300], 3, 8, 1, 64, 16, 40, [43, 42]),
+    ("both_ends", [160, 500], 5, 6, 2, 64, 128, 33, [37, 1]),
+    ("rows_16", [90, 300], 4, 4, 1, 128, 16, -1, [1, 2]),
+    ("rows_32_window", [90, 300, 33], 4, 16, 2, 128, 64, 64, [1, 67]),
+    ("rows_past_32", [150, 70], 50, 4, 2, 64, 32, -1, [1, 25, 49]),
+    ("rows_past_32_window", [400], 70, 8, 2, 128, 64, 100, [1, 65, 130]),
+    ("seen_by_all", [90, 65], 2, 4, 2, 64, 16, -1, [2, 30]),
+    ("long", [6000, 1], 3, 4, 1, 128, 64, 4000, [1, 2, 4003, 3000]),
+    ("more_queries_than_tokens", [2, 1, 9], 4, 4, 2, 64, 16, -1, [1]),
+]
+
+
+@pytest.mark.parametrize("case", NAN_HIDDEN, ids=[c[0] for c in NAN_HIDDEN])
+def test_decode_nan_reaches_only_queries_that_see_its_token(case):
+    """A token held as NaN reaches the queries that see it, in its own 16 dims and kv head, and no other
+    query: not those before a proposed token, nor those whose window it has left."""
+    name, lens, S_q, H_q, H_kv, d, page, window, back = case
+    c = Cache(lens, H_kv, d, page, seed=len(name))
+    places = [(b, L - n, (b + n) % H_kv, (37 * n + b) % d) for b, L in enumerate(lens) for n in back if n <= L]
+    _spoil(c, places)
+    q = torch.randn((len(lens), S_q, H_q, d), generator=torch.Generator().manual_seed(51)).to(torch.bfloat16)
+    sdpa = _sdpa()
+    o, lse = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, c.table, c.seq_lens, window=window, softmax_type="off_by_one")
+    o2, lse2 = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, c.table, c.seq_lens, window=window, softmax_type="off_by_one")
+    _clean()
+    assert torch.equal(torch.nan_to_num(o), torch.nan_to_num(o2)) and torch.equal(lse, lse2)
+    n = _check_decode_with_nans(c, q, o, lse, window=window, sink=np.zeros(H_q))
+    assert n > 0 and n < o.numel()
