@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeParams p, 
       const float f = m == -INFINITY ? 0.f : ex2(m - mn), w = mi == -INFINITY ? 0.f : ex2(mi - mn);
       l = (m == -INFINITY ? l : l * f) + (mi == -INFINITY ? li : li * w);  // (no key: 0, or a NaN that has to stay)
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] = a[e] * f + (w == 0.f ? 0.f : v[e] * w);
+      for (int e = 0; e < E; ++e) a[e] = a[e] * f + v[e] * w;  // (a NaN stays, also of a piece without weight)
       m = mn;
     }
   };

@@ -546,3 +546,28 @@ def test_decode_nan_reaches_only_queries_that_see_its_token(case):
     assert torch.equal(torch.nan_to_num(o), torch.nan_to_num(o2)) and torch.equal(lse, lse2)
     n = _check_decode_with_nans(c, q, o, lse, window=window, sink=np.zeros(H_q))
     assert n > 0 and n < o.numel()
+
+
+def test_decode_nan_of_a_token_without_weight_is_kept():
+    """A sequence whose first tokens outweigh all others by more than fp32 holds: a NaN value that a
+    query sees reaches it from any place in the sequence, however little its token weighs."""
+    sdpa = _sdpa()
+    L, H, d, page = 6000, 4, 128, 64
+    c = Cache([L], 1, d, page, seed=61)
+    q = torch.randn((1, 1, H, d), generator=torch.Generator().manual_seed(62)).to(torch.bfloat16)
+    # keys along the sum of the queries: scores of the first tokens above the others' by hundreds
+    c.kt[:64] = (q[0, 0].float().sum(0) * 20).to(torch.bfloat16)
+    sdpa.attn_kv4_append(c.kt.cuda(), c.vt.cuda(), _i32([0, L]), c.pool, c.table, _i32([0]))
+    s = q[0, 0].double().numpy() @ kv4.held(c.kt.double().numpy())[:, 0].T / np.sqrt(d)
+    assert (s[:, :64].min(1) - s[:, 64:].max(1)).min() > 128  # exp2(-128 log2(e)) is 0 in fp32
+    bad = c.vt[:1].clone()
+    bad[0, 0, 20] = float("nan")
+    outs = []
+    for at in range(64, L, 101):
+        sdpa.attn_kv4_append(c.kt[at:at + 1].cuda(), bad.cuda(), _i32([0, 1]), c.pool, c.table, _i32([at]))
+        outs.append((at, *sdpa.sdpa_decode_kv4(q.cuda(), c.pool, c.table, c.seq_lens)))
+        sdpa.attn_kv4_append(c.kt[at:at + 1].cuda(), c.vt[at:at + 1].cuda(), _i32([0, 1]), c.pool, c.table, _i32([at]))
+    _clean()
+    for at, o, lse in outs:
+        assert torch.isnan(o[0, 0, :, 16:32]).all(), f"token {at}"
+        assert torch.isfinite(o[0, 0, :, :16]).all() and torch.isfinite(o[0, 0, :, 32:]).all() and torch.isfinite(lse).all()
