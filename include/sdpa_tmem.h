@@ -438,8 +438,8 @@ int attn_bwd_fp8(const void* q8, const void* k8, const void* v8, const void* do8
  * attn_kv4_decode: q bf16 [B, S_q, H_q, d]: the S_q newest tokens of every sequence, whose
  *   seq_lens[b] tokens (these included; device int32 [B], clamped to [0, max_pages *
  *   page_size]) are in the cache.  Query s sits at pos = seq_lens[b] - S_q + s and sees the
- *   keys j <= pos, and j >= pos - window when window >= 0.  o bf16 [B, S_q, H_q, d]; lse
- *   fp32 [B, H_q, S_q] (may be NULL).  A query that sees no key gets o = 0 and lse = the
+ *   keys j <= pos, and j >= pos - window when window >= 0.  Pages of which no query sees a
+ *   token are not looked up.  o bf16 [B, S_q, H_q, d]; lse fp32 [B, H_q, S_q] (may be NULL).  A query that sees no key gets o = 0 and lse = the
  *   sink logit.  scale, window, softmax_type and softmax_offset as for attn_fwd
  *   (ATTN_ERR_UNSUPPORTED for a finite scale above 1e30).
  *   workspace: device scratch of attn_kv4_decode_workspace_size() bytes, 256-byte aligned,

@@ -94,15 +94,16 @@ __device__ __forceinline__ Kv4Sums kv4_finish(const Kv4DecodeParams& p, int h, f
 // The keys of one unit row and the sizes of one sequence.
 struct Seq {
   int len;    // tokens in the cache
-  int first;  // first unit any query sees
+  int lo;     // first token any query sees
+  int first;  // its unit
   int n;      // units
   __device__ __forceinline__ int numbers() const { return n > 0 ? n + kSegCost : 0; }
 };
 __device__ __forceinline__ Seq seq_of(const Kv4DecodeParams& p, int b) {
   Seq s;
   s.len = entry_len(p.seq_lens, b, p.c.max_pages * p.c.page_size);
-  const int lo = p.window >= 0 && s.len - p.S_q > p.window ? s.len - p.S_q - p.window : 0;  // the first query's
-  s.first = lo / kUnit;
+  s.lo = p.window >= 0 && s.len - p.S_q > p.window ? s.len - p.S_q - p.window : 0;  // the first query's
+  s.first = s.lo / kUnit;
   s.n = s.len > 0 ? (s.len - 1) / kUnit - s.first + 1 : 0;
   return s;
 }
@@ -268,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
-    // Lane i copies the block of page i of a unit (whole, also past the sequence's end).  Its page is
-    // looked up one unit ahead.
+    // Lane i copies the block of page i of a unit (whole, also past the sequence's end), if some query
+    // sees a token of it: the pages before a window may be gone from the table.  Its page is looked up
+    // one unit ahead.
     const int P = p.c.page_size, pieces = kUnit / P, t0 = lane * P;
     const int block = kv4_block_bytes(P, D);
     const size_t page_bytes = (size_t)block * p.c.H_kv;
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     };
     auto page_of = [&]() {
       const int tok = (at.s.first + unit) * kUnit + t0;
-      return lane < pieces && tok < at.s.len ? kv4_page(p.c, at.b, tok) : -2;
+      return lane < pieces && tok < at.s.len && tok + P > at.s.lo ? kv4_page(p.c, at.b, tok) : -2;
     };
     bool more = settle();
     int page = more ? page_of() : -2, n = 0;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
     // keys that every row sees: [lo_max, hi_min]; that some row sees: [lo_min, len - 1]
     const int hi_min = len - p.S_q + r0 / G;
     const int lo_max = p.window >= 0 ? len - 1 - p.window : 0;
-    const int lo_min = p.window >= 0 && len - p.S_q > p.window ? len - p.S_q - p.window : 0;
+    const int lo_min = at.s.lo;
     float acc[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {

@@ -571,3 +571,31 @@ def test_decode_nan_of_a_token_without_weight_is_kept():
     for at, o, lse in outs:
         assert torch.isnan(o[0, 0, :, 16:32]).all(), f"token {at}"
         assert torch.isfinite(o[0, 0, :, :16]).all() and torch.isfinite(o[0, 0, :, 32:]).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("page,d", [(16, 64), (32, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("window,S_q", [(0, 1), (1, 2), (15, 1), (40, 3), (127, 1), (200, 40)])
+def test_decode_needs_no_page_before_the_window(page, d, window, S_q):
+    """Pages whose tokens every query's window has left may be gone from the table (a negative entry, or one
+    outside the pool): nothing is reported, and the outputs are those of the whole cache."""
+    sdpa = _sdpa()
+    lens = [1, 127, 128, 129, 255, 256, 270, 333, 600, 641, 0, 1000]
+    c = Cache(lens, 2, d, page, seed=window)
+    q = torch.randn((len(lens), S_q, 4, d), generator=torch.Generator().manual_seed(71)).to(torch.bfloat16)
+    whole = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, c.table, c.seq_lens, window=window)
+    table, gone = c.table.clone(), 0
+    for b, L in enumerate(lens):
+        n = max(0, L - S_q - window) // page  # pages whose last token lies before the first query's window
+        table[b, :n] = torch.tensor([(-1, c.pool.shape[0], -2 ** 31, 2 ** 31 - 1)[i % 4] for i in range(n)], dtype=torch.int32)
+        gone += n
+    assert gone > 0
+    o, lse = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, table, c.seq_lens, window=window)
+    _clean()
+    assert torch.equal(o, whole[0]) and torch.equal(lse, whole[1])
+    _check_decode(c, q, o, lse, window=window)
+    # the first page that the window reaches is still needed
+    b = lens.index(1000)
+    table[b, max(0, 1000 - S_q - window) // page] = -1
+    sdpa.sdpa_decode_kv4(q.cuda(), c.pool, table, c.seq_lens, window=window)
+    torch.cuda.synchronize()
+    assert sdpa.attn_last_device_error() == (7, 3)
