@@ -145,8 +145,9 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
  * likewise, and computes as a batch entry of its own: attn_fwd / attn_bwd with B = 1 on
  * its rows (masks count positions from the sequence's first row).  cu_seqlens_kv NULL:
  * the same as cu_seqlens_q.  A sequence may have no queries, no keys or neither; a row
- * that sees no key gets o = 0 and lse = the sink logit.  lse: fp32 [H_q, T_q].  Values of
- * one sequence, infinities and NaN included, never reach another sequence's results.
+ * that sees no key gets o = 0 and lse = the sink logit, one with a NaN score lse = NaN (where
+ * attn_fwd gives -inf).  lse: fp32 [H_q, T_q].  Values of one sequence, infinities and NaN
+ * included, never reach another sequence's results.
  * Offsets are clamped to [0, T] and to their running maximum.  Rows that belong to no
  * sequence (past the last one, or before cu_seqlens[0]) are left alone; with zero_rest != 0
  * they get o, dq, dk, dv = 0 and lse = -inf.

@@ -764,7 +764,9 @@ __global__ void __launch_bounds__(320, 1)
       }
       if (row_ok) {
         const float m_sub = (m_run == -INFINITY) ? 0.f : m_run;
-        p.lse[((size_t)b * p.H_q + h) * p.S_q + T.q0 + i] = l > 0.f ? (m_sub + lg2(l)) * kLn2 : -INFINITY;
+        // (packed: the sum of a row with a NaN score is NaN, and so is its log)
+        const float none = PK && l != l ? l : -INFINITY;
+        p.lse[((size_t)b * p.H_q + h) * p.S_q + T.q0 + i] = l > 0.f ? (m_sub + lg2(l)) * kLn2 : none;
       }
     }
     if constexpr (PK) {

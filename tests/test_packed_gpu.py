@@ -555,3 +555,31 @@ def test_one_workspace_for_batches_after_another():
     for i, res in enumerate(got):
         for a, b in zip(res, alone[i % 6]):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)])
+def test_lse_of_a_row_with_a_nan_score_is_nan(dims):
+    """-inf would say that the row sees no key.  A query's NaN makes its own row's lse and o NaN, a key's
+    those of the rows that see it; the other rows' lse is as without it."""
+    sdpa = _sdpa()
+    lens = [150, 300, 40]
+    x = _inputs(lens, lens, 4, 2, *dims, seed=53)
+    cu = _cu(lens)
+    for st in (VANILLA, OFF_BY_ONE):
+        base = sdpa.sdpa_forward_packed(*(x[n].cuda() for n in "qkv"), cu, softmax_type=st)
+        q, k = x["q"].clone(), x["k"].clone()
+        q[7, 1, 3] = q[449, 2, 60] = q[489, 0, 0] = float("nan")
+        o, lse = sdpa.sdpa_forward_packed(q.cuda(), k.cuda(), x["v"].cuda(), cu, softmax_type=st)
+        bad = torch.zeros((4, 490), dtype=torch.bool, device="cuda")
+        bad[1, 7] = bad[2, 449] = bad[0, 489] = True
+        _clean()
+        assert torch.equal(torch.isnan(lse), bad) and torch.isnan(o[7, 1]).all()
+        assert torch.equal(lse[~bad], base[1][~bad])
+        k[150 + 133, 1, 5] = float("nan")  # key 133 of the second sequence, heads 2 and 3
+        o, lse = sdpa.sdpa_forward_packed(x["q"].cuda(), k.cuda(), x["v"].cuda(), cu, softmax_type=st, window=90)
+        base = sdpa.sdpa_forward_packed(*(x[n].cuda() for n in "qkv"), cu, softmax_type=st, window=90)
+        bad.zero_()
+        bad[2:, 150 + 133:150 + 133 + 91] = True
+        _clean()
+        assert torch.equal(torch.isnan(lse), bad) and torch.isnan(o[283:374, 2:]).all()
+        assert torch.equal(lse[~bad], base[1][~bad])
