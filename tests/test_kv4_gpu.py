@@ -599,3 +599,65 @@ def test_decode_needs_no_page_before_the_window(page, d, window, S_q):
     sdpa.sdpa_decode_kv4(q.cuda(), c.pool, table, c.seq_lens, window=window)
     torch.cuda.synchronize()
     assert sdpa.attn_last_device_error() == (7, 3)
+
+
+# sequences: up to 32 fit one lane each, beyond that they are taken in groups of 32
+@pytest.mark.parametrize("B", [31, 32, 33, 64, 65, 97, 200])
+@pytest.mark.parametrize("window,S_q,sink", [(-1, 1, "vanilla"), (60, 3, "learnable")])
+def test_decode_of_many_sequences(B, window, S_q, sink):
+    """Empty sequences across a border between groups, a long one that spans several blocks in the
+    middle, the rest of any short length."""
+    sdpa = _sdpa()
+    H_q, H_kv, d, page = 4, 2, 64, 32
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 200, B)
+    lens[28:35] = 0
+    if B > 64:
+        lens[60:66] = 0
+    lens[B // 2] = 5000
+    lens[-1] = 77
+    lens = lens.tolist()
+    c = Cache(lens, H_kv, d, page, seed=B)
+    gen = torch.Generator().manual_seed(81)
+    q = torch.randn((B, S_q, H_q, d), generator=gen).to(torch.bfloat16)
+    off = torch.randn(H_q, generator=gen)
+    kw = dict(window=window, softmax_type=sink, softmax_offset=off.cuda() if sink == "learnable" else None)
+    o, lse = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, c.table, c.seq_lens, **kw)
+    o2, lse2 = sdpa.sdpa_decode_kv4(q.cuda(), c.pool, c.table, c.seq_lens, **kw)
+    _clean()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _check_decode(c, q, o, lse, window=window, sink=off.double().numpy() if sink == "learnable" else None)
+
+
+@pytest.mark.parametrize("B", [16, 17, 18, 256, 257, 258, 1000, 4100])
+def test_append_and_gather_of_many_sequences(B):
+    """The search for a row's sequence takes 16 ways a step: one more step past 16, 256 and 4096
+    sequences.  Runs of empty sequences, and rows of no sequence behind the last."""
+    sdpa = _sdpa()
+    H, d, page = 1, 64, 16
+    rng = np.random.default_rng(B)
+    new = np.where(rng.random(B) < 0.3, 0, rng.integers(0, 4, B))
+    new[B // 3:B // 3 + 40] = 0
+    new[-1] = 2
+    start = rng.integers(0, 30, B)
+    T = int(new.sum())
+    gen = torch.Generator().manual_seed(B)
+    table, n_pages = _table(gen, [-(-int(a + b) // page) for a, b in zip(start, new)])
+    k, v = (torch.randn((T + 5, H, d), generator=gen).to(torch.bfloat16) for _ in range(2))
+    pool = torch.full((n_pages, H, sdpa.kv4_block_bytes(page, d)), 0xA5, dtype=torch.uint8, device="cuda")
+    ref = pool.cpu().numpy().copy()
+    cu, st = _cu(new.tolist()), _i32(start.tolist())
+    sdpa.attn_kv4_append(k.cuda(), v.cuda(), cu, pool, table.cuda(), st)
+    t = 0
+    for b in range(B):
+        for i in range(int(new[b])):
+            pos = int(start[b]) + i
+            kv4.write_token(ref[table[b, pos // page], 0], pos % page, k[t, 0].double().numpy(), v[t, 0].double().numpy(), page)
+            t += 1
+    _clean()
+    assert np.array_equal(pool.cpu().numpy(), ref)
+    ko, vo = sdpa.kv4_gather(pool, table.cuda(), cu, st, T + 5, d)
+    _clean()
+    assert np.array_equal(ko[:T].double().cpu().numpy(), kv4.held(k[:T].double().numpy()))
+    assert np.array_equal(vo[:T].double().cpu().numpy(), kv4.held(v[:T].double().numpy()))
+    assert torch.all(ko[T:] == 0) and torch.all(vo[T:] == 0)
