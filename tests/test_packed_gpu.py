@@ -583,3 +583,91 @@ def test_lse_of_a_row_with_a_nan_score_is_nan(dims):
         _clean()
         assert torch.equal(torch.isnan(lse), bad) and torch.isnan(o[283:374, 2:]).all()
         assert torch.equal(lse[~bad], base[1][~bad])
+
+
+def _fill_cache(k, v, lens, page):
+    """The packed keys and values in a new 4-bit cache: pool, page table."""
+    sdpa = _sdpa()
+    need = [-(-n // page) for n in lens]
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    pool = sdpa.kv4_pool(at, k.shape[1], k.shape[2], page)
+    sdpa.attn_kv4_append(k, v, _cu(lens), pool, table.cuda(), _i32([0] * len(lens)))
+    return pool, table.cuda()
+
+
+def _probabilities(q, k, keys):
+    """fp64 softmax of q [n, H, d] over k [m, H_kv, d], row i over the first keys[i] keys; [H, n, m]."""
+    q, k = q.double().cpu().numpy(), k.double().cpu().numpy()
+    G = q.shape[1] // k.shape[1]
+    s = np.stack([q[:, h] @ k[:, h // G].T for h in range(q.shape[1])]) / np.sqrt(q.shape[2])
+    s = np.where(np.arange(k.shape[0]) < np.asarray(keys)[:, None], s, -np.inf)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    return p / p.sum(-1, keepdims=True)
+
+
+def test_newest_token_over_the_cache_and_over_the_gathered_cache():
+    """Attention of the newest tokens over the cache, and packed attention of the same tokens over the
+    cache read back.  Each rounds P and o to bf16, 2^-8 each; a score is an fp32 sum of 128 products, off by
+    at most 2^-17 scale sum_x |q_x k_x|, 2^-13 for sums up to 16, and P by twice that, exponentials and
+    sums included: 2^-11.  So |error| <= 2^-8 (sum_j P_j |v_j| + |o|) + 2^-11 sum_j P_j |v_j|, and the two
+    differ by at most twice that."""
+    sdpa = _sdpa()
+    lens, H, H_kv, d, page = [300, 17, 129], 8, 2, 128, 32
+    x = _inputs(lens, lens, H, H_kv, d, d, 31)
+    q, k, v = (x[n].cuda() for n in "qkv")
+    pool, table = _fill_cache(k, v, lens, page)
+    last = torch.tensor(np.cumsum(lens) - 1, device="cuda")
+    o, lse = sdpa.sdpa_decode_kv4(q[last].unsqueeze(1).contiguous(), pool, table, _i32(lens))
+    kc, vc = sdpa.kv4_gather(pool, table, _cu(lens), _i32([0, 0, 0]), sum(lens), d)
+    o2, lse2 = sdpa.sdpa_forward_packed(q[last].contiguous(), kc, vc, _cu([1, 1, 1]), _cu(lens), causal=False)
+    _clean()
+    at = np.cumsum([0] + lens)
+    for b, n in enumerate(lens):
+        sl = slice(int(at[b]), int(at[b + 1]))
+        p = _probabilities(q[last[b]][None], kc[sl], [n])[:, 0]
+        vv = vc[sl].double().cpu().numpy().repeat(H // H_kv, 1)
+        exact, mag = np.einsum("hj,jhx->hx", p, vv), np.einsum("hj,jhx->hx", p, np.abs(vv))
+        bound = 2.0 ** -8 * (mag + np.abs(exact)) + 2.0 ** -11 * mag
+        one, two = o[b, 0].double().cpu().numpy(), o2[b].double().cpu().numpy()
+        assert np.all(np.abs(one - exact) <= bound) and np.all(np.abs(two - exact) <= bound)
+        assert np.all(np.abs(one - two) <= 2 * bound)
+    assert (lse[:, :, 0].t() - lse2).abs().max() <= TOL_LSE
+
+
+def test_prefill_of_several_tokens_over_a_cached_prefix():
+    """A continuation's rows attend over the cached prefix, read back, without a causal mask and over their
+    own rows with one; the two results joined by their lse are the attention over both.  Each result is
+    within 2^-8 (sum_j P_j |v_j| + |o|) + 2^-11 sum_j P_j |v_j| of its own value (P over its own keys, the
+    terms as in the test above), and |o| <= sum_j P_j |v_j|: with exact weights w and 1 - w the join is
+    within (2^-7 + 2^-11) sum_j P_j |v_j|, P over all keys.  Each lse is off by at most 2^-12, so w by at
+    most w (1 - w) 2^-11: another 2^-11 of that sum."""
+    sdpa = _sdpa()
+    H, H_kv, d, page = 8, 2, 128, 32
+    prefix, new = [300, 17, 129, 64], [5, 200, 1, 130]
+    xp, xn = _inputs(prefix, prefix, H, H_kv, d, d, 55), _inputs(new, new, H, H_kv, d, d, 56)
+    pool, table = _fill_cache(xp["k"].cuda(), xp["v"].cuda(), prefix, page)
+    kp, vp = sdpa.kv4_gather(pool, table, _cu(prefix), _i32([0] * 4), sum(prefix), d)
+    q, k, v = (xn[n].cuda() for n in "qkv")
+    o1, l1 = sdpa.sdpa_forward_packed(q, kp, vp, _cu(new), _cu(prefix), causal=False)
+    o2, l2 = sdpa.sdpa_forward_packed(q, k, v, _cu(new))
+    w = torch.sigmoid(l1 - l2).t()[..., None]
+    o = (w * o1.float() + (1 - w) * o2.float()).double().cpu().numpy()
+    lse = torch.logaddexp(l1, l2)
+    _clean()
+    ap, an = np.cumsum([0] + prefix), np.cumsum([0] + new)
+    for b, (m, n) in enumerate(zip(prefix, new)):
+        sp, sn = slice(int(ap[b]), int(ap[b + 1])), slice(int(an[b]), int(an[b + 1]))
+        kk, vv = (torch.cat([a[sp], c[sn]]) for a, c in ((kp, k), (vp, v)))
+        p = _probabilities(q[sn], kk, m + 1 + np.arange(n))
+        vv = vv.double().cpu().numpy().repeat(H // H_kv, 1)
+        exact, mag = np.einsum("hij,jhx->ihx", p, vv), np.einsum("hij,jhx->ihx", p, np.abs(vv))
+        assert np.all(np.abs(o[sn] - exact) <= (2.0 ** -7 + 2.0 ** -10) * mag), f"sequence {b}"
+        kd = kk.double().cpu().numpy().repeat(H // H_kv, 1)
+        s = np.einsum("ihx,jhx->hij", q[sn].double().cpu().numpy(), kd) / np.sqrt(d)
+        s = np.where(np.arange(m + n) < (m + 1 + np.arange(n))[:, None], s, -np.inf)
+        ref = s.max(-1) + np.log(np.exp(s - s.max(-1, keepdims=True)).sum(-1))
+        assert np.abs(lse[:, sn].double().cpu().numpy() - ref).max() <= TOL_LSE
