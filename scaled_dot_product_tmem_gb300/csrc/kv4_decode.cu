@@ -452,7 +452,48 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
         // ---- softmax: s[sub][nt][e + 2 f] is token 16 sub + g + 8 f, row r0 + 8 nt + 2 t + e.  The
         // running maximum (in log2 units) moves only when some score passes it by 2^8 (the sums
         // stay exact: they are relative to the maximum that was used)
+        uint32_t keep[2][2] = {{0xFFFFu, 0xFFFFu}, {0xFFFFu, 0xFFFFu}};  // the V scales that count, as read below
         if (edge) {
+          // A token that no row sees adds nothing, whatever its bytes are.  One with a NaN scale adds
+          // nothing either: rows that do not see it have P = 0, but 0 times NaN is NaN.  The rows that
+          // see it get their NaN here, and keep it.
+          uint32_t nans = 0u;  // eighth g of the warp's 32 tokens, a bit each
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const int u = 8 * sub + 4 * f + t, j = k0 + 2 * u;
+              uint32_t k2 = 0xFFFFu;
+              if (j > len - 1 || j < lo_min) k2 &= 0xFF00u;
+              if (j + 1 > len - 1 || j + 1 < lo_min) k2 &= 0x00FFu;
+              const uint32_t two = k2 & *reinterpret_cast<const unsigned short*>(st + off_sv + sub * d_sk + 4 * f * (D / 8));
+              if ((two & 0x00F8u) == 0x00F8u) {
+                nans |= 1u << (2 * u);
+                k2 &= 0xFF00u;
+              }
+              if ((two & 0xF800u) == 0xF800u) {
+                nans |= 2u << (2 * u);
+                k2 &= 0x00FFu;
+              }
+              keep[sub][f] = k2;
+            }
+          if (__any_sync(0xffffffffu, nans != 0u)) {  // (rare)
+            nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
+            nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int pos = len - p.S_q + min(r0 + 8 * nt + 2 * t + e, R - 1) / G;
+                const int lo = p.window >= 0 && pos > p.window ? pos - p.window : 0;
+                if (pos < k0 || lo - k0 > 31) continue;  // the row sees none of the 32
+                const int from = max(lo - k0, 0), to = min(pos - k0, 31);
+                if (nans & (0xffffffffu << from) & (0xffffffffu >> (31 - to))) {
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) acc[mt][nt][e] = acc[mt][nt][e + 2] = NAN;
+                }
+              }
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -512,16 +553,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
             }
         }
         // ---- outputs: lane (g, t) decodes eighth g of the head dim of token pairs t and t + 4
-        uint32_t nans = 0u;  // on an edge: its tokens with a NaN scale (a bit for each of the warp's 32)
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
           uint32_t lo[2][MT / 4], hi[2][MT / 4];  // [pair][word]: both tokens' nibbles 0-3, 4-7
           Kv4Small kv[2];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const int u = 8 * sub + 4 * f;  // (+ t)
             const uint8_t* va = st + off_v + sub * d_k + 4 * f * D;
-            uint32_t two = *reinterpret_cast<const unsigned short*>(st + off_sv + sub * d_sk + 4 * f * (D / 8));
+            const uint32_t two = *reinterpret_cast<const unsigned short*>(st + off_sv + sub * d_sk + 4 * f * (D / 8));
             if constexpr (D == 128) {
               const uint4 w = *reinterpret_cast<const uint4*>(va);  // token 2u: x, y; token 2u + 1: z, w
               lo[f][0] = __byte_perm(w.x, w.z, 0x5410);
@@ -533,22 +572,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
               lo[f][0] = __byte_perm(w.x, w.y, 0x5410);
               hi[f][0] = __byte_perm(w.x, w.y, 0x7632);
             }
-            if (edge) {  // tokens that no row sees: whatever their bytes are, they add nothing
-              const int j = k0 + 2 * (u + t);
-              if (j > len - 1 || j < lo_min) two &= 0xFF00u;
-              if (j + 1 > len - 1 || j + 1 < lo_min) two &= 0x00FFu;
-              // a row that does not see a token has P = 0, but 0 times NaN is NaN: such a token adds
-              // nothing here, and the rows that see it get their NaN below
-              if ((two & 0x00F8u) == 0x00F8u) {
-                nans |= 1u << (2 * (u + t));
-                two &= 0xFF00u;
-              }
-              if ((two & 0xF800u) == 0xF800u) {
-                nans |= 2u << (2 * (u + t));
-                two &= 0x00FFu;
-              }
-            }
-            kv[f] = small_scales(scale_pair(two));
+            kv[f] = small_scales(scale_pair(two & keep[sub][f]));
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -567,23 +591,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_16816(acc[mt][nt], a[0], a[1], a[2], a[3], pb[sub][nt][0], pb[sub][nt][1]);
           }
-        }
-        if (edge && __any_sync(0xffffffffu, nans != 0u)) {  // (rare)
-          nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
-          nans |= __shfl_xor_sync(0xffffffffu, nans, 2);  // all 32 tokens, eighth g
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int pos = len - p.S_q + min(r0 + 8 * nt + 2 * t + e, R - 1) / G;
-              const int lo = p.window >= 0 && pos > p.window ? pos - p.window : 0;
-              if (pos < k0 || lo - k0 > 31) continue;  // the row sees none of the 32
-              const int from = max(lo - k0, 0), to = min(pos - k0, 31);
-              if (nans & (0xffffffffu << from) & (0xffffffffu >> (31 - to))) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) acc[mt][nt][e] = acc[mt][nt][e + 2] = NAN;
-              }
-            }
         }
       }
       __syncwarp();  // every lane has read the stage: it may be filled again
