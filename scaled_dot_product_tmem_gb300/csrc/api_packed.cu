@@ -277,7 +277,7 @@ int attn_bwd_packed(const void* q, const void* k, const void* v, const void* o, 
       return wide ? sdpa::launch_bwd_kv_wide_packed(d_qk, tq128, tk, tv, tdo128, p, s)
                   : sdpa::launch_bwd_kv_packed_mla(tq64, tk, tv, tdo64, p, s);
     });
-  // (right behind the kv kernel, which it does not depend on, so that it fills that kernel's tail)
+  // (right behind the kv kernel, in whose tail it is set up)
   if (st == ATTN_OK && aq)
     st = launch(ATTN_KERNEL_BWD_Q, 1, "packed backward dQ kernel launch", s,
                 [&] { return sdpa::launch_bwd_q_packed(d_qk, d_v, tq128, tk, tv, tdo128, p, ak, s); });

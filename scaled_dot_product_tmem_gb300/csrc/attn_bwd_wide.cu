@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(352, 1)
   const int n_gr = p.H_kv * p.B * p.ns;
   if constexpr (PK) {
     grid_wait();  // the plan and the preprocess
-    grid_launch_dependents();  // (only now: the dQ kernel relies on the preprocess without waiting for it)
+    grid_launch_dependents();
   }
   const int n_tiles = PK ? p.counts->kv_tiles * p.H_kv * p.ns : n_kv * n_gr;
   if (PK && (int)blockIdx.x >= n_tiles) return;  // the grid is the host's bound on the tiles

@@ -109,11 +109,9 @@ static_assert(sizeof(PackedTile) == 32, "read as two 16-byte words");
 
 // Ordinary loads: the list is written while the kernel that reads it is already set up, and a
 // read-only load (__ldg) is defined only for data that nobody writes in the kernel's lifetime.
-// L2: past the SM's own cache, for a kernel that relies on an earlier one without waiting for it.
-template <bool L2 = false>
 __device__ __forceinline__ PackedTile load_packed_tile(const PackedTile* t, int i) {
   const int4* w = reinterpret_cast<const int4*>(t + i);
-  const int4 a = L2 ? __ldcg(w) : *w, b = L2 ? __ldcg(w + 1) : w[1];
+  const int4 a = w[0], b = w[1];
   return PackedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 

@@ -528,7 +528,7 @@ static int launch_q_packed_t(const CUtensorMap& tq, const CUtensorMap& tk, const
   return launch_kernel(kern, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, early, tq, tk, tv, tdo, p);
 }
 
-// early: right behind the kv kernel on the stream, whose tail it may overlap (it needs nothing of it).
+// early: right behind the kv kernel on the stream, in whose tail it is set up.
 int launch_bwd_q_packed(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& tdo, const BwdParams& p, bool early, cudaStream_t stream) {
   if (d_qk == 128 && d_v == 128) return launch_q_packed_t<128, 128>(tq, tk, tv, tdo, p, early, stream);

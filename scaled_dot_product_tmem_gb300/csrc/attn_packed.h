@@ -30,7 +30,7 @@ int launch_bwd_kv_wide_packed(int d, const CUtensorMap& tq128, const CUtensorMap
                               const CUtensorMap& tdo128, const BwdParams& p, cudaStream_t stream);
 int launch_bwd_kv_packed_mla(const CUtensorMap& tq64, const CUtensorMap& tk, const CUtensorMap& tv,
                              const CUtensorMap& tdo64, const BwdParams& p, cudaStream_t stream);
-// early: launched right behind the kv kernel, whose tail it may overlap.
+// early: launched right behind the kv kernel, in whose tail it is set up.
 int launch_bwd_q_packed(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& tdo, const BwdParams& p, bool early, cudaStream_t stream);
 

@@ -675,7 +675,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 // rows of sequences without a token.  One block per (sequence, kv head, row block, row): warp w
 // takes pieces w, w + 8, ..., then the eight are added in order.  (A warp per row, taking its
 // pieces one after another, took 12.3 us instead of 8.9 for 128 segments of 1 to 11 pieces.)
-// Launched while the decode kernel runs: it waits for that kernel's end before it reads a piece.
+// Launched while the decode kernel runs: it waits for that kernel's end before it reads a piece.  (The
+// lengths it reads before are older than the decode kernel, which began when all before it on the
+// stream had ended.)
 template <int D>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeParams p, int row_blocks, int rows, int grid,
                                                        const float* partial) {
