@@ -147,7 +147,9 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
  * the same as cu_seqlens_q.  A sequence may have no queries, no keys or neither; a row
  * that sees no key gets o = 0 and lse = the sink logit, one with a NaN score lse = NaN (where
  * attn_fwd gives -inf).  lse: fp32 [H_q, T_q].  Values of one sequence, infinities and NaN
- * included, never reach another sequence's results.
+ * included, never reach another sequence's results.  Inside a sequence, as in attn_fwd, an
+ * infinity or NaN can also reach rows whose mask hides it: their weight for it is 0, and 0
+ * times it is NaN.
  * Offsets are clamped to [0, T] and to their running maximum.  Rows that belong to no
  * sequence (past the last one, or before cu_seqlens[0]) are left alone; with zero_rest != 0
  * they get o, dq, dk, dv = 0 and lse = -inf.
@@ -410,8 +412,10 @@ int attn_bwd_fp8(const void* q8, const void* k8, const void* v8, const void* do8
  * A 4-bit paged key/value cache, for serving: tokens are quantised into pages
  * (attn_kv4_append), the newest tokens of every sequence attend over them
  * (attn_kv4_decode), and pages are copied when a sequence forks or a pool is compacted
- * (attn_kv4_copy_pages).  attn_kv4_gather reads tokens back as bf16, for example to
- * prefill a continuation over a cached prefix.
+ * (attn_kv4_copy_pages).  attn_kv4_gather reads tokens back as bf16.  (To prefill a
+ * continuation over a cached prefix, its rows attend over the prefix read back with
+ * attn_fwd_packed and causal = 0, and over themselves with causal = 1; the two results are
+ * joined by their lse.)
  *
  * Pool.  uint8 [n_pages, H_kv, attn_kv4_block_bytes(page_size, d)], 16-byte aligned,
  *   allocated by the caller; page_size in {16, 32, 64, 128} tokens, d = d_qk = d_v in
@@ -439,10 +443,11 @@ int attn_bwd_fp8(const void* q8, const void* k8, const void* v8, const void* do8
  * attn_kv4_decode: q bf16 [B, S_q, H_q, d]: the S_q newest tokens of every sequence, whose
  *   seq_lens[b] tokens (these included; device int32 [B], clamped to [0, max_pages *
  *   page_size]) are in the cache.  Query s sits at pos = seq_lens[b] - S_q + s and sees the
- *   keys j <= pos, and j >= pos - window when window >= 0.  Pages of which no query sees a
- *   token are not looked up.  o bf16 [B, S_q, H_q, d]; lse fp32 [B, H_q, S_q] (may be NULL).  A query that sees no key gets o = 0 and lse = the
- *   sink logit.  scale, window, softmax_type and softmax_offset as for attn_fwd
- *   (ATTN_ERR_UNSUPPORTED for a finite scale above 1e30).
+ *   keys j <= pos, and j >= pos - window when window >= 0; no other token reaches it, not
+ *   even one held as NaN.  Pages of which no query sees a token are not looked up.  o bf16
+ *   [B, S_q, H_q, d]; lse fp32 [B, H_q, S_q] (may be NULL).  A query that sees no key gets
+ *   o = 0 and lse = the sink logit.  scale, window, softmax_type and softmax_offset as for
+ *   attn_fwd (ATTN_ERR_UNSUPPORTED for a scale above 1e30).
  *   workspace: device scratch of attn_kv4_decode_workspace_size() bytes, 256-byte aligned,
  *   not shared with a call that may run at the same time.  Bitwise reproducible.
  * attn_kv4_copy_pages: page dst[i] = page src[i] for i < n, in each of n_layers pools that
@@ -453,9 +458,9 @@ int attn_bwd_fp8(const void* q8, const void* k8, const void* v8, const void* do8
  *   destination named twice, or a page that is both source and destination.
  *
  * Errors as attn_fwd (H_q % H_kv != 0 and null pointers: ATTN_ERR_INVALID_ARG; other page
- * sizes and head dims: ATTN_ERR_UNSUPPORTED).  A token whose page is not in the table
- * or the pool is not written, reads as zeros, and makes attn_last_device_error() return
- * ATTN_ERR_BAD_PAGE.
+ * sizes and head dims: ATTN_ERR_UNSUPPORTED).  A token that a call needs and whose page is
+ * not in the table or the pool is not written, reads as zeros, and makes
+ * attn_last_device_error() return ATTN_ERR_BAD_PAGE.
  */
 enum { ATTN_KV4_SITE_APPEND = 1, ATTN_KV4_SITE_GATHER = 2, ATTN_KV4_SITE_DECODE = 3 };
 /* Bytes of one page and kv head; 0 for an unsupported page size or head dim. */

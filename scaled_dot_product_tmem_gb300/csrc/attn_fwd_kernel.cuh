@@ -13,8 +13,9 @@
 //
 // A work tile is two 128-row query tiles of one (b, h); its CTA walks the kv tiles
 // that either of them can see.  CTAs are persistent (one per SM), each taking every
-// gridDim-th work tile, heaviest causal query blocks first, so one tile's output
-// epilogue overlaps the next tile's loads and first GEMM.  Warp roles (320 threads):
+// gridDim-th work tile (packed batches: its next one from a counter), heaviest causal
+// query blocks first, so one tile's output epilogue overlaps the next tile's loads and
+// first GEMM.  Warp roles (320 threads):
 //   warps 0-3 / 4-7  softmax warpgroup of query tile 0 / 1: thread r owns row r
 //                    (TMEM lane r); online softmax in fp32 with the sink folded
 //                    into the running max/denominator; writes bf16 P into TMEM

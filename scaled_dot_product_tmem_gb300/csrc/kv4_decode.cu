@@ -29,9 +29,11 @@
 //     bulk copy; each of the other four takes 32 tokens of every unit.
 //
 // Measured (d = 128, 8 kv heads): 329,377 tokens of 4 sequences with 8 query rows a kv head, 380 MB
-// of cache, 78 us (4.9 TB/s; 80 with four copies a page, 88 with an exponent set in every code
-// and a shift for three of four as well); 42,031 tokens of 16 sequences, 48 MB, 21 us, of which about 10 are
-// the chain lengths - page - copy - products - join.
+// of cache, 76 us (5.0 TB/s; the copies alone 66; 78 with hidden tokens masked in the output loop, two
+// more with four copies a page, ten more with an exponent set in every code and a shift for three of
+// four); 42,031 tokens of 16 sequences, 48 MB, 21 us, of which about 10 are the chain lengths - page -
+// copy - products - join.  More query rows a kv head are bound by the computing warps, of which fewer fit an
+// SM: the same tokens take 106 us with 9 to 16 rows and 176 with 17 to 32.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -674,7 +676,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 // Joins the pieces of every (sequence, head) that spans several CTAs, in CTA order, and writes the
 // rows of sequences without a token.  One block per (sequence, kv head, row block, row): warp w
 // takes pieces w, w + 8, ..., then the eight are added in order.  (A warp per row, taking its
-// pieces one after another, took 12.3 us instead of 8.9 for 128 segments of 1 to 11 pieces.)
+// pieces one after another, took 12.3 us instead of 8.9 for 128 segments of 1 to 11 pieces.)  Every
+// block works out the numbering for itself, so that above 32 sequences the join's work grows with the square of
+// their number: 256 sequences of 500 to 4000 tokens, 8 kv heads of 4 rows, take 183 us with a floor of
+// 94, 1024 of them 967 with a floor of 396.
 // Launched while the decode kernel runs: it waits for that kernel's end before it reads a piece.  (The
 // lengths it reads before are older than the decode kernel, which began when all before it on the
 // stream had ended.)
@@ -766,6 +771,11 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeParams p, 
 
 namespace {
 
+// Column blocks of 8 query rows a CTA takes at a time.  Fewer leave room for more CTAs an SM (3, 2, 1),
+// more decode each token less often.  329,377 tokens, 8 kv heads, d = 128, us with 1, 2 and 4 blocks:
+// 8 rows 77, 105, 170; 16 rows 139, 106, 172; 24 rows 203, 201, 175; 32 rows 267, 201, 176; and 160
+// rows of one kv head 167, 127, 112.  (Small caches prefer fewer at 32 rows: 42,031 tokens of one
+// kv head in 16 sequences 17, 19, 21.)
 int n_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 template <int D, int NT>
