@@ -29,9 +29,9 @@
 //     bulk copy; each of the other four takes 32 tokens of every unit.
 //
 // Measured (d = 128, 8 kv heads): 329,377 tokens of 4 sequences with 8 query rows a kv head, 380 MB
-// of cache, 76 us (5.0 TB/s; the copies alone 66; 78 with hidden tokens masked in the output loop, two
-// more with four copies a page, ten more with an exponent set in every code and a shift for three of
-// four); 42,031 tokens of 16 sequences, 48 MB, 21 us, of which about 10 are the chain lengths - page -
+// of cache, 76 us (5.0 TB/s; the copies alone 66.  Steps before: 88 with an exponent set in every code
+// and a shift for three of four, 80 with four copies a page, 78 with hidden tokens masked in the output
+// loop); 42,031 tokens of 16 sequences, 48 MB, 21 us, of which about 10 are the chain lengths - page -
 // copy - products - join.  More query rows a kv head are bound by the computing warps, of which fewer fit an
 // SM: the same tokens take 106 us with 9 to 16 rows and 176 with 17 to 32.
 #include <algorithm>
