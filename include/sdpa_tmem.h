@@ -462,7 +462,13 @@ int attn_bwd_fp8(const void* q8, const void* k8, const void* v8, const void* do8
  * not in the table or the pool is not written, reads as zeros, and makes
  * attn_last_device_error() return ATTN_ERR_BAD_PAGE.
  */
-enum { ATTN_KV4_SITE_APPEND = 1, ATTN_KV4_SITE_GATHER = 2, ATTN_KV4_SITE_DECODE = 3 };
+enum {
+  ATTN_KV4_SITE_APPEND = 1,
+  ATTN_KV4_SITE_GATHER = 2,
+  ATTN_KV4_SITE_DECODE = 3,
+  ATTN_KV4_SITE_TREE = 4,
+  ATTN_KV4_SITE_KEEP = 5
+};
 /* Bytes of one page and kv head; 0 for an unsupported page size or head dim. */
 int attn_kv4_block_bytes(int page_size, int d);
 int attn_kv4_append(const void* k, const void* v, const int* cu_seqlens, void* pool, const int* page_table,
@@ -478,6 +484,68 @@ int attn_kv4_decode(const void* q, const void* pool, const int* page_table, cons
                     size_t workspace_bytes, void* stream);
 int attn_kv4_copy_pages(void* pool, int n_layers, int n_pages, size_t page_bytes, const int* src, const int* dst,
                         int n, void* stream);
+
+/*
+ * Rotation of queries and keys by their rows' positions.
+ *
+ * attn_rope_table: table fp32 [T][2][n] = gain cos(p w), then gain sin(p w), of each row's position p
+ *   (device int32 [T]) and the n frequencies w (device fp64 [n], radians a position, finite).  The
+ *   angle is reduced without rounding, so far positions lose nothing.  n a multiple of 8, at most 128.
+ * attn_rope: q bf16 rows [T][H_q, d] (row t at q + t * q_stride elements; strides multiples of 8
+ *   and at least H_q * d) into q_out, k [T][H_k, d] into k_out alike; a tensor of no heads (H = 0) may
+ *   be NULL.  q_out == q (with the same stride) rotates in place; other overlaps are not allowed.  Row
+ *   t takes row t % table_rows of the table (T a multiple of table_rows: a batch whose entries share
+ *   their positions).  The pairs are dims (first_dim + f, first_dim + n + f), f < n, or with
+ *   interleaved (first_dim + 2f, first_dim + 2f + 1); (x1, x2) becomes (x1 c - x2 s, x2 c + x1 s),
+ *   computed in fp32 (the products rounded, then their sum) and rounded to bf16 once.  The other
+ *   dims are copied.  inverse: with -s, the transposed rotation, which takes the gradient of the
+ *   rotated rows to that of the rows.  d at most 256; d, first_dim and n multiples of 8.
+ * attn_kv4_append_rope: attn_kv4_append of the keys rotated (and rounded to bf16) by row t of the table
+ *   [T][2][n]; with H_q > 0 the rows q, H_q heads of the same d, rotated into q_out in the same launch
+ *   (all T of them, also past cu_seqlens[B]).  Keys and cache bit for bit as attn_rope and
+ *   attn_kv4_append give them.
+ * Errors as attn_fwd; other sizes are ATTN_ERR_UNSUPPORTED.
+ */
+int attn_rope_table(const double* inv_freq, const int* positions, float* table, int T, int n, float gain, void* stream);
+int attn_rope(const void* q, const void* k, const float* table, void* q_out, void* k_out, int T, int H_q, int H_k, int d,
+              int n, int first_dim, int table_rows, long long q_stride, long long k_stride, long long q_out_stride,
+              long long k_out_stride, int interleaved, int inverse, void* stream);
+int attn_kv4_append_rope(const void* q, const void* k, const void* v, const float* table, void* q_out, const int* cu_seqlens,
+                         void* pool, const int* page_table, const int* seq_lens, int B, int T, int H_q, int H_kv, int d,
+                         int n_pages, int page_size, int max_pages, int n, int first_dim, long long q_row_stride,
+                         long long k_row_stride, long long v_row_stride, long long q_out_row_stride, int interleaved,
+                         void* stream);
+
+/*
+ * Drafted trees over the 4-bit cache (speculative decoding).
+ *
+ * attn_kv4_tree: q bf16 [T, H_q, d]: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device int32 [B + 1],
+ *   ascending from 0) are the nodes 0, 1, ... of sequence b's tree, which attn_kv4_append has put into
+ *   the cache as its tokens seq_lens[b], seq_lens[b] + 1, ... (device int32 [B]: the tokens before the
+ *   tree, clamped to [0, max_pages * page_size]).  parents: device int32 [T], the number of a node's
+ *   parent within its sequence; a value that is negative or not below the node's own number makes it
+ *   a child of the last token before the tree.  NULL: a chain, every node's parent the one before it.
+ *   Node i, at position seq_lens[b] + depth(i), sees the tokens before the tree, its ancestors and
+ *   itself; with window >= 0 only those whose position is at least its own minus window.  No other
+ *   token reaches it, not even one held as NaN.  o bf16 [T, H_q, d], lse fp32 [H_q, T] (may be NULL);
+ *   a node that sees no token (those past max_pages * page_size do not exist) gets o = 0 and lse =
+ *   the sink logit.  Rows of no sequence are left alone, or with zero_rest get o = 0, lse = -inf.
+ *   Any number of nodes; scale, window, sinks, errors and workspace (attn_kv4_tree_workspace_size()
+ *   bytes) as attn_kv4_decode.  Bitwise reproducible.
+ * attn_kv4_keep: what verification accepted becomes the sequence's next tokens, in each of n_layers
+ *   pools that follow one another: for i = 0, 1, ... in this order token seq_lens[b] + kept[b][i] is copied
+ *   to token seq_lens[b] + i, until the first negative entry of kept (device int32 [B, most]).  Keys are
+ *   not rotated anew: an accepted path's nodes keep their positions.  A move whose source or
+ *   destination has no page is left out (ATTN_ERR_BAD_PAGE).  Different sequences must not write the
+ *   same page.
+ */
+size_t attn_kv4_tree_workspace_size(int B, int T, int H_q, int H_kv, int d);
+int attn_kv4_tree(const void* q, const int* cu_seqlens, const int* parents, const void* pool, const int* page_table,
+                  const int* seq_lens, void* o, float* lse, int B, int T, int H_q, int H_kv, int d, int n_pages,
+                  int page_size, int max_pages, float scale, int window, int softmax_type, const float* softmax_offset,
+                  int zero_rest, void* workspace, size_t workspace_bytes, void* stream);
+int attn_kv4_keep(void* pool, const int* page_table, const int* seq_lens, const int* kept, int B, int most, int n_layers,
+                  int H_kv, int d, int n_pages, int page_size, int max_pages, void* stream);
 
 /*
  * Failure-path self-test.  Every pipeline wait in the kernels is bounded (about one
@@ -508,8 +576,9 @@ enum {
   ATTN_KERNEL_BWD_Q = 3,           /* query-stationary deterministic dQ kernel */
   ATTN_KERNEL_BWD_DQ_CONVERT = 4,  /* fp32 dQ accumulator -> bf16; split dK/dV combine */
   ATTN_KERNEL_FP8_QUANT = 5,       /* E4M3 amax and quantisation */
-  ATTN_KERNEL_KV4 = 6,             /* 4-bit cache: append, gather, copy, decode */
-  ATTN_KERNEL_CLASSES = 7
+  ATTN_KERNEL_KV4 = 6,             /* 4-bit cache: append, gather, copy, decode, trees */
+  ATTN_KERNEL_ROPE = 7,            /* rotation by positions */
+  ATTN_KERNEL_CLASSES = 8
 };
 int attn_timing_enable(int on);
 int attn_timing_read(double* ms, int* launches, int n);

@@ -24,12 +24,26 @@ attn_kv4_copy_pages forks and compacts it, kv4_gather reads it back:
     pool = kv4_pool(n_pages, H_kv, d, page_size)
     attn_kv4_append(k, v, cu_seqlens, pool, page_table, seq_lens)
     o, lse = sdpa_decode_kv4(q, pool, page_table, seq_lens + 1)
+
+Rotary positions, by themselves (rope, differentiable), as an argument of attention and attention_packed,
+or on the way into the cache (kv4_append_rope):
+
+    inv_freq, gain = rope_frequencies(d)
+    table = rope_table(inv_freq, positions, gain=gain)
+    o = attention_packed(q, k, v, cu_seqlens, rope=table)
+
+Drafted trees over the cache (speculative decoding):
+
+    q = kv4_append_rope(q, k, v, table, cu_nodes, pool, page_table, seq_lens)
+    o, lse = sdpa_tree_kv4(q, cu_nodes, parents, pool, page_table, seq_lens)
+    attn_kv4_keep(pools, page_table, seq_lens, accepted, d)
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -143,6 +157,19 @@ def _load():
     lib.attn_kv4_decode.restype = i
     lib.attn_kv4_copy_pages.argtypes = [vp, i, i, sz, vp, vp, i, vp]
     lib.attn_kv4_copy_pages.restype = i
+    lib.attn_rope_table.argtypes = [vp, vp, vp, i, i, f, vp]
+    lib.attn_rope_table.restype = i
+    lib.attn_rope.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, ll, ll, ll, ll, i, i, vp]
+    lib.attn_rope.restype = i
+    lib.attn_kv4_append_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, i, ll, ll, ll, ll,
+                                         i, vp]
+    lib.attn_kv4_append_rope.restype = i
+    lib.attn_kv4_tree_workspace_size.argtypes = [i, i, i, i, i]
+    lib.attn_kv4_tree_workspace_size.restype = sz
+    lib.attn_kv4_tree.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, i, vp, i, vp, sz, vp]
+    lib.attn_kv4_tree.restype = i
+    lib.attn_kv4_keep.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp]
+    lib.attn_kv4_keep.restype = i
     _lib = lib
     return lib
 
@@ -396,7 +423,7 @@ def attn_bwd_bias(q, k, v, o, dout, lse, dq, dk, dv, d_offset, bias, dbias, **kw
     attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, d_offset, bias=bias, dbias=dbias, **kw)
 
 
-KERNEL_CLASSES = ("fwd", "bwd_preprocess", "bwd_kv", "bwd_q", "bwd_dq_convert", "fp8_quantize", "kv4")
+KERNEL_CLASSES = ("fwd", "bwd_preprocess", "bwd_kv", "bwd_q", "bwd_dq_convert", "fp8_quantize", "kv4", "rope")
 
 
 def attn_timing_enable(on: bool = True) -> None:
@@ -872,9 +899,12 @@ class SDPAPackedFunction(torch.autograd.Function):
 
 
 def attention_packed(q, k, v, cu_seqlens_q, cu_seqlens_kv=None, softmax_offset=None, *, causal=True, window=-1,
-                     softmax_type=VANILLA, scale=0.0):
+                     softmax_type=VANILLA, scale=0.0, rope=None, rope_interleaved=False, rope_first_dim=0):
     """Differentiable attention over packed sequences: q [T_q, H_q, d_qk], k [T_kv, H_kv, d_qk],
-    v [T_kv, H_kv, d_v]; q, k, v and the learnable offset receive gradients."""
+    v [T_kv, H_kv, d_v]; q, k, v and the learnable offset receive gradients.  rope: a table of the rows'
+    positions (rope_table), by which q and k (of the same rows) are rotated first."""
+    if rope is not None:
+        q, k = RopeFunction.apply(q, k, rope, bool(rope_interleaved), int(rope_first_dim))
     return SDPAPackedFunction.apply(q, k, v, cu_seqlens_q, cu_seqlens_kv, softmax_offset, causal, window,
                                     softmax_type, scale)
 
@@ -1109,6 +1139,377 @@ def attn_kv4_copy_pages(pool, src, dst, *, stream=None):
         raise AttnError(st, "attn_kv4_copy_pages")
 
 
+# ----------------------------------------------------------------------------- rotary positions
+
+
+def rope_frequencies(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original_length=None, slow_turns=1.0,
+                     fast_turns=32.0, gain=None, device="cuda"):
+    """The frequencies of rot_dim / 2 pairs (fp64 [rot_dim / 2] on `device`, radians a position) and
+    the gain of their cosines and sines: returns (inv_freq, gain), to be kept for all steps.
+
+    Pair f of n turns by base^(-f / n) a position.  For contexts `factor` times as long as the
+    model was trained for, scaling is "linear" (every frequency divided by the factor), "base" (the
+    base multiplied by factor^(n / (n - 1)): the slowest pair slows down by the factor, the
+    fastest stays) or "parts" (pairs that turn slow_turns times or less in original_length positions are
+    divided by the factor, those that turn fast_turns times or more stay, those between are
+    blended by the logarithm of their turns; the gain is 0.1 ln(factor) + 1).  gain: another one."""
+    n = int(rot_dim) // 2
+    if rot_dim != 2 * n or n <= 0 or n % 8 or n > 128:
+        raise ValueError(f"rot_dim must be a multiple of 16 and at most 256, got {rot_dim}")
+    if not (base > 0 and factor > 0 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError(f"base and factor must be positive, got {base} and {factor}")
+    if scaling not in ("none", "linear", "base", "parts"):
+        raise ValueError(f'scaling must be "none", "linear", "base" or "parts", got {scaling!r}')
+    f = torch.arange(n, dtype=torch.float64) / n
+    if scaling == "base":
+        base = base * factor ** (n / (n - 1))
+    w = torch.as_tensor(base, dtype=torch.float64) ** -f
+    if scaling == "linear":
+        w = w / factor
+    if scaling == "parts":
+        if original_length is None or original_length <= 0 or not 0 < slow_turns < fast_turns:
+            raise ValueError("scaling by parts needs the original_length, and 0 < slow_turns < fast_turns")
+        turns = original_length * w / (2 * math.pi)
+        keep = (torch.log(turns / slow_turns) / math.log(fast_turns / slow_turns)).clamp(0.0, 1.0)
+        w = w * keep + w / factor * (1 - keep)
+        if gain is None:
+            gain = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    return w.to(device), 1.0 if gain is None else float(gain)
+
+
+def attn_rope_table(inv_freq, positions, table, *, gain=1.0, stream=None):
+    """Cosines and sines of positions into the preallocated table (fp32 [T, 2, n]): table[t, 0] =
+    gain cos(p_t inv_freq), table[t, 1] = gain sin(p_t inv_freq).  inv_freq: fp64 [n] on the device;
+    positions: int32 of T values.  Angles are reduced without rounding, also those of far positions."""
+    _check(inv_freq, "inv_freq", torch.float64, 1)
+    _check(positions, "positions", torch.int32, positions.dim())
+    _check(table, "table", torch.float32, 3)
+    T, n = positions.numel(), inv_freq.shape[0]
+    if tuple(table.shape) != (T, 2, n):
+        raise ValueError(f"table must be {(T, 2, n)}, got {tuple(table.shape)}")
+    dev = _device_of(inv_freq, positions, table)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_rope_table(inv_freq, positions, table, gain=gain)
+    st = _load().attn_rope_table(_p(inv_freq), _p(positions), _p(table), T, n, float(gain), _raw_stream(dev, None))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_rope_table")
+
+
+def rope_table(inv_freq, positions, *, gain=1.0, stream=None):
+    """attn_rope_table into a new table [T, 2, n], T the positions' count: made once a step, for
+    the rotations of all its layers."""
+    dev = _device_of(inv_freq, positions)
+    if dev >= 0 and _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return rope_table(inv_freq, positions, gain=gain)
+    table = torch.empty((positions.numel(), 2, inv_freq.numel()), dtype=torch.float32, device=inv_freq.device)
+    attn_rope_table(inv_freq, positions, table, gain=gain)
+    return table
+
+
+def _row_stride(t, name):
+    """Elements between the rows of a bf16 tensor [.., H, d], which must be evenly apart."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [rows, H, d] or [B, S, H, d], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    H, d = t.shape[-2:]
+    if t.numel() == 0:
+        return H * d
+    if (t.stride(-1) != 1 and d > 1) or (t.stride(-2) != d and H > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    stride, reach = None, 0  # of the innermost rows; what the rows so far span
+    for size, step in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride, reach = step, step * size
+        elif step != reach:
+            raise ValueError(f"{name}: the rows must be evenly apart, got strides {t.stride()}")
+        else:
+            reach *= size
+    if stride is None:
+        return H * d
+    if stride < H * d or stride % 8:
+        raise ValueError(f"{name}: rows must not overlap and must be a multiple of 8 elements apart, got {stride}")
+    return stride
+
+
+def _check_rope(q, k, table):
+    """Checks of heads and their table; returns (T, H_q, H_k, d, n, table rows)."""
+    _check(table, "table", torch.float32, 3)
+    if table.shape[1] != 2:
+        raise ValueError(f"table must be [rows, 2, n], got {tuple(table.shape)}")
+    if q.dim() < 3:
+        raise ValueError(f"q must be [rows, H, d] or [B, S, H, d], got {tuple(q.shape)}")
+    rows, (H, d) = q.shape[:-2], q.shape[-2:]
+    T = math.prod(rows)
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != rows or k.shape[-1] != d):
+        raise ValueError(f"k must have q's rows and head dim, got {tuple(k.shape)} and {tuple(q.shape)}")
+    R = table.shape[0]
+    if R != T and not (len(rows) == 2 and R == rows[1]):
+        raise ValueError(f"table must have one row per row of q ({T})"
+                         + (f" or per position ({rows[1]})" if len(rows) == 2 else "") + f", got {R}")
+    return T, H, 0 if k is None else k.shape[-2], d, table.shape[2], R
+
+
+def attn_rope(q, k, table, q_out, k_out, *, interleaved=False, first_dim=0, inverse=False, stream=None):
+    """Rotate the heads of q and k (bf16 [T, H, d] or [B, S, H, d]; k may be None) by their rows'
+    positions into q_out, k_out of the same shapes; q_out may be q (in place).
+
+    table: fp32 [T, 2, n] (rope_table), one row per row of q; for [B, S, H, d] it may be [S, 2, n],
+    shared by the batch.  Dims first_dim .. first_dim + 2n of every head are turned, as pairs (f, n + f) or,
+    interleaved, (2f, 2f + 1); the others are copied.  inverse: the transposed rotation, which
+    takes the gradient of the results to that of q and k.  Rows may be apart (a slice of a fused
+    projection), evenly and by a multiple of 8 elements."""
+    T, H, H_k, d, n, R = _check_rope(q, k, table)
+    strides = [_row_stride(q, "q"), 0 if k is None else _row_stride(k, "k"), _row_stride(q_out, "q_out"),
+               0 if k is None else _row_stride(k_out, "k_out")]
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    dev = _device_of(q, k, table, q_out, k_out)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_rope(q, k, table, q_out, k_out, interleaved=interleaved, first_dim=first_dim, inverse=inverse)
+    _run_rope(q, k, table, q_out, k_out, (T, H, H_k, d, n), R, strides, dev, interleaved, first_dim, inverse)
+
+
+def _run_rope(q, k, table, q_out, k_out, sizes, R, strides, dev, interleaved, first_dim, inverse):
+    st = _load().attn_rope(_p(q), _p(k), _p(table), _p(q_out), _p(k_out), *sizes, int(first_dim), R, *strides,
+                           int(bool(interleaved)), int(bool(inverse)), _raw_stream(dev, None))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_rope")
+
+
+def _rope_new(q, k, table, interleaved, first_dim, inverse, stream):
+    sizes = _check_rope(q, k, table)
+    dev = _device_of(q, k, table)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return _rope_new(q, k, table, interleaved, first_dim, inverse, None)
+    H, H_k, d = sizes[1:4]
+    strides = [_row_stride(q, "q"), 0 if k is None else _row_stride(k, "k"), H * d, H_k * d]
+    q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    _run_rope(q, k, table, q_out, k_out, sizes[:5], sizes[5], strides, dev, interleaved, first_dim, inverse)
+    return q_out, k_out
+
+
+def rope_forward(q, k, table, *, interleaved=False, first_dim=0, stream=None):
+    """attn_rope into new tensors: returns (q, k) rotated."""
+    return _rope_new(q, k, table, interleaved, first_dim, False, stream)
+
+
+def rope_backward(dq, dk, table, *, interleaved=False, first_dim=0, stream=None):
+    """Gradients of rope_forward's inputs from those of its results: returns (dq, dk)."""
+    return _rope_new(dq, dk, table, interleaved, first_dim, True, stream)
+
+
+def _evenly(t):
+    """A gradient as autograd hands it over, copied if its rows are not as a kernel can read them."""
+    try:
+        _row_stride(t, "gradient")
+        return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+    except ValueError:
+        return t.contiguous()
+
+
+class RopeFunction(torch.autograd.Function):
+    """autograd wrapper of the rotation; its gradient is the transposed rotation."""
+
+    @staticmethod
+    def forward(ctx, q, k, table, interleaved, first_dim):
+        ctx.set_materialize_grads(False)
+        ctx.kw = dict(interleaved=interleaved, first_dim=first_dim)
+        ctx.save_for_backward(table)
+        return rope_forward(q, k, table, **ctx.kw)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        (table,) = ctx.saved_tensors
+        if dq is None and dk is None:
+            return None, None, None, None, None
+        if dq is None:
+            return None, rope_backward(_evenly(dk), None, table, **ctx.kw)[0], None, None, None
+        dq, dk = rope_backward(_evenly(dq), None if dk is None else _evenly(dk), table, **ctx.kw)
+        return dq, dk, None, None, None
+
+
+def rope(q, k, table, *, interleaved=False, first_dim=0):
+    """Differentiable rotation of q and k (k may be None) by positions: returns (q, k); arguments as
+    for attn_rope.  The table receives no gradient."""
+    return RopeFunction.apply(q, k, table, bool(interleaved), int(first_dim))
+
+
+def attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, *, interleaved=False, first_dim=0,
+                         stream=None):
+    """attn_kv4_append of keys rotated on the way, and the queries rotated in the same launch.
+
+    k, v (bf16 [T, H_kv, d]), cu_seqlens, pool, page_table, seq_lens as for attn_kv4_append; table: fp32
+    [T, 2, n], one row per row of k; q, q_out: bf16 [T, H_q, d], or None.  Results and cache are bit for
+    bit those of attn_rope and attn_kv4_append."""
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, H_kv, d], got shape {tuple(k.shape)}")
+    T, _, d = k.shape
+    B, n_pages, H_kv, page_size, max_pages = _check_paged(pool, page_table, seq_lens, d)
+    ks, vs = _check_rows(k, "k", H_kv, d), _check_rows(v, "v", H_kv, d)
+    if v.shape[0] != T:
+        raise ValueError(f"k and v must have the same rows, got {T} and {v.shape[0]}")
+    _check_cu(cu_seqlens, "cu_seqlens", B)
+    _check(table, "table", torch.float32, 3)
+    if tuple(table.shape[:2]) != (T, 2):
+        raise ValueError(f"table must be [{T}, 2, n], got {tuple(table.shape)}")
+    H_q = qs = qos = 0
+    if q is not None:
+        if q.dim() != 3 or q_out is None or q_out.shape != q.shape or q.shape[0] != T:
+            raise ValueError(f"q and q_out must be [{T}, H_q, {d}]")
+        H_q = q.shape[1]
+        qs, qos = _check_rows(q, "q", H_q, d), _check_rows(q_out, "q_out", H_q, d)
+    dev = _device_of(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out,
+                                        interleaved=interleaved, first_dim=first_dim)
+    st = _load().attn_kv4_append_rope(_p(q), _p(k), _p(v), _p(table), _p(q_out), _p(cu_seqlens), _p(pool), _p(page_table),
+                                      _p(seq_lens), B, T, H_q, H_kv, d, n_pages, page_size, max_pages, table.shape[2],
+                                      int(first_dim), qs, ks, vs, qos, int(bool(interleaved)), _raw_stream(dev, None))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_append_rope")
+
+
+def kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, *, interleaved=False, first_dim=0, stream=None):
+    """attn_kv4_append_rope with the rotated queries in a new tensor, which is returned (None
+    without q)."""
+    dev = _device_of(k)
+    if dev >= 0 and _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, interleaved=interleaved,
+                                   first_dim=first_dim)
+    q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16, device=k.device)
+    attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, interleaved=interleaved,
+                         first_dim=first_dim)
+    return q_out
+
+
+# ----------------------------------------------------------------------------- drafted trees
+
+
+@functools.lru_cache(maxsize=1024)
+def attn_kv4_tree_workspace_size(B, T, H_q, H_kv, d) -> int:
+    return int(_load().attn_kv4_tree_workspace_size(B, T, H_q, H_kv, d))
+
+
+def _check_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, softmax_offset):
+    """Checks of a tree's inputs; returns (B, T, H_q, H_kv, d, n_pages, page_size, max_pages)."""
+    _check(q, "q", torch.bfloat16, 3)
+    T, H_q, d = q.shape
+    B, n_pages, H_kv, page_size, max_pages = _check_paged(pool, page_table, seq_lens, d)
+    _check_cu(cu_seqlens, "cu_seqlens", B)
+    if parents is not None:
+        _check(parents, "parents", torch.int32, 1)
+        if parents.shape[0] != T:
+            raise ValueError(f"parents: one per row of q ({T}), got {parents.shape[0]}")
+    if softmax_offset is not None:
+        _check(softmax_offset, "softmax_offset", torch.float32, 1)
+        if softmax_offset.shape[0] != H_q:
+            raise ValueError(f"softmax_offset must have one value per query head ({H_q})")
+    return B, T, H_q, H_kv, d, n_pages, page_size, max_pages
+
+
+def attn_kv4_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, o, lse=None, *, window=-1, softmax_type=VANILLA,
+                  softmax_offset=None, scale=0.0, zero_rest=False, workspace=None, stream=None):
+    """Attention of drafted trees over their sequences' 4-bit caches, into preallocated o (bf16, q's
+    shape [T, H_q, d]) and, if given, lse (fp32 [H_q, T]).
+
+    Rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32 [B+1] on the device) are the nodes of sequence b's
+    tree, already in the cache as its tokens seq_lens[b], seq_lens[b] + 1, ... (seq_lens: int32 [B], the
+    tokens before the tree).  parents: int32 [T], the number of a node's parent within its sequence,
+    below its own; negative: a child of the last token before the tree.  None: a chain (tokens in
+    causal order, any number of them).  A node sees the tokens before the tree, its ancestors and
+    itself, with window >= 0 those of the last window + 1 positions.  Rows of no sequence are left
+    alone, or zeroed with zero_rest (lse -inf).  workspace: as for attn_kv4_decode."""
+    sizes = _check_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, softmax_offset)
+    T, H_q = sizes[1:3]
+    _check(o, "o", torch.bfloat16, 3)
+    if o.shape != q.shape:
+        raise ValueError(f"o must have q's shape {tuple(q.shape)}, got {tuple(o.shape)}")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, 2)
+        if lse.shape != (H_q, T):
+            raise ValueError(f"lse must be {(H_q, T)}, got {tuple(lse.shape)}")
+    dev = _device_of(q, cu_seqlens, parents, pool, page_table, seq_lens, o, lse, softmax_offset, workspace)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, o, lse, window=window,
+                                 softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
+                                 zero_rest=zero_rest, workspace=workspace)
+    _run_kv4_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, o, lse, sizes, dev, window, softmax_type,
+                  softmax_offset, scale, zero_rest, workspace)
+
+
+def _run_kv4_tree(q, cu, parents, pool, page_table, seq_lens, o, lse, sizes, dev, window, softmax_type, softmax_offset,
+                  scale, zero_rest, workspace):
+    ws = _workspace(workspace, attn_kv4_tree_workspace_size(*sizes[:5]) if workspace is None else 0, q.device)
+    st = _load().attn_kv4_tree(_p(q), _p(cu), _p(parents), _p(pool), _p(page_table), _p(seq_lens), _p(o), _p(lse), *sizes,
+                               float(scale or 0.0), _window(window), _stype(softmax_type), _p(softmax_offset),
+                               int(bool(zero_rest)), _p(ws), ws.numel(), _raw_stream(dev, None))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_tree")
+
+
+def sdpa_tree_kv4(q, cu_seqlens, parents, pool, page_table, seq_lens, *, window=-1, softmax_type=VANILLA,
+                  softmax_offset=None, scale=0.0, workspace=None, stream=None):
+    """Allocate O and LSE, run attn_kv4_tree, return (o, lse); rows of no sequence are zero (lse -inf)."""
+    sizes = _check_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, softmax_offset)
+    dev = _device_of(q, cu_seqlens, parents, pool, page_table, seq_lens, softmax_offset, workspace)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return sdpa_tree_kv4(q, cu_seqlens, parents, pool, page_table, seq_lens, window=window,
+                                 softmax_type=softmax_type, softmax_offset=softmax_offset, scale=scale,
+                                 workspace=workspace)
+    o = torch.empty_like(q)
+    lse = torch.empty((sizes[2], sizes[1]), dtype=torch.float32, device=q.device)
+    _run_kv4_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, o, lse, sizes, dev, window, softmax_type,
+                  softmax_offset, scale, True, workspace)
+    return o, lse
+
+
+def attn_kv4_keep(pool, page_table, seq_lens, kept, d, *, stream=None):
+    """Keep accepted nodes: token seq_lens[b] + kept[b, i] of sequence b becomes its token seq_lens[b] + i,
+    for i in order until the first negative entry, in the pool [n_pages, H_kv, block] or in each
+    layer of [n_layers, n_pages, H_kv, block].  kept: int32 [B, most] on the device, the numbers of
+    the accepted nodes, usually ascending (a path from the root); d: the head dim.  The caller
+    then adds the count of each row to seq_lens."""
+    if pool.dim() not in (3, 4):
+        raise ValueError(f"pool must be [n_pages, H_kv, block] or [n_layers, n_pages, H_kv, block], got "
+                         f"{tuple(pool.shape)}")
+    _check(pool, "pool", torch.uint8, pool.dim())
+    n_layers = pool.shape[0] if pool.dim() == 4 else 1
+    n_pages, H_kv, block = pool.shape[-3:]
+    _check(page_table, "page_table", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    _check(kept, "kept", torch.int32, 2)
+    d = int(d)
+    page_size = block * 8 // (9 * d) if d > 0 else 0
+    if kv4_block_bytes(page_size, d) != block:
+        raise ValueError(f"pool's blocks must be kv4_block_bytes(page_size, {d}) bytes, got {block}")
+    B, max_pages = page_table.shape
+    if seq_lens.shape[0] != B or kept.shape[0] != B:
+        raise ValueError(f"seq_lens and kept: one row per row of page_table ({B}), got {seq_lens.shape[0]} and "
+                         f"{kept.shape[0]}")
+    dev = _device_of(pool, page_table, seq_lens, kept)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_keep(pool, page_table, seq_lens, kept, d)
+    st = _load().attn_kv4_keep(_p(pool), _p(page_table), _p(seq_lens), _p(kept), B, kept.shape[1], n_layers, H_kv, d,
+                               n_pages, page_size, max_pages, _raw_stream(dev, None))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_keep")
+
+
 # ----------------------------------------------------------------------------- conveniences
 
 
@@ -1176,11 +1577,15 @@ def new_rng_state(device=None):
 
 
 def attention(q, k, v, softmax_offset=None, *, causal=True, window=-1, softmax_type=VANILLA, scale=0.0,
-              deterministic=True, bias=None, seq_lens_q=None, seq_lens_kv=None, dropout_p=0.0, rng_state=None):
+              deterministic=True, bias=None, seq_lens_q=None, seq_lens_kv=None, dropout_p=0.0, rng_state=None,
+              rope=None, rope_interleaved=False, rope_first_dim=0):
     """Differentiable fused attention. q, k, v, the learnable offset and the bias receive
     gradients. seq_lens_q / seq_lens_kv (int32 [B] on the device) make it a padded batch;
     dropout_p > 0 applies attention dropout with rng_state (a fresh one when None; the
-    backward regenerates the same decisions from it)."""
+    backward regenerates the same decisions from it).  rope: a table of positions (rope_table, one
+    row per position or per row), by which q and k (of the same rows) are rotated first."""
+    if rope is not None:
+        q, k = RopeFunction.apply(q, k, rope, bool(rope_interleaved), int(rope_first_dim))
     if dropout_p and rng_state is None:
         rng_state = new_rng_state(q.device)
     return SDPAFunction.apply(q, k, v, softmax_offset, bias, causal, window, softmax_type, scale, deterministic,

@@ -78,6 +78,42 @@ int attn_kv4_append(const void* k, const void* v, const int* cu_seqlens, void* p
   return launch("kv4 append launch", 1, s, [&] { return sdpa::launch_kv4_append(p, s); });
 }
 
+int attn_kv4_append_rope(const void* q, const void* k, const void* v, const float* table, void* q_out, const int* cu_seqlens,
+                         void* pool, const int* page_table, const int* seq_lens, int B, int T, int H_q, int H_kv, int d,
+                         int n_pages, int page_size, int max_pages, int n, int first_dim, long long q_row_stride,
+                         long long k_row_stride, long long v_row_stride, long long q_out_row_stride, int interleaved,
+                         void* stream) {
+  int st = check_sizes(B, H_kv, d, n_pages, page_size, max_pages);
+  if (st != ATTN_OK) return st;
+  sdpa::RopeParams rp;
+  st = sdpa::rope_params(&rp, q, nullptr, table, q_out, nullptr, T, H_q, 0, d, n, first_dim, T, q_row_stride, 0,
+                         q_out_row_stride, 0, 0);
+  if (st != ATTN_OK) return st;
+  if (k_row_stride < (long long)H_kv * d || v_row_stride < (long long)H_kv * d) return ATTN_ERR_INVALID_ARG;
+  if (T == 0 || (B == 0 && H_q == 0)) return ATTN_OK;
+  if (!table || (B > 0 && (!k || !v || !cu_seqlens || !pool || !page_table || !seq_lens))) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pool, 16) || k_row_stride % 8 || v_row_stride % 8 ||
+      !aligned(cu_seqlens, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(table, 16))
+    return ATTN_ERR_MISALIGNED;
+  sdpa::Kv4StoreParams p;
+  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d, log2_of(page_size)};
+  p.B = B;
+  p.T = T;
+  p.cu = cu_seqlens;
+  p.start = seq_lens;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_stride = k_row_stride;
+  p.v_stride = v_row_stride;
+  p.pool = static_cast<uint8_t*>(pool);
+  p.page_err = sdpa::device_page_error_word();
+  p.site = ATTN_KV4_SITE_APPEND;
+  if (!p.page_err) return ATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch("kv4 append with rotation launch", 1, s,
+                [&] { return sdpa::launch_kv4_append_rope(p, rp, interleaved != 0, s); });
+}
+
 int attn_kv4_gather(const void* pool, const int* page_table, const int* cu_seqlens, const int* seq_lens, void* k,
                     void* v, int B, int T, int H_kv, int d, int n_pages, int page_size, int max_pages, int zero_rest,
                     void* stream) {
@@ -152,6 +188,80 @@ int attn_kv4_decode(const void* q, const void* pool, const int* page_table, cons
   if (!p.err || !p.page_err) return ATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch("kv4 decode launch", 2, s, [&] { return sdpa::launch_kv4_decode(p, workspace, s); });
+}
+
+size_t attn_kv4_tree_workspace_size(int B, int T, int H_q, int H_kv, int d) {
+  if (B < 0 || T < 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || (d != 64 && d != 128)) return 0;
+  return sdpa::kv4_tree_workspace(B, T, H_q, H_kv, d);
+}
+
+int attn_kv4_tree(const void* q, const int* cu_seqlens, const int* parents, const void* pool, const int* page_table,
+                  const int* seq_lens, void* o, float* lse, int B, int T, int H_q, int H_kv, int d, int n_pages,
+                  int page_size, int max_pages, float scale, int window, int softmax_type, const float* softmax_offset,
+                  int zero_rest, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_sizes(B, H_kv, d, n_pages, page_size, max_pages);
+  if (st != ATTN_OK) return st;
+  st = sdpa::check_common(1, T, 0, H_q, H_kv, d, d, 1, window, softmax_type, softmax_offset);
+  if (st != ATTN_OK) return st;
+  if ((long long)T * H_q > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  // (the kernel multiplies scores held as 2^-23 of their value by scale 2^23 log2(e))
+  if (sdpa::resolve_scale(scale, d) > 1e30f) return ATTN_ERR_UNSUPPORTED;
+  if (T == 0 || (B == 0 && !zero_rest)) return ATTN_OK;
+  if (!q || !o || !cu_seqlens || (B > 0 && !seq_lens) || (B > 0 && max_pages > 0 && (!pool || !page_table)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(pool, 16) || !aligned(lse, 4) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(cu_seqlens, 4) || !aligned(parents, 4) || !aligned(softmax_offset, 4))
+    return ATTN_ERR_MISALIGNED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < sdpa::kv4_tree_workspace(B, T, H_q, H_kv, d))
+    return ATTN_ERR_WORKSPACE;
+  sdpa::Kv4TreeParams p;
+  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d, log2_of(page_size)};
+  p.B = B;
+  p.T = T;
+  p.H_q = H_q;
+  p.scale_log2 = sdpa::resolve_scale(scale, d) * 1.4426950408889634f;
+  p.window = window < 0 ? -1 : window;
+  p.softmax_type = softmax_type;
+  p.offset = softmax_offset;
+  p.cu = cu_seqlens;
+  p.start = seq_lens;
+  p.parents = parents;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.zero_rest = zero_rest != 0;
+  p.err = sdpa::device_error_word();
+  p.page_err = sdpa::device_page_error_word();
+  p.site = ATTN_KV4_SITE_TREE;
+  if (!p.err || !p.page_err) return ATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch("kv4 tree launch", 1, s, [&] { return sdpa::launch_kv4_tree(p, workspace, s); });
+}
+
+int attn_kv4_keep(void* pool, const int* page_table, const int* seq_lens, const int* kept, int B, int most, int n_layers,
+                  int H_kv, int d, int n_pages, int page_size, int max_pages, void* stream) {
+  const int st = check_sizes(B, H_kv, d, n_pages, page_size, max_pages);
+  if (st != ATTN_OK) return st;
+  if (most < 0 || n_layers < 0) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || most == 0 || n_layers == 0) return ATTN_OK;
+  if (B > 65535 || n_layers > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (!pool || !page_table || !seq_lens || !kept) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(pool, 16)) return ATTN_ERR_MISALIGNED;
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4)) return ATTN_ERR_MISALIGNED;
+  sdpa::Kv4KeepParams p;
+  p.c = {page_table, n_pages, page_size, max_pages, H_kv, d, log2_of(page_size)};
+  p.B = B;
+  p.most = most;
+  p.start = seq_lens;
+  p.kept = kept;
+  p.pool = static_cast<uint8_t*>(pool);
+  p.layer_bytes = (long long)n_pages * H_kv * sdpa::kv4_block_bytes(page_size, d);
+  p.page_err = sdpa::device_page_error_word();
+  p.site = ATTN_KV4_SITE_KEEP;
+  if (!p.page_err) return ATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch("kv4 keep launch", 1, s, [&] { return sdpa::launch_kv4_keep(p, n_layers, s); });
 }
 
 int attn_kv4_copy_pages(void* pool, int n_layers, int n_pages, size_t page_bytes, const int* src, const int* dst,

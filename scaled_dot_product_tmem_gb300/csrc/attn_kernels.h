@@ -7,6 +7,7 @@
 
 #include "attn_common.cuh"
 #include "kv4.cuh"
+#include "rope.cuh"
 
 namespace sdpa {
 
@@ -229,6 +230,54 @@ struct Kv4DecodeParams {
 };
 size_t kv4_decode_workspace(int B, int S_q, int H_q, int H_kv, int d);
 int launch_kv4_decode(const Kv4DecodeParams& p, void* workspace, cudaStream_t stream);
+
+// Rotation by positions (rope.cuh): cosines and sines of T rows, n <= 128 pairs; heads turned.
+int launch_rope_table(const double* inv_freq, const int* positions, float* table, int T, int n, float gain,
+                      cudaStream_t stream);
+int launch_rope(const RopeParams& p, bool interleaved, cudaStream_t stream);
+// The arguments of a rotation, checked: ATTN_OK or an error status of the public header.
+int rope_params(RopeParams* p, const void* q, const void* k, const float* table, void* q_out, void* k_out, int T, int H_q,
+                int H_k, int d, int n, int first_dim, int table_rows, long long q_stride, long long k_stride,
+                long long q_out_stride, long long k_out_stride, int inverse);
+// launch_kv4_append with the keys turned first (rp.table's rows are the packed rows), and the queries
+// rp.a turned in the same launch.
+int launch_kv4_append_rope(const Kv4StoreParams& p, const RopeParams& rp, bool interleaved, cudaStream_t stream);
+
+// Attention of the nodes of drafted trees over the cache: sequence b's nodes are rows cu[b] ..
+// cu[b + 1] - 1 of q and its tokens start[b], start[b] + 1, ...
+struct Kv4TreeParams {
+  Kv4Pool c;
+  int B, T, H_q;
+  float scale_log2;
+  int window, softmax_type;
+  const float* offset;
+  const int* cu;            // [B + 1]
+  const int* start;         // [B]
+  const int* parents;       // [T], within the sequence, below the node's own number; null: a chain
+  const __nv_bfloat16* q;   // [T, H_q, d]
+  const uint8_t* pool;
+  __nv_bfloat16* o;         // [T, H_q, d]
+  float* lse;               // [H_q, T] or null
+  int zero_rest;
+  int* page_err;
+  int site;
+  int* err;
+};
+size_t kv4_tree_workspace(int B, int T, int H_q, int H_kv, int d);
+int launch_kv4_tree(const Kv4TreeParams& p, void* workspace, cudaStream_t stream);
+
+// Accepted nodes: token start[b] + kept[b][i] becomes token start[b] + i, in every layer.
+struct Kv4KeepParams {
+  Kv4Pool c;
+  int B, most;
+  const int* start;  // [B]
+  const int* kept;   // [B, most], ended by a negative entry
+  uint8_t* pool;
+  long long layer_bytes;
+  int* page_err;
+  int site;
+};
+int launch_kv4_keep(const Kv4KeepParams& p, int n_layers, cudaStream_t stream);
 
 // One warp waits on an mbarrier nobody arrives at: after the wait limit it records
 // kErrTimeoutBase + site in *err and returns (the failure path, without a fault).

@@ -6,6 +6,7 @@
 #include "attn_kernels.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace sdpa {
 
@@ -117,27 +118,72 @@ __device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint
 // Consecutive threads take the groups of one token and head, then the block's tokens, then
 // heads: a warp reads whole rows of K or V and writes one contiguous run of codes (K) or
 // whole token pairs (V).
-template <int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4StoreParams p) {
+// ROT: 1 (half layout) or 2 (interleaved) turns K by the row's position first (rope.cuh): a thread
+// reads the partners of its 16 dims too (the lines are in L1 for the partner's own thread) and keeps its cosines
+// and sines for all heads.  The turned values are rounded to bf16, as a rotation of its own would
+// leave them, and then quantised.  Blocks behind those of the append turn the queries.
+template <int D, int ROT>
+__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4StoreParams p, const RopeParams rp, int gx, int gy) {
   constexpr int NG = D / 16, HS = 256 / (NG * kTok);  // heads a block takes at a time
+  int bx = blockIdx.x, by = blockIdx.y;
+  if constexpr (ROT != 0) {
+    if (bx >= gx * gy) return rope_block<ROT == 2>(rp, bx - gx * gy);
+    by = bx / gx;
+    bx -= by * gx;
+  } else {
+    gy = gridDim.y;
+  }
   __shared__ TokenAt at[kTok];
-  const int t0 = blockIdx.x * kTok;
+  const int t0 = bx * kTok;
   const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
   const int g = threadIdx.x % NG, tk = threadIdx.x / NG % kTok;
   const __nv_bfloat16* kr = p.k + (size_t)(t0 + tk) * p.k_stride + g * 16;
   const __nv_bfloat16* vr = p.v + (size_t)(t0 + tk) * p.v_stride + g * 16;
+  [[maybe_unused]] int part[2] = {0, 0};  // where the partners of dims 16 g + 8 i lie (0: these dims stay)
+  [[maybe_unused]] float c[ROT ? 2 : 1][8], sn[ROT ? 2 : 1][8];
+  if constexpr (ROT != 0) {
+    if (t0 + tk < p.T) {
+      const float* row = rp.table + (size_t)(t0 + tk) * 2 * rp.n;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int x = 16 * g + 8 * i - rp.first;
+        if (x < 0 || x >= 2 * rp.n) continue;
+        if constexpr (ROT == 1) {
+          part[i] = x < rp.n ? rp.n : -rp.n;
+          const float* f = row + (x < rp.n ? x : x - rp.n);
+          load8(f, c[i]);
+          load8(f + rp.n, sn[i]);
+          if (x >= rp.n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sn[i][j] = -sn[i][j];
+          }
+        } else {
+          part[i] = 1;
+          const float4 a = __ldg(reinterpret_cast<const float4*>(row + x / 2));
+          const float4 b = __ldg(reinterpret_cast<const float4*>(row + rp.n + x / 2));
+          c[i][0] = a.x, c[i][1] = a.y, c[i][2] = a.z, c[i][3] = a.w;
+          sn[i][0] = b.x, sn[i][1] = b.y, sn[i][2] = b.z, sn[i][3] = b.w;
+        }
+      }
+    }
+  }
   // a head's values are loaded ahead: the first while the tokens are looked up, then each while
   // the one before it is rounded
   uint4 k0, k1, v0, v1;
+  [[maybe_unused]] uint4 q0, q1;  // the partners
   auto load = [&](int h) {
     const uint4* ks = reinterpret_cast<const uint4*>(kr + (size_t)h * D);
     const uint4* vs = reinterpret_cast<const uint4*>(vr + (size_t)h * D);
     k0 = __ldg(ks);
     k1 = __ldg(ks + 1);
+    if constexpr (ROT == 1) {
+      q0 = __ldg(reinterpret_cast<const uint4*>(kr + (size_t)h * D + part[0]));
+      q1 = __ldg(reinterpret_cast<const uint4*>(kr + (size_t)h * D + 8 + part[1]));
+    }
     v0 = __ldg(vs);
     v1 = __ldg(vs + 1);
   };
-  int h = threadIdx.x / (NG * kTok) + HS * blockIdx.y;
+  int h = threadIdx.x / (NG * kTok) + HS * by;
   if (t0 + tk < p.T && h < p.c.H_kv) load(h);
   find_tokens(p, t0, at);
   const TokenAt a = at[tk];
@@ -148,20 +194,28 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4StoreParams p)
   const int at_v0 = kv4_off_v(P, D) + kv4_v_at(a.w, D == 128 ? g : 2 * g, D);
   const int at_v1 = kv4_off_v(P, D) + kv4_v_at(a.w, 2 * g + 1, D);  // D = 64: 16 dims are two eighths
 #pragma unroll 2
-  for (; h < p.c.H_kv; h += HS * gridDim.y) {
-    const uint4 ka = k0, kb = k1, va = v0, vb = v1;
-    if (h + HS * gridDim.y < p.c.H_kv) load(h + HS * gridDim.y);
+  for (; h < p.c.H_kv; h += HS * gy) {
+    uint4 ka = k0, kb = k1;
+    const uint4 va = v0, vb = v1;
+    if constexpr (ROT == 1) {
+      if (part[0]) ka = rope_turn8(k0, q0, c[0], sn[0]);
+      if (part[1]) kb = rope_turn8(k1, q1, c[1], sn[1]);
+    } else if constexpr (ROT == 2) {
+      if (part[0]) ka = rope_turn_pairs(k0, c[0], sn[0]);
+      if (part[1]) kb = rope_turn_pairs(k1, c[1], sn[1]);
+    }
+    if (h + HS * gy < p.c.H_kv) load(h + HS * gy);
     uint8_t* base = page + (size_t)h * blk;
-    uint32_t c[2];
-    int sb = quantise16(ka, kb, c);
-    *reinterpret_cast<uint2*>(base + at_k) = make_uint2(c[0], c[1]);
+    uint32_t cd[2];
+    int sb = quantise16(ka, kb, cd);
+    *reinterpret_cast<uint2*>(base + at_k) = make_uint2(cd[0], cd[1]);
     base[at_sk] = (uint8_t)sb;
-    sb = quantise16(va, vb, c);
+    sb = quantise16(va, vb, cd);
     if constexpr (D == 128) {
-      *reinterpret_cast<uint2*>(base + at_v0) = make_uint2(c[0], c[1]);
+      *reinterpret_cast<uint2*>(base + at_v0) = make_uint2(cd[0], cd[1]);
     } else {
-      *reinterpret_cast<uint32_t*>(base + at_v0) = c[0];
-      *reinterpret_cast<uint32_t*>(base + at_v1) = c[1];
+      *reinterpret_cast<uint32_t*>(base + at_v0) = cd[0];
+      *reinterpret_cast<uint32_t*>(base + at_v1) = cd[1];
     }
     base[at_sv] = (uint8_t)sb;
   }
@@ -225,8 +279,100 @@ static dim3 store_grid(const Kv4StoreParams& p, int heads) {
 
 int launch_kv4_append(const Kv4StoreParams& p, cudaStream_t stream) {
   const dim3 blocks = store_grid(p, 256 / (p.c.d / 16 * kTok));
-  if (p.c.d == 128) kv4_append_kernel<128><<<blocks, 256, 0, stream>>>(p);
-  else kv4_append_kernel<64><<<blocks, 256, 0, stream>>>(p);
+  const RopeParams none{};
+  if (p.c.d == 128) kv4_append_kernel<128, 0><<<blocks, 256, 0, stream>>>(p, none, 0, 0);
+  else kv4_append_kernel<64, 0><<<blocks, 256, 0, stream>>>(p, none, 0, 0);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_kv4_append_rope(const Kv4StoreParams& p, const RopeParams& rp, bool interleaved, cudaStream_t stream) {
+  dim3 g = store_grid(p, 256 / (p.c.d / 16 * kTok));
+  if (p.B == 0) g = dim3(0, 1);  // only queries to turn
+  const long long blocks = (long long)g.x * g.y + rope_blocks(rp);
+  if (blocks > 0x7fffffffLL) return -2;
+  auto kern = p.c.d == 128 ? (interleaved ? kv4_append_kernel<128, 2> : kv4_append_kernel<128, 1>)
+                           : (interleaved ? kv4_append_kernel<64, 2> : kv4_append_kernel<64, 1>);
+  kern<<<(unsigned)blocks, 256, 0, stream>>>(p, rp, (int)g.x, (int)g.y);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+// Kept tokens: node kept[b][i] of sequence b's tree (its token start[b] + kept[b][i]) becomes token
+// start[b] + i, in the order of i, until the first negative entry.  A thread owns the same few
+// bytes of every token of a sequence, head and layer, so the moves of one sequence follow one another
+// without a barrier, whatever the entries are.  Entries that only move down (kept >= i, as ascending
+// ones do) cannot read what an earlier move of the same four wrote, so four are loaded at once.
+// Bound by latency for few sequences: the chain entry - page - bytes, twice for up to eight tokens.
+template <int D>
+__global__ void __launch_bounds__(64) kv4_keep_kernel(const Kv4KeepParams p) {
+  // words (4 bytes) of K codes, of V codes, of K scales; then V's scale bytes
+  constexpr int KW = D / 8, VW = D / 8, SW = D / 64, NV = D / 16;
+  const int x = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
+  if (x >= KW + VW + SW + NV) return;
+  const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
+  uint8_t* layer = p.pool + (size_t)blockIdx.z * p.layer_bytes;
+  const int start = __ldg(p.start + b);
+  const int* kept = p.kept + (size_t)b * p.most;
+  const bool byte = x >= KW + VW + SW;
+  // this thread's bytes of token tok: their offset in the layer, or -1 (no page)
+  auto where = [&](long long tok) -> long long {
+    const int pg = tok > 0x7fffffffLL ? -1 : kv4_page(p.c, b, (int)tok);
+    if (pg < 0) {
+      atomicCAS(p.page_err, 0, p.site);
+      return -1;
+    }
+    const int w = (int)tok & (P - 1);
+    int at;
+    if (x < KW) at = w * (D / 2) + 4 * x;
+    else if (x < KW + VW) at = kv4_off_v(P, D) + kv4_v_at(w, (x - KW) * 4 / (D / 16), D) + (x - KW) * 4 % (D / 16);
+    else if (!byte) at = kv4_off_sk(P, D) + w * (D / 16) + 4 * (x - KW - VW);
+    else at = kv4_off_sv(P, D) + (w >> 1) * (D / 8) + 2 * (x - KW - VW - SW) + (w & 1);
+    return ((long long)pg * p.c.H_kv + h) * blk + at;
+  };
+  auto get = [&](long long at) { return byte ? (uint32_t)layer[at] : *reinterpret_cast<const uint32_t*>(layer + at); };
+  auto put = [&](long long at, uint32_t v) {
+    if (byte) layer[at] = (uint8_t)v;
+    else *reinterpret_cast<uint32_t*>(layer + at) = v;
+  };
+  for (int i = 0; i < p.most; i += 4) {
+    int from[4], n = 0;
+    bool down = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) from[j] = i + j < p.most ? __ldg(kept + i + j) : -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n == j && from[j] >= 0) ++n;
+      down = down && (n <= j || from[j] >= i + j);
+    }
+    long long src[4], dst[4];
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      src[j] = dst[j] = -1;
+      if (j < n && from[j] != i + j) {
+        src[j] = where((long long)start + from[j]);
+        dst[j] = where((long long)start + i + j);
+      }
+    }
+    if (down) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (src[j] >= 0) v[j] = get(src[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (src[j] >= 0 && dst[j] >= 0) put(dst[j], v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (src[j] >= 0 && dst[j] >= 0) put(dst[j], get(src[j]));
+    }
+    if (n < 4) break;
+  }
+}
+
+int launch_kv4_keep(const Kv4KeepParams& p, int n_layers, cudaStream_t stream) {
+  const dim3 grid((unsigned)p.c.H_kv, (unsigned)p.B, (unsigned)n_layers);
+  if (p.c.d == 128) kv4_keep_kernel<128><<<grid, 64, 0, stream>>>(p);
+  else kv4_keep_kernel<64><<<grid, 64, 0, stream>>>(p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 

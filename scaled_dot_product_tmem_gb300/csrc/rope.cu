@@ -1,0 +1,55 @@
+// rope.cu -- cosines and sines of positions, and heads rotated by them (rope.cuh).
+#include "attn_kernels.h"
+#include "rope.cuh"
+
+namespace sdpa {
+
+// table[t][0][f] = gain cos(p_t w_f), table[t][1][f] = gain sin(p_t w_f).
+//
+// An angle p w of a far position has lost its fraction of a turn long before 32 bits can hold it.
+// So a frequency becomes turns per position, w / 2 pi, as a 64-bit fraction of a turn (whole turns
+// dropped), and p times that in 64-bit whole numbers, wrapping, is the angle's fraction of a turn: exact
+// for every position, off only by what the frequency's own 53 bits leave (2^-54 of it).  The
+// frequencies are converted once a block: 64-bit floating point has 2 operations a cycle and SM.
+__global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq, const int* positions, float* table, int T,
+                                                         int n, float gain) {
+  __shared__ unsigned long long turns[128];
+  if (threadIdx.x < n) {
+    const double f = inv_freq[threadIdx.x] * 0.15915494309189533577;  // 1 / (2 pi)
+    turns[threadIdx.x] = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+  }
+  __syncthreads();
+  const int rows = 256 / n, f = threadIdx.x % n, r = threadIdx.x / n;
+  if (r >= rows) return;
+  const unsigned long long w = turns[f];
+  for (long long t = (long long)blockIdx.x * rows + r; t < T; t += (long long)gridDim.x * rows) {
+    const long long turn = (long long)((unsigned long long)(long long)__ldg(positions + t) * w);
+    float s, c;  // half turns in [-1, 1]
+    sincospif(__ll2float_rn(turn) * 1.08420217248550443401e-19f, &s, &c);
+    table[(size_t)t * 2 * n + f] = gain * c;
+    table[(size_t)t * 2 * n + n + f] = gain * s;
+  }
+}
+
+template <bool IL>
+__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+  rope_block<IL>(p, blockIdx.x);
+}
+
+int launch_rope_table(const double* inv_freq, const int* positions, float* table, int T, int n, float gain,
+                      cudaStream_t stream) {
+  const int rows = 256 / n;
+  const int blocks = (T + rows - 1) / rows;
+  rope_table_kernel<<<blocks < 152 * 8 ? blocks : 152 * 8, 256, 0, stream>>>(inv_freq, positions, table, T, n, gain);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_rope(const RopeParams& p, bool interleaved, cudaStream_t stream) {
+  const long long blocks = rope_blocks(p);
+  if (blocks > 0x7fffffffLL) return -2;
+  if (interleaved) rope_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(p);
+  else rope_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(p);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace sdpa

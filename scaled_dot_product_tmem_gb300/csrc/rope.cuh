@@ -1,0 +1,145 @@
+// rope.cuh -- rotation of query and key heads by their rows' positions, shared by the kernels
+// that rotate (rope.cu) and the one that rotates keys on their way into the cache (kv4_store.cu).
+//
+// A pair (x1, x2) of a head becomes (x1 c - x2 s, x2 c + x1 s) with c and s from a table
+// [rows][2][n] of fp32 (cosines, then sines, of a row's n pairs).  Dims first .. first + 2n of a
+// head hold the pairs: (f, f + n), or (2f, 2f + 1) when interleaved; the other dims stay.  The
+// two products of a value are rounded to fp32 before their sum, the same everywhere, so that a
+// key rotated on its way into the cache is bit for bit the one rotated by itself.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace sdpa {
+
+struct RopeHeads {  // one tensor's rows: x read, y written (may be the same)
+  const __nv_bfloat16* x = nullptr;
+  __nv_bfloat16* y = nullptr;
+  long long xs = 0, ys = 0;  // elements from row to row
+  int H = 0;
+};
+struct RopeParams {
+  RopeHeads a, b;      // queries and keys
+  const float* table;  // [table_rows][2][n]; row t takes table row t % table_rows
+  int T, table_rows, d, n, first;
+  int inverse;  // turn back: the transposed rotation
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// x1 c - x2 s of 8 values
+__device__ __forceinline__ uint4 rope_turn8(const uint4& x1, const uint4& x2, const float (&c)[8], const float (&s)[8]) {
+  const uint32_t u[4] = {x1.x, x1.y, x1.z, x1.w}, w[4] = {x2.x, x2.y, x2.z, x2.w};
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = pack_bf16x2(__fsub_rn(__fmul_rn(bf16_lo(u[i]), c[2 * i]), __fmul_rn(bf16_lo(w[i]), s[2 * i])),
+                       __fsub_rn(__fmul_rn(bf16_hi(u[i]), c[2 * i + 1]), __fmul_rn(bf16_hi(w[i]), s[2 * i + 1])));
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+// 4 pairs side by side
+__device__ __forceinline__ uint4 rope_turn_pairs(const uint4& x, const float* c, const float* s) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = bf16_lo(u[i]), b = bf16_hi(u[i]);
+    y[i] = pack_bf16x2(__fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i])), __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i])));
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// A head's work: n / 8 pieces of 8 pairs, and the dims that stay in pieces of 16.
+__host__ __device__ __forceinline__ int rope_pieces(int d, int n) { return n / 8 + (d - 2 * n + 15) / 16; }
+constexpr int kRopeItems = 4;  // pieces of a thread, all loaded before the first is stored
+__host__ __device__ __forceinline__ long long rope_blocks(const RopeParams& p) {
+  const long long items = (long long)p.T * (p.a.H + p.b.H) * rope_pieces(p.d, p.n);
+  return (items + 256 * kRopeItems - 1) / (256 * kRopeItems);
+}
+
+// Block `block` of rope_blocks(): 256 threads, consecutive ones take consecutive pieces of a head, then
+// heads, then rows.
+template <bool IL>
+__device__ __forceinline__ void rope_block(const RopeParams& p, long long block) {
+  const int pieces = rope_pieces(p.d, p.n), turn = p.n / 8, heads = p.a.H + p.b.H;
+  const long long items = (long long)p.T * heads * pieces;
+  uint4 v0[kRopeItems], v1[kRopeItems];
+  __nv_bfloat16* dst[kRopeItems];
+  const float* cs[kRopeItems];  // null: a piece that stays, or none
+  int kind[kRopeItems];         // bits 0, 1: which of the two vectors are stored
+  const int step1 = IL ? 8 : p.n;
+#pragma unroll
+  for (int i = 0; i < kRopeItems; ++i) {
+    const long long e = (block * kRopeItems + i) * 256 + threadIdx.x;
+    kind[i] = 0;
+    cs[i] = nullptr;
+    if (e >= items) continue;
+    int piece, h;
+    long long t;
+    if (items <= 0x7fffffffLL) {  // 32-bit division
+      const unsigned r = (unsigned)e / (unsigned)pieces;
+      piece = (int)((unsigned)e - r * pieces);
+      t = r / (unsigned)heads;
+      h = (int)(r - (unsigned)t * heads);
+    } else {
+      const long long r = e / pieces;
+      piece = (int)(e - r * pieces);
+      t = r / heads;
+      h = (int)(r - t * heads);
+    }
+    const bool q = h < p.a.H;
+    const RopeHeads& m = q ? p.a : p.b;
+    const int hh = q ? h : h - p.a.H;
+    const __nv_bfloat16* x = m.x + (size_t)t * m.xs + (size_t)hh * p.d;
+    __nv_bfloat16* y = m.y + (size_t)t * m.ys + (size_t)hh * p.d;
+    if (piece < turn) {
+      const int at = p.first + piece * (IL ? 16 : 8);
+      v0[i] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+      v1[i] = __ldcs(reinterpret_cast<const uint4*>(x + at + step1));
+      dst[i] = y + at;
+      cs[i] = p.table + (size_t)(t % p.table_rows) * 2 * p.n + piece * 8;
+      kind[i] = 3;
+    } else if (x != y) {
+      // the dims that stay, 16 from the piece's start on: those before `first`, then those behind the pairs
+      const int k = (piece - turn) * 16, end = p.d - 2 * p.n;
+      const int a0 = k < p.first ? k : k + 2 * p.n, a1 = k + 8 < p.first ? k + 8 : k + 8 + 2 * p.n;
+      v0[i] = __ldcs(reinterpret_cast<const uint4*>(x + a0));
+      __stcs(reinterpret_cast<uint4*>(y + a0), v0[i]);
+      if (k + 8 < end) __stcs(reinterpret_cast<uint4*>(y + a1), __ldcs(reinterpret_cast<const uint4*>(x + a1)));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRopeItems; ++i) {
+    if (kind[i] == 0) continue;
+    float c[8], s[8];
+    load8(cs[i], c);
+    load8(cs[i] + p.n, s);
+    if (p.inverse) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = -s[j];
+    }
+    uint4 y0, y1;
+    if constexpr (IL) {
+      y0 = rope_turn_pairs(v0[i], c, s);
+      y1 = rope_turn_pairs(v1[i], c + 4, s + 4);
+    } else {
+      y0 = rope_turn8(v0[i], v1[i], c, s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = -s[j];
+      y1 = rope_turn8(v1[i], v0[i], c, s);
+    }
+    *reinterpret_cast<uint4*>(dst[i]) = y0;
+    *reinterpret_cast<uint4*>(dst[i] + step1) = y1;
+  }
+}
+
+}  // namespace sdpa
