@@ -236,7 +236,7 @@ int attn_kv4_tree(const void* q, const int* cu_seqlens, const int* parents, cons
   p.site = ATTN_KV4_SITE_TREE;
   if (!p.err || !p.page_err) return ATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch("kv4 tree launch", 1, s, [&] { return sdpa::launch_kv4_tree(p, workspace, s); });
+  return launch("kv4 tree launch", 2, s, [&] { return sdpa::launch_kv4_tree(p, workspace, s); });
 }
 
 int attn_kv4_keep(void* pool, const int* page_table, const int* seq_lens, const int* kept, int B, int most, int n_layers,
