@@ -39,37 +39,30 @@ namespace {
 constexpr int kUnit = 128;    // tokens of a unit
 constexpr int kMaxGrid = 152;  // CTAs, and pairs of partial sums in the workspace
 constexpr int kSegCost = 2;   // a segment's fixed costs, in units
-constexpr int kDecWarps = 8;
-constexpr int kThreads = 32 * (8 + kDecWarps + 4);  // (the last two warps have nothing to do: registers are split by fours)
+constexpr int kThreads = 512;  // 8 warps softmax, 4 decode, 1 issues products, 1 loads (2 only share their registers)
 // Registers a thread of the launch, and after the split: softmax, decoding, the rest.
-constexpr int kRegs = 96, kRegsSoft = 136, kRegsDec = 72, kRegsRest = 64;
-static_assert(256 * kRegsSoft + 256 * kRegsDec + 128 * kRegsRest <= kThreads * kRegs, "the launch's registers");
+constexpr int kRegs = 128, kRegsSoft = 184, kRegsDec = 88, kRegsRest = 56;
+static_assert(256 * kRegsSoft + 128 * kRegsDec + 128 * kRegsRest <= kThreads * kRegs, "the launch's registers");
+constexpr int kDecWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 
 enum TreeSite { kTreeRawFull = 0xB0, kTreeRawEmpty, kTreeKFull, kTreeKEmpty, kTreeVFull, kTreeVEmpty, kTreeQFull, kTreeQEmpty,
-                kTreeS, kTreeP, kTreeO, kTreeDrain };
+                kTreeS, kTreeP, kTreeO, kTreeDrain, kTreePartFull, kTreePartEmpty };
 
-template <int D, bool TWO>
-struct TreeCfg {
-  static constexpr int ROWS = TWO ? 256 : 128;  // rows of a block
-  static constexpr int BLK = 128 * 128;         // one operand block: 128 rows of 64 bf16
-  static constexpr int TILE = BLK * (D / 64);
-  static constexpr int NK = 2, NV = TWO ? 1 : 2;
-  static constexpr int STAGES = D == 128 ? 3 : 6;
-  static constexpr int STAGE = kUnit * D * 9 / 8;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + (TWO ? 2 : 1) * TILE;
-  static constexpr int OFF_V = OFF_K + NK * TILE;
-  static constexpr int OFF_RAW = OFF_V + NV * TILE;
-  static constexpr int OFF_NAN = OFF_RAW + STAGES * STAGE;  // [NV][D / 16][64] bits of the two tokens of a pair
-  static constexpr int OFF_ML = OFF_NAN + NV * D / 16 * 64;  // [2][128] maxima, sums, NaN groups
-  static constexpr int OFF_BAR = OFF_ML + 3 * 2 * 128 * 4;
-  static constexpr int N_BAR = 2 * STAGES + 2 * NK + 2 * NV + 2 + 6 + 1;
-  static constexpr int OFF_SLOT = OFF_BAR + N_BAR * 8;
-  static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // (aligned by the kernel)
-  static constexpr int PART = ROWS * (D + 2);        // floats of one partial: sums, maxima, denominators
-  static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(SMEM > 116 * 1024, "one CTA per SM keeps the 512-column TMEM allocation uncontended");
-};
+// mbar_wait_warp() in fewer instructions: some thirty of them are in line, and every role's code comes
+// from the same instruction cache.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, int* err, int site) {
+  const uint32_t a = smem_u32(bar);
+  bool ok = mbar_try_wait(a, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    do {
+      ok = mbar_try_wait(a, parity) || mbar_try_wait(a, parity);
+      if (!ok && globaltimer_ns() - t0 > SDPA_WAIT_LIMIT_NS) atomicCAS(err, 0, kErrTimeoutBase + site);
+    } while (!ok && *(volatile int*)err == 0);
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
 
 // A sequence's sizes.
 struct TreeSeq {
@@ -93,126 +86,62 @@ __device__ __forceinline__ TreeSeq tree_seq(const Kv4TreeParams& p, int b) {
   s.blocks = (int)(((long long)s.n * (p.H_q / p.c.H_kv) + ROWS - 1) / ROWS);
   return s;
 }
-// Units that row block rb of the sequence needs: up to its last node's own token.
-template <int ROWS>
-__device__ __forceinline__ int block_units(const Kv4TreeParams& p, const TreeSeq& s, int rb) {
-  const int G = p.H_q / p.c.H_kv;
-  const int last = (int)min((long long)s.n - 1, (((long long)rb + 1) * ROWS - 1) / G);
-  const int len = (int)min((long long)s.L + last + 1, (long long)s.len);
-  return max((len - 1) / kUnit - s.first + 1, 0);
-}
-
 // How the units of a call are numbered: sequence by sequence, in it kv head by kv head, in it row
 // block by row block; each such segment has units + kSegCost numbers, the first kSegCost for its
-// fixed costs.  Every warp works this out for itself.
-template <int ROWS>
-struct TreeScan {
-  __device__ __forceinline__ static long long numbers(const Kv4TreeParams& p, int b) {
-    if (b >= p.B) return 0;
-    const TreeSeq s = tree_seq<ROWS>(p, b);
-    return (long long)s.seg() * s.blocks * p.c.H_kv;
-  }
-  __device__ static long long sum(const Kv4TreeParams& p, int end) {
-    long long t = 0;
-    for (int b = threadIdx.x % 32; b < end; b += 32) t += numbers(p, b);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    return t;
-  }
-  // The sequence that holds number u (below the total); the numbers before it are returned.
-  __device__ static long long find(const Kv4TreeParams& p, long long u, int* b) {
-    const int lane = threadIdx.x % 32;
-    long long carry = 0;
-    for (int base = 0;; base += 32) {
-      const long long m = numbers(p, base + lane);
-      long long s = m;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += o;
-      }
-      s += carry;
-      const unsigned holds = __ballot_sync(0xffffffffu, u < s);
-      if (holds || base + 32 >= p.B) {
-        const int w = holds ? __ffs(holds) - 1 : 0;
-        *b = base + w;
-        return __shfl_sync(0xffffffffu, s - m, w);
-      }
-      carry = __shfl_sync(0xffffffffu, s, 31);
-    }
-  }
+// fixed costs.  CTA c takes an even share of the numbers, in order.
+
+// A CTA's part of a segment, as the loading warp works it out for the others.
+struct TreePart {
+  int row0, n, L, len, lo;  // the sequence (TreeSeq)
+  int unit0, cnt;           // first unit (of 128 tokens) and how many; -1: there are no more parts
+  int hk, node0, rem0, R;   // kv head; the row block's first node, its first head in the group, its rows
+  int slot;                 // the whole of a segment: -1; a piece: which of the CTA's two places it takes
+  // Units below u_win and from u_tree on have tokens that not every row sees: at a window's lower end,
+  // and from the unit on that holds the tree's first node or ends past the tokens before it.
+  int u_win, u_tree;
+  int pad[2];
 };
+constexpr int kParts = 4;  // parts the loading warp may be ahead
 
-// CTA c of n takes numbers [tree_cut(c), tree_cut(c + 1)).
-__device__ __forceinline__ long long tree_cut(long long total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int tree_cta_of(long long total, int n, long long u) {
-  int c = (int)min((long long)n - 1, u * n / total);
-  while (c > 0 && tree_cut(total, n, c) > u) --c;
-  while (c + 1 < n && tree_cut(total, n, c + 1) <= u) ++c;
-  return c;
-}
-__device__ __forceinline__ int tree_ctas(long long total, int grid) {
-  const long long want = (total + kSegCost) / (kSegCost + 1);
-  return want < grid ? (int)want : grid;
-}
-
-// A CTA's run of segments.
-template <int ROWS>
-struct TreeWalk {
-  int b, vh;           // sequence; kv head and row block in it
-  int from, to;        // this CTA's units of the segment
-  long long left;      // numbers of this CTA after it
-  TreeSeq s;
-  __device__ __forceinline__ int segments(const Kv4TreeParams& p) const { return p.c.H_kv * s.blocks; }
-  __device__ __forceinline__ int hk() const { return vh / s.blocks; }
-  __device__ __forceinline__ int rb() const { return vh % s.blocks; }
-  __device__ __forceinline__ void enter(int number) {
-    const int take = (int)min((long long)(s.seg() - number), left);
-    from = max(number - kSegCost, 0);
-    to = max(number + take - kSegCost, 0);
-    left -= take;
-  }
-  __device__ __forceinline__ void begin(const Kv4TreeParams& p, long long u_begin, long long u_end) {
-    const long long r = u_begin - TreeScan<ROWS>::find(p, u_begin, &b);
-    s = tree_seq<ROWS>(p, b);
-    vh = (int)(r / s.seg());
-    left = u_end - u_begin;
-    enter((int)(r % s.seg()));
-  }
-  // To the next segment of which this CTA has units; false: none.
-  __device__ __forceinline__ bool settle(const Kv4TreeParams& p) {
-    while (from == to) {
-      if (left == 0) return false;
-      next(p);
-    }
-    return true;
-  }
-  __device__ __forceinline__ void next(const Kv4TreeParams& p) {
-    if (++vh == segments(p)) {
-      vh = 0;
-      do {
-        ++b;
-        s = tree_seq<ROWS>(p, b);
-      } while (s.units == 0);
-    }
-    enter(0);
-  }
-  __device__ __forceinline__ bool advance(const Kv4TreeParams& p) {
-    if (left == 0) return false;
-    next(p);
-    return settle(p);
-  }
-  // This CTA's units that the segment's row block needs.
-  __device__ __forceinline__ int count(const Kv4TreeParams& p) const {
-    return max(min(to, block_units<ROWS>(p, s, rb())) - from, 0);
-  }
+// What the join has to know of a piece.
+struct TreePiece {
+  int row0, node0, rem0, R, hk;
+  int valid, starts, ends;  // the segment's first piece, its last
 };
+static_assert(sizeof(TreePiece) == 32, "read as two 16-byte words");
 
-__device__ __forceinline__ int tree_parent(const Kv4TreeParams& p, const TreeSeq& s, int i) {
+__device__ __forceinline__ int tree_parent(const Kv4TreeParams& p, int row0, int i) {
   if (!p.parents) return i - 1;
-  const int a = __ldg(p.parents + s.row0 + i);
+  const int a = __ldg(p.parents + row0 + i);
   return a < i && a >= 0 ? a : -1;
 }
+
+// x / g for 0 <= x < 2^20, inv = 1 / g: the fp32 product is off by less than half of 1 / g.
+__device__ __forceinline__ int small_div(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
+
+template <int D, bool TWO>
+struct TreeCfg {
+  static constexpr int ROWS = TWO ? 256 : 128;  // rows of a block
+  static constexpr int BLK = 128 * 128;         // one operand block: 128 rows of 64 bf16
+  static constexpr int TILE = BLK * (D / 64);
+  static constexpr int NK = TWO ? 1 : 2, NV = 2;  // (two row tiles: S of a unit is done long before its P V)
+  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int STAGE = kUnit * D * 9 / 8;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + (TWO ? 2 : 1) * TILE;
+  static constexpr int OFF_V = OFF_K + NK * TILE;
+  static constexpr int OFF_RAW = OFF_V + NV * TILE;
+  static constexpr int OFF_NAN = OFF_RAW + STAGES * STAGE;  // [NV][D / 16][64] bits of the two tokens of a pair
+  static constexpr int OFF_ML = OFF_NAN + NV * D / 16 * 64;  // [2][128] maxima, sums, NaN groups
+  static constexpr int OFF_PART = OFF_ML + 3 * 2 * 128 * 4;
+  static constexpr int OFF_BAR = OFF_PART + kParts * (int)sizeof(TreePart);
+  static constexpr int N_BAR = 2 * STAGES + 2 * NK + 2 * NV + 2 + 6 + 1 + 2 * kParts;
+  static constexpr int OFF_SLOT = OFF_BAR + N_BAR * 8;
+  static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // (aligned by the kernel)
+  static constexpr int PART = ROWS * (D + 2);  // floats of one partial: sums, maxima, denominators
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SMEM > 116 * 1024, "one CTA per SM keeps the 512-column TMEM allocation uncontended");
+};
 
 template <int N>
 __device__ __forceinline__ void regs_less() {
@@ -263,9 +192,8 @@ __device__ __forceinline__ uint4 ordered8(const float* v) {
 }  // namespace
 
 template <int D, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreeParams p, float* partial) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreeParams p, TreePiece* pieces, float* partial) {
   using C = TreeCfg<D, TWO>;
-  using Walk = TreeWalk<C::ROWS>;
   constexpr int NST = C::STAGES, NK = C::NK, NV = C::NV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -281,105 +209,230 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
   uint64_t* p_ready = s_ready + 2;
   uint64_t* o_done = p_ready + 2;
   uint64_t* mma_done = o_done + 2;
+  uint64_t* part_full = mma_done + 1;
+  uint64_t* part_empty = part_full + kParts;
+  TreePart* parts = reinterpret_cast<TreePart*>(smem + C::OFF_PART);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int* err = p.err;
 
   grid_launch_dependents();  // the join may be set up meanwhile
-  const long long total = TreeScan<C::ROWS>::sum(p, p.B);
-  if (total == 0) return;
-  const int n_cta = tree_ctas(total, gridDim.x);
-  if ((int)blockIdx.x >= n_cta) return;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kDecWarps);
+      mbar_init(&raw_empty[s], 4);
     }
     for (int s = 0; s < NK; ++s) {
-      mbar_init(&k_full[s], kDecWarps);
+      mbar_init(&k_full[s], 4);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < NV; ++s) {
-      mbar_init(&v_full[s], kDecWarps);
+      mbar_init(&v_full[s], 4);
       mbar_init(&v_empty[s], 1);
     }
-    mbar_init(q_full, kDecWarps);
+    mbar_init(q_full, 4);
     mbar_init(q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_ready[t], 1);
-      mbar_init(&p_ready[t], 128);
+      mbar_init(&p_ready[t], 4);
       mbar_init(&o_done[t], 1);
     }
     mbar_init(mma_done, 1);
+    for (int s = 0; s < kParts; ++s) {
+      mbar_init(&part_full[s], 1);
+      mbar_init(&part_empty[s], 8 + 4 + 1);
+    }
     fence_barrier_init();
   }
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     tmem_alloc<512>(tmem_slot);
     tmem_relinquish();
+  }
+  // This CTA's numbers (the loading warp's): the sequence b they begin in, `skip` of its numbers before them,
+  // and how many.
+  int b = 0;
+  long long skip = 0, left = 0;
+  if (warp == kLoadWarp) {
+    long long total = 0, mine = 0, upto = 0, first = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      long long carry = 0;
+#pragma unroll 1
+      for (int base = 0; base < p.B && !found; base += 32) {
+        if (pass == 0 || p.B > 32) {
+          mine = 0;
+          if (base + lane < p.B) {
+            const TreeSeq s = tree_seq<C::ROWS>(p, base + lane);
+            mine = (long long)s.seg() * s.blocks * p.c.H_kv;
+          }
+          upto = mine;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += o;
+          }
+        }
+        if (pass == 1) {
+          const unsigned holds = __ballot_sync(0xffffffffu, first < carry + upto);
+          if (holds) {
+            const int w = __ffs(holds) - 1;
+            b = base + w;
+            skip = first - carry - __shfl_sync(0xffffffffu, upto - mine, w);
+            found = true;
+          }
+        }
+        carry += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (pass == 0) {
+        total = carry;
+        const long long want = total / (kSegCost + 1) + 1;  // at least a segment's cost and a unit each
+        const int n = (int)min((long long)gridDim.x, want);
+        if (total == 0 || (int)blockIdx.x >= n) break;
+        const long long q = total <= 0x7fffffffLL ? (long long)((unsigned)total / (unsigned)n) : total / n;
+        const int rest = (int)(total - q * n);
+        first = q * blockIdx.x + min((int)blockIdx.x, rest);
+        left = q + ((int)blockIdx.x < rest ? 1 : 0);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int G = p.H_q / p.c.H_kv;
-  Walk at;
-  at.begin(p, tree_cut(total, n_cta, blockIdx.x), tree_cut(total, n_cta, blockIdx.x + 1));
   bool ok = true;
+  // The next part of this CTA's work; cnt < 0: there is none.  It stays in shared memory (few registers hold
+  // what a role needs of it all the time) until part_done().
+  int n_part = 0;
+  auto next_part = [&]() {
+    ok = ok && tree_wait(&part_full[n_part % kParts], (n_part / kParts) & 1, err, kTreePartFull);
+    return ok && parts[n_part % kParts].cnt >= 0;
+  };
+  auto part_done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&part_empty[n_part % kParts]);
+    ++n_part;
+  };
 
-  if (warp >= 16) regs_less<kRegsRest>();
-  if (warp == 17) {
-    // ---------------------------------------------------------------- producer
-    // Lane i copies the block of page i of a unit (whole, also past the sequence's end), if some node
-    // sees a token of it: the pages before a window may be gone from the table.  Its page is looked up one
-    // unit ahead.
-    const int P = p.c.page_size, pieces = kUnit / P, t0 = lane * P;
-    const int block = kv4_block_bytes(P, D);
+  if (warp >= kMmaWarp) regs_less<kRegsRest>();
+  if (warp == kLoadWarp) {
+    // ---------------------------------------------------------------- loading warp
+    // Walks the CTA's segments, passes their parts on, and streams their units: lane i copies the block of
+    // page i of a unit (whole, also past the sequence's end), if some node sees a token of it: the pages
+    // before a window may be gone from the table.  Its page is looked up one unit ahead.
+    const int P = p.c.page_size, n_pages = kUnit / P, t0 = lane * P;
+    const int block = kv4_block_bytes(P, D), G = p.H_q / p.c.H_kv;
     const size_t page_bytes = (size_t)block * p.c.H_kv;
-    bool more = at.settle(p);
-    int k = 0, cnt = more ? at.count(p) : 0;
-    auto skip = [&]() {  // to the next unit there is
-      while (more && k >= cnt) {
-        more = at.advance(p);
-        k = 0;
-        cnt = more ? at.count(p) : 0;
-      }
-    };
-    auto page_of = [&]() {
-      const long long tok = (long long)(at.s.first + at.from + k) * kUnit + t0;
-      return lane < pieces && tok < at.s.len && tok + P > at.s.lo ? kv4_page(p.c, at.b, (int)tok) : -2;
-    };
-    skip();
-    int page = more ? page_of() : -2, n = 0;
-    for (; more && ok; ++n) {
-      const int stage = n % NST;
-      uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
-      const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (size_t)at.hk() * block;
-      const int have = page;
-      ++k;
-      skip();
-      if (more) page = page_of();
-      if (n >= NST) ok = mbar_wait_warp(&raw_empty[stage], (n / NST - 1) & 1, err, kTreeRawEmpty);
-      if (!ok) break;
-      if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
-        if (have == -1) {
-          for (int o = kv4_off_sk(P, D); o < block; o += 16)
-            *reinterpret_cast<uint4*>(st + lane * block + o) = make_uint4(0u, 0u, 0u, 0u);
-          atomicCAS(p.page_err, 0, p.site);
-          fence_proxy_async_smem();
+    TreeSeq s{};
+    int hk = 0, rb = 0, n = 0;
+    bool enter = true;          // the sequence's sizes are still to be read
+    int used = 0;               // this CTA's places for pieces that are taken, a bit each
+    bool first = true;
+#pragma unroll 1
+    while (ok) {
+      TreePart t{};
+      bool starts = false, ends = false;
+      if (left > 0) {
+        if (enter) {
+          if (b >= p.B) {  // (the offsets were changed meanwhile)
+            left = 0;
+            continue;
+          }
+          s = tree_seq<C::ROWS>(p, b);
+          if (s.seg() == 0) {
+            ++b;
+            continue;
+          }
+          const long long vh = skip <= 0x7fffffffLL ? (long long)((unsigned)skip / (unsigned)s.seg()) : skip / s.seg();
+          skip -= vh * s.seg();
+          hk = (int)((unsigned)vh / (unsigned)s.blocks);
+          rb = (int)vh - hk * s.blocks;
+          enter = false;
         }
-        __syncwarp();
+        // the CTA's units [from, to) of the segment
+        const int take = (int)min((long long)s.seg() - skip, left);
+        const int from = max((int)skip - kSegCost, 0), to = max((int)skip + take - kSegCost, 0);
+        left -= take;
+        skip = 0;
+        const int r0 = rb * C::ROWS;  // (rows of a kv head are below 2^31)
+        t.row0 = s.row0, t.n = s.n, t.L = s.L, t.len = s.len, t.lo = s.lo;
+        t.hk = hk;
+        t.node0 = r0 / G;
+        t.rem0 = r0 - t.node0 * G;
+        t.R = min(s.n * G - r0, C::ROWS);
+        // of them those that the row block needs: up to its last node's own token
+        const int last = t.node0 + (t.rem0 + t.R - 1) / G;
+        const int len = (int)min((long long)s.L + last + 1, (long long)s.len);
+        t.unit0 = s.first + from;
+        t.cnt = max(min(to, (len - 1) / kUnit - s.first + 1) - from, 0);
+        t.u_tree = s.L / kUnit;
+        const long long all_see = (long long)s.L + s.n - 1 - p.window;  // from this token on every row sees the prefix
+        t.u_win = p.window >= 0 && all_see > 0 ? (int)((unsigned)all_see / kUnit) + 1 : 0;
+        starts = from == 0;
+        ends = to == s.units;
+        t.slot = starts && ends ? -1 : first ? 0 : 1;
+        if (++rb == s.blocks) {
+          rb = 0;
+          if (++hk == p.c.H_kv) {
+            ++b;
+            enter = true;
+          }
+        }
+        if (from == to) continue;  // only fixed costs
+        first = false;
+        if (t.slot >= 0) {
+          used |= 1 << t.slot;
+          if (lane == 0) pieces[2 * blockIdx.x + t.slot] = TreePiece{t.row0, t.node0, t.rem0, t.R, t.hk, 1, starts, ends};
+        }
+      } else {
+        t.cnt = -1;
       }
-      const uint32_t all = __popc(__ballot_sync(0xffffffffu, have >= 0)) * block;
-      if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], all);
+      const int slot = n_part % kParts;
+      if (n_part >= kParts) ok = tree_wait(&part_empty[slot], (n_part / kParts - 1) & 1, err, kTreePartEmpty);
+      if (!ok) break;
+      if (lane == 0) {
+        parts[slot] = t;
+        mbar_arrive(&part_full[slot]);
+      }
+      ++n_part;
       __syncwarp();
-      if (have >= 0) bulk_load(st + lane * block, src, block, &raw_full[stage]);
+      if (t.cnt < 0) break;
+      auto page_of = [&](int k) {
+        const long long tok = (long long)(t.unit0 + k) * kUnit + t0;
+        return k < t.cnt && lane < n_pages && tok < t.len && tok + P > t.lo ? kv4_page(p.c, b - (enter ? 1 : 0), (int)tok) : -2;
+      };
+      int page = page_of(0);
+#pragma unroll 1
+      for (int k = 0; k < t.cnt; ++k, ++n) {
+        const int stage = n % NST;
+        uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
+        const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (size_t)t.hk * block;
+        const int have = page;
+        page = page_of(k + 1);
+        if (n >= NST) ok = tree_wait(&raw_empty[stage], (n / NST - 1) & 1, err, kTreeRawEmpty);
+        if (!ok) break;
+        if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
+          if (have == -1) {
+            for (int o = kv4_off_sk(P, D); o < block; o += 16)
+              *reinterpret_cast<uint4*>(st + lane * block + o) = make_uint4(0u, 0u, 0u, 0u);
+            atomicCAS(p.page_err, 0, p.site);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
+        const uint32_t all = __popc(__ballot_sync(0xffffffffu, have >= 0)) * block;
+        if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], all);
+        __syncwarp();
+        if (have >= 0) bulk_load(st + lane * block, src, block, &raw_full[stage]);
+      }
     }
+    if (lane < 2 && !(used >> lane & 1)) pieces[2 * blockIdx.x + lane].valid = 0;
     // every copy this warp started must land before the CTA may exit: wait for the last ones
     for (int s = 0; s < NST && s < n; ++s) {
       const int last = s + (n - 1 - s) / NST * NST;
-      mbar_wait_warp(&raw_full[s], (last / NST) & 1, err, kTreeDrain);
+      tree_wait(&raw_full[s], (last / NST) & 1, err, kTreeDrain);
     }
-  } else if (warp == 16) {
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false), idO = idesc_bf16_f32(128, D, false, true);
     const uint32_t sQ = smem_u32(smem + C::OFF_Q), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
@@ -399,17 +452,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
       for (int kk = 0; kk < kUnit / 16; ++kk)
         mma_ts_warp(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, desc_add(dv, kk * 2048), idO, (acc || kk > 0) ? 1u : 0u);
     };
-    int nq = 0, nk = 0, nv = 0, np[2] = {0, 0};  // phases consumed
+    int nq = 0, nk = 0, nv = 0;  // phases consumed
+    uint32_t np = 0u;            // parities of p_ready, a bit a tile
     bool issued = false;
     auto wait_K = [&]() {
-      ok = ok && mbar_wait_warp(&k_full[nk % NK], (nk / NK) & 1, err, kTreeKFull);
+      ok = ok && tree_wait(&k_full[nk % NK], (nk / NK) & 1, err, kTreeKFull);
       if (ok) tc_fence_after();
       return ok;
     };
-    for (bool more = at.settle(p); more && ok; more = at.advance(p)) {
-      const int cnt = at.count(p);
+#pragma unroll 1
+    while (next_part()) {
+      const int cnt = parts[n_part % kParts].cnt;
+      part_done();
       if (cnt == 0) continue;
-      ok = mbar_wait_warp(q_full, nq++ & 1, err, kTreeQFull);
+      ok = tree_wait(q_full, nq++ & 1, err, kTreeQFull);
       if (!ok) break;
       issued = true;
       if constexpr (TWO) {
@@ -420,22 +476,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         if (cnt == 1) mma_commit_warp(q_empty);
         for (int k = 0; k < cnt && ok; ++k) {
           const bool need_k = k + 1 < cnt;
-          ok = mbar_wait_warp(&v_full[nv % NV], (nv / NV) & 1, err, kTreeVFull);
-          if (ok && need_k) wait_K();
+          ok = tree_wait(&v_full[nv % NV], (nv / NV) & 1, err, kTreeVFull);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            ok = ok && mbar_wait_warp(&p_ready[t], np[t] & 1, err, kTreeP);
+            ok = ok && tree_wait(&p_ready[t], np >> t & 1u, err, kTreeP);
             if (!ok) break;
-            ++np[t];
+            np ^= 1u << t;
             tc_fence_after();
             issue_PV(t, nv % NV, k > 0);
-            if (!need_k) mma_commit_warp(&o_done[t]);
-            else issue_S(t, nk % NK);
+            if (!need_k) {
+              mma_commit_warp(&o_done[t]);
+            } else {
+              if (t == 0 && !wait_K()) break;
+              issue_S(t, nk % NK);
+            }
           }
           if (!ok) break;
           mma_commit_warp(&v_empty[nv++ % NV]);
           if (need_k) mma_commit_warp(&k_empty[nk++ % NK]);
-          if (k + 2 == cnt) mma_commit_warp(q_empty);  // every S of the segment is issued
+          if (k + 2 == cnt) mma_commit_warp(q_empty);  // every S of the part is issued
         }
       } else {
         for (int k = 0; k < min(cnt, 2); ++k) {
@@ -447,11 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         if (cnt <= 2) mma_commit_warp(q_empty);
         for (int k = 0; k < cnt; ++k) {
           const int t = k & 1;
-          ok = mbar_wait_warp(&v_full[nv % NV], (nv / NV) & 1, err, kTreeVFull);
-          ok = ok && mbar_wait_warp(&p_ready[t], (t ? np[1] : np[0]) & 1, err, kTreeP);
+          ok = tree_wait(&v_full[nv % NV], (nv / NV) & 1, err, kTreeVFull);
+          ok = ok && tree_wait(&p_ready[t], np >> t & 1u, err, kTreeP);
           if (!ok) break;
-          if (t) ++np[1];
-          else ++np[0];
+          np ^= 1u << t;
           tc_fence_after();
           issue_PV(t, nv % NV, k > 1);
           mma_commit_warp(&v_empty[nv++ % NV]);
@@ -469,66 +527,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
     // every MMA must be complete before TMEM is released
     if (issued) {
       mma_commit_warp(mma_done);
-      mbar_wait_warp(mma_done, 0, err, kTreeDrain);
+      tree_wait(mma_done, 0, err, kTreeDrain);
     }
-  } else if (warp >= 8 && warp < 16) {
+  } else if (warp >= kDecWarp && warp < kDecWarp + 4) {
     // ---------------------------------------------------------------- decoding warps
     regs_less<kRegsDec>();
-    const int tid = threadIdx.x - 256, P = p.c.page_size, block = kv4_block_bytes(P, D);
-    constexpr int KI = D / 64, VI = D / 64;  // 16-byte pieces of K, of V a thread takes of a unit
-    int k_code[KI], k_scale[KI], k_dst[KI], v_code[VI], v_scale[VI], v_dst[VI], v_tok[VI], v_flip[VI];
-    bool k_swap[KI];
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      // 32 dims q of a token.  Lanes of dims 64.. store their pieces two further on: the quarter warp's
-      // eight stores then fall on eight different banks groups
-      const int e = i * 256 + tid, tok = e / (D / 32), q = e % (D / 32), w = tok & (P - 1), base = tok / P * block;
-      k_code[i] = base + w * (D / 2) + q * 16;
-      k_scale[i] = base + kv4_off_sk(P, D) + w * (D / 16) + q * 2;
-      k_dst[i] = (q / 2) * C::BLK + tok * 128 + ((((q & 1) * 4) ^ (tok & 7)) << 4);
-      k_swap[i] = q >= 2;
-    }
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      // 16 dims (group g) of a pair of tokens
-      const int e = i * 256 + tid, u = e / (D / 16), s = e % (D / 16), w = 2 * u & (P - 1), base = 2 * u / P * block;
-      const int x = kv4_slot_xor(w / 2, D), g = D == 128 ? s ^ x : s ^ (x >> 1);
-      v_code[i] = base + kv4_off_v(P, D) + (w / 2) * D + s * 16;
-      v_scale[i] = base + kv4_off_sv(P, D) + (w / 2) * (D / 8) + 2 * g;
-      v_tok[i] = 2 * u;
-      v_dst[i] = g;
-      v_flip[i] = D == 128 ? g / 4 : u & 1;  // which of the two pieces is stored first: different banks again
-    }
-    int nq = 0, n = 0;
-    for (bool more = at.settle(p); more && ok; more = at.advance(p)) {
-      const int cnt = at.count(p);
+    const int tid = threadIdx.x % 128, P = p.c.page_size, block = kv4_block_bytes(P, D);
+    constexpr int N = D / 32, STEP = 128 / N, NG = D / 16;  // 16-byte pieces a thread takes of K, of V; tokens between them
+    auto page_at = [&](int tok) { return tok / P * block; };
+    // K: 32 dims (quarter q) of a token a piece.  Lanes of dims 64.. store their four chunks two further on:
+    // the eight lanes of a quarter warp then hit all banks.
+    const int tok_k = tid / N, q = tid % N, w_k = tok_k & (P - 1);
+    const int code_k = page_at(tok_k) + w_k * (D / 2) + q * 16;
+    const int scale_k = page_at(tok_k) + kv4_off_sk(P, D) + w_k * (D / 16) + q * 2;
+    const int dst_k = (q / 2) * C::BLK + tok_k * 128 + (((((q & 1) * 4) ^ (tok_k & 7)) << 4) ^ (q >= 2 ? 32 : 0));
+    const bool swap = q >= 2;
+    // V: 16 dims (group g) of a pair of tokens a piece; which of a token's two chunks is stored first differs
+    // between the lanes of a quarter warp that would meet in a bank.
+    const int u = tid / NG, w_v = 2 * u & (P - 1), x_v = kv4_slot_xor(w_v / 2, D);
+    const int g = D == 128 ? (tid % NG) ^ x_v : (tid % NG) ^ (x_v >> 1), flip = D == 128 ? g / 4 : u & 1;
+    const int code_v = page_at(2 * u) + kv4_off_v(P, D) + w_v / 2 * D + tid % NG * 16;
+    const int scale_v = page_at(2 * u) + kv4_off_sv(P, D) + w_v / 2 * (D / 8) + 2 * g;
+    const int dst_v = (g / 4) * C::BLK + 2 * u * 128 + (((2 * (g % 4) + flip) ^ (2 * u & 7)) << 4);
+    const int G = p.H_q / p.c.H_kv;
+    const float inv_G = 1.f / (float)G;
+    int n = 0, nq = 0;
+#pragma unroll 1
+    for (; next_part(); part_done()) {
+      const TreePart& part = parts[n_part % kParts];
+      const int cnt = part.cnt;
       if (cnt == 0) continue;
-      // ---- Q: loaded while the segment before is still computed, stored when its last scores are done
+      // ---- Q: loaded early, stored when the last scores of the part before are done
       {
-        constexpr int QI = C::ROWS * (D / 8) / 256, QB = QI < 8 ? QI : 8;
-        const int R = (int)min((long long)at.s.n * G - (long long)at.rb() * C::ROWS, (long long)C::ROWS);
-        const long long r0 = (long long)at.rb() * C::ROWS;
-        const int hk = at.hk();
+        constexpr int QI = C::ROWS * (D / 8) / 128, QB = 8;
+        const int R = part.R, rem0 = part.rem0;
+        const __nv_bfloat16* q0 = p.q + ((size_t)(part.row0 + part.node0) * p.H_q + part.hk * G) * D;
 #pragma unroll 1
         for (int i0 = 0; i0 < QI; i0 += QB) {
           uint4 w[QB];
 #pragma unroll
           for (int i = 0; i < QB; ++i) {
-            const int e = (i0 + i) * 256 + tid, r = e / (D / 8), c = e % (D / 8);
+            const int e = (i0 + i) * 128 + tid, r = e / (D / 8), c = e % (D / 8);
             w[i] = make_uint4(0u, 0u, 0u, 0u);
             if (r < R) {
-              const long long rr = r0 + r, node = rr / G;
-              w[i] = __ldg(reinterpret_cast<const uint4*>(
-                  p.q + ((size_t)(at.s.row0 + node) * p.H_q + (size_t)hk * G + (rr - node * G)) * D + c * 8));
+              const int node = small_div(rem0 + r, inv_G);
+              w[i] = __ldg(reinterpret_cast<const uint4*>(q0 + ((size_t)node * p.H_q + (rem0 + r - node * G)) * D + c * 8));
             }
           }
           if (i0 == 0 && nq > 0) {
-            ok = mbar_wait_warp(q_empty, (nq - 1) & 1, err, kTreeQEmpty);
+            ok = tree_wait(q_empty, (nq - 1) & 1, err, kTreeQEmpty);
             if (!ok) break;
           }
 #pragma unroll
           for (int i = 0; i < QB; ++i) {
-            const int e = (i0 + i) * 256 + tid, r = e / (D / 8), c = e % (D / 8), rt = r % 128;
+            const int e = (i0 + i) * 128 + tid, r = e / (D / 8), c = e % (D / 8), rt = r % 128;
             uint8_t* dst = smem + C::OFF_Q + (r / 128) * C::TILE + (c / 8) * C::BLK + rt * 128 + (((c % 8) ^ (rt & 7)) << 4);
             *reinterpret_cast<uint4*>(dst) =
                 make_uint4(__byte_perm(w[i].x, w[i].z, 0x5410), __byte_perm(w[i].x, w[i].z, 0x7632),
@@ -541,63 +593,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         if (lane == 0) mbar_arrive(q_full);
         ++nq;
       }
-      // units whose tokens are not all seen by all rows, as the softmax warps decide it
-      long long k0 = (long long)(at.s.first + at.from) * kUnit;
-      for (int k = 0; k < cnt; ++k, ++n, k0 += kUnit) {
+      int unit = part.unit0;
+      const int u_win = part.u_win, u_tree = part.u_tree;
+#pragma unroll 1
+      for (int k = 0; k < cnt; ++k, ++n, ++unit) {
         const int stage = n % NST, sk = n % NK, sv = n % NV;
         const uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
-        ok = mbar_wait_warp(&raw_full[stage], (n / NST) & 1, err, kTreeRawFull);
-        if (ok && n >= NK) ok = mbar_wait_warp(&k_empty[sk], (n / NK - 1) & 1, err, kTreeKEmpty);
+        ok = tree_wait(&raw_full[stage], (n / NST) & 1, err, kTreeRawFull);
         if (!ok) break;
-        uint8_t* kd = smem + C::OFF_K + sk * C::TILE;
+        // both operands' bytes are read at once, so that the stage is free early
+        uint4 wk[N], wv[N];
+        uint32_t sc[N], two[N];
 #pragma unroll
-        for (int i = 0; i < KI; ++i) {
-          uint4 w = *reinterpret_cast<const uint4*>(st + k_code[i]);
-          const uint32_t sp = scale_pair(*reinterpret_cast<const unsigned short*>(st + k_scale[i]));
-          Kv4Small a = scales_low(sp), b = scales_high(sp);
-          // words 0, 1 share the first scale, 2, 3 the second; word c goes to piece c
-          if (k_swap[i]) {
-            w = make_uint4(w.z, w.w, w.x, w.y);
-            const Kv4Small t = a;
-            a = b;
-            b = t;
+        for (int i = 0; i < N; ++i) {
+          const int off = page_at(STEP * i), in = STEP * i & (P - 1);
+          wk[i] = *reinterpret_cast<const uint4*>(st + code_k + off + in * (D / 2));
+          sc[i] = *reinterpret_cast<const unsigned short*>(st + scale_k + off + in * (D / 16));
+          wv[i] = *reinterpret_cast<const uint4*>(st + code_v + off + in / 2 * D);
+          two[i] = *reinterpret_cast<const unsigned short*>(st + scale_v + off + in / 2 * (D / 8));
+        }
+        if (n >= NK) ok = tree_wait(&k_empty[sk], (n / NK - 1) & 1, err, kTreeKEmpty);
+        if (!ok) break;
+        __syncwarp();  // every lane has read its pieces
+        if (lane == 0) mbar_arrive(&raw_empty[stage]);
+        {
+          uint8_t* d = smem + C::OFF_K + sk * C::TILE;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const uint32_t sp = scale_pair(swap ? __byte_perm(sc[i], 0u, 0x4401) : sc[i]);
+            const Kv4Small a = scales_low(sp), b2 = scales_high(sp);
+            const uint4 x = swap ? make_uint4(wk[i].z, wk[i].w, wk[i].x, wk[i].y) : wk[i];
+            *reinterpret_cast<uint4*>(d + i * STEP * 128 + dst_k) = decode8(x.x, a);
+            *reinterpret_cast<uint4*>(d + i * STEP * 128 + (dst_k ^ 16)) = decode8(x.y, a);
+            *reinterpret_cast<uint4*>(d + i * STEP * 128 + (dst_k ^ 32)) = decode8(x.z, b2);
+            *reinterpret_cast<uint4*>(d + i * STEP * 128 + (dst_k ^ 48)) = decode8(x.w, b2);
           }
-          uint8_t* d = kd + k_dst[i];
-          const int x = k_swap[i] ? 32 : 0;  // piece c ^ 2 first
-          // (the destination's piece number is k_dst's exclusive-or c: c lies in its low two bits)
-          uint8_t* base = reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(d) & ~(uintptr_t)127);
-          const int at16 = (int)(reinterpret_cast<uintptr_t>(d) & 127);
-          *reinterpret_cast<uint4*>(base + (at16 ^ x)) = decode8(w.x, a);
-          *reinterpret_cast<uint4*>(base + (at16 ^ x ^ 16)) = decode8(w.y, a);
-          *reinterpret_cast<uint4*>(base + (at16 ^ x ^ 32)) = decode8(w.z, b);
-          *reinterpret_cast<uint4*>(base + (at16 ^ x ^ 48)) = decode8(w.w, b);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[sk]);
-        if (n >= NV) ok = mbar_wait_warp(&v_empty[sv], (n / NV - 1) & 1, err, kTreeVEmpty);
+        if (n >= NV) ok = tree_wait(&v_empty[sv], (n / NV - 1) & 1, err, kTreeVEmpty);
         if (!ok) break;
-        const bool edge = k0 + kUnit > at.s.L || (p.window >= 0 && k0 < (long long)at.s.L + at.s.n - 1 - p.window);
-        uint8_t* vd = smem + C::OFF_V + sv * C::TILE;
-        uint4 w[VI];
-        uint32_t two[VI];
+        // units whose tokens are not all seen by all rows, as the softmax warps decide it
+        if (unit < u_win || unit >= u_tree) {
+          const int len = part.len - unit * kUnit, lo = part.lo - unit * kUnit;  // (a token's number is below 2^31)
+          // A token that no row sees adds nothing, whatever its bytes are.  One held as NaN adds nothing
+          // either: rows that do not see it have P = 0, but 0 times NaN is NaN.  The rows that see it
+          // learn of it from these bits.
 #pragma unroll
-        for (int i = 0; i < VI; ++i) {
-          w[i] = *reinterpret_cast<const uint4*>(st + v_code[i]);
-          two[i] = *reinterpret_cast<const unsigned short*>(st + v_scale[i]);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[stage]);  // the stage is read
-#pragma unroll
-        for (int i = 0; i < VI; ++i) {
-          const int g = v_dst[i], tok = v_tok[i];
-          if (edge) {
-            // A token that no row sees adds nothing, whatever its bytes are.  One held as NaN adds nothing
-            // either: rows that do not see it have P = 0, but 0 times NaN is NaN.  The rows that see it
-            // learn of it from these bits.
+          for (int i = 0; i < N; ++i) {
+            const int tok = 2 * u + STEP * i;
             uint32_t bits = 0u;
-            if (k0 + tok >= at.s.len || k0 + tok < at.s.lo) two[i] &= 0xFF00u;
-            if (k0 + tok + 1 >= at.s.len || k0 + tok + 1 < at.s.lo) two[i] &= 0x00FFu;
+            if (tok >= len || tok < lo) two[i] &= 0xFF00u;
+            if (tok + 1 >= len || tok + 1 < lo) two[i] &= 0x00FFu;
             if ((two[i] & 0x00F8u) == 0x00F8u) {
               bits |= 1u;
               two[i] &= 0xFF00u;
@@ -606,105 +654,124 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
               bits |= 2u;
               two[i] &= 0x00FFu;
             }
-            smem[C::OFF_NAN + (sv * (D / 16) + g) * 64 + tok / 2] = (uint8_t)bits;
+            smem[C::OFF_NAN + (sv * NG + g) * 64 + tok / 2] = (uint8_t)bits;
           }
-          const uint32_t sp = scale_pair(two[i]);
-          const Kv4Small a = scales_low(sp), b = scales_high(sp);
-          uint8_t* d = vd + (g / 4) * C::BLK + tok * 128;
-          const int c0 = 2 * (g % 4), fl = v_flip[i];
-          // (D = 128: 8 bytes a token; D = 64: the two eighths' 4 bytes a token)
-          const uint32_t t0w0 = w[i].x, t0w1 = D == 128 ? w[i].y : w[i].z, t1w0 = D == 128 ? w[i].z : w[i].y, t1w1 = w[i].w;
-          const int r0 = tok & 7, r1 = (tok + 1) & 7;
-          *reinterpret_cast<uint4*>(d + (((c0 + fl) ^ r0) << 4)) = decode8(fl ? t0w1 : t0w0, a);
-          *reinterpret_cast<uint4*>(d + (((c0 + 1 - fl) ^ r0) << 4)) = decode8(fl ? t0w0 : t0w1, a);
-          *reinterpret_cast<uint4*>(d + 128 + (((c0 + fl) ^ r1) << 4)) = decode8(fl ? t1w1 : t1w0, b);
-          *reinterpret_cast<uint4*>(d + 128 + (((c0 + 1 - fl) ^ r1) << 4)) = decode8(fl ? t1w0 : t1w1, b);
+        }
+        {
+          uint8_t* d = smem + C::OFF_V + sv * C::TILE;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const uint32_t sp = scale_pair(two[i]);
+            const Kv4Small a = scales_low(sp), b2 = scales_high(sp);
+            // (D = 128: 8 bytes a token; D = 64: the two eighths' 4 bytes a token)
+            const uint32_t t0w0 = wv[i].x, t0w1 = D == 128 ? wv[i].y : wv[i].z, t1w0 = D == 128 ? wv[i].z : wv[i].y,
+                           t1w1 = wv[i].w;
+            uint8_t* di = d + i * STEP * 128;  // (the chunk's exclusive-or with 1: the row's next token)
+            *reinterpret_cast<uint4*>(di + dst_v) = decode8(flip ? t0w1 : t0w0, a);
+            *reinterpret_cast<uint4*>(di + (dst_v ^ 16)) = decode8(flip ? t0w0 : t0w1, a);
+            *reinterpret_cast<uint4*>(di + 128 + (dst_v ^ 16)) = decode8(flip ? t1w1 : t1w0, b2);
+            *reinterpret_cast<uint4*>(di + 128 + dst_v) = decode8(flip ? t1w0 : t1w1, b2);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[sv]);
       }
+      if (!ok) break;
     }
   } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax and output
     regs_more<kRegsSoft>();
     const int t = warp / 4, r = (warp % 4) * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
-    const uint32_t colS = t * 256, colO = t * 256 + 128;
+    const uint32_t aS = lane_addr + t * 256, aO = aS + 128;
     const float sl2 = p.scale_log2 * kKv4SmallUndo;
+    const int G = p.H_q / p.c.H_kv;
+    const float inv_G = 1.f / (float)G;
     float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);  // [2][128] maxima, sums, NaN groups of the two halves
     float* xl = xm + 256;
     uint32_t* xn = reinterpret_cast<uint32_t*>(xl + 256);
-    int ns = 0, no[2] = {0, 0}, n_seg0 = 0;  // s_ready and o_done phases consumed; units of the segments before
-    bool at_begin = true;
-    for (bool more = at.settle(p); more && ok; more = at.advance(p), at_begin = false) {
-      const int cnt = at.count(p);
-      const bool whole = at.from == 0 && at.to == at.s.units;
-      const int hk = at.hk();
-      const long long r_all = (long long)at.rb() * C::ROWS + (TWO ? t * 128 : 0) + r;  // this thread's row of the kv head
-      const bool row_ok = r_all < (long long)at.s.n * G;
-      const bool warp_ok = r_all - lane < (long long)at.s.n * G;
-      const int node = row_ok ? (int)(r_all / G) : at.s.n - 1, h = hk * G + (row_ok ? (int)(r_all % G) : 0);
-      const int L = at.s.L;
-      int lo_row = 0;  // first token before the tree that this row sees
-      if (p.window >= 0) {
-        int depth = 0;
-        if (p.parents) {
-          for (int a = tree_parent(p, at.s, node); a >= 0; a = tree_parent(p, at.s, a)) ++depth;
-        } else {
-          depth = node;
-        }
-        lo_row = (int)min(max((long long)L + depth - p.window, 0LL), 0x7fffffffLL);
-      }
+    int ns = 0, n_before = 0;  // s_ready phases consumed; units of the parts before
+    uint32_t no = 0u;          // parities of o_done
+#pragma unroll 1
+    for (; next_part(); part_done()) {
+      const TreePart& part = parts[n_part % kParts];
+      const int cnt = part.cnt, rr = (TWO ? t * 128 : 0) + r;
+      const bool row_ok = rr < part.R, warp_ok = rr - lane < part.R;
+      // this row's node, and its head
+      int node = small_div(part.rem0 + (row_ok ? rr : 0), inv_G);
+      const int h = part.hk * G + part.rem0 + (row_ok ? rr : 0) - node * G;
+      node += part.node0;
       float m_run = -INFINITY, l = 0.f;
       uint32_t nans = 0u;  // groups of 16 dims in which this row sees a NaN
-      long long k0 = (long long)(at.s.first + at.from + (TWO ? 0 : t)) * kUnit;
       bool first = true;
-      for (int k = TWO ? 0 : t; k < cnt; k += TWO ? 1 : 2, k0 += TWO ? kUnit : 2 * kUnit) {
-        const bool edge = k0 + kUnit > L || (p.window >= 0 && k0 < (long long)L + at.s.n - 1 - p.window);
-        uint32_t vis[4] = {0u, 0u, 0u, 0u};
+      int unit = part.unit0 + (TWO ? 0 : t);
+      const int u_win = part.u_win, u_tree = part.u_tree;
+#pragma unroll 1
+      for (int k = TWO ? 0 : t; k < cnt; k += TWO ? 1 : 2, unit += TWO ? 1 : 2) {
+        const bool edge = unit < u_win || unit >= u_tree;
+        uint32_t vis[4] = {0u, 0u, 0u, 0u};  // the unit's tokens that this row sees
         if (edge && warp_ok) {
-          set_range(vis, (int)max((long long)lo_row - k0, 0LL), (int)min((long long)L - k0, (long long)kUnit));
-          const long long a0 = k0 - L;  // the node at the unit's first token
+          const int L = part.L, row0 = part.row0;
+          const long long k0 = (long long)unit * kUnit, a0 = k0 - L;  // the unit's first token; the node there
+          long long lo = 0;  // first token before the tree that this row sees
+          if (p.window >= 0) {
+            int depth = node;
+            if (p.parents) {
+              depth = 0;
+              for (int a = tree_parent(p, row0, node); a >= 0; a = tree_parent(p, row0, a)) ++depth;
+            }
+            lo = (long long)L + depth - p.window;
+          }
+          set_range(vis, (int)min(max(lo - k0, 0LL), (long long)kUnit), (int)max(min(L - k0, (long long)kUnit), 0LL));
           if (!p.parents) {
             const long long from = p.window >= 0 ? max((long long)node - p.window, 0LL) : 0;
-            set_range(vis, (int)min(max(max(from, 0LL) - a0, 0LL), (long long)kUnit),
-                      (int)min(min((long long)node + 1, (long long)at.s.len - L) - a0, (long long)kUnit));
+            set_range(vis, (int)min(max(from - a0, 0LL), (long long)kUnit),
+                      (int)max(min(min((long long)node + 1, (long long)part.len - L) - a0, (long long)kUnit), 0LL));
           } else {
             int step = 0;
-            for (int a = node; a >= 0 && a >= a0 && (p.window < 0 || step <= p.window); a = tree_parent(p, at.s, a), ++step) {
+            for (int a = node; a >= 0 && a >= a0 && (p.window < 0 || step <= p.window); a = tree_parent(p, row0, a), ++step) {
               const long long j = a - a0;
-              if (j < kUnit && L + a < at.s.len) {
+              if (j < kUnit && a < part.len - L) {
+                const uint32_t bit = 1u << ((int)j & 31);
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                  if ((int)j / 32 == w) vis[w] |= 1u << ((int)j & 31);
+                  if ((int)j / 32 == w) vis[w] |= bit;
               }
             }
           }
         }
-        ok = mbar_wait_warp(&s_ready[t], ns & 1, err, kTreeS);
+        ok = tree_wait(&s_ready[t], ns & 1, err, kTreeS);
         ++ns;
         if (!ok) break;
         if (!warp_ok) {  // no row of this warp exists: its P may be anything
-          mbar_arrive(&p_ready[t]);
-          first = false;
+          if (lane == 0) mbar_arrive(&p_ready[t]);
           continue;
         }
         tc_fence_after();
-        float mx = -INFINITY;
+        if (edge) {  // hidden tokens' scores become -inf where they are
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t s[16];
+            tmem_ld16(aS + 16 * c, s);
+            const uint32_t word = (c & 4 ? (c & 2 ? vis[3] : vis[2]) : (c & 2 ? vis[1] : vis[0])) >> ((c & 1) * 16);
+            tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          float cm;
-          tmem_ld32_max(lane_addr + colS + 32 * c, s, cm);
-          tmem_ld_wait();
-          if (edge) {
-            cm = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) cm = fmaxf(cm, vis[c] >> e & 1u ? __uint_as_float(s[e]) : -INFINITY);
+            for (int e = 0; e < 16; ++e)
+              if (!(word >> e & 1u)) s[e] = 0xff800000u;
+            tmem_st16(aS + 16 * c, s);
           }
-          mx = fmaxf(mx, cm);
+          tmem_st_wait();
         }
+        // the row's 128 scores in one batch of loads, each with the maximum of its 32
+        uint32_t s[4][32];
+        float c0, c1, c2, c3;
+        tmem_ld32_max(aS, s[0], c0);
+        tmem_ld32_max(aS + 32, s[1], c1);
+        tmem_ld32_max(aS + 64, s[2], c2);
+        tmem_ld32_max(aS + 96, s[3], c3);
+        tmem_ld_wait();
+        const float mx = fmax3(c0, c1, fmaxf(c2, c3));
         const float m_tile = mx * sl2;
         // The running maximum (log2 units) moves only when some row of the warp passes it by 2^8; the
         // sums stay exact, they are relative to the maximum that was used.
@@ -716,61 +783,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 16) {
               uint32_t o[16];
-              tmem_ld16(lane_addr + colO + c0, o);
+              tmem_ld16(aO + c0, o);
               tmem_ld_wait();
 #pragma unroll
               for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              tmem_st16(lane_addr + colO + c0, o);
+              tmem_st16(aO + c0, o);
             }
           }
           m_run = m_new;
+          // (read anew, so that this rare path does not need the registers of 128 scores beside its own)
+          tmem_ld32(aS, s[0]);
+          tmem_ld32(aS + 32, s[1]);
+          tmem_ld32(aS + 64, s[2]);
+          tmem_ld32(aS + 96, s[3]);
+          tmem_ld_wait();
         }
         first = false;
         const float neg = m_run == -INFINITY ? 0.f : -m_run;
         const uint64_t sl2x2 = f2_pack(sl2, sl2), neg2 = f2_pack(neg, neg);
-        uint64_t ls[2] = {0ull, 0ull};
+        uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t s[32], pk[16];
-          tmem_ld32(lane_addr + colS + 32 * c, s);
-          tmem_ld_wait();
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(vis[c] >> e & 1u)) s[e] = 0xff800000u;
-          }
+          uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float xa, xb;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sl2x2, neg2), xa, xb);
-            const float a = ex2(xa), b = ex2(xb);
-            ls[e % 2] = f2_add(ls[e % 2], f2_pack(a, b));
-            pk[e] = pack_bf16x2(a, b);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sl2x2, neg2), xa, xb);
+            const float a = ex2(xa), b2 = ex2(xb);
+            ls[e % 4] = f2_add(ls[e % 4], f2_pack(a, b2));
+            pk[e] = pack_bf16x2(a, b2);
           }
-          tmem_st16(lane_addr + colS + 16 * c, pk);
+          tmem_st16(aS + 16 * c, pk);
         }
         {
-          float a, b, c, d;
-          f2_unpack(ls[0], a, b);
-          f2_unpack(ls[1], c, d);
-          l += (a + b) + (c + d);
+          float a, b2;
+          f2_unpack(f2_add(f2_add(ls[0], ls[1]), f2_add(ls[2], ls[3])), a, b2);
+          l += a + b2;
         }
         if (edge) {  // NaN values that this row sees
-          const int nu = n_seg0 + k;  // the CTA's unit
-          ok = mbar_wait_warp(&v_full[nu % NV], (nu / NV) & 1, err, kTreeVFull);
+          const int nu = n_before + k;  // the CTA's unit
+          ok = tree_wait(&v_full[nu % NV], (nu / NV) & 1, err, kTreeVFull);
           if (!ok) break;
-          const uint4* bits = reinterpret_cast<const uint4*>(smem + C::OFF_NAN + (nu % NV) * (D / 16) * 64);
+          const uint8_t* by = smem + C::OFF_NAN + (nu % NV) * (D / 16) * 64;
           uint32_t any = 0u;
-#pragma unroll 4
-          for (int i = 0; i < D / 16 * 4; ++i) any |= bits[i].x | bits[i].y | bits[i].z | bits[i].w;
-          if (any) {
-            const uint8_t* by = reinterpret_cast<const uint8_t*>(bits);
+          for (int i = lane; i < D / 16 * 16; i += 32) any |= reinterpret_cast<const uint32_t*>(by)[i];
+          if (__any_sync(0xffffffffu, any != 0u)) {
+#pragma unroll 1
             for (int u = 0; u < 64; ++u) {
-              uint32_t word = 0u;
-#pragma unroll
-              for (int w = 0; w < 4; ++w)
-                if (u / 16 == w) word = vis[w];
+              const uint32_t word = u & 32 ? (u & 16 ? vis[3] : vis[2]) : (u & 16 ? vis[1] : vis[0]);
               const uint32_t seen = word >> (2 * u & 31) & 3u;
+#pragma unroll 1
               for (int g = 0; g < D / 16; ++g)
                 if (by[g * 64 + u] & seen) nans |= 1u << g;
             }
@@ -778,27 +840,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_ready[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[t]);
       }
-      n_seg0 += cnt;
-      // ---- the segment's end: whole, its outputs; a piece of it, its sums
+      n_before += cnt;
+      // ---- the part's end: of a whole segment the outputs, of a piece its sums
       const bool have0 = TWO ? (t == 0 && cnt > 0) : cnt > 0, have1 = TWO ? (t == 1 && cnt > 0) : cnt > 1;
       if (ok && have0) {
-        ok = mbar_wait_warp(&o_done[0], no[0] & 1, err, kTreeO);
-        ++no[0];
+        ok = tree_wait(&o_done[0], no & 1u, err, kTreeO);
+        no ^= 1u;
       }
       if (ok && have1) {
-        ok = mbar_wait_warp(&o_done[1], no[1] & 1, err, kTreeO);
-        ++no[1];
+        ok = tree_wait(&o_done[1], no >> 1 & 1u, err, kTreeO);
+        no ^= 2u;
       }
       float m = m_run, f0 = 1.f, f1 = 1.f;
       if constexpr (!TWO) {
+        // (a warp whose wait gave up comes here too, so that nobody waits for it, and all stop)
         xm[t * 128 + r] = m_run;
         xl[t * 128 + r] = l;
         xn[t * 128 + r] = nans;
-      }
-      if constexpr (!TWO) {
-        // (a warp whose wait gave up comes here too, so that nobody waits for it, and all stop)
         ok = bar_red_and(1, 256, ok);
         const float m0 = xm[r], m1 = xm[128 + r], l0 = xl[r], l1 = xl[128 + r];
         nans = xn[r] | xn[128 + r];
@@ -811,25 +872,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
       if (!ok) break;
       tc_fence_after();
       if (warp_ok) {
+        const bool whole = part.slot < 0;
         TreeSums z{0.f, 0.f};
         if (whole && row_ok) z = tree_finish(p, h, m, l);
-        float* slot = partial + ((size_t)2 * blockIdx.x + (at_begin ? 0 : 1)) * C::PART;
-        const int rr = (TWO ? t * 128 : 0) + r;
-        __nv_bfloat16* o = p.o + ((size_t)(at.s.row0 + node) * p.H_q + h) * D;
+        float* slot = partial + ((size_t)2 * blockIdx.x + max(part.slot, 0)) * C::PART;
+        __nv_bfloat16* o = p.o + ((size_t)(part.row0 + node) * p.H_q + h) * D;
         constexpr int COLS = TWO ? D : D / 2;  // one tile: each half of the warps stores half of the dims
         const int c_first = TWO ? 0 : t * COLS;
 #pragma unroll 1
         for (int c0 = c_first; c0 < c_first + COLS; c0 += 16) {
-          uint32_t a[16], b[16];
+          uint32_t a[16], b2[16];
           float v[16];
           if (have0) tmem_ld16(lane_addr + 128 + c0, a);
-          if (have1) tmem_ld16(lane_addr + 256 + 128 + c0, b);
+          if (have1) tmem_ld16(lane_addr + 256 + 128 + c0, b2);
           tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             v[c] = 0.f;
             if (have0) v[c] = __uint_as_float(a[c]) * f0;
-            if (have1) v[c] = fmaf(__uint_as_float(b[c]), f1, v[c]);
+            if (have1) v[c] = fmaf(__uint_as_float(b2[c]), f1, v[c]);
           }
           if (nans >> (c0 / 16) & 1u) {
 #pragma unroll
@@ -848,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         }
         if (row_ok && (TWO || t == 0)) {
           if (whole) {
-            if (p.lse) p.lse[(size_t)h * p.T + at.s.row0 + node] = z.lse;
+            if (p.lse) p.lse[(size_t)h * p.T + part.row0 + node] = z.lse;
           } else {
             slot[C::ROWS * D + rr] = m;
             slot[C::ROWS * D + C::ROWS + rr] = l;
@@ -862,112 +923,94 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
 }
 
-// Joins the pieces of every segment that spans several CTAs, in CTA order, and writes the rows without a
-// token and, on request, those of no sequence.  WPR warps a row: warp w takes pieces w, w + WPR, ...,
-// then their sums are added in order.
+// Joins the pieces of every segment that spans several CTAs, in CTA order: block (c, y) the segment whose
+// first piece is CTA c's, if there is one, a warp a row.  Then the rows without a token, and on request
+// those of no sequence.
 // Launched while the kernel before it runs: it waits for that kernel's end before it reads a piece.
-// Every block waits, also one with nothing to do: this grid must not end before that kernel, or what
-// follows on the stream could start beside it.
-template <int D, int ROWS, int WPR>
-__global__ void __launch_bounds__(256) kv4_tree_join_kernel(const Kv4TreeParams p, int grid, const float* partial) {
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) kv4_tree_join_kernel(const Kv4TreeParams p, const TreePiece* pieces, const float* partial) {
   constexpr int PART = ROWS * (D + 2), E = D / 32;
-  __shared__ float red[2][8], sums[8][D];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, wr = warp % WPR;
-  const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
-  const int G = p.H_q / p.c.H_kv;
-  const bool have = row < (long long)p.T * p.H_q;
-  const int t = have ? (int)(row / p.H_q) : 0, h = have ? (int)(row % p.H_q) : 0, hk = h / G;
-  int b = -1;  // the row's sequence
-  for (int base = 0; base < p.B && b < 0; base += 32) {
-    const int i = base + lane;
-    const unsigned in = __ballot_sync(0xffffffffu, i < p.B && __ldg(p.cu + i) <= t && t < __ldg(p.cu + min(i, p.B - 1) + 1));
-    if (in) b = base + __ffs(in) - 1;
-  }
-  TreeSeq s{};
-  long long total = 0, u0 = 0;
-  int n_cta = 1, c0 = 0, c1 = 0, r = 0;
-  if (b >= 0) {
-    s = tree_seq<ROWS>(p, b);
-    total = TreeScan<ROWS>::sum(p, p.B);
-    if (s.units > 0) {
-      const long long r_all = (long long)(t - s.row0) * G + h % G;
-      r = (int)(r_all % ROWS);
-      u0 = TreeScan<ROWS>::sum(p, b) + ((long long)hk * s.blocks + r_all / ROWS) * s.seg();
-      n_cta = tree_ctas(total, grid);
-      c0 = tree_cta_of(total, n_cta, u0 + kSegCost);
-      c1 = tree_cta_of(total, n_cta, u0 + kSegCost + s.units - 1);
-    }
-  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = p.H_q / p.c.H_kv;
   grid_wait();
-  if (!have || (b < 0 && !p.zero_rest) || (s.units > 0 && c0 == c1)) return;  // one CTA had all of it
-  float a[E], m = -INFINITY, l = 0.f;
+  // (ordinary loads: the pieces were written while this kernel was already set up)
+  auto piece = [&](int i) {
+    const int4* w = reinterpret_cast<const int4*>(pieces + i);
+    const int4 a = w[0], b = w[1];
+    return TreePiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  };
+  auto store = [&](int t, int h, const float (&a)[E], const TreeSums& z) {
+    // lane's columns back to their dims: of 8 columns 0 .. 7 the dims 0 4 1 5 2 6 3 7
+    __nv_bfloat16* o = p.o + ((size_t)t * p.H_q + h) * D;
 #pragma unroll
-  for (int e = 0; e < E; ++e) a[e] = 0.f;
-  if (s.units > 0) {
+    for (int e = 0; e < E; ++e) {
+      const int col = lane * E + e, c = col & 7;
+      o[(col & ~7) + (c >> 1) + (c & 1) * 4] = __float2bfloat16(a[e] * z.mul);
+    }
+    if (lane == 0 && p.lse) p.lse[(size_t)h * p.T + t] = z.lse;
+  };
+  const int c = blockIdx.x;
+  const TreePiece p0 = piece(2 * c), p1 = piece(2 * c + 1);
+  const bool second = p1.valid != 0;
+  const TreePiece f = second ? p1 : p0;
+  if (f.valid && f.starts) {
+    int last = c;  // the CTA of the last piece
+    for (bool end = f.ends; !end && last + 1 < (int)gridDim.x;) end = piece(2 * ++last).ends;
+    for (int r = blockIdx.y * 8 + warp; r < f.R; r += gridDim.y * 8) {
+      float a[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] = 0.f;
 #pragma unroll 4
-    for (int c = c0 + wr; c <= c1; c += WPR) {
-      // the piece is the CTA's first where the CTA starts inside the segment
-      const float* sl = partial + ((size_t)2 * c + (tree_cut(total, n_cta, c) >= u0 ? 0 : 1)) * PART;
-      const float mi = sl[ROWS * D + r], li = sl[ROWS * D + ROWS + r];
-      float v[E];
+      for (int i = c; i <= last; ++i) {
+        const float* sl = partial + ((size_t)2 * i + (i == c && second ? 1 : 0)) * PART;
+        const float mi = sl[ROWS * D + r], li = sl[ROWS * D + ROWS + r];
+        float v[E];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(sl + r * D + lane * E + e);
-        v[e] = x.x;
-        v[e + 1] = x.y;
+        for (int e = 0; e < E; e += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(sl + r * D + lane * E + e);
+          v[e] = x.x;
+          v[e + 1] = x.y;
+        }
+        const float mn = fmaxf(m, mi);
+        const float fo = m == -INFINITY ? 0.f : ex2(m - mn), w = mi == -INFINITY ? 0.f : ex2(mi - mn);
+        l = (m == -INFINITY ? l : l * fo) + (mi == -INFINITY ? li : li * w);  // (no key: 0, or a NaN that has to stay)
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = a[e] * fo + v[e] * w;  // (a NaN stays, also of a piece without weight)
+        m = mn;
       }
-      const float mn = fmaxf(m, mi);
-      const float f = m == -INFINITY ? 0.f : ex2(m - mn), w = mi == -INFINITY ? 0.f : ex2(mi - mn);
-      l = (m == -INFINITY ? l : l * f) + (mi == -INFINITY ? li : li * w);  // (no key: 0, or a NaN that has to stay)
-#pragma unroll
-      for (int e = 0; e < E; ++e) a[e] = a[e] * f + v[e] * w;  // (a NaN stays, also of a piece without weight)
-      m = mn;
+      const int node = (f.rem0 + r) / G, h = f.hk * G + f.rem0 + r - node * G;
+      store(f.row0 + f.node0 + node, h, a, tree_finish(p, h, m, l));
     }
   }
-  if constexpr (WPR > 1) {
-    if (lane == 0) {
-      red[0][warp] = m;
-      red[1][warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = a[e];
-    __syncthreads();
-    if (warp > 0) return;
-    m = red[0][0];
-    for (int w = 1; w < WPR; ++w) m = fmaxf(m, red[0][w]);
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) a[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) {
-      const float f = red[0][w] == -INFINITY ? 0.f : ex2(red[0][w] - m);
-      l += red[0][w] == -INFINITY ? red[1][w] : red[1][w] * f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) a[e] = fmaf(sums[w][lane * E + e], f, a[e]);
+  const float none[E] = {};
+  const int w_all = ((int)blockIdx.x * gridDim.y + blockIdx.y) * 8 + warp, n_all = gridDim.x * gridDim.y * 8;
+  for (int b = w_all; b < p.B; b += n_all) {
+    const TreeSeq s = tree_seq<ROWS>(p, b);
+    if (s.units > 0) continue;
+    for (int t = s.row0; t < s.row0 + s.n; ++t)
+      for (int h = 0; h < p.H_q; ++h) store(t, h, none, tree_finish(p, h, -INFINITY, 0.f));
+  }
+  if (p.zero_rest) {
+    const int first = max(p.cu[0], 0), end = max(min(p.cu[p.B], p.T), 0);
+    for (int t = w_all; t < p.T; t += n_all) {
+      if (t >= first && t < end) continue;
+      for (int h = 0; h < p.H_q; ++h) store(t, h, none, TreeSums{0.f, -INFINITY});
     }
   }
-  const TreeSums z = b < 0 ? TreeSums{0.f, -INFINITY} : tree_finish(p, h, m, l);
-  // lane's columns back to their dims: of 8 columns 0 .. 7 the dims 0 4 1 5 2 6 3 7
-  __nv_bfloat16* o = p.o + ((size_t)t * p.H_q + h) * D;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int col = lane * E + e, c = col & 7;
-    o[(col & ~7) + (c >> 1) + (c & 1) * 4] = __float2bfloat16(a[e] * z.mul);
-  }
-  if (lane == 0 && p.lse) p.lse[(size_t)h * p.T + t] = z.lse;
 }
 
 namespace {
 
+constexpr size_t kPieceBytes = (kMaxGrid * 2 * sizeof(TreePiece) + 255) / 256 * 256;
+
 template <int D, bool TWO>
-int launch_t(const Kv4TreeParams& p, float* partial, cudaStream_t stream) {
+int launch_t(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
   using C = TreeCfg<D, TWO>;
   if (!allow_smem<kv4_tree_kernel<D, TWO>>(C::SMEM)) return -1;
   static std::atomic<int> sms[64];  // SMs of each device
@@ -979,13 +1022,12 @@ int launch_t(const Kv4TreeParams& p, float* partial, cudaStream_t stream) {
     sms[dev].store(n, std::memory_order_release);
   }
   const int grid = std::min(n, kMaxGrid);
-  if (launch_kernel(kv4_tree_kernel<D, TWO>, dim3((unsigned)grid), kThreads, C::SMEM, stream, false, p, partial) != 0) return -1;
-  const long long rows = (long long)p.T * p.H_q;
-  if (rows <= 1216)  // few rows: eight warps take a row's pieces
-    return launch_kernel(kv4_tree_join_kernel<D, C::ROWS, 8>, dim3((unsigned)rows), 256, 0, stream, true, p, grid,
-                         (const float*)partial);
-  return launch_kernel(kv4_tree_join_kernel<D, C::ROWS, 1>, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, true, p, grid,
-                       (const float*)partial);
+  TreePiece* pieces = static_cast<TreePiece*>(workspace);
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPieceBytes);
+  if (launch_kernel(kv4_tree_kernel<D, TWO>, dim3((unsigned)grid), kThreads, C::SMEM, stream, false, p, pieces, partial) != 0)
+    return -1;
+  return launch_kernel(kv4_tree_join_kernel<D, C::ROWS>, dim3((unsigned)grid, 8), 256, 0, stream, true, p,
+                       (const TreePiece*)pieces, (const float*)partial);
 }
 
 // Two row tiles a block where the sequences have more than 128 rows a kv head on average.
@@ -994,14 +1036,13 @@ bool two_tiles(int B, int T, int H_q, int H_kv) { return B > 0 && (long long)T *
 }  // namespace
 
 size_t kv4_tree_workspace(int B, int T, int H_q, int H_kv, int d) {
-  return (size_t)kMaxGrid * 2 * (two_tiles(B, T, H_q, H_kv) ? 256 : 128) * (d + 2) * sizeof(float);
+  return kPieceBytes + (size_t)kMaxGrid * 2 * (two_tiles(B, T, H_q, H_kv) ? 256 : 128) * (d + 2) * sizeof(float);
 }
 
 int launch_kv4_tree(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
-  float* partial = static_cast<float*>(workspace);
   const bool two = two_tiles(p.B, p.T, p.H_q, p.c.H_kv);
-  if (p.c.d == 128) return two ? launch_t<128, true>(p, partial, stream) : launch_t<128, false>(p, partial, stream);
-  return two ? launch_t<64, true>(p, partial, stream) : launch_t<64, false>(p, partial, stream);
+  if (p.c.d == 128) return two ? launch_t<128, true>(p, workspace, stream) : launch_t<128, false>(p, workspace, stream);
+  return two ? launch_t<64, true>(p, workspace, stream) : launch_t<64, false>(p, workspace, stream);
 }
 
 }  // namespace sdpa
