@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
     auto issue_S = [&](int t, int stage) {
       const uint64_t dq = smem_desc_sw128(sQ + (TWO ? t * C::TILE : 0), 16, 1024);
       const uint64_t dk = smem_desc_sw128(sK + stage * C::TILE, 16, 1024);
-#pragma unroll
+#pragma unroll(TWO ? 4 : 2)
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
         mma_ss_warp(tmem + t * 256, desc_add(dq, off), desc_add(dk, off), idS, kk > 0);
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
     };
     auto issue_PV = [&](int t, int stage, bool acc) {
       const uint64_t dv = smem_desc_sw128(sV + stage * C::TILE, C::BLK, 1024);
-#pragma unroll
+#pragma unroll(TWO ? 4 : 2)
       for (int kk = 0; kk < kUnit / 16; ++kk)
         mma_ts_warp(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, desc_add(dv, kk * 2048), idO, (acc || kk > 0) ? 1u : 0u);
     };
