@@ -38,15 +38,11 @@ namespace {
 
 constexpr int kUnit = 128;    // tokens of a unit
 constexpr int kMaxGrid = 152;  // CTAs, and pairs of partial sums in the workspace
-constexpr int kSegCost = 2;   // a segment's fixed costs, in units
-constexpr int kThreads = 512;  // 8 warps softmax, 4 decode, 1 issues products, 1 loads (2 only share their registers)
-// Registers a thread of the launch, and after the split: softmax, decoding, the rest.
-constexpr int kRegs = 128, kRegsSoft = 184, kRegsDec = 88, kRegsRest = 56;
-static_assert(256 * kRegsSoft + 128 * kRegsDec + 128 * kRegsRest <= kThreads * kRegs, "the launch's registers");
-constexpr int kDecWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
-
+// a segment's fixed costs, in units
+template <int ROWS>
+constexpr int kSegCost = ROWS == 128 ? 4 : 2;
 enum TreeSite { kTreeRawFull = 0xB0, kTreeRawEmpty, kTreeKFull, kTreeKEmpty, kTreeVFull, kTreeVEmpty, kTreeQFull, kTreeQEmpty,
-                kTreeS, kTreeP, kTreeO, kTreeDrain, kTreePartFull, kTreePartEmpty };
+                kTreeS, kTreeP, kTreeO, kTreeDrain, kTreePartFull, kTreePartEmpty, kTreeShare };
 
 // mbar_wait_warp() in fewer instructions: some thirty of them are in line, and every role's code comes
 // from the same instruction cache.
@@ -70,7 +66,7 @@ struct TreeSeq {
   int L, len;    // tokens before the tree, and all (as far as the table goes)
   int lo, first;  // first token some node sees, its unit
   int units, blocks;
-  __device__ __forceinline__ int seg() const { return units > 0 ? units + kSegCost : 0; }
+  int seg;       // numbers of a segment (below)
 };
 template <int ROWS>
 __device__ __forceinline__ TreeSeq tree_seq(const Kv4TreeParams& p, int b) {
@@ -83,6 +79,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const Kv4TreeParams& p, int b) {
   s.lo = p.window >= 0 && s.L > p.window ? s.L - p.window : 0;
   s.first = s.lo / kUnit;
   s.units = s.n > 0 && s.len > 0 ? max((s.len - 1) / kUnit - s.first + 1, 0) : 0;
+  s.seg = s.units > 0 ? s.units + kSegCost<ROWS> : 0;
   s.blocks = (int)(((long long)s.n * (p.H_q / p.c.H_kv) + ROWS - 1) / ROWS);
   return s;
 }
@@ -127,6 +124,14 @@ struct TreeCfg {
   static constexpr int NK = TWO ? 1 : 2, NV = 2;  // (two row tiles: S of a unit is done long before its P V)
   static constexpr int STAGES = D == 128 ? 3 : 6;
   static constexpr int STAGE = kUnit * D * 9 / 8;
+  // Warps: 8 softmax, 4 decode, one or two issue the products, one loads (the last shares their registers).
+  // One row tile has an issuer for each warpgroup's units: with one for both, its waits and instructions
+  // bound the call (110 instead of 98 us for 131,072 tokens, 8 kv heads, 64 rows).  Two row tiles have one
+  // issuer, which takes them in turn: with two 180 instead of 156 us for 256 rows.
+  static constexpr int DEC_WARP = 8, MMA_WARP = 12, ISSUERS = TWO ? 1 : 2, LOAD_WARP = 14, THREADS = 512;
+  // registers a thread of the launch, and after the split: softmax, decoding, the rest
+  static constexpr int REGS = 128, REGS_SOFT = 184, REGS_DEC = 88, REGS_REST = 56;
+  static_assert(256 * REGS_SOFT + 128 * REGS_DEC + 128 * REGS_REST <= THREADS * REGS, "the launch's registers");
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + (TWO ? 2 : 1) * TILE;
   static constexpr int OFF_V = OFF_K + NK * TILE;
@@ -135,7 +140,7 @@ struct TreeCfg {
   static constexpr int OFF_ML = OFF_NAN + NV * D / 16 * 64;  // [2][128] maxima, sums, NaN groups
   static constexpr int OFF_PART = OFF_ML + 3 * 2 * 128 * 4;
   static constexpr int OFF_BAR = OFF_PART + kParts * (int)sizeof(TreePart);
-  static constexpr int N_BAR = 2 * STAGES + 2 * NK + 2 * NV + 2 + 6 + 1 + 2 * kParts;
+  static constexpr int N_BAR = 2 * STAGES + 2 * NK + 2 * NV + 2 + 6 + 2 + 2 * kParts + 4;
   static constexpr int OFF_SLOT = OFF_BAR + N_BAR * 8;
   static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // (aligned by the kernel)
   static constexpr int PART = ROWS * (D + 2);  // floats of one partial: sums, maxima, denominators
@@ -192,7 +197,7 @@ __device__ __forceinline__ uint4 ordered8(const float* v) {
 }  // namespace
 
 template <int D, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreeParams p, TreePiece* pieces, float* partial) {
+__global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(const Kv4TreeParams p, TreePiece* pieces, float* partial) {
   using C = TreeCfg<D, TWO>;
   constexpr int NST = C::STAGES, NK = C::NK, NV = C::NV;
   extern __shared__ uint8_t smem_raw[];
@@ -209,8 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
   uint64_t* p_ready = s_ready + 2;
   uint64_t* o_done = p_ready + 2;
   uint64_t* mma_done = o_done + 2;
-  uint64_t* part_full = mma_done + 1;
+  uint64_t* part_full = mma_done + 2;
   uint64_t* part_empty = part_full + kParts;
+  uint64_t* x_ready = part_empty + kParts;  // [2] a warpgroup's sums of a shared part are there
+  uint64_t* x_read = x_ready + 2;           // [2] it has read the other's
   TreePart* parts = reinterpret_cast<TreePart*>(smem + C::OFF_PART);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -231,20 +238,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
       mbar_init(&v_empty[s], 1);
     }
     mbar_init(q_full, 4);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, C::ISSUERS);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_ready[t], 1);
       mbar_init(&p_ready[t], 4);
       mbar_init(&o_done[t], 1);
+      mbar_init(&x_ready[t], 4);
+      mbar_init(&x_read[t], 4);
+      mbar_init(&mma_done[t], 1);
     }
-    mbar_init(mma_done, 1);
     for (int s = 0; s < kParts; ++s) {
       mbar_init(&part_full[s], 1);
-      mbar_init(&part_empty[s], 8 + 4 + 1);
+      mbar_init(&part_empty[s], 8 + 4 + C::ISSUERS);
     }
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == C::MMA_WARP) {
     tmem_alloc<512>(tmem_slot);
     tmem_relinquish();
   }
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
   // and how many.
   int b = 0;
   long long skip = 0, left = 0;
-  if (warp == kLoadWarp) {
+  if (warp == C::LOAD_WARP) {
     long long total = 0, mine = 0, upto = 0, first = 0;
     bool found = false;
 #pragma unroll 1
@@ -264,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
           mine = 0;
           if (base + lane < p.B) {
             const TreeSeq s = tree_seq<C::ROWS>(p, base + lane);
-            mine = (long long)s.seg() * s.blocks * p.c.H_kv;
+            mine = (long long)s.seg * s.blocks * p.c.H_kv;
           }
           upto = mine;
 #pragma unroll
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
       }
       if (pass == 0) {
         total = carry;
-        const long long want = total / (kSegCost + 1) + 1;  // at least a segment's cost and a unit each
+        const long long want = total / (kSegCost<C::ROWS> + 1) + 1;  // at least a segment's cost and a unit each
         const int n = (int)min((long long)gridDim.x, want);
         if (total == 0 || (int)blockIdx.x >= n) break;
         const long long q = total <= 0x7fffffffLL ? (long long)((unsigned)total / (unsigned)n) : total / n;
@@ -314,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
     ++n_part;
   };
 
-  if (warp >= kMmaWarp) regs_less<kRegsRest>();
-  if (warp == kLoadWarp) {
+  if (warp >= C::MMA_WARP) regs_less<C::REGS_REST>();
+  if (warp == C::LOAD_WARP) {
     // ---------------------------------------------------------------- loading warp
     // Walks the CTA's segments, passes their parts on, and streams their units: lane i copies the block of
     // page i of a unit (whole, also past the sequence's end), if some node sees a token of it: the pages
@@ -339,19 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
             continue;
           }
           s = tree_seq<C::ROWS>(p, b);
-          if (s.seg() == 0) {
+          if (s.seg == 0) {
             ++b;
             continue;
           }
-          const long long vh = skip <= 0x7fffffffLL ? (long long)((unsigned)skip / (unsigned)s.seg()) : skip / s.seg();
-          skip -= vh * s.seg();
+          const long long vh = skip <= 0x7fffffffLL ? (long long)((unsigned)skip / (unsigned)s.seg) : skip / s.seg;
+          skip -= vh * s.seg;
           hk = (int)((unsigned)vh / (unsigned)s.blocks);
           rb = (int)vh - hk * s.blocks;
           enter = false;
         }
         // the CTA's units [from, to) of the segment
-        const int take = (int)min((long long)s.seg() - skip, left);
-        const int from = max((int)skip - kSegCost, 0), to = max((int)skip + take - kSegCost, 0);
+        const int take = (int)min((long long)s.seg - skip, left);
+        const int from = max((int)skip - kSegCost<C::ROWS>, 0), to = max((int)skip + take - kSegCost<C::ROWS>, 0);
         left -= take;
         skip = 0;
         const int r0 = rb * C::ROWS;  // (rows of a kv head are below 2^31)
@@ -432,43 +441,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
       const int last = s + (n - 1 - s) / NST * NST;
       tree_wait(&raw_full[s], (last / NST) & 1, err, kTreeDrain);
     }
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
+  } else if (warp >= C::MMA_WARP && warp < C::MMA_WARP + C::ISSUERS) {
+    // ---------------------------------------------------------------- issuers of the products
     constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false), idO = idesc_bf16_f32(128, D, false, true);
-    const uint32_t sQ = smem_u32(smem + C::OFF_Q), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
-    auto issue_S = [&](int t, int stage) {
-      const uint64_t dq = smem_desc_sw128(sQ + (TWO ? t * C::TILE : 0), 16, 1024);
-      const uint64_t dk = smem_desc_sw128(sK + stage * C::TILE, 16, 1024);
-#pragma unroll(TWO ? 4 : 2)
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
-        mma_ss_warp(tmem + t * 256, desc_add(dq, off), desc_add(dk, off), idS, kk > 0);
-      }
-      mma_commit_warp(&s_ready[t]);
-    };
-    auto issue_PV = [&](int t, int stage, bool acc) {
-      const uint64_t dv = smem_desc_sw128(sV + stage * C::TILE, C::BLK, 1024);
-#pragma unroll(TWO ? 4 : 2)
-      for (int kk = 0; kk < kUnit / 16; ++kk)
-        mma_ts_warp(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, desc_add(dv, kk * 2048), idO, (acc || kk > 0) ? 1u : 0u);
-    };
-    int nq = 0, nk = 0, nv = 0;  // phases consumed
-    uint32_t np = 0u;            // parities of p_ready, a bit a tile
     bool issued = false;
-    auto wait_K = [&]() {
-      ok = ok && tree_wait(&k_full[nk % NK], (nk / NK) & 1, err, kTreeKFull);
-      if (ok) tc_fence_after();
-      return ok;
-    };
+    if constexpr (TWO) {
+      const uint32_t sQ = smem_u32(smem + C::OFF_Q), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
+      auto issue_S = [&](int t, int stage) {
+        const uint64_t dq = smem_desc_sw128(sQ + (TWO ? t * C::TILE : 0), 16, 1024);
+        const uint64_t dk = smem_desc_sw128(sK + stage * C::TILE, 16, 1024);
+#pragma unroll 4
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
+          mma_ss_warp(tmem + t * 256, desc_add(dq, off), desc_add(dk, off), idS, kk > 0);
+        }
+        mma_commit_warp(&s_ready[t]);
+      };
+      auto issue_PV = [&](int t, int stage, bool acc) {
+        const uint64_t dv = smem_desc_sw128(sV + stage * C::TILE, C::BLK, 1024);
+#pragma unroll 4
+        for (int kk = 0; kk < kUnit / 16; ++kk)
+          mma_ts_warp(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, desc_add(dv, kk * 2048), idO, (acc || kk > 0) ? 1u : 0u);
+      };
+      int nq = 0, nk = 0, nv = 0;  // phases consumed
+      uint32_t np = 0u;            // parities of p_ready, a bit a tile
+      auto wait_K = [&]() {
+        ok = ok && tree_wait(&k_full[nk % NK], (nk / NK) & 1, err, kTreeKFull);
+        if (ok) tc_fence_after();
+        return ok;
+      };
 #pragma unroll 1
-    while (next_part()) {
-      const int cnt = parts[n_part % kParts].cnt;
-      part_done();
-      if (cnt == 0) continue;
-      ok = tree_wait(q_full, nq++ & 1, err, kTreeQFull);
-      if (!ok) break;
-      issued = true;
-      if constexpr (TWO) {
+      while (next_part()) {
+        const int cnt = parts[n_part % kParts].cnt;
+        part_done();
+        if (cnt == 0) continue;
+        ok = tree_wait(q_full, nq++ & 1, err, kTreeQFull);
+        if (!ok) break;
+        issued = true;
         if (!wait_K()) break;
         issue_S(0, nk % NK);
         issue_S(1, nk % NK);
@@ -496,42 +505,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
           if (need_k) mma_commit_warp(&k_empty[nk++ % NK]);
           if (k + 2 == cnt) mma_commit_warp(q_empty);  // every S of the part is issued
         }
-      } else {
-        for (int k = 0; k < min(cnt, 2); ++k) {
-          if (!wait_K()) break;
-          issue_S(k, nk % NK);
-          mma_commit_warp(&k_empty[nk++ % NK]);
-        }
+      }
+    } else {
+      // A tile's S, P V and next S follow one another (P lies where S was); the two warpgroups' tiles are
+      // independent.
+      const int t = warp - C::MMA_WARP;
+      const uint32_t tS = tmem + t * 256, tO = tS + 128;
+      const uint64_t dQ = smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BLK, 1024);
+      int n = 0, nq = 0, np = 0;  // units of the CTA's stream; parts with units; phases of p_ready
+#pragma unroll 1
+      while (ok && next_part()) {
+        const int cnt = parts[n_part % kParts].cnt;
+        part_done();
+        if (cnt == 0) continue;
+        ok = tree_wait(q_full, nq++ & 1, err, kTreeQFull);
         if (!ok) break;
-        if (cnt <= 2) mma_commit_warp(q_empty);
-        for (int k = 0; k < cnt; ++k) {
-          const int t = k & 1;
-          ok = tree_wait(&v_full[nv % NV], (nv / NV) & 1, err, kTreeVFull);
-          ok = ok && tree_wait(&p_ready[t], np >> t & 1u, err, kTreeP);
-          if (!ok) break;
-          np ^= 1u << t;
-          tc_fence_after();
-          issue_PV(t, nv % NV, k > 1);
-          mma_commit_warp(&v_empty[nv++ % NV]);
-          if (k + 2 >= cnt) {
-            mma_commit_warp(&o_done[t]);
-            continue;
-          }
-          if (!wait_K()) break;
-          issue_S(t, nk % NK);
-          mma_commit_warp(&k_empty[nk++ % NK]);
-          if (k + 3 == cnt) mma_commit_warp(q_empty);
+        const int k_first = (n ^ t) & 1;
+        if (k_first >= cnt) {  // the other tile has the part's only unit
+          if (lane == 0) mbar_arrive(q_empty);
+          n += cnt;
+          continue;
         }
+        issued = true;
+#pragma unroll 1
+        for (int k = k_first; k < cnt; k += 2) {
+          const int u = n + k, sk = u % NK, sv = u % NV;
+          const bool last = k + 2 >= cnt;
+          ok = tree_wait(&k_full[sk], (u / NK) & 1, err, kTreeKFull);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 2
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
+            mma_ss_warp(tS, desc_add(dQ, off), desc_add(dK, sk * C::TILE + off), idS, kk > 0);
+          }
+          mma_commit_warp(&s_ready[t]);
+          mma_commit_warp(&k_empty[sk]);
+          if (last) mma_commit_warp(q_empty);  // every S of the part is issued
+          ok = tree_wait(&v_full[sv], (u / NV) & 1, err, kTreeVFull);
+          ok = ok && tree_wait(&p_ready[t], np++ & 1, err, kTreeP);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 2
+          for (int kk = 0; kk < kUnit / 16; ++kk)
+            mma_ts_warp(tO, tS + kk * 8, desc_add(dV, sv * C::TILE + kk * 2048), idO, (k > k_first || kk > 0) ? 1u : 0u);
+          mma_commit_warp(&v_empty[sv]);
+          if (last) mma_commit_warp(&o_done[t]);
+        }
+        n += cnt;
       }
     }
-    // every MMA must be complete before TMEM is released
+    // every product must be complete before TMEM is released
     if (issued) {
-      mma_commit_warp(mma_done);
-      tree_wait(mma_done, 0, err, kTreeDrain);
+      uint64_t* bar = &mma_done[warp - C::MMA_WARP];
+      mma_commit_warp(bar);
+      tree_wait(bar, 0, err, kTreeDrain);
     }
-  } else if (warp >= kDecWarp && warp < kDecWarp + 4) {
+  } else if (warp >= C::DEC_WARP && warp < C::MMA_WARP) {
     // ---------------------------------------------------------------- decoding warps
-    regs_less<kRegsDec>();
+    regs_less<C::REGS_DEC>();
     const int tid = threadIdx.x % 128, P = p.c.page_size, block = kv4_block_bytes(P, D);
     constexpr int N = D / 32, STEP = 128 / N, NG = D / 16;  // 16-byte pieces a thread takes of K, of V; tokens between them
     auto page_at = [&](int tok) { return tok / P * block; };
@@ -601,28 +635,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         const uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
         ok = tree_wait(&raw_full[stage], (n / NST) & 1, err, kTreeRawFull);
         if (!ok) break;
-        // both operands' bytes are read at once, so that the stage is free early
-        uint4 wk[N], wv[N];
-        uint32_t sc[N], two[N];
+        uint4 w[N];
+        uint32_t sc[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int off = page_at(STEP * i), in = STEP * i & (P - 1);
-          wk[i] = *reinterpret_cast<const uint4*>(st + code_k + off + in * (D / 2));
+          w[i] = *reinterpret_cast<const uint4*>(st + code_k + off + in * (D / 2));
           sc[i] = *reinterpret_cast<const unsigned short*>(st + scale_k + off + in * (D / 16));
-          wv[i] = *reinterpret_cast<const uint4*>(st + code_v + off + in / 2 * D);
-          two[i] = *reinterpret_cast<const unsigned short*>(st + scale_v + off + in / 2 * (D / 8));
         }
         if (n >= NK) ok = tree_wait(&k_empty[sk], (n / NK - 1) & 1, err, kTreeKEmpty);
         if (!ok) break;
-        __syncwarp();  // every lane has read its pieces
-        if (lane == 0) mbar_arrive(&raw_empty[stage]);
         {
           uint8_t* d = smem + C::OFF_K + sk * C::TILE;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const uint32_t sp = scale_pair(swap ? __byte_perm(sc[i], 0u, 0x4401) : sc[i]);
             const Kv4Small a = scales_low(sp), b2 = scales_high(sp);
-            const uint4 x = swap ? make_uint4(wk[i].z, wk[i].w, wk[i].x, wk[i].y) : wk[i];
+            const uint4 x = swap ? make_uint4(w[i].z, w[i].w, w[i].x, w[i].y) : w[i];
             *reinterpret_cast<uint4*>(d + i * STEP * 128 + dst_k) = decode8(x.x, a);
             *reinterpret_cast<uint4*>(d + i * STEP * 128 + (dst_k ^ 16)) = decode8(x.y, a);
             *reinterpret_cast<uint4*>(d + i * STEP * 128 + (dst_k ^ 32)) = decode8(x.z, b2);
@@ -632,6 +661,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[sk]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int off = page_at(STEP * i), in = STEP * i & (P - 1);
+          w[i] = *reinterpret_cast<const uint4*>(st + code_v + off + in / 2 * D);
+          sc[i] = *reinterpret_cast<const unsigned short*>(st + scale_v + off + in / 2 * (D / 8));
+        }
+        __syncwarp();  // every lane has read its pieces
+        if (lane == 0) mbar_arrive(&raw_empty[stage]);
         if (n >= NV) ok = tree_wait(&v_empty[sv], (n / NV - 1) & 1, err, kTreeVEmpty);
         if (!ok) break;
         // units whose tokens are not all seen by all rows, as the softmax warps decide it
@@ -644,15 +681,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
           for (int i = 0; i < N; ++i) {
             const int tok = 2 * u + STEP * i;
             uint32_t bits = 0u;
-            if (tok >= len || tok < lo) two[i] &= 0xFF00u;
-            if (tok + 1 >= len || tok + 1 < lo) two[i] &= 0x00FFu;
-            if ((two[i] & 0x00F8u) == 0x00F8u) {
+            if (tok >= len || tok < lo) sc[i] &= 0xFF00u;
+            if (tok + 1 >= len || tok + 1 < lo) sc[i] &= 0x00FFu;
+            if ((sc[i] & 0x00F8u) == 0x00F8u) {
               bits |= 1u;
-              two[i] &= 0xFF00u;
+              sc[i] &= 0xFF00u;
             }
-            if ((two[i] & 0xF800u) == 0xF800u) {
+            if ((sc[i] & 0xF800u) == 0xF800u) {
               bits |= 2u;
-              two[i] &= 0x00FFu;
+              sc[i] &= 0x00FFu;
             }
             smem[C::OFF_NAN + (sv * NG + g) * 64 + tok / 2] = (uint8_t)bits;
           }
@@ -661,11 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
           uint8_t* d = smem + C::OFF_V + sv * C::TILE;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const uint32_t sp = scale_pair(two[i]);
+            const uint32_t sp = scale_pair(sc[i]);
             const Kv4Small a = scales_low(sp), b2 = scales_high(sp);
             // (D = 128: 8 bytes a token; D = 64: the two eighths' 4 bytes a token)
-            const uint32_t t0w0 = wv[i].x, t0w1 = D == 128 ? wv[i].y : wv[i].z, t1w0 = D == 128 ? wv[i].z : wv[i].y,
-                           t1w1 = wv[i].w;
+            const uint32_t t0w0 = w[i].x, t0w1 = D == 128 ? w[i].y : w[i].z, t1w0 = D == 128 ? w[i].z : w[i].y,
+                           t1w1 = w[i].w;
             uint8_t* di = d + i * STEP * 128;  // (the chunk's exclusive-or with 1: the row's next token)
             *reinterpret_cast<uint4*>(di + dst_v) = decode8(flip ? t0w1 : t0w0, a);
             *reinterpret_cast<uint4*>(di + (dst_v ^ 16)) = decode8(flip ? t0w0 : t0w1, a);
@@ -681,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
     }
   } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax and output
-    regs_more<kRegsSoft>();
+    regs_more<C::REGS_SOFT>();
     const int t = warp / 4, r = (warp % 4) * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const uint32_t aS = lane_addr + t * 256, aO = aS + 128;
@@ -691,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
     float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);  // [2][128] maxima, sums, NaN groups of the two halves
     float* xl = xm + 256;
     uint32_t* xn = reinterpret_cast<uint32_t*>(xl + 256);
-    int ns = 0, n_before = 0;  // s_ready phases consumed; units of the parts before
-    uint32_t no = 0u;          // parities of o_done
+    int ns = 0, nx = 0, n_before = 0;  // s_ready phases consumed; parts shared with the other warpgroup; units of the parts before
+    uint32_t no = 0u;          // parity of o_done
 #pragma unroll 1
     for (; next_part(); part_done()) {
       const TreePart& part = parts[n_part % kParts];
@@ -705,38 +742,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
       float m_run = -INFINITY, l = 0.f;
       uint32_t nans = 0u;  // groups of 16 dims in which this row sees a NaN
       bool first = true;
-      int unit = part.unit0 + (TWO ? 0 : t);
+      // one tile: unit n of the CTA's stream is warpgroup n % 2's
+      const int k_first = TWO ? 0 : (n_before ^ t) & 1;
+      if (!TWO && cnt <= 1 && k_first != 0) {  // the other warpgroup has all of it
+        n_before += cnt;
+        continue;
+      }
+      int unit = part.unit0 + k_first;
       const int u_win = part.u_win, u_tree = part.u_tree;
 #pragma unroll 1
-      for (int k = TWO ? 0 : t; k < cnt; k += TWO ? 1 : 2, unit += TWO ? 1 : 2) {
+      for (int k = k_first; k < cnt; k += TWO ? 1 : 2, unit += TWO ? 1 : 2) {
         const bool edge = unit < u_win || unit >= u_tree;
         uint32_t vis[4] = {0u, 0u, 0u, 0u};  // the unit's tokens that this row sees
         if (edge && warp_ok) {
-          const int L = part.L, row0 = part.row0;
-          const long long k0 = (long long)unit * kUnit, a0 = k0 - L;  // the unit's first token; the node there
-          long long lo = 0;  // first token before the tree that this row sees
+          const int L = part.L, row0 = part.row0, k0 = unit * kUnit, a0 = k0 - L;  // the unit's first token; the node there
+          const int end = part.len - L;  // nodes that have a token
+          int lo = 0;                    // first token before the tree that this row sees
           if (p.window >= 0) {
             int depth = node;
             if (p.parents) {
               depth = 0;
               for (int a = tree_parent(p, row0, node); a >= 0; a = tree_parent(p, row0, a)) ++depth;
             }
-            lo = (long long)L + depth - p.window;
+            lo = depth >= p.window ? L : max(L - (p.window - depth), 0);
           }
-          set_range(vis, (int)min(max(lo - k0, 0LL), (long long)kUnit), (int)max(min(L - k0, (long long)kUnit), 0LL));
+          set_range(vis, lo - k0, L - k0);
           if (!p.parents) {
-            const long long from = p.window >= 0 ? max((long long)node - p.window, 0LL) : 0;
-            set_range(vis, (int)min(max(from - a0, 0LL), (long long)kUnit),
-                      (int)max(min(min((long long)node + 1, (long long)part.len - L) - a0, (long long)kUnit), 0LL));
+            set_range(vis, (p.window >= 0 && node > p.window ? node - p.window : 0) - a0, min(node + 1, end) - a0);
           } else {
             int step = 0;
-            for (int a = node; a >= 0 && a >= a0 && (p.window < 0 || step <= p.window); a = tree_parent(p, row0, a), ++step) {
-              const long long j = a - a0;
-              if (j < kUnit && a < part.len - L) {
-                const uint32_t bit = 1u << ((int)j & 31);
+            for (int a = node; a >= max(a0, 0) && (p.window < 0 || step <= p.window); a = tree_parent(p, row0, a), ++step) {
+              const int j = a - a0;
+              if (j < kUnit && a < end) {
+                const uint32_t bit = 1u << (j & 31);
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                  if ((int)j / 32 == w) vis[w] |= bit;
+                  if (j / 32 == w) vis[w] |= bit;
               }
             }
           }
@@ -765,13 +806,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         }
         // the row's 128 scores in one batch of loads, each with the maximum of its 32
         uint32_t s[4][32];
-        float c0, c1, c2, c3;
-        tmem_ld32_max(aS, s[0], c0);
-        tmem_ld32_max(aS + 32, s[1], c1);
-        tmem_ld32_max(aS + 64, s[2], c2);
-        tmem_ld32_max(aS + 96, s[3], c3);
+        float cm[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_max(aS + 32 * c, s[c], cm[c]);
         tmem_ld_wait();
-        const float mx = fmax3(c0, c1, fmaxf(c2, c3));
+        const float mx = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
         const float m_tile = mx * sl2;
         // The running maximum (log2 units) moves only when some row of the warp passes it by 2^8; the
         // sums stay exact, they are relative to the maximum that was used.
@@ -791,11 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
             }
           }
           m_run = m_new;
-          // (read anew, so that this rare path does not need the registers of 128 scores beside its own)
-          tmem_ld32(aS, s[0]);
-          tmem_ld32(aS + 32, s[1]);
-          tmem_ld32(aS + 64, s[2]);
-          tmem_ld32(aS + 96, s[3]);
+          // (read anew, so that this rare path does not need the scores' registers beside its own)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(aS + 32 * c, s[c]);
           tmem_ld_wait();
         }
         first = false;
@@ -845,29 +882,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
       }
       n_before += cnt;
       // ---- the part's end: of a whole segment the outputs, of a piece its sums
-      const bool have0 = TWO ? (t == 0 && cnt > 0) : cnt > 0, have1 = TWO ? (t == 1 && cnt > 0) : cnt > 1;
-      if (ok && have0) {
-        ok = tree_wait(&o_done[0], no & 1u, err, kTreeO);
+      const bool both = !TWO && cnt > 1;  // the other warpgroup has sums of these rows too
+      if (ok && cnt > 0) {
+        ok = tree_wait(&o_done[t], no & 1u, err, kTreeO);
         no ^= 1u;
       }
-      if (ok && have1) {
-        ok = tree_wait(&o_done[1], no >> 1 & 1u, err, kTreeO);
-        no ^= 2u;
-      }
-      float m = m_run, f0 = 1.f, f1 = 1.f;
-      if constexpr (!TWO) {
-        // (a warp whose wait gave up comes here too, so that nobody waits for it, and all stop)
+      float m = m_run, f_own = 1.f, f_other = 0.f;
+      if (both) {
         xm[t * 128 + r] = m_run;
         xl[t * 128 + r] = l;
         xn[t * 128 + r] = nans;
-        ok = bar_red_and(1, 256, ok);
-        const float m0 = xm[r], m1 = xm[128 + r], l0 = xl[r], l1 = xl[128 + r];
-        nans = xn[r] | xn[128 + r];
-        m = fmaxf(m0, m1);
-        f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
-        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_ready[t]);
+        ok = ok && tree_wait(&x_ready[1 - t], nx & 1, err, kTreeShare);
+        const float m2 = xm[(1 - t) * 128 + r], l2 = xl[(1 - t) * 128 + r];
+        nans |= xn[(1 - t) * 128 + r];
+        m = fmaxf(m_run, m2);
+        f_own = m_run == -INFINITY ? 0.f : ex2(m_run - m);
+        f_other = m2 == -INFINITY ? 0.f : ex2(m2 - m);
         // (no key: the sum is 0, or a NaN that has to stay)
-        l = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
+        const float a = m_run == -INFINITY ? l : l * f_own, b2 = m2 == -INFINITY ? l2 : l2 * f_other;
+        l = t == 0 ? a + b2 : b2 + a;
       }
       if (!ok) break;
       tc_fence_after();
@@ -877,20 +913,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         if (whole && row_ok) z = tree_finish(p, h, m, l);
         float* slot = partial + ((size_t)2 * blockIdx.x + max(part.slot, 0)) * C::PART;
         __nv_bfloat16* o = p.o + ((size_t)(part.row0 + node) * p.H_q + h) * D;
-        constexpr int COLS = TWO ? D : D / 2;  // one tile: each half of the warps stores half of the dims
-        const int c_first = TWO ? 0 : t * COLS;
+        // where both warpgroups have sums, each stores half of the dims
+        const int c_first = both ? t * (D / 2) : 0, c_end = both ? c_first + D / 2 : D;
 #pragma unroll 1
-        for (int c0 = c_first; c0 < c_first + COLS; c0 += 16) {
+        for (int c0 = c_first; c0 < c_end; c0 += 16) {
           uint32_t a[16], b2[16];
           float v[16];
-          if (have0) tmem_ld16(lane_addr + 128 + c0, a);
-          if (have1) tmem_ld16(lane_addr + 256 + 128 + c0, b2);
+          if (cnt > 0) tmem_ld16(aO + c0, a);
+          if (both) tmem_ld16(lane_addr + (1 - t) * 256 + 128 + c0, b2);
           tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            v[c] = 0.f;
-            if (have0) v[c] = __uint_as_float(a[c]) * f0;
-            if (have1) v[c] = fmaf(__uint_as_float(b2[c]), f1, v[c]);
+            v[c] = cnt > 0 ? __uint_as_float(a[c]) * f_own : 0.f;
+            if (both) v[c] = fmaf(__uint_as_float(b2[c]), f_other, v[c]);
           }
           if (nans >> (c0 / 16) & 1u) {
 #pragma unroll
@@ -907,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
               *reinterpret_cast<float4*>(slot + rr * D + c0 + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
         }
-        if (row_ok && (TWO || t == 0)) {
+        if (row_ok && (!both || t == 0)) {
           if (whole) {
             if (p.lse) p.lse[(size_t)h * p.T + part.row0 + node] = z.lse;
           } else {
@@ -917,13 +952,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4TreePara
         }
       }
       tc_fence_before();
-      if constexpr (!TWO) named_bar_sync(1, 256);  // both halves have read the sums: they may be overwritten
+      if (both) {  // the other warpgroup has read this one's sums: they may be overwritten
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_read[t]);
+        ok = tree_wait(&x_read[1 - t], nx & 1, err, kTreeShare);
+        ++nx;
+      }
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == C::MMA_WARP) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc<512>(tmem);
@@ -1024,7 +1064,7 @@ int launch_t(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
   const int grid = std::min(n, kMaxGrid);
   TreePiece* pieces = static_cast<TreePiece*>(workspace);
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPieceBytes);
-  if (launch_kernel(kv4_tree_kernel<D, TWO>, dim3((unsigned)grid), kThreads, C::SMEM, stream, false, p, pieces, partial) != 0)
+  if (launch_kernel(kv4_tree_kernel<D, TWO>, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, false, p, pieces, partial) != 0)
     return -1;
   return launch_kernel(kv4_tree_join_kernel<D, C::ROWS>, dim3((unsigned)grid, 8), 256, 0, stream, true, p,
                        (const TreePiece*)pieces, (const float*)partial);
