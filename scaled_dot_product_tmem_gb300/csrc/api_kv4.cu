@@ -256,12 +256,13 @@ int attn_kv4_keep(void* pool, const int* page_table, const int* seq_lens, const 
   p.start = seq_lens;
   p.kept = kept;
   p.pool = static_cast<uint8_t*>(pool);
+  p.n_layers = n_layers;
   p.layer_bytes = (long long)n_pages * H_kv * sdpa::kv4_block_bytes(page_size, d);
   p.page_err = sdpa::device_page_error_word();
   p.site = ATTN_KV4_SITE_KEEP;
   if (!p.page_err) return ATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch("kv4 keep launch", 1, s, [&] { return sdpa::launch_kv4_keep(p, n_layers, s); });
+  return launch("kv4 keep launch", 1, s, [&] { return sdpa::launch_kv4_keep(p, s); });
 }
 
 int attn_kv4_copy_pages(void* pool, int n_layers, int n_pages, size_t page_bytes, const int* src, const int* dst,

@@ -91,6 +91,7 @@ int rope_params(RopeParams* p, const void* q, const void* k, const float* table,
   p->n = n;
   p->first = first_dim;
   p->inverse = inverse != 0;
+  p->copies = 2 * n < d && ((H_q > 0 && q != q_out) || (H_k > 0 && k != k_out));
   return ATTN_OK;
 }
 

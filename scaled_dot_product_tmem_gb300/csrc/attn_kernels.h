@@ -273,11 +273,12 @@ struct Kv4KeepParams {
   const int* start;  // [B]
   const int* kept;   // [B, most], ended by a negative entry
   uint8_t* pool;
+  int n_layers;
   long long layer_bytes;
   int* page_err;
   int site;
 };
-int launch_kv4_keep(const Kv4KeepParams& p, int n_layers, cudaStream_t stream);
+int launch_kv4_keep(const Kv4KeepParams& p, cudaStream_t stream);
 
 // One warp waits on an mbarrier nobody arrives at: after the wait limit it records
 // kErrTimeoutBase + site in *err and returns (the failure path, without a fault).

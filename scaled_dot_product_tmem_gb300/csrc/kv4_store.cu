@@ -123,7 +123,7 @@ __device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint
 // and sines for all heads.  The turned values are rounded to bf16, as a rotation of its own would
 // leave them, and then quantised.  Blocks behind those of the append turn the queries.
 template <int D, int ROT>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4StoreParams p, const RopeParams rp, int gx, int gy) {
+__global__ void __launch_bounds__(256, ROT ? 3 : 1) kv4_append_kernel(const Kv4StoreParams p, const RopeParams rp, int gx, int gy) {
   constexpr int NG = D / 16, HS = 256 / (NG * kTok);  // heads a block takes at a time
   int bx = blockIdx.x, by = blockIdx.y;
   if constexpr (ROT != 0) {
@@ -297,89 +297,99 @@ int launch_kv4_append_rope(const Kv4StoreParams& p, const RopeParams& rp, bool i
 }
 
 // Kept tokens: node kept[b][i] of sequence b's tree (its token start[b] + kept[b][i]) becomes token
-// start[b] + i, in the order of i, until the first negative entry.  A thread owns the same few
-// bytes of every token of a sequence, head and layer, so the moves of one sequence follow one another
-// without a barrier, whatever the entries are.  Entries that only move down (kept >= i, as ascending
-// ones do) cannot read what an earlier move of the same four wrote, so four are loaded at once.
-// Bound by latency for few sequences: the chain entry - page - bytes, twice for up to eight tokens.
+// start[b] + i, in the order of i, until the first negative entry.  A block takes one sequence: a warp
+// looks 32 entries' pages up at once, for all heads and layers that the block then walks.  A thread owns
+// the same few bytes of every token of a head and layer, so its moves follow one another without a
+// barrier, whatever the entries are.  Entries that only move down (kept >= i, as ascending ones do)
+// cannot read what an earlier one of the same eight wrote, so eight are loaded at once.
 template <int D>
-__global__ void __launch_bounds__(64) kv4_keep_kernel(const Kv4KeepParams p) {
+__global__ void __launch_bounds__(256) kv4_keep_kernel(const Kv4KeepParams p) {
   // words (4 bytes) of K codes, of V codes, of K scales; then V's scale bytes
-  constexpr int KW = D / 8, VW = D / 8, SW = D / 64, NV = D / 16;
-  const int x = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
-  if (x >= KW + VW + SW + NV) return;
-  const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
-  uint8_t* layer = p.pool + (size_t)blockIdx.z * p.layer_bytes;
+  constexpr int KW = D / 8, VW = D / 8, SW = D / 64, NV = D / 16, BATCH = 8;
+  static_assert(KW + VW + SW + NV <= 64, "64 threads a head and layer");
+  struct Move {
+    long long src, dst;  // a page's offset in a layer, or -1: this entry moves nothing
+    int ws, wd;          // the tokens' places in their pages
+  };
+  __shared__ Move moves[32];
+  __shared__ int n_moves, n_down;  // entries until the end; how many of the first keep to kept >= i
+  const int x = threadIdx.x % 64, b = blockIdx.y;
+  const int P = p.c.page_size, blk = kv4_block_bytes(P, D), units = p.c.H_kv * p.n_layers;
+  const long long page_bytes = (long long)p.c.H_kv * blk;
   const int start = __ldg(p.start + b);
-  const int* kept = p.kept + (size_t)b * p.most;
+  // this thread's bytes of the token at place w of a page
+  auto place = [&](int w) {
+    if (x < KW) return w * (D / 2) + 4 * x;
+    if (x < KW + VW) return kv4_off_v(P, D) + kv4_v_at(w, (x - KW) * 4 / (D / 16), D) + (x - KW) * 4 % (D / 16);
+    if (x < KW + VW + SW) return kv4_off_sk(P, D) + w * (D / 16) + 4 * (x - KW - VW);
+    return kv4_off_sv(P, D) + (w >> 1) * (D / 8) + 2 * (x - KW - VW - SW) + (w & 1);
+  };
   const bool byte = x >= KW + VW + SW;
-  // this thread's bytes of token tok: their offset in the layer, or -1 (no page)
-  auto where = [&](long long tok) -> long long {
-    const int pg = tok > 0x7fffffffLL ? -1 : kv4_page(p.c, b, (int)tok);
-    if (pg < 0) {
-      atomicCAS(p.page_err, 0, p.site);
-      return -1;
-    }
-    const int w = (int)tok & (P - 1);
-    int at;
-    if (x < KW) at = w * (D / 2) + 4 * x;
-    else if (x < KW + VW) at = kv4_off_v(P, D) + kv4_v_at(w, (x - KW) * 4 / (D / 16), D) + (x - KW) * 4 % (D / 16);
-    else if (!byte) at = kv4_off_sk(P, D) + w * (D / 16) + 4 * (x - KW - VW);
-    else at = kv4_off_sv(P, D) + (w >> 1) * (D / 8) + 2 * (x - KW - VW - SW) + (w & 1);
-    return ((long long)pg * p.c.H_kv + h) * blk + at;
-  };
-  auto get = [&](long long at) { return byte ? (uint32_t)layer[at] : *reinterpret_cast<const uint32_t*>(layer + at); };
-  auto put = [&](long long at, uint32_t v) {
-    if (byte) layer[at] = (uint8_t)v;
-    else *reinterpret_cast<uint32_t*>(layer + at) = v;
-  };
-  for (int i = 0; i < p.most; i += 4) {
-    int from[4], n = 0;
-    bool down = true;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) from[j] = i + j < p.most ? __ldg(kept + i + j) : -1;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n == j && from[j] >= 0) ++n;
-      down = down && (n <= j || from[j] >= i + j);
-    }
-    long long src[4], dst[4];
-    uint32_t v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      src[j] = dst[j] = -1;
-      if (j < n && from[j] != i + j) {
-        src[j] = where((long long)start + from[j]);
-        dst[j] = where((long long)start + i + j);
+  for (int i0 = 0; i0 < p.most; i0 += 32) {
+    if (threadIdx.x < 32) {
+      const int i = i0 + threadIdx.x, from = i < p.most ? __ldg(p.kept + (size_t)b * p.most + i) : -1;
+      const unsigned end = __ballot_sync(0xffffffffu, from < 0), up = __ballot_sync(0xffffffffu, from < i);
+      const int n = end ? __ffs(end) - 1 : 32;
+      Move m{-1, -1, 0, 0};
+      if ((int)threadIdx.x < n && from != i) {
+        const long long ts = (long long)start + from, td = (long long)start + i;
+        const int ps = ts > 0x7fffffffLL ? -1 : kv4_page(p.c, b, (int)ts), pd = td > 0x7fffffffLL ? -1 : kv4_page(p.c, b, (int)td);
+        if (ps >= 0 && pd >= 0) m = Move{ps * page_bytes, pd * page_bytes, (int)ts & (P - 1), (int)td & (P - 1)};
+        else atomicCAS(p.page_err, 0, p.site);
+      }
+      moves[threadIdx.x] = m;
+      if (threadIdx.x == 0) {
+        n_moves = n;
+        n_down = up ? __ffs(up) - 1 : 32;
       }
     }
-    if (down) {
+    __syncthreads();
+    const int n = n_moves, down = n_down;
+    if (x < KW + VW + SW + NV) {
+      for (int u = blockIdx.x * 4 + threadIdx.x / 64; u < units; u += gridDim.x * 4) {
+        uint8_t* base = p.pool + (size_t)(u / p.c.H_kv) * p.layer_bytes + (size_t)(u % p.c.H_kv) * blk;
+        auto get = [&](const Move& m) {
+          const uint8_t* a = base + m.src + place(m.ws);
+          return byte ? (uint32_t)*a : *reinterpret_cast<const uint32_t*>(a);
+        };
+        auto put = [&](const Move& m, uint32_t v) {
+          uint8_t* a = base + m.dst + place(m.wd);
+          if (byte) *a = (uint8_t)v;
+          else *reinterpret_cast<uint32_t*>(a) = v;
+        };
+        int j = 0;
+        for (; j < min(n, down); j += BATCH) {
+          uint32_t v[BATCH];
+          const int last = min(j + BATCH, min(n, down));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (src[j] >= 0) v[j] = get(src[j]);
+          for (int q = 0; q < BATCH; ++q)
+            if (j + q < last && moves[j + q].src >= 0) v[q] = get(moves[j + q]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (src[j] >= 0 && dst[j] >= 0) put(dst[j], v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (src[j] >= 0 && dst[j] >= 0) put(dst[j], get(src[j]));
+          for (int q = 0; q < BATCH; ++q)
+            if (j + q < last && moves[j + q].src >= 0) put(moves[j + q], v[q]);
+        }
+        for (j = min(n, down); j < n; ++j)
+          if (moves[j].src >= 0) put(moves[j], get(moves[j]));
+      }
     }
-    if (n < 4) break;
+    if (n < 32) break;
+    __syncthreads();
   }
-}
-
-int launch_kv4_keep(const Kv4KeepParams& p, int n_layers, cudaStream_t stream) {
-  const dim3 grid((unsigned)p.c.H_kv, (unsigned)p.B, (unsigned)n_layers);
-  if (p.c.d == 128) kv4_keep_kernel<128><<<grid, 64, 0, stream>>>(p);
-  else kv4_keep_kernel<64><<<grid, 64, 0, stream>>>(p);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_kv4_gather(const Kv4StoreParams& p, cudaStream_t stream) {
   const dim3 blocks = store_grid(p, 1);
   if (p.c.d == 128) kv4_gather_kernel<128><<<blocks, 256, 0, stream>>>(p);
   else kv4_gather_kernel<64><<<blocks, 256, 0, stream>>>(p);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_kv4_keep(const Kv4KeepParams& p, cudaStream_t stream) {
+  // four (head, layer) units a block at a time; enough blocks a sequence to fill the device
+  const int units = (p.c.H_kv * p.n_layers + 3) / 4, fill = (152 * 8 + p.B - 1) / p.B;
+  const dim3 grid((unsigned)(units < fill ? units : fill), (unsigned)p.B);
+  if (p.c.d == 128) kv4_keep_kernel<128><<<grid, 256, 0, stream>>>(p);
+  else kv4_keep_kernel<64><<<grid, 256, 0, stream>>>(p);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 

@@ -27,19 +27,24 @@ struct RopeParams {
   const float* table;  // [table_rows][2][n]; row t takes table row t % table_rows
   int T, table_rows, d, n, first;
   int inverse;  // turn back: the transposed rotation
+  int copies;   // some tensor is turned out of place: the dims that stay are copied
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// x1 c - x2 s of 8 values
+// x1 c - x2 s of 8 values, or x1 c + x2 s.  (Single operations: paired ones, mul.rn.f32x2 and add.rn.f32x2, are
+// fused into one rounding by the assembler in spite of their .rn.)
+template <bool ADD = false>
 __device__ __forceinline__ uint4 rope_turn8(const uint4& x1, const uint4& x2, const float (&c)[8], const float (&s)[8]) {
   const uint32_t u[4] = {x1.x, x1.y, x1.z, x1.w}, w[4] = {x2.x, x2.y, x2.z, x2.w};
   uint32_t y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    y[i] = pack_bf16x2(__fsub_rn(__fmul_rn(bf16_lo(u[i]), c[2 * i]), __fmul_rn(bf16_lo(w[i]), s[2 * i])),
-                       __fsub_rn(__fmul_rn(bf16_hi(u[i]), c[2 * i + 1]), __fmul_rn(bf16_hi(w[i]), s[2 * i + 1])));
+  for (int i = 0; i < 4; ++i) {
+    const float a0 = __fmul_rn(bf16_lo(u[i]), c[2 * i]), a1 = __fmul_rn(bf16_hi(u[i]), c[2 * i + 1]);
+    const float b0 = __fmul_rn(bf16_lo(w[i]), s[2 * i]), b1 = __fmul_rn(bf16_hi(w[i]), s[2 * i + 1]);
+    y[i] = ADD ? pack_bf16x2(__fadd_rn(a0, b0), __fadd_rn(a1, b1)) : pack_bf16x2(__fsub_rn(a0, b0), __fsub_rn(a1, b1));
+  }
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 // 4 pairs side by side
@@ -58,87 +63,86 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// A head's work: n / 8 pieces of 8 pairs, and the dims that stay in pieces of 16.
-__host__ __device__ __forceinline__ int rope_pieces(int d, int n) { return n / 8 + (d - 2 * n + 15) / 16; }
+// A head's work: n / 8 pieces of 8 pairs, and, out of place, the dims that stay in pieces of 16.
+__host__ __device__ __forceinline__ int rope_pieces(const RopeParams& p) {
+  return p.n / 8 + (p.copies ? (p.d - 2 * p.n + 15) / 16 : 0);
+}
 constexpr int kRopeItems = 4;  // pieces of a thread, all loaded before the first is stored
 __host__ __device__ __forceinline__ long long rope_blocks(const RopeParams& p) {
-  const long long items = (long long)p.T * (p.a.H + p.b.H) * rope_pieces(p.d, p.n);
+  const long long items = (long long)p.T * (p.a.H + p.b.H) * rope_pieces(p);
   return (items + 256 * kRopeItems - 1) / (256 * kRopeItems);
 }
 
 // Block `block` of rope_blocks(): 256 threads, consecutive ones take consecutive pieces of a head, then
-// heads, then rows.
+// heads, then rows.  Bound by memory: a piece is 32 bytes read and written, and its 64 bytes of
+// the table come from L1 for all heads of a row but the first.
 template <bool IL>
 __device__ __forceinline__ void rope_block(const RopeParams& p, long long block) {
-  const int pieces = rope_pieces(p.d, p.n), turn = p.n / 8, heads = p.a.H + p.b.H;
+  const unsigned pieces = rope_pieces(p), turn = p.n / 8, heads = p.a.H + p.b.H;
   const long long items = (long long)p.T * heads * pieces;
   uint4 v0[kRopeItems], v1[kRopeItems];
   __nv_bfloat16* dst[kRopeItems];
-  const float* cs[kRopeItems];  // null: a piece that stays, or none
-  int kind[kRopeItems];         // bits 0, 1: which of the two vectors are stored
-  const int step1 = IL ? 8 : p.n;
+  const float* cs[kRopeItems];  // null: a piece that stays
+  int second[kRopeItems];       // from a piece's first vector to its second; 0: there is none, -1: no piece
 #pragma unroll
   for (int i = 0; i < kRopeItems; ++i) {
     const long long e = (block * kRopeItems + i) * 256 + threadIdx.x;
-    kind[i] = 0;
-    cs[i] = nullptr;
+    second[i] = -1;
     if (e >= items) continue;
-    int piece, h;
+    unsigned piece, h;
     long long t;
-    if (items <= 0x7fffffffLL) {  // 32-bit division
-      const unsigned r = (unsigned)e / (unsigned)pieces;
-      piece = (int)((unsigned)e - r * pieces);
-      t = r / (unsigned)heads;
-      h = (int)(r - (unsigned)t * heads);
+    if (items <= 0xffffffffLL) {  // 32-bit division
+      const unsigned r = (unsigned)e / pieces, tt = r / heads;
+      piece = (unsigned)e - r * pieces;
+      t = tt;
+      h = r - tt * heads;
     } else {
       const long long r = e / pieces;
-      piece = (int)(e - r * pieces);
+      piece = (unsigned)(e - r * pieces);
       t = r / heads;
-      h = (int)(r - t * heads);
+      h = (unsigned)(r - t * heads);
     }
-    const bool q = h < p.a.H;
-    const RopeHeads& m = q ? p.a : p.b;
-    const int hh = q ? h : h - p.a.H;
-    const __nv_bfloat16* x = m.x + (size_t)t * m.xs + (size_t)hh * p.d;
-    __nv_bfloat16* y = m.y + (size_t)t * m.ys + (size_t)hh * p.d;
+    const bool q = h < (unsigned)p.a.H;
+    const unsigned hh = q ? h : h - p.a.H;
+    const __nv_bfloat16* x = (q ? p.a.x : p.b.x) + (size_t)t * (q ? p.a.xs : p.b.xs) + (size_t)hh * p.d;
+    int at;
     if (piece < turn) {
-      const int at = p.first + piece * (IL ? 16 : 8);
-      v0[i] = __ldcs(reinterpret_cast<const uint4*>(x + at));
-      v1[i] = __ldcs(reinterpret_cast<const uint4*>(x + at + step1));
-      dst[i] = y + at;
-      cs[i] = p.table + (size_t)(t % p.table_rows) * 2 * p.n + piece * 8;
-      kind[i] = 3;
-    } else if (x != y) {
+      at = p.first + piece * (IL ? 16 : 8);
+      second[i] = IL ? 8 : p.n;
+      cs[i] = p.table + (size_t)(p.table_rows == p.T ? t : t % p.table_rows) * 2 * p.n + piece * 8;
+    } else {
       // the dims that stay, 16 from the piece's start on: those before `first`, then those behind the pairs
-      const int k = (piece - turn) * 16, end = p.d - 2 * p.n;
-      const int a0 = k < p.first ? k : k + 2 * p.n, a1 = k + 8 < p.first ? k + 8 : k + 8 + 2 * p.n;
-      v0[i] = __ldcs(reinterpret_cast<const uint4*>(x + a0));
-      __stcs(reinterpret_cast<uint4*>(y + a0), v0[i]);
-      if (k + 8 < end) __stcs(reinterpret_cast<uint4*>(y + a1), __ldcs(reinterpret_cast<const uint4*>(x + a1)));
+      const int k = (piece - turn) * 16;
+      at = k < p.first ? k : k + 2 * p.n;
+      second[i] = k + 8 >= p.d - 2 * p.n ? 0 : k + 8 < p.first ? 8 : k + 8 + 2 * p.n - at;
+      cs[i] = nullptr;
     }
+    v0[i] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+    if (second[i] > 0) v1[i] = __ldcs(reinterpret_cast<const uint4*>(x + at + second[i]));
+    dst[i] = (q ? p.a.y : p.b.y) + (size_t)t * (q ? p.a.ys : p.b.ys) + (size_t)hh * p.d + at;
   }
 #pragma unroll
   for (int i = 0; i < kRopeItems; ++i) {
-    if (kind[i] == 0) continue;
-    float c[8], s[8];
-    load8(cs[i], c);
-    load8(cs[i] + p.n, s);
-    if (p.inverse) {
+    if (second[i] < 0) continue;
+    uint4 y0 = v0[i], y1 = v1[i];
+    if (cs[i]) {
+      float c[8], s[8];
+      load8(cs[i], c);
+      load8(cs[i] + p.n, s);
+      if (p.inverse) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = -s[j];
-    }
-    uint4 y0, y1;
-    if constexpr (IL) {
-      y0 = rope_turn_pairs(v0[i], c, s);
-      y1 = rope_turn_pairs(v1[i], c + 4, s + 4);
-    } else {
-      y0 = rope_turn8(v0[i], v1[i], c, s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = -s[j];
-      y1 = rope_turn8(v1[i], v0[i], c, s);
+        for (int j = 0; j < 8; ++j) s[j] = -s[j];
+      }
+      if constexpr (IL) {
+        y0 = rope_turn_pairs(v0[i], c, s);
+        y1 = rope_turn_pairs(v1[i], c + 4, s + 4);
+      } else {
+        y0 = rope_turn8(v0[i], v1[i], c, s);
+        y1 = rope_turn8<true>(v1[i], v0[i], c, s);
+      }
     }
     *reinterpret_cast<uint4*>(dst[i]) = y0;
-    *reinterpret_cast<uint4*>(dst[i] + step1) = y1;
+    if (second[i] > 0) *reinterpret_cast<uint4*>(dst[i] + second[i]) = y1;
   }
 }
 
