@@ -11,6 +11,8 @@ namespace sdpa {
 // dropped), and p times that in 64-bit whole numbers, wrapping, is the angle's fraction of a turn: exact
 // for every position, off only by what the frequency's own 53 bits leave (2^-54 of it).  The
 // frequencies are converted once a block: 64-bit floating point has 2 operations a cycle and SM.
+// Sine and cosine of what is left after whole quarter turns are their power series: on |x| <= pi / 4 the
+// first left-out terms are x^11 / 11! < 2^-29 and x^10 / 10! < 2^-25.
 __global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq, const int* positions, float* table, int T,
                                                          int n, float gain) {
   __shared__ unsigned long long turns[128];
@@ -23,11 +25,17 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq,
   if (r >= rows) return;
   const unsigned long long w = turns[f];
   for (long long t = (long long)blockIdx.x * rows + r; t < T; t += (long long)gridDim.x * rows) {
-    const long long turn = (long long)((unsigned long long)(long long)__ldg(positions + t) * w);
-    float s, c;  // half turns in [-1, 1]
-    sincospif(__ll2float_rn(turn) * 1.08420217248550443401e-19f, &s, &c);
-    table[(size_t)t * 2 * n + f] = gain * c;
-    table[(size_t)t * 2 * n + n + f] = gain * s;
+    const unsigned long long turn = (unsigned long long)(long long)__ldg(positions + t) * w;
+    // the nearest quarter turn, and what is left, in [-2^61, 2^61) of 2^64, as two words
+    const unsigned quarter = (unsigned)(turn >> 61) + 1u >> 1;
+    const long long left = (long long)(turn - ((unsigned long long)quarter << 62));
+    const float x = fmaf((float)(int)(left >> 32), 1.46291807926715970e-9f, (float)(unsigned)left * 3.40611980845280650e-19f);
+    const float q = x * x;  // x in radians: the factors are 2 pi / 2^32 and 2 pi / 2^64
+    const float sx = x + x * q * fmaf(q, fmaf(q, fmaf(q, 2.75573192e-6f, -1.98412698e-4f), 8.33333333e-3f), -1.66666667e-1f);
+    const float cx = fmaf(q, fmaf(q, fmaf(q, fmaf(q, 2.48015873e-5f, -1.38888889e-3f), 4.16666667e-2f), -0.5f), 1.f);
+    const float c = quarter & 1 ? sx : cx, s = quarter & 1 ? cx : sx;
+    table[(size_t)t * 2 * n + f] = (quarter + 1) & 2 ? -gain * c : gain * c;
+    table[(size_t)t * 2 * n + n + f] = quarter & 2 ? -gain * s : gain * s;
   }
 }
 
@@ -40,7 +48,7 @@ int launch_rope_table(const double* inv_freq, const int* positions, float* table
                       cudaStream_t stream) {
   const int rows = 256 / n;
   const int blocks = (T + rows - 1) / rows;
-  rope_table_kernel<<<blocks < 152 * 8 ? blocks : 152 * 8, 256, 0, stream>>>(inv_freq, positions, table, T, n, gain);
+  rope_table_kernel<<<blocks < 152 * 4 ? blocks : 152 * 4, 256, 0, stream>>>(inv_freq, positions, table, T, n, gain);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 

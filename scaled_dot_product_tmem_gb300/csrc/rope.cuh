@@ -67,72 +67,73 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 __host__ __device__ __forceinline__ int rope_pieces(const RopeParams& p) {
   return p.n / 8 + (p.copies ? (p.d - 2 * p.n + 15) / 16 : 0);
 }
-constexpr int kRopeItems = 4;  // pieces of a thread, all loaded before the first is stored
+constexpr int kRopeHeads = 4;  // heads of a thread: h, h + groups, ...; all loaded before the first is stored
+__host__ __device__ __forceinline__ int rope_groups(const RopeParams& p) { return (p.a.H + p.b.H + kRopeHeads - 1) / kRopeHeads; }
 __host__ __device__ __forceinline__ long long rope_blocks(const RopeParams& p) {
-  const long long items = (long long)p.T * (p.a.H + p.b.H) * rope_pieces(p);
-  return (items + 256 * kRopeItems - 1) / (256 * kRopeItems);
+  const long long items = (long long)p.T * rope_groups(p) * rope_pieces(p);
+  return (items + 255) / 256;
 }
 
 // Block `block` of rope_blocks(): 256 threads, consecutive ones take consecutive pieces of a head, then
-// heads, then rows.  Bound by memory: a piece is 32 bytes read and written, and its 64 bytes of
-// the table come from L1 for all heads of a row but the first.
+// heads, then rows.  Bound by memory: a piece is 32 bytes read and written; its place and its 64 bytes
+// of the table serve all heads of a thread.
 template <bool IL>
 __device__ __forceinline__ void rope_block(const RopeParams& p, long long block) {
-  const unsigned pieces = rope_pieces(p), turn = p.n / 8, heads = p.a.H + p.b.H;
-  const long long items = (long long)p.T * heads * pieces;
-  uint4 v0[kRopeItems], v1[kRopeItems];
-  __nv_bfloat16* dst[kRopeItems];
-  const float* cs[kRopeItems];  // null: a piece that stays
-  int second[kRopeItems];       // from a piece's first vector to its second; 0: there is none, -1: no piece
-#pragma unroll
-  for (int i = 0; i < kRopeItems; ++i) {
-    const long long e = (block * kRopeItems + i) * 256 + threadIdx.x;
-    second[i] = -1;
-    if (e >= items) continue;
-    unsigned piece, h;
-    long long t;
-    if (items <= 0xffffffffLL) {  // 32-bit division
-      const unsigned r = (unsigned)e / pieces, tt = r / heads;
-      piece = (unsigned)e - r * pieces;
-      t = tt;
-      h = r - tt * heads;
-    } else {
-      const long long r = e / pieces;
-      piece = (unsigned)(e - r * pieces);
-      t = r / heads;
-      h = (unsigned)(r - t * heads);
-    }
-    const bool q = h < (unsigned)p.a.H;
-    const unsigned hh = q ? h : h - p.a.H;
-    const __nv_bfloat16* x = (q ? p.a.x : p.b.x) + (size_t)t * (q ? p.a.xs : p.b.xs) + (size_t)hh * p.d;
-    int at;
-    if (piece < turn) {
-      at = p.first + piece * (IL ? 16 : 8);
-      second[i] = IL ? 8 : p.n;
-      cs[i] = p.table + (size_t)(p.table_rows == p.T ? t : t % p.table_rows) * 2 * p.n + piece * 8;
-    } else {
-      // the dims that stay, 16 from the piece's start on: those before `first`, then those behind the pairs
-      const int k = (piece - turn) * 16;
-      at = k < p.first ? k : k + 2 * p.n;
-      second[i] = k + 8 >= p.d - 2 * p.n ? 0 : k + 8 < p.first ? 8 : k + 8 + 2 * p.n - at;
-      cs[i] = nullptr;
-    }
-    v0[i] = __ldcs(reinterpret_cast<const uint4*>(x + at));
-    if (second[i] > 0) v1[i] = __ldcs(reinterpret_cast<const uint4*>(x + at + second[i]));
-    dst[i] = (q ? p.a.y : p.b.y) + (size_t)t * (q ? p.a.ys : p.b.ys) + (size_t)hh * p.d + at;
+  const unsigned pieces = rope_pieces(p), turn = p.n / 8, heads = p.a.H + p.b.H, groups = rope_groups(p);
+  const long long e = block * 256 + threadIdx.x;
+  unsigned piece, g;
+  long long t;
+  if (e <= 0xffffffffLL) {  // 32-bit division
+    const unsigned r = (unsigned)e / pieces, tt = r / groups;
+    piece = (unsigned)e - r * pieces;
+    t = tt;
+    g = r - tt * groups;
+  } else {
+    const long long r = e / pieces;
+    piece = (unsigned)(e - r * pieces);
+    t = r / groups;
+    g = (unsigned)(r - t * groups);
   }
+  if (t >= p.T) return;
+  const bool turns = piece < turn;
+  int at, second;  // a piece's first vector, and from it to the second (0: there is none)
+  if (turns) {
+    at = p.first + piece * (IL ? 16 : 8);
+    second = IL ? 8 : p.n;
+  } else {
+    // the dims that stay, 16 from the piece's start on: those before `first`, then those behind the pairs
+    const int k = (piece - turn) * 16;
+    at = k < p.first ? k : k + 2 * p.n;
+    second = k + 8 >= p.d - 2 * p.n ? 0 : k + 8 < p.first ? 8 : k + 8 + 2 * p.n - at;
+  }
+  const long long xa = t * p.a.xs + at, xb = t * p.b.xs + at;
+  uint4 v0[kRopeHeads], v1[kRopeHeads];
 #pragma unroll
-  for (int i = 0; i < kRopeItems; ++i) {
-    if (second[i] < 0) continue;
+  for (int i = 0; i < kRopeHeads; ++i) {
+    const unsigned h = g + i * groups;
+    if (h >= heads) continue;
+    const __nv_bfloat16* x = h < (unsigned)p.a.H ? p.a.x + xa + (size_t)h * p.d : p.b.x + xb + (size_t)(h - p.a.H) * p.d;
+    v0[i] = __ldcs(reinterpret_cast<const uint4*>(x));
+    if (second) v1[i] = __ldcs(reinterpret_cast<const uint4*>(x + second));
+  }
+  float c[8], s[8];
+  if (turns) {
+    const float* cs = p.table + (size_t)(p.table_rows == p.T ? t : t % p.table_rows) * 2 * p.n + piece * 8;
+    load8(cs, c);
+    load8(cs + p.n, s);
+    if (p.inverse) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = -s[j];
+    }
+  }
+  const long long ya = t * p.a.ys + at, yb = t * p.b.ys + at;
+#pragma unroll
+  for (int i = 0; i < kRopeHeads; ++i) {
+    const unsigned h = g + i * groups;
+    if (h >= heads) continue;
+    __nv_bfloat16* y = h < (unsigned)p.a.H ? p.a.y + ya + (size_t)h * p.d : p.b.y + yb + (size_t)(h - p.a.H) * p.d;
     uint4 y0 = v0[i], y1 = v1[i];
-    if (cs[i]) {
-      float c[8], s[8];
-      load8(cs[i], c);
-      load8(cs[i] + p.n, s);
-      if (p.inverse) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = -s[j];
-      }
+    if (turns) {
       if constexpr (IL) {
         y0 = rope_turn_pairs(v0[i], c, s);
         y1 = rope_turn_pairs(v1[i], c + 4, s + 4);
@@ -141,8 +142,8 @@ __device__ __forceinline__ void rope_block(const RopeParams& p, long long block)
         y1 = rope_turn8<true>(v1[i], v0[i], c, s);
       }
     }
-    *reinterpret_cast<uint4*>(dst[i]) = y0;
-    if (second[i] > 0) *reinterpret_cast<uint4*>(dst[i] + second[i]) = y1;
+    *reinterpret_cast<uint4*>(y) = y0;
+    if (second) *reinterpret_cast<uint4*>(y + second) = y1;
   }
 }
 
