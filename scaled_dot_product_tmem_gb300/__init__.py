@@ -1191,6 +1191,10 @@ def attn_rope_table(inv_freq, positions, table, *, gain=1.0, stream=None):
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attn_rope_table(inv_freq, positions, table, gain=gain)
+    _run_rope_table(inv_freq, positions, table, T, n, dev, gain)
+
+
+def _run_rope_table(inv_freq, positions, table, T, n, dev, gain):
     st = _load().attn_rope_table(_p(inv_freq), _p(positions), _p(table), T, n, float(gain), _raw_stream(dev, None))
     if st != ATTN_OK:
         raise AttnError(st, "attn_rope_table")
@@ -1199,12 +1203,15 @@ def attn_rope_table(inv_freq, positions, table, *, gain=1.0, stream=None):
 def rope_table(inv_freq, positions, *, gain=1.0, stream=None):
     """attn_rope_table into a new table [T, 2, n], T the positions' count: made once a step, for
     the rotations of all its layers."""
+    _check(inv_freq, "inv_freq", torch.float64, 1)
+    _check(positions, "positions", torch.int32, positions.dim())
     dev = _device_of(inv_freq, positions)
-    if dev >= 0 and _elsewhere(dev, stream):
+    if _elsewhere(dev, stream):
         with _on(dev, stream):
             return rope_table(inv_freq, positions, gain=gain)
-    table = torch.empty((positions.numel(), 2, inv_freq.numel()), dtype=torch.float32, device=inv_freq.device)
-    attn_rope_table(inv_freq, positions, table, gain=gain)
+    T, n = positions.numel(), inv_freq.shape[0]
+    table = inv_freq.new_empty((T, 2, n), dtype=torch.float32)
+    _run_rope_table(inv_freq, positions, table, T, n, dev, gain)
     return table
 
 
@@ -1216,13 +1223,14 @@ def _row_stride(t, name):
         raise ValueError(f"{name} must be [rows, H, d] or [B, S, H, d], got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    H, d = t.shape[-2:]
-    if t.numel() == 0:
+    shape, strides = t.shape, t.stride()
+    H, d = shape[-2:]
+    if t.is_contiguous() or t.numel() == 0:
         return H * d
-    if (t.stride(-1) != 1 and d > 1) or (t.stride(-2) != d and H > 1):
+    if (strides[-1] != 1 and d > 1) or (strides[-2] != d and H > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     stride, reach = None, 0  # of the innermost rows; what the rows so far span
-    for size, step in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+    for size, step in zip(shape[-3::-1], strides[-3::-1]):
         if size == 1:
             continue
         if stride is None:
@@ -1292,8 +1300,8 @@ def _rope_new(q, k, table, interleaved, first_dim, inverse, stream):
             return _rope_new(q, k, table, interleaved, first_dim, inverse, None)
     H, H_k, d = sizes[1:4]
     strides = [_row_stride(q, "q"), 0 if k is None else _row_stride(k, "k"), H * d, H_k * d]
-    q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    q_out = q.new_empty(q.shape)
+    k_out = None if k is None else k.new_empty(k.shape)
     _run_rope(q, k, table, q_out, k_out, sizes[:5], sizes[5], strides, dev, interleaved, first_dim, inverse)
     return q_out, k_out
 
@@ -1344,13 +1352,8 @@ def rope(q, k, table, *, interleaved=False, first_dim=0):
     return RopeFunction.apply(q, k, table, bool(interleaved), int(first_dim))
 
 
-def attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, *, interleaved=False, first_dim=0,
-                         stream=None):
-    """attn_kv4_append of keys rotated on the way, and the queries rotated in the same launch.
-
-    k, v (bf16 [T, H_kv, d]), cu_seqlens, pool, page_table, seq_lens as for attn_kv4_append; table: fp32
-    [T, 2, n], one row per row of k; q, q_out: bf16 [T, H_q, d], or None.  Results and cache are bit for
-    bit those of attn_rope and attn_kv4_append."""
+def _check_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens):
+    """Checks shared by the appends with a rotation; returns the sizes and strides as the C call takes them."""
     if k.dim() != 3:
         raise ValueError(f"k must be [T, H_kv, d], got shape {tuple(k.shape)}")
     T, _, d = k.shape
@@ -1360,37 +1363,59 @@ def attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens,
         raise ValueError(f"k and v must have the same rows, got {T} and {v.shape[0]}")
     _check_cu(cu_seqlens, "cu_seqlens", B)
     _check(table, "table", torch.float32, 3)
-    if tuple(table.shape[:2]) != (T, 2):
+    if table.shape[0] != T or table.shape[1] != 2:
         raise ValueError(f"table must be [{T}, 2, n], got {tuple(table.shape)}")
-    H_q = qs = qos = 0
+    H_q = qs = 0
     if q is not None:
-        if q.dim() != 3 or q_out is None or q_out.shape != q.shape or q.shape[0] != T:
-            raise ValueError(f"q and q_out must be [{T}, H_q, {d}]")
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError(f"q must be [{T}, H_q, {d}], got {tuple(q.shape)}")
         H_q = q.shape[1]
-        qs, qos = _check_rows(q, "q", H_q, d), _check_rows(q_out, "q_out", H_q, d)
+        qs = _check_rows(q, "q", H_q, d)
+    return (B, T, H_q, H_kv, d, n_pages, page_size, max_pages, table.shape[2]), (qs, ks, vs)
+
+
+def _run_append_rope(q, k, v, table, cu, pool, page_table, seq_lens, q_out, sizes, strides, qos, dev, interleaved, first_dim):
+    st = _load().attn_kv4_append_rope(_p(q), _p(k), _p(v), _p(table), _p(q_out), _p(cu), _p(pool), _p(page_table),
+                                      _p(seq_lens), *sizes, int(first_dim), *strides, qos, int(bool(interleaved)),
+                                      _raw_stream(dev, None))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_kv4_append_rope")
+
+
+def attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, *, interleaved=False, first_dim=0,
+                         stream=None):
+    """attn_kv4_append of keys rotated on the way, and the queries rotated in the same launch.
+
+    k, v (bf16 [T, H_kv, d]), cu_seqlens, pool, page_table, seq_lens as for attn_kv4_append; table: fp32
+    [T, 2, n], one row per row of k; q, q_out: bf16 [T, H_q, d], or None.  Results and cache are bit for
+    bit those of attn_rope and attn_kv4_append."""
+    sizes, strides = _check_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens)
+    qos = 0
+    if q is not None:
+        if q_out is None or q_out.shape != q.shape:
+            raise ValueError(f"q_out must have q's shape {tuple(q.shape)}")
+        qos = _check_rows(q_out, "q_out", q.shape[1], q.shape[2])
     dev = _device_of(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out,
                                         interleaved=interleaved, first_dim=first_dim)
-    st = _load().attn_kv4_append_rope(_p(q), _p(k), _p(v), _p(table), _p(q_out), _p(cu_seqlens), _p(pool), _p(page_table),
-                                      _p(seq_lens), B, T, H_q, H_kv, d, n_pages, page_size, max_pages, table.shape[2],
-                                      int(first_dim), qs, ks, vs, qos, int(bool(interleaved)), _raw_stream(dev, None))
-    if st != ATTN_OK:
-        raise AttnError(st, "attn_kv4_append_rope")
+    _run_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, sizes, strides, qos, dev, interleaved,
+                     first_dim)
 
 
 def kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, *, interleaved=False, first_dim=0, stream=None):
     """attn_kv4_append_rope with the rotated queries in a new tensor, which is returned (None
     without q)."""
-    dev = _device_of(k)
-    if dev >= 0 and _elsewhere(dev, stream):
+    sizes, strides = _check_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens)
+    dev = _device_of(q, k, v, table, cu_seqlens, pool, page_table, seq_lens)
+    if _elsewhere(dev, stream):
         with _on(dev, stream):
             return kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, interleaved=interleaved,
                                    first_dim=first_dim)
-    q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16, device=k.device)
-    attn_kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, interleaved=interleaved,
-                         first_dim=first_dim)
+    q_out = None if q is None else q.new_empty(q.shape)
+    _run_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, sizes, strides,
+                     sizes[2] * sizes[4], dev, interleaved, first_dim)
     return q_out
 
 

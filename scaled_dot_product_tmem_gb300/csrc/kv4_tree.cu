@@ -37,10 +37,9 @@ namespace sdpa {
 namespace {
 
 constexpr int kUnit = 128;    // tokens of a unit
-constexpr int kMaxGrid = 152;  // CTAs, and pairs of partial sums in the workspace
 // a segment's fixed costs, in units
 template <int ROWS>
-constexpr int kSegCost = ROWS == 128 ? 4 : 2;
+constexpr int kSegCost = ROWS == 128 ? 4 : ROWS == 256 ? 2 : 1;
 enum TreeSite { kTreeRawFull = 0xB0, kTreeRawEmpty, kTreeKFull, kTreeKEmpty, kTreeVFull, kTreeVEmpty, kTreeQFull, kTreeQEmpty,
                 kTreeS, kTreeP, kTreeO, kTreeDrain, kTreePartFull, kTreePartEmpty, kTreeShare };
 
@@ -116,8 +115,184 @@ __device__ __forceinline__ int tree_parent(const Kv4TreeParams& p, int row0, int
 // x / g for 0 <= x < 2^20, inv = 1 / g: the fp32 product is off by less than half of 1 / g.
 __device__ __forceinline__ int small_div(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
 
+// This CTA's numbers (a whole warp): the sequence b they begin in, `skip` of its numbers before them, and how
+// many.
+template <int ROWS>
+__device__ __forceinline__ void tree_share(const Kv4TreeParams& p, int& b, long long& skip, long long& left) {
+  const int lane = threadIdx.x % 32;
+  long long total = 0, mine = 0, upto = 0, first = 0;
+  bool found = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    long long carry = 0;
+#pragma unroll 1
+    for (int base = 0; base < p.B && !found; base += 32) {
+      if (pass == 0 || p.B > 32) {
+        mine = 0;
+        if (base + lane < p.B) {
+          const TreeSeq s = tree_seq<ROWS>(p, base + lane);
+          mine = (long long)s.seg * s.blocks * p.c.H_kv;
+        }
+        upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long o = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += o;
+        }
+      }
+      if (pass == 1) {
+        const unsigned holds = __ballot_sync(0xffffffffu, first < carry + upto);
+        if (holds) {
+          const int w = __ffs(holds) - 1;
+          b = base + w;
+          skip = first - carry - __shfl_sync(0xffffffffu, upto - mine, w);
+          found = true;
+        }
+      }
+      carry += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (pass == 0) {
+      total = carry;
+      const long long want = total / (kSegCost<ROWS> + 1) + 1;  // at least a segment's cost and a unit each
+      const int n = (int)min((long long)gridDim.x, want);
+      if (total == 0 || (int)blockIdx.x >= n) break;
+      const long long q = total <= 0x7fffffffLL ? (long long)((unsigned)total / (unsigned)n) : total / n;
+      const int rest = (int)(total - q * n);
+      first = q * blockIdx.x + min((int)blockIdx.x, rest);
+      left = q + ((int)blockIdx.x < rest ? 1 : 0);
+    }
+  }
+}
+
+// The loading warp: walks the CTA's segments, passes their parts on, and streams their units.
+template <class C>
+__device__ __forceinline__ void tree_load(const Kv4TreeParams& p, TreePiece* pieces, uint8_t* smem, uint64_t* raw_full,
+                                          uint64_t* raw_empty, TreePart* parts, uint64_t* part_full, uint64_t* part_empty, int b,
+                                          long long skip, long long left) {
+  constexpr int D = C::DIM;
+  const int lane = threadIdx.x % 32;
+  int* err = p.err;
+  int n_part = 0;
+  bool ok = true;
+  // Lane i copies the block of page i of a unit (whole, also past the sequence's end), if some node sees a token of it: the pages
+  // before a window may be gone from the table.  Its page is looked up one unit ahead.
+  const int P = p.c.page_size, n_pages = kUnit / P, t0 = lane * P;
+  const int block = kv4_block_bytes(P, D), G = p.H_q / p.c.H_kv;
+  const size_t page_bytes = (size_t)block * p.c.H_kv;
+  TreeSeq s{};
+  int hk = 0, rb = 0, n = 0;
+  bool enter = true;          // the sequence's sizes are still to be read
+  int used = 0;               // this CTA's places for pieces that are taken, a bit each
+  bool first = true;
+#pragma unroll 1
+  while (ok) {
+    TreePart t{};
+    bool starts = false, ends = false;
+    if (left > 0) {
+      if (enter) {
+        if (b >= p.B) {  // (the offsets were changed meanwhile)
+          left = 0;
+          continue;
+        }
+        s = tree_seq<C::ROWS>(p, b);
+        if (s.seg == 0) {
+          ++b;
+          continue;
+        }
+        const long long vh = skip <= 0x7fffffffLL ? (long long)((unsigned)skip / (unsigned)s.seg) : skip / s.seg;
+        skip -= vh * s.seg;
+        hk = (int)((unsigned)vh / (unsigned)s.blocks);
+        rb = (int)vh - hk * s.blocks;
+        enter = false;
+      }
+      // the CTA's units [from, to) of the segment
+      const int take = (int)min((long long)s.seg - skip, left);
+      const int from = max((int)skip - kSegCost<C::ROWS>, 0), to = max((int)skip + take - kSegCost<C::ROWS>, 0);
+      left -= take;
+      skip = 0;
+      const int r0 = rb * C::ROWS;  // (rows of a kv head are below 2^31)
+      t.row0 = s.row0, t.n = s.n, t.L = s.L, t.len = s.len, t.lo = s.lo;
+      t.hk = hk;
+      t.node0 = r0 / G;
+      t.rem0 = r0 - t.node0 * G;
+      t.R = min(s.n * G - r0, C::ROWS);
+      // of them those that the row block needs: up to its last node's own token
+      const int last = t.node0 + (t.rem0 + t.R - 1) / G;
+      const int len = (int)min((long long)s.L + last + 1, (long long)s.len);
+      t.unit0 = s.first + from;
+      t.cnt = max(min(to, (len - 1) / kUnit - s.first + 1) - from, 0);
+      t.u_tree = s.L / kUnit;
+      const long long all_see = (long long)s.L + s.n - 1 - p.window;  // from this token on every row sees the prefix
+      t.u_win = p.window >= 0 && all_see > 0 ? (int)((unsigned)all_see / kUnit) + 1 : 0;
+      starts = from == 0;
+      ends = to == s.units;
+      t.slot = starts && ends ? -1 : first ? 0 : 1;
+      if (++rb == s.blocks) {
+        rb = 0;
+        if (++hk == p.c.H_kv) {
+          ++b;
+          enter = true;
+        }
+      }
+      if (from == to) continue;  // only fixed costs
+      first = false;
+      if (t.slot >= 0) {
+        used |= 1 << t.slot;
+        if (lane == 0) pieces[2 * blockIdx.x + t.slot] = TreePiece{t.row0, t.node0, t.rem0, t.R, t.hk, 1, starts, ends};
+      }
+    } else {
+      t.cnt = -1;
+    }
+    const int slot = n_part % kParts;
+    if (n_part >= kParts) ok = tree_wait(&part_empty[slot], (n_part / kParts - 1) & 1, err, kTreePartEmpty);
+    if (!ok) break;
+    if (lane == 0) {
+      parts[slot] = t;
+      mbar_arrive(&part_full[slot]);
+    }
+    ++n_part;
+    __syncwarp();
+    if (t.cnt < 0) break;
+    auto page_of = [&](int k) {
+      const long long tok = (long long)(t.unit0 + k) * kUnit + t0;
+      return k < t.cnt && lane < n_pages && tok < t.len && tok + P > t.lo ? kv4_page(p.c, b - (enter ? 1 : 0), (int)tok) : -2;
+    };
+    int page = page_of(0);
+#pragma unroll 1
+    for (int k = 0; k < t.cnt; ++k, ++n) {
+      const int stage = n % C::STAGES;
+      uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
+      const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (size_t)t.hk * block;
+      const int have = page;
+      page = page_of(k + 1);
+      if (n >= C::STAGES) ok = tree_wait(&raw_empty[stage], (n / C::STAGES - 1) & 1, err, kTreeRawEmpty);
+      if (!ok) break;
+      if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
+        if (have == -1) {
+          for (int o = kv4_off_sk(P, D); o < block; o += 16)
+            *reinterpret_cast<uint4*>(st + lane * block + o) = make_uint4(0u, 0u, 0u, 0u);
+          atomicCAS(p.page_err, 0, p.site);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+      }
+      const uint32_t all = __popc(__ballot_sync(0xffffffffu, have >= 0)) * block;
+      if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], all);
+      __syncwarp();
+      if (have >= 0) bulk_load(st + lane * block, src, block, &raw_full[stage]);
+    }
+  }
+  if (lane < 2 && !(used >> lane & 1)) pieces[2 * blockIdx.x + lane].valid = 0;
+  // every copy this warp started must land before the CTA may exit: wait for the last ones
+  for (int s = 0; s < C::STAGES && s < n; ++s) {
+    const int last = s + (n - 1 - s) / C::STAGES * C::STAGES;
+    tree_wait(&raw_full[s], (last / C::STAGES) & 1, err, kTreeDrain);
+  }
+}
+
 template <int D, bool TWO>
 struct TreeCfg {
+  static constexpr int DIM = D;
   static constexpr int ROWS = TWO ? 256 : 128;  // rows of a block
   static constexpr int BLK = 128 * 128;         // one operand block: 128 rows of 64 bf16
   static constexpr int TILE = BLK * (D / 64);
@@ -257,54 +432,9 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
     tmem_alloc<512>(tmem_slot);
     tmem_relinquish();
   }
-  // This CTA's numbers (the loading warp's): the sequence b they begin in, `skip` of its numbers before them,
-  // and how many.
   int b = 0;
   long long skip = 0, left = 0;
-  if (warp == C::LOAD_WARP) {
-    long long total = 0, mine = 0, upto = 0, first = 0;
-    bool found = false;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      long long carry = 0;
-#pragma unroll 1
-      for (int base = 0; base < p.B && !found; base += 32) {
-        if (pass == 0 || p.B > 32) {
-          mine = 0;
-          if (base + lane < p.B) {
-            const TreeSeq s = tree_seq<C::ROWS>(p, base + lane);
-            mine = (long long)s.seg * s.blocks * p.c.H_kv;
-          }
-          upto = mine;
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += o;
-          }
-        }
-        if (pass == 1) {
-          const unsigned holds = __ballot_sync(0xffffffffu, first < carry + upto);
-          if (holds) {
-            const int w = __ffs(holds) - 1;
-            b = base + w;
-            skip = first - carry - __shfl_sync(0xffffffffu, upto - mine, w);
-            found = true;
-          }
-        }
-        carry += __shfl_sync(0xffffffffu, upto, 31);
-      }
-      if (pass == 0) {
-        total = carry;
-        const long long want = total / (kSegCost<C::ROWS> + 1) + 1;  // at least a segment's cost and a unit each
-        const int n = (int)min((long long)gridDim.x, want);
-        if (total == 0 || (int)blockIdx.x >= n) break;
-        const long long q = total <= 0x7fffffffLL ? (long long)((unsigned)total / (unsigned)n) : total / n;
-        const int rest = (int)(total - q * n);
-        first = q * blockIdx.x + min((int)blockIdx.x, rest);
-        left = q + ((int)blockIdx.x < rest ? 1 : 0);
-      }
-    }
-  }
+  if (warp == C::LOAD_WARP) tree_share<C::ROWS>(p, b, skip, left);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -325,122 +455,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
 
   if (warp >= C::MMA_WARP) regs_less<C::REGS_REST>();
   if (warp == C::LOAD_WARP) {
-    // ---------------------------------------------------------------- loading warp
-    // Walks the CTA's segments, passes their parts on, and streams their units: lane i copies the block of
-    // page i of a unit (whole, also past the sequence's end), if some node sees a token of it: the pages
-    // before a window may be gone from the table.  Its page is looked up one unit ahead.
-    const int P = p.c.page_size, n_pages = kUnit / P, t0 = lane * P;
-    const int block = kv4_block_bytes(P, D), G = p.H_q / p.c.H_kv;
-    const size_t page_bytes = (size_t)block * p.c.H_kv;
-    TreeSeq s{};
-    int hk = 0, rb = 0, n = 0;
-    bool enter = true;          // the sequence's sizes are still to be read
-    int used = 0;               // this CTA's places for pieces that are taken, a bit each
-    bool first = true;
-#pragma unroll 1
-    while (ok) {
-      TreePart t{};
-      bool starts = false, ends = false;
-      if (left > 0) {
-        if (enter) {
-          if (b >= p.B) {  // (the offsets were changed meanwhile)
-            left = 0;
-            continue;
-          }
-          s = tree_seq<C::ROWS>(p, b);
-          if (s.seg == 0) {
-            ++b;
-            continue;
-          }
-          const long long vh = skip <= 0x7fffffffLL ? (long long)((unsigned)skip / (unsigned)s.seg) : skip / s.seg;
-          skip -= vh * s.seg;
-          hk = (int)((unsigned)vh / (unsigned)s.blocks);
-          rb = (int)vh - hk * s.blocks;
-          enter = false;
-        }
-        // the CTA's units [from, to) of the segment
-        const int take = (int)min((long long)s.seg - skip, left);
-        const int from = max((int)skip - kSegCost<C::ROWS>, 0), to = max((int)skip + take - kSegCost<C::ROWS>, 0);
-        left -= take;
-        skip = 0;
-        const int r0 = rb * C::ROWS;  // (rows of a kv head are below 2^31)
-        t.row0 = s.row0, t.n = s.n, t.L = s.L, t.len = s.len, t.lo = s.lo;
-        t.hk = hk;
-        t.node0 = r0 / G;
-        t.rem0 = r0 - t.node0 * G;
-        t.R = min(s.n * G - r0, C::ROWS);
-        // of them those that the row block needs: up to its last node's own token
-        const int last = t.node0 + (t.rem0 + t.R - 1) / G;
-        const int len = (int)min((long long)s.L + last + 1, (long long)s.len);
-        t.unit0 = s.first + from;
-        t.cnt = max(min(to, (len - 1) / kUnit - s.first + 1) - from, 0);
-        t.u_tree = s.L / kUnit;
-        const long long all_see = (long long)s.L + s.n - 1 - p.window;  // from this token on every row sees the prefix
-        t.u_win = p.window >= 0 && all_see > 0 ? (int)((unsigned)all_see / kUnit) + 1 : 0;
-        starts = from == 0;
-        ends = to == s.units;
-        t.slot = starts && ends ? -1 : first ? 0 : 1;
-        if (++rb == s.blocks) {
-          rb = 0;
-          if (++hk == p.c.H_kv) {
-            ++b;
-            enter = true;
-          }
-        }
-        if (from == to) continue;  // only fixed costs
-        first = false;
-        if (t.slot >= 0) {
-          used |= 1 << t.slot;
-          if (lane == 0) pieces[2 * blockIdx.x + t.slot] = TreePiece{t.row0, t.node0, t.rem0, t.R, t.hk, 1, starts, ends};
-        }
-      } else {
-        t.cnt = -1;
-      }
-      const int slot = n_part % kParts;
-      if (n_part >= kParts) ok = tree_wait(&part_empty[slot], (n_part / kParts - 1) & 1, err, kTreePartEmpty);
-      if (!ok) break;
-      if (lane == 0) {
-        parts[slot] = t;
-        mbar_arrive(&part_full[slot]);
-      }
-      ++n_part;
-      __syncwarp();
-      if (t.cnt < 0) break;
-      auto page_of = [&](int k) {
-        const long long tok = (long long)(t.unit0 + k) * kUnit + t0;
-        return k < t.cnt && lane < n_pages && tok < t.len && tok + P > t.lo ? kv4_page(p.c, b - (enter ? 1 : 0), (int)tok) : -2;
-      };
-      int page = page_of(0);
-#pragma unroll 1
-      for (int k = 0; k < t.cnt; ++k, ++n) {
-        const int stage = n % NST;
-        uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
-        const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (size_t)t.hk * block;
-        const int have = page;
-        page = page_of(k + 1);
-        if (n >= NST) ok = tree_wait(&raw_empty[stage], (n / NST - 1) & 1, err, kTreeRawEmpty);
-        if (!ok) break;
-        if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
-          if (have == -1) {
-            for (int o = kv4_off_sk(P, D); o < block; o += 16)
-              *reinterpret_cast<uint4*>(st + lane * block + o) = make_uint4(0u, 0u, 0u, 0u);
-            atomicCAS(p.page_err, 0, p.site);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-        }
-        const uint32_t all = __popc(__ballot_sync(0xffffffffu, have >= 0)) * block;
-        if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], all);
-        __syncwarp();
-        if (have >= 0) bulk_load(st + lane * block, src, block, &raw_full[stage]);
-      }
-    }
-    if (lane < 2 && !(used >> lane & 1)) pieces[2 * blockIdx.x + lane].valid = 0;
-    // every copy this warp started must land before the CTA may exit: wait for the last ones
-    for (int s = 0; s < NST && s < n; ++s) {
-      const int last = s + (n - 1 - s) / NST * NST;
-      tree_wait(&raw_full[s], (last / NST) & 1, err, kTreeDrain);
-    }
+    tree_load<C>(p, pieces, smem, raw_full, raw_empty, parts, part_full, part_empty, b, skip, left);
   } else if (warp >= C::MMA_WARP && warp < C::MMA_WARP + C::ISSUERS) {
     // ---------------------------------------------------------------- issuers of the products
     constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false), idO = idesc_bf16_f32(128, D, false, true);
@@ -970,6 +985,448 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
   }
 }
 
+// ------------------------------------------------------------------------------------------ few rows
+// Up to 32 rows a kv head fill little of a 128-row tile, and its chain S - softmax - P V bounds a unit
+// whatever its rows are.  So few rows are the columns of mma.sync products instead, whose 16 rows are tokens
+// (scores) or head dims (outputs): four computing warps take 32 tokens of every unit each, decode their
+// operands in registers, and keep their own sums.
+// d (16 x 8 fp32) += a (16 x 16 bf16, rows) b (16 x 8 bf16, columns)
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8 x 8 matrix of 16-bit values spread over a warp
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int NT>
+struct FewCfg {
+  static constexpr int DIM = D, ROWS = 8 * NT, WARPS = 4, THREADS = 32 * (WARPS + 1), LOAD_WARP = WARPS;
+  static constexpr int CTAS = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // CTAs an SM
+  static constexpr int STAGES = NT == 4 ? 6 : 3, STAGE = kUnit * D * 9 / 8;
+  static constexpr bool Q_SMEM = NT > 2;  // query fragments that do not fit the registers
+  static constexpr int OFF_RAW = 0;
+  static constexpr int OFF_Q = OFF_RAW + STAGES * STAGE;
+  static constexpr int XS = D + 4;  // row stride of the exchange (bank spread)
+  static constexpr int OFF_X = OFF_Q + (Q_SMEM ? (D / 16) * NT * 32 * 8 : 0);  // [WARPS][ROWS][XS] sums of the four warps
+  static constexpr int OFF_ML = OFF_X + WARPS * ROWS * XS * 4;                 // [WARPS][ROWS] maxima, then denominators
+  static constexpr int OFF_PART = OFF_ML + 2 * WARPS * ROWS * 4;
+  static constexpr int OFF_BAR = OFF_PART + kParts * (int)sizeof(TreePart);
+  static constexpr int SMEM = OFF_BAR + (2 * STAGES + 2 * kParts + 3) * 8 + 128;  // (aligned by the kernel)
+  static constexpr int PART = ROWS * (D + 2);
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
+    kv4_tree_few_kernel(const Kv4TreeParams p, TreePiece* pieces, float* partial) {
+  using C = FewCfg<D, NT>;
+  constexpr int MT = D / 16;  // 16-row tiles of the head dim = k steps of a score
+  constexpr int NST = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* raw_empty = raw_full + NST;
+  uint64_t* part_full = raw_empty + NST;
+  uint64_t* part_empty = part_full + kParts;
+  uint64_t* x_ready = part_empty + kParts;  // every warp's sums of the part are there
+  uint64_t* x_read = x_ready + 1;           // and every warp has read them
+  uint64_t* q_ready = x_read + 1;
+  TreePart* parts = reinterpret_cast<TreePart*>(smem + C::OFF_PART);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int* err = p.err;
+  grid_launch_dependents();  // the join may be set up meanwhile
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], C::WARPS);
+    }
+    for (int s = 0; s < kParts; ++s) {
+      mbar_init(&part_full[s], 1);
+      mbar_init(&part_empty[s], C::WARPS);
+    }
+    mbar_init(x_ready, C::WARPS);
+    mbar_init(x_read, C::WARPS);
+    mbar_init(q_ready, C::WARPS);
+    fence_barrier_init();
+  }
+  int b = 0;
+  long long skip = 0, left = 0;
+  if (warp == C::LOAD_WARP) tree_share<C::ROWS>(p, b, skip, left);
+  __syncthreads();
+  if (warp == C::LOAD_WARP) {
+    tree_load<C>(p, pieces, smem, raw_full, raw_empty, parts, part_full, part_empty, b, skip, left);
+    return;
+  }
+  // ------------------------------------------------------------------ computing warps
+  float* xch = reinterpret_cast<float*>(smem + C::OFF_X);
+  float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* xl = xm + C::WARPS * C::ROWS;
+  [[maybe_unused]] uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
+  const int g = lane / 4, t = lane % 4, G = p.H_q / p.c.H_kv;
+  const float inv_G = 1.f / (float)G, sl2 = p.scale_log2 * kKv4SmallUndo;
+  // where this warp's tokens lie in a stage: tokens warp * 32 + 16 sub on start at token `in` of a
+  // page, and sub 1 follows in the same page or is the next one
+  const int P = p.c.page_size, in = warp * 32 & (P - 1);
+  const int at_page = warp * 32 / P * kv4_block_bytes(P, D);
+  const bool next_page = P == 16;
+  const int d_k = next_page ? kv4_block_bytes(16, D) : 16 * (D / 2), d_sk = next_page ? d_k : 16 * (D / 16);
+  const int off_k = at_page + (in + g) * (D / 2) + t * (D / 8);
+  const int off_sk = at_page + kv4_off_sk(P, D) + (in + g) * (D / 16) + t * (D / 64);
+  // token pairs u = 4 n + t of this warp's tokens: the slot permutation depends on t alone
+  const int off_v = at_page + kv4_off_v(P, D) + (in / 2 + t) * D + (g ^ kv4_slot_xor(t, D)) * (D / 8);
+  const int off_sv = at_page + kv4_off_sv(P, D) + (in / 2 + t) * (D / 8) + 2 * (D == 128 ? g : g / 2);
+  int i = 0, n_part = 0;  // units, parts consumed
+  bool ok = true;
+  for (;; ++n_part) {
+    ok = tree_wait(&part_full[n_part % kParts], (n_part / kParts) & 1, err, kTreePartFull);
+    const TreePart& part = parts[n_part % kParts];
+    if (!ok || part.cnt < 0) break;
+    const int cnt = part.cnt, rem0 = part.rem0, node0 = part.node0, R = part.R, hk = part.hk, row0 = part.row0;
+    // query fragments: lane (g, t) holds row 8 nt + g; dims [t D/4, (t + 1) D/4), in pairs (x, x + 4) of each
+    // 8, the pairing of a code word's nibbles
+    uint32_t qf[C::Q_SMEM ? 1 : MT][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (C::Q_SMEM && nt != warp) continue;  // (every warp stores a quarter; all have left the part before, see x_ready)
+      const int r = 8 * nt + g, node = small_div(rem0 + r, inv_G);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + ((size_t)(row0 + node0 + node) * p.H_q + hk * G + (rem0 + r - node * G)) * D + t * (D / 4));
+#pragma unroll
+      for (int j = 0; j < MT / 2; ++j) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (r < R) w = __ldg(src + j);
+        const uint32_t p0 = __byte_perm(w.x, w.z, 0x5410), p1 = __byte_perm(w.x, w.z, 0x7632);
+        const uint32_t p2 = __byte_perm(w.y, w.w, 0x5410), p3 = __byte_perm(w.y, w.w, 0x7632);
+        if constexpr (C::Q_SMEM) {
+          qs[((2 * j) * NT + nt) * 32 + lane] = make_uint2(p0, p1);
+          qs[((2 * j + 1) * NT + nt) * 32 + lane] = make_uint2(p2, p3);
+        } else {
+          qf[2 * j][nt][0] = p0;
+          qf[2 * j][nt][1] = p1;
+          qf[2 * j + 1][nt][0] = p2;
+          qf[2 * j + 1][nt][1] = p3;
+        }
+      }
+    }
+    if constexpr (C::Q_SMEM) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+      ok = tree_wait(q_ready, n_part & 1, err, kTreeQFull);
+      if (!ok) break;
+    }
+    float acc[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    int unit = part.unit0;
+    const int u_win = part.u_win, u_tree = part.u_tree;
+    for (int k = 0; k < cnt; ++k, ++i, ++unit) {
+      const int stage = i % NST, k0 = unit * kUnit + warp * 32;  // this warp's first token of the unit
+      ok = tree_wait(&raw_full[stage], (i / NST) & 1, err, kTreeRawFull);
+      if (!ok) break;
+      const bool edge = unit < u_win || unit >= u_tree;  // some token is hidden from some row
+      const int len = part.len;
+      if (!edge || (k0 < len && k0 + 32 > part.lo)) {
+        const uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
+        float s[2][NT][4];
+        // ---- scores of 2 x 16 tokens: lane (g, t) decodes tokens g, g + 8, its quarter of the dims
+        uint32_t wk[2][2][MT / 2], sk[2][2];  // [half of 16][token g or g + 8]
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint8_t* kc = st + off_k + sub * d_k + 8 * f * (D / 2);
+            const uint8_t* ks = st + off_sk + sub * d_sk + 8 * f * (D / 16);
+            if constexpr (D == 128) {
+              *reinterpret_cast<uint4*>(wk[sub][f]) = *reinterpret_cast<const uint4*>(kc);
+              sk[sub][f] = scale_pair(*reinterpret_cast<const unsigned short*>(ks));
+            } else {
+              *reinterpret_cast<uint2*>(wk[sub][f]) = *reinterpret_cast<const uint2*>(kc);
+              sk[sub][f] = scale_pair(ks[0]);
+            }
+          }
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[sub][nt][e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < MT / 2; ++j)  // a word: 8 dims, two k steps; 16 dims share a scale
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const Kv4Small k2 = j < 2 ? scales_low(sk[sub][f]) : scales_high(sk[sub][f]);
+              const uint4 v = decode8(wk[sub][f][j], k2);
+              a[f][0] = v.x, a[f][1] = v.y, a[f][2] = v.z, a[f][3] = v.w;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint2 q0, q1;
+              if constexpr (C::Q_SMEM) {
+                q0 = qs[((2 * j) * NT + nt) * 32 + lane];
+                q1 = qs[((2 * j + 1) * NT + nt) * 32 + lane];
+              } else {
+                q0 = make_uint2(qf[2 * j][nt][0], qf[2 * j][nt][1]);
+                q1 = make_uint2(qf[2 * j + 1][nt][0], qf[2 * j + 1][nt][1]);
+              }
+              mma_16816(s[sub][nt], a[0][0], a[1][0], a[0][1], a[1][1], q0.x, q0.y);
+              mma_16816(s[sub][nt], a[0][2], a[1][2], a[0][3], a[1][3], q1.x, q1.y);
+            }
+          }
+        // ---- softmax: s[sub][nt][e + 2 f] is token 16 sub + g + 8 f, row 8 nt + 2 t + e.  The running
+        // maximum (in log2 units) moves only when some score passes it by 2^8
+        uint32_t keep[2][2] = {{0xFFFFu, 0xFFFFu}, {0xFFFFu, 0xFFFFu}};  // the V scales that count, as read below
+        if (edge) {
+          uint32_t sees = 0u;  // lane r: the warp's 32 tokens that row r sees
+          if (lane < C::ROWS) {
+            const int node = node0 + small_div(rem0 + min(lane, R - 1), inv_G), L = part.L, a0 = k0 - L, end = len - L;
+            int lo = 0;
+            if (p.window >= 0) {
+              int depth = node;
+              if (p.parents) {
+                depth = 0;
+                for (int a = tree_parent(p, row0, node); a >= 0; a = tree_parent(p, row0, a)) ++depth;
+              }
+              lo = depth >= p.window ? L : max(L - (p.window - depth), 0);
+            }
+            auto range = [&](int from, int to) {
+              from = max(from, 0);
+              to = min(to, 32);
+              if (from < to) sees |= (0xffffffffu << from) & (0xffffffffu >> (32 - to));
+            };
+            range(lo - k0, L - k0);
+            if (!p.parents) {
+              range((p.window >= 0 && node > p.window ? node - p.window : 0) - a0, min(node + 1, end) - a0);
+            } else {
+              int step = 0;
+              for (int a = node; a >= max(a0, 0) && (p.window < 0 || step <= p.window); a = tree_parent(p, row0, a), ++step)
+                if (a - a0 < 32 && a < end) sees |= 1u << (a - a0);
+            }
+          }
+          __syncwarp();
+          // A token that no row sees adds nothing, whatever its bytes are.  One with a NaN scale adds
+          // nothing either: rows that do not see it have P = 0, but 0 times NaN is NaN.  The rows that see it
+          // get their NaN here, and keep it.
+          uint32_t nans = 0u;  // eighth g of the warp's 32 tokens, a bit each
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const int u = 8 * sub + 4 * f + t, j = k0 + 2 * u;
+              uint32_t k2 = 0xFFFFu;
+              if (j >= len || j < part.lo) k2 &= 0xFF00u;
+              if (j + 1 >= len || j + 1 < part.lo) k2 &= 0x00FFu;
+              const uint32_t two = k2 & *reinterpret_cast<const unsigned short*>(st + off_sv + sub * d_sk + 4 * f * (D / 8));
+              if ((two & 0x00F8u) == 0x00F8u) {
+                nans |= 1u << (2 * u);
+                k2 &= 0xFF00u;
+              }
+              if ((two & 0xF800u) == 0xF800u) {
+                nans |= 2u << (2 * u);
+                k2 &= 0x00FFu;
+              }
+              keep[sub][f] = k2;
+            }
+          nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
+          nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t row = __shfl_sync(0xffffffffu, sees, 8 * nt + 2 * t + e);
+              if (nans & row) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[mt][nt][e] = acc[mt][nt][e + 2] = NAN;
+              }
+#pragma unroll
+              for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                  if (!(row >> (16 * sub + g + 8 * f) & 1u)) s[sub][nt][e + 2 * f] = -INFINITY;
+            }
+        }
+        float mx[NT][2];
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx[nt][e] = sl2 * fmaxf(fmax3(s[0][nt][e], s[0][nt][e + 2], s[1][nt][e]), s[1][nt][e + 2]);
+            grow |= mx[nt][e] > m[nt][e] + 8.f;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1)
+                mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
+              const float mn = fmaxf(m[nt][e], mx[nt][e]);
+              const float alpha = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
+              m[nt][e] = mn;
+              l[nt][e] *= alpha;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                acc[mt][nt][e] *= alpha;
+                acc[mt][nt][e + 2] *= alpha;
+              }
+            }
+        }
+        uint32_t pb[2][NT][2];  // P as the column operand: rows of the product = tokens
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const float x0 = ex2(fmaf(s[sub][nt][2 * f], sl2, m0));
+              const float x1 = ex2(fmaf(s[sub][nt][2 * f + 1], sl2, m1));
+              l[nt][0] += x0;
+              l[nt][1] += x1;
+              pb[sub][nt][f] = transpose_8x8(pack_bf16x2(x0, x1));
+            }
+        }
+        // ---- outputs: lane (g, t) decodes eighth g of the head dim of token pairs t and t + 4
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          uint32_t lo[2][MT / 4], hi[2][MT / 4];  // [pair][word]: both tokens' nibbles 0-3, 4-7
+          Kv4Small kv[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint8_t* va = st + off_v + sub * d_k + 4 * f * D;
+            const uint32_t two = *reinterpret_cast<const unsigned short*>(st + off_sv + sub * d_sk + 4 * f * (D / 8));
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(va);  // token 2u: x, y; token 2u + 1: z, w
+              lo[f][0] = __byte_perm(w.x, w.z, 0x5410);
+              hi[f][0] = __byte_perm(w.x, w.z, 0x7632);
+              lo[f][1] = __byte_perm(w.y, w.w, 0x5410);
+              hi[f][1] = __byte_perm(w.y, w.w, 0x7632);
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(va);
+              lo[f][0] = __byte_perm(w.x, w.y, 0x5410);
+              hi[f][0] = __byte_perm(w.x, w.y, 0x7632);
+            }
+            kv[f] = small_scales(scale_pair(two & keep[sub][f]));
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            // rows g and g + 8 of the tile: dims x and x + D/16 of the eighth
+            uint32_t a[4];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const int e = mt % 4;  // nibble of the half
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t* half = D == 128 ? (mt < 4 ? lo[f] : hi[f]) + (r * MT / 8) : r == 0 ? lo[f] : hi[f];
+                const uint32_t w = *half >> (e < 2 ? 0 : 8);
+                a[2 * f + r] = e % 2 == 0 ? decode_small_lo(w, kv[f]) : decode_small_hi(w, kv[f]);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(acc[mt][nt], a[0], a[1], a[2], a[3], pb[sub][nt][0], pb[sub][nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage: it may be filled again
+      if (lane == 0) mbar_arrive(&raw_empty[stage]);
+    }
+    if (!ok) break;
+
+    // ---- the warps' sums become one: each leaves its own, with its maxima and denominators
+    if (n_part > 0) ok = tree_wait(x_read, (n_part - 1) & 1, err, kTreeShare);
+    if (!ok) break;
+    {
+      float* mine = xch + warp * C::ROWS * C::XS;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * nt + 2 * t + e;
+          float ll = l[nt][e];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
+          if (g == 0) {
+            xm[warp * C::ROWS + r] = m[nt][e];
+            xl[warp * C::ROWS + r] = ll;
+          }
+#pragma unroll
+          for (int q = 0; q < MT / 2; ++q) {
+            // D/8 consecutive dims of row r: tiles 0.. give the first half, their + 8 rows the second
+            constexpr int QH = MT / 4;
+            const int mt = 4 * (q % QH), hf = q / QH;
+            *reinterpret_cast<float4*>(mine + r * C::XS + g * (D / 8) + 4 * q) =
+                make_float4(acc[mt][nt][e + 2 * hf], acc[mt + 1][nt][e + 2 * hf], acc[mt + 2][nt][e + 2 * hf],
+                            acc[mt + 3][nt][e + 2 * hf]);
+          }
+        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x_ready);
+    ok = tree_wait(x_ready, n_part & 1, err, kTreeShare);
+    if (!ok) break;
+    // ---- the whole of a segment: outputs; a piece of it: partial sums
+    const bool whole = part.slot < 0;
+    float* slot = partial + ((size_t)2 * blockIdx.x + max(part.slot, 0)) * C::PART;
+    for (int r = warp; r < R; r += C::WARPS) {
+      float mm = xm[r], ll = 0.f, f[C::WARPS];
+#pragma unroll
+      for (int w = 1; w < C::WARPS; ++w) mm = fmaxf(mm, xm[w * C::ROWS + r]);
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) {
+        const float mw = xm[w * C::ROWS + r], lw = xl[w * C::ROWS + r];
+        f[w] = mw == -INFINITY ? 0.f : ex2(mw - mm);
+        ll += mw == -INFINITY ? lw : lw * f[w];  // (no key: lw is 0, or a NaN that has to stay)
+      }
+      const int node = small_div(rem0 + r, inv_G), h = hk * G + rem0 + r - node * G, row = row0 + node0 + node;
+      TreeSums z{1.f, 0.f};
+      if (whole) z = tree_finish(p, h, mm, ll);
+#pragma unroll
+      for (int x = 2 * lane; x < D; x += 64) {
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float2 o = *reinterpret_cast<const float2*>(xch + (w * C::ROWS + r) * C::XS + x);
+          v.x = fmaf(o.x, f[w], v.x);
+          v.y = fmaf(o.y, f[w], v.y);
+        }
+        if (whole) *reinterpret_cast<uint32_t*>(p.o + ((size_t)row * p.H_q + h) * D + x) = pack_bf16x2(v.x * z.mul, v.y * z.mul);
+        else *reinterpret_cast<float2*>(slot + r * D + x) = v;
+      }
+      if (lane == 0) {
+        if (!whole) {
+          slot[C::ROWS * D + r] = mm;
+          slot[C::ROWS * D + C::ROWS + r] = ll;
+        } else if (p.lse) {
+          p.lse[(size_t)h * p.T + row] = z.lse;
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(x_read);
+      mbar_arrive(&part_empty[n_part % kParts]);
+    }
+  }
+}
+
 // Joins the pieces of every segment that spans several CTAs, in CTA order: block (c, y) the segment whose
 // first piece is CTA c's, if there is one, a warp a row.  Then the rows without a token, and on request
 // those of no sequence.
@@ -986,12 +1443,12 @@ __global__ void __launch_bounds__(256) kv4_tree_join_kernel(const Kv4TreeParams 
     return TreePiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   };
   auto store = [&](int t, int h, const float (&a)[E], const TreeSums& z) {
-    // lane's columns back to their dims: of 8 columns 0 .. 7 the dims 0 4 1 5 2 6 3 7
+    // of 8 columns 0 .. 7 the tiles' forms hold the dims 0 4 1 5 2 6 3 7
     __nv_bfloat16* o = p.o + ((size_t)t * p.H_q + h) * D;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int col = lane * E + e, c = col & 7;
-      o[(col & ~7) + (c >> 1) + (c & 1) * 4] = __float2bfloat16(a[e] * z.mul);
+      o[ROWS >= 128 ? (col & ~7) + (c >> 1) + (c & 1) * 4 : col] = __float2bfloat16(a[e] * z.mul);
     }
     if (lane == 0 && p.lse) p.lse[(size_t)h * p.T + t] = z.lse;
   };
@@ -1047,42 +1504,65 @@ __global__ void __launch_bounds__(256) kv4_tree_join_kernel(const Kv4TreeParams 
 
 namespace {
 
+constexpr int kMaxGrid = 152 * 3;  // CTAs, each with two places for partial sums
 constexpr size_t kPieceBytes = (kMaxGrid * 2 * sizeof(TreePiece) + 255) / 256 * 256;
 
-template <int D, bool TWO>
-int launch_t(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
-  using C = TreeCfg<D, TWO>;
-  if (!allow_smem<kv4_tree_kernel<D, TWO>>(C::SMEM)) return -1;
-  static std::atomic<int> sms[64];  // SMs of each device
+// SMs of the current device (0: CUDA cannot tell), looked up once.
+int device_sms() {
+  static std::atomic<int> sms[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = sms[dev].load(std::memory_order_acquire);
   if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return -1;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 0;
     sms[dev].store(n, std::memory_order_release);
   }
-  const int grid = std::min(n, kMaxGrid);
-  TreePiece* pieces = static_cast<TreePiece*>(workspace);
-  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPieceBytes);
-  if (launch_kernel(kv4_tree_kernel<D, TWO>, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, false, p, pieces, partial) != 0)
-    return -1;
-  return launch_kernel(kv4_tree_join_kernel<D, C::ROWS>, dim3((unsigned)grid, 8), 256, 0, stream, true, p,
-                       (const TreePiece*)pieces, (const float*)partial);
+  return n;
 }
 
-// Two row tiles a block where the sequences have more than 128 rows a kv head on average.
-bool two_tiles(int B, int T, int H_q, int H_kv) { return B > 0 && (long long)T * (H_q / H_kv) > 128LL * B; }
+template <auto KERN, class C>
+int launch_t(const Kv4TreeParams& p, int ctas, void* workspace, cudaStream_t stream) {
+  const int n = device_sms();
+  if (n == 0 || !allow_smem<KERN>(C::SMEM)) return -1;
+  const int grid = std::min(n, 152) * ctas;
+  TreePiece* pieces = static_cast<TreePiece*>(workspace);
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPieceBytes);
+  if (launch_kernel(KERN, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, false, p, pieces, partial) != 0) return -1;
+  return launch_kernel(kv4_tree_join_kernel<C::DIM, C::ROWS>, dim3((unsigned)grid, ctas > 1 ? 2 : 8), 256, 0, stream, true, p,
+                       (const TreePiece*)pieces, (const float*)partial);
+}
+template <int D, int NT>
+int launch_few(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
+  using C = FewCfg<D, NT>;
+  return launch_t<kv4_tree_few_kernel<D, NT>, C>(p, C::CTAS, workspace, stream);
+}
+template <int D, bool TWO>
+int launch_tiles(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
+  return launch_t<kv4_tree_kernel<D, TWO>, TreeCfg<D, TWO>>(p, 1, workspace, stream);
+}
+
+// Rows of a block, by the sequences' rows a kv head on average: a block of more than a sequence has works on
+// rows that do not exist, a smaller one decodes the cache again for the rest.
+int block_rows(int B, int T, int H_q, int H_kv) {
+  const long long rows = (long long)T * (H_q / H_kv), n = B > 0 ? B : 1;
+  return rows <= 8 * n ? 8 : rows <= 16 * n ? 16 : rows <= 32 * n ? 32 : rows <= 128 * n ? 128 : 256;
+}
 
 }  // namespace
 
 size_t kv4_tree_workspace(int B, int T, int H_q, int H_kv, int d) {
-  return kPieceBytes + (size_t)kMaxGrid * 2 * (two_tiles(B, T, H_q, H_kv) ? 256 : 128) * (d + 2) * sizeof(float);
+  const int rows = block_rows(B, T, H_q, H_kv), ctas = rows == 8 ? 3 : rows == 16 ? 2 : 1;
+  return kPieceBytes + (size_t)152 * ctas * 2 * rows * (d + 2) * sizeof(float);
 }
 
 int launch_kv4_tree(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
-  const bool two = two_tiles(p.B, p.T, p.H_q, p.c.H_kv);
-  if (p.c.d == 128) return two ? launch_t<128, true>(p, workspace, stream) : launch_t<128, false>(p, workspace, stream);
-  return two ? launch_t<64, true>(p, workspace, stream) : launch_t<64, false>(p, workspace, stream);
+  switch (block_rows(p.B, p.T, p.H_q, p.c.H_kv)) {
+    case 8: return p.c.d == 128 ? launch_few<128, 1>(p, workspace, stream) : launch_few<64, 1>(p, workspace, stream);
+    case 16: return p.c.d == 128 ? launch_few<128, 2>(p, workspace, stream) : launch_few<64, 2>(p, workspace, stream);
+    case 32: return p.c.d == 128 ? launch_few<128, 4>(p, workspace, stream) : launch_few<64, 4>(p, workspace, stream);
+    case 128: return p.c.d == 128 ? launch_tiles<128, false>(p, workspace, stream) : launch_tiles<64, false>(p, workspace, stream);
+    default: return p.c.d == 128 ? launch_tiles<128, true>(p, workspace, stream) : launch_tiles<64, true>(p, workspace, stream);
+  }
 }
 
 }  // namespace sdpa

@@ -95,6 +95,10 @@ CASES = [  # lens, nodes, H, H_kv, d, page
     ([77, 500, 130], [12, 1, 64], 6, 2, 64, 128),
     ([1500], [3], 3, 3, 128, 128),
     ([2, 700], [65, 20], 14, 2, 128, 16),                 # 7 heads a group: rows of no power of two
+    ([400, 10, 0, 129, 77, 1000], [30, 1, 1, 1, 1, 1], 1, 1, 64, 16),   # 6 rows a sequence on average, 30 of one
+    ([400, 10, 0, 129, 77], [20, 1, 1, 1, 1], 4, 2, 128, 32),           # 10 on average, 40 of one
+    ([40, 3000, 256], [9, 2, 6], 15, 3, 128, 64),                       # 28 on average, 45 of one
+    ([127, 2000], [3, 8], 6, 2, 64, 128),
 ]
 
 
@@ -105,6 +109,17 @@ def test_tree_parity(lens, nodes, H, H_kv, d, page, chain):
     o, lse = t.call()
     _clean()
     t.check(o, lse)
+
+
+# heads a kv head such that a sequence has 8, 16, 32, 128 and more rows on average: the kernels' forms
+@pytest.mark.parametrize("G", [1, 2, 4, 14, 40])
+@pytest.mark.parametrize("window", [0, 1, 3, 50, 128, 300, 2 ** 31 - 1])
+def test_windows(window, G):
+    lens, nodes = [0, 40, 333, 128, 700, 510], [9, 8, 7, 1, 12, 4]
+    t = Trees(lens, nodes, 2 * G, 2, 64 if window % 2 else 128, 16, seed=window % 97)
+    o, lse = t.call(window=window)
+    _clean()
+    t.check(o, lse, window=window)
 
 
 @pytest.mark.parametrize("window", [0, 1, 3, 50, 128, 300, 2 ** 31 - 1])
@@ -130,11 +145,12 @@ def test_many_sequences(window):
     t.check(o, lse, window=window)
 
 
-def test_long_context_is_split():
+@pytest.mark.parametrize("nodes,H", [([33, 2], 4), ([4, 1], 3), ([9, 2], 2), ([9, 3], 4), ([60, 9], 8)])
+def test_long_context_is_split(nodes, H):
     """A long prefix (its units spread over many CTAs) with a large score in one far token."""
     def edit(t, k, v):
         k[77] *= 4.0
-    t = Trees([20000, 3], [33, 2], 4, 1, 128, 64, seed=9, edit=edit)
+    t = Trees([20000, 3], nodes, H, 1, 128, 64, seed=9, edit=edit)
     o, lse = t.call()
     _clean()
     t.check(o, lse)
@@ -174,11 +190,13 @@ def test_parents_out_of_range_are_roots():
     _clean()
 
 
+@pytest.mark.parametrize("H", [2, 4, 8, 16, 64])  # 6 to 192 rows a kv head
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("side", ["k", "v"])
-def test_nan_tokens_reach_only_their_descendants(side):
+def test_nan_tokens_reach_only_their_descendants(side, d, H):
     """Node 1 and a prefix token before the window are NaN (held as NaN in 16 dims): nodes that do not see
     them are exact; those that do get NaN, for a value in its dims, for a key everywhere."""
-    L, n, d = 140, 6, 64
+    L, n = 140, 6
     par = [-1, 0, 0, 1, 2, -1]
 
     def edit(t, k, v):
@@ -186,7 +204,7 @@ def test_nan_tokens_reach_only_their_descendants(side):
         x[L + 1, :, 20] = float("nan")
         x[3, :, 20] = float("inf")
 
-    t = Trees([L], [n], 4, 2, d, 16, edit=edit)
+    t = Trees([L], [n], H, 2, d, 16, edit=edit)
     t.par = par
     o, lse = t.call(window=100)
     _clean()
@@ -205,25 +223,28 @@ def test_nan_tokens_reach_only_their_descendants(side):
     assert np.all(np.abs(o[ok] - ro[ok]) <= 2.0 ** -8 * (a[ok] + np.abs(ro[ok])) + 2.0 ** -14 * a[ok])
 
 
-def test_a_nan_prefix_token_reaches_every_node():
+@pytest.mark.parametrize("H", [2, 10, 30, 100])
+def test_a_nan_prefix_token_reaches_every_node(H):
     def edit(t, k, v):
         v[10, :, 0] = float("nan")
-    t = Trees([300], [3], 2, 1, 64, 64, edit=edit)
+    t = Trees([300], [3], H, 1, 64, 64, edit=edit)
     o, lse = t.call()
     assert torch.isnan(o[:, :, :16]).all() and torch.isfinite(o[:, :, 16:]).all() and torch.isfinite(lse).all()
 
 
-def test_nan_query_rows_stay_alone():
-    t = Trees([200], [4], 4, 2, 128, 64)
+@pytest.mark.parametrize("H", [4, 12, 40, 160])
+def test_nan_query_rows_stay_alone(H):
+    t = Trees([200], [4], H, 2, 128, 64)
     t.q[2, 1, 5] = float("nan")
     o, lse = t.call()
     bad = torch.isnan(o).all(-1)
     assert bad[2, 1] and torch.isnan(lse[1, 2]) and int(bad.sum()) == 1 and int(torch.isnan(lse).sum()) == 1
 
 
-def test_missing_pages_read_as_zeros():
+@pytest.mark.parametrize("H", [1, 2, 6, 20, 60])
+def test_missing_pages_read_as_zeros(H):
     sdpa = _sdpa()
-    t = Trees([100], [5], 2, 1, 64, 16)
+    t = Trees([100], [5], H, 1, 64, 16)
     t.table[0, 2] = -1
     t.table[0, 4] = 10 ** 6
     o, lse = t.call()
@@ -241,8 +262,9 @@ def test_missing_pages_read_as_zeros():
     t.check(o, lse, window=9)
 
 
-def test_tokens_past_the_table_do_not_exist():
-    t = Trees([60], [8], 2, 1, 64, 16)
+@pytest.mark.parametrize("H", [1, 2, 4, 9, 40])
+def test_tokens_past_the_table_do_not_exist(H):
+    t = Trees([60], [8], H, 1, 64, 16)
     t.table = t.table[:, :4].contiguous()   # 64 tokens: nodes 4.. have no token
     o, lse = t.call()
     _clean()
