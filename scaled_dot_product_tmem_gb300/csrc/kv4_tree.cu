@@ -39,7 +39,7 @@ namespace {
 constexpr int kUnit = 128;    // tokens of a unit
 // a segment's fixed costs, in units
 template <int ROWS>
-constexpr int kSegCost = ROWS == 128 ? 4 : ROWS == 256 ? 2 : 1;
+constexpr int kSegCost = ROWS == 8 ? 1 : ROWS == 16 ? 2 : ROWS == 256 ? 3 : 4;
 enum TreeSite { kTreeRawFull = 0xB0, kTreeRawEmpty, kTreeKFull, kTreeKEmpty, kTreeVFull, kTreeVEmpty, kTreeQFull, kTreeQEmpty,
                 kTreeS, kTreeP, kTreeO, kTreeDrain, kTreePartFull, kTreePartEmpty, kTreeShare };
 
@@ -153,7 +153,7 @@ __device__ __forceinline__ void tree_share(const Kv4TreeParams& p, int& b, long 
     }
     if (pass == 0) {
       total = carry;
-      const long long want = total / (kSegCost<ROWS> + 1) + 1;  // at least a segment's cost and a unit each
+      const long long want = total / 2 + 1;
       const int n = (int)min((long long)gridDim.x, want);
       if (total == 0 || (int)blockIdx.x >= n) break;
       const long long q = total <= 0x7fffffffLL ? (long long)((unsigned)total / (unsigned)n) : total / n;
@@ -332,14 +332,14 @@ __device__ __forceinline__ void regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// bits [from, to) of the 128 tokens of a unit
+// sets bits [from, to) of the 128 tokens of a unit
 __device__ __forceinline__ void set_range(uint32_t (&vis)[4], int from, int to) {
-  from = max(from, 0);
-  to = min(to, kUnit);
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const int a = max(from - 32 * w, 0), z = min(to - 32 * w, 32);
-    if (a < z) vis[w] |= (0xffffffffu << a) & (0xffffffffu >> (32 - z));
+    const int a = min(max(from - 32 * w, 0), 32), z = min(max(to - 32 * w, 0), 32);
+    // (funnel shifts: a shift by 32 leaves nothing)
+    const uint32_t below_a = __funnelshift_lc(0xffffffffu, 0u, a), below_z = __funnelshift_lc(0xffffffffu, 0u, z);
+    vis[w] |= below_z & ~below_a;
   }
 }
 
@@ -930,30 +930,39 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         __nv_bfloat16* o = p.o + ((size_t)(part.row0 + node) * p.H_q + h) * D;
         // where both warpgroups have sums, each stores half of the dims
         const int c_first = both ? t * (D / 2) : 0, c_end = both ? c_first + D / 2 : D;
+        constexpr int EC = TWO ? 32 : 16;  // columns at a time (two tiles' sums of 32 would not fit the registers)
 #pragma unroll 1
-        for (int c0 = c_first; c0 < c_end; c0 += 16) {
-          uint32_t a[16], b2[16];
-          float v[16];
-          if (cnt > 0) tmem_ld16(aO + c0, a);
-          if (both) tmem_ld16(lane_addr + (1 - t) * 256 + 128 + c0, b2);
+        for (int c0 = c_first; c0 < c_end; c0 += EC) {
+          uint32_t a[EC], b2[TWO ? 1 : EC];
+          if constexpr (TWO) {
+            if (cnt > 0) tmem_ld32(aO + c0, a);
+          } else {
+            if (cnt > 0) tmem_ld16(aO + c0, a);
+            if (both) tmem_ld16(lane_addr + (1 - t) * 256 + 128 + c0, b2);
+          }
           tmem_ld_wait();
+          float v[EC];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < EC; ++c) {
             v[c] = cnt > 0 ? __uint_as_float(a[c]) * f_own : 0.f;
-            if (both) v[c] = fmaf(__uint_as_float(b2[c]), f_other, v[c]);
+            if constexpr (!TWO) {
+              if (both) v[c] = fmaf(__uint_as_float(b2[c]), f_other, v[c]);
+            }
           }
-          if (nans >> (c0 / 16) & 1u) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = NAN;
-          }
+          for (int q = 0; q < EC / 16; ++q)
+            if (nans >> (c0 / 16 + q) & 1u) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) v[16 * q + c] = NAN;
+            }
           if (row_ok && whole) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] *= z.mul;
-            *reinterpret_cast<uint4*>(o + c0) = ordered8(v);
-            *reinterpret_cast<uint4*>(o + c0 + 8) = ordered8(v + 8);
+            for (int c = 0; c < EC; ++c) v[c] *= z.mul;
+#pragma unroll
+            for (int q = 0; q < EC / 8; ++q) *reinterpret_cast<uint4*>(o + c0 + 8 * q) = ordered8(v + 8 * q);
           } else if (row_ok) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < EC / 4; ++q)
               *reinterpret_cast<float4*>(slot + rr * D + c0 + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
         }
@@ -1428,12 +1437,14 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
 }
 
 // Joins the pieces of every segment that spans several CTAs, in CTA order: block (c, y) the segment whose
-// first piece is CTA c's, if there is one, a warp a row.  Then the rows without a token, and on request
-// those of no sequence.
+// first piece is CTA c's, if there is one.  WPR warps a row (few rows, whose segments span more CTAs): warp w
+// takes pieces w, w + WPR, ..., then their sums are added in order.  Then the rows without a token, and on
+// request those of no sequence.
 // Launched while the kernel before it runs: it waits for that kernel's end before it reads a piece.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) kv4_tree_join_kernel(const Kv4TreeParams p, const TreePiece* pieces, const float* partial) {
-  constexpr int PART = ROWS * (D + 2), E = D / 32;
+  constexpr int PART = ROWS * (D + 2), E = D / 32, WPR = ROWS <= 32 ? 64 / ROWS : 1, RPB = 8 / WPR;  // warps a row, rows a block
+  __shared__ float red[2][8], sums[WPR > 1 ? 8 : 1][D];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = p.H_q / p.c.H_kv;
   grid_wait();
   // (ordinary loads: the pieces were written while this kernel was already set up)
@@ -1457,32 +1468,67 @@ __global__ void __launch_bounds__(256) kv4_tree_join_kernel(const Kv4TreeParams 
   const bool second = p1.valid != 0;
   const TreePiece f = second ? p1 : p0;
   if (f.valid && f.starts) {
-    int last = c;  // the CTA of the last piece
-    for (bool end = f.ends; !end && last + 1 < (int)gridDim.x;) end = piece(2 * ++last).ends;
-    for (int r = blockIdx.y * 8 + warp; r < f.R; r += gridDim.y * 8) {
+    int last = c;  // the CTA of the last piece: the next whose first piece is its segment's end
+    if (!f.ends) {
+      for (int base = c + 1; base < (int)gridDim.x; base += 32) {
+        const int i = min(base + lane, (int)gridDim.x - 1);
+        const unsigned end = __ballot_sync(0xffffffffu, pieces[2 * i].ends != 0 || i == (int)gridDim.x - 1);
+        last = min(base + (end ? __ffs(end) - 1 : 31), (int)gridDim.x - 1);
+        if (end) break;
+      }
+    }
+    for (int r0 = blockIdx.y * RPB; r0 < f.R; r0 += gridDim.y * RPB) {
+      const int r = r0 + warp / WPR;
       float a[E], m = -INFINITY, l = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) a[e] = 0.f;
+      if (r < f.R) {
 #pragma unroll 4
-      for (int i = c; i <= last; ++i) {
-        const float* sl = partial + ((size_t)2 * i + (i == c && second ? 1 : 0)) * PART;
-        const float mi = sl[ROWS * D + r], li = sl[ROWS * D + ROWS + r];
-        float v[E];
+        for (int i = c + warp % WPR; i <= last; i += WPR) {
+          const float* sl = partial + ((size_t)2 * i + (i == c && second ? 1 : 0)) * PART;
+          const float mi = sl[ROWS * D + r], li = sl[ROWS * D + ROWS + r];
+          float v[E];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(sl + r * D + lane * E + e);
-          v[e] = x.x;
-          v[e + 1] = x.y;
+          for (int e = 0; e < E; e += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(sl + r * D + lane * E + e);
+            v[e] = x.x;
+            v[e + 1] = x.y;
+          }
+          const float mn = fmaxf(m, mi);
+          const float fo = m == -INFINITY ? 0.f : ex2(m - mn), w = mi == -INFINITY ? 0.f : ex2(mi - mn);
+          l = (m == -INFINITY ? l : l * fo) + (mi == -INFINITY ? li : li * w);  // (no key: 0, or a NaN that has to stay)
+#pragma unroll
+          for (int e = 0; e < E; ++e) a[e] = a[e] * fo + v[e] * w;  // (a NaN stays, also of a piece without weight)
+          m = mn;
         }
-        const float mn = fmaxf(m, mi);
-        const float fo = m == -INFINITY ? 0.f : ex2(m - mn), w = mi == -INFINITY ? 0.f : ex2(mi - mn);
-        l = (m == -INFINITY ? l : l * fo) + (mi == -INFINITY ? li : li * w);  // (no key: 0, or a NaN that has to stay)
-#pragma unroll
-        for (int e = 0; e < E; ++e) a[e] = a[e] * fo + v[e] * w;  // (a NaN stays, also of a piece without weight)
-        m = mn;
       }
-      const int node = (f.rem0 + r) / G, h = f.hk * G + f.rem0 + r - node * G;
-      store(f.row0 + f.node0 + node, h, a, tree_finish(p, h, m, l));
+      if constexpr (WPR > 1) {
+        __syncthreads();  // (the sums of the row before are read)
+        if (lane == 0) {
+          red[0][warp] = m;
+          red[1][warp] = l;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = a[e];
+        __syncthreads();
+        if (warp % WPR != 0) continue;
+        m = red[0][warp];
+        for (int w = 1; w < WPR; ++w) m = fmaxf(m, red[0][warp + w]);
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+          const float mw = red[0][warp + w], lw = red[1][warp + w], fo = mw == -INFINITY ? 0.f : ex2(mw - m);
+          l += mw == -INFINITY ? lw : lw * fo;
+#pragma unroll
+          for (int e = 0; e < E; ++e) a[e] = fmaf(sums[warp + w][lane * E + e], fo, a[e]);
+        }
+      }
+      if (r < f.R) {
+        const int node = (f.rem0 + r) / G, h = f.hk * G + f.rem0 + r - node * G;
+        store(f.row0 + f.node0 + node, h, a, tree_finish(p, h, m, l));
+      }
     }
   }
   const float none[E] = {};
@@ -1528,7 +1574,7 @@ int launch_t(const Kv4TreeParams& p, int ctas, void* workspace, cudaStream_t str
   TreePiece* pieces = static_cast<TreePiece*>(workspace);
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPieceBytes);
   if (launch_kernel(KERN, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, false, p, pieces, partial) != 0) return -1;
-  return launch_kernel(kv4_tree_join_kernel<C::DIM, C::ROWS>, dim3((unsigned)grid, ctas > 1 ? 2 : 8), 256, 0, stream, true, p,
+  return launch_kernel(kv4_tree_join_kernel<C::DIM, C::ROWS>, dim3((unsigned)grid, 8), 256, 0, stream, true, p,
                        (const TreePiece*)pieces, (const float*)partial);
 }
 template <int D, int NT>
