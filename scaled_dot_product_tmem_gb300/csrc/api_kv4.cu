@@ -203,7 +203,7 @@ int attn_kv4_tree(const void* q, const int* cu_seqlens, const int* parents, cons
   if (st != ATTN_OK) return st;
   st = sdpa::check_common(1, T, 0, H_q, H_kv, d, d, 1, window, softmax_type, softmax_offset);
   if (st != ATTN_OK) return st;
-  if ((long long)T * H_q > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)T * H_q > 0x7fffffffLL || H_q / H_kv > 65535) return ATTN_ERR_UNSUPPORTED;
   // (the kernel multiplies scores held as 2^-23 of their value by scale 2^23 log2(e))
   if (sdpa::resolve_scale(scale, d) > 1e30f) return ATTN_ERR_UNSUPPORTED;
   if (T == 0 || (B == 0 && !zero_rest)) return ATTN_OK;

@@ -301,11 +301,11 @@ int launch_kv4_append_rope(const Kv4StoreParams& p, const RopeParams& rp, bool i
 // looks 32 entries' pages up at once, for all heads and layers that the block then walks.  A thread owns
 // the same few bytes of every token of a head and layer, so its moves follow one another without a
 // barrier, whatever the entries are.  Entries that only move down (kept >= i, as ascending ones do)
-// cannot read what an earlier one of the same eight wrote, so eight are loaded at once.
+// cannot read what an earlier one of the same sixteen wrote, so sixteen are loaded at once.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_keep_kernel(const Kv4KeepParams p) {
   // words (4 bytes) of K codes, of V codes, of K scales; then V's scale bytes
-  constexpr int KW = D / 8, VW = D / 8, SW = D / 64, NV = D / 16, BATCH = 8;
+  constexpr int KW = D / 8, VW = D / 8, SW = D / 64, NV = D / 16, BATCH = 16;
   static_assert(KW + VW + SW + NV <= 64, "64 threads a head and layer");
   struct Move {
     long long src, dst;  // a page's offset in a layer, or -1: this entry moves nothing

@@ -156,6 +156,26 @@ def test_long_context_is_split(nodes, H):
     t.check(o, lse)
 
 
+@pytest.mark.parametrize("H,window", [(1, -1), (4, 300)])
+def test_a_long_chain(H, window):
+    """A prompt's continuation over a cached prefix: several row blocks, each up to its own last token."""
+    t = Trees([333, 0], [700, 130], H, 1, 64, 64, seed=4, chain=True)
+    o, lse = t.call(window=window)
+    _clean()
+    t.check(o, lse, window=window)
+
+
+def test_no_sequences():
+    sdpa = _sdpa()
+    q = torch.ones((3, 4, 64), dtype=torch.bfloat16, device="cuda")
+    pool = sdpa.kv4_pool(1, 2, 64, 16)
+    o, lse = sdpa.sdpa_tree_kv4(q, _i32([0]), None, pool, torch.zeros((0, 2), dtype=torch.int32, device="cuda"), _i32([]))
+    assert torch.all(o == 0) and torch.all(lse == -np.inf)
+    o, lse = sdpa.sdpa_tree_kv4(q[:0], _i32([0, 0]), None, pool, torch.zeros((1, 2), dtype=torch.int32, device="cuda"), _i32([5]))
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    _clean()
+
+
 def test_a_chain_equals_the_decode_of_the_newest_tokens():
     sdpa = _sdpa()
     lens, n = [130, 64, 1000], 3

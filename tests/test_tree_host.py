@@ -117,6 +117,7 @@ def test_tree_validation(lib):
 
     assert tr(H=7) == INVALID and tr(B=-1) == INVALID and tr(T=-1) == INVALID
     assert tr(d=192) == UNSUPPORTED and tr(page=20) == UNSUPPORTED and tr(scale=2e30) == UNSUPPORTED
+    assert tr(H=1 << 17, Hk=1, T=1) == UNSUPPORTED and tr(T=1 << 29) == UNSUPPORTED
     assert tr(st=3) == INVALID and tr(st=2) == INVALID
     assert tr(q=None) == INVALID and tr(o=None) == INVALID and tr(lens=None) == INVALID and tr(cu=None) == INVALID
     assert tr(pool=None) == INVALID
