@@ -648,18 +648,41 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
       for (int k = 0; k < cnt; ++k, ++n, ++unit) {
         const int stage = n % NST, sk = n % NK, sv = n % NV;
         const uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
-        ok = tree_wait(&raw_full[stage], (n / NST) & 1, err, kTreeRawFull);
+        // The unit's bytes, and K's place free.  One row tile, whose pace the decoding sets: half of the lanes looks
+        // at each barrier, so that two waits cost one (200 of some 2700 cycles a unit).  Two: K's place is
+        // what the call waits for, so the bytes are in registers by then.
+        if constexpr (TWO) {
+          ok = tree_wait(&raw_full[stage], (n / NST) & 1, err, kTreeRawFull);
+        } else {
+          const bool other = lane % 2 == 1 && n >= NK;
+          ok = tree_wait(other ? &k_empty[sk] : &raw_full[stage], other ? (n / NK - 1) & 1 : (n / NST) & 1, err,
+                         other ? kTreeKEmpty : kTreeRawFull);
+        }
         if (!ok) break;
-        uint4 w[N];
-        uint32_t sc[N];
+        uint4 w[N], wv[N];
+        uint32_t sc[N], sv2[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int off = page_at(STEP * i), in = STEP * i & (P - 1);
           w[i] = *reinterpret_cast<const uint4*>(st + code_k + off + in * (D / 2));
           sc[i] = *reinterpret_cast<const unsigned short*>(st + scale_k + off + in * (D / 16));
         }
-        if (n >= NK) ok = tree_wait(&k_empty[sk], (n / NK - 1) & 1, err, kTreeKEmpty);
-        if (!ok) break;
+        auto load_V = [&]() {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int off = page_at(STEP * i), in = STEP * i & (P - 1);
+            wv[i] = *reinterpret_cast<const uint4*>(st + code_v + off + in / 2 * D);
+            sv2[i] = *reinterpret_cast<const unsigned short*>(st + scale_v + off + in / 2 * (D / 8));
+          }
+          __syncwarp();  // every lane has read its pieces
+          if (lane == 0) mbar_arrive(&raw_empty[stage]);
+        };
+        if constexpr (TWO) {
+          if (n >= NK) ok = tree_wait(&k_empty[sk], (n / NK - 1) & 1, err, kTreeKEmpty);
+          if (!ok) break;
+        } else {
+          load_V();
+        }
         {
           uint8_t* d = smem + C::OFF_K + sk * C::TILE;
 #pragma unroll
@@ -676,14 +699,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[sk]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int off = page_at(STEP * i), in = STEP * i & (P - 1);
-          w[i] = *reinterpret_cast<const uint4*>(st + code_v + off + in / 2 * D);
-          sc[i] = *reinterpret_cast<const unsigned short*>(st + scale_v + off + in / 2 * (D / 8));
-        }
-        __syncwarp();  // every lane has read its pieces
-        if (lane == 0) mbar_arrive(&raw_empty[stage]);
+        if constexpr (TWO) load_V();
         if (n >= NV) ok = tree_wait(&v_empty[sv], (n / NV - 1) & 1, err, kTreeVEmpty);
         if (!ok) break;
         // units whose tokens are not all seen by all rows, as the softmax warps decide it
@@ -696,15 +712,15 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
           for (int i = 0; i < N; ++i) {
             const int tok = 2 * u + STEP * i;
             uint32_t bits = 0u;
-            if (tok >= len || tok < lo) sc[i] &= 0xFF00u;
-            if (tok + 1 >= len || tok + 1 < lo) sc[i] &= 0x00FFu;
-            if ((sc[i] & 0x00F8u) == 0x00F8u) {
+            if (tok >= len || tok < lo) sv2[i] &= 0xFF00u;
+            if (tok + 1 >= len || tok + 1 < lo) sv2[i] &= 0x00FFu;
+            if ((sv2[i] & 0x00F8u) == 0x00F8u) {
               bits |= 1u;
-              sc[i] &= 0xFF00u;
+              sv2[i] &= 0xFF00u;
             }
-            if ((sc[i] & 0xF800u) == 0xF800u) {
+            if ((sv2[i] & 0xF800u) == 0xF800u) {
               bits |= 2u;
-              sc[i] &= 0x00FFu;
+              sv2[i] &= 0x00FFu;
             }
             smem[C::OFF_NAN + (sv * NG + g) * 64 + tok / 2] = (uint8_t)bits;
           }
@@ -713,11 +729,11 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
           uint8_t* d = smem + C::OFF_V + sv * C::TILE;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const uint32_t sp = scale_pair(sc[i]);
+            const uint32_t sp = scale_pair(sv2[i]);
             const Kv4Small a = scales_low(sp), b2 = scales_high(sp);
             // (D = 128: 8 bytes a token; D = 64: the two eighths' 4 bytes a token)
-            const uint32_t t0w0 = w[i].x, t0w1 = D == 128 ? w[i].y : w[i].z, t1w0 = D == 128 ? w[i].z : w[i].y,
-                           t1w1 = w[i].w;
+            const uint32_t t0w0 = wv[i].x, t0w1 = D == 128 ? wv[i].y : wv[i].z, t1w0 = D == 128 ? wv[i].z : wv[i].y,
+                           t1w1 = wv[i].w;
             uint8_t* di = d + i * STEP * 128;  // (the chunk's exclusive-or with 1: the row's next token)
             *reinterpret_cast<uint4*>(di + dst_v) = decode8(flip ? t0w1 : t0w0, a);
             *reinterpret_cast<uint4*>(di + (dst_v ^ 16)) = decode8(flip ? t0w0 : t0w1, a);
