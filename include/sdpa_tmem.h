@@ -524,7 +524,8 @@ int attn_kv4_append_rope(const void* q, const void* k, const void* v, const floa
  *   the cache as its tokens seq_lens[b], seq_lens[b] + 1, ... (device int32 [B]: the tokens before the
  *   tree, clamped to [0, max_pages * page_size]).  parents: device int32 [T], the number of a node's
  *   parent within its sequence; a value that is negative or not below the node's own number makes it
- *   a child of the last token before the tree.  NULL: a chain, every node's parent the one before it.
+ *   a child of the last token before the tree.  NULL: a chain, every node's parent the one before it (any
+ *   length; a long chain given as parents costs a walk up of its whole depth for every 128 tokens of it).
  *   Node i, at position seq_lens[b] + depth(i), sees the tokens before the tree, its ancestors and
  *   itself; with window >= 0 only those whose position is at least its own minus window.  No other
  *   token reaches it, not even one held as NaN.  o bf16 [T, H_q, d], lse fp32 [H_q, T] (may be NULL);

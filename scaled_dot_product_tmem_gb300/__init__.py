@@ -1453,7 +1453,7 @@ def attn_kv4_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, o, lse=Non
     tree, already in the cache as its tokens seq_lens[b], seq_lens[b] + 1, ... (seq_lens: int32 [B], the
     tokens before the tree).  parents: int32 [T], the number of a node's parent within its sequence,
     below its own; negative: a child of the last token before the tree.  None: a chain (tokens in
-    causal order, any number of them).  A node sees the tokens before the tree, its ancestors and
+    causal order, any number of them; much faster than a long chain given as parents).  A node sees the tokens before the tree, its ancestors and
     itself, with window >= 0 those of the last window + 1 positions.  Rows of no sequence are left
     alone, or zeroed with zero_rest (lse -inf).  workspace: as for attn_kv4_decode."""
     sizes = _check_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, softmax_offset)

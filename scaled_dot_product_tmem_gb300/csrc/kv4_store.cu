@@ -2,7 +2,9 @@
 // number format in kv4.cuh).  Each kernel moves each byte once.  Measured with 8 heads of 128:
 // 15,677 tokens appended in 16 us (83 MB; 18 us without the loads ahead of the lookup) and
 // read back in 14 us; 1500 pages of 64 tokens copied in 4 layers in 134 us (885 MB moved,
-// 6.6 TB/s); one token of each of 64 sequences appended or read back in about 3 us (lookups).
+// 6.6 TB/s); one token of each of 64 sequences appended or read back in about 3 us (lookups).  With the keys
+// rotated on the way and 32 query heads beside them, 15,677 tokens in 67 us (347 MB).  Up to 9 kept tokens of
+// each of 64 sequences moved in 32 layers in 15 us (23 with their places worked out anew for every head).
 #include "attn_kernels.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -123,16 +125,13 @@ __device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint
 // and sines for all heads.  The turned values are rounded to bf16, as a rotation of its own would
 // leave them, and then quantised.  Blocks behind those of the append turn the queries.
 template <int D, int ROT>
-__global__ void __launch_bounds__(256, ROT ? 3 : 1) kv4_append_kernel(const Kv4StoreParams p, const RopeParams rp, int gx, int gy) {
+__global__ void __launch_bounds__(256, ROT == 0 ? 4 : ROT == 1 ? 2 : 3) kv4_append_kernel(const Kv4StoreParams p, const RopeParams rp, int gx, int gy) {
   constexpr int NG = D / 16, HS = 256 / (NG * kTok);  // heads a block takes at a time
-  int bx = blockIdx.x, by = blockIdx.y;
   if constexpr (ROT != 0) {
-    if (bx >= gx * gy) return rope_block<ROT == 2>(rp, bx - gx * gy);
-    by = bx / gx;
-    bx -= by * gx;
-  } else {
-    gy = gridDim.y;
+    if ((int)blockIdx.x >= gx * gy) return rope_block<ROT == 2>(rp, blockIdx.x - gx * gy);
   }
+  const int by = ROT ? blockIdx.x / gx : blockIdx.y, bx = ROT ? blockIdx.x - by * gx : blockIdx.x;
+  const int step = HS * (ROT ? gy : gridDim.y);
   __shared__ TokenAt at[kTok];
   const int t0 = bx * kTok;
   const int P = p.c.page_size, blk = kv4_block_bytes(P, D);
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(256, ROT ? 3 : 1) kv4_append_kernel(const Kv4S
   const int at_v0 = kv4_off_v(P, D) + kv4_v_at(a.w, D == 128 ? g : 2 * g, D);
   const int at_v1 = kv4_off_v(P, D) + kv4_v_at(a.w, 2 * g + 1, D);  // D = 64: 16 dims are two eighths
 #pragma unroll 2
-  for (; h < p.c.H_kv; h += HS * gy) {
+  for (; h < p.c.H_kv; h += step) {
     uint4 ka = k0, kb = k1;
     const uint4 va = v0, vb = v1;
     if constexpr (ROT == 1) {
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(256, ROT ? 3 : 1) kv4_append_kernel(const Kv4S
       if (part[0]) ka = rope_turn_pairs(k0, c[0], sn[0]);
       if (part[1]) kb = rope_turn_pairs(k1, c[1], sn[1]);
     }
-    if (h + HS * gy < p.c.H_kv) load(h + HS * gy);
+    if (h + step < p.c.H_kv) load(h + step);
     uint8_t* base = page + (size_t)h * blk;
     uint32_t cd[2];
     int sb = quantise16(ka, kb, cd);
@@ -312,6 +311,7 @@ __global__ void __launch_bounds__(256) kv4_keep_kernel(const Kv4KeepParams p) {
     int ws, wd;          // the tokens' places in their pages
   };
   __shared__ Move moves[32];
+  __shared__ longlong2 at[32][64];  // where each thread's bytes of a move lie in a layer's head 0 (x < 0: it moves nothing)
   __shared__ int n_moves, n_down;  // entries until the end; how many of the first keep to kept >= i
   const int x = threadIdx.x % 64, b = blockIdx.y;
   const int P = p.c.page_size, blk = kv4_block_bytes(P, D), units = p.c.H_kv * p.n_layers;
@@ -344,32 +344,34 @@ __global__ void __launch_bounds__(256) kv4_keep_kernel(const Kv4KeepParams p) {
       }
     }
     __syncthreads();
-    const int n = n_moves, down = n_down;
+    const int n = n_moves, down = min(n_down, n);
+    if (x < KW + VW + SW + NV)
+      for (int j = threadIdx.x / 64; j < n; j += 4) {
+        const Move m = moves[j];
+        at[j][x] = m.src < 0 ? make_longlong2(-1, -1) : make_longlong2(m.src + place(m.ws), m.dst + place(m.wd));
+      }
+    __syncthreads();
     if (x < KW + VW + SW + NV) {
       for (int u = blockIdx.x * 4 + threadIdx.x / 64; u < units; u += gridDim.x * 4) {
         uint8_t* base = p.pool + (size_t)(u / p.c.H_kv) * p.layer_bytes + (size_t)(u % p.c.H_kv) * blk;
-        auto get = [&](const Move& m) {
-          const uint8_t* a = base + m.src + place(m.ws);
-          return byte ? (uint32_t)*a : *reinterpret_cast<const uint32_t*>(a);
-        };
-        auto put = [&](const Move& m, uint32_t v) {
-          uint8_t* a = base + m.dst + place(m.wd);
-          if (byte) *a = (uint8_t)v;
-          else *reinterpret_cast<uint32_t*>(a) = v;
+        auto get = [&](long long o) { return byte ? (uint32_t)base[o] : *reinterpret_cast<const uint32_t*>(base + o); };
+        auto put = [&](long long o, uint32_t v) {
+          if (byte) base[o] = (uint8_t)v;
+          else *reinterpret_cast<uint32_t*>(base + o) = v;
         };
         int j = 0;
-        for (; j < min(n, down); j += BATCH) {
+        for (; j < down; j += BATCH) {
           uint32_t v[BATCH];
-          const int last = min(j + BATCH, min(n, down));
+          const int last = min(BATCH, down - j);
 #pragma unroll
           for (int q = 0; q < BATCH; ++q)
-            if (j + q < last && moves[j + q].src >= 0) v[q] = get(moves[j + q]);
+            if (q < last && at[j + q][x].x >= 0) v[q] = get(at[j + q][x].x);
 #pragma unroll
           for (int q = 0; q < BATCH; ++q)
-            if (j + q < last && moves[j + q].src >= 0) put(moves[j + q], v[q]);
+            if (q < last && at[j + q][x].x >= 0) put(at[j + q][x].y, v[q]);
         }
-        for (j = min(n, down); j < n; ++j)
-          if (moves[j].src >= 0) put(moves[j], get(moves[j]));
+        for (j = down; j < n; ++j)
+          if (at[j][x].x >= 0) put(at[j][x].y, get(at[j][x].x));
       }
     }
     if (n < 32) break;

@@ -5,24 +5,41 @@
 //   S_j = scale q.k_j over the tokens j < L, the node's ancestors and itself, under a window only
 //   those of the last window + 1 positions; softmax with an optional sink logit; o = P V.
 //
-// All nodes and all query heads of a kv head share every byte of the cache: n G rows.  Up to about 64 rows
-// the call is bound by reading the cache, from 128 on by the tensor cores, so the products run there:
-//   - A unit is 128 tokens of one sequence and kv head.  A producer warp streams its pages' blocks into
-//     shared memory; eight warps decode K and V into bf16 operand tiles (128-byte swizzle, a lane's
-//     16-byte stores of a quarter warp on different banks); one warp issues S = Q K^T and O += P V
-//     (tcgen05, 128 rows a tile); two warpgroups take the softmax, a thread a row, with P back into
-//     TMEM where S was.
+// All n nodes and all G query heads of a kv head share every byte of the cache: n G rows.  Reading the cache
+// bounds a call of few rows, the tensor cores one of many (256 rows: 178 us of products, 56 us of
+// bytes for 329,377 tokens of 8 kv heads of 128).  So there are five forms, by the sequences' rows a kv head
+// on average (block_rows):
+//   - Up to 8, 16 and 32 rows (kv4_tree_few_kernel): rows are the 8-wide columns of mma.sync products whose
+//     16 rows are tokens (scores) or head dims (outputs); operands are decoded in registers.
+//   - Up to 128 rows, and more (kv4_tree_kernel): tcgen05 products of 128-row tiles.  Four warps decode
+//     K and V into bf16 operand tiles in shared memory (128-byte swizzle; the eight lanes of a quarter
+//     warp store to different banks), S = Q K^T and O += P V accumulate in TMEM, two warpgroups take the
+//     softmax, a thread a row, with P where S was.  Up to 128 rows they take the units in turn, each with its
+//     own sums, joined at a part's end; above, they hold a row tile each and share the operands.
+// All forms:
+//   - A unit is 128 tokens of one sequence and kv head.  A loading warp works out the CTA's work, looks pages up
+//     and streams their blocks into shared memory, a page and head in one bulk copy.
 //   - Codes are decoded as (c - 8) s 2^-23 (kv4.cuh), exact; the power of two is undone in the scores'
 //     scale and in the outputs.  Eight dims of a word come out in the order 0 4 1 5 2 6 3 7: Q is
 //     laid out alike, and the outputs are put back when they are stored.
-//   - Up to 128 rows: one row tile, whose even units one warpgroup takes and whose odd units the
-//     other, each with its own sums, joined at the end.  More rows: two row tiles that share the
-//     decoded operands (a tile of its own would decode the cache again).
 //   - Work is cut evenly over a persistent grid, whatever the lengths (units of one sequence, kv head
 //     and row block in order, and kSegCost units more for each such segment); a segment that spans
 //     several CTAs leaves fp32 partial sums in the workspace, joined in CTA order by a second kernel:
 //     bitwise reproducible.
 //   - The probabilities are rounded to bf16 (2^-9 relative) for P V; their sum is fp32.
+//   - Units with tokens that some row does not see (the tree's own, the ends of a window) take each row's 128 bits
+//     of what it sees, found by walking up from its node: the walk is a dependent load a level.
+//
+// Measured on the device (329,377 tokens of 4 sequences, 8 kv heads of 128, 4 query heads each): 2 nodes 82 us,
+// 4 nodes 109, 8 nodes 192, 16 and 32 nodes 192 and 197, 64 nodes 280 (1.2 PFLOP/s, 63 % of the measured bf16
+// rate), 128 nodes 521.  16 sequences of 1 to 8191 tokens with 16 nodes: 49 us.  What the steps brought, for
+// 131,072 tokens and 64 / 16 nodes: sizes worked out by every warp 200 / 127 us; by the loading warp, rare
+// paths without the scores' registers 165 / 114; shorter loops of products 151 / 98; join's pieces
+// found at once and longer output steps 136 / 92; K and V of a unit loaded together 136 / 89.
+// What bounds it: one tile, decoding (some 2400 cycles a unit, a chain of loads, conversions and stores in four
+// warps; eight warps did not pay for the registers they take from the softmax) beside the chain S - softmax -
+// P V; two tiles, that chain with both tiles' products (2048 cycles a unit at full rate) and the decoded operands'
+// way through shared memory.  Few rows: the copies and the decoding arithmetic, as in kv4_decode.cu.
 #include <algorithm>
 #include <atomic>
 

@@ -399,6 +399,27 @@ def test_keep_moves_whole_tokens(page, d, layers):
     assert np.array_equal(pool.cpu().numpy(), ref)
 
 
+@pytest.mark.parametrize("order", ["ascending", "any"])
+def test_keep_of_many_entries(order):
+    """More entries than are looked up at once, against the moves one after another on whole tokens."""
+    sdpa = _sdpa()
+    rng = np.random.default_rng(7)
+    page, d, H, L, n = 32, 64, 2, 45, 150
+    k, v = (torch.from_numpy(rng.standard_normal((L + n, H, d))).to(torch.bfloat16) for _ in range(2))
+    need = -(-(L + n) // page)
+    pool = sdpa.kv4_pool(need, H, d, page).fill_(0xFF)
+    table = _i32([rng.permutation(need).tolist()])
+    sdpa.attn_kv4_append(k.cuda(), v.cuda(), _i32([0, L + n]), pool, table, _i32([0]))
+    kept = (np.sort(rng.permutation(n)[:97]) if order == "ascending" else rng.integers(0, n, 97)).tolist()
+    toks = list(range(L + n))
+    tree.keep(toks, L, kept)
+    sdpa.attn_kv4_keep(pool, table, _i32([L]), _i32([kept + [-1] * 3]), d)
+    gk, gv = sdpa.kv4_gather(pool, table, _i32([0, L + n]), _i32([0]), L + n, d)
+    _clean()
+    assert np.array_equal(gk.double().cpu().numpy(), kv4.held(k.double().numpy())[toks])
+    assert np.array_equal(gv.double().cpu().numpy(), kv4.held(v.double().numpy())[toks])
+
+
 def test_keep_without_a_page():
     sdpa = _sdpa()
     pool = torch.randint(0, 256, (2, 1, sdpa.kv4_block_bytes(16, 64)), dtype=torch.uint8, device="cuda")
