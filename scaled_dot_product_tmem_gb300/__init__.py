@@ -1195,6 +1195,8 @@ def attn_rope_table(inv_freq, positions, table, *, gain=1.0, stream=None):
 
 
 def _run_rope_table(inv_freq, positions, table, T, n, dev, gain):
+    if T > 0x7FFFFFFF:
+        raise ValueError(f"at most 2^31 - 1 positions, got {T}")
     st = _load().attn_rope_table(_p(inv_freq), _p(positions), _p(table), T, n, float(gain), _raw_stream(dev, None))
     if st != ATTN_OK:
         raise AttnError(st, "attn_rope_table")
@@ -1255,6 +1257,8 @@ def _check_rope(q, k, table):
         raise ValueError(f"q must be [rows, H, d] or [B, S, H, d], got {tuple(q.shape)}")
     rows, (H, d) = q.shape[:-2], q.shape[-2:]
     T = math.prod(rows)
+    if T > 0x7FFFFFFF:
+        raise ValueError(f"at most 2^31 - 1 rows, got {T}")
     if k is not None and (k.dim() != q.dim() or k.shape[:-2] != rows or k.shape[-1] != d):
         raise ValueError(f"k must have q's rows and head dim, got {tuple(k.shape)} and {tuple(q.shape)}")
     R = table.shape[0]
@@ -1274,10 +1278,10 @@ def attn_rope(q, k, table, q_out, k_out, *, interleaved=False, first_dim=0, inve
     takes the gradient of the results to that of q and k.  Rows may be apart (a slice of a fused
     projection), evenly and by a multiple of 8 elements."""
     T, H, H_k, d, n, R = _check_rope(q, k, table)
+    if q_out is None or q_out.shape != q.shape or (k is not None and (k_out is None or k_out.shape != k.shape)):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
     strides = [_row_stride(q, "q"), 0 if k is None else _row_stride(k, "k"), _row_stride(q_out, "q_out"),
                0 if k is None else _row_stride(k_out, "k_out")]
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise ValueError("q_out and k_out must have the shapes of q and k")
     dev = _device_of(q, k, table, q_out, k_out)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -1326,29 +1330,35 @@ def _evenly(t):
 
 
 class RopeFunction(torch.autograd.Function):
-    """autograd wrapper of the rotation; its gradient is the transposed rotation."""
+    """autograd wrapper of the rotation; its gradient is the transposed rotation, differentiable in turn."""
 
     @staticmethod
-    def forward(ctx, q, k, table, interleaved, first_dim):
+    def forward(ctx, q, k, table, interleaved, first_dim, inverse=False):
         ctx.set_materialize_grads(False)
-        ctx.kw = dict(interleaved=interleaved, first_dim=first_dim)
+        ctx.args = interleaved, first_dim, inverse
         ctx.save_for_backward(table)
-        return rope_forward(q, k, table, **ctx.kw)
+        return _rope_new(q, k, table, *ctx.args, None)
 
     @staticmethod
     def backward(ctx, dq, dk):
         (table,) = ctx.saved_tensors
+        interleaved, first_dim, inverse = ctx.args
+        dq, dk = (None if g is None else _evenly(g) for g in (dq, dk))
         if dq is None and dk is None:
-            return None, None, None, None, None
+            return None, None, None, None, None, None
+        rest = table, interleaved, first_dim, not inverse
+        turn = RopeFunction.apply if torch.is_grad_enabled() else lambda *a: _rope_new(*a, None)
         if dq is None:
-            return None, rope_backward(_evenly(dk), None, table, **ctx.kw)[0], None, None, None
-        dq, dk = rope_backward(_evenly(dq), None if dk is None else _evenly(dk), table, **ctx.kw)
-        return dq, dk, None, None, None
+            return None, turn(dk, None, *rest)[0], None, None, None, None
+        return (*turn(dq, dk, *rest), None, None, None, None)
 
 
 def rope(q, k, table, *, interleaved=False, first_dim=0):
     """Differentiable rotation of q and k (k may be None) by positions: returns (q, k); arguments as
-    for attn_rope.  The table receives no gradient."""
+    for attn_rope.  The table receives no gradient.
+
+    A step captured into a CUDA graph (this or any other differentiable call): no result of an eager call whose
+    gradient still leads to the same leaves may be alive, or autograd ends the capture."""
     return RopeFunction.apply(q, k, table, bool(interleaved), int(first_dim))
 
 

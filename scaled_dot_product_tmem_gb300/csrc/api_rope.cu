@@ -57,6 +57,7 @@ int rope_params(RopeParams* p, const void* q, const void* k, const float* table,
   if (T < 0 || H_q < 0 || H_k < 0 || d <= 0 || n < 0 || first_dim < 0 || table_rows < 0) return ATTN_ERR_INVALID_ARG;
   if (n == 0 || n % 8 != 0 || d % 8 != 0 || first_dim % 8 != 0 || d > 256) return ATTN_ERR_UNSUPPORTED;
   if (first_dim + 2LL * n > d) return ATTN_ERR_INVALID_ARG;
+  if ((long long)H_q + H_k > 0x7ffffff0LL) return ATTN_ERR_UNSUPPORTED;
   const struct {
     const void* x;
     void* y;

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
 int launch_rope_table(const double* inv_freq, const int* positions, float* table, int T, int n, float gain,
                       cudaStream_t stream) {
   const int rows = 256 / n;
-  const int blocks = (T + rows - 1) / rows;
+  const int blocks = T / rows + (T % rows != 0);
   rope_table_kernel<<<blocks < 152 * 4 ? blocks : 152 * 4, 256, 0, stream>>>(inv_freq, positions, table, T, n, gain);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

@@ -289,6 +289,61 @@ def test_captured_and_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_gradient_of_the_gradient():
+    """The rotation is linear: the gradient of <rotated back w, u> by w is u rotated."""
+    sdpa = _sdpa()
+    inv, gain = sdpa.rope_frequencies(32)
+    table = sdpa.rope_table(inv, _i32([5, 0, 77]))
+    q, k = (_randn(3, h, 64, seed=h).cuda().requires_grad_() for h in (4, 2))
+    wq, wk = (_randn(3, h, 64, seed=10 + h).cuda().requires_grad_() for h in (4, 2))
+    uq, uk = (_randn(3, h, 64, seed=20 + h).cuda() for h in (4, 2))
+    grads = torch.autograd.grad(sdpa.rope(q, k, table, first_dim=16), (q, k), (wq, wk), create_graph=True)
+    for got, want in zip(grads, sdpa.rope_backward(wq.detach(), wk.detach(), table, first_dim=16)):
+        assert torch.equal(got, want)
+    second = torch.autograd.grad(grads, (wq, wk), (uq, uk))
+    for got, want in zip(second, sdpa.rope_forward(uq, uk, table, first_dim=16)):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_training_step_captured(packed):
+    """Attention with positions, forward and backward, replayed with other inputs."""
+    sdpa = _sdpa()
+    B, S, H, d = 2, 96, 2, 64
+    shape = (B * S, H, d) if packed else (B, S, H, d)
+    q, k, v, w = (_randn(*shape, seed=i).cuda() for i in range(4))
+    for t in (q, k, v):
+        t.requires_grad_()
+    inv, _ = sdpa.rope_frequencies(d)
+    pos, cu = torch.arange(S, dtype=torch.int32, device="cuda"), _i32([0, S, 2 * S])
+
+    def step():
+        table = sdpa.rope_table(inv, pos.repeat(B) if packed else pos)
+        if packed:
+            o = sdpa.attention_packed(q, k, v, cu, rope=table)
+        else:
+            o = sdpa.attention(q, k, v, rope=table)
+        return (o.detach(), *torch.autograd.grad(o, (q, k, v), w))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    with torch.no_grad():
+        q.copy_(_randn(*shape, seed=9).cuda())
+        pos.add_(1000)
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, step()):
+        assert torch.equal(a, b)
+    _clean()
+
+
 def test_python_refusals():
     sdpa = _sdpa()
     inv, _ = sdpa.rope_frequencies(32)
@@ -296,6 +351,10 @@ def test_python_refusals():
     q, k = _randn(4, 2, 64).cuda(), _randn(4, 1, 64).cuda()
     with pytest.raises(ValueError, match="one row per row"):
         sdpa.rope_forward(q[:2], k[:2], table)
+    with pytest.raises(ValueError, match="shapes of q and k"):
+        sdpa.attn_rope(q, k, table, torch.empty_like(q), None)
+    with pytest.raises(ValueError, match="shapes of q and k"):
+        sdpa.attn_rope(q, None, table, torch.empty_like(k), None)
     with pytest.raises(ValueError, match="q's rows"):
         sdpa.rope_forward(q, k[:3], table)
     with pytest.raises(TypeError):
