@@ -57,23 +57,34 @@ constexpr int kUnit = 128;    // tokens of a unit
 // a segment's fixed costs, in units
 template <int ROWS>
 constexpr int kSegCost = ROWS == 8 ? 1 : ROWS == 16 ? 2 : ROWS == 256 ? 3 : 4;
-enum TreeSite { kTreeRawFull = 0xB0, kTreeRawEmpty, kTreeKFull, kTreeKEmpty, kTreeVFull, kTreeVEmpty, kTreeQFull, kTreeQEmpty,
-                kTreeS, kTreeP, kTreeO, kTreeDrain, kTreePartFull, kTreePartEmpty, kTreeShare };
+// What an expired wait is reported as: the role that gave up.
+enum TreeSite { kTreeLoad = 0xB0, kTreeIssue, kTreeDecode, kTreeSoftmax, kTreeFew };
 
-// mbar_wait_warp() in fewer instructions: some thirty of them are in line, and every role's code comes
-// from the same instruction cache.
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, int* err, int site) {
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
+// A bounded wait of a whole warp for a barrier's phase, true if it completed.  Some thirty of these are in line, and all
+// roles' code comes from the same instruction cache, so a warp reports an expired wait once, where its role ends
+// (tree_report): 16 sequences of 16 nodes took 45 us, 47 with the report in line, 49 with a look at the other roles'
+// reports in the loop.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
+  static_assert(SDPA_WAIT_LIMIT_NS < 0xffffffffull, "32 bits of the timer");
   const uint32_t a = smem_u32(bar);
   bool ok = mbar_try_wait(a, parity);
   if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
+    const uint32_t t0 = globaltimer_lo();
 #pragma unroll 1
     do {
       ok = mbar_try_wait(a, parity) || mbar_try_wait(a, parity);
-      if (!ok && globaltimer_ns() - t0 > SDPA_WAIT_LIMIT_NS) atomicCAS(err, 0, kErrTimeoutBase + site);
-    } while (!ok && *(volatile int*)err == 0);
+    } while (!ok && globaltimer_lo() - t0 <= (uint32_t)SDPA_WAIT_LIMIT_NS);
   }
   return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ void tree_report(const Kv4TreeParams& p, bool ok, int site) {
+  if (!ok && threadIdx.x % 32 == 0) atomicCAS(p.err, 0, kErrTimeoutBase + site);
 }
 
 // A sequence's sizes.
@@ -112,7 +123,8 @@ struct TreePart {
   // Units below u_win and from u_tree on have tokens that not every row sees: at a window's lower end,
   // and from the unit on that holds the tree's first node or ends past the tokens before it.
   int u_win, u_tree;
-  int pad[2];
+  int G;       // query heads a kv head
+  float inv_G;
 };
 constexpr int kParts = 4;  // parts the loading warp may be ahead
 
@@ -131,6 +143,12 @@ __device__ __forceinline__ int tree_parent(const Kv4TreeParams& p, int row0, int
 
 // x / g for 0 <= x < 2^20, inv = 1 / g: the fp32 product is off by less than half of 1 / g.
 __device__ __forceinline__ int small_div(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
+
+// x / n for 0 <= x, in one place: 64-bit division is long.
+__device__ __noinline__ long long divide(long long x, unsigned n) {
+  if (x <= 0xffffffffLL) return (unsigned)x / n;
+  return (unsigned long long)x / n;
+}
 
 // This CTA's numbers (a whole warp): the sequence b they begin in, `skip` of its numbers before them, and how
 // many.
@@ -151,7 +169,7 @@ __device__ __forceinline__ void tree_share(const Kv4TreeParams& p, int& b, long 
           mine = (long long)s.seg * s.blocks * p.c.H_kv;
         }
         upto = mine;
-#pragma unroll
+#pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
           const long long o = __shfl_up_sync(0xffffffffu, upto, off);
           if (lane >= off) upto += o;
@@ -173,7 +191,7 @@ __device__ __forceinline__ void tree_share(const Kv4TreeParams& p, int& b, long 
       const long long want = total / 2 + 1;
       const int n = (int)min((long long)gridDim.x, want);
       if (total == 0 || (int)blockIdx.x >= n) break;
-      const long long q = total <= 0x7fffffffLL ? (long long)((unsigned)total / (unsigned)n) : total / n;
+      const long long q = divide(total, (unsigned)n);
       const int rest = (int)(total - q * n);
       first = q * blockIdx.x + min((int)blockIdx.x, rest);
       left = q + ((int)blockIdx.x < rest ? 1 : 0);
@@ -188,14 +206,14 @@ __device__ __forceinline__ void tree_load(const Kv4TreeParams& p, TreePiece* pie
                                           long long skip, long long left) {
   constexpr int D = C::DIM;
   const int lane = threadIdx.x % 32;
-  int* err = p.err;
   int n_part = 0;
   bool ok = true;
   // Lane i copies the block of page i of a unit (whole, also past the sequence's end), if some node sees a token of it: the pages
   // before a window may be gone from the table.  Its page is looked up one unit ahead.
-  const int P = p.c.page_size, n_pages = kUnit / P, t0 = lane * P;
+  const int P = p.c.page_size, n_pages = kUnit >> p.c.page_shift, t0 = lane * P;
   const int block = kv4_block_bytes(P, D), G = p.H_q / p.c.H_kv;
   const size_t page_bytes = (size_t)block * p.c.H_kv;
+  const float inv_G = __fdividef(1.f, (float)G);
   TreeSeq s{};
   int hk = 0, rb = 0, n = 0;
   bool enter = true;          // the sequence's sizes are still to be read
@@ -216,10 +234,11 @@ __device__ __forceinline__ void tree_load(const Kv4TreeParams& p, TreePiece* pie
           ++b;
           continue;
         }
-        const long long vh = skip <= 0x7fffffffLL ? (long long)((unsigned)skip / (unsigned)s.seg) : skip / s.seg;
+        const long long vh = divide(skip, (unsigned)s.seg);
         skip -= vh * s.seg;
         hk = (int)((unsigned)vh / (unsigned)s.blocks);
         rb = (int)vh - hk * s.blocks;
+        hk = min(hk, p.c.H_kv - 1);  // (the offsets were changed meanwhile)
         enter = false;
       }
       // the CTA's units [from, to) of the segment
@@ -229,6 +248,8 @@ __device__ __forceinline__ void tree_load(const Kv4TreeParams& p, TreePiece* pie
       skip = 0;
       const int r0 = rb * C::ROWS;  // (rows of a kv head are below 2^31)
       t.row0 = s.row0, t.n = s.n, t.L = s.L, t.len = s.len, t.lo = s.lo;
+      t.G = G;
+      t.inv_G = inv_G;
       t.hk = hk;
       t.node0 = r0 / G;
       t.rem0 = r0 - t.node0 * G;
@@ -261,7 +282,7 @@ __device__ __forceinline__ void tree_load(const Kv4TreeParams& p, TreePiece* pie
       t.cnt = -1;
     }
     const int slot = n_part % kParts;
-    if (n_part >= kParts) ok = tree_wait(&part_empty[slot], (n_part / kParts - 1) & 1, err, kTreePartEmpty);
+    if (n_part >= kParts) ok = tree_wait(&part_empty[slot], (n_part / kParts - 1) & 1);
     if (!ok) break;
     if (lane == 0) {
       parts[slot] = t;
@@ -282,10 +303,11 @@ __device__ __forceinline__ void tree_load(const Kv4TreeParams& p, TreePiece* pie
       const uint8_t* src = p.pool + (size_t)max(page, 0) * page_bytes + (size_t)t.hk * block;
       const int have = page;
       page = page_of(k + 1);
-      if (n >= C::STAGES) ok = tree_wait(&raw_empty[stage], (n / C::STAGES - 1) & 1, err, kTreeRawEmpty);
+      if (n >= C::STAGES) ok = tree_wait(&raw_empty[stage], (n / C::STAGES - 1) & 1);
       if (!ok) break;
       if (__any_sync(0xffffffffu, have == -1)) {  // not a page: its tokens read as zeros (scale 0)
         if (have == -1) {
+#pragma unroll 1
           for (int o = kv4_off_sk(P, D); o < block; o += 16)
             *reinterpret_cast<uint4*>(st + lane * block + o) = make_uint4(0u, 0u, 0u, 0u);
           atomicCAS(p.page_err, 0, p.site);
@@ -301,10 +323,12 @@ __device__ __forceinline__ void tree_load(const Kv4TreeParams& p, TreePiece* pie
   }
   if (lane < 2 && !(used >> lane & 1)) pieces[2 * blockIdx.x + lane].valid = 0;
   // every copy this warp started must land before the CTA may exit: wait for the last ones
+#pragma unroll 1
   for (int s = 0; s < C::STAGES && s < n; ++s) {
     const int last = s + (n - 1 - s) / C::STAGES * C::STAGES;
-    tree_wait(&raw_full[s], (last / C::STAGES) & 1, err, kTreeDrain);
+    ok = tree_wait(&raw_full[s], (last / C::STAGES) & 1) && ok;
   }
+  tree_report(p, ok, kTreeLoad);
 }
 
 template <int D, bool TWO>
@@ -413,7 +437,6 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
   TreePart* parts = reinterpret_cast<TreePart*>(smem + C::OFF_PART);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int* err = p.err;
 
   grid_launch_dependents();  // the join may be set up meanwhile
   if (threadIdx.x == 0) {
@@ -461,7 +484,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
   // what a role needs of it all the time) until part_done().
   int n_part = 0;
   auto next_part = [&]() {
-    ok = ok && tree_wait(&part_full[n_part % kParts], (n_part / kParts) & 1, err, kTreePartFull);
+    ok = ok && tree_wait(&part_full[n_part % kParts], (n_part / kParts) & 1);
     return ok && parts[n_part % kParts].cnt >= 0;
   };
   auto part_done = [&]() {
@@ -498,7 +521,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
       int nq = 0, nk = 0, nv = 0;  // phases consumed
       uint32_t np = 0u;            // parities of p_ready, a bit a tile
       auto wait_K = [&]() {
-        ok = ok && tree_wait(&k_full[nk % NK], (nk / NK) & 1, err, kTreeKFull);
+        ok = ok && tree_wait(&k_full[nk % NK], (nk / NK) & 1);
         if (ok) tc_fence_after();
         return ok;
       };
@@ -507,7 +530,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         const int cnt = parts[n_part % kParts].cnt;
         part_done();
         if (cnt == 0) continue;
-        ok = tree_wait(q_full, nq++ & 1, err, kTreeQFull);
+        ok = tree_wait(q_full, nq++ & 1);
         if (!ok) break;
         issued = true;
         if (!wait_K()) break;
@@ -517,10 +540,10 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         if (cnt == 1) mma_commit_warp(q_empty);
         for (int k = 0; k < cnt && ok; ++k) {
           const bool need_k = k + 1 < cnt;
-          ok = tree_wait(&v_full[nv % NV], (nv / NV) & 1, err, kTreeVFull);
+          ok = tree_wait(&v_full[nv % NV], (nv / NV) & 1);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            ok = ok && tree_wait(&p_ready[t], np >> t & 1u, err, kTreeP);
+            ok = ok && tree_wait(&p_ready[t], np >> t & 1u);
             if (!ok) break;
             np ^= 1u << t;
             tc_fence_after();
@@ -552,7 +575,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         const int cnt = parts[n_part % kParts].cnt;
         part_done();
         if (cnt == 0) continue;
-        ok = tree_wait(q_full, nq++ & 1, err, kTreeQFull);
+        ok = tree_wait(q_full, nq++ & 1);
         if (!ok) break;
         const int k_first = (n ^ t) & 1;
         if (k_first >= cnt) {  // the other tile has the part's only unit
@@ -565,7 +588,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         for (int k = k_first; k < cnt; k += 2) {
           const int u = n + k, sk = u % NK, sv = u % NV;
           const bool last = k + 2 >= cnt;
-          ok = tree_wait(&k_full[sk], (u / NK) & 1, err, kTreeKFull);
+          ok = tree_wait(&k_full[sk], (u / NK) & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 2
@@ -576,8 +599,8 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
           mma_commit_warp(&s_ready[t]);
           mma_commit_warp(&k_empty[sk]);
           if (last) mma_commit_warp(q_empty);  // every S of the part is issued
-          ok = tree_wait(&v_full[sv], (u / NV) & 1, err, kTreeVFull);
-          ok = ok && tree_wait(&p_ready[t], np++ & 1, err, kTreeP);
+          ok = tree_wait(&v_full[sv], (u / NV) & 1);
+          ok = ok && tree_wait(&p_ready[t], np++ & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 2
@@ -593,14 +616,19 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
     if (issued) {
       uint64_t* bar = &mma_done[warp - C::MMA_WARP];
       mma_commit_warp(bar);
-      tree_wait(bar, 0, err, kTreeDrain);
+      ok = tree_wait(bar, 0) && ok;
     }
   } else if (warp >= C::DEC_WARP && warp < C::MMA_WARP) {
     // ---------------------------------------------------------------- decoding warps
     regs_less<C::REGS_DEC>();
     const int tid = threadIdx.x % 128, P = p.c.page_size, block = kv4_block_bytes(P, D);
     constexpr int N = D / 32, STEP = 128 / N, NG = D / 16;  // 16-byte pieces a thread takes of K, of V; tokens between them
-    auto page_at = [&](int tok) { return tok / P * block; };
+    auto page_at = [&](int tok) { return (tok >> p.c.page_shift) * block; };
+    // what 32 and 64 tokens on adds to the place of a code, of a scale (of K and of V alike): pages are whole powers of two
+    const int c64 = P <= 64 ? page_at(64) : 64 * (D / 2), s64 = P <= 64 ? c64 : 64 * (D / 16);
+    const int c32 = P <= 32 ? page_at(32) : 32 * (D / 2), s32 = P <= 32 ? c32 : 32 * (D / 16);
+    auto code_at = [&](int tok) { return (tok & 32 ? c32 : 0) + (tok & 64 ? c64 : 0); };
+    auto scale_at = [&](int tok) { return (tok & 32 ? s32 : 0) + (tok & 64 ? s64 : 0); };
     // K: 32 dims (quarter q) of a token a piece.  Lanes of dims 64.. store their four chunks two further on:
     // the eight lanes of a quarter warp then hit all banks.
     const int tok_k = tid / N, q = tid % N, w_k = tok_k & (P - 1);
@@ -615,8 +643,6 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
     const int code_v = page_at(2 * u) + kv4_off_v(P, D) + w_v / 2 * D + tid % NG * 16;
     const int scale_v = page_at(2 * u) + kv4_off_sv(P, D) + w_v / 2 * (D / 8) + 2 * g;
     const int dst_v = (g / 4) * C::BLK + 2 * u * 128 + (((2 * (g % 4) + flip) ^ (2 * u & 7)) << 4);
-    const int G = p.H_q / p.c.H_kv;
-    const float inv_G = 1.f / (float)G;
     int n = 0, nq = 0;
 #pragma unroll 1
     for (; next_part(); part_done()) {
@@ -626,7 +652,8 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
       // ---- Q: loaded early, stored when the last scores of the part before are done
       {
         constexpr int QI = C::ROWS * (D / 8) / 128, QB = 8;
-        const int R = part.R, rem0 = part.rem0;
+        const int R = part.R, rem0 = part.rem0, G = part.G;
+        const float inv_G = part.inv_G;
         const __nv_bfloat16* q0 = p.q + ((size_t)(part.row0 + part.node0) * p.H_q + part.hk * G) * D;
 #pragma unroll 1
         for (int i0 = 0; i0 < QI; i0 += QB) {
@@ -641,7 +668,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
             }
           }
           if (i0 == 0 && nq > 0) {
-            ok = tree_wait(q_empty, (nq - 1) & 1, err, kTreeQEmpty);
+            ok = tree_wait(q_empty, (nq - 1) & 1);
             if (!ok) break;
           }
 #pragma unroll
@@ -669,33 +696,30 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         // at each barrier, so that two waits cost one (200 of some 2700 cycles a unit).  Two: K's place is
         // what the call waits for, so the bytes are in registers by then.
         if constexpr (TWO) {
-          ok = tree_wait(&raw_full[stage], (n / NST) & 1, err, kTreeRawFull);
+          ok = tree_wait(&raw_full[stage], (n / NST) & 1);
         } else {
           const bool other = lane % 2 == 1 && n >= NK;
-          ok = tree_wait(other ? &k_empty[sk] : &raw_full[stage], other ? (n / NK - 1) & 1 : (n / NST) & 1, err,
-                         other ? kTreeKEmpty : kTreeRawFull);
+          ok = tree_wait(other ? &k_empty[sk] : &raw_full[stage], other ? (n / NK - 1) & 1 : (n / NST) & 1);
         }
         if (!ok) break;
         uint4 w[N], wv[N];
         uint32_t sc[N], sv2[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int off = page_at(STEP * i), in = STEP * i & (P - 1);
-          w[i] = *reinterpret_cast<const uint4*>(st + code_k + off + in * (D / 2));
-          sc[i] = *reinterpret_cast<const unsigned short*>(st + scale_k + off + in * (D / 16));
+          w[i] = *reinterpret_cast<const uint4*>(st + code_k + code_at(STEP * i));
+          sc[i] = *reinterpret_cast<const unsigned short*>(st + scale_k + scale_at(STEP * i));
         }
         auto load_V = [&]() {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const int off = page_at(STEP * i), in = STEP * i & (P - 1);
-            wv[i] = *reinterpret_cast<const uint4*>(st + code_v + off + in / 2 * D);
-            sv2[i] = *reinterpret_cast<const unsigned short*>(st + scale_v + off + in / 2 * (D / 8));
+            wv[i] = *reinterpret_cast<const uint4*>(st + code_v + code_at(STEP * i));
+            sv2[i] = *reinterpret_cast<const unsigned short*>(st + scale_v + scale_at(STEP * i));
           }
           __syncwarp();  // every lane has read its pieces
           if (lane == 0) mbar_arrive(&raw_empty[stage]);
         };
         if constexpr (TWO) {
-          if (n >= NK) ok = tree_wait(&k_empty[sk], (n / NK - 1) & 1, err, kTreeKEmpty);
+          if (n >= NK) ok = tree_wait(&k_empty[sk], (n / NK - 1) & 1);
           if (!ok) break;
         } else {
           load_V();
@@ -717,7 +741,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[sk]);
         if constexpr (TWO) load_V();
-        if (n >= NV) ok = tree_wait(&v_empty[sv], (n / NV - 1) & 1, err, kTreeVEmpty);
+        if (n >= NV) ok = tree_wait(&v_empty[sv], (n / NV - 1) & 1);
         if (!ok) break;
         // units whose tokens are not all seen by all rows, as the softmax warps decide it
         if (unit < u_win || unit >= u_tree) {
@@ -771,8 +795,6 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
     const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const uint32_t aS = lane_addr + t * 256, aO = aS + 128;
     const float sl2 = p.scale_log2 * kKv4SmallUndo;
-    const int G = p.H_q / p.c.H_kv;
-    const float inv_G = 1.f / (float)G;
     float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);  // [2][128] maxima, sums, NaN groups of the two halves
     float* xl = xm + 256;
     uint32_t* xn = reinterpret_cast<uint32_t*>(xl + 256);
@@ -784,8 +806,8 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
       const int cnt = part.cnt, rr = (TWO ? t * 128 : 0) + r;
       const bool row_ok = rr < part.R, warp_ok = rr - lane < part.R;
       // this row's node, and its head
-      int node = small_div(part.rem0 + (row_ok ? rr : 0), inv_G);
-      const int h = part.hk * G + part.rem0 + (row_ok ? rr : 0) - node * G;
+      int node = small_div(part.rem0 + (row_ok ? rr : 0), part.inv_G);
+      const int h = part.hk * part.G + part.rem0 + (row_ok ? rr : 0) - node * part.G;
       node += part.node0;
       float m_run = -INFINITY, l = 0.f;
       uint32_t nans = 0u;  // groups of 16 dims in which this row sees a NaN
@@ -816,7 +838,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
           }
           set_range(vis, lo - k0, L - k0);
           if (!p.parents) {
-            set_range(vis, (p.window >= 0 && node > p.window ? node - p.window : 0) - a0, min(node + 1, end) - a0);
+            set_range(vis, (p.window >= 0 && node > p.window ? min(node - p.window, end) : 0) - a0, min(node + 1, end) - a0);
           } else {
             int step = 0;
             for (int a = node; a >= max(a0, 0) && (p.window < 0 || step <= p.window); a = tree_parent(p, row0, a), ++step) {
@@ -830,7 +852,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
             }
           }
         }
-        ok = tree_wait(&s_ready[t], ns & 1, err, kTreeS);
+        ok = tree_wait(&s_ready[t], ns & 1);
         ++ns;
         if (!ok) break;
         if (!warp_ok) {  // no row of this warp exists: its P may be anything
@@ -907,7 +929,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         }
         if (edge) {  // NaN values that this row sees
           const int nu = n_before + k;  // the CTA's unit
-          ok = tree_wait(&v_full[nu % NV], (nu / NV) & 1, err, kTreeVFull);
+          ok = tree_wait(&v_full[nu % NV], (nu / NV) & 1);
           if (!ok) break;
           const uint8_t* by = smem + C::OFF_NAN + (nu % NV) * (D / 16) * 64;
           uint32_t any = 0u;
@@ -932,7 +954,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
       // ---- the part's end: of a whole segment the outputs, of a piece its sums
       const bool both = !TWO && cnt > 1;  // the other warpgroup has sums of these rows too
       if (ok && cnt > 0) {
-        ok = tree_wait(&o_done[t], no & 1u, err, kTreeO);
+        ok = tree_wait(&o_done[t], no & 1u);
         no ^= 1u;
       }
       float m = m_run, f_own = 1.f, f_other = 0.f;
@@ -943,7 +965,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&x_ready[t]);
-        ok = ok && tree_wait(&x_ready[1 - t], nx & 1, err, kTreeShare);
+        ok = ok && tree_wait(&x_ready[1 - t], nx & 1);
         const float m2 = xm[(1 - t) * 128 + r], l2 = xl[(1 - t) * 128 + r];
         nans |= xn[(1 - t) * 128 + r];
         m = fmaxf(m_run, m2);
@@ -1012,12 +1034,13 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
       if (both) {  // the other warpgroup has read this one's sums: they may be overwritten
         __syncwarp();
         if (lane == 0) mbar_arrive(&x_read[t]);
-        ok = tree_wait(&x_read[1 - t], nx & 1, err, kTreeShare);
+        ok = tree_wait(&x_read[1 - t], nx & 1);
         ++nx;
       }
     }
   }
 
+  tree_report(p, ok, warp < C::DEC_WARP ? kTreeSoftmax : warp < C::MMA_WARP ? kTreeDecode : kTreeIssue);
   tc_fence_before();
   __syncthreads();
   if (warp == C::MMA_WARP) {
@@ -1051,7 +1074,7 @@ struct FewCfg {
   static constexpr int DIM = D, ROWS = 8 * NT, WARPS = 4, THREADS = 32 * (WARPS + 1), LOAD_WARP = WARPS;
   static constexpr int CTAS = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // CTAs an SM
   static constexpr int STAGES = NT == 4 ? 6 : 3, STAGE = kUnit * D * 9 / 8;
-  static constexpr bool Q_SMEM = NT > 2;  // query fragments that do not fit the registers
+  static constexpr bool Q_SMEM = NT > 1;  // query fragments that do not fit the registers
   static constexpr int OFF_RAW = 0;
   static constexpr int OFF_Q = OFF_RAW + STAGES * STAGE;
   static constexpr int XS = D + 4;  // row stride of the exchange (bank spread)
@@ -1081,7 +1104,6 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
   uint64_t* q_ready = x_read + 1;
   TreePart* parts = reinterpret_cast<TreePart*>(smem + C::OFF_PART);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int* err = p.err;
   grid_launch_dependents();  // the join may be set up meanwhile
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
@@ -1110,12 +1132,12 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
   float* xm = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* xl = xm + C::WARPS * C::ROWS;
   [[maybe_unused]] uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
-  const int g = lane / 4, t = lane % 4, G = p.H_q / p.c.H_kv;
-  const float inv_G = 1.f / (float)G, sl2 = p.scale_log2 * kKv4SmallUndo;
+  const int g = lane / 4, t = lane % 4;
+  const float sl2 = p.scale_log2 * kKv4SmallUndo;
   // where this warp's tokens lie in a stage: tokens warp * 32 + 16 sub on start at token `in` of a
   // page, and sub 1 follows in the same page or is the next one
   const int P = p.c.page_size, in = warp * 32 & (P - 1);
-  const int at_page = warp * 32 / P * kv4_block_bytes(P, D);
+  const int at_page = (warp * 32 >> p.c.page_shift) * kv4_block_bytes(P, D);
   const bool next_page = P == 16;
   const int d_k = next_page ? kv4_block_bytes(16, D) : 16 * (D / 2), d_sk = next_page ? d_k : 16 * (D / 16);
   const int off_k = at_page + (in + g) * (D / 2) + t * (D / 8);
@@ -1126,40 +1148,45 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
   int i = 0, n_part = 0;  // units, parts consumed
   bool ok = true;
   for (;; ++n_part) {
-    ok = tree_wait(&part_full[n_part % kParts], (n_part / kParts) & 1, err, kTreePartFull);
+    ok = tree_wait(&part_full[n_part % kParts], (n_part / kParts) & 1);
     const TreePart& part = parts[n_part % kParts];
     if (!ok || part.cnt < 0) break;
-    const int cnt = part.cnt, rem0 = part.rem0, node0 = part.node0, R = part.R, hk = part.hk, row0 = part.row0;
+    const int cnt = part.cnt;
+    // (the rest of the part is read from shared memory where it is needed: few registers are left)
     // query fragments: lane (g, t) holds row 8 nt + g; dims [t D/4, (t + 1) D/4), in pairs (x, x + 4) of each
     // 8, the pairing of a code word's nibbles
     uint32_t qf[C::Q_SMEM ? 1 : MT][NT][2];
+    {
+      const int rem0 = part.rem0, node0 = part.node0, R = part.R, hk = part.hk, row0 = part.row0, G = part.G;
+      const float inv_G = part.inv_G;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (C::Q_SMEM && nt != warp) continue;  // (every warp stores a quarter; all have left the part before, see x_ready)
-      const int r = 8 * nt + g, node = small_div(rem0 + r, inv_G);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((size_t)(row0 + node0 + node) * p.H_q + hk * G + (rem0 + r - node * G)) * D + t * (D / 4));
+      for (int nt = 0; nt < NT; ++nt) {
+        if (C::Q_SMEM && nt != warp) continue;  // (every warp stores a quarter; all have left the part before, see x_ready)
+        const int r = 8 * nt + g, node = small_div(rem0 + r, inv_G);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + ((size_t)(row0 + node0 + node) * p.H_q + hk * G + (rem0 + r - node * G)) * D + t * (D / 4));
 #pragma unroll
-      for (int j = 0; j < MT / 2; ++j) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R) w = __ldg(src + j);
-        const uint32_t p0 = __byte_perm(w.x, w.z, 0x5410), p1 = __byte_perm(w.x, w.z, 0x7632);
-        const uint32_t p2 = __byte_perm(w.y, w.w, 0x5410), p3 = __byte_perm(w.y, w.w, 0x7632);
-        if constexpr (C::Q_SMEM) {
-          qs[((2 * j) * NT + nt) * 32 + lane] = make_uint2(p0, p1);
-          qs[((2 * j + 1) * NT + nt) * 32 + lane] = make_uint2(p2, p3);
-        } else {
-          qf[2 * j][nt][0] = p0;
-          qf[2 * j][nt][1] = p1;
-          qf[2 * j + 1][nt][0] = p2;
-          qf[2 * j + 1][nt][1] = p3;
+        for (int j = 0; j < MT / 2; ++j) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (r < R) w = __ldg(src + j);
+          const uint32_t p0 = __byte_perm(w.x, w.z, 0x5410), p1 = __byte_perm(w.x, w.z, 0x7632);
+          const uint32_t p2 = __byte_perm(w.y, w.w, 0x5410), p3 = __byte_perm(w.y, w.w, 0x7632);
+          if constexpr (C::Q_SMEM) {
+            qs[((2 * j) * NT + nt) * 32 + lane] = make_uint2(p0, p1);
+            qs[((2 * j + 1) * NT + nt) * 32 + lane] = make_uint2(p2, p3);
+          } else {
+            qf[2 * j][nt][0] = p0;
+            qf[2 * j][nt][1] = p1;
+            qf[2 * j + 1][nt][0] = p2;
+            qf[2 * j + 1][nt][1] = p3;
+          }
         }
       }
     }
     if constexpr (C::Q_SMEM) {
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
-      ok = tree_wait(q_ready, n_part & 1, err, kTreeQFull);
+      ok = tree_wait(q_ready, n_part & 1);
       if (!ok) break;
     }
     float acc[MT][NT][4], m[NT][2], l[NT][2];
@@ -1174,14 +1201,12 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
     }
 
     int unit = part.unit0;
-    const int u_win = part.u_win, u_tree = part.u_tree;
     for (int k = 0; k < cnt; ++k, ++i, ++unit) {
       const int stage = i % NST, k0 = unit * kUnit + warp * 32;  // this warp's first token of the unit
-      ok = tree_wait(&raw_full[stage], (i / NST) & 1, err, kTreeRawFull);
+      ok = tree_wait(&raw_full[stage], (i / NST) & 1);
       if (!ok) break;
-      const bool edge = unit < u_win || unit >= u_tree;  // some token is hidden from some row
-      const int len = part.len;
-      if (!edge || (k0 < len && k0 + 32 > part.lo)) {
+      const bool edge = unit < part.u_win || unit >= part.u_tree;  // some token is hidden from some row
+      if (!edge || (k0 < part.len && k0 + 32 > part.lo)) {
         const uint8_t* st = smem + C::OFF_RAW + stage * C::STAGE;
         float s[2][NT][4];
         // ---- scores of 2 x 16 tokens: lane (g, t) decodes tokens g, g + 8, its quarter of the dims
@@ -1235,9 +1260,10 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
         // maximum (in log2 units) moves only when some score passes it by 2^8
         uint32_t keep[2][2] = {{0xFFFFu, 0xFFFFu}, {0xFFFFu, 0xFFFFu}};  // the V scales that count, as read below
         if (edge) {
+          const int len = part.len;
           uint32_t sees = 0u;  // lane r: the warp's 32 tokens that row r sees
           if (lane < C::ROWS) {
-            const int node = node0 + small_div(rem0 + min(lane, R - 1), inv_G), L = part.L, a0 = k0 - L, end = len - L;
+            const int row0 = part.row0, node = part.node0 + small_div(part.rem0 + min(lane, part.R - 1), part.inv_G), L = part.L, a0 = k0 - L, end = len - L;
             int lo = 0;
             if (p.window >= 0) {
               int depth = node;
@@ -1254,7 +1280,7 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
             };
             range(lo - k0, L - k0);
             if (!p.parents) {
-              range((p.window >= 0 && node > p.window ? node - p.window : 0) - a0, min(node + 1, end) - a0);
+              range((p.window >= 0 && node > p.window ? min(node - p.window, end) : 0) - a0, min(node + 1, end) - a0);
             } else {
               int step = 0;
               for (int a = node; a >= max(a0, 0) && (p.window < 0 || step <= p.window); a = tree_parent(p, row0, a), ++step)
@@ -1393,7 +1419,7 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
     if (!ok) break;
 
     // ---- the warps' sums become one: each leaves its own, with its maxima and denominators
-    if (n_part > 0) ok = tree_wait(x_read, (n_part - 1) & 1, err, kTreeShare);
+    if (n_part > 0) ok = tree_wait(x_read, (n_part - 1) & 1);
     if (!ok) break;
     {
       float* mine = xch + warp * C::ROWS * C::XS;
@@ -1422,11 +1448,13 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(x_ready);
-    ok = tree_wait(x_ready, n_part & 1, err, kTreeShare);
+    ok = tree_wait(x_ready, n_part & 1);
     if (!ok) break;
     // ---- the whole of a segment: outputs; a piece of it: partial sums
     const bool whole = part.slot < 0;
     float* slot = partial + ((size_t)2 * blockIdx.x + max(part.slot, 0)) * C::PART;
+    const int rem0 = part.rem0, node0 = part.node0, R = part.R, hk = part.hk, row0 = part.row0, G = part.G;
+    const float inv_G = part.inv_G;
     for (int r = warp; r < R; r += C::WARPS) {
       float mm = xm[r], ll = 0.f, f[C::WARPS];
 #pragma unroll
@@ -1467,6 +1495,7 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
       mbar_arrive(&part_empty[n_part % kParts]);
     }
   }
+  tree_report(p, ok, kTreeFew);
 }
 
 // Joins the pieces of every segment that spans several CTAs, in CTA order: block (c, y) the segment whose
