@@ -7,9 +7,9 @@
 //
 // All n nodes and all G query heads of a kv head share every byte of the cache: n G rows.  Reading the cache
 // bounds a call of few rows, the tensor cores one of many (256 rows: 178 us of products, 56 us of
-// bytes for 329,377 tokens of 8 kv heads of 128).  So there are five forms, by the sequences' rows a kv head
+// bytes for 329,377 tokens of 8 kv heads of 128).  So there are four forms, by the sequences' rows a kv head
 // on average (block_rows):
-//   - Up to 8, 16 and 32 rows (kv4_tree_few_kernel): rows are the 8-wide columns of mma.sync products whose
+//   - Up to 8 and 16 rows (kv4_tree_few_kernel): rows are the 8-wide columns of mma.sync products whose
 //     16 rows are tokens (scores) or head dims (outputs); operands are decoded in registers.
 //   - Up to 128 rows, and more (kv4_tree_kernel): tcgen05 products of 128-row tiles.  Four warps decode
 //     K and V into bf16 operand tiles in shared memory (128-byte swizzle; the eight lanes of a quarter
@@ -56,7 +56,7 @@ namespace {
 constexpr int kUnit = 128;    // tokens of a unit
 // a segment's fixed costs, in units
 template <int ROWS>
-constexpr int kSegCost = ROWS == 8 ? 1 : ROWS == 16 ? 2 : ROWS == 256 ? 3 : 4;
+constexpr int kSegCost = ROWS == 8 ? 1 : ROWS == 16 ? 2 : ROWS == 256 ? 5 : 4;
 // What an expired wait is reported as: the role that gave up.
 enum TreeSite { kTreeLoad = 0xB0, kTreeIssue, kTreeDecode, kTreeSoftmax, kTreeFew };
 
@@ -1051,7 +1051,7 @@ __global__ void __launch_bounds__(TreeCfg<D, TWO>::THREADS, 1) kv4_tree_kernel(c
 }
 
 // ------------------------------------------------------------------------------------------ few rows
-// Up to 32 rows a kv head fill little of a 128-row tile, and its chain S - softmax - P V bounds a unit
+// Up to 16 rows a kv head fill little of a 128-row tile, and its chain S - softmax - P V bounds a unit
 // whatever its rows are.  So few rows are the columns of mma.sync products instead, whose 16 rows are tokens
 // (scores) or head dims (outputs): four computing warps take 32 tokens of every unit each, decode their
 // operands in registers, and keep their own sums.
@@ -1072,8 +1072,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 template <int D, int NT>
 struct FewCfg {
   static constexpr int DIM = D, ROWS = 8 * NT, WARPS = 4, THREADS = 32 * (WARPS + 1), LOAD_WARP = WARPS;
-  static constexpr int CTAS = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // CTAs an SM
-  static constexpr int STAGES = NT == 4 ? 6 : 3, STAGE = kUnit * D * 9 / 8;
+  static constexpr int CTAS = NT == 1 ? 3 : 2;  // CTAs an SM
+  static constexpr int STAGES = 3, STAGE = kUnit * D * 9 / 8;
   static constexpr bool Q_SMEM = NT > 1;  // query fragments that do not fit the registers
   static constexpr int OFF_RAW = 0;
   static constexpr int OFF_Q = OFF_RAW + STAGES * STAGE;
@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(FewCfg<D, NT>::THREADS, FewCfg<D, NT>::CTAS)
       const float inv_G = part.inv_G;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (C::Q_SMEM && nt != warp) continue;  // (every warp stores a quarter; all have left the part before, see x_ready)
+        if (C::Q_SMEM && nt != warp) continue;  // (warp nt stores tile nt; all have left the part before, see x_ready)
         const int r = 8 * nt + g, node = small_div(rem0 + r, inv_G);
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + ((size_t)(row0 + node0 + node) * p.H_q + hk * G + (rem0 + r - node * G)) * D + t * (D / 4));
@@ -1650,10 +1650,13 @@ int launch_tiles(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
 }
 
 // Rows of a block, by the sequences' rows a kv head on average: a block of more than a sequence has works on
-// rows that do not exist, a smaller one decodes the cache again for the rest.
+// rows that do not exist, a smaller one decodes the cache again for the rest.  Measured on both sides of a bound (heads
+// of 128 / 64): 131,072 tokens with 16 rows 52 / 37 us as columns, 78 / 59 as a tile; with 32 rows 87 / 57 as columns, 78 /
+// 59 as a tile, and 76 sequences of 100 tokens 39 / 31 and 29 / 23.  One tile 178 us and two 260 for 329,377 tokens of 8
+// heads, so that 256 rows as two blocks of one tile would take 356.
 int block_rows(int B, int T, int H_q, int H_kv) {
   const long long rows = (long long)T * (H_q / H_kv), n = B > 0 ? B : 1;
-  return rows <= 8 * n ? 8 : rows <= 16 * n ? 16 : rows <= 32 * n ? 32 : rows <= 128 * n ? 128 : 256;
+  return rows <= 8 * n ? 8 : rows <= 16 * n ? 16 : rows <= 128 * n ? 128 : 256;
 }
 
 }  // namespace
@@ -1667,7 +1670,6 @@ int launch_kv4_tree(const Kv4TreeParams& p, void* workspace, cudaStream_t stream
   switch (block_rows(p.B, p.T, p.H_q, p.c.H_kv)) {
     case 8: return p.c.d == 128 ? launch_few<128, 1>(p, workspace, stream) : launch_few<64, 1>(p, workspace, stream);
     case 16: return p.c.d == 128 ? launch_few<128, 2>(p, workspace, stream) : launch_few<64, 2>(p, workspace, stream);
-    case 32: return p.c.d == 128 ? launch_few<128, 4>(p, workspace, stream) : launch_few<64, 4>(p, workspace, stream);
     case 128: return p.c.d == 128 ? launch_tiles<128, false>(p, workspace, stream) : launch_tiles<64, false>(p, workspace, stream);
     default: return p.c.d == 128 ? launch_tiles<128, true>(p, workspace, stream) : launch_tiles<64, true>(p, workspace, stream);
   }
