@@ -1212,7 +1212,7 @@ def rope_table(inv_freq, positions, *, gain=1.0, stream=None):
         with _on(dev, stream):
             return rope_table(inv_freq, positions, gain=gain)
     T, n = positions.numel(), inv_freq.shape[0]
-    table = inv_freq.new_empty((T, 2, n), dtype=torch.float32)
+    table = torch.empty((T, 2, n), dtype=torch.float32, device=inv_freq.device)
     _run_rope_table(inv_freq, positions, table, T, n, dev, gain)
     return table
 
@@ -1251,21 +1251,26 @@ def _row_stride(t, name):
 def _check_rope(q, k, table):
     """Checks of heads and their table; returns (T, H_q, H_k, d, n, table rows)."""
     _check(table, "table", torch.float32, 3)
-    if table.shape[1] != 2:
+    R, two, n = table.shape
+    if two != 2:
         raise ValueError(f"table must be [rows, 2, n], got {tuple(table.shape)}")
-    if q.dim() < 3:
-        raise ValueError(f"q must be [rows, H, d] or [B, S, H, d], got {tuple(q.shape)}")
-    rows, (H, d) = q.shape[:-2], q.shape[-2:]
-    T = math.prod(rows)
+    shape = q.shape
+    dims = len(shape)
+    if dims < 3:
+        raise ValueError(f"q must be [rows, H, d] or [B, S, H, d], got {tuple(shape)}")
+    T, H, d = shape[0] if dims == 3 else math.prod(shape[:-2]), shape[-2], shape[-1]
     if T > 0x7FFFFFFF:
         raise ValueError(f"at most 2^31 - 1 rows, got {T}")
-    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != rows or k.shape[-1] != d):
-        raise ValueError(f"k must have q's rows and head dim, got {tuple(k.shape)} and {tuple(q.shape)}")
-    R = table.shape[0]
-    if R != T and not (len(rows) == 2 and R == rows[1]):
+    H_k = 0
+    if k is not None:
+        other = k.shape
+        if len(other) != dims or other[-1] != d or (other[0] != T if dims == 3 else other[:-2] != shape[:-2]):
+            raise ValueError(f"k must have q's rows and head dim, got {tuple(other)} and {tuple(shape)}")
+        H_k = other[-2]
+    if R != T and not (dims == 4 and R == shape[1]):
         raise ValueError(f"table must have one row per row of q ({T})"
-                         + (f" or per position ({rows[1]})" if len(rows) == 2 else "") + f", got {R}")
-    return T, H, 0 if k is None else k.shape[-2], d, table.shape[2], R
+                         + (f" or per position ({shape[1]})" if dims == 4 else "") + f", got {R}")
+    return T, H, H_k, d, n, R
 
 
 def attn_rope(q, k, table, q_out, k_out, *, interleaved=False, first_dim=0, inverse=False, stream=None):
@@ -1304,8 +1309,8 @@ def _rope_new(q, k, table, interleaved, first_dim, inverse, stream):
             return _rope_new(q, k, table, interleaved, first_dim, inverse, None)
     H, H_k, d = sizes[1:4]
     strides = [_row_stride(q, "q"), 0 if k is None else _row_stride(k, "k"), H * d, H_k * d]
-    q_out = q.new_empty(q.shape)
-    k_out = None if k is None else k.new_empty(k.shape)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
     _run_rope(q, k, table, q_out, k_out, sizes[:5], sizes[5], strides, dev, interleaved, first_dim, inverse)
     return q_out, k_out
 
@@ -1423,7 +1428,7 @@ def kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, *, i
         with _on(dev, stream):
             return kv4_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, interleaved=interleaved,
                                    first_dim=first_dim)
-    q_out = None if q is None else q.new_empty(q.shape)
+    q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
     _run_append_rope(q, k, v, table, cu_seqlens, pool, page_table, seq_lens, q_out, sizes, strides,
                      sizes[2] * sizes[4], dev, interleaved, first_dim)
     return q_out
