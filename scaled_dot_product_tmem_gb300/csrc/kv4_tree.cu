@@ -30,16 +30,18 @@
 //   - Units with tokens that some row does not see (the tree's own, the ends of a window) take each row's 128 bits
 //     of what it sees, found by walking up from its node: the walk is a dependent load a level.
 //
-// Measured on the device (329,377 tokens of 4 sequences, 8 kv heads of 128, 4 query heads each): 2 nodes 82 us,
-// 4 nodes 109, 8 nodes 192, 16 and 32 nodes 192 and 197, 64 nodes 280 (1.2 PFLOP/s, 63 % of the measured bf16
-// rate), 128 nodes 521.  16 sequences of 1 to 8191 tokens with 16 nodes: 49 us.  What the steps brought, for
+// Measured on the device (329,377 tokens of 4 sequences, 8 kv heads of 128, 4 query heads each): 2 nodes 79 us,
+// 4 nodes 104, 8 and 16 nodes 167 and 172, 32 nodes 179, 64 nodes 255 (1.33 PFLOP/s, 70 % of the measured bf16
+// rate), 128 nodes 480.  16 sequences of 1 to 8191 tokens with 16 nodes: 41 us.  What the steps brought, for
 // 131,072 tokens and 64 / 16 nodes: sizes worked out by every warp 200 / 127 us; by the loading warp, rare
 // paths without the scores' registers 165 / 114; shorter loops of products 151 / 98; join's pieces
-// found at once and longer output steps 136 / 92; K and V of a unit loaded together 136 / 89.
-// What bounds it: one tile, decoding (some 2400 cycles a unit, a chain of loads, conversions and stores in four
-// warps; eight warps did not pay for the registers they take from the softmax) beside the chain S - softmax -
-// P V; two tiles, that chain with both tiles' products (2048 cycles a unit at full rate) and the decoded operands'
-// way through shared memory.  Few rows: the copies and the decoding arithmetic, as in kv4_decode.cu.
+// found at once and longer output steps 136 / 92; K and V of a unit loaded together 136 / 89; waits without
+// reports and other code out of the roles' loops 133 / 86; places of pieces by two offsets 130 / 81; more blocks of
+// the join 121 / 81.
+// What bounds it: one tile, decoding (some 2500 cycles a unit in four warps, their waits included; with eight warps the
+// chain S - softmax - P V of a warpgroup's units, 4900 cycles for two, gives the same); two tiles, that chain with both
+// tiles' products (2048 cycles a unit at full rate) and the decoded operands' way through shared memory.  Few rows:
+// the copies and the decoding arithmetic, as in kv4_decode.cu.
 #include <algorithm>
 #include <atomic>
 
@@ -1636,7 +1638,9 @@ int launch_t(const Kv4TreeParams& p, int ctas, void* workspace, cudaStream_t str
   TreePiece* pieces = static_cast<TreePiece*>(workspace);
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPieceBytes);
   if (launch_kernel(KERN, dim3((unsigned)grid), C::THREADS, C::SMEM, stream, false, p, pieces, partial) != 0) return -1;
-  return launch_kernel(kv4_tree_join_kernel<C::DIM, C::ROWS>, dim3((unsigned)grid, 8), 256, 0, stream, true, p,
+  // (256 rows: 16 blocks a segment, two rows a warp; with 8 one sequence of 131,072 tokens takes 127 us instead of 121.
+  // Fewer rows: more blocks take longer to start than they save.)
+  return launch_kernel(kv4_tree_join_kernel<C::DIM, C::ROWS>, dim3((unsigned)grid, C::ROWS == 256 ? 16 : 8), 256, 0, stream, true, p,
                        (const TreePiece*)pieces, (const float*)partial);
 }
 template <int D, int NT>

@@ -111,7 +111,17 @@ def test_tree_parity(lens, nodes, H, H_kv, d, page, chain):
     t.check(o, lse)
 
 
-# heads a kv head such that a sequence has 8, 16, 32, 128 and more rows on average: the kernels' forms
+@pytest.mark.parametrize("nodes", [[1, 1, 1], [3, 0, 2]])
+@pytest.mark.parametrize("G", [257, 300, 513])
+def test_more_heads_a_kv_head_than_rows_of_a_block(G, nodes):
+    """One node's heads span several blocks of rows."""
+    t = Trees([130, 0, 64], nodes, G, 1, 64, 32, seed=G)
+    o, lse = t.call()
+    _clean()
+    t.check(o, lse)
+
+
+# heads a kv head such that a sequence has 8, 16, 32, 128 and more rows on average (32: a tile as well): the kernels' forms
 @pytest.mark.parametrize("G", [1, 2, 4, 14, 40])
 @pytest.mark.parametrize("window", [0, 1, 3, 50, 128, 300, 2 ** 31 - 1])
 def test_windows(window, G):
