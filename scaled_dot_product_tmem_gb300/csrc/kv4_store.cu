@@ -7,6 +7,7 @@
 // each of 64 sequences moved in 32 layers in 15 us (23 with their places worked out anew for every head).
 #include "attn_kernels.h"
 #include "kv4.cuh"
+#include "launch.h"
 #include "ptx.cuh"
 #include "rope.cuh"
 
@@ -128,6 +129,7 @@ template <int D, int ROT>
 __global__ void __launch_bounds__(256, ROT == 0 ? 4 : ROT == 1 ? 2 : 3) kv4_append_kernel(const Kv4StoreParams p, const RopeParams rp, int gx, int gy) {
   constexpr int NG = D / 16, HS = 256 / (NG * kTok);  // heads a block takes at a time
   if constexpr (ROT != 0) {
+    grid_wait();  // the table, or whatever was before
     if ((int)blockIdx.x >= gx * gy) return rope_block<ROT == 2>(rp, blockIdx.x - gx * gy);
   }
   const int by = ROT ? blockIdx.x / gx : blockIdx.y, bx = ROT ? blockIdx.x - by * gx : blockIdx.x;
@@ -291,8 +293,7 @@ int launch_kv4_append_rope(const Kv4StoreParams& p, const RopeParams& rp, bool i
   if (blocks > 0x7fffffffLL) return -2;
   auto kern = p.c.d == 128 ? (interleaved ? kv4_append_kernel<128, 2> : kv4_append_kernel<128, 1>)
                            : (interleaved ? kv4_append_kernel<64, 2> : kv4_append_kernel<64, 1>);
-  kern<<<(unsigned)blocks, 256, 0, stream>>>(p, rp, (int)g.x, (int)g.y);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(kern, dim3((unsigned)blocks), 256, 0, stream, true, p, rp, (int)g.x, (int)g.y);
 }
 
 // Kept tokens: node kept[b][i] of sequence b's tree (its token start[b] + kept[b][i]) becomes token

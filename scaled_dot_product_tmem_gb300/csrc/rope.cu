@@ -1,5 +1,7 @@
 // rope.cu -- cosines and sines of positions, and heads rotated by them (rope.cuh).
 #include "attn_kernels.h"
+#include "launch.h"
+#include "ptx.cuh"
 #include "rope.cuh"
 
 namespace sdpa {
@@ -17,6 +19,7 @@ namespace sdpa {
 __global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq, const int* positions, float* table, int T,
                                                          int n, float gain) {
   __shared__ unsigned long long turns[128];
+  grid_launch_dependents();  // the rotation may be set up meanwhile
   if (threadIdx.x < n) {
     const double f = inv_freq[threadIdx.x] * 0.15915494309189533577;  // 1 / (2 pi)
     turns[threadIdx.x] = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
@@ -45,6 +48,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq,
 // another third more where half of a head stays.
 template <bool IL>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+  grid_wait();  // the table, or whatever was before
   rope_block<IL>(p, blockIdx.x);
 }
 
@@ -59,9 +63,7 @@ int launch_rope_table(const double* inv_freq, const int* positions, float* table
 int launch_rope(const RopeParams& p, bool interleaved, cudaStream_t stream) {
   const long long blocks = rope_blocks(p);
   if (blocks > 0x7fffffffLL) return -2;
-  if (interleaved) rope_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(p);
-  else rope_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(p);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(interleaved ? rope_kernel<true> : rope_kernel<false>, dim3((unsigned)blocks), 256, 0, stream, true, p);
 }
 
 }  // namespace sdpa
