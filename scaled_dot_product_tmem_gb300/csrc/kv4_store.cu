@@ -3,8 +3,8 @@
 // 15,677 tokens appended in 16 us (83 MB; 18 us without the loads ahead of the lookup) and
 // read back in 14 us; 1500 pages of 64 tokens copied in 4 layers in 134 us (885 MB moved,
 // 6.6 TB/s); one token of each of 64 sequences appended or read back in about 3 us (lookups).  With the keys
-// rotated on the way and 32 query heads beside them, 15,677 tokens in 67 us (347 MB).  Up to 9 kept tokens of
-// each of 64 sequences moved in 32 layers in 15 us (23 with their places worked out anew for every head).
+// rotated on the way and 32 query heads beside them, 15,677 tokens in 61 us (347 MB).  Up to 9 kept tokens of
+// each of 64 sequences moved in 32 layers in 14 us (23 with their places worked out anew for every head).
 #include "attn_kernels.h"
 #include "kv4.cuh"
 #include "launch.h"
@@ -301,11 +301,12 @@ int launch_kv4_append_rope(const Kv4StoreParams& p, const RopeParams& rp, bool i
 // looks 32 entries' pages up at once, for all heads and layers that the block then walks.  A thread owns
 // the same few bytes of every token of a head and layer, so its moves follow one another without a
 // barrier, whatever the entries are.  Entries that only move down (kept >= i, as ascending ones do)
-// cannot read what an earlier one of the same sixteen wrote, so sixteen are loaded at once.
+// cannot read what an earlier one of the same eight wrote, so eight are loaded at once (sixteen: 15.0 instead of 14.2 us
+// for up to 9 tokens of each of 64 sequences in 32 layers).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_keep_kernel(const Kv4KeepParams p) {
   // words (4 bytes) of K codes, of V codes, of K scales; then V's scale bytes
-  constexpr int KW = D / 8, VW = D / 8, SW = D / 64, NV = D / 16, BATCH = 16;
+  constexpr int KW = D / 8, VW = D / 8, SW = D / 64, NV = D / 16, BATCH = 8;
   static_assert(KW + VW + SW + NV <= 64, "64 threads a head and layer");
   struct Move {
     long long src, dst;  // a page's offset in a layer, or -1: this entry moves nothing
