@@ -289,6 +289,58 @@ def test_captured_and_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.parametrize("before", ["nothing", "copy", "fill", "join of streams", "another operator"])
+def test_captured_behind(before):
+    """Rotation and append with rotation as a graph's first node, behind a copy, a fill, two streams, attention."""
+    sdpa = _sdpa()
+    T, H, Hk, d = 48, 4, 2, 64
+    x, k = _randn(T, H, d, seed=1).cuda(), _randn(T, Hk, d, seed=2).cuda()
+    q = torch.zeros_like(x)
+    inv, _ = sdpa.rope_frequencies(d)
+    table = sdpa.rope_table(inv, _i32(list(range(T))))
+    pages, cu, start = _i32([[0, 1, 2, 3]]), _i32([0, T]), _i32([0])
+    pool = sdpa.kv4_pool(4, Hk, d, 16)
+    side = torch.cuda.Stream()
+    o = torch.empty_like(x)
+
+    def step():
+        if before == "copy":
+            q.copy_(x)
+        elif before == "fill":
+            q.zero_()
+            q.add_(x)
+        elif before == "join of streams":
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                q.copy_(x)
+            o.copy_(x)
+            main.wait_stream(side)
+        elif before == "another operator":
+            q.copy_(sdpa.sdpa_forward_packed(x, k, k, cu)[0])
+        a = sdpa.rope_forward(q, k, table)
+        return (*a, sdpa.kv4_append_rope(q, k, k, table, cu, pool, pages, start))
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for seed in (5, 6):
+        x.copy_(_randn(T, H, d, seed=seed).cuda())
+        if before == "nothing":
+            q.copy_(x)
+        pool.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        held = pool.clone()
+        pool.zero_()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+        assert torch.equal(pool, held)
+    _clean()
+
+
 def test_gradient_of_the_gradient():
     """The rotation is linear: the gradient of <rotated back w, u> by w is u rotated."""
     sdpa = _sdpa()
