@@ -117,10 +117,19 @@ constexpr float kKv4SmallUndo = 8388608.f;  // 2^23
 
 constexpr int kKv4BadScale = 0xFF;  // 16 values with an infinity or NaN among them: a NaN scale
 
+// A load of what no kernel writes while this one lives; with EARLY, in a kernel that is launched while the one before it
+// runs, an ordinary load, since that one may write it (a read-only load is then undefined).
+template <bool EARLY, class T>
+__device__ __forceinline__ T load_input(const T* p) {
+  if constexpr (EARLY) return *p;
+  else return __ldg(p);
+}
+
 // The page that holds token `pos` of sequence b, or -1 (outside the table or the pool).
+template <bool EARLY = false>
 __device__ __forceinline__ int kv4_page(const Kv4Pool& c, int b, int pos) {
   if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) return -1;
-  const int pg = __ldg(c.page_table + (size_t)b * c.max_pages + (pos >> c.page_shift));
+  const int pg = load_input<EARLY>(c.page_table + (size_t)b * c.max_pages + (pos >> c.page_shift));
   return (pg < 0 || pg >= c.n_pages) ? -1 : pg;
 }
 

@@ -26,13 +26,14 @@ struct TokenAt {
 // last b with cu[b] <= t (checked against its end): 16 lanes search the offsets 16 ways at a
 // time, so that a few dependent loads find it.  Offsets that are not ascending may give any
 // sequence, never a row outside the one returned.
+template <bool EARLY = false>
 __device__ __forceinline__ void find_tokens(const Kv4StoreParams& p, int t0, TokenAt* at) {
   const int lane16 = threadIdx.x % 16, half = threadIdx.x & 16, i = threadIdx.x / 16;
   const int t = t0 + i;
   int lo = 0, n = p.B;  // the count of cu[0 .. B) that are <= t lies in [lo, lo + n]
   while (__any_sync(0xffffffffu, n > 0)) {
     const int step = (n + 15) / 16, at_ = lo + lane16 * step;
-    const bool le = lane16 * step < n && __ldg(p.cu + at_) <= t;
+    const bool le = lane16 * step < n && load_input<EARLY>(p.cu + at_) <= t;
     const int c = __popc((__ballot_sync(0xffffffffu, le) >> half) & 0xFFFFu);
     if (c == 0) {
       n = 0;
@@ -46,10 +47,10 @@ __device__ __forceinline__ void find_tokens(const Kv4StoreParams& p, int t0, Tok
     TokenAt a{-2, 0};
     const int b = lo - 1;
     if (t < p.T && b >= 0) {
-      const int first = __ldg(p.cu + b), end = __ldg(p.cu + b + 1), start = __ldg(p.start + b);
+      const int first = load_input<EARLY>(p.cu + b), end = load_input<EARLY>(p.cu + b + 1), start = load_input<EARLY>(p.start + b);
       if (first <= t && t < end) {
         const long long pos = (long long)start + (t - first);
-        const int pg = pos > 0x7fffffffLL ? -1 : kv4_page(p.c, b, (int)pos);  // (pos may be negative)
+        const int pg = pos > 0x7fffffffLL ? -1 : kv4_page<EARLY>(p.c, b, (int)pos);  // (pos may be negative)
         a.block = -1;
         if (pg >= 0) {
           a.block = (long long)pg * p.c.H_kv * kv4_block_bytes(p.c.page_size, p.c.d);
@@ -128,6 +129,7 @@ __device__ __forceinline__ int quantise16(const uint4& x0, const uint4& x1, uint
 template <int D, int ROT>
 __global__ void __launch_bounds__(256, ROT == 0 ? 4 : ROT == 1 ? 2 : 3) kv4_append_kernel(const Kv4StoreParams p, const RopeParams rp, int gx, int gy) {
   constexpr int NG = D / 16, HS = 256 / (NG * kTok);  // heads a block takes at a time
+  constexpr bool EARLY = ROT != 0;                    // launched while the kernel before it runs
   if constexpr (ROT != 0) {
     grid_wait();  // the table, or whatever was before
     if ((int)blockIdx.x >= gx * gy) return rope_block<ROT == 2>(rp, blockIdx.x - gx * gy);
@@ -160,8 +162,7 @@ __global__ void __launch_bounds__(256, ROT == 0 ? 4 : ROT == 1 ? 2 : 3) kv4_appe
           }
         } else {
           part[i] = 1;
-          const float4 a = __ldg(reinterpret_cast<const float4*>(row + x / 2));
-          const float4 b = __ldg(reinterpret_cast<const float4*>(row + rp.n + x / 2));
+          const float4 a = load4(row + x / 2), b = load4(row + rp.n + x / 2);
           c[i][0] = a.x, c[i][1] = a.y, c[i][2] = a.z, c[i][3] = a.w;
           sn[i][0] = b.x, sn[i][1] = b.y, sn[i][2] = b.z, sn[i][3] = b.w;
         }
@@ -175,18 +176,18 @@ __global__ void __launch_bounds__(256, ROT == 0 ? 4 : ROT == 1 ? 2 : 3) kv4_appe
   auto load = [&](int h) {
     const uint4* ks = reinterpret_cast<const uint4*>(kr + (size_t)h * D);
     const uint4* vs = reinterpret_cast<const uint4*>(vr + (size_t)h * D);
-    k0 = __ldg(ks);
-    k1 = __ldg(ks + 1);
+    k0 = load_input<EARLY>(ks);
+    k1 = load_input<EARLY>(ks + 1);
     if constexpr (ROT == 1) {
-      q0 = __ldg(reinterpret_cast<const uint4*>(kr + (size_t)h * D + part[0]));
-      q1 = __ldg(reinterpret_cast<const uint4*>(kr + (size_t)h * D + 8 + part[1]));
+      q0 = load_input<EARLY>(reinterpret_cast<const uint4*>(kr + (size_t)h * D + part[0]));
+      q1 = load_input<EARLY>(reinterpret_cast<const uint4*>(kr + (size_t)h * D + 8 + part[1]));
     }
-    v0 = __ldg(vs);
-    v1 = __ldg(vs + 1);
+    v0 = load_input<EARLY>(vs);
+    v1 = load_input<EARLY>(vs + 1);
   };
   int h = threadIdx.x / (NG * kTok) + HS * by;
   if (t0 + tk < p.T && h < p.c.H_kv) load(h);
-  find_tokens(p, t0, at);
+  find_tokens<EARLY>(p, t0, at);
   const TokenAt a = at[tk];
   if (a.block < 0) return;
   uint8_t* page = p.pool + a.block;

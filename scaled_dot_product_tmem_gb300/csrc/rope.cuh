@@ -58,8 +58,11 @@ __device__ __forceinline__ uint4 rope_turn_pairs(const uint4& x, const float* c,
   }
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
+// (Ordinary loads: the table is written while the kernel that reads it is already set up, and a read-only load
+// (__ldg) is defined only for data that nobody writes in the kernel's lifetime.)
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = load4(p), b = load4(p + 4);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 

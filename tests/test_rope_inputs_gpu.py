@@ -1,0 +1,115 @@
+"""Rotations whose inputs are written by the kernel right before them on the stream.
+
+The rotation and the append with rotation are set up while that kernel still runs, so nothing they read may
+be taken from before its end: a table buffer is written for one set of positions after another, keys and values
+come from a rotation in place, offsets, lengths and page tables from copies, each followed by its reader at once.
+Every result is compared bit for bit with the same calls waited for one by one."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+STEPS = 12
+
+
+def _sdpa():
+    import scaled_dot_product_tmem_gb300 as sdpa
+    return sdpa
+
+
+def _clean():
+    torch.cuda.synchronize()
+    st, site = _sdpa().attn_last_device_error()
+    assert st == 0, f"device error status {st} site {site:#x}"
+
+
+def _randn(*shape, seed=0):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T", [3, 700, 5001])
+@pytest.mark.parametrize("d,rot,first,il", [(64, 64, 0, False), (128, 128, 0, False), (128, 64, 8, True), (64, 32, 16, True)])
+def test_one_table_buffer_for_positions_one_after_another(d, rot, first, il, T, captured):
+    sdpa = _sdpa()
+    H, Hk, page = 4, 2, 32
+    kw = dict(interleaved=il, first_dim=first)
+    q, k, v = _randn(T, H, d, seed=1), _randn(T, Hk, d, seed=2), _randn(T, Hk, d, seed=3)
+    inv, gain = sdpa.rope_frequencies(rot)
+    pos = [torch.arange(T, dtype=torch.int32, device="cuda") * (i + 1) + 1009 * i for i in range(STEPS)]
+    n_pages = -(-T // page)
+    pages = torch.randperm(n_pages, generator=torch.Generator().manual_seed(4)).to(torch.int32).view(1, -1).cuda()
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    start = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = torch.zeros((T, 2, rot // 2), device="cuda")
+
+    def steps(wait):
+        out = []
+        for i, p in enumerate(pos):
+            pool = sdpa.kv4_pool(n_pages, Hk, d, page).zero_()
+            sdpa.attn_rope_table(inv, p, table, gain=gain)
+            wait()
+            if i % 2:
+                out += [*sdpa.rope_forward(q, k, table, **kw)]
+            else:
+                out += [sdpa.kv4_append_rope(q, k, v, table, cu, pool, pages, start, **kw), pool]
+            wait()
+        return out
+
+    want = steps(torch.cuda.synchronize)
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            got = steps(lambda: None)
+        g.replay()
+    else:
+        got = steps(lambda: None)
+    _clean()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("il", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_offsets_and_pages_written_right_before_the_append(d, il):
+    """Keys and values are the results of a rotation in place, which is itself set up early; then the offsets, the
+    lengths and the page table are copied into their buffers before the next append."""
+    sdpa = _sdpa()
+    H, Hk, page, T = 4, 3, 16, 900
+    inv, _ = sdpa.rope_frequencies(d)
+    table = sdpa.rope_table(inv, torch.arange(T, dtype=torch.int32, device="cuda"))
+    cuts = [[0, 1, T], [0, 500, T], [0, T - 1, T], [0, 0, T]]
+    n_pages = 2 * (T // page + 2)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    cu, start = i32([0, 0, 0]), i32([0, 0])
+    pages = torch.full((2, T // page + 2), -1, dtype=torch.int32, device="cuda")
+    gen = torch.Generator().manual_seed(5)
+    tables = [torch.randperm(n_pages, generator=gen).to(torch.int32).view(2, -1).cuda() for _ in cuts]
+    cus, starts = [i32(c) for c in cuts], [i32([i, 2 * i + 1]) for i in range(len(cuts))]
+
+    def steps(wait):
+        q, k, v = _randn(T, H, d, seed=6), _randn(T, Hk, d, seed=7), _randn(T, Hk, d, seed=8)
+        out = []
+        for i in range(len(cuts)):
+            pool = sdpa.kv4_pool(n_pages, Hk, d, page).zero_()
+            cu.copy_(cus[i])
+            start.copy_(starts[i])
+            pages.copy_(tables[i])
+            wait()
+            sdpa.attn_rope(k, v, table, k, v, interleaved=il)
+            wait()
+            out += [sdpa.kv4_append_rope(q, k, v, table, cu, pool, pages, start, interleaved=il), pool, k.clone()]
+            wait()
+            pages.copy_(tables[i - 1])
+            pool = sdpa.kv4_pool(n_pages, Hk, d, page).zero_()
+            start.copy_(starts[i - 1])
+            wait()
+            out += [sdpa.kv4_append_rope(q, k, v, table, cu, pool, pages, start, interleaved=il), pool]
+            wait()
+        return out
+
+    want = steps(torch.cuda.synchronize)
+    for _ in range(3):
+        got = steps(lambda: None)
+        _clean()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
