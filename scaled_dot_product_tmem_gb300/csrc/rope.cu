@@ -9,9 +9,11 @@ namespace sdpa {
 // table[t][0][f] = gain cos(p_t w_f), table[t][1][f] = gain sin(p_t w_f).
 //
 // An angle p w of a far position has lost its fraction of a turn long before 32 bits can hold it.
-// So a frequency becomes turns per position, w / 2 pi, as a 64-bit fraction of a turn (whole turns
-// dropped), and p times that in 64-bit whole numbers, wrapping, is the angle's fraction of a turn: exact
-// for every position, off only by what the frequency's own 53 bits leave (2^-54 of it).  The
+// So a frequency becomes f turns per position, w / 2 pi, as a 64-bit fraction of a turn (whole turns
+// dropped), and p times that in 64-bit whole numbers, wrapping, is the angle's fraction of a turn.  The product
+// is exact for every position; the frequency has two roundings (of 1 / 2 pi and of f, 2^-52 of it together) and is
+// cut to a multiple of 2^-64, so an angle is off by at most |p| (2^-64 + 2^-52 f) turns.  A negative frequency
+// is its magnitude negated: 1 less a small fraction would lose all but 2^-53 of a turn.  The
 // frequencies are converted once a block: 64-bit floating point has 2 operations a cycle and SM.
 // Sine and cosine of what is left after whole quarter turns are their power series: on |x| <= pi / 4 the
 // first left-out terms are x^11 / 11! < 2^-29 and x^10 / 10! < 2^-25.  (The library's sine and cosine of half
@@ -21,8 +23,9 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq,
   __shared__ unsigned long long turns[128];
   grid_launch_dependents();  // the rotation may be set up meanwhile
   if (threadIdx.x < n) {
-    const double f = inv_freq[threadIdx.x] * 0.15915494309189533577;  // 1 / (2 pi)
-    turns[threadIdx.x] = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+    const double a = inv_freq[threadIdx.x] * 0.15915494309189533577, f = fabs(a);  // 1 / (2 pi)
+    const unsigned long long u = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+    turns[threadIdx.x] = a < 0.0 ? 0ull - u : u;
   }
   __syncthreads();
   const int rows = 256 / n, f = threadIdx.x % n, r = threadIdx.x / n;

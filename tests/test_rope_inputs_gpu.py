@@ -113,3 +113,28 @@ def test_keys_offsets_and_pages_written_right_before_the_append(d, il):
         got = steps(lambda: None)
         _clean()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("gain", [1.0, 1.375])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_table_of_slow_and_negative_frequencies(sign, gain):
+    """Against extended precision, up to the last int32 position, within what the number format leaves.
+
+    A frequency becomes f turns a position with two roundings of 2^-53 (of 1 / 2 pi and of the product), held as a
+    multiple of 2^-64: an angle is off by at most |p| (2^-64 + 2^-52 f) turns.  What is left after quarter turns is at most
+    pi / 4 in fp32, off by 3 roundings (2.4 of 2^-24); sine and cosine turn that into at most 2.4 and 2 of 2^-24,
+    their series and its roundings add at most 1.1 and 2.1 of 2^-24, the product with the gain one: 6 of 2^-24 in all."""
+    from oracle import tree
+    sdpa = _sdpa()
+    gen = torch.Generator().manual_seed(9)
+    w = torch.cat([10.0 ** -(torch.rand(96, generator=gen, dtype=torch.float64) * 12),
+                   torch.tensor([1e-300, 2.0 ** -66, 1.0, 6.0, 7.0, 100.5, 1e-9, 0.0], dtype=torch.float64)]) * sign
+    pos = torch.cat([torch.tensor([0, 1, -1, 131071, 2 ** 30 + 1, 2 ** 31 - 1, -2 ** 31], dtype=torch.int64),
+                     torch.randint(-2 ** 31, 2 ** 31, (200,), generator=gen)]).to(torch.int32)
+    got = sdpa.rope_table(w.cuda(), pos.cuda(), gain=gain).double().cpu()
+    a = torch.from_numpy(tree.angles(pos.numpy(), w.numpy()))
+    turns = pos.double().abs()[:, None] * (2.0 ** -64 + 2.0 ** -52 * w.abs()[None] / (2 * torch.pi))
+    bound = gain * (6 * 2.0 ** -24 + 2 * torch.pi * turns)
+    for y, ref in ((got[:, 0], a.cos()), (got[:, 1], a.sin())):
+        assert bool(((y - gain * ref).abs() <= bound).all()), float(((y - gain * ref).abs() - bound).max())
+    _clean()
