@@ -1177,10 +1177,19 @@ def rope_frequencies(rot_dim, *, base=10000.0, scaling="none", factor=1.0, origi
     return w.to(device), 1.0 if gain is None else float(gain)
 
 
+def _written(*tensors):
+    """Tells autograd that a kernel wrote tensors of the caller's: a gradient that still needs what they held
+    is then refused instead of wrong."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def attn_rope_table(inv_freq, positions, table, *, gain=1.0, stream=None):
     """Cosines and sines of positions into the preallocated table (fp32 [T, 2, n]): table[t, 0] =
     gain cos(p_t inv_freq), table[t, 1] = gain sin(p_t inv_freq).  inv_freq: fp64 [n] on the device;
-    positions: int32 of T values.  Angles are reduced without rounding, also those of far positions."""
+    positions: int32 of T values.  Angles are reduced without rounding, also those of far positions.  (A
+    gradient of a rotation by what the table held before is refused afterwards.)"""
     _check(inv_freq, "inv_freq", torch.float64, 1)
     _check(positions, "positions", torch.int32, positions.dim())
     _check(table, "table", torch.float32, 3)
@@ -1192,6 +1201,7 @@ def attn_rope_table(inv_freq, positions, table, *, gain=1.0, stream=None):
         with _on(dev, stream):
             return attn_rope_table(inv_freq, positions, table, gain=gain)
     _run_rope_table(inv_freq, positions, table, T, n, dev, gain)
+    _written(table)
 
 
 def _run_rope_table(inv_freq, positions, table, T, n, dev, gain):
@@ -1292,6 +1302,7 @@ def attn_rope(q, k, table, q_out, k_out, *, interleaved=False, first_dim=0, inve
         with _on(dev, stream):
             return attn_rope(q, k, table, q_out, k_out, interleaved=interleaved, first_dim=first_dim, inverse=inverse)
     _run_rope(q, k, table, q_out, k_out, (T, H, H_k, d, n), R, strides, dev, interleaved, first_dim, inverse)
+    _written(q_out, k_out)
 
 
 def _run_rope(q, k, table, q_out, k_out, sizes, R, strides, dev, interleaved, first_dim, inverse):

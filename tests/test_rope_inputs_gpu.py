@@ -138,3 +138,28 @@ def test_table_of_slow_and_negative_frequencies(sign, gain):
     for y, ref in ((got[:, 0], a.cos()), (got[:, 1], a.sin())):
         assert bool(((y - gain * ref).abs() <= bound).all()), float(((y - gain * ref).abs() - bound).max())
     _clean()
+
+
+def test_a_gradient_whose_table_was_rewritten_is_refused():
+    """Two micro-batches whose tables share a buffer: the first one's gradient must not turn by the second's angles."""
+    sdpa = _sdpa()
+    T, H, d = 5, 2, 64
+    inv, _ = sdpa.rope_frequencies(d)
+    q = _randn(T, H, d, seed=1).requires_grad_()
+    table = torch.empty((T, 2, d // 2), device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    for other_stream in (False, True):
+        sdpa.attn_rope_table(inv, pos, table)
+        y, _ = sdpa.rope(q, None, table)
+        s = torch.cuda.Stream() if other_stream else None
+        torch.cuda.synchronize()
+        sdpa.attn_rope_table(inv, pos + 100, table, stream=s)
+        torch.cuda.synchronize()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward(torch.ones_like(y))
+    assert q.grad is None
+    with torch.inference_mode():  # tensors without a version
+        t = torch.empty((T, 2, d // 2), device="cuda")
+        sdpa.attn_rope_table(inv, pos, t)
+        sdpa.attn_rope(q, None, t, torch.empty_like(q), None)
+    _clean()
