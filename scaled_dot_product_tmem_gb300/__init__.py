@@ -1291,8 +1291,11 @@ def attn_rope(q, k, table, q_out, k_out, *, interleaved=False, first_dim=0, inve
     shared by the batch.  Dims first_dim .. first_dim + 2n of every head are turned, as pairs (f, n + f) or,
     interleaved, (2f, 2f + 1); the others are copied.  inverse: the transposed rotation, which
     takes the gradient of the results to that of q and k.  Rows may be apart (a slice of a fused
-    projection), evenly and by a multiple of 8 elements."""
+    projection), evenly and by a multiple of 8 elements.  Not differentiable (rope is): results that are part of
+    a graph, as q of a projection in training rotated in place, are refused."""
     T, H, H_k, d, n, R = _check_rope(q, k, table)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q_out, k_out)):
+        raise ValueError("q_out and k_out must not require gradients: rope() is the differentiable rotation")
     if q_out is None or q_out.shape != q.shape or (k is not None and (k_out is None or k_out.shape != k.shape)):
         raise ValueError("q_out and k_out must have the shapes of q and k")
     strides = [_row_stride(q, "q"), 0 if k is None else _row_stride(k, "k"), _row_stride(q_out, "q_out"),

@@ -163,3 +163,29 @@ def test_a_gradient_whose_table_was_rewritten_is_refused():
         sdpa.attn_rope_table(inv, pos, t)
         sdpa.attn_rope(q, None, t, torch.empty_like(q), None)
     _clean()
+
+
+def test_rotation_in_place_within_a_graph_is_refused():
+    sdpa = _sdpa()
+    T, H, d = 96, 2, 64
+    inv, _ = sdpa.rope_frequencies(d)
+    table = sdpa.rope_table(inv, torch.arange(T, dtype=torch.int32, device="cuda"))
+    x = _randn(T, H, d, seed=1).requires_grad_()
+    y = x * 2
+    held = y.detach().clone()
+    with pytest.raises(ValueError, match="differentiable"):
+        sdpa.attn_rope(y, None, table, y, None)
+    with pytest.raises(ValueError, match="differentiable"):
+        sdpa.attn_rope(x.detach(), x.detach(), table, torch.empty_like(held), y)
+    assert torch.equal(y.detach(), held)
+    # queries that attention keeps for its gradient, turned afterwards
+    q, k, v = (_randn(1, T, H, d, seed=s) for s in (2, 3, 4))
+    v.requires_grad_()
+    o = sdpa.attention(q, k, v)
+    sdpa.attn_rope(q, None, table, q, None)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.backward(torch.ones_like(o))
+    with torch.no_grad():
+        sdpa.attn_rope(y, None, table, y, None)
+        assert torch.equal(y, sdpa.rope_forward(held, None, table)[0])
+    _clean()
