@@ -490,7 +490,8 @@ int attn_kv4_copy_pages(void* pool, int n_layers, int n_pages, size_t page_bytes
  *
  * attn_rope_table: table fp32 [T][2][n] = gain cos(p w), then gain sin(p w), of each row's position p
  *   (device int32 [T]) and the n frequencies w (device fp64 [n], radians a position, finite).  The
- *   angle is reduced without rounding, so far positions lose nothing.  n a multiple of 8, at most 128.
+ *   angle is reduced without rounding; a frequency in turns is off by at most 2^-64 + 2^-52 of it, so an angle by
+ *   |p| times that, at most 2^-33 turns for a slow pair's last position.  n a multiple of 8, at most 128.
  * attn_rope: q bf16 rows [T][H_q, d] (row t at q + t * q_stride elements; strides multiples of 8
  *   and at least H_q * d) into q_out, k [T][H_k, d] into k_out alike; a tensor of no heads (H = 0) may
  *   be NULL.  q_out == q (with the same stride) rotates in place; other overlaps are not allowed.  Row
@@ -532,7 +533,8 @@ int attn_kv4_append_rope(const void* q, const void* k, const void* v, const floa
  *   a node that sees no token (those past max_pages * page_size do not exist) gets o = 0 and lse =
  *   the sink logit.  Rows of no sequence are left alone, or with zero_rest get o = 0, lse = -inf.
  *   Any number of nodes; scale, window, sinks, errors and workspace (attn_kv4_tree_workspace_size()
- *   bytes) as attn_kv4_decode.  Bitwise reproducible.
+ *   bytes) as attn_kv4_decode.  Bitwise reproducible.  The kernel is chosen by the rows on average, T / B, so
+ *   sequences of very different sizes (and T or B with much room to spare) are faster in calls of their own.
  * attn_kv4_keep: what verification accepted becomes the sequence's next tokens, in each of n_layers
  *   pools that follow one another: for i = 0, 1, ... in this order token seq_lens[b] + kept[b][i] is copied
  *   to token seq_lens[b] + i, until the first negative entry of kept (device int32 [B, most]).  Keys are

@@ -1152,7 +1152,9 @@ def rope_frequencies(rot_dim, *, base=10000.0, scaling="none", factor=1.0, origi
     base multiplied by factor^(n / (n - 1)): the slowest pair slows down by the factor, the
     fastest stays) or "parts" (pairs that turn slow_turns times or less in original_length positions are
     divided by the factor, those that turn fast_turns times or more stay, those between are
-    blended by the logarithm of their turns; the gain is 0.1 ln(factor) + 1).  gain: another one."""
+    blended by the logarithm of their turns, not rounded to whole pairs; the gain is 0.1 ln(factor) + 1).
+    gain: another one.  A model whose frequencies are blended otherwise (linearly in the turns, or with whole pairs
+    as bounds) brings its own inv_freq."""
     n = int(rot_dim) // 2
     if rot_dim != 2 * n or n <= 0 or n % 8 or n > 128:
         raise ValueError(f"rot_dim must be a multiple of 16 and at most 256, got {rot_dim}")
@@ -1484,7 +1486,10 @@ def attn_kv4_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, o, lse=Non
     below its own; negative: a child of the last token before the tree.  None: a chain (tokens in
     causal order, any number of them; much faster than a long chain given as parents).  A node sees the tokens before the tree, its ancestors and
     itself, with window >= 0 those of the last window + 1 positions.  Rows of no sequence are left
-    alone, or zeroed with zero_rest (lse -inf).  workspace: as for attn_kv4_decode."""
+    alone, or zeroed with zero_rest (lse -inf).  workspace: as for attn_kv4_decode.
+
+    The kernel is chosen by the rows on average, T / B: a large tree or chain among many single tokens, idle sequences or
+    spare rows of q is read several times over, and is faster in a call of its own."""
     sizes = _check_tree(q, cu_seqlens, parents, pool, page_table, seq_lens, softmax_offset)
     T, H_q = sizes[1:3]
     _check(o, "o", torch.bfloat16, 3)

@@ -8,7 +8,8 @@
 // All n nodes and all G query heads of a kv head share every byte of the cache: n G rows.  Reading the cache
 // bounds a call of few rows, the tensor cores one of many (256 rows: 178 us of products, 56 us of
 // bytes for 329,377 tokens of 8 kv heads of 128).  So there are four forms, by the sequences' rows a kv head
-// on average (block_rows):
+// on average (block_rows); a call has one form for all of its sequences, and a sequence of more rows than its blocks have
+// is read and decoded again for each of them (what that costs an uneven batch stands at block_rows):
 //   - Up to 8 and 16 rows (kv4_tree_few_kernel): rows are the 8-wide columns of mma.sync products whose
 //     16 rows are tokens (scores) or head dims (outputs); operands are decoded in registers.
 //   - Up to 128 rows, and more (kv4_tree_kernel): tcgen05 products of 128-row tiles.  Four warps decode
@@ -26,7 +27,9 @@
 //     and row block in order, and kSegCost units more for each such segment); a segment that spans
 //     several CTAs leaves fp32 partial sums in the workspace, joined in CTA order by a second kernel:
 //     bitwise reproducible.
-//   - The probabilities are rounded to bf16 (2^-9 relative) for P V; their sum is fp32.
+//   - The probabilities are rounded to bf16 (2^-8 of each at most) for P V, the operand type of the products; their sum
+//     is of the unrounded ones, fp32.  Against 64 bits an output's error, of which its own rounding to bf16 is 0.00166
+//     (root mean square, relative), becomes 0.00186 for 16 sequences of 16 nodes, 0.0023 for tokens of much the same weight.
 //   - Units with tokens that some row does not see (the tree's own, the ends of a window) take each row's 128 bits
 //     of what it sees, found by walking up from its node: the walk is a dependent load a level.
 //
@@ -39,7 +42,9 @@
 // reports and other code out of the roles' loops 133 / 86; places of pieces by two offsets 130 / 81; more blocks of
 // the join 121 / 81.
 // What bounds it: one tile, decoding (some 2500 cycles a unit in four warps, their waits included; with eight warps the
-// chain S - softmax - P V of a warpgroup's units, 4900 cycles for two, gives the same); two tiles, that chain with both
+// chain S - softmax - P V of a warpgroup's units, 4900 cycles for two, gives the same).  That chain is as long as it is
+// because rows are the tile's lanes: a thread takes 128 exponentials and the products 128 rows whether 32 or 128 of them
+// exist.  Tokens on the lanes and rows as columns, as in the few-row form, have not been tried with tcgen05.  Two tiles, that chain with both
 // tiles' products (2048 cycles a unit at full rate) and the decoded operands' way through shared memory.  Few rows:
 // the copies and the decoding arithmetic, as in kv4_decode.cu.
 #include <algorithm>
@@ -1658,6 +1663,10 @@ int launch_tiles(const Kv4TreeParams& p, void* workspace, cudaStream_t stream) {
 // of 128 / 64): 131,072 tokens with 16 rows 52 / 37 us as columns, 78 / 59 as a tile; with 32 rows 87 / 57 as columns, 78 /
 // 59 as a tile, and 76 sequences of 100 tokens 39 / 31 and 29 / 23.  One tile 178 us and two 260 for 329,377 tokens of 8
 // heads, so that 256 rows as two blocks of one tile would take 356.
+// These are even batches.  The average counts sequences without nodes and rows of no sequence too, so a large sequence among
+// small ones gets blocks too small for it: 131,072 tokens with 64 nodes (4 heads a kv head) take 124 us alone, 822 beside 31
+// sequences without nodes and 596 beside 31 of 2000 tokens with one node (29 alone); a chain of 512 nodes over 4096 tokens 60
+// alone, 348 beside 255 of 2000 tokens with one node (133 alone).
 int block_rows(int B, int T, int H_q, int H_kv) {
   const long long rows = (long long)T * (H_q / H_kv), n = B > 0 ? B : 1;
   return rows <= 8 * n ? 8 : rows <= 16 * n ? 16 : rows <= 128 * n ? 128 : 256;

@@ -2,9 +2,11 @@
 same roundings in torch, gradients, strided and in-place rows, and keys rotated on their way into the
 4-bit cache.
 
-Bounds.  A table entry: the angle is exact in whole-number arithmetic but for the frequency's 53 bits and
-its rounding to fp32 as a part of a half turn (2^-24 of at most pi), sine and cosine are off by at most
-2 units in the last place (2^-22), the gain's product by 2^-24: 2^-21 gain in all.  A rotated value is
+Bounds.  A table entry: the angle is reduced to its nearest quarter turn in whole-number arithmetic, off only by the
+frequency's two roundings and its last bit (the test's own term for far positions).  What is left, at most pi / 4, takes
+three roundings to fp32 (2.4 of 2^-24); sine and cosine, power series to x^9 and x^8 whose left-out terms are below 2^-29
+and 2^-25, turn that and their own roundings into at most 4.2 of 2^-24, the gain's product adds one: within 2^-21 gain
+in all.  A rotated value is
 two products, a sum and a rounding to bf16: 2^-8 |y| + 2^-22 (|x1 c| + |x2 s|)."""
 import numpy as np
 import pytest
